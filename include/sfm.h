@@ -72,7 +72,8 @@ typedef void *sfm_stream_t;
  * (blocks, block_size, 1, row) addressed through a block table. */
 enum sfm_layout { SFM_LAYOUT_BSND = 0, SFM_LAYOUT_TND = 1, SFM_LAYOUT_PAGED = 2 };
 
-enum sfm_dtype { SFM_DTYPE_BF16 = 0, SFM_DTYPE_FP16 = 1 };
+/* E4M3: index queries and keys only (sfm_index_scores). */
+enum sfm_dtype { SFM_DTYPE_BF16 = 0, SFM_DTYPE_FP16 = 1, SFM_DTYPE_E4M3 = 2 };
 
 /* KV row formats.
  *   SFM_KV_PLAIN        512 bf16/fp16 values per row (1024 bytes).
@@ -87,8 +88,12 @@ enum sfm_dtype { SFM_DTYPE_BF16 = 0, SFM_DTYPE_FP16 = 1 };
  *                       the same 528 / 656-byte rows with the 512 NoPE bytes
  *                       FLOAT8_E4M3FN values (sign, 4 exponent bits biased by
  *                       7, 3 mantissa bits, no infinity, S.1111.111 = NaN):
- *                       K~[d] = e4m3(byte d) * scale[d / 128]. */
-enum sfm_kv_format { SFM_KV_PLAIN = 0, SFM_KV_INT8_PACKED = 1, SFM_KV_FP8_PACKED = 2 };
+ *                       K~[d] = e4m3(byte d) * scale[d / 128].
+ *   SFM_KV_FP8_ROWS     index rows: FLOAT8_E4M3FN values only, one fp32 scale
+ *                       per row in an array of its own.  Written by
+ *                       sfm_kv_store() for sfm_index_scores(); sfm_forward()
+ *                       does not take it. */
+enum sfm_kv_format { SFM_KV_PLAIN = 0, SFM_KV_INT8_PACKED = 1, SFM_KV_FP8_PACKED = 2, SFM_KV_FP8_ROWS = 3 };
 
 /* How sfm_metadata sizes the split-KV chunks of a query row ("sparse_flash_mla"
  * doc, 确定性计算: deterministic results and batch invariance are the default).
@@ -309,6 +314,192 @@ int sfm_debug_attended(const sfm_params *params, const sfm_tensors *inputs, cons
  * cudaEventElapsedTime.  (NULL, NULL) turns it off.  Process-wide setting,
  * not synchronised: set it from the thread that calls sfm_forward(). */
 int sfm_set_profile_events(void *begin, void *end);
+
+/* ---------------------------------------------------------------------------
+ * Around the attention: rotary positions, the rows of the caches, and the
+ * scores and selection that make sparse indices.
+ *
+ * The conventions above hold for these entry points too: device pointers of
+ * the current device, caller-owned buffers, no allocation, no
+ * synchronisation, work in stream order, SFM_ERR_* for what the host can see
+ * and status bits for tensor values.  Results are deterministic.  A call with
+ * no rows (tokens, rows or total_q of 0) enqueues nothing and returns SFM_OK.
+ * ------------------------------------------------------------------------- */
+
+/* Which values of a head form the rotated pairs: (2i, 2i + 1), or
+ * (i, i + rope_dim / 2) ("half"). */
+enum sfm_rope_layout { SFM_ROPE_INTERLEAVED = 0, SFM_ROPE_HALF = 1 };
+
+/* How sfm_rope_frequencies() stretches the positions of a long context by
+ * `factor` (>= 1):
+ *   NONE    f_i = base^(-2i / rope_dim)
+ *   LINEAR  f_i / factor
+ *   NTK     base replaced by base * factor^(rope_dim / (rope_dim - 2)):
+ *           the slowest pair slows down by factor, the fastest not at all
+ *   YARN    pairs that turn more than beta_fast times within
+ *           original_max_position keep f_i, those that turn fewer than
+ *           beta_slow times get f_i / factor, a linear ramp over the pair
+ *           index between; the amplitude is 0.1 ln(factor) + 1. */
+enum sfm_rope_scaling { SFM_ROPE_SCALING_NONE = 0, SFM_ROPE_SCALING_LINEAR = 1, SFM_ROPE_SCALING_NTK = 2,
+                        SFM_ROPE_SCALING_YARN = 3 };
+
+typedef struct sfm_rope_spec {
+    int32_t rope_dim;               /* even, > 0 (NTK: > 2) */
+    int32_t scaling;                /* enum sfm_rope_scaling */
+    double base;                    /* > 1 */
+    double factor;                  /* >= 1; NONE ignores it */
+    double beta_fast, beta_slow;    /* YARN: beta_fast > beta_slow > 0 */
+    int32_t original_max_position;  /* YARN: > 0 */
+    int32_t reserved;               /* 0 */
+} sfm_rope_spec;
+
+/* Angles per position in radians (HOST array of rope_dim / 2 doubles) and the
+ * amplitude (HOST) of the rotated values.  Host only, needs no GPU. */
+int sfm_rope_frequencies(const sfm_rope_spec *spec, double *inv_freq, float *amplitude);
+
+/* sfm_rope(): strides are in elements. */
+typedef struct sfm_rope_params {
+    int32_t tokens, heads;          /* >= 0, 1.. */
+    int32_t head_dim;               /* values per head, 1..4096 */
+    int32_t rope_dim, rope_offset;  /* the rotated values [rope_offset, rope_offset + rope_dim), rope_dim even */
+    int32_t rope_layout;            /* enum sfm_rope_layout */
+    int32_t inverse;                /* 1: the transpose of the forward map */
+    int32_t dtype;                  /* enum sfm_dtype of x and y: BF16 or FP16 */
+    float amplitude;                /* finite */
+    int32_t reserved;               /* 0 */
+    int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+} sfm_rope_params;
+
+/* Rotary positions.  For every pair (a, b) of the rotated part and its angle
+ * t = position * inv_freq[i]:
+ *     a' = amplitude (a cos t - b sin t),   b' = amplitude (b cos t + a sin t);
+ * inverse = 1 changes the sign of t, which is the forward map's transpose: it
+ * gives the gradient of x from the gradient of y, and for amplitude 1 it
+ * undoes the rotation (of an attention output whose values carried positions).
+ * x, y: tokens x heads x head_dim; y == x rotates in place (same strides) and
+ * touches the rotated part only, otherwise every value of y is written and the
+ * two must not overlap.  positions: (tokens) int32, any sign.  inv_freq:
+ * DEVICE array of rope_dim / 2 doubles.  The angle is reduced to one turn in
+ * 64 bits, so far positions are as exact as near ones. */
+int sfm_rope(const sfm_rope_params *params, const void *x, const int32_t *positions, const double *inv_freq, void *y,
+             sfm_stream_t stream);
+
+/* sfm_kv_store(): x_*_stride in elements (multiples of 8), row_stride in bytes. */
+typedef struct sfm_store_params {
+    int32_t tokens, heads;          /* rows of x: tokens x heads */
+    int32_t head_dim;               /* values per row of x: PLAIN and FP8_ROWS a multiple of 16 up to 512;
+                                       packed: 512 or 576 (512 NoPE values, then 64 rope values) */
+    int32_t dtype;                  /* enum sfm_dtype of x (and of PLAIN rows / packed rope parts): BF16 or FP16 */
+    int32_t kv_format;              /* enum sfm_kv_format of the cache rows */
+    int32_t norm;                   /* 1: RMS norm over the row's first min(head_dim, 512) values */
+    float norm_eps;                 /* >= 0, finite */
+    int32_t rope_dim;               /* 0: no rotation; else a multiple of 16 */
+    int32_t rope_offset;            /* a multiple of 8 */
+    int32_t rope_layout;            /* enum sfm_rope_layout */
+    float amplitude;                /* of the rotated values */
+    int32_t reserved;               /* 0 */
+    int64_t x_token_stride, x_head_stride;
+    int64_t row_stride;             /* bytes between cache rows: >= the row, a multiple of 16 */
+    int64_t rows;                   /* rows the cache (and `scales`) holds */
+} sfm_store_params;
+
+/* Write rows into a cache in the format sfm_forward() (PLAIN and packed rows)
+ * or sfm_index_scores() (PLAIN and FP8_ROWS) reads.  Per row, in fp32:
+ *     v = x / sqrt(mean(x^2) + eps) * norm_weight      (norm; over the first min(head_dim, 512) values)
+ *     v rotated at the token's position as in sfm_rope  (rope_dim > 0)
+ * then rounded to the format: PLAIN to dtype; the others per tile (packed:
+ * 128 values, FP8_ROWS: the row)
+ *     scale = max(max |v| / M, 2^-126),   code = round(v / scale),   M = 127 (int8) or 448 (E4M3),
+ * to nearest, ties to even; packed rope values (512..575) are rounded to
+ * dtype.  A NaN anywhere in a tile makes its scale NaN.
+ *   slots    (tokens) int32 or NULL (identity): head h of token t goes to cache
+ *            row slots[t] * heads + h.  A negative slot writes nothing (padding).
+ *            A slot whose rows lie outside the cache writes nothing and sets
+ *            SFM_STATUS_BAD_BLOCK.  Two tokens of one call must not name the
+ *            same slot: each 16-byte piece of that row is then one of the two.
+ *            Rows no slot names are left as they were.
+ *   norm_weight  (min(head_dim, 512)) fp32 or NULL (ones)
+ *   positions, inv_freq  as in sfm_rope (NULL without rotation)
+ *   scales   (rows) fp32, FP8_ROWS only
+ * x and cache are 16-byte aligned. */
+int sfm_kv_store(const sfm_store_params *params, const void *x, const float *norm_weight, const int32_t *positions,
+                 const double *inv_freq, const int32_t *slots, void *cache, float *scales, int32_t *status,
+                 sfm_stream_t stream);
+
+typedef struct sfm_index_params {
+    int32_t num_heads;          /* index heads, 1..128 */
+    int32_t index_dim;          /* 128 */
+    int32_t batch_size;         /* b (> 0) */
+    int32_t max_seqlen_q;       /* BSND: q_s; TND: max q length */
+    int32_t total_q;            /* TND: rows of q; ignored for BSND */
+    int32_t max_seqlen_kv;      /* columns of the scores; BSND: S dim of k; TND / paged: max key count */
+    int32_t cmp_ratio;          /* tokens per key (1: one key per token) */
+    int32_t mask_mode;          /* 0 no mask, 3 right-down causal */
+    int32_t layout_q;           /* SFM_LAYOUT_BSND or SFM_LAYOUT_TND */
+    int32_t layout_kv;          /* BSND, TND or PAGED; non-paged must equal layout_q */
+    int32_t dtype;              /* of q and k: BF16, FP16 or E4M3 */
+    int32_t block_size;         /* paged: rows per block, multiple of 16, <= 1024 */
+} sfm_index_params;
+
+/*   q              BSND (b, q_s, num_heads, 128) / TND (q_t, num_heads, 128), 16-byte aligned
+ *   k              BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned;
+ *                  k_row_stride bytes apart (multiple of 16), k_rows rows in all
+ *   k_scales       (k_rows) fp32 or NULL (ones), >= 0
+ *   weights        (tokens, num_heads) fp32
+ *   the length tensors as in sfm_tensors (seqused_kv required for PAGED;
+ *   cmp_residual_kv required for mask mode 3 with cmp_ratio > 1) */
+typedef struct sfm_index_tensors {
+    const void *q;
+    const void *k;
+    int64_t k_row_stride;
+    int64_t k_rows;
+    const float *k_scales;
+    const float *weights;
+    const int32_t *block_table;
+    int32_t block_table_stride;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_kv;
+    const int32_t *seqused_q;
+    const int32_t *seqused_kv;
+    const int32_t *cmp_residual_kv;
+} sfm_index_tensors;
+
+/* The cheap score that picks what a query attends to:
+ *     scores[t][j] = sum_h weights[t][h] * max(0, k_scales[j] * (q[t][h] . k[j])),   j < visible(t)
+ *     scores[t][j] = -inf                                                            visible(t) <= j < max_seqlen_kv
+ * with visible(t) = the keys of t's sequence under the compressed source's
+ * mask of sfm_forward: j is visible iff (j + 1) * cmp_ratio <= p + 1,
+ * p = len * cmp_ratio + residual - q_len + i (mode 3), or always (mode 0).
+ * Products are exact, sums are in fp32.  A key whose block id is outside the
+ * cache scores -inf and sets SFM_STATUS_BAD_BLOCK.  Rows of q at or beyond
+ * seqused_q score -inf everywhere; rows behind the last sequence (TND) are
+ * left as they were.
+ * scores: device fp32, score_stride (>= max_seqlen_kv) elements apart.
+ * visible: device int32 (tokens) or NULL: visible(t). */
+int sfm_index_scores(const sfm_index_params *params, const sfm_index_tensors *tensors, float *scores,
+                     int64_t score_stride, int32_t *visible, int32_t *status, sfm_stream_t stream);
+
+typedef struct sfm_topk_params {
+    int32_t rows;               /* >= 0 */
+    int32_t n;                  /* scores per row, > 0 */
+    int32_t k;                  /* indices per row, > 0 */
+    int32_t block_size;         /* scores per selected block: 1 or a power of two <= 128 */
+    int32_t first_blocks;       /* blocks at the row's start that are always selected */
+    int32_t last_blocks;        /* blocks at the row's end that are always selected; first + last <= k */
+    int64_t score_stride;       /* elements between rows, >= n */
+} sfm_topk_params;
+
+/* The k best positions (block_size 1) or blocks of every row, as the sparse
+ * indices that sfm_forward() takes (cmp_sparse_indices, ori_sparse_indices
+ * with sparse_block_size = block_size).  Row r has lengths[r] scores (NULL: n;
+ * a length outside [0, n] is clamped and sets SFM_STATUS_BAD_LENGTH), and
+ * ceil(length / block_size) blocks, the last one possibly short; a block's
+ * value is its largest score.  A NaN or -inf counts as no score: a block of
+ * nothing else is selected only if it is one of the row's first_blocks or
+ * last_blocks.  Equal values (-0 = 0) go to the lower index.
+ * indices: device int32 (rows, k): ascending, then -1 where a row has fewer. */
+int sfm_topk_select(const sfm_topk_params *params, const float *scores, const int32_t *lengths, int32_t *indices,
+                    int32_t *status, sfm_stream_t stream);
 
 /* Static description of an sfm_error code. */
 const char *sfm_error_string(int code);

@@ -13,7 +13,12 @@ Two layers:
   ctypes structs and raw device pointers;
 * ``sparse_flash_mla_metadata`` / ``sparse_flash_mla`` -- the two-call torch
   API of the "sparse_flash_mla" doc (函数原型), building those structs from
-  tensors and keyword attributes.
+  tensors and keyword attributes;
+* ``rope_frequencies`` / ``apply_rope`` / ``store_kv`` / ``index_scores`` /
+  ``select_topk`` -- the operators around the attention in the same form, over
+  ``sfm_rope_frequencies`` / ``sfm_rope`` / ``sfm_kv_store`` /
+  ``sfm_index_scores`` / ``sfm_topk_select``: rotary positions, the rows of the
+  caches, and the sparse indices the attention reads.
 """
 from __future__ import annotations
 
@@ -29,8 +34,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libsfm.so")
 
 BSND, TND, PAGED = 0, 1, 2
-BF16, FP16 = 0, 1
-KV_PLAIN, KV_INT8_PACKED, KV_FP8_PACKED = 0, 1, 2
+BF16, FP16, E4M3 = 0, 1, 2
+KV_PLAIN, KV_INT8_PACKED, KV_FP8_PACKED, KV_FP8_ROWS = 0, 1, 2, 3
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 SPLIT_BATCH_INVARIANT, SPLIT_OCCUPANCY = 0, 1
 _LAYOUTS = {"BSND": BSND, "TND": TND, "PAGED": PAGED, "PA_BBND": PAGED, "PA_BSND": PAGED, "PA_ND": PAGED}
 
@@ -40,6 +47,7 @@ STATUS_BAD_LENGTH = 0x04
 STATUS_METADATA_MISMATCH = 0x08
 STATUS_WORKSPACE_OVERFLOW = 0x10
 STATUS_PLAN_OVERFLOW = 0x20
+STATUS_TIMEOUT = 0x40
 
 
 class SfmParams(C.Structure):
@@ -67,8 +75,58 @@ class SfmTensors(C.Structure):
     ]
 
 
+class _Params(C.Structure):
+    """A struct whose fields are all given by name."""
+
+    def __init__(self, **kw):
+        super().__init__()
+        names = {n for n, _ in self._fields_}
+        if set(kw) - names:
+            raise TypeError(f"unknown fields {sorted(set(kw) - names)}")
+        for k, v in kw.items():
+            setattr(self, k, v)
+
+
+def _i32(*names):
+    return [(n, C.c_int32) for n in names]
+
+
+class SfmRopeSpec(_Params):
+    _fields_ = _i32("rope_dim", "scaling") + [(n, C.c_double) for n in ("base", "factor", "beta_fast", "beta_slow")] + \
+        _i32("original_max_position", "reserved")
+
+
+class SfmRopeParams(_Params):
+    _fields_ = _i32("tokens", "heads", "head_dim", "rope_dim", "rope_offset", "rope_layout", "inverse", "dtype") + \
+        [("amplitude", C.c_float)] + _i32("reserved") + \
+        [(n, C.c_int64) for n in ("x_token_stride", "x_head_stride", "y_token_stride", "y_head_stride")]
+
+
+class SfmStoreParams(_Params):
+    _fields_ = _i32("tokens", "heads", "head_dim", "dtype", "kv_format", "norm") + [("norm_eps", C.c_float)] + \
+        _i32("rope_dim", "rope_offset", "rope_layout") + [("amplitude", C.c_float)] + _i32("reserved") + \
+        [(n, C.c_int64) for n in ("x_token_stride", "x_head_stride", "row_stride", "rows")]
+
+
+class SfmIndexParams(_Params):
+    _fields_ = _i32("num_heads", "index_dim", "batch_size", "max_seqlen_q", "total_q", "max_seqlen_kv", "cmp_ratio",
+                    "mask_mode", "layout_q", "layout_kv", "dtype", "block_size")
+
+
+class SfmIndexTensors(_Params):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("k_row_stride", C.c_int64), ("k_rows", C.c_int64),
+                ("k_scales", C.c_void_p), ("weights", C.c_void_p), ("block_table", C.c_void_p),
+                ("block_table_stride", C.c_int32), ("cu_seqlens_q", C.c_void_p), ("cu_seqlens_kv", C.c_void_p),
+                ("seqused_q", C.c_void_p), ("seqused_kv", C.c_void_p), ("cmp_residual_kv", C.c_void_p)]
+
+
+class SfmTopkParams(_Params):
+    _fields_ = _i32("rows", "n", "k", "block_size", "first_blocks", "last_blocks") + [("score_stride", C.c_int64)]
+
+
 EXPORTS = ("sfm_metadata_size", "sfm_workspace_size", "sfm_metadata", "sfm_forward", "sfm_forward_noalloc",
-           "sfm_debug_attended", "sfm_set_profile_events", "sfm_error_string", "sfm_abi_version")
+           "sfm_debug_attended", "sfm_set_profile_events", "sfm_error_string", "sfm_abi_version",
+           "sfm_rope_frequencies", "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select")
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 
 _lib = None
@@ -100,8 +158,15 @@ def lib():
         l.sfm_set_profile_events.argtypes = [C.c_void_p, C.c_void_p]
         l.sfm_error_string.argtypes = [C.c_int]
         l.sfm_error_string.restype = C.c_char_p
+        V = C.c_void_p
+        l.sfm_rope_frequencies.argtypes = [C.POINTER(SfmRopeSpec), C.POINTER(C.c_double), C.POINTER(C.c_float)]
+        l.sfm_rope.argtypes = [C.POINTER(SfmRopeParams), V, V, V, V, V]
+        l.sfm_kv_store.argtypes = [C.POINTER(SfmStoreParams), V, V, V, V, V, V, V, V, V]
+        l.sfm_index_scores.argtypes = [C.POINTER(SfmIndexParams), C.POINTER(SfmIndexTensors), V, C.c_int64, V, V, V]
+        l.sfm_topk_select.argtypes = [C.POINTER(SfmTopkParams), V, V, V, V, V]
         for n in ("sfm_metadata_size", "sfm_workspace_size", "sfm_metadata", "sfm_forward", "sfm_forward_noalloc",
-                  "sfm_debug_attended", "sfm_set_profile_events", "sfm_abi_version"):
+                  "sfm_debug_attended", "sfm_set_profile_events", "sfm_abi_version", "sfm_rope_frequencies",
+                  "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select"):
             getattr(l, n).restype = C.c_int
         _lib = l
     return _lib
@@ -344,3 +409,292 @@ def sparse_flash_mla(q: torch.Tensor, *, metadata: Metadata, ori_kv=None, cmp_kv
     sfm_forward(params, tensors, metadata.tensor, softmax_scale, out, lse if params.return_lse else None,
                 workspace, status, stream)
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# around the attention: rotary positions, cache rows, sparse indices
+# ---------------------------------------------------------------------------
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(name, x, dtype=None, shape=None, device=None):
+    """Check one tensor argument and return its device address (None for None)."""
+    if x is None:
+        return None
+    _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
+    if dtype is not None:
+        _require(x.dtype in (dtype if isinstance(dtype, tuple) else (dtype,)), f"{name}: dtype {x.dtype}, expected {dtype}")
+    if shape is not None:
+        _require(tuple(x.shape) == tuple(shape), f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+        _require(x.is_contiguous(), f"{name}: not contiguous")
+    _require(x.is_cuda, f"{name}: not on a CUDA device")
+    if device is not None:
+        _require(x.device == device, f"{name}: on {x.device}, expected {device}")
+    return x.data_ptr()
+
+
+class _Launch:
+    """The device and stream of one call: makes the inputs' device current
+    and allocates results on the stream that writes them."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        given = stream is not None and not hasattr(stream, "cuda_stream")
+        self.given = torch.cuda.ExternalStream(int(stream), device=device) if given else stream
+        self.stream = self.given
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.given is None:
+            self.stream = torch.cuda.current_stream()
+            self.on = None
+        else:
+            self.on = torch.cuda.stream(self.given)
+            self.on.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.on is not None:
+            self.on.__exit__(*exc)
+        return self.device.__exit__(*exc)
+
+
+def rope_frequencies(rope_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_max_position: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Angles per position (float64, rope_dim / 2) and the amplitude of rotary
+    positions; ``scaling`` ("none", "linear", "ntk", "yarn") stretches them by
+    ``factor`` for long contexts (see sfm_rope_frequencies in include/sfm.h)."""
+    _require(scaling in ROPE_SCALINGS, f"scaling: {scaling!r}")
+    spec = SfmRopeSpec(rope_dim=rope_dim, scaling=ROPE_SCALINGS[scaling], base=base, factor=factor, beta_fast=beta_fast,
+                       beta_slow=beta_slow, original_max_position=original_max_position)
+    freq = (C.c_double * max(rope_dim // 2, 1))()
+    amplitude = C.c_float(1.0)
+    _check("sfm_rope_frequencies", lib().sfm_rope_frequencies(C.byref(spec), freq, C.byref(amplitude)))
+    return torch.tensor(list(freq), dtype=torch.float64, device=device), amplitude.value
+
+
+def _dtype_code(x, name, fp8=False):
+    codes = {torch.bfloat16: BF16, torch.float16: FP16}
+    if fp8:
+        codes[torch.float8_e4m3fn] = E4M3
+    _require(x.dtype in codes, f"{name}: dtype {x.dtype}")
+    return codes[x.dtype]
+
+
+def _heads_view(x, name):
+    """(tokens, heads, dim) of a (..., heads, dim) tensor, without a copy."""
+    _require(isinstance(x, torch.Tensor) and x.dim() >= 2, f"{name}: needs (..., heads, values)")
+    _require(x.stride(-1) == 1 or x.shape[-1] == 1, f"{name}: the last dimension must be contiguous")
+    tokens = 1
+    for n in x.shape[:-2]:
+        tokens *= n
+    try:
+        return x.view(tokens, x.shape[-2], x.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: the token dimensions do not flatten to one stride") from None
+
+
+def _strides(v):
+    """(token, head) strides of a (tokens, heads, dim) view; a dimension of one entry gets the stride of dense rows
+    (torch may report any)."""
+    head = v.stride(1) if v.shape[1] > 1 else v.shape[2]
+    token = v.stride(0) if v.shape[0] > 1 else max(head * v.shape[1], v.shape[2])
+    return token, head
+
+
+def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, amplitude: float = 1.0,
+               rope_offset: int = 0, interleaved: bool = True, inverse: bool = False, out=None, stream=None):
+    """Rotary positions of x (..., heads, head_dim), bf16 or fp16.
+
+    The values [rope_offset, rope_offset + 2 len(inv_freq)) of every head are
+    rotated by position * inv_freq as pairs (2i, 2i + 1), or (i, i + n / 2)
+    with ``interleaved=False``, and multiplied by ``amplitude``.
+    positions: int32, one per token.  ``inverse=True`` applies the transposed
+    map: the gradient with respect to x, and the way back for amplitude 1.
+    ``out``: None for a new tensor, x itself to rotate in place, or a tensor
+    of x's shape that does not overlap it.  Views with strides are taken as they are."""
+    v = _heads_view(x, "x")
+    dtype = _dtype_code(x, "x")
+    _tensor("x", x)
+    _require(inv_freq.dim() == 1 and inv_freq.numel() > 0, "inv_freq: needs one dimension")
+    pos = _tensor("positions", positions, torch.int32, x.shape[:-2] if positions.dim() != 1 else (v.shape[0],), x.device)
+    freq = _tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), x.device)
+    with _Launch(x.device, stream) as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _tensor("out", out, x.dtype, None, x.device)
+            _require(out.shape == x.shape, f"out: shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+        o = _heads_view(out, "out")
+        (xt, xh), (yt, yh) = _strides(v), _strides(o)
+        params = SfmRopeParams(tokens=v.shape[0], heads=max(v.shape[1], 1), head_dim=v.shape[2],
+                               rope_dim=2 * inv_freq.numel(), rope_offset=rope_offset,
+                               rope_layout=ROPE_INTERLEAVED if interleaved else ROPE_HALF, inverse=int(inverse),
+                               dtype=dtype, amplitude=amplitude, x_token_stride=xt, x_head_stride=xh,
+                               y_token_stride=yt, y_head_stride=yh)
+        if v.shape[1] == 0:
+            params.tokens = 0
+        _check("sfm_rope", lib().sfm_rope(C.byref(params), v.data_ptr(), pos, freq, o.data_ptr(), st))
+    return out
+
+
+def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_format: int = KV_PLAIN, norm_weight=None,
+             norm_eps: Optional[float] = None, positions=None, inv_freq=None, amplitude: float = 1.0,
+             rope_offset: Optional[int] = None, interleaved: bool = True, scales=None, status=None, stream=None):
+    """Write the rows x (tokens, dim) or (tokens, heads, dim), bf16 or fp16,
+    into ``cache`` as sfm_kv_store does: RMS norm (with ``norm_eps``; weight
+    fp32 or ones), rotary positions (with ``positions`` and ``inv_freq``; the
+    last 2 len(inv_freq) values unless ``rope_offset`` says otherwise), then
+    the rounding of ``kv_format``.  Returns ``cache``.
+
+    cache: (..., row) with dense rows: values of x's dtype (KV_PLAIN), bytes
+    of packed rows, uint8 (KV_INT8_PACKED, KV_FP8_PACKED), or float8_e4m3fn values
+    with fp32 ``scales``, one per row (KV_FP8_ROWS).  Rows may be padded apart.
+    slot_mapping: int32, one per token: head h goes to row slot * heads + h;
+    negative: not written; None: row t * heads + h."""
+    _require(isinstance(x, torch.Tensor) and x.dim() in (2, 3), "x: needs (tokens, dim) or (tokens, heads, dim)")
+    v = _heads_view(x.unsqueeze(1) if x.dim() == 2 else x, "x")
+    dtype = _dtype_code(x, "x")
+    T, H, D = v.shape
+    _tensor("x", x)
+    packed = kv_format in (KV_INT8_PACKED, KV_FP8_PACKED)
+    kind = torch.uint8 if packed else torch.float8_e4m3fn if kv_format == KV_FP8_ROWS else x.dtype
+    _tensor("cache", cache, kind, None, x.device)
+    _require(cache.dim() >= 2 and (cache.stride(-1) == 1 or cache.shape[-1] == 1),
+             "cache: needs (..., row) with contiguous rows")
+    width = 512 + 2 * (D - 512) + 16 if packed else D
+    _require(cache.shape[-1] == width, f"cache: rows of {cache.shape[-1]}, expected {width}")
+    rows = 1
+    for n in cache.shape[:-1]:
+        rows *= n
+    try:
+        flat = cache.view(rows, width)
+    except RuntimeError:
+        raise ValueError("cache: the row dimensions do not flatten to one stride") from None
+    _require((scales is not None) == (kv_format == KV_FP8_ROWS), "scales: go with KV_FP8_ROWS rows")
+    _require((positions is None) == (inv_freq is None), "positions and inv_freq go together")
+    _require(norm_eps is not None or norm_weight is None, "norm_weight: needs norm_eps")
+    if scales is not None:
+        _tensor("scales", scales, torch.float32, None, x.device)
+        _require(scales.numel() == rows and scales.is_contiguous(), f"scales: {rows} contiguous values expected")
+    if inv_freq is not None:
+        _require(inv_freq.dim() == 1, "inv_freq: needs one dimension")
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    xt, xh = _strides(v)
+    params = SfmStoreParams(
+        tokens=T if H else 0, heads=max(H, 1), head_dim=D, dtype=dtype, kv_format=kv_format,
+        norm=int(norm_eps is not None), norm_eps=norm_eps if norm_eps is not None else 0.0, rope_dim=rot,
+        rope_offset=(D - rot if rope_offset is None else rope_offset) if rot else 0,
+        rope_layout=ROPE_INTERLEAVED if interleaved else ROPE_HALF, amplitude=amplitude, x_token_stride=xt,
+        x_head_stride=xh, row_stride=(flat.stride(0) if rows > 1 else width) * cache.element_size(), rows=rows)
+    args = (_tensor("norm_weight", norm_weight, torch.float32, (min(D, 512),), x.device),
+            _tensor("positions", positions, torch.int32, (T,), x.device),
+            _tensor("inv_freq", inv_freq, torch.float64, (rot // 2,), x.device),
+            _tensor("slot_mapping", slot_mapping, torch.int32, (T,), x.device))
+    _tensor("status", status, torch.int32, None, x.device)
+    with _Launch(x.device, stream) as st:
+        _check("sfm_kv_store", lib().sfm_kv_store(C.byref(params), v.data_ptr(), *args, flat.data_ptr(), _ptr(scales),
+                                                  _ptr(status), st))
+    return cache
+
+
+def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, *, max_seqlen_kv: int, k_scales=None,
+                 block_table=None, cu_seqlens_q=None, cu_seqlens_kv=None, seqused_q=None, seqused_kv=None,
+                 cmp_residual_kv=None, max_seqlen_q: int = 0, cmp_ratio: int = 1, mask_mode: int = 3,
+                 layout_q="BSND", layout_kv="BSND", out=None, visible=None, status=None, stream=None):
+    """Scores of every query against the index keys of its sequence, and the
+    number of keys each query may see (see sfm_index_scores).
+
+    q: (b, q_s, heads, 128) or TND (tokens, heads, 128) in bf16, fp16 or
+    float8_e4m3fn; index_k: (b, S, 128), (t, 128) or paged (blocks,
+    block_size, 128) of the same dtype, rows may be padded apart; weights:
+    fp32 (tokens, heads) in q's leading shape; k_scales: fp32, one per row of
+    index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, -inf where a key
+    is not visible; visible (tokens) int32).  ``out`` may be a
+    view with wider rows."""
+    lq, lkv = _LAYOUTS[layout_q], _LAYOUTS[layout_kv]
+    _require(isinstance(q, torch.Tensor) and q.dim() == (4 if lq == BSND else 3), "q: BSND has 4 dimensions, TND 3")
+    dtype = _dtype_code(q, "q", fp8=True)
+    tokens, heads = q.shape[:-2].numel(), q.shape[-2]
+    _tensor("q", q, None, q.shape)
+    dev = q.device
+    _tensor("index_k", index_k, q.dtype, None, dev)
+    _require(index_k.dim() == (2 if lkv == TND else 3) and index_k.shape[-1] == q.shape[-1] and index_k.stride(-1) == 1,
+             "index_k: needs (t, dim), (b, S, dim) or (blocks, block_size, dim) with contiguous rows of q's dim")
+    rows = index_k.shape[:-1].numel()
+    try:
+        flat = index_k.view(rows, index_k.shape[-1])
+    except RuntimeError:
+        raise ValueError("index_k: the row dimensions do not flatten to one stride") from None
+    _tensor("weights", weights, torch.float32, q.shape[:-1], dev)
+    if lkv == BSND:
+        _require(index_k.shape[1] == max_seqlen_kv and index_k.shape[0] == q.shape[0], "index_k: needs (b, max_seqlen_kv, dim)")
+    if lq == BSND:
+        batch, max_seqlen_q = q.shape[0], q.shape[1]
+    else:
+        _require(cu_seqlens_q is not None, "cu_seqlens_q: required for TND")
+        batch = cu_seqlens_q.numel() - 1
+    if k_scales is not None:
+        _tensor("k_scales", k_scales, torch.float32, None, dev)
+        _require(k_scales.numel() == rows and k_scales.is_contiguous(), f"k_scales: {rows} contiguous values expected")
+    if block_table is not None:
+        _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: needs (b, blocks)")
+    params = SfmIndexParams(
+        num_heads=heads, index_dim=q.shape[-1], batch_size=batch, max_seqlen_q=max_seqlen_q, total_q=tokens,
+        max_seqlen_kv=max_seqlen_kv, cmp_ratio=cmp_ratio, mask_mode=mask_mode, layout_q=lq, layout_kv=lkv, dtype=dtype,
+        block_size=index_k.shape[1] if lkv == PAGED else 0)
+
+    def ints(name, x, shape):
+        return _tensor(name, x, torch.int32, shape, dev)
+
+    tensors = SfmIndexTensors(
+        q=q.data_ptr(), k=flat.data_ptr(),
+        k_row_stride=(flat.stride(0) if rows > 1 else flat.shape[1]) * flat.element_size(), k_rows=rows,
+        k_scales=_ptr(k_scales), weights=weights.data_ptr(),
+        block_table=ints("block_table", block_table, block_table.shape if block_table is not None else None),
+        block_table_stride=block_table.shape[1] if block_table is not None else 0,
+        cu_seqlens_q=ints("cu_seqlens_q", cu_seqlens_q, (batch + 1,)),
+        cu_seqlens_kv=ints("cu_seqlens_kv", cu_seqlens_kv, (batch + 1,)), seqused_q=ints("seqused_q", seqused_q, (batch,)),
+        seqused_kv=ints("seqused_kv", seqused_kv, (batch,)),
+        cmp_residual_kv=ints("cmp_residual_kv", cmp_residual_kv, (batch,)))
+    _tensor("status", status, torch.int32, None, dev)
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty(tokens, max(max_seqlen_kv, 0), dtype=torch.float32, device=dev)
+        else:
+            _tensor("out", out, torch.float32, None, dev)
+            _require(tuple(out.shape) == (tokens, max_seqlen_kv) and out.stride(1) == 1,
+                     f"out: needs ({tokens}, {max_seqlen_kv}) with contiguous rows")
+        if visible is None:
+            visible = torch.empty(tokens, dtype=torch.int32, device=dev)
+        seen = ints("visible", visible, (tokens,))
+        stride = out.stride(0) if tokens > 1 else max(max_seqlen_kv, 1)
+        _check("sfm_index_scores", lib().sfm_index_scores(C.byref(params), C.byref(tensors), out.data_ptr(), stride, seen,
+                                                          _ptr(status), st))
+    return out, visible
+
+
+def select_topk(scores: torch.Tensor, k: int, *, lengths=None, block_size: int = 1, first_blocks: int = 0,
+                last_blocks: int = 0, out=None, status=None, stream=None):
+    """Indices (rows, k) int32, ascending and padded with -1, of the k largest
+    scores of every row of ``scores`` (rows, n) fp32, or with ``block_size``
+    of the k blocks with the largest score in them, the row's ``first_blocks``
+    and ``last_blocks`` always among them (see sfm_topk_select).  They are what
+    sparse_flash_mla takes as cmp_sparse_indices / ori_sparse_indices.
+    lengths: int32 (rows), scores a row really has (None: n)."""
+    _require(isinstance(scores, torch.Tensor) and scores.dim() == 2, "scores: needs (rows, n)")
+    _tensor("scores", scores, torch.float32)
+    rows, n = scores.shape
+    _require(scores.stride(1) == 1 or n == 1, "scores: rows must be contiguous")
+    args = _tensor("lengths", lengths, torch.int32, (rows,), scores.device)
+    _tensor("status", status, torch.int32, None, scores.device)
+    params = SfmTopkParams(rows=rows, n=n, k=k, block_size=block_size, first_blocks=first_blocks, last_blocks=last_blocks,
+                           score_stride=scores.stride(0) if rows > 1 else n)
+    with _Launch(scores.device, stream) as st:
+        if out is None:
+            out = torch.empty(rows, max(k, 0), dtype=torch.int32, device=scores.device)
+        got = _tensor("out", out, torch.int32, (rows, k), scores.device)
+        _check("sfm_topk_select", lib().sfm_topk_select(C.byref(params), scores.data_ptr(), args, got, _ptr(status), st))
+    return out

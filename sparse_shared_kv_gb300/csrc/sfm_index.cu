@@ -1,0 +1,604 @@
+// sfm_index.cu -- index scores (sfm_index_scores):
+//     scores[t][j] = sum_h w[t][h] max(0, s[j] q[t][h] . k[j])
+// over paged or contiguous index keys of 128 values (bf16, fp16 or E4M3).
+//
+// The products are a matrix product per sequence, keys x (queries x heads),
+// followed by a clipped weighted sum over the heads.  A tile is 128 keys (the
+// rows of the accumulator, one per TMEM lane) by the heads of up to 256 / HP
+// queries (its columns, HP = the heads rounded up to 16, 32, 64 or 128): with
+// keys on the lanes, the sum over the heads stays inside a thread, a key that
+// must not count spoils nothing but its own lane, and scores of neighbouring
+// keys are stored side by side.
+//
+// One persistent CTA per SM walks work units; a unit is up to `chunk` tiles of
+// keys for one group of queries of one sequence.
+//   warp 16       loads: the unit's queries (two buffers) and its key tiles
+//                 (a ring of stages) by TMA into 128-byte-swizzled operands,
+//                 one box per run of keys that lies inside a page;
+//   warp 17       tcgen05.mma, M = 128, N = queries x HP, K = 128 -> TMEM;
+//   warps 0-15    four warpgroups that drain the accumulator: a warpgroup
+//                 takes 64 columns of a tile.  Its weights stay in registers
+//                 for the whole unit, so a score costs a clip and a
+//                 multiply-add per head and no shared-memory traffic.  Units
+//                 of few queries are narrower than 256 columns: then TMEM
+//                 holds more tiles and the warpgroups take different ones.
+// With one query per sequence the kernel is bound by reading the keys; with
+// many it is bound by the matrix products and the clipped sums beside them.
+//
+// Every wait is bounded as in the attention kernel (sfm_tc.cuh).
+#include <cuda.h>
+#include <math.h>
+
+#include "sfm_internal.cuh"
+#include "sfm_tc.cuh"
+
+namespace sfm {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;                     // keys per tile
+constexpr int kDim = 128;                      // values per key
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kMaxStages = 8;
+constexpr int kMaxAcc = 8;                     // accumulator tiles in TMEM
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSmemLimit = 232448;
+constexpr uint32_t kMiscBytes = 384 + 1024;    // barriers and flags, then the HP 128 exchange
+
+struct IndexArgs {
+    const float *weights, *k_scales;
+    float *scores;
+    int32_t *visible, *status;
+    const int32_t *table, *cu_q, *cu_k, *used_q, *used_k, *residual;
+    int64_t stride, k_rows;
+    int32_t heads, batch, max_q, total_q, max_k, ratio, causal, layout_q, layout_kv, block, table_stride;
+    int32_t groups_per_seq, groups, chunk, units;   // tiles per unit; units in all
+    int32_t run;                               // keys per TMA box
+    int32_t parts_log2;                        // 64-column parts of a tile: 1, 2 or 4
+    int32_t stages;
+    FastDiv block_div, ratio_div;
+    uint32_t idesc;                            // instruction descriptor without N
+    int32_t fp8;
+};
+
+struct Unit {
+    int32_t b, t0, nq, rows;                   // sequence, first token, live queries, query rows to write
+    int32_t i0, q_len, len, tiles, first_tile; // position of the first query, lengths, tiles with visible keys
+    int64_t p0;                                // visible(i) = floor((p0 + i) / ratio) for query i of the unit
+    int64_t k_base;                            // first key row (contiguous layouts)
+};
+
+__device__ __forceinline__ int32_t clamp_to(int64_t v, int64_t lo, int64_t hi, bool *bad)
+{
+    if (v < lo || v > hi) {
+        *bad = true;
+        v = v < lo ? lo : hi;
+    }
+    return (int32_t)v;
+}
+
+__device__ __forceinline__ int32_t visible_of(const IndexArgs &a, const Unit &u, int i)
+{
+    if (i >= u.nq) return 0;
+    if (!a.causal) return u.len;
+    const int64_t p = u.p0 + i;                // tokens up to and including the query's own
+    if (p <= 0) return 0;
+    const int64_t v = p <= 0xffffffffll ? (int64_t)fdiv((uint32_t)p, a.ratio_div) : p / a.ratio;
+    return (int32_t)(v < u.len ? v : u.len);
+}
+
+__device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int queries, bool *bad)
+{
+    Unit u;
+    const int c = unit / a.groups, g = unit - c * a.groups;
+    u.b = g / a.groups_per_seq;
+    u.i0 = (g - u.b * a.groups_per_seq) * queries;
+    int q_cap, t_base;
+    if (a.layout_q == SFM_LAYOUT_BSND) {
+        t_base = u.b * a.max_q;
+        q_cap = a.max_q;
+    } else {
+        t_base = clamp_to(__ldg(a.cu_q + u.b), 0, a.total_q, bad);
+        const int end = clamp_to(__ldg(a.cu_q + u.b + 1), t_base, a.total_q, bad);
+        q_cap = clamp_to(end - t_base, 0, a.max_q, bad);
+    }
+    u.q_len = a.used_q ? clamp_to(__ldg(a.used_q + u.b), 0, q_cap, bad) : q_cap;
+    u.t0 = t_base + u.i0;
+    u.rows = min(max(q_cap - u.i0, 0), queries);
+    u.nq = min(max(u.q_len - u.i0, 0), queries);
+
+    int cap = a.max_k;
+    u.k_base = 0;
+    if (a.layout_kv == SFM_LAYOUT_BSND) {
+        u.k_base = (int64_t)u.b * a.max_k;
+    } else if (a.layout_kv == SFM_LAYOUT_TND) {
+        const int64_t k0 = __ldg(a.cu_k + u.b), k1 = __ldg(a.cu_k + u.b + 1);
+        u.k_base = k0 < 0 ? 0 : k0;
+        if (k0 < 0) *bad = true;
+        cap = clamp_to(k1 - u.k_base, 0, a.max_k, bad);
+    }
+    u.len = a.used_k ? clamp_to(__ldg(a.used_k + u.b), 0, cap, bad) : cap;
+    const int64_t rest = a.residual ? (int64_t)__ldg(a.residual + u.b) : 0;
+    u.p0 = (int64_t)u.len * a.ratio + rest - u.q_len + u.i0 + 1;
+    u.first_tile = c * a.chunk;
+    const int most = u.nq > 0 ? visible_of(a, u, u.nq - 1) : 0;
+    u.tiles = min(max((most + kTile - 1) / kTile - u.first_tile, 0), a.chunk);
+    return u;
+}
+
+// Cache row of key j, or -1 where the block table does not lead into the cache.
+__device__ __forceinline__ int64_t key_row(const IndexArgs &a, const Unit &u, int j)
+{
+    int64_t row;
+    if (a.layout_kv == SFM_LAYOUT_PAGED) {
+        const int page = (int)fdiv((uint32_t)j, a.block_div);
+        if (page >= a.table_stride) return -1;
+        const int32_t id = __ldg(a.table + (int64_t)u.b * a.table_stride + page);
+        row = id < 0 ? -1 : (int64_t)id * a.block + (j - page * a.block);
+    } else {
+        row = u.k_base + j;
+    }
+    return row < a.k_rows ? row : -1;
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ float clip(uint32_t x)          // max(0, x), NaN kept
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(__uint_as_float(x)));
+    return r;
+}
+
+// HP: columns per query
+template <int HP>
+__global__ void __launch_bounds__(kThreads, 1)
+sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map)
+{
+    constexpr int kQueries = 256 / HP;         // queries of a full tile
+    constexpr int kSums = HP <= 64 ? 64 / HP : 1;   // queries whose heads a 64-column part holds
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int parts = 1 << a.parts_log2;
+    const int queries = min(kQueries, parts * 64 / HP);
+    const uint32_t elem = a.fp8 ? 1 : 2;
+    const uint32_t q_rows = parts * 64;                       // rows of a Q buffer
+    const uint32_t q_bytes = q_rows * kDim * elem, k_bytes = kTile * kDim * elem;
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t q_smem = base, k_smem = base + 2 * q_bytes, misc = k_smem + a.stages * k_bytes;
+    const uint32_t bars = misc;
+    auto q_full = [&](int i) { return bars + 8u * i; };
+    auto q_empty = [&](int i) { return bars + 16u + 8u * i; };
+    auto k_full = [&](int i) { return bars + 32u + 8u * i; };
+    auto k_empty = [&](int i) { return bars + 96u + 8u * i; };
+    auto acc_full = [&](int i) { return bars + 160u + 8u * i; };
+    auto acc_empty = [&](int i) { return bars + 224u + 8u * i; };
+    auto half_full = [&](int w) { return bars + 288u + 8u * w; };  // HP 128: a part's sums are in shared memory
+    const uint32_t teardown = bars + 320u;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + (misc - base) + 336);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gbase + (misc - base) + 340);
+    float *half_sum = reinterpret_cast<float *>(gbase + (misc - base) + 384);     // [2 pairs][128]
+
+    const int accs = kMaxAcc >> a.parts_log2;                 // accumulator tiles of parts * 64 columns
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < 2; ++i) mbar_init(q_full(i), 1), mbar_init(q_empty(i), 1);
+        for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
+        for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), 4 * parts);
+        for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
+        mbar_init(teardown, 1);
+        fence_barrier_init();
+    }
+    if (a.heads != HP) {                                      // rows of padding heads: zeros that no load overwrites
+        for (uint32_t i = tid * 16; i < 2 * q_bytes; i += kThreads * 16)
+            *reinterpret_cast<uint4 *>(gbase + i) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    if (warp == 17) {
+        tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_ptr;
+
+    bool bad = false;
+    if (warp == 16) {
+        // ---------------- loads ----------------
+        int stage = 0, ks = 0, kphase = 0, n = 0;             // ks: stages filled so far (capped); n: units with tiles
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            const Unit u = unit_of(a, unit, queries, &bad);
+            if (u.tiles == 0) continue;
+            const int qb = n & 1;
+            ok = warp_wait(q_empty(qb), ((n >> 1) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            if (lane == 0) mbar_expect(q_full(qb), (uint32_t)(u.nq * a.heads) * kDim * elem);
+            __syncwarp();
+            for (int i = lane; i < u.nq; i += 32) {
+                const uint32_t dst = q_smem + qb * q_bytes + i * HP * 128;
+                const int row = (u.t0 + i) * a.heads;
+                tma_load(dst, &q_map, 0, row, q_full(qb));
+                if (!a.fp8) tma_load(dst + q_rows * 128, &q_map, 64, row, q_full(qb));
+            }
+            ++n;
+            for (int t = 0; t < u.tiles; ++t) {
+                const int j = (u.first_tile + t) * kTile + lane * a.run;
+                int64_t row = -1;
+                if (lane * a.run < kTile && j < u.len) row = key_row(a, u, j);
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                ok = warp_wait(k_empty(stage), kphase ^ 1, abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_expect(k_full(stage), boxes * a.run * kDim * elem);
+                __syncwarp();
+                if (row >= 0) {
+                    const uint32_t dst = k_smem + stage * k_bytes + lane * a.run * 128;
+                    tma_load(dst, &k_map, 0, (int)row, k_full(stage));
+                    if (!a.fp8) tma_load(dst + kTile * 128, &k_map, 64, (int)row, k_full(stage));
+                }
+                if (ks < a.stages) ++ks;
+                if (++stage == a.stages) stage = 0, kphase ^= 1;
+            }
+        }
+        if (!ok) {
+            // given up: the copies in flight must land before the CTA ends.  Every
+            // stage and query buffer that was filled is waited for, either phase.
+            const uint64_t t0 = globaltimer_ns();
+            for (int s = 0; s < ks; ++s) {
+                const int filled = s < stage ? kphase : kphase ^ 1;
+                while (!mbar_try_wait(k_full(s), filled) && globaltimer_ns() - t0 < kTimeoutNs) {
+                }
+            }
+            for (int q = 0; q < 2 && q < n; ++q) {
+                const int last = (n - 1 - q) >> 1, qb = (n - 1 - q) & 1;
+                while (!mbar_try_wait(q_full(qb), last & 1) && globaltimer_ns() - t0 < kTimeoutNs) {
+                }
+            }
+        }
+    } else if (warp == 17) {
+        // ---------------- products ----------------
+        int stage = 0, kphase = 0, acc = 0, aphase = 0, n = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            const Unit u = unit_of(a, unit, queries, &bad);
+            if (u.tiles == 0) continue;
+            const int qb = n & 1;
+            ok = warp_wait(q_full(qb), (n >> 1) & 1, abort_flag);
+            if (!ok) break;
+            const uint32_t idesc = a.idesc | ((uint32_t)(u.nq * HP >> 3) << 17);
+            const uint64_t bdesc = sdesc_sw128(q_smem + qb * q_bytes, 16, 1024);
+            for (int t = 0; t < u.tiles; ++t) {
+                ok = warp_wait(k_full(stage), kphase, abort_flag) && warp_wait(acc_empty(acc), aphase ^ 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t adesc = sdesc_sw128(k_smem + stage * k_bytes, 16, 1024);
+                    const uint32_t d = tmem + acc * (parts * 64);
+                    if (a.fp8) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) umma_f8(d, adesc + 2 * k, bdesc + 2 * k, idesc, k > 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            umma_f16(d, adesc + (k >> 2) * (kTile * 128 >> 4) + 2 * (k & 3),
+                                     bdesc + (k >> 2) * (q_rows * 128 >> 4) + 2 * (k & 3), idesc, k > 0);
+                    }
+                    umma_commit(k_empty(stage));
+                    umma_commit(acc_full(acc));
+                    if (t == u.tiles - 1) umma_commit(q_empty(qb));
+                }
+                __syncwarp();
+                if (++stage == a.stages) stage = 0, kphase ^= 1;
+                if (++acc == accs) acc = 0, aphase ^= 1;
+            }
+            ++n;
+        }
+        if (!ok && lane == 0) {
+            umma_commit(teardown);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(teardown, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- clipped sums ----------------
+        const int wg = warp >> 2, part = wg & (parts - 1);
+        const int turns = 4 >> a.parts_log2;                  // warpgroups that share a part take turns
+        const int turn = wg >> a.parts_log2;
+        const int i_part = HP <= 64 ? part * kSums : part >> 1;         // first query of this part
+        const int key_lane = (warp & 3) * 32 + lane;
+        int64_t done = 0;                                     // tiles of this CTA before the unit
+        int halves = 0;                                       // HP 128: exchanges so far
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            const Unit u = unit_of(a, unit, queries, &bad);
+            if (a.visible && u.first_tile == 0 && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
+            float w[64];
+            int vis[kSums];
+            if (u.tiles) {
+#pragma unroll
+                for (int q = 0; q < kSums; ++q) {
+                    const int i = i_part + q;
+                    vis[q] = visible_of(a, u, i);
+                    const float *src = a.weights + (int64_t)(u.t0 + i) * a.heads;
+#pragma unroll
+                    for (int h = 0; h < 64 / kSums; ++h) {
+                        const int hh = HP <= 64 ? h : h + 64 * (part & 1);
+                        w[q * (64 / kSums) + h] = i < u.nq && hh < a.heads ? __ldg(src + hh) : 0.f;
+                    }
+                }
+            }
+            for (int t = 0; t < u.tiles; ++t) {
+                const int64_t g = done + t;                   // the CTA's tile number
+                if ((int)(g & (turns - 1)) != turn) continue;
+                const int j = (u.first_tile + t) * kTile + key_lane;
+                const int64_t row = j < u.len ? key_row(a, u, j) : 0;
+                if (row < 0 && i_part < u.nq && j < visible_of(a, u, u.nq - 1) && a.status)
+                    atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
+                const float scale = a.k_scales && row >= 0 && j < u.len ? __ldg(a.k_scales + row) : 1.f;
+                const int acc = (int)(g & (accs - 1)), phase = (int)((g >> (3 - a.parts_log2)) & 1);
+                ok = warp_wait(acc_full(acc), phase, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                float sum[kSums];
+#pragma unroll
+                for (int q = 0; q < kSums; ++q) sum[q] = 0.f;
+                const uint32_t at = tmem + acc * (parts * 64) + part * 64 + ((uint32_t)((warp & 3) * 32) << 16);
+                const bool live = i_part < u.nq;
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[16];
+                        tmem_ld16(at + c * 16, r);
+                        tmem_wait_ld();
+                        if (c == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(acc_empty(acc));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            constexpr int kPer = 64 / kSums;
+                            sum[(c * 16 + e) / kPer] = fmaf(clip(r[e]), w[c * 16 + e], sum[(c * 16 + e) / kPer]);
+                        }
+                    }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty(acc));
+                }
+                if constexpr (HP == 128) {                    // the odd part hands its half to the even one
+                    float *mine = half_sum + (wg >> 1) * 128 + key_lane;
+                    if (part & 1) {
+                        ok = halves == 0 || warp_wait(half_full(wg ^ 1), (halves - 1) & 1, abort_flag);   // taken
+                        if (!ok) break;
+                        *mine = sum[0];
+                    } else {
+                        ok = warp_wait(half_full(wg ^ 1), halves & 1, abort_flag);
+                        if (!ok) break;
+                        sum[0] += *mine;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half_full(wg));
+                    ++halves;
+                    if (part & 1) continue;
+                }
+                if (live && j < a.max_k) {
+#pragma unroll
+                    for (int q = 0; q < kSums; ++q) {
+                        const int i = i_part + q;
+                        if (i < u.nq)
+                            a.scores[(int64_t)(u.t0 + i) * a.stride + j] =
+                                j < vis[q] && row >= 0 ? sum[q] * scale : -INFINITY;
+                    }
+                }
+            }
+            done += u.tiles;
+            if (!ok) break;
+            // columns that no product reached, and rows without a query
+            const int c0 = u.first_tile * kTile, c1 = min(c0 + a.chunk * kTile, a.max_k);
+            for (int i = warp; i < u.rows; i += kEpiWarps) {
+                float *dst = a.scores + (int64_t)(u.t0 + i) * a.stride;
+                for (int j = c0 + (i < u.nq ? u.tiles * kTile : 0) + lane; j < c1; j += 32) dst[j] = -INFINITY;
+            }
+        }
+        if (bad && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag && a.status) atomicOr(a.status, SFM_STATUS_TIMEOUT);
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+// the driver's encoder of TMA descriptors (a pure host function), looked up once
+EncodeFn encoder()
+{
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows)
+{
+    const EncodeFn encode = encoder();
+    if (!encode) return SFM_ERR_CUDA;
+    const bool fp8 = dtype == SFM_DTYPE_E4M3;
+    const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[2] = {kDim, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {fp8 ? 128u : 64u, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    const CUresult r = encode(map, type, 2, const_cast<void *>(ptr), dims, strides, box, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SFM_OK : SFM_ERR_CUDA;
+}
+
+template <int HP>
+cudaError_t launch(const IndexArgs &a, const CUtensorMap &q, const CUtensorMap &k, int grid, size_t smem, cudaStream_t st)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(sfm_index_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    sfm_index_kernel<HP><<<grid, kThreads, smem, st>>>(a, q, k);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sfm
+
+using namespace sfm;
+
+extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tensors *t, float *scores,
+                                int64_t score_stride, int32_t *visible, int32_t *status, sfm_stream_t stream)
+{
+    if (!pp || !t) return SFM_ERR_INVALID_ARG;
+    const sfm_index_params &p = *pp;
+    if (p.num_heads < 1 || p.num_heads > 128) return SFM_ERR_INVALID_ARG;
+    if (p.index_dim != kDim) return SFM_ERR_UNSUPPORTED;
+    if (p.dtype != SFM_DTYPE_BF16 && p.dtype != SFM_DTYPE_FP16 && p.dtype != SFM_DTYPE_E4M3) return SFM_ERR_INVALID_ARG;
+    if (p.layout_q != SFM_LAYOUT_BSND && p.layout_q != SFM_LAYOUT_TND) return SFM_ERR_LAYOUT;
+    if (p.layout_kv != SFM_LAYOUT_BSND && p.layout_kv != SFM_LAYOUT_TND && p.layout_kv != SFM_LAYOUT_PAGED)
+        return SFM_ERR_LAYOUT;
+    if (p.layout_kv != SFM_LAYOUT_PAGED && p.layout_kv != p.layout_q) return SFM_ERR_LAYOUT;
+    if (p.batch_size <= 0 || p.max_seqlen_q <= 0 || p.max_seqlen_kv <= 0 || p.cmp_ratio <= 0) return SFM_ERR_INVALID_ARG;
+    if (p.mask_mode != 0 && p.mask_mode != 3) return SFM_ERR_INVALID_ARG;
+    if (p.layout_q == SFM_LAYOUT_TND && p.total_q < 0) return SFM_ERR_INVALID_ARG;
+    const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
+    if (tokens * p.num_heads > INT32_MAX) return SFM_ERR_UNSUPPORTED;      // rows that a copy's coordinate names
+    const bool paged = p.layout_kv == SFM_LAYOUT_PAGED;
+    if (paged && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
+    if (score_stride < p.max_seqlen_kv) return SFM_ERR_LAYOUT;
+    const int elem = p.dtype == SFM_DTYPE_E4M3 ? 1 : 2;
+    if (t->k_row_stride < kDim * elem || t->k_row_stride % 16 || t->k_rows <= 0) return SFM_ERR_LAYOUT;
+    if (t->k_rows > ((int64_t)1 << 31) - 2) return SFM_ERR_UNSUPPORTED;
+    if (p.layout_q == SFM_LAYOUT_TND && !t->cu_seqlens_q) return SFM_ERR_INVALID_ARG;
+    if (p.layout_kv == SFM_LAYOUT_TND && !t->cu_seqlens_kv) return SFM_ERR_INVALID_ARG;
+    if (paged ? !t->seqused_kv || !t->block_table || t->block_table_stride <= 0 : t->block_table != nullptr)
+        return SFM_ERR_INVALID_ARG;
+    if (p.mask_mode == 3 && p.cmp_ratio > 1 && !t->cmp_residual_kv) return SFM_ERR_INVALID_ARG;
+    if (tokens == 0) return SFM_OK;
+    if (!t->q || !t->k || !t->weights || !scores) return SFM_ERR_INVALID_ARG;
+    if (((uintptr_t)t->q | (uintptr_t)t->k) & 15u) return SFM_ERR_LAYOUT;
+    if (((uintptr_t)t->k_scales | (uintptr_t)t->weights | (uintptr_t)scores | (uintptr_t)visible) & 3u)
+        return SFM_ERR_LAYOUT;
+
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SFM_ERR_CUDA;
+
+    const int hp = p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : p.num_heads <= 64 ? 64 : 128;
+    IndexArgs a = {};
+    a.weights = t->weights;
+    a.k_scales = t->k_scales;
+    a.scores = scores;
+    a.visible = visible;
+    a.status = status;
+    a.table = t->block_table;
+    a.table_stride = t->block_table_stride;
+    a.cu_q = p.layout_q == SFM_LAYOUT_TND ? t->cu_seqlens_q : nullptr;
+    a.cu_k = p.layout_kv == SFM_LAYOUT_TND ? t->cu_seqlens_kv : nullptr;
+    a.used_q = t->seqused_q;
+    a.used_k = t->seqused_kv;
+    a.residual = t->cmp_residual_kv;
+    a.stride = score_stride;
+    a.k_rows = t->k_rows;
+    a.heads = p.num_heads;
+    a.batch = p.batch_size;
+    a.max_q = p.max_seqlen_q;
+    a.total_q = p.total_q;
+    a.max_k = p.max_seqlen_kv;
+    a.ratio = p.cmp_ratio;
+    a.causal = p.mask_mode == 3;
+    a.layout_q = p.layout_q;
+    a.layout_kv = p.layout_kv;
+    a.block = p.block_size;
+    a.block_div = make_fastdiv(paged ? (uint32_t)p.block_size : 1u);
+    a.ratio_div = make_fastdiv((uint32_t)p.cmp_ratio);
+    a.fp8 = p.dtype == SFM_DTYPE_E4M3;
+
+    // 64-column parts of a tile: as many as one sequence's queries fill
+    const int64_t cols = (int64_t)p.max_seqlen_q * hp;
+    a.parts_log2 = cols <= 64 ? 0 : cols <= 128 ? 1 : 2;
+    const int queries = (64 << a.parts_log2) / hp;
+    // accumulate in fp32; types of A and B; M = 128
+    a.idesc = (1u << 4) | ((p.dtype == SFM_DTYPE_BF16 ? 1u : 0u) << 7) | ((p.dtype == SFM_DTYPE_BF16 ? 1u : 0u) << 10) |
+              ((uint32_t)(kTile >> 4) << 24);
+    // keys per box: the largest power of two that divides a page
+    a.run = kTile;
+    if (paged) {
+        a.run = p.block_size & -p.block_size;
+        if (a.run > kTile) a.run = kTile;
+    }
+    const uint32_t q_bytes = (64u << a.parts_log2) * kDim * elem, k_bytes = kTile * kDim * elem;
+    const int fit = (int)((kSmemLimit - 1024 - kMiscBytes - 2 * q_bytes) / k_bytes);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+
+    // units: some six per CTA, so that sequences of different lengths even out,
+    // but not more than 32 tiles
+    a.groups_per_seq = (p.max_seqlen_q + queries - 1) / queries;
+    const int64_t groups = (int64_t)a.groups_per_seq * p.batch_size;
+    const int64_t tiles = (p.max_seqlen_kv + kTile - 1) / kTile;
+    if (groups > INT32_MAX) return SFM_ERR_UNSUPPORTED;
+    int64_t chunk = groups * tiles / (6 * (int64_t)sms);
+    chunk = chunk < 1 ? 1 : chunk > 32 ? 32 : chunk;
+    const int64_t chunks = (tiles + chunk - 1) / chunk;
+    a.chunk = (int32_t)((tiles + chunks - 1) / chunks);
+    const int64_t units = groups * ((tiles + a.chunk - 1) / a.chunk);
+    if (units > INT32_MAX - sms) return SFM_ERR_UNSUPPORTED;
+    a.groups = (int32_t)groups;
+    a.units = (int32_t)units;
+
+    CUtensorMap q_map, k_map;
+    int rc = make_map(&q_map, t->q, p.dtype, tokens * p.num_heads, (int64_t)kDim * elem, p.num_heads);
+    if (!rc) rc = make_map(&k_map, t->k, p.dtype, t->k_rows, t->k_row_stride, a.run);
+    if (rc) return rc;
+    const size_t smem = 1024 + 2 * q_bytes + (size_t)a.stages * k_bytes + kMiscBytes;
+    const int grid = (int)(units < sms ? units : sms);
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    switch (hp) {
+    case 16: e = launch<16>(a, q_map, k_map, grid, smem, st); break;
+    case 32: e = launch<32>(a, q_map, k_map, grid, smem, st); break;
+    case 64: e = launch<64>(a, q_map, k_map, grid, smem, st); break;
+    default: e = launch<128>(a, q_map, k_map, grid, smem, st); break;
+    }
+    return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
+}

@@ -1,0 +1,341 @@
+// sfm_store.cu -- the write side of the caches: RMS norm, rotary positions,
+// quantisation and the store of each row at its slot (sfm_kv_store).
+//
+// Each value of x is read once and each cache byte written once, so memory
+// bounds it.  A group of lanes holds one row in registers, eight values (one
+// 16-byte load) per lane and step, so that 16 neighbouring lanes hold one
+// 128-value tile: the sum of squares and each tile's largest magnitude are
+// shuffles, and nothing but the cosines and (for half-layout pairs, which sit
+// in other lanes) the rotated part goes through shared memory.  Everything
+// is held in fp32 until the one rounding to the cache's format.
+#include <math.h>
+
+#include "sfm_internal.cuh"
+#include "sfm_rope.cuh"
+
+namespace sfm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 576;
+constexpr float kTiny = 0x1p-126f;
+
+struct StoreArgs {
+    const void *x;
+    const float *weight;
+    const int32_t *positions, *slots;
+    const double *inv_freq;
+    uint8_t *cache;
+    float *scales;
+    int32_t *status;
+    int64_t xt, xh, row_stride, rows, total;   // total: rows of x
+    int32_t heads, dim, norm_dim, rot, off, packed_rope;
+    FastDiv heads_div;
+    float eps, amplitude, inv_norm_dim;
+    int32_t norm, half;
+};
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ uint32_t s8x4(float a, float b, float c, float d)
+{
+    const float f[4] = {a, b, c, d};
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)__float2int_rn(fminf(fmaxf(f[i], -127.f), 127.f)) & 0xffu) << (8 * i);
+    return w;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// LANES lanes per row, STEPS 16-byte accesses per lane; FORMAT: enum sfm_kv_format
+template <typename T, int FORMAT, int LANES, int STEPS>
+__global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
+{
+    constexpr int kGroups = kThreads / LANES;
+    __shared__ unsigned long long step[kMaxDim / 2];
+    __shared__ float2 cs_all[kGroups][LANES * STEPS * 4 < kMaxDim / 2 ? LANES * STEPS * 4 : kMaxDim / 2];
+    extern __shared__ float turn_all[];          // half layout: [kGroups][rot]
+
+    const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
+    float2 *cs = cs_all[group];
+    float *turn = turn_all + group * a.rot;
+    const int pairs = a.rot / 2;
+    for (int i = tid; i < pairs; i += kThreads) step[i] = rope::turn_step(__ldg(a.inv_freq + i));
+    __syncthreads();
+
+    // a group takes a run of neighbouring rows, so that the heads of a token
+    // share its cosines
+    const int64_t groups = (int64_t)gridDim.x * kGroups;
+    const int64_t per = (a.total + groups - 1) / groups;
+    const int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * per;
+    const int64_t r1 = min(r0 + per, a.total);
+    int last_token = -1;
+    for (int64_t rr = r0; rr < r0 + per; ++rr) {     // every group runs the same count: warp collectives inside
+        const bool live = rr < r1;
+        const int64_t r = live ? rr : 0;
+        const int token = a.heads == 1 ? (int)r : (int)fdiv((uint32_t)r, a.heads_div);
+        const int head = (int)(r - (int64_t)token * a.heads);
+        const int64_t slot = a.slots ? (int64_t)__ldg(a.slots + token) : token;
+        const int64_t row = slot * a.heads + head;
+        const bool inside = slot >= 0 && row < a.rows;
+        if (live && slot >= 0 && !inside && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
+
+        float v[STEPS][8];
+        const T *src = static_cast<const T *>(a.x) + (int64_t)token * a.xt + (int64_t)head * a.xh;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int at = (s * LANES + lane) * 8;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live && at < a.dim) w = __ldg(reinterpret_cast<const uint4 *>(src + at));
+            rope::unpack8<T>(w, v[s]);
+        }
+
+        if (a.norm) {
+            float sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                if ((s * LANES + lane) * 8 < a.norm_dim) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum = fmaf(v[s][e], v[s][e], sum);
+                }
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            // 1 / sqrt: correctly rounded parts, so the norm costs no precision
+            const float rs = 1.f / sqrtf(fmaf(sum, a.inv_norm_dim, a.eps));
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int at = (s * LANES + lane) * 8;
+                if (at < a.norm_dim) {
+                    if (a.weight) {
+                        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + at));
+                        const float4 w1 = __ldg(reinterpret_cast<const float4 *>(a.weight + at + 4));
+                        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[s][e] = v[s][e] * rs * w[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[s][e] *= rs;
+                    }
+                }
+            }
+        }
+
+        if (pairs) {
+            __syncwarp();
+            if (token != last_token) {
+                const int32_t p = __ldg(a.positions + token);
+                for (int i = lane; i < pairs; i += LANES) cs[i] = rope::cos_sin(p, step[i], a.amplitude, false);
+                last_token = token;
+            }
+            if (a.half) {
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const int at = (s * LANES + lane) * 8 - a.off;
+                    if (at >= 0 && at < a.rot) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) turn[at + e] = v[s][e];
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int at = (s * LANES + lane) * 8 - a.off;
+                if (at < 0 || at >= a.rot) continue;
+                if (a.half) {
+                    const bool second = at >= pairs;
+                    const int i = second ? at - pairs : at;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float other = turn[second ? i + e : i + pairs + e];
+                        const float2 q = second ? rope::rotate(other, v[s][e], cs[i + e])
+                                                : rope::rotate(v[s][e], other, cs[i + e]);
+                        v[s][e] = second ? q.y : q.x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 q = rope::rotate(v[s][2 * e], v[s][2 * e + 1], cs[at / 2 + e]);
+                        v[s][2 * e] = q.x;
+                        v[s][2 * e + 1] = q.y;
+                    }
+                }
+            }
+        }
+
+        uint8_t *dst = a.cache + row * a.row_stride;
+        const bool write = live && inside;
+        if constexpr (FORMAT == SFM_KV_PLAIN) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int at = (s * LANES + lane) * 8;
+                if (write && at < a.dim) *reinterpret_cast<uint4 *>(dst + at * 2) = rope::pack8<T>(v[s]);
+            }
+        } else {
+            // largest magnitude per tile: 16 lanes of a step (packed) or the whole row (index rows)
+            constexpr bool kRow = FORMAT == SFM_KV_FP8_ROWS;
+            float most[STEPS];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                most[s] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most[s] = max_nan(most[s], fabsf(v[s][e]));
+            }
+            if (kRow) {
+#pragma unroll
+                for (int s = 1; s < STEPS; ++s) most[0] = max_nan(most[0], most[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < (kRow ? 1 : STEPS); ++s) {
+#pragma unroll
+                for (int o = (kRow ? LANES : 16) / 2; o > 0; o >>= 1)
+                    most[s] = max_nan(most[s], __shfl_xor_sync(0xffffffffu, most[s], o));
+            }
+            constexpr float kMost = FORMAT == SFM_KV_INT8_PACKED ? 127.f : 448.f;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int at = (s * LANES + lane) * 8;
+                if (!write || at >= a.dim) continue;
+                if (!kRow && at >= 512) {            // the packed row's rope values
+                    *reinterpret_cast<uint4 *>(dst + 512 + (at - 512) * 2) = rope::pack8<T>(v[s]);
+                    continue;
+                }
+                const float scale = max_nan(most[kRow ? 0 : s] / kMost, kTiny);
+                const float inv = 1.f / scale;
+                const float(&f)[8] = v[s];
+                uint2 w;
+                if (FORMAT == SFM_KV_INT8_PACKED) {
+                    w.x = s8x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                    w.y = s8x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+                } else {
+                    w.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                    w.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+                }
+                *reinterpret_cast<uint2 *>(dst + at) = w;
+                if (kRow) {
+                    if (at == 0) a.scales[row] = scale;
+                } else if (at % 128 == 0) {
+                    reinterpret_cast<float *>(dst + 512 + 2 * a.packed_rope)[at / 128] = scale;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int FORMAT, int LANES, int STEPS>
+cudaError_t launch(const StoreArgs &a, cudaStream_t st)
+{
+    constexpr int kGroups = kThreads / LANES;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.total + kGroups - 1) / kGroups, most = (int64_t)sms * 8;
+    const size_t smem = a.half ? (size_t)kGroups * a.rot * sizeof(float) : 0;
+    auto kernel = sfm_store_kernel<T, FORMAT, LANES, STEPS>;
+    kernel<<<(unsigned)(want < most ? want : most), kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const StoreArgs &a, int format, cudaStream_t st)
+{
+    switch (format) {
+    case SFM_KV_PLAIN:
+        return a.dim <= 128 ? launch<T, SFM_KV_PLAIN, 16, 1>(a, st) : launch<T, SFM_KV_PLAIN, 32, 2>(a, st);
+    case SFM_KV_FP8_ROWS:
+        return a.dim <= 128 ? launch<T, SFM_KV_FP8_ROWS, 16, 1>(a, st) : launch<T, SFM_KV_FP8_ROWS, 32, 2>(a, st);
+    case SFM_KV_INT8_PACKED:
+        return a.dim == 512 ? launch<T, SFM_KV_INT8_PACKED, 32, 2>(a, st) : launch<T, SFM_KV_INT8_PACKED, 32, 3>(a, st);
+    default:
+        return a.dim == 512 ? launch<T, SFM_KV_FP8_PACKED, 32, 2>(a, st) : launch<T, SFM_KV_FP8_PACKED, 32, 3>(a, st);
+    }
+}
+
+}  // namespace
+}  // namespace sfm
+
+using namespace sfm;
+
+extern "C" int sfm_kv_store(const sfm_store_params *pp, const void *x, const float *norm_weight,
+                            const int32_t *positions, const double *inv_freq, const int32_t *slots, void *cache,
+                            float *scales, int32_t *status, sfm_stream_t stream)
+{
+    if (!pp) return SFM_ERR_INVALID_ARG;
+    const sfm_store_params &p = *pp;
+    if (p.tokens < 0 || p.heads < 1 || p.reserved) return SFM_ERR_INVALID_ARG;
+    if (p.dtype != SFM_DTYPE_BF16 && p.dtype != SFM_DTYPE_FP16) return SFM_ERR_INVALID_ARG;
+    const bool packed = p.kv_format == SFM_KV_INT8_PACKED || p.kv_format == SFM_KV_FP8_PACKED;
+    int64_t row_bytes;
+    if (packed) {
+        if (p.head_dim != 512 && p.head_dim != 576) return SFM_ERR_INVALID_ARG;
+        row_bytes = 512 + 2 * (int64_t)(p.head_dim - 512) + 16;
+    } else if (p.kv_format == SFM_KV_PLAIN || p.kv_format == SFM_KV_FP8_ROWS) {
+        if (p.head_dim < 16 || p.head_dim > 512 || p.head_dim % 16) return SFM_ERR_INVALID_ARG;
+        row_bytes = (int64_t)p.head_dim * (p.kv_format == SFM_KV_PLAIN ? 2 : 1);
+    } else {
+        return SFM_ERR_INVALID_ARG;
+    }
+    if (p.norm != 0 && p.norm != 1) return SFM_ERR_INVALID_ARG;
+    if (p.norm && (!(p.norm_eps >= 0.f) || !isfinite(p.norm_eps))) return SFM_ERR_INVALID_ARG;
+    if (p.rope_dim < 0 || p.rope_dim % 16 || p.rope_offset < 0 || p.rope_offset % 8 ||
+        p.rope_offset > p.head_dim - p.rope_dim)
+        return SFM_ERR_INVALID_ARG;
+    if (p.rope_layout != SFM_ROPE_INTERLEAVED && p.rope_layout != SFM_ROPE_HALF) return SFM_ERR_INVALID_ARG;
+    if (p.rope_dim && !isfinite(p.amplitude)) return SFM_ERR_INVALID_ARG;
+    if (p.rows < 0 || p.rows > ((int64_t)1 << 31) - 2) return SFM_ERR_UNSUPPORTED;
+    if ((int64_t)p.tokens * p.heads > ((int64_t)1 << 31) - 2) return SFM_ERR_UNSUPPORTED;
+    if (p.row_stride < row_bytes || p.row_stride % 16) return SFM_ERR_LAYOUT;
+    if (p.x_token_stride < 0 || p.x_head_stride < 0 || p.x_token_stride % 8 || p.x_head_stride % 8)
+        return SFM_ERR_LAYOUT;
+    if (norm_weight && !p.norm) return SFM_ERR_INVALID_ARG;
+    if ((p.kv_format == SFM_KV_FP8_ROWS) != (scales != nullptr) && p.tokens > 0) return SFM_ERR_INVALID_ARG;
+    if (p.tokens == 0) return SFM_OK;
+    if (!x || !cache || (p.rope_dim && (!positions || !inv_freq))) return SFM_ERR_INVALID_ARG;
+    if (((uintptr_t)x | (uintptr_t)cache | (uintptr_t)norm_weight) & 15u) return SFM_ERR_LAYOUT;
+    if (((uintptr_t)positions | (uintptr_t)slots | (uintptr_t)scales) & 3u || (uintptr_t)inv_freq & 7u)
+        return SFM_ERR_LAYOUT;
+
+    StoreArgs a = {};
+    a.x = x;
+    a.weight = norm_weight;
+    a.positions = positions;
+    a.slots = slots;
+    a.inv_freq = inv_freq;
+    a.cache = static_cast<uint8_t *>(cache);
+    a.scales = scales;
+    a.status = status;
+    a.xt = p.x_token_stride;
+    a.xh = p.x_head_stride;
+    a.row_stride = p.row_stride;
+    a.rows = p.rows;
+    a.total = (int64_t)p.tokens * p.heads;
+    a.heads = p.heads;
+    a.dim = p.head_dim;
+    a.norm_dim = p.head_dim < 512 ? p.head_dim : 512;
+    a.rot = p.rope_dim;
+    a.off = p.rope_offset;
+    a.packed_rope = packed ? p.head_dim - 512 : 0;
+    a.heads_div = make_fastdiv((uint32_t)p.heads);
+    a.eps = p.norm_eps;
+    a.inv_norm_dim = 1.f / (float)a.norm_dim;
+    a.amplitude = p.amplitude;
+    a.norm = p.norm;
+    a.half = p.rope_dim && p.rope_layout == SFM_ROPE_HALF;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = p.dtype == SFM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, p.kv_format, st)
+                                                    : launch_type<__half>(a, p.kv_format, st);
+    return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
+}

@@ -1,0 +1,660 @@
+"""The operators around the attention on the GPU, against their definitions in
+64 bits (``_plain64``), and a run of them together with the attention.
+
+Tolerances, from the arithmetic (u = 2^-24, one fp32 rounding; e = half a step of
+the output type relative to the value):
+* rotation: a coefficient (cos or sin times the amplitude) is off by the angle's
+  error -- below 2^-31 pi of the truncated turn plus u pi of its rounding to fp32 --
+  and by sincospif's two steps and the product with the amplitude, together below
+  2^-21; the two products and the sum add 3 u of (|a| + |b|).  Bound: 2^-20 amplitude
+  (|a| + |b|), then e of the value.
+* RMS norm: the sum of squares of 512 values in runs of 24 and five shuffles is
+  off by at most 32 u, its square root by half of that, the division and the two
+  products by 5 u: below 2^-19 of the value.
+* a stored code: half a step of the code times the scale, beside the value's own
+  error (2^-19 of the tile's largest magnitude and, rotated, 2^-20 of the pair's);
+  for E4M3 half a step is 2^-4 of the value, or 2^-10 scales below the normal range.
+* scores: 128 products per head, exact, added in fp32 by the tensor cores, each
+  step off by at most 2^-23 of the magnitudes so far, then at most 128 + 2 fp32
+  steps over the heads: (128 2^-23 + 130 u) of the sum of all magnitudes.
+* selected indices are whole numbers and equal.
+"""
+import math
+
+import pytest
+import torch
+
+import oracle
+import sfm_inputs as S
+import sparse_shared_kv_gb300 as sfm
+from tests import _plain64 as P, _sfm
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+SCORE_TOL = 128 * 2.0 ** -23 + 130 * 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp8": torch.float8_e4m3fn}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    sfm.build()
+    torch.cuda.init()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(g, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=g).to(dtype)
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def floor_of(dtype):
+    """Half the step of the smallest values of the type."""
+    return torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+
+
+def assert_within(got, want, bound, what=""):
+    off = (got.detach().cpu().to(F64) - want).abs()
+    bad = ~(off <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} values off, worst {float((off / bound.clamp(min=1e-300)).max()):.3g} bounds"
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def rope_check(got, x, pos, f, off, inter, inv, amp):
+    want, mag = P.rope_parts(x.cpu(), pos.cpu().tolist(), f.cpu(), off, inter, inv, amp)
+    turned = mag > 0
+    bound = torch.where(turned, 2.0 ** -20 * abs(amp) * mag * (1 + half_step(x.dtype)) + half_step(x.dtype) * want.abs()
+                        + floor_of(x.dtype), 0.0)
+    assert_within(got, want, bound, "rope")
+
+
+# tokens, heads, dim, rot, offset
+ROPE_SHAPES = [(1, 1, 64, 64, 0), (3, 5, 128, 64, 0), (17, 2, 576, 64, 512), (2, 128, 512, 64, 448), (33, 3, 192, 128, 64),
+               (700, 1, 64, 16, 48), (5, 3, 20, 10, 6), (4, 2, 66, 2, 64), (2, 1, 4096, 4096, 0), (3, 7, 130, 24, 8)]
+
+
+@pytest.mark.parametrize("shape", ROPE_SHAPES, ids=str)
+@pytest.mark.parametrize("inter", [True, False], ids=["pairs", "halves"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_rope(shape, inter, dt):
+    T, H, D, rot, off = shape
+    g = gen(T * 1000 + D)
+    x = randn(g, T, H, D, dtype=DT[dt]).cuda()
+    pos = torch.randint(-(1 << 31), (1 << 31) - 1, (T,), generator=g, dtype=torch.int64).to(torch.int32)
+    pos[0] = 0 if T % 2 else (1 << 31) - 1
+    f, _ = sfm.rope_frequencies(rot, device="cuda")
+    for inv, amp in ((False, 1.0), (True, 1.25)):
+        y = sfm.apply_rope(x, pos.cuda(), f, rope_offset=off, interleaved=inter, inverse=inv, amplitude=amp)
+        rope_check(y, x, pos, f, off, inter, inv, amp)
+        z = x.clone()
+        assert sfm.apply_rope(z, pos.cuda(), f, rope_offset=off, interleaved=inter, inverse=inv, amplitude=amp, out=z) is z
+        assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("inter", [True, False], ids=["pairs", "halves"])
+def test_rope_strided_views(inter):
+    g = gen(5)
+    big = randn(g, 6, 4, 520, dtype=torch.bfloat16).cuda()
+    pos = torch.tensor([0, 1, 7, 4095, 100000, 999999], dtype=torch.int32)
+    f, amp = sfm.rope_frequencies(32, scaling="yarn", factor=16.0, original_max_position=4096, device="cuda")
+    for x in (big[..., 456:], big[..., 3:67], big[:, 1:3, 8:136], big.transpose(0, 1).contiguous().transpose(0, 1)[..., 8:72]):
+        before = big.clone()
+        rope_check(sfm.apply_rope(x, pos.cuda(), f, interleaved=inter, amplitude=amp), x, pos, f, 0, inter, False, amp)
+        out = torch.full((6, x.shape[1], x.shape[2] + 5), 7.0, dtype=x.dtype, device="cuda")
+        got = sfm.apply_rope(x, pos.cuda(), f, interleaved=inter, amplitude=amp, out=out[..., :x.shape[2]])
+        rope_check(got, x, pos, f, 0, inter, False, amp)
+        assert bool((out[..., x.shape[2]:] == 7.0).all()) and torch.equal(big, before)
+    # broadcast heads are fine to read, in place they are refused
+    one = big[:, :1, :64].expand(6, 4, 64)
+    rope_check(sfm.apply_rope(one, pos.cuda(), f, interleaved=inter), one, pos, f, 0, inter, False, 1.0)
+    with pytest.raises(sfm.SfmError):
+        sfm.apply_rope(one, pos.cuda(), f, out=one)
+
+
+def test_rope_gradient_is_the_inverse_call():
+    g = gen(9)
+    x, gy = randn(g, 3, 2, 64, dtype=torch.float16).cuda(), randn(g, 3, 2, 64, dtype=torch.float16).cuda()
+    pos = torch.tensor([3, 70000, -5], dtype=torch.int32)
+    f, _ = sfm.rope_frequencies(32, device="cuda")
+    for inter in (True, False):
+        gx = sfm.apply_rope(gy, pos.cuda(), f, rope_offset=16, interleaved=inter, inverse=True, amplitude=1.5)
+        # differences of the formula's <y, gy>, which is linear in x: exact up to 64-bit rounding
+        def loss(v):
+            return float((P.rope_parts(v, pos.tolist(), f.cpu(), 16, inter, False, 1.5)[0] * gy.cpu().to(F64)).sum())
+        base = torch.zeros(3, 2, 64, dtype=F64)
+        for at in ((0, 0, 0), (0, 1, 16), (1, 0, 17), (1, 1, 40), (2, 0, 47), (2, 1, 63)):
+            e = base.clone()
+            e[at] = 1.0
+            d = (loss(e) - loss(-e)) / 2
+            lim = half_step(torch.float16) * abs(d) + 2.0 ** -20 * 1.5 * 8 + floor_of(torch.float16)
+            assert abs(float(gx[at]) - d) <= lim, at
+        # amplitude 1: there and back, two roundings of each member of a pair
+        back = sfm.apply_rope(sfm.apply_rope(x, pos.cuda(), f, interleaved=inter), pos.cuda(), f, interleaved=inter, inverse=True)
+        _, mag = P.rope_parts(x.cpu(), pos.tolist(), f.cpu(), 0, inter)
+        lim = 2 * half_step(torch.float16) * mag * 1.01 + half_step(torch.float16) * x.cpu().to(F64).abs() + 2.0 ** -18 * mag
+        assert_within(back, x.cpu().to(F64), torch.where(mag > 0, lim + 2 * floor_of(torch.float16), 0.0))
+
+
+def test_rope_without_tokens_and_on_another_stream():
+    f, _ = sfm.rope_frequencies(64, device="cuda")
+    assert sfm.apply_rope(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"),
+                          torch.empty(0, dtype=torch.int32, device="cuda"), f).shape == (0, 4, 64)
+    g = gen(2)
+    x, pos = randn(g, 64, 8, 128, dtype=torch.bfloat16).cuda(), torch.arange(64, dtype=torch.int32).cuda()
+    want = sfm.apply_rope(x, pos, f)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for given in (s, s.cuda_stream):
+        y = sfm.apply_rope(x, pos, f, stream=given)
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------------------
+# cache rows
+# ---------------------------------------------------------------------------
+FORMATS = {"plain": sfm.KV_PLAIN, "int8": sfm.KV_INT8_PACKED, "fp8": sfm.KV_FP8_PACKED, "rows": sfm.KV_FP8_ROWS}
+
+
+def make_cache(fmt, rows, dim, dtype, pad=0):
+    """A cache of recognisable bytes; pad: extra bytes between rows (a multiple of 16)."""
+    if fmt == "plain":
+        kind, width = dtype, dim
+    elif fmt == "rows":
+        kind, width = torch.float8_e4m3fn, dim
+    else:
+        kind, width = torch.uint8, 512 + 2 * (dim - 512) + 16
+    e = 2 if fmt == "plain" else 1
+    raw = torch.full((rows, width * e + pad), 0x33, dtype=torch.uint8, device="cuda")
+    return raw, raw[:, :width * e].view(kind) if kind != torch.uint8 else raw[:, :width]
+
+
+def check_rows(fmt, cache, scales, rows, values, mag, dtype, amp=1.0):
+    """Rows `rows` of the cache hold `values` (n, dim; 64 bits) within the format's rounding."""
+    c = cache[rows.cuda()].cpu()
+    n, D = values.shape
+    u = values.abs() * 2.0 ** -19 + 2.0 ** -20 * abs(amp) * mag
+
+    def plain_bound(v, err, dt):
+        return half_step(dt) * (v.abs() + err) + err + floor_of(dt)
+    if fmt == "plain":
+        assert_within(c, values, plain_bound(values, u, dtype), "plain")
+        return
+    nd = D if fmt == "rows" else 512
+    tile = nd if fmt == "rows" else 128
+    most = 127.0 if fmt == "int8" else 448.0
+    t, tu = values[:, :nd].reshape(n, -1, tile), u[:, :nd].reshape(n, -1, tile)
+    if fmt == "rows":
+        got_scale = scales[rows.cuda()].cpu().to(F64)[:, None]
+    else:
+        got_scale = c[:, -16:].contiguous().view(torch.float32).to(F64)
+    want_scale = (t.abs().amax(-1) / most).clamp(min=P.TINY)
+    err = tu.amax(-1)
+    assert_within(got_scale, want_scale, err / most + 2.0 ** -22 * want_scale + 2.0 ** -149, "scale")
+    codes = c[:, :nd].contiguous()
+    codes = codes.view(torch.int8).to(F64) if fmt == "int8" else codes.view(torch.float8_e4m3fn).to(torch.float32).to(F64)
+    if fmt == "int8":
+        assert int(codes.abs().max()) <= 127
+    back = codes.reshape(n, -1, tile) * got_scale[..., None]
+    s = got_scale[..., None]
+    # value / scale is rounded twice in fp32 (the reciprocal and the product) before the code's own rounding
+    q = t.abs() * 2.0 ** -22 + tu
+    bound = s / 2 + q if fmt == "int8" else 2.0 ** -4 * (t.abs() + q) + q + 2.0 ** -10 * s
+    assert_within(back, t, bound, fmt)
+    if D > nd:
+        rope = c[:, 512:512 + 2 * (D - 512)].contiguous().view(dtype)
+        assert_within(rope, values[:, 512:], plain_bound(values[:, 512:], u[:, 512:], dtype), "rope part")
+
+
+STORE_CASES = [   # format, dim, rot, offset, interleaved, heads
+    ("plain", 512, 64, 448, True, 1), ("plain", 512, 512, 0, False, 1), ("plain", 512, 0, 0, True, 1),
+    ("plain", 128, 64, 0, False, 1), ("plain", 16, 16, 0, True, 3), ("plain", 272, 32, 8, False, 1),
+    ("int8", 576, 64, 512, True, 1), ("int8", 576, 64, 512, False, 1), ("int8", 512, 0, 0, True, 1),
+    ("int8", 512, 64, 448, False, 1), ("fp8", 576, 64, 512, True, 1), ("fp8", 576, 576, 0, False, 1),
+    ("fp8", 512, 32, 480, True, 1), ("rows", 128, 64, 0, False, 1), ("rows", 128, 64, 64, True, 5),
+    ("rows", 512, 64, 448, True, 1), ("rows", 48, 0, 0, True, 64),
+]
+
+
+@pytest.mark.parametrize("case", STORE_CASES, ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tokens", [1, 37])
+def test_store(case, dt, tokens):
+    fmt, D, rot, off, inter, H = case
+    g = gen(D * 7 + tokens)
+    dtype = DT[dt]
+    x = randn(g, tokens, H, D, dtype=dtype) * (0.1 + torch.rand(tokens, 1, 1, generator=g).to(dtype))
+    x = x.to(dtype)
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g).to(torch.int32)
+    f = sfm.rope_frequencies(rot, device="cuda")[0] if rot else None
+    slots = torch.randperm(tokens + 11, generator=g)[:tokens].to(torch.int32)
+    if tokens > 1:
+        slots[5] = -1
+        slots[tokens - 1] = -7
+    rows = (tokens + 11) * H
+    for norm in (False, True):
+        w = 1 + 0.2 * randn(g, min(D, 512)) if norm and tokens > 1 else None
+        raw, cache = make_cache(fmt, rows, D, dtype, pad=32)
+        scales = torch.full((rows,), 9.0, device="cuda") if fmt == "rows" else None
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sfm.store_kv(x.cuda(), cache, slot_mapping=slots.cuda(), kv_format=FORMATS[fmt], norm_weight=w.cuda() if w is not None else None,
+                     norm_eps=1e-5 if norm else None, positions=pos.cuda() if rot else None, inv_freq=f,
+                     rope_offset=off if rot else None, interleaved=inter, scales=scales, status=status)
+        v, mag = P.store_values(x, w, 1e-5 if norm else None, pos.tolist(), f.cpu() if rot else None, off, inter)
+        if norm and rot:      # the pair's magnitudes after the norm
+            _, mag = P.rope_parts(P.store_values(x, w, 1e-5, None, None, 0, True)[0], pos.tolist(), f.cpu(), off, inter)
+        keep = slots >= 0
+        at = (slots[keep].long()[:, None] * H + torch.arange(H)).reshape(-1)
+        check_rows(fmt, cache, scales, at, v[keep].reshape(-1, D), mag[keep].reshape(-1, D), dtype)
+        assert int(status) == 0
+        left = torch.ones(rows, dtype=torch.bool)
+        left[at] = False
+        assert bool((raw[left.cuda()] == 0x33).all()), "rows that no slot names"
+        assert bool((raw[:, -32:] == 0x33).all()), "bytes between rows"
+        if scales is not None:
+            assert bool((scales[left.cuda()] == 9.0).all())
+
+
+@pytest.mark.parametrize("fmt,D", [("plain", 512), ("int8", 576), ("fp8", 512), ("rows", 128)])
+def test_store_slots_outside_the_cache(fmt, D):
+    g = gen(3)
+    x = randn(g, 6, 1, D, dtype=torch.bfloat16).cuda()
+    raw, cache = make_cache(fmt, 4, D, torch.bfloat16)
+    scales = torch.full((4,), 9.0, device="cuda") if fmt == "rows" else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([4, 2, (1 << 31) - 1, -(1 << 31), 0, -1], dtype=torch.int32).cuda()
+    sfm.store_kv(x, cache, slot_mapping=slots, kv_format=FORMATS[fmt], scales=scales, status=status)
+    assert int(status) == sfm.STATUS_BAD_BLOCK
+    check_rows(fmt, cache, scales, torch.tensor([2, 0]), x.cpu()[[1, 4], 0].to(F64), torch.zeros(2, D, dtype=F64), torch.bfloat16)
+    assert bool((raw[[1, 3]] == 0x33).all())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "rows"])
+def test_store_extreme_tiles(fmt):
+    """Zero tiles, tiny ones, large ones, and a NaN that spoils its own tile alone."""
+    D = 128 if fmt == "rows" else 512
+    x = torch.zeros(5, 1, D, dtype=torch.bfloat16)
+    x[1, 0, :7] = 2.0 ** -130
+    x[2, 0, ::3] = 3e38
+    x[2, 0, 1] = -3e38
+    x[3, 0] = 1.0
+    x[3, 0, 5] = math.nan
+    x[4, 0, 9] = math.inf
+    raw, cache = make_cache(fmt, 5, D, torch.bfloat16)
+    scales = torch.zeros(5, device="cuda") if fmt == "rows" else None
+    sfm.store_kv(x.cuda(), cache, kv_format=FORMATS[fmt], scales=scales)
+    check_rows(fmt, cache, scales, torch.tensor([0, 1, 2]), x[:3, 0].to(F64), torch.zeros(3, D, dtype=F64), torch.bfloat16)
+    got = scales[:, None] if fmt == "rows" else cache[:, -16:].contiguous().view(torch.float32)
+    assert bool(got[3, :1].isnan().all()) and bool(got[3, 1:].isfinite().all()) and bool(got[4, :1].isinf().all())
+    assert bool((raw[0, :D] == 0).all())
+
+
+def test_store_without_tokens_and_noncontiguous_input():
+    raw, cache = make_cache("plain", 3, 512, torch.bfloat16)
+    sfm.store_kv(torch.empty(0, 512, dtype=torch.bfloat16, device="cuda"), cache)
+    assert bool((raw == 0x33).all())
+    g = gen(1)
+    wide = randn(g, 3, 1024, dtype=torch.bfloat16).cuda()
+    sfm.store_kv(wide[:, 512:], cache)
+    assert torch.equal(cache, wide[:, 512:])
+    with pytest.raises(sfm.SfmError):
+        sfm.store_kv(wide[:, 4:516], cache)          # rows off their 16-byte boundaries
+    with pytest.raises(ValueError):
+        sfm.store_kv(wide[:, ::2], cache)
+    with pytest.raises(ValueError):
+        sfm.store_kv(wide[:, :512], cache, kv_format=sfm.KV_FP8_ROWS)
+
+
+# ---------------------------------------------------------------------------
+# index scores
+# ---------------------------------------------------------------------------
+def index_problem(seed, dt, heads, q_lens, lens, layout_q, layout_kv, block=64, ratio=1, pad=0, scales=None):
+    """Keys of every sequence, and the same keys in a cache of the layout."""
+    g = gen(seed)
+    dtype = DT[dt]
+    B = len(lens)
+
+    def values(*shape):
+        return (randn(g, *shape) * (50 if dt == "fp8" else 1)).clamp(-448, 448).to(dtype)
+    keys = [values(n, 128) for n in lens]
+    scales = dt == "fp8" if scales is None else scales
+    ks = [0.01 + torch.rand(n, generator=g) for n in lens]
+    maxk = max(max(lens), 1)
+    if layout_kv == "PAGED":
+        pages = [-(-n // block) for n in lens]
+        total, cols = sum(pages) + 2, max(max(pages), 1)
+        perm = torch.randperm(total, generator=g)
+        table, pool, pool_s = torch.zeros(B, cols, dtype=torch.int32), torch.full((total * block, 128), math.nan), torch.full((total * block,), math.nan)
+        at = 0
+        for b, n in enumerate(lens):
+            table[b, :pages[b]] = perm[at:at + pages[b]]
+            at += pages[b]
+            j = torch.arange(n)
+            row = table[b].long()[j // block] * block + j % block
+            pool[row], pool_s[row] = keys[b].float(), ks[b]
+        shape = (total, block)
+    elif layout_kv == "TND":
+        pool, pool_s, table, shape = torch.cat(keys).float(), torch.cat(ks), None, (sum(lens),)
+    else:
+        pool, pool_s, table, shape = torch.full((B * maxk, 128), math.nan), torch.full((B * maxk,), math.nan), None, (B, maxk)
+        for b, n in enumerate(lens):
+            pool[b * maxk:b * maxk + n], pool_s[b * maxk:b * maxk + n] = keys[b].float(), ks[b]
+    wide = torch.zeros(pool.shape[0], 128 + pad).to(dtype)
+    wide.view(torch.uint8)[:, :128 * wide.element_size()] = pool.to(dtype).view(torch.uint8)
+    cache = wide.cuda()[:, :128].unflatten(0, shape)
+    S_ = max(q_lens)
+    tokens = len(lens) * S_ if layout_q == "BSND" else sum(q_lens)
+    q, w = values(tokens, heads, 128), randn(g, tokens, heads)
+    first = [b * S_ for b in range(B)] if layout_q == "BSND" else [sum(q_lens[:b]) for b in range(B)]
+    rest = [int(torch.randint(0, ratio, (1,), generator=g)) for _ in lens]
+
+    def ints(v):
+        return torch.tensor(v, dtype=torch.int32).cuda()
+    kw = dict(max_seqlen_kv=maxk, layout_q=layout_q, layout_kv=layout_kv, cmp_ratio=ratio, cmp_residual_kv=ints(rest),
+              k_scales=pool_s.cuda().contiguous() if scales else None)
+    if layout_kv == "PAGED":
+        kw.update(block_table=table.cuda(), seqused_kv=ints(lens))
+    elif layout_kv == "TND":
+        kw.update(cu_seqlens_kv=ints([sum(lens[:b]) for b in range(B + 1)]))
+    else:
+        kw.update(seqused_kv=ints(lens))
+    if layout_q == "TND":
+        kw.update(cu_seqlens_q=ints([sum(q_lens[:b]) for b in range(B + 1)]), max_seqlen_q=S_)
+    qd = q.cuda().view(B, S_, heads, 128) if layout_q == "BSND" else q.cuda()
+    wd = w.cuda().view(B, S_, heads) if layout_q == "BSND" else w.cuda()
+    return dict(q=q, w=w, keys=keys, ks=ks if scales else [None] * B, first=first, rest=rest, kw=kw, qd=qd, wd=wd,
+                cache=cache, tokens=tokens, maxk=maxk, S=S_)
+
+
+def check_scores(p, q_lens, lens, ratio, causal, got, seen, used_q=None):
+    got, seen = got.cpu(), seen.cpu()
+    for b, n in enumerate(lens):
+        ql = used_q[b] if used_q else q_lens[b]
+        vis = P.visible(ql, n, ratio, p["rest"][b], causal)
+        t0 = p["first"][b]
+        rows = p["S"] if p["kw"]["layout_q"] == "BSND" else q_lens[b]
+        assert seen[t0:t0 + rows].tolist() == vis + [0] * (rows - ql), f"sequence {b}"
+        want, mag = P.scores(p["q"][t0:t0 + ql], p["keys"][b], p["w"][t0:t0 + ql], p["ks"][b])
+        block = got[t0:t0 + rows]
+        shown = torch.arange(p["maxk"])[None] < torch.tensor(vis + [0] * (rows - ql))[:, None]
+        assert bool(torch.isneginf(block[~shown]).all()), f"sequence {b}: hidden keys"
+        if ql and n:
+            s = shown[:ql, :n]
+            assert_within(block[:ql, :n][s], want[s], SCORE_TOL * mag[s] + 1e-30, f"sequence {b}")
+
+
+INDEX_CASES = [   # dtype, heads, q_lens, key counts, layouts, block, ratio
+    ("bf16", 64, [1, 1, 1], [1, 127, 300], "BSND", "PAGED", 64, 1), ("fp8", 64, [1, 1], [1000, 129], "BSND", "PAGED", 128, 4),
+    ("fp16", 64, [5, 5], [700, 64], "BSND", "PAGED", 16, 4), ("bf16", 1, [3], [200], "BSND", "PAGED", 48, 1),
+    ("bf16", 5, [40], [260], "TND", "PAGED", 1024, 1), ("fp8", 16, [33, 1, 0, 7], [130, 50, 9, 0], "TND", "PAGED", 32, 1),
+    ("bf16", 24, [9, 2], [300, 128], "TND", "TND", 0, 1), ("fp16", 32, [17, 17], [256, 77], "BSND", "BSND", 0, 2),
+    ("bf16", 100, [3, 1], [400, 33], "TND", "PAGED", 64, 4), ("fp8", 128, [7], [513], "BSND", "PAGED", 64, 1),
+    ("bf16", 128, [1, 1], [640, 250], "BSND", "PAGED", 128, 1), ("bf16", 128, [2, 2], [140, 250], "BSND", "PAGED", 128, 1),
+    ("bf16", 64, [130], [1500], "TND", "TND", 0, 1), ("fp8", 33, [4], [90], "BSND", "BSND", 0, 1),
+    ("bf16", 8, [16], [385], "BSND", "PAGED", 80, 1), ("fp16", 64, [2, 2], [5000, 129], "BSND", "PAGED", 64, 4),
+]
+
+
+@pytest.mark.parametrize("case", INDEX_CASES, ids=str)
+@pytest.mark.parametrize("mask", [3, 0])
+def test_index_scores(case, mask):
+    dt, heads, q_lens, lens, lq, lkv, block, ratio = case
+    p = index_problem(17 + heads, dt, heads, q_lens, lens, lq, lkv, block, ratio)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], mask_mode=mask, status=status, **p["kw"])
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    check_scores(p, q_lens, lens, ratio, mask == 3, got, seen)
+    again, _ = sfm.index_scores(p["qd"], p["cache"], p["wd"], mask_mode=mask, **p["kw"])
+    assert torch.equal(got, again)
+
+
+def test_index_scores_padded_rows_strided_output_and_used_queries():
+    for dt, scales in (("bf16", True), ("fp8", False)):
+        p = index_problem(3, dt, 64, [6, 6], [300, 40], "BSND", "PAGED", 64, 1, pad=16, scales=scales)
+        used = [4, 0]
+        wide = torch.full((12, p["maxk"] + 7), 5.0, device="cuda")
+        got, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], out=wide[:, :p["maxk"]],
+                                     seqused_q=torch.tensor(used, dtype=torch.int32).cuda(), **p["kw"])
+        check_scores(p, [6, 6], [300, 40], 1, True, got, seen, used)
+        assert bool((wide[:, p["maxk"]:] == 5.0).all())
+
+
+def test_index_scores_rows_behind_the_last_sequence_stay():
+    p = index_problem(4, "bf16", 16, [5, 3], [70, 30], "TND", "PAGED", 16)
+    q = torch.cat((p["qd"], p["qd"][:4]))
+    w = torch.cat((p["wd"], p["wd"][:4]))
+    out = torch.full((12, p["maxk"]), 5.0, device="cuda")
+    vis = torch.full((12,), -9, dtype=torch.int32, device="cuda")
+    sfm.index_scores(q, p["cache"], w, out=out, visible=vis, **p["kw"])
+    check_scores(p, [5, 3], [70, 30], 1, True, out[:8], vis[:8])
+    assert bool((out[8:] == 5.0).all()) and vis[8:].tolist() == [-9] * 4
+
+
+def test_index_scores_bad_blocks_and_lengths():
+    p = index_problem(5, "bf16", 64, [1, 1], [300, 200], "BSND", "PAGED", 64)
+    p["kw"]["block_table"][0, 2] = 1 << 20
+    p["kw"]["block_table"][1, 0] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], status=status, **p["kw"])
+    assert int(status) == sfm.STATUS_BAD_BLOCK and seen.tolist() == [300, 200]
+    want, mag = P.scores(p["q"], p["keys"][0], p["w"])
+    lost = (torch.arange(300) // 64) == 2
+    assert bool(torch.isneginf(got[0, :300].cpu()[lost]).all())
+    assert_within(got[0, :300].cpu()[~lost], want[0][~lost], SCORE_TOL * mag[0][~lost])
+    assert bool(torch.isneginf(got[1, :64]).all()) and bool(torch.isfinite(got[1, 64:200]).all())
+    p = index_problem(5, "bf16", 64, [1, 1], [300, 200], "BSND", "PAGED", 64)
+    p["kw"]["seqused_kv"][1] = 5000
+    status.zero_()
+    _, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], status=status, **p["kw"])
+    assert int(status) & sfm.STATUS_BAD_LENGTH and seen.tolist() == [300, 300]
+
+
+def test_index_scores_keep_nan_and_infinities_where_they_are():
+    p = index_problem(6, "bf16", 64, [2], [300], "BSND", "BSND")
+    clean, _ = sfm.index_scores(p["qd"], p["cache"], p["wd"], **p["kw"])
+    dirty = p["cache"].clone()
+    dirty[0, 7, 3] = math.nan
+    dirty[0, 200, 5] = math.inf
+    got, _ = sfm.index_scores(p["qd"], dirty, p["wd"], **p["kw"])
+    assert bool(got[:, 7].isnan().all()) and bool((~got[:, 200].isfinite()).all())
+    keep = torch.ones(300, dtype=torch.bool)
+    keep[[7, 200]] = False
+    assert torch.equal(got[:, keep.cuda()], clean[:, keep.cuda()])
+
+
+# ---------------------------------------------------------------------------
+# selection
+# ---------------------------------------------------------------------------
+def topk_check(x, k, lengths=None, **kw):
+    got = sfm.select_topk(x, k, lengths=lengths, **kw).cpu()
+    host = x.cpu().tolist()
+    ends = lengths.cpu().tolist() if lengths is not None else [x.shape[1]] * len(host)
+    for r, row in enumerate(host):
+        want = P.topk(row, k, ends[r], kw.get("block_size", 1), kw.get("first_blocks", 0), kw.get("last_blocks", 0))
+        assert got[r].tolist() == want, f"row {r}"
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 100, 1000, 4097, 20001])
+@pytest.mark.parametrize("k", [1, 8, 512, 2048])
+def test_topk(n, k):
+    g = gen(n + k)
+    x = torch.stack([randn(g, n), (randn(g, n) + 1).relu(), (randn(g, n) * 3).round(), torch.zeros(n),
+                     torch.where(torch.rand(n, generator=g) < 0.9, -math.inf, randn(g, n))]).cuda()
+    topk_check(x, k)
+    topk_check(x, k, torch.tensor([n, n // 2, 0, 1, n - n // 3], dtype=torch.int32).cuda())
+
+
+def test_topk_special_values():
+    inf, nan, low = math.inf, math.nan, torch.finfo(torch.float32).min
+    rows = [[nan, 1.0, -inf, 2.0, nan, inf], [-inf] * 6, [nan] * 6, [low, -inf, low, 0.0, -0.0, 1e-45], [-0.0, 0.0, -0.0, 0.0, -1e-45, nan],
+            [inf, inf, -1.0, inf, inf, inf]]
+    x = torch.tensor(rows).cuda()
+    for k in (1, 2, 3, 4, 6, 9):
+        topk_check(x, k)
+
+
+@pytest.mark.parametrize("block", [2, 4, 16, 64, 128])
+@pytest.mark.parametrize("n", [1, 130, 1000, 9001])
+def test_topk_blocks(block, n):
+    g = gen(n + block)
+    x = torch.stack([randn(g, n), (randn(g, n) * 2).round(), torch.full((n,), -math.inf), randn(g, n)]).cuda()
+    x[3, ::2] = math.nan
+    lengths = torch.tensor([n, max(n - 5, 0), n, n // 2], dtype=torch.int32).cuda()
+    for k, first, last in ((1, 0, 0), (8, 1, 2), (40, 0, 3), (3, 3, 0), (4, 2, 2)):
+        topk_check(x, k, None, block_size=block, first_blocks=first, last_blocks=last)
+        topk_check(x, k, lengths, block_size=block, first_blocks=first, last_blocks=last)
+
+
+def test_topk_strided_rows_and_bad_lengths():
+    g = gen(8)
+    wide = randn(g, 5, 1003).cuda()
+    topk_check(wide[:, 1:1000], 100)
+    topk_check(wide[::2, :997], 100)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([-3, 2000, 5, 0, 1003], dtype=torch.int32).cuda()
+    got = sfm.select_topk(wide, 4, lengths=lengths, status=status)
+    assert int(status) == sfm.STATUS_BAD_LENGTH
+    for r, n in enumerate([0, 1003, 5, 0, 1003]):
+        assert got[r].tolist() == P.topk(wide[r].tolist(), 4, n)
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 300001, 2048), (2, 900003, 1000), (400, 5000, 64), (1, 60000, 60001)])
+def test_topk_long_and_many_rows(rows, n, k):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = (torch.randn(rows, n, generator=g, device="cuda") * 50).round() / 8         # many equal values
+    got = sfm.select_topk(x, k)
+    order = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k].sort(1).values.to(torch.int32)
+    assert torch.equal(got[:, :min(k, n)], order) and bool((got[:, n:] == -1).all())
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+def _slots(table, block, b, n):
+    j = torch.arange(n, device="cuda")
+    return (table[b].long()[j // block] * block + j % block).to(torch.int32)
+
+
+def together(packed):
+    """One decode step of a small batch through every operator into the
+    attention; returns the problem as the attention saw it, and its output."""
+    prob = S.build("together", seed=5, device="cuda", q_n=16, q_lens=[2, 2], kv_lens=[1003, 1500], layout_q="BSND",
+                   layout_kv="PAGED", mode="ori_sparse" if packed else "csa", cmp_ratio=1 if packed else 4,
+                   cmp_topk=0 if packed else 32, ori_topk=64 if packed else 0, win_left=63,
+                   kv_format="fp8_packed" if packed else "plain", rope_head_dim=64 if packed else 0, sinks=not packed)
+    t, g = prob.t, gen(1)
+    which = "ori" if packed else "cmp"
+    f, _ = sfm.rope_frequencies(64, device="cuda")
+    lens = [1003, 1500] if packed else [1003 // 4, 1500 // 4]
+    table, block = t[f"{which}_block_table"], 128
+    dim = 576 if packed else 512
+    for b, n in enumerate([1003, 1500]):
+        x = randn(g, n, dim, dtype=torch.bfloat16).cuda()
+        sfm.store_kv(x, t["ori_kv"].view(-1, t["ori_kv"].shape[-1]), slot_mapping=_slots(t["ori_block_table"], 128, b, n),
+                     kv_format=sfm.KV_FP8_PACKED if packed else sfm.KV_PLAIN, norm_eps=1e-6,
+                     positions=torch.arange(n, dtype=torch.int32, device="cuda"), inv_freq=f)
+    if not packed:
+        for b, n in enumerate(lens):
+            sfm.store_kv(randn(g, n, 512, dtype=torch.bfloat16).cuda(), t["cmp_kv"].view(-1, 512),
+                         slot_mapping=_slots(table, block, b, n), norm_eps=1e-6, inv_freq=f,
+                         positions=torch.arange(0, 4 * n, 4, dtype=torch.int32, device="cuda"))
+    rows = (int(table.max()) + 1) * block
+    keys = torch.zeros(rows, 128, dtype=torch.float8_e4m3fn, device="cuda")
+    ks = torch.zeros(rows, device="cuda")
+    for b, n in enumerate(lens):
+        sfm.store_kv(randn(g, n, 128, dtype=torch.bfloat16).cuda(), keys, slot_mapping=_slots(table, block, b, n),
+                     kv_format=sfm.KV_FP8_ROWS, scales=ks)
+    pos = torch.tensor([1001, 1002, 1498, 1499], dtype=torch.int32, device="cuda")
+    t["q"].copy_(sfm.apply_rope(t["q"], pos, f, rope_offset=dim - 64))
+    iq = torch.zeros(4 * 8, 128, dtype=torch.float8_e4m3fn, device="cuda")
+    iqs = torch.zeros(4 * 8, device="cuda")
+    sfm.store_kv(randn(g, 4, 8, 128, dtype=torch.bfloat16).cuda(), iq, kv_format=sfm.KV_FP8_ROWS, scales=iqs, positions=pos,
+                 inv_freq=f, rope_offset=0, interleaved=False)
+    w = torch.rand(4, 8, generator=g).cuda() * iqs.view(4, 8)
+    state = dict(iq=iq.view(2, 2, 8, 128), w=w.view(2, 2, 8), keys=keys.view(-1, block, 128), ks=ks, table=table,
+                 seqused_kv=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                 rest=torch.tensor([1003 % 4, 1500 % 4] if not packed else [0, 0], dtype=torch.int32, device="cuda"),
+                 k=64 if packed else 32, ratio=1 if packed else 4, name=f"{which}_sparse_indices", maxk=max(lens))
+    return prob, state
+
+
+def select(state, out=None):
+    scores, seen = sfm.index_scores(state["iq"], state["keys"], state["w"], max_seqlen_kv=state["maxk"], k_scales=state["ks"],
+                                    block_table=state["table"], seqused_kv=state["seqused_kv"],
+                                    cmp_residual_kv=state["rest"], cmp_ratio=state["ratio"], layout_kv="PAGED")
+    return scores, seen, sfm.select_topk(scores, state["k"], lengths=seen, out=out)
+
+
+@pytest.mark.parametrize("packed", [False, True], ids=["csa", "packed"])
+def test_operators_feed_the_attention(packed):
+    prob, state = together(packed)
+    scores, seen, picked = select(state)
+    host = scores.cpu().tolist()
+    for r in range(4):
+        assert picked[r].tolist() == P.topk(host[r], state["k"], int(seen[r]))
+    prob.t[state["name"]] = picked.view(2, 2, 1, state["k"])
+    out, lse, status = _sfm.run(prob)
+    assert status == 0
+    O, L = oracle.forward(prob.to("cpu"))
+    got = out.reshape(O.shape).float().cpu().numpy()
+    assert (abs(got - O) <= 2e-2 + 2e-2 * abs(O)).all()
+    assert abs(lse.reshape(L.shape).cpu().numpy() - L).max() <= 1e-3
+
+
+def test_captured_step_replays_on_new_inputs():
+    """The selection and attention of a step, captured once: new queries in the
+    same buffers give what an eager step gives, bit for bit."""
+    prob, state = together(False)
+    idx = torch.empty(4, state["k"], dtype=torch.int32, device="cuda")
+    prob.t[state["name"]] = idx.view(2, 2, 1, state["k"])
+    f, _ = sfm.rope_frequencies(64, device="cuda")
+    pos = torch.tensor([1001, 1002, 1498, 1499], dtype=torch.int32, device="cuda")
+    q_in = prob.t["q"].clone()
+    r = _sfm.Runner(prob)
+
+    def step():
+        sfm.apply_rope(q_in, pos, f, rope_offset=448, out=prob.t["q"])
+        select(state, out=idx)
+        r.plan()
+        r.forward()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for _ in range(3):
+        q_in.copy_(torch.randn(q_in.shape, generator=g, device="cuda").to(q_in.dtype))
+        state["w"].copy_(torch.rand(state["w"].shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = r.out.clone(), r.lse.clone(), idx.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], r.out) and torch.equal(got[1], r.lse) and torch.equal(got[2], idx)
+
+
+def test_calls_on_two_streams_at_once():
+    a, b = together(False)[1], together(True)[1]
+    want = [select(s)[2].clone() for s in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, (s, st) in enumerate(zip(streams, (a, b))):
+            with torch.cuda.stream(s):
+                got[i].append(select(st)[2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
