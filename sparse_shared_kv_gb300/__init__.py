@@ -22,9 +22,11 @@ Two layers:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -160,10 +162,11 @@ def lib():
         l.sfm_error_string.restype = C.c_char_p
         V = C.c_void_p
         l.sfm_rope_frequencies.argtypes = [C.POINTER(SfmRopeSpec), C.POINTER(C.c_double), C.POINTER(C.c_float)]
-        l.sfm_rope.argtypes = [C.POINTER(SfmRopeParams), V, V, V, V, V]
-        l.sfm_kv_store.argtypes = [C.POINTER(SfmStoreParams), V, V, V, V, V, V, V, V, V]
-        l.sfm_index_scores.argtypes = [C.POINTER(SfmIndexParams), C.POINTER(SfmIndexTensors), V, C.c_int64, V, V, V]
-        l.sfm_topk_select.argtypes = [C.POINTER(SfmTopkParams), V, V, V, V, V]
+        # the structs of these come as ctypes structs or packed bytes
+        l.sfm_rope.argtypes = [V] * 6
+        l.sfm_kv_store.argtypes = [V] * 10
+        l.sfm_index_scores.argtypes = [V, V, V, C.c_int64, V, V, V]
+        l.sfm_topk_select.argtypes = [V] * 6
         for n in ("sfm_metadata_size", "sfm_workspace_size", "sfm_metadata", "sfm_forward", "sfm_forward_noalloc",
                   "sfm_debug_attended", "sfm_set_profile_events", "sfm_abi_version", "sfm_rope_frequencies",
                   "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select"):
@@ -414,51 +417,67 @@ def sparse_flash_mla(q: torch.Tensor, *, metadata: Metadata, ori_kv=None, cmp_kv
 # ---------------------------------------------------------------------------
 # around the attention: rotary positions, cache rows, sparse indices
 # ---------------------------------------------------------------------------
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+# The structs of include/sfm.h as native-layout packers (the calls below build them every time; packing
+# all fields at once costs a fraction of setting them one by one)
+_ROPE_PARAMS = struct.Struct("@8ifi4q")
+_STORE_PARAMS = struct.Struct("@6if3ifi4q")
+_INDEX_PARAMS = struct.Struct("@12i")
+_INDEX_TENSORS = struct.Struct("@PPqqPPPiPPPPP")
+_TOPK_PARAMS = struct.Struct("@6iq")
+_SIXTEEN_BIT = {torch.bfloat16: BF16, torch.float16: FP16}
+_INDEX_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
+
+
 def _require(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _tensor(name, x, dtype=None, shape=None, device=None):
-    """Check one tensor argument and return its device address (None for None)."""
-    if x is None:
-        return None
+def _first(name, x, types):
+    """Check a call's first tensor: its dtype's code and its device's index."""
     _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
-    if dtype is not None:
-        _require(x.dtype in (dtype if isinstance(dtype, tuple) else (dtype,)), f"{name}: dtype {x.dtype}, expected {dtype}")
-    if shape is not None:
-        _require(tuple(x.shape) == tuple(shape), f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-        _require(x.is_contiguous(), f"{name}: not contiguous")
-    _require(x.is_cuda, f"{name}: not on a CUDA device")
-    if device is not None:
-        _require(x.device == device, f"{name}: on {x.device}, expected {device}")
+    code = types.get(x.dtype)
+    _require(code is not None, f"{name}: dtype {x.dtype}")
+    dev = x.get_device()
+    _require(dev >= 0, f"{name}: not on a CUDA device")
+    return code, dev
+
+
+def _address(name, x, dtype, dev, shape):
+    """Device address of a contiguous tensor argument (0 for None)."""
+    if x is None:
+        return 0
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == dev and x.shape == shape
+            and x.is_contiguous()):
+        _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
+        _require(x.dtype is dtype, f"{name}: dtype {x.dtype}, expected {dtype}")
+        _require(x.get_device() >= 0, f"{name}: not on a CUDA device")
+        _require(x.get_device() == dev, f"{name}: on {x.device}, expected cuda:{dev}")
+        _require(x.shape == shape, f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name}: not contiguous")
     return x.data_ptr()
 
 
-class _Launch:
-    """The device and stream of one call: makes the inputs' device current
-    and allocates results on the stream that writes them."""
+def _status_address(status, dev):
+    if status is None:
+        return 0
+    _require(isinstance(status, torch.Tensor) and status.dtype is torch.int32 and status.get_device() == dev
+             and status.numel() >= 1, f"status: needs an int32 tensor on cuda:{dev}")
+    return status.data_ptr()
 
-    def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        given = stream is not None and not hasattr(stream, "cuda_stream")
-        self.given = torch.cuda.ExternalStream(int(stream), device=device) if given else stream
-        self.stream = self.given
 
-    def __enter__(self):
-        self.device.__enter__()
-        if self.given is None:
-            self.stream = torch.cuda.current_stream()
-            self.on = None
-        else:
-            self.on = torch.cuda.stream(self.given)
-            self.on.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.on is not None:
-            self.on.__exit__(*exc)
-        return self.device.__exit__(*exc)
+def _on(dev, stream):
+    """A context that makes the device and the stream (torch's, or a raw cudaStream_t) current, so that results
+    are allocated on the stream that writes them."""
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
 
 
 def rope_frequencies(rope_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -475,33 +494,36 @@ def rope_frequencies(rope_dim: int, *, base: float = 10000.0, scaling: str = "no
     return torch.tensor(list(freq), dtype=torch.float64, device=device), amplitude.value
 
 
-def _dtype_code(x, name, fp8=False):
-    codes = {torch.bfloat16: BF16, torch.float16: FP16}
-    if fp8:
-        codes[torch.float8_e4m3fn] = E4M3
-    _require(x.dtype in codes, f"{name}: dtype {x.dtype}")
-    return codes[x.dtype]
+def _heads(x, name):
+    """(tokens, heads, dim, token stride, head stride) of a (..., heads, dim) tensor with contiguous values."""
+    shape, strides = x.shape, x.stride()
+    _require(len(shape) >= 2, f"{name}: needs (..., heads, values)")
+    if len(shape) != 3:
+        try:
+            x = x.view(-1, shape[-2], shape[-1]) if x.numel() else x.reshape(shape[:-2].numel(), shape[-2], shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}: the token dimensions do not flatten to one stride") from None
+        shape, strides = x.shape, x.stride()
+    tokens, heads, dim = shape
+    _require(strides[2] == 1 or dim == 1, f"{name}: the last dimension must be contiguous")
+    # a dimension of one entry may report any stride: it gets that of dense rows
+    head = strides[1] if heads > 1 else dim
+    return tokens, heads, dim, strides[0] if tokens > 1 else max(head * heads, dim), head
 
 
-def _heads_view(x, name):
-    """(tokens, heads, dim) of a (..., heads, dim) tensor, without a copy."""
-    _require(isinstance(x, torch.Tensor) and x.dim() >= 2, f"{name}: needs (..., heads, values)")
-    _require(x.stride(-1) == 1 or x.shape[-1] == 1, f"{name}: the last dimension must be contiguous")
-    tokens = 1
-    for n in x.shape[:-2]:
-        tokens *= n
-    try:
-        return x.view(tokens, x.shape[-2], x.shape[-1])
-    except RuntimeError:
-        raise ValueError(f"{name}: the token dimensions do not flatten to one stride") from None
-
-
-def _strides(v):
-    """(token, head) strides of a (tokens, heads, dim) view; a dimension of one entry gets the stride of dense rows
-    (torch may report any)."""
-    head = v.stride(1) if v.shape[1] > 1 else v.shape[2]
-    token = v.stride(0) if v.shape[0] > 1 else max(head * v.shape[1], v.shape[2])
-    return token, head
+def _rows(x, name):
+    """(rows, bytes between them) of a (..., row) tensor with contiguous rows."""
+    shape, strides = x.shape, x.stride()
+    _require(len(shape) >= 2 and (strides[-1] == 1 or shape[-1] == 1), f"{name}: needs (..., row) with contiguous rows")
+    rows, stride = shape[0], strides[0]
+    if len(shape) != 2:
+        rows, stride = shape[:-1].numel(), strides[-2]
+        for i in range(len(shape) - 2):
+            _require(shape[i] == 1 or strides[i] == strides[i + 1] * shape[i + 1],
+                     f"{name}: the row dimensions do not flatten to one stride")
+        if shape[-2] == 1:      # the stride of the innermost dimension with more than one entry
+            stride = next((strides[i] for i in range(len(shape) - 2, -1, -1) if shape[i] > 1), shape[-1])
+    return rows, (stride if rows > 1 else shape[-1]) * x.element_size()
 
 
 def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, amplitude: float = 1.0,
@@ -515,28 +537,29 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     map: the gradient with respect to x, and the way back for amplitude 1.
     ``out``: None for a new tensor, x itself to rotate in place, or a tensor
     of x's shape that does not overlap it.  Views with strides are taken as they are."""
-    v = _heads_view(x, "x")
-    dtype = _dtype_code(x, "x")
-    _tensor("x", x)
-    _require(inv_freq.dim() == 1 and inv_freq.numel() > 0, "inv_freq: needs one dimension")
-    pos = _tensor("positions", positions, torch.int32, x.shape[:-2] if positions.dim() != 1 else (v.shape[0],), x.device)
-    freq = _tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), x.device)
-    with _Launch(x.device, stream) as st:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _tensor("out", out, x.dtype, None, x.device)
-            _require(out.shape == x.shape, f"out: shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-        o = _heads_view(out, "out")
-        (xt, xh), (yt, yh) = _strides(v), _strides(o)
-        params = SfmRopeParams(tokens=v.shape[0], heads=max(v.shape[1], 1), head_dim=v.shape[2],
-                               rope_dim=2 * inv_freq.numel(), rope_offset=rope_offset,
-                               rope_layout=ROPE_INTERLEAVED if interleaved else ROPE_HALF, inverse=int(inverse),
-                               dtype=dtype, amplitude=amplitude, x_token_stride=xt, x_head_stride=xh,
-                               y_token_stride=yt, y_head_stride=yh)
-        if v.shape[1] == 0:
-            params.tokens = 0
-        _check("sfm_rope", lib().sfm_rope(C.byref(params), v.data_ptr(), pos, freq, o.data_ptr(), st))
+    code, dev = _first("x", x, _SIXTEEN_BIT)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return apply_rope(x, positions, inv_freq, amplitude=amplitude, rope_offset=rope_offset, interleaved=interleaved,
+                              inverse=inverse, out=out)
+    tokens, heads, dim, xt, xh = _heads(x, "x")
+    pos = _address("positions", positions, torch.int32, dev, (tokens,) if positions.dim() == 1 else x.shape[:-2])
+    n = inv_freq.numel()
+    freq = _address("inv_freq", inv_freq, torch.float64, dev, (n,))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        yt, yh = heads * dim, dim
+    elif out is x:
+        yt, yh = xt, xh
+    else:
+        _require(isinstance(out, torch.Tensor) and out.dtype is x.dtype and out.get_device() == dev and out.shape == x.shape,
+                 f"out: needs {tuple(x.shape)} of {x.dtype} on cuda:{dev}")
+        _, _, _, yt, yh = _heads(out, "out")
+    params = _ROPE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, 2 * n, rope_offset,
+                               ROPE_INTERLEAVED if interleaved else ROPE_HALF, bool(inverse), code, amplitude, 0, xt, xh, yt, yh)
+    rc = (_lib or lib()).sfm_rope(params, x.data_ptr(), pos, freq, out.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_rope", rc)
     return out
 
 
@@ -554,49 +577,46 @@ def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_form
     with fp32 ``scales``, one per row (KV_FP8_ROWS).  Rows may be padded apart.
     slot_mapping: int32, one per token: head h goes to row slot * heads + h;
     negative: not written; None: row t * heads + h."""
-    _require(isinstance(x, torch.Tensor) and x.dim() in (2, 3), "x: needs (tokens, dim) or (tokens, heads, dim)")
-    v = _heads_view(x.unsqueeze(1) if x.dim() == 2 else x, "x")
-    dtype = _dtype_code(x, "x")
-    T, H, D = v.shape
-    _tensor("x", x)
-    packed = kv_format in (KV_INT8_PACKED, KV_FP8_PACKED)
-    kind = torch.uint8 if packed else torch.float8_e4m3fn if kv_format == KV_FP8_ROWS else x.dtype
-    _tensor("cache", cache, kind, None, x.device)
-    _require(cache.dim() >= 2 and (cache.stride(-1) == 1 or cache.shape[-1] == 1),
-             "cache: needs (..., row) with contiguous rows")
-    width = 512 + 2 * (D - 512) + 16 if packed else D
+    code, dev = _first("x", x, _SIXTEEN_BIT)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return store_kv(x, cache, slot_mapping=slot_mapping, kv_format=kv_format, norm_weight=norm_weight, norm_eps=norm_eps,
+                            positions=positions, inv_freq=inv_freq, amplitude=amplitude, rope_offset=rope_offset,
+                            interleaved=interleaved, scales=scales, status=status)
+    if x.dim() == 2:
+        tokens, dim = x.shape
+        strides = x.stride()
+        _require(strides[1] == 1 or dim == 1, "x: the last dimension must be contiguous")
+        heads, xh, xt = 1, dim, strides[0] if tokens > 1 else dim
+    else:
+        _require(x.dim() == 3, "x: needs (tokens, dim) or (tokens, heads, dim)")
+        tokens, heads, dim, xt, xh = _heads(x, "x")
+    if kv_format == KV_INT8_PACKED or kv_format == KV_FP8_PACKED:
+        kind, width = torch.uint8, 512 + 2 * (dim - 512) + 16
+    else:
+        kind, width = torch.float8_e4m3fn if kv_format == KV_FP8_ROWS else x.dtype, dim
+    _require(isinstance(cache, torch.Tensor) and cache.dtype is kind and cache.get_device() == dev,
+             f"cache: needs {kind} on cuda:{dev}")
+    rows, row_stride = _rows(cache, "cache")
     _require(cache.shape[-1] == width, f"cache: rows of {cache.shape[-1]}, expected {width}")
-    rows = 1
-    for n in cache.shape[:-1]:
-        rows *= n
-    try:
-        flat = cache.view(rows, width)
-    except RuntimeError:
-        raise ValueError("cache: the row dimensions do not flatten to one stride") from None
     _require((scales is not None) == (kv_format == KV_FP8_ROWS), "scales: go with KV_FP8_ROWS rows")
     _require((positions is None) == (inv_freq is None), "positions and inv_freq go together")
     _require(norm_eps is not None or norm_weight is None, "norm_weight: needs norm_eps")
-    if scales is not None:
-        _tensor("scales", scales, torch.float32, None, x.device)
-        _require(scales.numel() == rows and scales.is_contiguous(), f"scales: {rows} contiguous values expected")
-    if inv_freq is not None:
-        _require(inv_freq.dim() == 1, "inv_freq: needs one dimension")
     rot = 2 * inv_freq.numel() if inv_freq is not None else 0
-    xt, xh = _strides(v)
-    params = SfmStoreParams(
-        tokens=T if H else 0, heads=max(H, 1), head_dim=D, dtype=dtype, kv_format=kv_format,
-        norm=int(norm_eps is not None), norm_eps=norm_eps if norm_eps is not None else 0.0, rope_dim=rot,
-        rope_offset=(D - rot if rope_offset is None else rope_offset) if rot else 0,
-        rope_layout=ROPE_INTERLEAVED if interleaved else ROPE_HALF, amplitude=amplitude, x_token_stride=xt,
-        x_head_stride=xh, row_stride=(flat.stride(0) if rows > 1 else width) * cache.element_size(), rows=rows)
-    args = (_tensor("norm_weight", norm_weight, torch.float32, (min(D, 512),), x.device),
-            _tensor("positions", positions, torch.int32, (T,), x.device),
-            _tensor("inv_freq", inv_freq, torch.float64, (rot // 2,), x.device),
-            _tensor("slot_mapping", slot_mapping, torch.int32, (T,), x.device))
-    _tensor("status", status, torch.int32, None, x.device)
-    with _Launch(x.device, stream) as st:
-        _check("sfm_kv_store", lib().sfm_kv_store(C.byref(params), v.data_ptr(), *args, flat.data_ptr(), _ptr(scales),
-                                                  _ptr(status), st))
+    offset = 0 if not rot else dim - rot if rope_offset is None else rope_offset
+    params = _STORE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, code, kv_format, norm_eps is not None,
+                                norm_eps or 0.0, rot, offset, ROPE_INTERLEAVED if interleaved else ROPE_HALF, amplitude, 0,
+                                xt, xh, row_stride, rows)
+    each = (tokens,)
+    rc = (_lib or lib()).sfm_kv_store(
+        params, x.data_ptr(), _address("norm_weight", norm_weight, torch.float32, dev, (min(dim, 512),)),
+        _address("positions", positions, torch.int32, dev, each),
+        _address("inv_freq", inv_freq, torch.float64, dev, (rot // 2,)),
+        _address("slot_mapping", slot_mapping, torch.int32, dev, each), cache.data_ptr(),
+        0 if scales is None else _address("scales", scales, torch.float32, dev, (rows,) if scales.dim() == 1 else cache.shape[:-1]),
+        _status_address(status, dev), _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_kv_store", rc)
     return cache
 
 
@@ -614,65 +634,62 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, -inf where a key
     is not visible; visible (tokens) int32).  ``out`` may be a
     view with wider rows."""
+    code, dev = _first("q", q, _INDEX_TYPES)
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return index_scores(q, index_k, weights, max_seqlen_kv=max_seqlen_kv, k_scales=k_scales, block_table=block_table,
+                                cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv, seqused_q=seqused_q,
+                                seqused_kv=seqused_kv, cmp_residual_kv=cmp_residual_kv, max_seqlen_q=max_seqlen_q,
+                                cmp_ratio=cmp_ratio, mask_mode=mask_mode, layout_q=layout_q, layout_kv=layout_kv, out=out,
+                                visible=visible, status=status)
     lq, lkv = _LAYOUTS[layout_q], _LAYOUTS[layout_kv]
-    _require(isinstance(q, torch.Tensor) and q.dim() == (4 if lq == BSND else 3), "q: BSND has 4 dimensions, TND 3")
-    dtype = _dtype_code(q, "q", fp8=True)
-    tokens, heads = q.shape[:-2].numel(), q.shape[-2]
-    _tensor("q", q, None, q.shape)
-    dev = q.device
-    _tensor("index_k", index_k, q.dtype, None, dev)
-    _require(index_k.dim() == (2 if lkv == TND else 3) and index_k.shape[-1] == q.shape[-1] and index_k.stride(-1) == 1,
-             "index_k: needs (t, dim), (b, S, dim) or (blocks, block_size, dim) with contiguous rows of q's dim")
-    rows = index_k.shape[:-1].numel()
-    try:
-        flat = index_k.view(rows, index_k.shape[-1])
-    except RuntimeError:
-        raise ValueError("index_k: the row dimensions do not flatten to one stride") from None
-    _tensor("weights", weights, torch.float32, q.shape[:-1], dev)
-    if lkv == BSND:
-        _require(index_k.shape[1] == max_seqlen_kv and index_k.shape[0] == q.shape[0], "index_k: needs (b, max_seqlen_kv, dim)")
+    shape = q.shape
+    _require(len(shape) == (4 if lq == BSND else 3), "q: BSND has 4 dimensions, TND 3")
+    heads, dim = shape[-2], shape[-1]
     if lq == BSND:
-        batch, max_seqlen_q = q.shape[0], q.shape[1]
+        batch, max_seqlen_q = shape[0], shape[1]
+        tokens = batch * max_seqlen_q
     else:
         _require(cu_seqlens_q is not None, "cu_seqlens_q: required for TND")
-        batch = cu_seqlens_q.numel() - 1
-    if k_scales is not None:
-        _tensor("k_scales", k_scales, torch.float32, None, dev)
-        _require(k_scales.numel() == rows and k_scales.is_contiguous(), f"k_scales: {rows} contiguous values expected")
+        batch, tokens = cu_seqlens_q.numel() - 1, shape[0]
+    _require(isinstance(index_k, torch.Tensor) and index_k.dtype is q.dtype and index_k.get_device() == dev,
+             f"index_k: needs {q.dtype} on cuda:{dev}")
+    kshape = index_k.shape
+    _require(len(kshape) == (2 if lkv == TND else 3) and kshape[-1] == dim,
+             "index_k: needs (t, dim), (b, S, dim) or (blocks, block_size, dim) with q's dim")
+    if lkv == BSND:
+        _require(kshape[1] == max_seqlen_kv and kshape[0] == batch, "index_k: needs (b, max_seqlen_kv, dim)")
+    rows, row_stride = _rows(index_k, "index_k")
+    cols = 0
     if block_table is not None:
         _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: needs (b, blocks)")
-    params = SfmIndexParams(
-        num_heads=heads, index_dim=q.shape[-1], batch_size=batch, max_seqlen_q=max_seqlen_q, total_q=tokens,
-        max_seqlen_kv=max_seqlen_kv, cmp_ratio=cmp_ratio, mask_mode=mask_mode, layout_q=lq, layout_kv=lkv, dtype=dtype,
-        block_size=index_k.shape[1] if lkv == PAGED else 0)
-
-    def ints(name, x, shape):
-        return _tensor(name, x, torch.int32, shape, dev)
-
-    tensors = SfmIndexTensors(
-        q=q.data_ptr(), k=flat.data_ptr(),
-        k_row_stride=(flat.stride(0) if rows > 1 else flat.shape[1]) * flat.element_size(), k_rows=rows,
-        k_scales=_ptr(k_scales), weights=weights.data_ptr(),
-        block_table=ints("block_table", block_table, block_table.shape if block_table is not None else None),
-        block_table_stride=block_table.shape[1] if block_table is not None else 0,
-        cu_seqlens_q=ints("cu_seqlens_q", cu_seqlens_q, (batch + 1,)),
-        cu_seqlens_kv=ints("cu_seqlens_kv", cu_seqlens_kv, (batch + 1,)), seqused_q=ints("seqused_q", seqused_q, (batch,)),
-        seqused_kv=ints("seqused_kv", seqused_kv, (batch,)),
-        cmp_residual_kv=ints("cmp_residual_kv", cmp_residual_kv, (batch,)))
-    _tensor("status", status, torch.int32, None, dev)
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty(tokens, max(max_seqlen_kv, 0), dtype=torch.float32, device=dev)
-        else:
-            _tensor("out", out, torch.float32, None, dev)
-            _require(tuple(out.shape) == (tokens, max_seqlen_kv) and out.stride(1) == 1,
-                     f"out: needs ({tokens}, {max_seqlen_kv}) with contiguous rows")
-        if visible is None:
-            visible = torch.empty(tokens, dtype=torch.int32, device=dev)
-        seen = ints("visible", visible, (tokens,))
-        stride = out.stride(0) if tokens > 1 else max(max_seqlen_kv, 1)
-        _check("sfm_index_scores", lib().sfm_index_scores(C.byref(params), C.byref(tensors), out.data_ptr(), stride, seen,
-                                                          _ptr(status), st))
+        cols = block_table.shape[1]
+    params = _INDEX_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, cmp_ratio, mask_mode, lq, lkv, code,
+                                kshape[1] if lkv == PAGED else 0)
+    each, i32 = (batch,), torch.int32
+    tensors = _INDEX_TENSORS.pack(
+        _address("q", q, q.dtype, dev, shape), index_k.data_ptr(), row_stride, rows,
+        0 if k_scales is None else _address("k_scales", k_scales, torch.float32, dev, (rows,) if k_scales.dim() == 1 else kshape[:-1]),
+        _address("weights", weights, torch.float32, dev, shape[:-1]),
+        _address("block_table", block_table, i32, dev, (batch, cols)), cols,
+        _address("cu_seqlens_q", cu_seqlens_q, i32, dev, (batch + 1,)),
+        _address("cu_seqlens_kv", cu_seqlens_kv, i32, dev, (batch + 1,)), _address("seqused_q", seqused_q, i32, dev, each),
+        _address("seqused_kv", seqused_kv, i32, dev, each), _address("cmp_residual_kv", cmp_residual_kv, i32, dev, each))
+    if out is None:
+        out = torch.empty((tokens, max(max_seqlen_kv, 0)), dtype=torch.float32, device=q.device)
+        stride = max_seqlen_kv
+    else:
+        _require(isinstance(out, torch.Tensor) and out.dtype is torch.float32 and out.get_device() == dev
+                 and out.shape == (tokens, max_seqlen_kv) and (out.stride(1) == 1 or max_seqlen_kv == 1),
+                 f"out: needs fp32 ({tokens}, {max_seqlen_kv}) with contiguous rows on cuda:{dev}")
+        stride = out.stride(0) if tokens > 1 else max_seqlen_kv
+    if visible is None:
+        visible = torch.empty(tokens, dtype=i32, device=q.device)
+    rc = (_lib or lib()).sfm_index_scores(params, tensors, out.data_ptr(), stride,
+                                          _address("visible", visible, i32, dev, (tokens,)), _status_address(status, dev),
+                                          _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_index_scores", rc)
     return out, visible
 
 
@@ -684,17 +701,23 @@ def select_topk(scores: torch.Tensor, k: int, *, lengths=None, block_size: int =
     and ``last_blocks`` always among them (see sfm_topk_select).  They are what
     sparse_flash_mla takes as cmp_sparse_indices / ori_sparse_indices.
     lengths: int32 (rows), scores a row really has (None: n)."""
-    _require(isinstance(scores, torch.Tensor) and scores.dim() == 2, "scores: needs (rows, n)")
-    _tensor("scores", scores, torch.float32)
+    _, dev = _first("scores", scores, {torch.float32: 0})
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(dev, stream):
+            return select_topk(scores, k, lengths=lengths, block_size=block_size, first_blocks=first_blocks,
+                               last_blocks=last_blocks, out=out, status=status)
+    _require(scores.dim() == 2, "scores: needs (rows, n)")
     rows, n = scores.shape
-    _require(scores.stride(1) == 1 or n == 1, "scores: rows must be contiguous")
-    args = _tensor("lengths", lengths, torch.int32, (rows,), scores.device)
-    _tensor("status", status, torch.int32, None, scores.device)
-    params = SfmTopkParams(rows=rows, n=n, k=k, block_size=block_size, first_blocks=first_blocks, last_blocks=last_blocks,
-                           score_stride=scores.stride(0) if rows > 1 else n)
-    with _Launch(scores.device, stream) as st:
-        if out is None:
-            out = torch.empty(rows, max(k, 0), dtype=torch.int32, device=scores.device)
-        got = _tensor("out", out, torch.int32, (rows, k), scores.device)
-        _check("sfm_topk_select", lib().sfm_topk_select(C.byref(params), scores.data_ptr(), args, got, _ptr(status), st))
+    strides = scores.stride()
+    _require(strides[1] == 1 or n == 1, "scores: rows must be contiguous")
+    if out is None:
+        out = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=scores.device)
+        got = out.data_ptr()
+    else:
+        got = _address("out", out, torch.int32, dev, (rows, k))
+    params = _TOPK_PARAMS.pack(rows, n, k, block_size, first_blocks, last_blocks, strides[0] if rows > 1 else n)
+    rc = (_lib or lib()).sfm_topk_select(params, scores.data_ptr(), _address("lengths", lengths, torch.int32, dev, (rows,)), got,
+                                         _status_address(status, dev), _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_topk_select", rc)
     return out

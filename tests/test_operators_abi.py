@@ -165,6 +165,16 @@ def test_topk_refuses_pointers(lib):
     assert lib.sfm_topk_select(C.byref(_topk(rows=0)), None, None, None, None, None) == 0
 
 
+def test_packed_structs_match_the_ctypes_ones():
+    for packer, struct in ((sfm._ROPE_PARAMS, sfm.SfmRopeParams), (sfm._STORE_PARAMS, sfm.SfmStoreParams),
+                           (sfm._INDEX_PARAMS, sfm.SfmIndexParams), (sfm._INDEX_TENSORS, sfm.SfmIndexTensors),
+                           (sfm._TOPK_PARAMS, sfm.SfmTopkParams)):
+        n = len(struct._fields_)
+        values = list(range(1, n + 1))
+        made = struct(**{name: float(v) if kind is C.c_float else v for v, (name, kind) in zip(values, struct._fields_)})
+        assert packer.size == C.sizeof(struct) and packer.pack(*values) == bytes(made), struct
+
+
 # ---------------------------------------------------------------------------
 # frequencies
 # ---------------------------------------------------------------------------
