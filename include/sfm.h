@@ -471,7 +471,8 @@ typedef struct sfm_index_tensors {
  * mask of sfm_forward: j is visible iff (j + 1) * cmp_ratio <= p + 1,
  * p = len * cmp_ratio + residual - q_len + i (mode 3), or always (mode 0).
  * Products are exact, sums are in fp32.  A key whose block id is outside the
- * cache scores -inf and sets SFM_STATUS_BAD_BLOCK.  Rows of q at or beyond
+ * cache scores -inf and sets SFM_STATUS_BAD_BLOCK (as does one behind the
+ * cache's last row, with up to three neighbours).  Rows of q at or beyond
  * seqused_q score -inf everywhere; rows behind the last sequence (TND) are
  * left as they were.
  * scores: device fp32, score_stride (>= max_seqlen_kv) elements apart.

@@ -16,6 +16,8 @@
 //                 (a ring of stages) by TMA into 128-byte-swizzled operands,
 //                 one box per run of keys that lies inside a page;
 //   warp 17       tcgen05.mma, M = 128, N = queries x HP, K = 128 -> TMEM;
+//   warp 18       tells the sums which keys exist and brings their scales
+//                 (cp.async), so that no sum waits for global memory;
 //   warps 0-15    four warpgroups that drain the accumulator: a warpgroup
 //                 takes 64 columns of a tile.  Its weights stay in registers
 //                 for the whole unit, so a score costs a clip and a
@@ -40,12 +42,13 @@ using namespace tc;
 constexpr int kTile = 128;                     // keys per tile
 constexpr int kDim = 128;                      // values per key
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kThreads = (kEpiWarps + 3) * 32;   // 96 registers each
 constexpr int kMaxStages = 8;
 constexpr int kMaxAcc = 8;                     // accumulator tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemLimit = 232448;
-constexpr uint32_t kMiscBytes = 384 + 1024;    // barriers and flags, then the HP 128 exchange
+constexpr uint32_t kMiscBytes = 512 + 1024;    // barriers, flags and masks, then the HP 128 exchange
+constexpr uint32_t kScaleBytes = kMaxAcc * kTile * 4;
 
 struct IndexArgs {
     const float *weights, *k_scales;
@@ -128,20 +131,31 @@ __device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int querie
     return u;
 }
 
-// Cache row of key j, or -1 where the block table does not lead into the cache.
-__device__ __forceinline__ int64_t key_row(const IndexArgs &a, const Unit &u, int j)
+// Block id of key j (paged; -1 behind the table), and key j's cache row from
+// it, or -1 where it is not in the cache.
+__device__ __forceinline__ int32_t page_of(const IndexArgs &a, const Unit &u, int j)
 {
-    int64_t row;
+    if (a.layout_kv != SFM_LAYOUT_PAGED) return 0;
+    const int page = (int)fdiv((uint32_t)j, a.block_div);
+    return page < a.table_stride ? __ldg(a.table + (int64_t)u.b * a.table_stride + page) : -1;
+}
+
+__device__ __forceinline__ int64_t row_of(const IndexArgs &a, const Unit &u, int j, int32_t id)
+{
+    int64_t row = u.k_base + j;
     if (a.layout_kv == SFM_LAYOUT_PAGED) {
-        const int page = (int)fdiv((uint32_t)j, a.block_div);
-        if (page >= a.table_stride) return -1;
-        const int32_t id = __ldg(a.table + (int64_t)u.b * a.table_stride + page);
-        row = id < 0 ? -1 : (int64_t)id * a.block + (j - page * a.block);
-    } else {
-        row = u.k_base + j;
+        const int in = j - (int)fdiv((uint32_t)j, a.block_div) * a.block;
+        row = id < 0 ? -1 : (int64_t)id * a.block + in;
     }
     return row < a.k_rows ? row : -1;
 }
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
@@ -171,6 +185,17 @@ __device__ __forceinline__ float clip(uint32_t x)          // max(0, x), NaN kep
     return r;
 }
 
+// two fp32 multiply-adds in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // HP: columns per query
 template <int HP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -197,10 +222,14 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     auto acc_full = [&](int i) { return bars + 160u + 8u * i; };
     auto acc_empty = [&](int i) { return bars + 224u + 8u * i; };
     auto half_full = [&](int w) { return bars + 288u + 8u * w; };  // HP 128: a part's sums are in shared memory
-    const uint32_t teardown = bars + 320u;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + (misc - base) + 336);
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gbase + (misc - base) + 340);
-    float *half_sum = reinterpret_cast<float *>(gbase + (misc - base) + 384);     // [2 pairs][128]
+    auto row_full = [&](int i) { return bars + 320u + 8u * i; };   // an accumulator tile's masks and scales are there
+    const uint32_t teardown = bars + 384u;
+    uint8_t *gmisc = gbase + (misc - base);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 392);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 396);
+    volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 400);     // [kMaxAcc] a bit per four keys
+    float *half_sum = reinterpret_cast<float *>(gmisc + 512);                           // [2 pairs][128]
+    float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes);                  // [kMaxAcc][kTile], with scales only
 
     const int accs = kMaxAcc >> a.parts_log2;                 // accumulator tiles of parts * 64 columns
     if (tid == 0) {
@@ -209,6 +238,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
         for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
+        for (int i = 0; i < accs; ++i) mbar_init(row_full(i), 33);
         mbar_init(teardown, 1);
         fence_barrier_init();
     }
@@ -246,10 +276,13 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 if (!a.fp8) tma_load(dst + q_rows * 128, &q_map, 64, row, q_full(qb));
             }
             ++n;
-            for (int t = 0; t < u.tiles; ++t) {
-                const int j = (u.first_tile + t) * kTile + lane * a.run;
-                int64_t row = -1;
-                if (lane * a.run < kTile && j < u.len) row = key_row(a, u, j);
+            const bool mine = lane * a.run < kTile;           // the lane's box of every tile
+            int j = u.first_tile * kTile + lane * a.run;
+            int32_t page = mine && j < u.len ? page_of(a, u, j) : -1;
+            for (int t = 0; t < u.tiles; ++t, j += kTile) {
+                const int64_t row = mine && j < u.len ? row_of(a, u, j, page) : -1;
+                // the next tile's block id is under way while this tile's stage is waited for
+                if (t + 1 < u.tiles) page = mine && j + kTile < u.len ? page_of(a, u, j + kTile) : -1;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 ok = warp_wait(k_empty(stage), kphase ^ 1, abort_flag);
                 if (!ok) break;
@@ -324,6 +357,43 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             }
         }
         __syncwarp();
+    } else if (warp == 18) {
+        // ---------------- masks and scales of the keys ----------------
+        int acc = 0, aphase = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            const Unit u = unit_of(a, unit, queries, &bad);
+            if (u.tiles == 0) continue;
+            const int most = visible_of(a, u, u.nq - 1);
+            int j = u.first_tile * kTile + 4 * lane;          // four neighbouring keys per lane: they share a page
+            int32_t page = j < u.len ? page_of(a, u, j) : -1;
+            for (int t = 0; t < u.tiles; ++t, j += kTile) {
+                int64_t row = j < u.len ? row_of(a, u, j, page) : -1;
+                if (t + 1 < u.tiles) page = j + kTile < u.len ? page_of(a, u, j + kTile) : -1;
+                const int n = min(4, u.len - j);
+                if (row > a.k_rows - n) row = -1;
+                if (row < 0 && j < most && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
+                ok = warp_wait(acc_empty(acc), aphase ^ 1, abort_flag);        // the slot's last tile has been summed
+                if (!ok) break;
+                if (a.k_scales && row >= 0) {
+                    const float *src = a.k_scales + row;
+                    const uint32_t dst = smem_u32(key_scales + acc * kTile + 4 * lane);
+                    if (n == 4 && ((uintptr_t)src & 15u) == 0) {
+                        cp_async16(dst, src, 16);
+                    } else {
+                        for (int i = 0; i < n; ++i) cp_async4(dst + 4 * i, src + i);
+                    }
+                }
+                const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
+                cp_async_arrive_noinc(row_full(acc));
+                if (lane == 0) {
+                    key_mask[acc] = mask;
+                    mbar_arrive(row_full(acc));
+                }
+                if (++acc == accs) acc = 0, aphase ^= 1;
+            }
+        }
+        cp_async_wait_all();                                  // this warp's own copies
     } else {
         // ---------------- clipped sums ----------------
         const int wg = warp >> 2, part = wg & (parts - 1);
@@ -337,36 +407,34 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
             const Unit u = unit_of(a, unit, queries, &bad);
             if (a.visible && u.first_tile == 0 && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
-            float w[64];
+            float2 w[32];                                     // this part's weights, pairs of heads
             int vis[kSums];
             if (u.tiles) {
 #pragma unroll
                 for (int q = 0; q < kSums; ++q) {
                     const int i = i_part + q;
                     vis[q] = visible_of(a, u, i);
-                    const float *src = a.weights + (int64_t)(u.t0 + i) * a.heads;
+                    const float *src = a.weights + (int64_t)(u.t0 + i) * a.heads + (HP <= 64 ? 0 : 64 * (part & 1));
+                    const int have = i < u.nq ? a.heads - (HP <= 64 ? 0 : 64 * (part & 1)) : 0;
 #pragma unroll
-                    for (int h = 0; h < 64 / kSums; ++h) {
-                        const int hh = HP <= 64 ? h : h + 64 * (part & 1);
-                        w[q * (64 / kSums) + h] = i < u.nq && hh < a.heads ? __ldg(src + hh) : 0.f;
-                    }
+                    for (int h = 0; h < 32 / kSums; ++h)
+                        w[q * (32 / kSums) + h] = make_float2(2 * h < have ? __ldg(src + 2 * h) : 0.f,
+                                                              2 * h + 1 < have ? __ldg(src + 2 * h + 1) : 0.f);
                 }
             }
             for (int t = 0; t < u.tiles; ++t) {
                 const int64_t g = done + t;                   // the CTA's tile number
                 if ((int)(g & (turns - 1)) != turn) continue;
                 const int j = (u.first_tile + t) * kTile + key_lane;
-                const int64_t row = j < u.len ? key_row(a, u, j) : 0;
-                if (row < 0 && i_part < u.nq && j < visible_of(a, u, u.nq - 1) && a.status)
-                    atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
-                const float scale = a.k_scales && row >= 0 && j < u.len ? __ldg(a.k_scales + row) : 1.f;
                 const int acc = (int)(g & (accs - 1)), phase = (int)((g >> (3 - a.parts_log2)) & 1);
-                ok = warp_wait(acc_full(acc), phase, abort_flag);
+                ok = warp_wait(row_full(acc), phase, abort_flag) && warp_wait(acc_full(acc), phase, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float sum[kSums];
+                const bool there = key_mask[acc] >> (key_lane >> 2) & 1u;
+                const float scale = a.k_scales ? *(volatile float *)(key_scales + acc * kTile + key_lane) : 1.f;
+                float2 sum2[kSums];
 #pragma unroll
-                for (int q = 0; q < kSums; ++q) sum[q] = 0.f;
+                for (int q = 0; q < kSums; ++q) sum2[q] = make_float2(0.f, 0.f);
                 const uint32_t at = tmem + acc * (parts * 64) + part * 64 + ((uint32_t)((warp & 3) * 32) << 16);
                 const bool live = i_part < u.nq;
                 if (live) {
@@ -381,9 +449,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                             if (lane == 0) mbar_arrive(acc_empty(acc));
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            constexpr int kPer = 64 / kSums;
-                            sum[(c * 16 + e) / kPer] = fmaf(clip(r[e]), w[c * 16 + e], sum[(c * 16 + e) / kPer]);
+                        for (int e = 0; e < 8; ++e) {
+                            constexpr int kPer = 32 / kSums;
+                            const int q = (c * 8 + e) / kPer;
+                            sum2[q] = fma2(make_float2(clip(r[2 * e]), clip(r[2 * e + 1])), w[c * 8 + e], sum2[q]);
                         }
                     }
                 } else {
@@ -391,6 +460,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty(acc));
                 }
+                float sum[kSums];
+#pragma unroll
+                for (int q = 0; q < kSums; ++q) sum[q] = sum2[q].x + sum2[q].y;
                 if constexpr (HP == 128) {                    // the odd part hands its half to the even one
                     float *mine = half_sum + (wg >> 1) * 128 + key_lane;
                     if (part & 1) {
@@ -413,7 +485,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                         const int i = i_part + q;
                         if (i < u.nq)
                             a.scores[(int64_t)(u.t0 + i) * a.stride + j] =
-                                j < vis[q] && row >= 0 ? sum[q] * scale : -INFINITY;
+                                j < vis[q] && there ? sum[q] * scale : -INFINITY;
                     }
                 }
             }
@@ -568,7 +640,8 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
         if (a.run > kTile) a.run = kTile;
     }
     const uint32_t q_bytes = (64u << a.parts_log2) * kDim * elem, k_bytes = kTile * kDim * elem;
-    const int fit = (int)((kSmemLimit - 1024 - kMiscBytes - 2 * q_bytes) / k_bytes);
+    const uint32_t scale_bytes = t->k_scales ? kScaleBytes : 0;
+    const int fit = (int)((kSmemLimit - 1024 - kMiscBytes - scale_bytes - 2 * q_bytes) / k_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 
     // units: some six per CTA, so that sequences of different lengths even out,
@@ -590,7 +663,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     int rc = make_map(&q_map, t->q, p.dtype, tokens * p.num_heads, (int64_t)kDim * elem, p.num_heads);
     if (!rc) rc = make_map(&k_map, t->k, p.dtype, t->k_rows, t->k_row_stride, a.run);
     if (rc) return rc;
-    const size_t smem = 1024 + 2 * q_bytes + (size_t)a.stages * k_bytes + kMiscBytes;
+    const size_t smem = 1024 + 2 * q_bytes + (size_t)a.stages * k_bytes + kMiscBytes + scale_bytes;
     const int grid = (int)(units < sms ? units : sms);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
