@@ -47,7 +47,7 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxAcc = 8;                     // accumulator tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemLimit = 232448;
-constexpr uint32_t kMiscBytes = 512 + 1024;    // barriers, flags and masks, then the HP 128 exchange
+constexpr uint32_t kMiscBytes = 512 + 2048 + 1024;   // barriers, flags and masks, two units' weights, the HP 128 exchange
 constexpr uint32_t kScaleBytes = kMaxAcc * kTile * 4;
 
 struct IndexArgs {
@@ -203,7 +203,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
 {
     constexpr int kQueries = 256 / HP;         // queries of a full tile
     constexpr int kSums = HP <= 64 ? 64 / HP : 1;   // queries whose heads a 64-column part holds
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = 1 << a.parts_log2;
     const int queries = min(kQueries, parts * 64 / HP);
@@ -211,8 +211,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     const uint32_t q_rows = parts * 64;                       // rows of a Q buffer
     const uint32_t q_bytes = q_rows * kDim * elem, k_bytes = kTile * kDim * elem;
 
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t *gbase = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t base = smem_u32(smem_raw);
+    uint8_t *gbase = smem_raw;
     const uint32_t q_smem = base, k_smem = base + 2 * q_bytes, misc = k_smem + a.stages * k_bytes;
     const uint32_t bars = misc;
     auto q_full = [&](int i) { return bars + 8u * i; };
@@ -228,8 +228,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 392);
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 396);
     volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 400);     // [kMaxAcc] a bit per four keys
-    float *half_sum = reinterpret_cast<float *>(gmisc + 512);                           // [2 pairs][128]
-    float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes);                  // [kMaxAcc][kTile], with scales only
+    auto w_full = [&](int i) { return bars + 432u + 8u * i; };     // a unit's weights are there
+    float *weights = reinterpret_cast<float *>(gmisc + 512);                            // [2][256]: by column
+    float *half_sum = weights + 512;                                                    // HP 128 only: [2 pairs][128]
+    float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes - (HP == 128 ? 0 : 1024));   // [kMaxAcc][kTile]
 
     const int accs = kMaxAcc >> a.parts_log2;                 // accumulator tiles of parts * 64 columns
     if (tid == 0) {
@@ -238,6 +240,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
         for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
+        for (int i = 0; i < 2; ++i) mbar_init(w_full(i), kEpiWarps);
         for (int i = 0; i < accs; ++i) mbar_init(row_full(i), 33);
         mbar_init(teardown, 1);
         fence_barrier_init();
@@ -403,25 +406,29 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         const int key_lane = (warp & 3) * 32 + lane;
         int64_t done = 0;                                     // tiles of this CTA before the unit
         int halves = 0;                                       // HP 128: exchanges so far
+        int n = 0;                                            // units with tiles
         bool ok = true;
         for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
             const Unit u = unit_of(a, unit, queries, &bad);
             if (a.visible && u.first_tile == 0 && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
-            float2 w[32];                                     // this part's weights, pairs of heads
             int vis[kSums];
+            float *w = weights + (n & 1) * 256;
             if (u.tiles) {
 #pragma unroll
-                for (int q = 0; q < kSums; ++q) {
-                    const int i = i_part + q;
-                    vis[q] = visible_of(a, u, i);
-                    const float *src = a.weights + (int64_t)(u.t0 + i) * a.heads + (HP <= 64 ? 0 : 64 * (part & 1));
-                    const int have = i < u.nq ? a.heads - (HP <= 64 ? 0 : 64 * (part & 1)) : 0;
-#pragma unroll
-                    for (int h = 0; h < 32 / kSums; ++h)
-                        w[q * (32 / kSums) + h] = make_float2(2 * h < have ? __ldg(src + 2 * h) : 0.f,
-                                                              2 * h + 1 < have ? __ldg(src + 2 * h + 1) : 0.f);
+                for (int q = 0; q < kSums; ++q) vis[q] = visible_of(a, u, i_part + q);
+                // the unit's weights, zero for heads and queries that are not there.  The buffer was last read two
+                // units ago, and every warp has since arrived here for the unit between
+                if (lane < 16) {
+                    const int col = warp * 16 + lane, i = col / HP, h = col % HP;
+                    w[col] = i < u.nq && h < a.heads ? __ldg(a.weights + (int64_t)(u.t0 + i) * a.heads + h) : 0.f;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_full(n & 1));
+                ok = warp_wait(w_full(n & 1), (n >> 1) & 1, abort_flag);
+                if (!ok) break;
+                ++n;
             }
+            w += part * 64;
             for (int t = 0; t < u.tiles; ++t) {
                 const int64_t g = done + t;                   // the CTA's tile number
                 if ((int)(g & (turns - 1)) != turn) continue;
@@ -438,22 +445,22 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 const uint32_t at = tmem + acc * (parts * 64) + part * 64 + ((uint32_t)((warp & 3) * 32) << 16);
                 const bool live = i_part < u.nq;
                 if (live) {
+                    // all of the part leaves TMEM first, so that the next product can start
+                    uint32_t r[2][32];
+                    tmem_ld32(at, r[0]);
+                    tmem_ld32(at + 32, r[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty(acc));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[16];
-                        tmem_ld16(at + c * 16, r);
-                        tmem_wait_ld();
-                        if (c == 3) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(acc_empty(acc));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            constexpr int kPer = 32 / kSums;
-                            const int q = (c * 8 + e) / kPer;
-                            sum2[q] = fma2(make_float2(clip(r[2 * e]), clip(r[2 * e + 1])), w[c * 8 + e], sum2[q]);
-                        }
+                    for (int e = 0; e < 16; ++e) {
+                        constexpr int kPer = 16 / kSums;
+                        const float4 v = *reinterpret_cast<const float4 *>(w + 4 * e);
+                        const uint32_t *x = r[e >> 3] + 4 * (e & 7);
+                        const int q = e / kPer;
+                        sum2[q] = fma2(make_float2(clip(x[0]), clip(x[1])), make_float2(v.x, v.y), sum2[q]);
+                        sum2[q] = fma2(make_float2(clip(x[2]), clip(x[3])), make_float2(v.z, v.w), sum2[q]);
                     }
                 } else {
                     tc_fence_before();
@@ -641,7 +648,8 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     }
     const uint32_t q_bytes = (64u << a.parts_log2) * kDim * elem, k_bytes = kTile * kDim * elem;
     const uint32_t scale_bytes = t->k_scales ? kScaleBytes : 0;
-    const int fit = (int)((kSmemLimit - 1024 - kMiscBytes - scale_bytes - 2 * q_bytes) / k_bytes);
+    const uint32_t misc_bytes = kMiscBytes - (hp == 128 ? 0 : 1024) + scale_bytes;
+    const int fit = (int)((kSmemLimit - misc_bytes - 2 * q_bytes) / k_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 
     // units: some six per CTA, so that sequences of different lengths even out,
@@ -663,7 +671,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     int rc = make_map(&q_map, t->q, p.dtype, tokens * p.num_heads, (int64_t)kDim * elem, p.num_heads);
     if (!rc) rc = make_map(&k_map, t->k, p.dtype, t->k_rows, t->k_row_stride, a.run);
     if (rc) return rc;
-    const size_t smem = 1024 + 2 * q_bytes + (size_t)a.stages * k_bytes + kMiscBytes + scale_bytes;
+    const size_t smem = 2 * q_bytes + (size_t)a.stages * k_bytes + misc_bytes;
     const int grid = (int)(units < sms ? units : sms);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
