@@ -61,7 +61,7 @@ struct IndexArgs {
     int32_t run;                               // keys per TMA box
     int32_t parts_log2;                        // 64-column parts of a tile: 1, 2 or 4
     int32_t stages;
-    FastDiv block_div, ratio_div;
+    FastDiv block_div, ratio_div, groups_div, seq_div;
     uint32_t idesc;                            // instruction descriptor without N
     int32_t fp8;
 };
@@ -95,8 +95,8 @@ __device__ __forceinline__ int32_t visible_of(const IndexArgs &a, const Unit &u,
 __device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int queries, bool *bad)
 {
     Unit u;
-    const int c = unit / a.groups, g = unit - c * a.groups;
-    u.b = g / a.groups_per_seq;
+    const int c = (int)fdiv((uint32_t)unit, a.groups_div), g = unit - c * a.groups;
+    u.b = (int)fdiv((uint32_t)g, a.seq_div);
     u.i0 = (g - u.b * a.groups_per_seq) * queries;
     int q_cap, t_base;
     if (a.layout_q == SFM_LAYOUT_BSND) {
@@ -178,6 +178,18 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t ad, uint64_t bd, ui
         ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// Bounded wait of a whole warp, every lane polling: cheaper than one lane that
+// tells the others when the phase is usually complete already.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) ok = mbar_wait(bar, parity, abort);
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+}
+
 __device__ __forceinline__ float clip(uint32_t x)          // max(0, x), NaN kept
 {
     float r;
@@ -219,10 +231,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     auto q_empty = [&](int i) { return bars + 16u + 8u * i; };
     auto k_full = [&](int i) { return bars + 32u + 8u * i; };
     auto k_empty = [&](int i) { return bars + 96u + 8u * i; };
-    auto acc_full = [&](int i) { return bars + 160u + 8u * i; };
+    auto acc_full = [&](int i) { return bars + 160u + 8u * i; };   // the product, and the keys' mask and scales
     auto acc_empty = [&](int i) { return bars + 224u + 8u * i; };
     auto half_full = [&](int w) { return bars + 288u + 8u * w; };  // HP 128: a part's sums are in shared memory
-    auto row_full = [&](int i) { return bars + 320u + 8u * i; };   // an accumulator tile's masks and scales are there
     const uint32_t teardown = bars + 384u;
     uint8_t *gmisc = gbase + (misc - base);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 392);
@@ -238,10 +249,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         *abort_flag = 0;
         for (int i = 0; i < 2; ++i) mbar_init(q_full(i), 1), mbar_init(q_empty(i), 1);
         for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
-        for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 1), mbar_init(acc_empty(i), 4 * parts);
+        for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 34), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
         for (int i = 0; i < 2; ++i) mbar_init(w_full(i), kEpiWarps);
-        for (int i = 0; i < accs; ++i) mbar_init(row_full(i), 33);
         mbar_init(teardown, 1);
         fence_barrier_init();
     }
@@ -268,7 +278,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             const Unit u = unit_of(a, unit, queries, &bad);
             if (u.tiles == 0) continue;
             const int qb = n & 1;
-            ok = warp_wait(q_empty(qb), ((n >> 1) & 1) ^ 1, abort_flag);
+            ok = wait_warp(q_empty(qb), ((n >> 1) & 1) ^ 1, abort_flag);
             if (!ok) break;
             if (lane == 0) mbar_expect(q_full(qb), (uint32_t)(u.nq * a.heads) * kDim * elem);
             __syncwarp();
@@ -287,7 +297,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 // the next tile's block id is under way while this tile's stage is waited for
                 if (t + 1 < u.tiles) page = mine && j + kTile < u.len ? page_of(a, u, j + kTile) : -1;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                ok = warp_wait(k_empty(stage), kphase ^ 1, abort_flag);
+                ok = wait_warp(k_empty(stage), kphase ^ 1, abort_flag);
                 if (!ok) break;
                 if (lane == 0) mbar_expect(k_full(stage), boxes * a.run * kDim * elem);
                 __syncwarp();
@@ -316,22 +326,21 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             }
         }
     } else if (warp == 17) {
-        // ---------------- products ----------------
-        int stage = 0, kphase = 0, acc = 0, aphase = 0, n = 0;
-        bool ok = true;
-        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-            const Unit u = unit_of(a, unit, queries, &bad);
-            if (u.tiles == 0) continue;
-            const int qb = n & 1;
-            ok = warp_wait(q_full(qb), (n >> 1) & 1, abort_flag);
-            if (!ok) break;
-            const uint32_t idesc = a.idesc | ((uint32_t)(u.nq * HP >> 3) << 17);
-            const uint64_t bdesc = sdesc_sw128(q_smem + qb * q_bytes, 16, 1024);
-            for (int t = 0; t < u.tiles; ++t) {
-                ok = warp_wait(k_full(stage), kphase, abort_flag) && warp_wait(acc_empty(acc), aphase ^ 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
+        // ---------------- products: one thread, so that nothing stands between them ----------------
+        if (lane == 0) {
+            int stage = 0, kphase = 0, acc = 0, aphase = 0, n = 0;
+            bool ok = true;
+            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+                const Unit u = unit_of(a, unit, queries, &bad);
+                if (u.tiles == 0) continue;
+                const int qb = n & 1;
+                ok = mbar_wait(q_full(qb), (n >> 1) & 1, abort_flag);
+                const uint32_t idesc = a.idesc | ((uint32_t)(u.nq * HP >> 3) << 17);
+                const uint64_t bdesc = sdesc_sw128(q_smem + qb * q_bytes, 16, 1024);
+                for (int t = 0; t < u.tiles && ok; ++t) {
+                    ok = mbar_wait(k_full(stage), kphase, abort_flag) && mbar_wait(acc_empty(acc), aphase ^ 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint64_t adesc = sdesc_sw128(k_smem + stage * k_bytes, 16, 1024);
                     const uint32_t d = tmem + acc * (parts * 64);
                     if (a.fp8) {
@@ -346,17 +355,16 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                     umma_commit(k_empty(stage));
                     umma_commit(acc_full(acc));
                     if (t == u.tiles - 1) umma_commit(q_empty(qb));
+                    if (++stage == a.stages) stage = 0, kphase ^= 1;
+                    if (++acc == accs) acc = 0, aphase ^= 1;
                 }
-                __syncwarp();
-                if (++stage == a.stages) stage = 0, kphase ^= 1;
-                if (++acc == accs) acc = 0, aphase ^= 1;
+                ++n;
             }
-            ++n;
-        }
-        if (!ok && lane == 0) {
-            umma_commit(teardown);
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(teardown, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+            if (!ok) {
+                umma_commit(teardown);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(teardown, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+                }
             }
         }
         __syncwarp();
@@ -376,7 +384,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 const int n = min(4, u.len - j);
                 if (row > a.k_rows - n) row = -1;
                 if (row < 0 && j < most && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
-                ok = warp_wait(acc_empty(acc), aphase ^ 1, abort_flag);        // the slot's last tile has been summed
+                ok = wait_warp(acc_empty(acc), aphase ^ 1, abort_flag);        // the slot's last tile has been summed
                 if (!ok) break;
                 if (a.k_scales && row >= 0) {
                     const float *src = a.k_scales + row;
@@ -388,10 +396,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                     }
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
-                cp_async_arrive_noinc(row_full(acc));
+                cp_async_arrive_noinc(acc_full(acc));
                 if (lane == 0) {
                     key_mask[acc] = mask;
-                    mbar_arrive(row_full(acc));
+                    mbar_arrive(acc_full(acc));
                 }
                 if (++acc == accs) acc = 0, aphase ^= 1;
             }
@@ -424,17 +432,18 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_full(n & 1));
-                ok = warp_wait(w_full(n & 1), (n >> 1) & 1, abort_flag);
+                ok = wait_warp(w_full(n & 1), (n >> 1) & 1, abort_flag);
                 if (!ok) break;
                 ++n;
             }
             w += part * 64;
+            float *out = a.scores + (int64_t)(u.t0 + i_part) * a.stride;
             for (int t = 0; t < u.tiles; ++t) {
                 const int64_t g = done + t;                   // the CTA's tile number
                 if ((int)(g & (turns - 1)) != turn) continue;
                 const int j = (u.first_tile + t) * kTile + key_lane;
                 const int acc = (int)(g & (accs - 1)), phase = (int)((g >> (3 - a.parts_log2)) & 1);
-                ok = warp_wait(row_full(acc), phase, abort_flag) && warp_wait(acc_full(acc), phase, abort_flag);
+                ok = wait_warp(acc_full(acc), phase, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 const bool there = key_mask[acc] >> (key_lane >> 2) & 1u;
@@ -473,11 +482,11 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 if constexpr (HP == 128) {                    // the odd part hands its half to the even one
                     float *mine = half_sum + (wg >> 1) * 128 + key_lane;
                     if (part & 1) {
-                        ok = halves == 0 || warp_wait(half_full(wg ^ 1), (halves - 1) & 1, abort_flag);   // taken
+                        ok = halves == 0 || wait_warp(half_full(wg ^ 1), (halves - 1) & 1, abort_flag);   // taken
                         if (!ok) break;
                         *mine = sum[0];
                     } else {
-                        ok = warp_wait(half_full(wg ^ 1), halves & 1, abort_flag);
+                        ok = wait_warp(half_full(wg ^ 1), halves & 1, abort_flag);
                         if (!ok) break;
                         sum[0] += *mine;
                     }
@@ -487,13 +496,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                     if (part & 1) continue;
                 }
                 if (live && j < a.max_k) {
+                    float *dst = out + j;
 #pragma unroll
-                    for (int q = 0; q < kSums; ++q) {
-                        const int i = i_part + q;
-                        if (i < u.nq)
-                            a.scores[(int64_t)(u.t0 + i) * a.stride + j] =
-                                j < vis[q] && there ? sum[q] * scale : -INFINITY;
-                    }
+                    for (int q = 0; q < kSums; ++q, dst += a.stride)
+                        if (i_part + q < u.nq) *dst = j < vis[q] && there ? sum[q] * scale : -INFINITY;
                 }
             }
             done += u.tiles;
@@ -666,6 +672,8 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     if (units > INT32_MAX - sms) return SFM_ERR_UNSUPPORTED;
     a.groups = (int32_t)groups;
     a.units = (int32_t)units;
+    a.groups_div = make_fastdiv((uint32_t)groups);
+    a.seq_div = make_fastdiv((uint32_t)a.groups_per_seq);
 
     CUtensorMap q_map, k_map;
     int rc = make_map(&q_map, t->q, p.dtype, tokens * p.num_heads, (int64_t)kDim * elem, p.num_heads);
