@@ -15,7 +15,9 @@
 //   warp 16       loads: the unit's queries (two buffers) and its key tiles
 //                 (a ring of stages) by TMA into 128-byte-swizzled operands,
 //                 one box per run of keys that lies inside a page;
-//   warp 17       tcgen05.mma, M = 128, N = queries x HP, K = 128 -> TMEM;
+//   warps 17, 19  tcgen05.mma, M = 128, N = queries x HP, K = 128 -> TMEM, in
+//                 turns, so that one tile's waits and commits run beside the
+//                 other's products (issuing blocks while the pipe is busy);
 //   warp 18       tells the sums which keys exist and brings their scales
 //                 (cp.async), so that no sum waits for global memory;
 //   warps 0-15    four warpgroups that drain the accumulator: a warpgroup
@@ -42,7 +44,7 @@ using namespace tc;
 constexpr int kTile = 128;                     // keys per tile
 constexpr int kDim = 128;                      // values per key
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = (kEpiWarps + 3) * 32;   // 96 registers each
+constexpr int kThreads = (kEpiWarps + 4) * 32;   // 96 registers each
 constexpr int kMaxStages = 8;
 constexpr int kMaxAcc = 8;                     // accumulator tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
@@ -234,12 +236,12 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     auto acc_full = [&](int i) { return bars + 160u + 8u * i; };   // the product, and the keys' mask and scales
     auto acc_empty = [&](int i) { return bars + 224u + 8u * i; };
     auto half_full = [&](int w) { return bars + 288u + 8u * w; };  // HP 128: a part's sums are in shared memory
-    const uint32_t teardown = bars + 384u;
+    auto w_full = [&](int i) { return bars + 320u + 8u * i; };     // a unit's weights are there
+    const uint32_t teardown = bars + 336u;                         // two
     uint8_t *gmisc = gbase + (misc - base);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 392);
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 396);
-    volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 400);     // [kMaxAcc] a bit per four keys
-    auto w_full = [&](int i) { return bars + 432u + 8u * i; };     // a unit's weights are there
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 352);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 356);
+    volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 360);     // [kMaxAcc] a bit per four keys
     float *weights = reinterpret_cast<float *>(gmisc + 512);                            // [2][256]: by column
     float *half_sum = weights + 512;                                                    // HP 128 only: [2 pairs][128]
     float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes - (HP == 128 ? 0 : 1024));   // [kMaxAcc][kTile]
@@ -247,12 +249,12 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     const int accs = kMaxAcc >> a.parts_log2;                 // accumulator tiles of parts * 64 columns
     if (tid == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < 2; ++i) mbar_init(q_full(i), 1), mbar_init(q_empty(i), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(q_full(i), 1), mbar_init(q_empty(i), 2);
         for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
         for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 34), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
         for (int i = 0; i < 2; ++i) mbar_init(w_full(i), kEpiWarps);
-        mbar_init(teardown, 1);
+        mbar_init(teardown, 1), mbar_init(teardown + 8, 1);
         fence_barrier_init();
     }
     if (a.heads != HP) {                                      // rows of padding heads: zeros that no load overwrites
@@ -325,9 +327,11 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 }
             }
         }
-    } else if (warp == 17) {
-        // ---------------- products: one thread, so that nothing stands between them ----------------
+    } else if (warp == 17 || warp == 19) {
+        // ---------------- products: one thread each, even and odd tiles of the CTA ----------------
         if (lane == 0) {
+            const int odd = warp == 19;
+            int64_t g = 0;
             int stage = 0, kphase = 0, acc = 0, aphase = 0, n = 0;
             bool ok = true;
             for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
@@ -337,33 +341,35 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 ok = mbar_wait(q_full(qb), (n >> 1) & 1, abort_flag);
                 const uint32_t idesc = a.idesc | ((uint32_t)(u.nq * HP >> 3) << 17);
                 const uint64_t bdesc = sdesc_sw128(q_smem + qb * q_bytes, 16, 1024);
-                for (int t = 0; t < u.tiles && ok; ++t) {
-                    ok = mbar_wait(k_full(stage), kphase, abort_flag) && mbar_wait(acc_empty(acc), aphase ^ 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t adesc = sdesc_sw128(k_smem + stage * k_bytes, 16, 1024);
-                    const uint32_t d = tmem + acc * (parts * 64);
-                    if (a.fp8) {
+                for (int t = 0; t < u.tiles && ok; ++t, ++g) {
+                    if ((int)(g & 1) == odd) {
+                        ok = mbar_wait(k_full(stage), kphase, abort_flag) && mbar_wait(acc_empty(acc), aphase ^ 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t adesc = sdesc_sw128(k_smem + stage * k_bytes, 16, 1024);
+                        const uint32_t d = tmem + acc * (parts * 64);
+                        if (a.fp8) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) umma_f8(d, adesc + 2 * k, bdesc + 2 * k, idesc, k > 0);
-                    } else {
+                            for (int k = 0; k < 4; ++k) umma_f8(d, adesc + 2 * k, bdesc + 2 * k, idesc, k > 0);
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            umma_f16(d, adesc + (k >> 2) * (kTile * 128 >> 4) + 2 * (k & 3),
-                                     bdesc + (k >> 2) * (q_rows * 128 >> 4) + 2 * (k & 3), idesc, k > 0);
+                            for (int k = 0; k < 8; ++k)
+                                umma_f16(d, adesc + (k >> 2) * (kTile * 128 >> 4) + 2 * (k & 3),
+                                         bdesc + (k >> 2) * (q_rows * 128 >> 4) + 2 * (k & 3), idesc, k > 0);
+                        }
+                        umma_commit(k_empty(stage));
+                        umma_commit(acc_full(acc));
                     }
-                    umma_commit(k_empty(stage));
-                    umma_commit(acc_full(acc));
-                    if (t == u.tiles - 1) umma_commit(q_empty(qb));
                     if (++stage == a.stages) stage = 0, kphase ^= 1;
                     if (++acc == accs) acc = 0, aphase ^= 1;
                 }
+                umma_commit(q_empty(qb));                     // this thread's products of the unit
                 ++n;
             }
             if (!ok) {
-                umma_commit(teardown);
+                umma_commit(teardown + 8 * odd);
                 const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(teardown, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+                while (!mbar_try_wait(teardown + 8 * odd, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
                 }
             }
         }
