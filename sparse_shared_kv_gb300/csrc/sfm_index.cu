@@ -60,7 +60,7 @@ struct IndexArgs {
     int64_t stride, k_rows;
     int32_t heads, batch, max_q, total_q, max_k, ratio, causal, layout_q, layout_kv, block, table_stride;
     int32_t groups_per_seq, groups, chunk, units;   // tiles per unit; units in all
-    int32_t run;                               // keys per TMA box
+    int32_t run, boxes_log2;                   // keys per TMA box, boxes per tile
     int32_t parts_log2;                        // 64-column parts of a tile: 1, 2 or 4
     int32_t stages;
     FastDiv block_div, ratio_div, groups_div, seq_div;
@@ -133,23 +133,52 @@ __device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int querie
     return u;
 }
 
-// Block id of key j (paged; -1 behind the table), and key j's cache row from
-// it, or -1 where it is not in the cache.
-__device__ __forceinline__ int32_t page_of(const IndexArgs &a, const Unit &u, int j)
-{
-    if (a.layout_kv != SFM_LAYOUT_PAGED) return 0;
-    const int page = (int)fdiv((uint32_t)j, a.block_div);
-    return page < a.table_stride ? __ldg(a.table + (int64_t)u.b * a.table_stride + page) : -1;
-}
+// The units of a CTA, for a warp: each lane works one of the next 32 out, and
+// the warp takes them from there one after the other (working a unit out is a
+// long chain of dependent steps).
+struct Units {
+    Unit ahead;
+    int32_t k = 0;                             // units taken so far
 
-__device__ __forceinline__ int64_t row_of(const IndexArgs &a, const Unit &u, int j, int32_t id)
+    __device__ __forceinline__ bool next(const IndexArgs &a, int queries, int lane, bool *bad, Unit &u)
+    {
+        const int64_t unit = blockIdx.x + (int64_t)k * gridDim.x;
+        if (unit >= a.units) return false;
+        if ((k & 31) == 0) {
+            const int64_t mine = unit + (int64_t)lane * gridDim.x;
+            if (mine < a.units) ahead = unit_of(a, (int)mine, queries, bad);
+        }
+        const int src = k & 31;
+        auto take = [&](auto v) { return __shfl_sync(0xffffffffu, v, src); };
+        u.b = take(ahead.b);
+        u.t0 = take(ahead.t0);
+        u.nq = take(ahead.nq);
+        u.rows = take(ahead.rows);
+        u.i0 = take(ahead.i0);
+        u.q_len = take(ahead.q_len);
+        u.len = take(ahead.len);
+        u.tiles = take(ahead.tiles);
+        u.first_tile = take(ahead.first_tile);
+        u.p0 = take(ahead.p0);
+        u.k_base = take(ahead.k_base);
+        ++k;
+        return true;
+    }
+};
+
+// Cache rows of the boxes of a batch of tiles, one box per lane: tile lane >> boxes_log2 of the batch whose first key
+// is j0, box lane & (boxes - 1) of it.  -1 where the box's first key does not exist or is not in the cache.
+__device__ __forceinline__ int32_t rows_of(const IndexArgs &a, const Unit &u, int j0, int lane)
 {
+    const int64_t j = j0 + (int64_t)lane * a.run;
+    if (j >= u.len) return -1;
     int64_t row = u.k_base + j;
     if (a.layout_kv == SFM_LAYOUT_PAGED) {
-        const int in = j - (int)fdiv((uint32_t)j, a.block_div) * a.block;
-        row = id < 0 ? -1 : (int64_t)id * a.block + in;
+        const int page = (int)fdiv((uint32_t)j, a.block_div);
+        const int32_t id = page < a.table_stride ? __ldg(a.table + (int64_t)u.b * a.table_stride + page) : -1;
+        row = id < 0 ? -1 : (int64_t)id * a.block + (j - (int64_t)page * a.block);
     }
-    return row < a.k_rows ? row : -1;
+    return row < a.k_rows ? (int32_t)row : -1;
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
@@ -276,8 +305,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         // ---------------- loads ----------------
         int stage = 0, ks = 0, kphase = 0, n = 0;             // ks: stages filled so far (capped); n: units with tiles
         bool ok = true;
-        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-            const Unit u = unit_of(a, unit, queries, &bad);
+        Units units;
+        Unit u = {};
+        while (ok && units.next(a, queries, lane, &bad, u)) {
             if (u.tiles == 0) continue;
             const int qb = n & 1;
             ok = wait_warp(q_empty(qb), ((n >> 1) & 1) ^ 1, abort_flag);
@@ -291,13 +321,12 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 if (!a.fp8) tma_load(dst + q_rows * 128, &q_map, 64, row, q_full(qb));
             }
             ++n;
-            const bool mine = lane * a.run < kTile;           // the lane's box of every tile
-            int j = u.first_tile * kTile + lane * a.run;
-            int32_t page = mine && j < u.len ? page_of(a, u, j) : -1;
-            for (int t = 0; t < u.tiles; ++t, j += kTile) {
-                const int64_t row = mine && j < u.len ? row_of(a, u, j, page) : -1;
-                // the next tile's block id is under way while this tile's stage is waited for
-                if (t + 1 < u.tiles) page = mine && j + kTile < u.len ? page_of(a, u, j + kTile) : -1;
+            int32_t batch = -1;
+            for (int t = 0; t < u.tiles; ++t) {
+                const int in = (t << a.boxes_log2) & 31;      // the tile's first box in the batch
+                if (in == 0) batch = rows_of(a, u, (u.first_tile + t) * kTile, lane);
+                int32_t row = __shfl_sync(0xffffffffu, batch, in + (lane & ((1 << a.boxes_log2) - 1)));
+                if (lane >> a.boxes_log2) row = -1;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 ok = wait_warp(k_empty(stage), kphase ^ 1, abort_flag);
                 if (!ok) break;
@@ -305,8 +334,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 __syncwarp();
                 if (row >= 0) {
                     const uint32_t dst = k_smem + stage * k_bytes + lane * a.run * 128;
-                    tma_load(dst, &k_map, 0, (int)row, k_full(stage));
-                    if (!a.fp8) tma_load(dst + kTile * 128, &k_map, 64, (int)row, k_full(stage));
+                    tma_load(dst, &k_map, 0, row, k_full(stage));
+                    if (!a.fp8) tma_load(dst + kTile * 128, &k_map, 64, row, k_full(stage));
                 }
                 if (ks < a.stages) ++ks;
                 if (++stage == a.stages) stage = 0, kphase ^= 1;
@@ -378,15 +407,18 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         // ---------------- masks and scales of the keys ----------------
         int acc = 0, aphase = 0;
         bool ok = true;
-        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-            const Unit u = unit_of(a, unit, queries, &bad);
+        Units units;
+        Unit u = {};
+        while (ok && units.next(a, queries, lane, &bad, u)) {
             if (u.tiles == 0) continue;
             const int most = visible_of(a, u, u.nq - 1);
-            int j = u.first_tile * kTile + 4 * lane;          // four neighbouring keys per lane: they share a page
-            int32_t page = j < u.len ? page_of(a, u, j) : -1;
+            int j = u.first_tile * kTile + 4 * lane;          // four neighbouring keys per lane: they share a box
+            int32_t batch = -1;
             for (int t = 0; t < u.tiles; ++t, j += kTile) {
-                int64_t row = j < u.len ? row_of(a, u, j, page) : -1;
-                if (t + 1 < u.tiles) page = j + kTile < u.len ? page_of(a, u, j + kTile) : -1;
+                const int in = (t << a.boxes_log2) & 31;
+                if (in == 0) batch = rows_of(a, u, (u.first_tile + t) * kTile, lane);
+                int64_t row = __shfl_sync(0xffffffffu, batch, in + (4 * lane >> (7 - a.boxes_log2)));
+                row = row >= 0 && j < u.len ? row + (4 * lane & (a.run - 1)) : -1;
                 const int n = min(4, u.len - j);
                 if (row > a.k_rows - n) row = -1;
                 if (row < 0 && j < most && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
@@ -422,8 +454,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         int halves = 0;                                       // HP 128: exchanges so far
         int n = 0;                                            // units with tiles
         bool ok = true;
-        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-            const Unit u = unit_of(a, unit, queries, &bad);
+        Units units;
+        Unit u = {};
+        while (ok && units.next(a, queries, lane, &bad, u)) {
             if (a.visible && u.first_tile == 0 && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
             int vis[kSums];
             float *w = weights + (n & 1) * 256;
@@ -460,22 +493,23 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 const uint32_t at = tmem + acc * (parts * 64) + part * 64 + ((uint32_t)((warp & 3) * 32) << 16);
                 const bool live = i_part < u.nq;
                 if (live) {
-                    // all of the part leaves TMEM first, so that the next product can start
-                    uint32_t r[2][32];
-                    tmem_ld32(at, r[0]);
-                    tmem_ld32(at + 32, r[1]);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty(acc));
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        constexpr int kPer = 16 / kSums;
-                        const float4 v = *reinterpret_cast<const float4 *>(w + 4 * e);
-                        const uint32_t *x = r[e >> 3] + 4 * (e & 7);
-                        const int q = e / kPer;
-                        sum2[q] = fma2(make_float2(clip(x[0]), clip(x[1])), make_float2(v.x, v.y), sum2[q]);
-                        sum2[q] = fma2(make_float2(clip(x[2]), clip(x[3])), make_float2(v.z, v.w), sum2[q]);
+                    for (int half = 0; half < 2; ++half) {    // 32 columns at a time
+                        uint32_t r[32];
+                        tmem_ld32(at + 32 * half, r);
+                        tmem_wait_ld();
+                        if (half == 1) {                      // all of the part has left TMEM: the next product can start
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(acc_empty(acc));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 v = *reinterpret_cast<const float4 *>(w + 32 * half + 4 * e);
+                            float2 &s2 = sum2[(half * 8 + e) / (16 / kSums)];
+                            s2 = fma2(make_float2(clip(r[4 * e]), clip(r[4 * e + 1])), make_float2(v.x, v.y), s2);
+                            s2 = fma2(make_float2(clip(r[4 * e + 2]), clip(r[4 * e + 3])), make_float2(v.z, v.w), s2);
+                        }
                     }
                 } else {
                     tc_fence_before();
@@ -517,7 +551,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 for (int j = c0 + (i < u.nq ? u.tiles * kTile : 0) + lane; j < c1; j += 32) dst[j] = -INFINITY;
             }
         }
-        if (bad && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
+        if (bad && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
     }
 
     tc_fence_before();
@@ -658,6 +692,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
         a.run = p.block_size & -p.block_size;
         if (a.run > kTile) a.run = kTile;
     }
+    while ((a.run << a.boxes_log2) < kTile) ++a.boxes_log2;
     const uint32_t q_bytes = (64u << a.parts_log2) * kDim * elem, k_bytes = kTile * kDim * elem;
     const uint32_t scale_bytes = t->k_scales ? kScaleBytes : 0;
     const uint32_t misc_bytes = kMiscBytes - (hp == 128 ? 0 : 1024) + scale_bytes;

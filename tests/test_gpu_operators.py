@@ -400,10 +400,14 @@ INDEX_CASES = [   # dtype, heads, q_lens, key counts, layouts, block, ratio
     ("bf16", 128, [1, 1], [640, 250], "BSND", "PAGED", 128, 1), ("bf16", 128, [2, 2], [140, 250], "BSND", "PAGED", 128, 1),
     ("bf16", 64, [130], [1500], "TND", "TND", 0, 1), ("fp8", 33, [4], [90], "BSND", "BSND", 0, 1),
     ("bf16", 8, [16], [385], "BSND", "PAGED", 80, 1), ("fp16", 64, [2, 2], [5000, 129], "BSND", "PAGED", 64, 4),
+    # enough work that a unit holds several tiles of keys
+    ("fp8", 64, [96, 96, 96], [5000, 4100, 7000], "TND", "PAGED", 32, 1), ("bf16", 64, [200], [6001], "BSND", "PAGED", 128, 1),
+    ("fp8", 16, [1] * 48, [6000 - 50 * b for b in range(48)], "BSND", "PAGED", 128, 4),
+    ("bf16", 128, [1] * 30, [8000 - 99 * b for b in range(30)], "BSND", "PAGED", 16, 1),
 ]
 
 
-@pytest.mark.parametrize("case", INDEX_CASES, ids=str)
+@pytest.mark.parametrize("case", INDEX_CASES, ids=lambda c: f"{c[0]}-{c[1]}-{max(c[2])}x{len(c[2])}-{max(c[3])}-{c[4]}-{c[5]}-{c[6]}-{c[7]}")
 @pytest.mark.parametrize("mask", [3, 0])
 def test_index_scores(case, mask):
     dt, heads, q_lens, lens, lq, lkv, block, ratio = case
