@@ -418,6 +418,8 @@ def sparse_flash_mla(q: torch.Tensor, *, metadata: Metadata, ori_kv=None, cmp_kv
 # around the attention: rotary positions, cache rows, sparse indices
 # ---------------------------------------------------------------------------
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 # The structs of include/sfm.h as native-layout packers (the calls below build them every time; packing
 # all fields at once costs a fraction of setting them one by one)
@@ -426,6 +428,7 @@ _STORE_PARAMS = struct.Struct("@6if3ifi4q")
 _INDEX_PARAMS = struct.Struct("@12i")
 _INDEX_TENSORS = struct.Struct("@PPqqPPPiPPPPP")
 _TOPK_PARAMS = struct.Struct("@6iq")
+_SCORE_TYPES = {torch.float32: 0}
 _SIXTEEN_BIT = {torch.bfloat16: BF16, torch.float16: FP16}
 _INDEX_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
 
@@ -437,34 +440,38 @@ def _require(ok, what):
 
 def _first(name, x, types):
     """Check a call's first tensor: its dtype's code and its device's index."""
-    _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{name}: not a tensor")
     code = types.get(x.dtype)
-    _require(code is not None, f"{name}: dtype {x.dtype}")
+    if code is None:
+        raise ValueError(f"{name}: dtype {x.dtype}")
     dev = x.get_device()
-    _require(dev >= 0, f"{name}: not on a CUDA device")
+    if dev < 0:
+        raise ValueError(f"{name}: not on a CUDA device")
     return code, dev
 
 
+def _refuse(name, x, dtype, dev, shape=None):
+    """Say what is wrong with a tensor argument."""
+    _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
+    _require(x.dtype is dtype, f"{name}: dtype {x.dtype}, expected {dtype}")
+    _require(x.get_device() >= 0, f"{name}: not on a CUDA device")
+    _require(x.get_device() == dev, f"{name}: on {x.device}, expected cuda:{dev}")
+    _require(shape is None or x.shape == shape, f"{name}: shape {tuple(x.shape)}, expected {shape and tuple(shape)}")
+    raise ValueError(f"{name}: not contiguous")
+
+
 def _address(name, x, dtype, dev, shape):
-    """Device address of a contiguous tensor argument (0 for None)."""
-    if x is None:
-        return 0
-    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == dev and x.shape == shape
+    """Device address of a contiguous tensor argument."""
+    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == dev and x.shape == shape
             and x.is_contiguous()):
-        _require(isinstance(x, torch.Tensor), f"{name}: not a tensor")
-        _require(x.dtype is dtype, f"{name}: dtype {x.dtype}, expected {dtype}")
-        _require(x.get_device() >= 0, f"{name}: not on a CUDA device")
-        _require(x.get_device() == dev, f"{name}: on {x.device}, expected cuda:{dev}")
-        _require(x.shape == shape, f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{name}: not contiguous")
-    return x.data_ptr()
+        return x.data_ptr()
+    _refuse(name, x, dtype, dev, shape)
 
 
 def _status_address(status, dev):
-    if status is None:
-        return 0
-    _require(isinstance(status, torch.Tensor) and status.dtype is torch.int32 and status.get_device() == dev
-             and status.numel() >= 1, f"status: needs an int32 tensor on cuda:{dev}")
+    if not (isinstance(status, torch.Tensor) and status.dtype is _I32 and status.get_device() == dev and status.numel() >= 1):
+        raise ValueError(f"status: needs an int32 tensor on cuda:{dev}")
     return status.data_ptr()
 
 
@@ -497,15 +504,16 @@ def rope_frequencies(rope_dim: int, *, base: float = 10000.0, scaling: str = "no
 def _heads(x, name):
     """(tokens, heads, dim, token stride, head stride) of a (..., heads, dim) tensor with contiguous values."""
     shape, strides = x.shape, x.stride()
-    _require(len(shape) >= 2, f"{name}: needs (..., heads, values)")
     if len(shape) != 3:
+        _require(len(shape) >= 2, f"{name}: needs (..., heads, values)")
         try:
             x = x.view(-1, shape[-2], shape[-1]) if x.numel() else x.reshape(shape[:-2].numel(), shape[-2], shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}: the token dimensions do not flatten to one stride") from None
         shape, strides = x.shape, x.stride()
     tokens, heads, dim = shape
-    _require(strides[2] == 1 or dim == 1, f"{name}: the last dimension must be contiguous")
+    if strides[2] != 1 and dim != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
     # a dimension of one entry may report any stride: it gets that of dense rows
     head = strides[1] if heads > 1 else dim
     return tokens, heads, dim, strides[0] if tokens > 1 else max(head * heads, dim), head
@@ -514,13 +522,14 @@ def _heads(x, name):
 def _rows(x, name):
     """(rows, bytes between them) of a (..., row) tensor with contiguous rows."""
     shape, strides = x.shape, x.stride()
-    _require(len(shape) >= 2 and (strides[-1] == 1 or shape[-1] == 1), f"{name}: needs (..., row) with contiguous rows")
+    if len(shape) < 2 or (strides[-1] != 1 and shape[-1] != 1):
+        raise ValueError(f"{name}: needs (..., row) with contiguous rows")
     rows, stride = shape[0], strides[0]
     if len(shape) != 2:
         rows, stride = shape[:-1].numel(), strides[-2]
         for i in range(len(shape) - 2):
-            _require(shape[i] == 1 or strides[i] == strides[i + 1] * shape[i + 1],
-                     f"{name}: the row dimensions do not flatten to one stride")
+            if shape[i] != 1 and strides[i] != strides[i + 1] * shape[i + 1]:
+                raise ValueError(f"{name}: the row dimensions do not flatten to one stride")
         if shape[-2] == 1:      # the stride of the innermost dimension with more than one entry
             stride = next((strides[i] for i in range(len(shape) - 2, -1, -1) if shape[i] > 1), shape[-1])
     return rows, (stride if rows > 1 else shape[-1]) * x.element_size()
@@ -538,22 +547,22 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     ``out``: None for a new tensor, x itself to rotate in place, or a tensor
     of x's shape that does not overlap it.  Views with strides are taken as they are."""
     code, dev = _first("x", x, _SIXTEEN_BIT)
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return apply_rope(x, positions, inv_freq, amplitude=amplitude, rope_offset=rope_offset, interleaved=interleaved,
                               inverse=inverse, out=out)
     tokens, heads, dim, xt, xh = _heads(x, "x")
-    pos = _address("positions", positions, torch.int32, dev, (tokens,) if positions.dim() == 1 else x.shape[:-2])
+    pos = _address("positions", positions, _I32, dev, (tokens,) if positions.dim() == 1 else x.shape[:-2])
     n = inv_freq.numel()
-    freq = _address("inv_freq", inv_freq, torch.float64, dev, (n,))
+    freq = _address("inv_freq", inv_freq, _F64, dev, (n,))
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         yt, yh = heads * dim, dim
     elif out is x:
         yt, yh = xt, xh
     else:
-        _require(isinstance(out, torch.Tensor) and out.dtype is x.dtype and out.get_device() == dev and out.shape == x.shape,
-                 f"out: needs {tuple(x.shape)} of {x.dtype} on cuda:{dev}")
+        if not (isinstance(out, torch.Tensor) and out.dtype is x.dtype and out.get_device() == dev and out.shape == x.shape):
+            raise ValueError(f"out: needs {tuple(x.shape)} of {x.dtype} on cuda:{dev}")
         _, _, _, yt, yh = _heads(out, "out")
     params = _ROPE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, 2 * n, rope_offset,
                                ROPE_INTERLEAVED if interleaved else ROPE_HALF, bool(inverse), code, amplitude, 0, xt, xh, yt, yh)
@@ -578,7 +587,7 @@ def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_form
     slot_mapping: int32, one per token: head h goes to row slot * heads + h;
     negative: not written; None: row t * heads + h."""
     code, dev = _first("x", x, _SIXTEEN_BIT)
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return store_kv(x, cache, slot_mapping=slot_mapping, kv_format=kv_format, norm_weight=norm_weight, norm_eps=norm_eps,
                             positions=positions, inv_freq=inv_freq, amplitude=amplitude, rope_offset=rope_offset,
@@ -586,35 +595,41 @@ def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_form
     if x.dim() == 2:
         tokens, dim = x.shape
         strides = x.stride()
-        _require(strides[1] == 1 or dim == 1, "x: the last dimension must be contiguous")
+        if strides[1] != 1 and dim != 1:
+            raise ValueError("x: the last dimension must be contiguous")
         heads, xh, xt = 1, dim, strides[0] if tokens > 1 else dim
-    else:
-        _require(x.dim() == 3, "x: needs (tokens, dim) or (tokens, heads, dim)")
+    elif x.dim() == 3:
         tokens, heads, dim, xt, xh = _heads(x, "x")
+    else:
+        raise ValueError("x: needs (tokens, dim) or (tokens, heads, dim)")
     if kv_format == KV_INT8_PACKED or kv_format == KV_FP8_PACKED:
         kind, width = torch.uint8, 512 + 2 * (dim - 512) + 16
     else:
         kind, width = torch.float8_e4m3fn if kv_format == KV_FP8_ROWS else x.dtype, dim
-    _require(isinstance(cache, torch.Tensor) and cache.dtype is kind and cache.get_device() == dev,
-             f"cache: needs {kind} on cuda:{dev}")
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is kind and cache.get_device() == dev):
+        raise ValueError(f"cache: needs {kind} on cuda:{dev}")
     rows, row_stride = _rows(cache, "cache")
-    _require(cache.shape[-1] == width, f"cache: rows of {cache.shape[-1]}, expected {width}")
-    _require((scales is not None) == (kv_format == KV_FP8_ROWS), "scales: go with KV_FP8_ROWS rows")
-    _require((positions is None) == (inv_freq is None), "positions and inv_freq go together")
-    _require(norm_eps is not None or norm_weight is None, "norm_weight: needs norm_eps")
-    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    if cache.shape[-1] != width:
+        raise ValueError(f"cache: rows of {cache.shape[-1]}, expected {width}")
+    if (scales is not None) != (kv_format == KV_FP8_ROWS):
+        raise ValueError("scales: go with KV_FP8_ROWS rows")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    if norm_eps is None and norm_weight is not None:
+        raise ValueError("norm_weight: needs norm_eps")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     offset = 0 if not rot else dim - rot if rope_offset is None else rope_offset
     params = _STORE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, code, kv_format, norm_eps is not None,
                                 norm_eps or 0.0, rot, offset, ROPE_INTERLEAVED if interleaved else ROPE_HALF, amplitude, 0,
                                 xt, xh, row_stride, rows)
     each = (tokens,)
     rc = (_lib or lib()).sfm_kv_store(
-        params, x.data_ptr(), _address("norm_weight", norm_weight, torch.float32, dev, (min(dim, 512),)),
-        _address("positions", positions, torch.int32, dev, each),
-        _address("inv_freq", inv_freq, torch.float64, dev, (rot // 2,)),
-        _address("slot_mapping", slot_mapping, torch.int32, dev, each), cache.data_ptr(),
-        0 if scales is None else _address("scales", scales, torch.float32, dev, (rows,) if scales.dim() == 1 else cache.shape[:-1]),
-        _status_address(status, dev), _raw_stream(dev))
+        params, x.data_ptr(), 0 if norm_weight is None else _address("norm_weight", norm_weight, _F32, dev, (min(dim, 512),)),
+        0 if positions is None else _address("positions", positions, _I32, dev, each),
+        0 if inv_freq is None else _address("inv_freq", inv_freq, _F64, dev, (rot // 2,)),
+        0 if slot_mapping is None else _address("slot_mapping", slot_mapping, _I32, dev, each), cache.data_ptr(),
+        0 if scales is None else _address("scales", scales, _F32, dev, (rows,) if scales.dim() == 1 else cache.shape[:-1]),
+        0 if status is None else _status_address(status, dev), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_kv_store", rc)
     return cache
@@ -635,7 +650,7 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     is not visible; visible (tokens) int32).  ``out`` may be a
     view with wider rows."""
     code, dev = _first("q", q, _INDEX_TYPES)
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return index_scores(q, index_k, weights, max_seqlen_kv=max_seqlen_kv, k_scales=k_scales, block_table=block_table,
                                 cu_seqlens_q=cu_seqlens_q, cu_seqlens_kv=cu_seqlens_kv, seqused_q=seqused_q,
@@ -644,50 +659,57 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
                                 visible=visible, status=status)
     lq, lkv = _LAYOUTS[layout_q], _LAYOUTS[layout_kv]
     shape = q.shape
-    _require(len(shape) == (4 if lq == BSND else 3), "q: BSND has 4 dimensions, TND 3")
+    if len(shape) != (4 if lq == BSND else 3):
+        raise ValueError("q: BSND has 4 dimensions, TND 3")
     heads, dim = shape[-2], shape[-1]
     if lq == BSND:
         batch, max_seqlen_q = shape[0], shape[1]
         tokens = batch * max_seqlen_q
+    elif cu_seqlens_q is None:
+        raise ValueError("cu_seqlens_q: required for TND")
     else:
-        _require(cu_seqlens_q is not None, "cu_seqlens_q: required for TND")
         batch, tokens = cu_seqlens_q.numel() - 1, shape[0]
-    _require(isinstance(index_k, torch.Tensor) and index_k.dtype is q.dtype and index_k.get_device() == dev,
-             f"index_k: needs {q.dtype} on cuda:{dev}")
+    if not (isinstance(index_k, torch.Tensor) and index_k.dtype is q.dtype and index_k.get_device() == dev):
+        raise ValueError(f"index_k: needs {q.dtype} on cuda:{dev}")
     kshape = index_k.shape
-    _require(len(kshape) == (2 if lkv == TND else 3) and kshape[-1] == dim,
-             "index_k: needs (t, dim), (b, S, dim) or (blocks, block_size, dim) with q's dim")
-    if lkv == BSND:
-        _require(kshape[1] == max_seqlen_kv and kshape[0] == batch, "index_k: needs (b, max_seqlen_kv, dim)")
+    if len(kshape) != (2 if lkv == TND else 3) or kshape[-1] != dim:
+        raise ValueError("index_k: needs (t, dim), (b, S, dim) or (blocks, block_size, dim) with q's dim")
+    if lkv == BSND and (kshape[1] != max_seqlen_kv or kshape[0] != batch):
+        raise ValueError("index_k: needs (b, max_seqlen_kv, dim)")
     rows, row_stride = _rows(index_k, "index_k")
-    cols = 0
+    cols = table = 0
+    each = (batch,)
     if block_table is not None:
-        _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: needs (b, blocks)")
+        if block_table.dim() != 2:
+            raise ValueError("block_table: needs (b, blocks)")
         cols = block_table.shape[1]
+        table = _address("block_table", block_table, _I32, dev, (batch, cols))
     params = _INDEX_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, cmp_ratio, mask_mode, lq, lkv, code,
                                 kshape[1] if lkv == PAGED else 0)
-    each, i32 = (batch,), torch.int32
     tensors = _INDEX_TENSORS.pack(
         _address("q", q, q.dtype, dev, shape), index_k.data_ptr(), row_stride, rows,
-        0 if k_scales is None else _address("k_scales", k_scales, torch.float32, dev, (rows,) if k_scales.dim() == 1 else kshape[:-1]),
-        _address("weights", weights, torch.float32, dev, shape[:-1]),
-        _address("block_table", block_table, i32, dev, (batch, cols)), cols,
-        _address("cu_seqlens_q", cu_seqlens_q, i32, dev, (batch + 1,)),
-        _address("cu_seqlens_kv", cu_seqlens_kv, i32, dev, (batch + 1,)), _address("seqused_q", seqused_q, i32, dev, each),
-        _address("seqused_kv", seqused_kv, i32, dev, each), _address("cmp_residual_kv", cmp_residual_kv, i32, dev, each))
+        0 if k_scales is None else _address("k_scales", k_scales, _F32, dev, (rows,) if k_scales.dim() == 1 else kshape[:-1]),
+        _address("weights", weights, _F32, dev, shape[:-1]), table, cols,
+        0 if cu_seqlens_q is None else _address("cu_seqlens_q", cu_seqlens_q, _I32, dev, (batch + 1,)),
+        0 if cu_seqlens_kv is None else _address("cu_seqlens_kv", cu_seqlens_kv, _I32, dev, (batch + 1,)),
+        0 if seqused_q is None else _address("seqused_q", seqused_q, _I32, dev, each),
+        0 if seqused_kv is None else _address("seqused_kv", seqused_kv, _I32, dev, each),
+        0 if cmp_residual_kv is None else _address("cmp_residual_kv", cmp_residual_kv, _I32, dev, each))
     if out is None:
-        out = torch.empty((tokens, max(max_seqlen_kv, 0)), dtype=torch.float32, device=q.device)
+        out = torch.empty((tokens, max(max_seqlen_kv, 0)), dtype=_F32, device=q.device)
         stride = max_seqlen_kv
     else:
-        _require(isinstance(out, torch.Tensor) and out.dtype is torch.float32 and out.get_device() == dev
-                 and out.shape == (tokens, max_seqlen_kv) and (out.stride(1) == 1 or max_seqlen_kv == 1),
-                 f"out: needs fp32 ({tokens}, {max_seqlen_kv}) with contiguous rows on cuda:{dev}")
+        if not (isinstance(out, torch.Tensor) and out.dtype is _F32 and out.get_device() == dev
+                and out.shape == (tokens, max_seqlen_kv) and (out.stride(1) == 1 or max_seqlen_kv == 1)):
+            raise ValueError(f"out: needs fp32 ({tokens}, {max_seqlen_kv}) with contiguous rows on cuda:{dev}")
         stride = out.stride(0) if tokens > 1 else max_seqlen_kv
     if visible is None:
-        visible = torch.empty(tokens, dtype=i32, device=q.device)
-    rc = (_lib or lib()).sfm_index_scores(params, tensors, out.data_ptr(), stride,
-                                          _address("visible", visible, i32, dev, (tokens,)), _status_address(status, dev),
-                                          _raw_stream(dev))
+        visible = torch.empty(each if tokens == batch else (tokens,), dtype=_I32, device=q.device)
+        seen = visible.data_ptr()
+    else:
+        seen = _address("visible", visible, _I32, dev, (tokens,))
+    rc = (_lib or lib()).sfm_index_scores(params, tensors, out.data_ptr(), stride, seen,
+                                          0 if status is None else _status_address(status, dev), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_index_scores", rc)
     return out, visible
@@ -701,23 +723,26 @@ def select_topk(scores: torch.Tensor, k: int, *, lengths=None, block_size: int =
     and ``last_blocks`` always among them (see sfm_topk_select).  They are what
     sparse_flash_mla takes as cmp_sparse_indices / ori_sparse_indices.
     lengths: int32 (rows), scores a row really has (None: n)."""
-    _, dev = _first("scores", scores, {torch.float32: 0})
-    if stream is not None or dev != torch.cuda.current_device():
+    _, dev = _first("scores", scores, _SCORE_TYPES)
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return select_topk(scores, k, lengths=lengths, block_size=block_size, first_blocks=first_blocks,
                                last_blocks=last_blocks, out=out, status=status)
-    _require(scores.dim() == 2, "scores: needs (rows, n)")
+    if scores.dim() != 2:
+        raise ValueError("scores: needs (rows, n)")
     rows, n = scores.shape
     strides = scores.stride()
-    _require(strides[1] == 1 or n == 1, "scores: rows must be contiguous")
+    if strides[1] != 1 and n != 1:
+        raise ValueError("scores: rows must be contiguous")
     if out is None:
-        out = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=scores.device)
+        out = torch.empty((rows, max(k, 0)), dtype=_I32, device=scores.device)
         got = out.data_ptr()
     else:
-        got = _address("out", out, torch.int32, dev, (rows, k))
+        got = _address("out", out, _I32, dev, (rows, k))
     params = _TOPK_PARAMS.pack(rows, n, k, block_size, first_blocks, last_blocks, strides[0] if rows > 1 else n)
-    rc = (_lib or lib()).sfm_topk_select(params, scores.data_ptr(), _address("lengths", lengths, torch.int32, dev, (rows,)), got,
-                                         _status_address(status, dev), _raw_stream(dev))
+    rc = (_lib or lib()).sfm_topk_select(params, scores.data_ptr(),
+                                         0 if lengths is None else _address("lengths", lengths, _I32, dev, (rows,)), got,
+                                         0 if status is None else _status_address(status, dev), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_topk_select", rc)
     return out
