@@ -596,13 +596,19 @@ int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t
 }
 
 template <int HP>
-cudaError_t launch(const IndexArgs &a, const CUtensorMap &q, const CUtensorMap &k, int grid, size_t smem, cudaStream_t st)
+cudaError_t launch(const IndexArgs &a, const CUtensorMap &q, const CUtensorMap &k, int device, int grid, size_t smem,
+                   cudaStream_t st)
 {
-    const cudaError_t e =
-        cudaFuncSetAttribute(sfm_index_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    sfm_index_kernel<HP><<<grid, kThreads, smem, st>>>(a, q, k);
-    return cudaGetLastError();
+    static std::atomic<bool> ready[kMaxDevices];
+    return prepared_launch(
+        ready, device,
+        [&] {
+            return cudaFuncSetAttribute(sfm_index_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+        },
+        [&] {
+            sfm_index_kernel<HP><<<grid, kThreads, smem, st>>>(a, q, k);
+            return cudaGetLastError();
+        });
 }
 
 }  // namespace
@@ -645,9 +651,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
         return SFM_ERR_LAYOUT;
 
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SFM_ERR_CUDA;
+    if (current_sms(&dev, &sms) != cudaSuccess) return SFM_ERR_CUDA;
 
     const int hp = p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : p.num_heads <= 64 ? 64 : 128;
     IndexArgs a = {};
@@ -725,10 +729,10 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     switch (hp) {
-    case 16: e = launch<16>(a, q_map, k_map, grid, smem, st); break;
-    case 32: e = launch<32>(a, q_map, k_map, grid, smem, st); break;
-    case 64: e = launch<64>(a, q_map, k_map, grid, smem, st); break;
-    default: e = launch<128>(a, q_map, k_map, grid, smem, st); break;
+    case 16: e = launch<16>(a, q_map, k_map, dev, grid, smem, st); break;
+    case 32: e = launch<32>(a, q_map, k_map, dev, grid, smem, st); break;
+    case 64: e = launch<64>(a, q_map, k_map, dev, grid, smem, st); break;
+    default: e = launch<128>(a, q_map, k_map, dev, grid, smem, st); break;
     }
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }

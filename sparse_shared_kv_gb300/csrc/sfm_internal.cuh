@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sfm.h"
 
 namespace sfm {
@@ -359,6 +361,42 @@ inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 blo
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ----------------------------------------------------------------------------
+// what a launch asks the runtime for, remembered per device (each question
+// costs a good part of a launch)
+// ----------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+
+inline cudaError_t current_sms(int *device, int *sms)
+{
+    static std::atomic<int> known[kMaxDevices];
+    const cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return e;
+    const bool keep = *device < kMaxDevices;
+    *sms = keep ? known[*device].load(std::memory_order_relaxed) : 0;
+    if (*sms > 0) return cudaSuccess;
+    const cudaError_t q = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
+    if (q == cudaSuccess && keep) known[*device].store(*sms, std::memory_order_relaxed);
+    return q;
+}
+
+// Launch with `prepare` (function attributes) done once per device.  `ready`:
+// one flag per device, of this kernel and its attributes.  Attributes are lost
+// when the device is reset: a refused launch prepares again, once.
+template <typename Prepare, typename Launch>
+inline cudaError_t prepared_launch(std::atomic<bool> (&ready)[kMaxDevices], int device, Prepare prepare, Launch launch)
+{
+    const bool keep = device < kMaxDevices;
+    if (keep && ready[device].load(std::memory_order_acquire)) {
+        if (launch() == cudaSuccess) return cudaSuccess;
+        cudaGetLastError();
+    }
+    cudaError_t e = prepare();
+    if (e != cudaSuccess) return e;
+    if (keep) ready[device].store(true, std::memory_order_release);
+    return launch();
 }
 
 // ----------------------------------------------------------------------------

@@ -5,9 +5,12 @@
 // bounds it.  A group of lanes holds one row in registers, eight values (one
 // 16-byte load) per lane and step, so that 16 neighbouring lanes hold one
 // 128-value tile: the sum of squares and each tile's largest magnitude are
-// shuffles, and nothing but the cosines and (for half-layout pairs, which sit
-// in other lanes) the rotated part goes through shared memory.  Everything
-// is held in fp32 until the one rounding to the cache's format.
+// shuffles, and so are the partners of half-layout pairs where they sit in the
+// same step.  The lanes of a group work out a token's cosines and sines
+// together, hand them over through shared memory and keep their own for the
+// token's other heads.  The next row's values are under way while a row is
+// worked on.  Everything is held in fp32 until the one rounding to the
+// cache's format.
 #include <math.h>
 
 #include "sfm_internal.cuh"
@@ -59,21 +62,28 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// LANES lanes per row, STEPS 16-byte accesses per lane; FORMAT: enum sfm_kv_format
-template <typename T, int FORMAT, int LANES, int STEPS>
+__device__ __forceinline__ float fast_inverse(float x)      // one unit in the last place
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// LANES lanes per row, STEPS 16-byte accesses per lane; FORMAT: enum sfm_kv_format;
+// ROPE: 0 none, 1 interleaved, 2 half with the rotated part inside one step, 3 half
+template <typename T, int FORMAT, int LANES, int STEPS, int ROPE>
 __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
 {
     constexpr int kGroups = kThreads / LANES;
-    __shared__ unsigned long long step[kMaxDim / 2];
-    __shared__ float2 cs_all[kGroups][LANES * STEPS * 4 < kMaxDim / 2 ? LANES * STEPS * 4 : kMaxDim / 2];
-    extern __shared__ float turn_all[];          // half layout: [kGroups][rot]
+    constexpr int kPairs = ROPE == 0 ? 1 : LANES * STEPS * 4 < kMaxDim / 2 ? LANES * STEPS * 4 : kMaxDim / 2;
+    __shared__ unsigned long long step[kPairs];
+    __shared__ __align__(16) float2 cs_all[kGroups][kPairs];
+    extern __shared__ float turn_all[];          // ROPE 3: [kGroups][rot]
 
     const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
     float2 *cs = cs_all[group];
     float *turn = turn_all + group * a.rot;
-    const int pairs = a.rot / 2;
-    for (int i = tid; i < pairs; i += kThreads) step[i] = rope::turn_step(__ldg(a.inv_freq + i));
-    __syncthreads();
+    const int pairs = ROPE ? a.rot / 2 : 0;
 
     // a group takes a run of neighbouring rows, so that the heads of a token
     // share its cosines
@@ -81,26 +91,53 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
     const int64_t per = (a.total + groups - 1) / groups;
     const int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * per;
     const int64_t r1 = min(r0 + per, a.total);
-    int last_token = -1;
-    for (int64_t rr = r0; rr < r0 + per; ++rr) {     // every group runs the same count: warp collectives inside
-        const bool live = rr < r1;
-        const int64_t r = live ? rr : 0;
-        const int token = a.heads == 1 ? (int)r : (int)fdiv((uint32_t)r, a.heads_div);
-        const int head = (int)(r - (int64_t)token * a.heads);
-        const int64_t slot = a.slots ? (int64_t)__ldg(a.slots + token) : token;
-        const int64_t row = slot * a.heads + head;
-        const bool inside = slot >= 0 && row < a.rows;
-        if (live && slot >= 0 && !inside && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
 
-        float v[STEPS][8];
+    uint4 w[STEPS];
+    int32_t token, head, position, slot;
+    auto load = [&](int64_t r) {                  // row r: its values, position and slot
+        token = a.heads == 1 ? (int)r : (int)fdiv((uint32_t)r, a.heads_div);
+        head = (int)(r - (int64_t)token * a.heads);
         const T *src = static_cast<const T *>(a.x) + (int64_t)token * a.xt + (int64_t)head * a.xh;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int at = (s * LANES + lane) * 8;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live && at < a.dim) w = __ldg(reinterpret_cast<const uint4 *>(src + at));
-            rope::unpack8<T>(w, v[s]);
+            w[s] = at < a.dim ? __ldg(reinterpret_cast<const uint4 *>(src + at)) : make_uint4(0, 0, 0, 0);
         }
+        slot = a.slots ? __ldg(a.slots + token) : token;
+        if (ROPE) position = __ldg(a.positions + token);
+    };
+    load(r0 < r1 ? r0 : 0);
+    if (ROPE) {
+        for (int i = tid; i < pairs; i += kThreads) step[i] = rope::turn_step(__ldg(a.inv_freq + i));
+        __syncthreads();
+    }
+
+    // cosines and sines of a lane's values: with one step per row (index rows, many heads per token) they stay in
+    // registers while the token stays the same
+    constexpr int kOwn = ROPE == 1 ? 4 : 8;
+    constexpr bool kKeep = ROPE != 0 && STEPS == 1;
+    float2 kept[kKeep ? kOwn : 1];
+    auto own = [&](int at, float2 (&c)[kOwn]) {
+        const int first = ROPE == 1 ? at / 2 : at >= pairs ? at - pairs : at;
+#pragma unroll
+        for (int e = 0; e < kOwn; e += 2) {
+            const float4 two = *reinterpret_cast<const float4 *>(cs + first + e);
+            c[e] = make_float2(two.x, two.y);
+            c[e + 1] = make_float2(two.z, two.w);
+        }
+    };
+    int last_token = -1;
+    for (int64_t i = 0; i < per; ++i) {          // every group runs the same count: warp collectives inside
+        const int64_t r = r0 + i;
+        const bool live = r < r1;
+        float v[STEPS][8];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) rope::unpack8<T>(w[s], v[s]);
+        const int64_t row = (int64_t)slot * a.heads + head;
+        const bool inside = slot >= 0 && row < a.rows;
+        if (live && slot >= 0 && !inside && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
+        const int32_t this_token = token, this_position = position;
+        if (r + 1 < r1) load(r + 1);
 
         if (a.norm) {
             float sum = 0.f;
@@ -112,8 +149,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
                 }
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            // 1 / sqrt: correctly rounded parts, so the norm costs no precision
-            const float rs = 1.f / sqrtf(fmaf(sum, a.inv_norm_dim, a.eps));
+            const float rs = rsqrtf(fmaf(sum, a.inv_norm_dim, a.eps));
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int at = (s * LANES + lane) * 8;
@@ -121,9 +157,9 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
                     if (a.weight) {
                         const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + at));
                         const float4 w1 = __ldg(reinterpret_cast<const float4 *>(a.weight + at + 4));
-                        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[s][e] = v[s][e] * rs * w[e];
+                        for (int e = 0; e < 8; ++e) v[s][e] = v[s][e] * rs * wt[e];
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[s][e] *= rs;
@@ -132,14 +168,19 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
             }
         }
 
-        if (pairs) {
-            __syncwarp();
-            if (token != last_token) {
-                const int32_t p = __ldg(a.positions + token);
-                for (int i = lane; i < pairs; i += LANES) cs[i] = rope::cos_sin(p, step[i], a.amplitude, false);
-                last_token = token;
+        if (ROPE) {
+            if (__any_sync(0xffffffffu, this_token != last_token)) {
+                __syncwarp();
+                for (int p = lane; p < pairs; p += LANES) cs[p] = rope::cos_sin(this_position, step[p], a.amplitude, false);
+                __syncwarp();
+                if constexpr (kKeep) {
+                    const int at = lane * 8 - a.off;
+                    if (at >= 0 && at < a.rot) own(at, kept);
+                }
+                last_token = this_token;
             }
-            if (a.half) {
+            if (ROPE == 3) {
+                __syncwarp();
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
                     const int at = (s * LANES + lane) * 8 - a.off;
@@ -148,28 +189,36 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
                         for (int e = 0; e < 8; ++e) turn[at + e] = v[s][e];
                     }
                 }
+                __syncwarp();
             }
-            __syncwarp();
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int at = (s * LANES + lane) * 8 - a.off;
-                if (at < 0 || at >= a.rot) continue;
-                if (a.half) {
-                    const bool second = at >= pairs;
-                    const int i = second ? at - pairs : at;
+                const bool in = at >= 0 && at < a.rot;
+                // (half layout inside one step: the other steps rotate nothing in any lane)
+                if (ROPE == 2 ? a.off / (LANES * 8) != s : !in) continue;
+                float2 c[kOwn];
+                if constexpr (kKeep) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float other = turn[second ? i + e : i + pairs + e];
-                        const float2 q = second ? rope::rotate(other, v[s][e], cs[i + e])
-                                                : rope::rotate(v[s][e], other, cs[i + e]);
-                        v[s][e] = second ? q.y : q.x;
-                    }
-                } else {
+                    for (int e = 0; e < kOwn; ++e) c[e] = kept[e];
+                } else if (in) {
+                    own(at, c);
+                }
+                const bool second = at >= pairs;
+                if (ROPE == 1) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 q = rope::rotate(v[s][2 * e], v[s][2 * e + 1], cs[at / 2 + e]);
+                        const float2 q = rope::rotate(v[s][2 * e], v[s][2 * e + 1], c[e]);
                         v[s][2 * e] = q.x;
                         v[s][2 * e + 1] = q.y;
+                    }
+                } else {
+                    const int from = (tid & 31) + (in ? (second ? -pairs : pairs) / 8 : 0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float other = ROPE == 2 ? __shfl_sync(0xffffffffu, v[s][e], from)
+                                                      : turn[second ? at - pairs + e : at + pairs + e];
+                        if (in) v[s][e] = fmaf(v[s][e], c[e % kOwn].x, second ? other * c[e % kOwn].y : -other * c[e % kOwn].y);
                     }
                 }
             }
@@ -212,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
                     *reinterpret_cast<uint4 *>(dst + 512 + (at - 512) * 2) = rope::pack8<T>(v[s]);
                     continue;
                 }
-                const float scale = max_nan(most[kRow ? 0 : s] / kMost, kTiny);
-                const float inv = 1.f / scale;
+                const float scale = max_nan(most[kRow ? 0 : s] * (1.f / kMost), kTiny);
+                const float inv = fast_inverse(scale);
                 const float(&f)[8] = v[s];
                 uint2 w;
                 if (FORMAT == SFM_KV_INT8_PACKED) {
@@ -239,13 +288,19 @@ cudaError_t launch(const StoreArgs &a, cudaStream_t st)
 {
     constexpr int kGroups = kThreads / LANES;
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.total + kGroups - 1) / kGroups, most = (int64_t)sms * 8;
-    const size_t smem = a.half ? (size_t)kGroups * a.rot * sizeof(float) : 0;
-    auto kernel = sfm_store_kernel<T, FORMAT, LANES, STEPS>;
-    kernel<<<(unsigned)(want < most ? want : most), kThreads, smem, st>>>(a);
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    const int width = LANES * 8;
+    const int form = !a.rot ? 0 : !a.half ? 1 : a.off / width == (a.off + a.rot - 1) / width ? 2 : 3;
+    const size_t smem = form == 3 ? (size_t)kGroups * a.rot * sizeof(float) : 0;
+    switch (form) {
+    case 0: sfm_store_kernel<T, FORMAT, LANES, STEPS, 0><<<grid, kThreads, smem, st>>>(a); break;
+    case 1: sfm_store_kernel<T, FORMAT, LANES, STEPS, 1><<<grid, kThreads, smem, st>>>(a); break;
+    case 2: sfm_store_kernel<T, FORMAT, LANES, STEPS, 2><<<grid, kThreads, smem, st>>>(a); break;
+    default: sfm_store_kernel<T, FORMAT, LANES, STEPS, 3><<<grid, kThreads, smem, st>>>(a); break;
+    }
     return cudaGetLastError();
 }
 

@@ -68,6 +68,9 @@ struct ClusterShared {
     uint32_t list_n, list_base;
 };
 
+constexpr int kMaxDynamic = kMaxSlice * 4 + kMaxSlice / 4 + (int)sizeof(ClusterShared);
+static_assert(kMaxDynamic + sizeof(Shared) <= 232448, "shared memory budget");
+
 __device__ __forceinline__ uint32_t key_of(float x)
 {
     const uint32_t b = __float_as_uint(x + 0.f);          // -0 becomes 0
@@ -624,25 +627,30 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
 }
 
 template <int NT, bool CACHED>
-cudaError_t launch(const TopkArgs &a, int64_t rows, size_t smem, cudaStream_t st)
+cudaError_t launch(const TopkArgs &a, int device, int64_t rows, size_t smem, cudaStream_t st)
 {
+    static std::atomic<bool> ready[kMaxDevices];
     auto kernel = sfm_topk_kernel<NT, CACHED>;
-    cudaError_t e = cudaSuccess;
-    if (smem > 16384) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * a.cluster));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return prepared_launch(
+        ready, device,
+        [&] {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
+            return e == cudaSuccess ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
+        },
+        [&] {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(rows * a.cluster));
+            cfg.blockDim = dim3(NT);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = st;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)a.cluster;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+            return cudaLaunchKernelEx(&cfg, kernel, a);
+        });
 }
 
 }  // namespace
@@ -665,9 +673,7 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     if (((uintptr_t)scores | (uintptr_t)lengths | (uintptr_t)indices) & 3u) return SFM_ERR_LAYOUT;
 
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SFM_ERR_CUDA;
+    if (current_sms(&dev, &sms) != cudaSuccess) return SFM_ERR_CUDA;
 
     TopkArgs a = {};
     a.scores = scores;
@@ -695,9 +701,9 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     const size_t smem = (size_t)a.slice_cap * 4 + (size_t)a.slice_cap / 4 + (c > 1 ? sizeof(ClusterShared) : 0);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (!cached) e = launch<1024, false>(a, p.rows, smem, st);
-    else if (slice(c) > 16384) e = launch<1024, true>(a, p.rows, smem, st);
-    else if (c > 1) e = launch<512, true>(a, p.rows, smem, st);
-    else e = launch<256, true>(a, p.rows, smem, st);
+    if (!cached) e = launch<1024, false>(a, dev, p.rows, smem, st);
+    else if (slice(c) > 16384) e = launch<1024, true>(a, dev, p.rows, smem, st);
+    else if (c > 1) e = launch<512, true>(a, dev, p.rows, smem, st);
+    else e = launch<256, true>(a, dev, p.rows, smem, st);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
