@@ -2,11 +2,11 @@
 // frequencies of the usual context stretchings (sfm_rope_frequencies, host).
 //
 // Every value is read and written once, so memory bounds it.  A block takes
-// up to 1024 units of one token (or of up to 16 tokens with few heads): each
-// thread first issues the 16-byte loads of its four units, the block then
-// computes the token's cosines and sines once for all heads into shared
-// memory while those loads are in flight, and the units are rotated in fp32
-// and stored, one rounding per value.
+// steps of 1024 units of one token (or one step of up to 16 tokens with few
+// heads): each thread first issues the 16-byte loads of its four units, the
+// block then computes the token's cosines and sines once for all heads into
+// shared memory while those loads are in flight, and the units are rotated in
+// fp32 and stored, one rounding per value.
 #include <math.h>
 
 #include "sfm_internal.cuh"
@@ -29,20 +29,89 @@ struct RopeArgs {
     int64_t xt, xh, yt, yh;                    // strides in elements
     int32_t tokens, heads, dim, rot, off;
     int32_t units, token_units, block_tokens;  // units per head, per token; tokens per block
+    int32_t block_units;                       // units per block
     FastDiv units_div, token_div;
     float amplitude;
     int32_t inverse, in_place;
 };
 
-// VEC: values per access (8 or 1).  A unit of an interleaved row of vectors is
-// one vector of four pairs; in every other case it is two accesses that hold
-// the first and second members of VEC pairs, or one access outside the rotated
+// The common form: 16-byte accesses in the order of memory, out of place (or in
+// place with interleaved pairs).  A half-layout vector also reads its partners
+// (a neighbour loads them too, so they come from L1) and writes its own values
+// only.  A block takes a run of a token's vectors, as long as there are blocks
+// enough for every SM, so that a long row works its cosines out a few times
+// only.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(const RopeArgs a)
+{
+    __shared__ __align__(16) float2 cs[kMaxPairs];
+    const int tid = threadIdx.x, half = a.rot / 2;
+    const int64_t t0 = (int64_t)blockIdx.x * a.block_tokens;
+    const int ntok = (int)min((int64_t)a.block_tokens, a.tokens - t0);
+    const int first = blockIdx.y * a.block_units;
+    const int last = min(first + a.block_units, ntok * a.token_units);
+
+    for (int base = first; base < last; base += kBlockUnits) {
+        uint4 va[kUnits], vb[kUnits];
+        int32_t tok[kUnits], head[kUnits], at[kUnits];
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const int u = base + k * kThreads + tid;
+            if (u >= last) continue;
+            tok[k] = (int)fdiv((uint32_t)u, a.token_div);
+            const int r = u - tok[k] * a.token_units;
+            head[k] = (int)fdiv((uint32_t)r, a.units_div);
+            at[k] = (r - head[k] * a.units) * 8 + (a.in_place ? a.off : 0);
+            const T *src = static_cast<const T *>(a.x) + (t0 + tok[k]) * a.xt + (int64_t)head[k] * a.xh + at[k];
+            va[k] = *reinterpret_cast<const uint4 *>(src);
+            const int in = at[k] - a.off;
+            if (HALF && in >= 0 && in < a.rot) vb[k] = *reinterpret_cast<const uint4 *>(src + (in < half ? half : -half));
+        }
+        if (base == first) {
+            for (int i = tid; i < ntok * half; i += kThreads) {
+                const int t = i / half;
+                cs[i] = rope::cos_sin(__ldg(a.positions + t0 + t), rope::turn_step(__ldg(a.inv_freq + i - t * half)),
+                                      a.amplitude, a.inverse != 0);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            if (base + k * kThreads + tid >= last) continue;
+            const int in = at[k] - a.off;
+            if (in >= 0 && in < a.rot) {
+                float p[8];
+                rope::unpack8<T>(va[k], p);
+                const float2 *c = cs + tok[k] * half + (HALF ? (in < half ? in : in - half) : in / 2);
+                if (HALF) {
+                    float q[8];
+                    rope::unpack8<T>(vb[k], q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] = fmaf(p[e], c[e].x, in < half ? -q[e] * c[e].y : q[e] * c[e].y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 r = rope::rotate(p[2 * e], p[2 * e + 1], c[e]);
+                        p[2 * e] = r.x;
+                        p[2 * e + 1] = r.y;
+                    }
+                }
+                va[k] = rope::pack8<T>(p);
+            }
+            T *dst = static_cast<T *>(a.y) + (t0 + tok[k]) * a.yt + (int64_t)head[k] * a.yh + at[k];
+            *reinterpret_cast<uint4 *>(dst) = va[k];
+        }
+    }
+}
+
+// The other forms: half layout in place, and rows without 16-byte accesses.
+// VEC: values per access (8 or 1).  A unit is two accesses that hold the
+// first and second members of VEC pairs, or one access outside the rotated
 // part, which is copied.
 template <typename T, int VEC, bool HALF>
 __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
 {
     using Access = typename std::conditional<VEC == 8, uint4, T>::type;
-    constexpr bool kTwo = HALF || VEC == 1;
     __shared__ float2 cs[kMaxPairs];
 
     const int tid = threadIdx.x;
@@ -50,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
     const int ntok = (int)min((int64_t)a.block_tokens, a.tokens - t0);
     const int first = blockIdx.y * kBlockUnits;
     const int last = min(first + kBlockUnits, ntok * a.token_units);
-    const int pair_units = kTwo ? a.rot / 2 / VEC : a.rot / VEC;
+    const int pair_units = a.rot / 2 / VEC;
 
     Access va[kUnits], vb[kUnits];
     int64_t ya[kUnits];
@@ -67,24 +136,18 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
         const int i = r - head * a.units;
         const int64_t t = t0 + tok;
         int at;
-        if (kTwo) {
-            if (i < pair_units) {
-                at = a.off + (HALF ? i * VEC : 2 * i);
-                other[k] = HALF ? a.rot / 2 : 1;
-                pair[k] = tok * (a.rot / 2) + i * VEC;
-            } else {
-                at = (i - pair_units) * VEC;
-                if (at >= a.off) at += a.rot;
-                pair[k] = -1;
-            }
+        if (i < pair_units) {
+            at = a.off + (HALF ? i * VEC : 2 * i);
+            other[k] = HALF ? a.rot / 2 : 1;
+            pair[k] = tok * (a.rot / 2) + i * VEC;
         } else {
-            at = i * VEC + (a.in_place ? a.off : 0);
-            const bool inside = at >= a.off && at < a.off + a.rot;
-            pair[k] = inside ? tok * (a.rot / 2) + (at - a.off) / 2 : -1;
+            at = (i - pair_units) * VEC;
+            if (at >= a.off) at += a.rot;
+            pair[k] = -1;
         }
         const T *src = static_cast<const T *>(a.x) + t * a.xt + (int64_t)head * a.xh + at;
         va[k] = *reinterpret_cast<const Access *>(src);
-        if (kTwo && other[k]) vb[k] = *reinterpret_cast<const Access *>(src + other[k]);
+        if (other[k]) vb[k] = *reinterpret_cast<const Access *>(src + other[k]);
         ya[k] = t * a.yt + (int64_t)head * a.yh + at;
     }
 
@@ -104,24 +167,15 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
             if constexpr (VEC == 8) {
                 float p[8], q[8];
                 rope::unpack8<T>(va[k], p);
-                if constexpr (HALF) {
-                    rope::unpack8<T>(vb[k], q);
+                rope::unpack8<T>(vb[k], q);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 r = rope::rotate(p[e], q[e], cs[pair[k] + e]);
-                        p[e] = r.x;
-                        q[e] = r.y;
-                    }
-                    vb[k] = rope::pack8<T>(q);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 r = rope::rotate(p[2 * e], p[2 * e + 1], cs[pair[k] + e]);
-                        p[2 * e] = r.x;
-                        p[2 * e + 1] = r.y;
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const float2 r = rope::rotate(p[e], q[e], cs[pair[k] + e]);
+                    p[e] = r.x;
+                    q[e] = r.y;
                 }
                 va[k] = rope::pack8<T>(p);
+                vb[k] = rope::pack8<T>(q);
             } else {
                 const float2 r = rope::rotate(rope::Pair<T>::one(va[k]), rope::Pair<T>::one(vb[k]), cs[pair[k]]);
                 va[k] = rope::Pair<T>::round(r.x);
@@ -129,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
             }
         }
         *reinterpret_cast<Access *>(dst) = va[k];
-        if (kTwo && other[k]) *reinterpret_cast<Access *>(dst + other[k]) = vb[k];
+        if (other[k]) *reinterpret_cast<Access *>(dst + other[k]) = vb[k];
     }
 }
 
@@ -156,10 +210,18 @@ cudaError_t launch(const RopeArgs &a, dim3 grid, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_type(const RopeArgs &a, int vec, bool half, dim3 grid, cudaStream_t st)
+template <typename T, bool HALF>
+cudaError_t launch_rows(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    if (vec == 8) return half ? launch<T, 8, true>(a, grid, st) : launch<T, 8, false>(a, grid, st);
+    sfm_rope_rows_kernel<T, HALF><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const RopeArgs &a, int vec, bool half, bool rows, dim3 grid, cudaStream_t st)
+{
+    if (rows) return half ? launch_rows<T, true>(a, grid, st) : launch_rows<T, false>(a, grid, st);
+    if (vec == 8) return launch<T, 8, true>(a, grid, st);
     return half ? launch<T, 1, true>(a, grid, st) : launch<T, 1, false>(a, grid, st);
 }
 
@@ -253,10 +315,17 @@ extern "C" int sfm_rope(const sfm_rope_params *pp, const void *x, const int32_t 
     a.inverse = p.inverse;
     a.in_place = in_place;
     a.amplitude = p.amplitude;
-    const int pair_units = half || vec == 1 ? p.rope_dim / 2 / vec : p.rope_dim / vec;
-    a.units = pair_units + (in_place ? 0 : (p.head_dim - p.rope_dim) / vec);
+    const bool rows = vec == 8 && (!half || !in_place);
+    a.units = (rows ? p.rope_dim / vec : p.rope_dim / 2 / vec) + (in_place ? 0 : (p.head_dim - p.rope_dim) / vec);
     const int64_t token_units = (int64_t)a.units * p.heads;
-    const int64_t chunks = (token_units + kBlockUnits - 1) / kBlockUnits;
+    int dev = 0, sms = 0;
+    if (current_sms(&dev, &sms) != cudaSuccess) return SFM_ERR_CUDA;
+    // rows: a block takes up to eight steps of a token while the tokens alone
+    // give every SM its blocks
+    int64_t steps = 1;
+    while (rows && steps < 8 && p.tokens * token_units / (2 * steps * kBlockUnits) >= 16 * (int64_t)sms) steps *= 2;
+    a.block_units = (int32_t)(steps * kBlockUnits);
+    const int64_t chunks = (token_units + a.block_units - 1) / a.block_units;
     if (chunks > 65535) return SFM_ERR_UNSUPPORTED;
     a.token_units = (int32_t)token_units;
     int64_t bt = kBlockUnits / token_units;
@@ -266,7 +335,7 @@ extern "C" int sfm_rope(const sfm_rope_params *pp, const void *x, const int32_t 
     a.token_div = make_fastdiv((uint32_t)token_units);
     const dim3 grid((unsigned)((p.tokens + (int64_t)a.block_tokens - 1) / a.block_tokens), (unsigned)chunks);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = p.dtype == SFM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, vec, half, grid, st)
-                                                    : launch_type<__half>(a, vec, half, grid, st);
+    const cudaError_t e = p.dtype == SFM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, vec, half, rows, grid, st)
+                                                    : launch_type<__half>(a, vec, half, rows, grid, st);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
