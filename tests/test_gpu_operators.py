@@ -540,6 +540,31 @@ def test_topk_long_and_many_rows(rows, n, k):
     assert torch.equal(got[:, :min(k, n)], order) and bool((got[:, n:] == -1).all())
 
 
+@pytest.mark.parametrize("rows,n,k", [(5, 8192, 512), (300, 8191, 1000), (2, 70001, 64), (1, 200003, 2048), (3, 20000, 8)])
+def test_topk_rows_that_mislead_a_sample(rows, n, k):
+    """Orders and repetitions in which no part of a row is like the whole."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    r = torch.randn(rows, n, generator=g, device="cuda")
+    j = torch.arange(n, device="cuda").expand(rows, n)
+    cases = [r.sort(1).values, r.sort(1, descending=True).values, torch.where((j // 4) % 32 == 0, r, r - 10),
+             torch.where((j // 4) % 32 == 0, r - 10, r), torch.where(j > n - 2 * k, r + 10, r),
+             torch.where(j % 1000 == 0, math.inf, r), torch.where(j < n // 2, math.nan, r), torch.zeros_like(r),
+             (r > 1).float(), torch.where(j < k + 1, r, -math.inf), torch.where(j < k - 1, r, -math.inf), -r.abs() * 1e38]
+    lengths = torch.full((rows,), n, dtype=torch.int32, device="cuda")
+    lengths[0] = n - n // 3
+    for x in cases:
+        for kw in (dict(), dict(lengths=lengths), dict(lengths=lengths, first_blocks=3, last_blocks=5)):
+            got = sfm.select_topk(x, k, **kw)
+            y = x.double().nan_to_num(nan=-math.inf, posinf=1e300, neginf=-math.inf)
+            ends = lengths[:, None] if "lengths" in kw else n
+            y = torch.where(j < ends, y, -math.inf)
+            if "first_blocks" in kw:
+                y = torch.where((j < ends) & ((j < 3) | (j >= ends - 5)), math.inf, y)
+            best = torch.sort(y, dim=1, descending=True, stable=True)
+            want = torch.where(best.values[:, :k] > -math.inf, best.indices[:, :k], n).sort(1).values
+            assert torch.equal(got, torch.where(want < n, want, -1).to(torch.int32))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
