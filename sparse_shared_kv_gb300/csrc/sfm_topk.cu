@@ -28,11 +28,11 @@ namespace cg = cooperative_groups;
 namespace sfm {
 namespace {
 
-constexpr int kBins = 4096;
-constexpr int kList = kBins;                   // the list takes the histogram's place
+constexpr int kBins = 4096;                    // of a cluster's histogram
 constexpr int kMaxCluster = 16;
 constexpr int kMaxSlice = 40448;               // keys of a CTA: 158 KB and 10 KB of bits
 constexpr uint32_t kForced = 0xffffffffu;
+constexpr uint32_t kLeast = 0x00800000u;       // the least key of a score: below it there is none
 
 struct TopkArgs {
     const float *scores;
@@ -45,8 +45,9 @@ struct TopkArgs {
     int32_t aligned;                           // rows start on 16-byte boundaries
 };
 
+template <int BINS>
 struct Shared {
-    uint32_t hist[kBins];
+    uint32_t hist[BINS];                       // then the list's place, in one CTA
     uint32_t search[256];                      // bins of the list's search
     uint32_t few[32];
     uint32_t warp_above[32], warp_equal[32];
@@ -63,19 +64,21 @@ __device__ __forceinline__ int key_slot(int i) { return quad_at(i >> 2) << 2 | (
 // Behind the keys and their bits, in the CTAs of a cluster only.
 struct ClusterShared {
     uint32_t total[kBins];                     // the cluster's histogram
-    uint32_t list[kList];
+    uint32_t list[kBins];
     uint32_t above[kMaxCluster], equal[kMaxCluster];   // selected keys per CTA
     uint32_t list_n, list_base;
 };
 
 constexpr int kMaxDynamic = kMaxSlice * 4 + kMaxSlice / 4 + (int)sizeof(ClusterShared);
-static_assert(kMaxDynamic + sizeof(Shared) <= 232448, "shared memory budget");
+static_assert(kMaxDynamic + sizeof(Shared<kBins>) <= 232448, "shared memory budget");
 
+// x's key.  NaN and -inf get one of eight keys below kLeast by lane, so that
+// rows of little else do not meet in one bin of the histogram.
 __device__ __forceinline__ uint32_t key_of(float x)
 {
     const uint32_t b = __float_as_uint(x + 0.f);          // -0 becomes 0
     const uint32_t key = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return x > -INFINITY ? key : 0u;                      // NaN and -inf: no score
+    return x > -INFINITY ? key : (threadIdx.x & 7u) << 20;
 }
 
 // the key of block j of a row: scores [j << l, min((j + 1) << l, len))
@@ -93,12 +96,12 @@ __device__ __forceinline__ uint32_t block_key(const float *row, int j, int l, in
 // it.  With fewer than `need` keys in all nothing is found (found[2] = 0).
 // Warp w sums the w-th share of the bins from the top, four neighbouring bins
 // per lane and step; the warp that holds the key looks closer.
-template <int NT>
+template <int NT, int BINS>
 __device__ __forceinline__ void find_bin(const uint32_t *bins, uint32_t need, uint32_t *warp_sums, uint32_t *found)
 {
-    constexpr int NW = NT / 32, kSteps = kBins / NW / 128;
+    constexpr int NW = NT / 32, kSteps = BINS / NW / 128;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int top = kBins / 4 - 1 - warp * (kBins / NW / 4) - lane;     // this lane's quad of the first step
+    const int top = BINS / 4 - 1 - warp * (BINS / NW / 4) - lane;     // this lane's quad of the first step
     uint32_t sums[kSteps], mine = 0;
 #pragma unroll
     for (int q = 0; q < kSteps; ++q) {
@@ -147,8 +150,8 @@ __device__ __forceinline__ void find_bin(const uint32_t *bins, uint32_t need, ui
 // `open`: selected are keys > sh.threshold and the first sh.take_equal equal to
 // it.  All threads of the CTA call it.  Eight bits at a time; the last 32
 // candidates are ranked in one warp.
-template <int NT>
-__device__ __forceinline__ void search_list(Shared &sh, const uint32_t *list, uint32_t n, int open, uint32_t prefix,
+template <int NT, int BINS>
+__device__ __forceinline__ void search_list(Shared<BINS> &sh, const uint32_t *list, uint32_t n, int open, uint32_t prefix,
                                             uint32_t want)
 {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -264,11 +267,14 @@ __device__ __forceinline__ void pool_chunk(const float4 *src, int lane, Store st
     }
 }
 
+// CTAs of 256 threads work on many short rows: fewer bins and registers, so that five of them share an SM (2048 rows of
+// 8192: 50 -> 42 us, 2048 rows of 256 blocks: 39 -> 34 us).
 template <int NT, bool CACHED>
-__global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
+__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const TopkArgs a)
 {
     constexpr int NW = NT / 32;
-    __shared__ Shared sh;
+    constexpr int kTop = NT == 256 ? 11 : 12, kMine = 1 << kTop;       // bits of the first digit, bins
+    __shared__ Shared<kMine> sh;
     extern __shared__ __align__(16) uint32_t keys[];
     uint32_t *bits = keys + a.slice_cap;          // a word per 16 keys: above the digit, and (upper half) in it
     ClusterShared &cs = *reinterpret_cast<ClusterShared *>(bits + a.slice_cap / 16);
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
     auto clear = [&](uint32_t *words, int n) {
         for (int i = tid; i < n / 4; i += NT) reinterpret_cast<uint4 *>(words)[i] = make_uint4(0, 0, 0, 0);
     };
-    clear(sh.hist, kBins);
+    clear(sh.hist, kMine);
     if (C > 1) {
         clear(cs.total, kBins);
         if (tid == 0) cs.list_n = 0;
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
         return forced(base + i) ? kForced : block_key(row, base + i, l, len);
     };
     auto count = [&](uint32_t key) {
-        if (key) atomicAdd(&sh.hist[key >> 20], 1u);
+        atomicAdd(&sh.hist[key >> (32 - kTop)], 1u);
     };
 
     // ---- keys, and the histogram of their top 12 bits ------------------------------
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
 
     // ---- the k-th largest key -------------------------------------------------
     // selected: key > threshold, and the first take_equal keys equal to it
-    uint32_t prefix = 0, need = (uint32_t)a.k, threshold = 0, take_equal = 0;
+    uint32_t prefix = 0, need = (uint32_t)a.k, threshold = kLeast - 1, take_equal = 0;
     bool listed = false;
     // each warp's part of the slice, in order: 16 neighbouring keys per lane and step
     const int seg = ((cnt + NW - 1) / NW + 511) & ~511;
@@ -442,9 +448,9 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
     };
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
+        const int shift = pass == 0 ? 32 - kTop : pass == 1 ? 10 : 0, bits_n = pass == 0 ? kTop : pass == 1 ? 22 - kTop : 10;
         if (pass > 0) {                           // too many keys share the digits so far: count the next ones
-            clear(sh.hist, kBins);
+            clear(sh.hist, kMine);
             if (C > 1) {
                 clear(cs.total, kBins);
                 cluster.sync();
@@ -453,23 +459,25 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
             }
             for (int i = tid; i < cnt; i += NT) {
                 const uint32_t key = key_at(i);
-                if (key != 0 && (key >> (shift + 10)) == prefix) atomicAdd(&sh.hist[(key >> shift) & 1023u], 1u);
+                if ((key >> (shift + bits_n)) == prefix) atomicAdd(&sh.hist[(key >> shift) & ((1u << bits_n) - 1)], 1u);
             }
             __syncthreads();
         }
         if (C > 1) {
-            for (int b = tid; b < kBins; b += NT) {
+            for (int b = tid; b < kMine; b += NT) {
                 const uint32_t s = sh.hist[b];
                 if (s)
                     for (int q = 0; q < C; ++q) atomicAdd(cluster.map_shared_rank(&cs.total[b], q), s);
             }
             cluster.sync();
         }
-        find_bin<NT>(C > 1 ? cs.total : sh.hist, need, sh.warp_above, sh.found);
+        if (C > 1) find_bin<NT, kBins>(cs.total, need, sh.warp_above, sh.found);
+        else find_bin<NT, kMine>(sh.hist, need, sh.warp_above, sh.found);
         const uint32_t in_bin = sh.found[2];
-        if (in_bin == 0) break;                   // first pass: fewer scores than k, all are taken
+        // first pass: fewer scores than k (or the k-th would be none), all are taken
+        if (in_bin == 0 || (pass == 0 && sh.found[0] < kLeast >> shift)) break;
         need -= sh.found[1];
-        prefix = pass == 0 ? sh.found[0] : prefix << 10 | sh.found[0];
+        prefix = prefix << bits_n | sh.found[0];
         if (in_bin == need) {                     // the whole bin is taken
             threshold = (prefix << shift) - 1;
             break;
@@ -479,14 +487,14 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
             take_equal = need;
             break;
         }
-        if (in_bin > (uint32_t)kList) continue;
+        if (in_bin > (uint32_t)kMine) continue;
 
         // ---- the list of the keys in the bin, in the cluster's first CTA ----
         uint32_t *to = sh.hist;                   // one CTA: the list takes the histogram's place
         if (tid == 0) {
             sh.list_n = 0;
             if (C > 1)                            // where this CTA's keys go: one remote addition
-                cs.list_base = atomicAdd(cluster.map_shared_rank(&cs.list_n, 0), sh.hist[prefix & (pass ? 1023u : kBins - 1)]);
+                cs.list_base = atomicAdd(cluster.map_shared_rank(&cs.list_n, 0), sh.hist[prefix & ((1u << bits_n) - 1)]);
         }
         __syncthreads();
         if (C > 1) to = cluster.map_shared_rank(cs.list, 0) + cs.list_base;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(NT) sfm_topk_kernel(const TopkArgs a)
         }
         if (C > 1) cluster.sync(); else __syncthreads();
         if (rank == 0) {
-            search_list<NT>(sh, C > 1 ? cs.list : sh.hist, in_bin, shift, prefix, need);
+            search_list<NT, kMine>(sh, C > 1 ? cs.list : sh.hist, in_bin, shift, prefix, need);
             if (tid > 0 && tid < C) {
                 *cluster.map_shared_rank(&sh.threshold, tid) = sh.threshold;
                 *cluster.map_shared_rank(&sh.take_equal, tid) = sh.take_equal;
