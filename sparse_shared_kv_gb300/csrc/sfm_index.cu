@@ -260,17 +260,20 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     const uint32_t bars = misc;
     auto q_full = [&](int i) { return bars + 8u * i; };
     auto q_empty = [&](int i) { return bars + 16u + 8u * i; };
+    // One barrier per stage and turn of the products' two warps: a barrier's phases are waited for by one thread, in
+    // order (2 x stages of them; with one per stage and an odd number of stages, a thread could ask for a phase while
+    // the one before, the other thread's, was not complete, and take the answer of the phase before that)
     auto k_full = [&](int i) { return bars + 32u + 8u * i; };
-    auto k_empty = [&](int i) { return bars + 96u + 8u * i; };
-    auto acc_full = [&](int i) { return bars + 160u + 8u * i; };   // the product, and the keys' mask and scales
-    auto acc_empty = [&](int i) { return bars + 224u + 8u * i; };
-    auto half_full = [&](int w) { return bars + 288u + 8u * w; };  // HP 128: a part's sums are in shared memory
-    auto w_full = [&](int i) { return bars + 320u + 8u * i; };     // a unit's weights are there
-    const uint32_t teardown = bars + 336u;                         // two
+    auto k_empty = [&](int i) { return bars + 160u + 8u * i; };
+    auto acc_full = [&](int i) { return bars + 224u + 8u * i; };   // the product, and the keys' mask and scales
+    auto acc_empty = [&](int i) { return bars + 288u + 8u * i; };
+    auto half_full = [&](int w) { return bars + 352u + 8u * w; };  // HP 128: a part's sums are in shared memory
+    auto w_full = [&](int i) { return bars + 384u + 8u * i; };     // a unit's weights are there
+    const uint32_t teardown = bars + 400u;                         // two
     uint8_t *gmisc = gbase + (misc - base);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 352);
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 356);
-    volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 360);     // [kMaxAcc] a bit per four keys
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 416);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 420);
+    volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 424);     // [kMaxAcc] a bit per four keys
     float *weights = reinterpret_cast<float *>(gmisc + 512);                            // [2][256]: by column
     float *half_sum = weights + 512;                                                    // HP 128 only: [2 pairs][128]
     float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes - (HP == 128 ? 0 : 1024));   // [kMaxAcc][kTile]
@@ -279,7 +282,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < 2; ++i) mbar_init(q_full(i), 1), mbar_init(q_empty(i), 2);
-        for (int i = 0; i < a.stages; ++i) mbar_init(k_full(i), 1), mbar_init(k_empty(i), 1);
+        for (int i = 0; i < 2 * a.stages; ++i) mbar_init(k_full(i), 1);
+        for (int i = 0; i < a.stages; ++i) mbar_init(k_empty(i), 1);
         for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 34), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
         for (int i = 0; i < 2; ++i) mbar_init(w_full(i), kEpiWarps);
@@ -303,7 +307,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     bool bad = false;
     if (warp == 16) {
         // ---------------- loads ----------------
-        int stage = 0, ks = 0, kphase = 0, n = 0;             // ks: stages filled so far (capped); n: units with tiles
+        int stage = 0, kphase = 0, n = 0;                     // the next stage and its phase; units with tiles
+        int kb = 0, fphase = 0, fills = 0;                    // the next fill's barrier and its phase; fills so far
         bool ok = true;
         Units units;
         Unit u = {};
@@ -330,24 +335,32 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 ok = wait_warp(k_empty(stage), kphase ^ 1, abort_flag);
                 if (!ok) break;
-                if (lane == 0) mbar_expect(k_full(stage), boxes * a.run * kDim * elem);
+                if (lane == 0) mbar_expect(k_full(kb), boxes * a.run * kDim * elem);
                 __syncwarp();
                 if (row >= 0) {
                     const uint32_t dst = k_smem + stage * k_bytes + lane * a.run * 128;
-                    tma_load(dst, &k_map, 0, row, k_full(stage));
-                    if (!a.fp8) tma_load(dst + kTile * 128, &k_map, 64, row, k_full(stage));
+                    tma_load(dst, &k_map, 0, row, k_full(kb));
+                    if (!a.fp8) tma_load(dst + kTile * 128, &k_map, 64, row, k_full(kb));
                 }
-                if (ks < a.stages) ++ks;
+                ++fills;
                 if (++stage == a.stages) stage = 0, kphase ^= 1;
+                if (++kb == 2 * a.stages) kb = 0, fphase ^= 1;
             }
         }
+        // The products' last arrivals on the stages and query buffers are asynchronous: they land before the CTA ends
+        // (its shared memory may be another's a moment later).  Arrivals on acc_full are waited for by the sums.
+        for (int i = 0; ok && i < a.stages; ++i) {
+            ok = wait_warp(k_empty(stage), kphase ^ 1, abort_flag);
+            if (ok && ++stage == a.stages) stage = 0, kphase ^= 1;
+        }
+        for (int i = 0; ok && i < 2; ++i) ok = wait_warp(q_empty((n + i) & 1), (((n + i) >> 1) & 1) ^ 1, abort_flag);
         if (!ok) {
-            // given up: the copies in flight must land before the CTA ends.  Every
-            // stage and query buffer that was filled is waited for, either phase.
+            // given up: the copies in flight, at most the last `stages` fills and two query loads, must land before
+            // the CTA ends
             const uint64_t t0 = globaltimer_ns();
-            for (int s = 0; s < ks; ++s) {
-                const int filled = s < stage ? kphase : kphase ^ 1;
-                while (!mbar_try_wait(k_full(s), filled) && globaltimer_ns() - t0 < kTimeoutNs) {
+            for (int i = 0; i < a.stages && i < fills; ++i) {
+                if (--kb < 0) kb = 2 * a.stages - 1, fphase ^= 1;
+                while (!mbar_try_wait(k_full(kb), fphase) && globaltimer_ns() - t0 < kTimeoutNs) {
                 }
             }
             for (int q = 0; q < 2 && q < n; ++q) {
@@ -359,9 +372,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     } else if (warp == 17 || warp == 19) {
         // ---------------- products: one thread each, even and odd tiles of the CTA ----------------
         if (lane == 0) {
-            const int odd = warp == 19;
+            const int odd = warp == 19;     // (and so are its accumulator tiles and k_full barriers: both rings are even)
             int64_t g = 0;
-            int stage = 0, kphase = 0, acc = 0, aphase = 0, n = 0;
+            int stage = 0, kb = 0, fphase = 0, acc = 0, aphase = 0, n = 0;
             bool ok = true;
             for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
                 const Unit u = unit_of(a, unit, queries, &bad);
@@ -372,7 +385,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 const uint64_t bdesc = sdesc_sw128(q_smem + qb * q_bytes, 16, 1024);
                 for (int t = 0; t < u.tiles && ok; ++t, ++g) {
                     if ((int)(g & 1) == odd) {
-                        ok = mbar_wait(k_full(stage), kphase, abort_flag) && mbar_wait(acc_empty(acc), aphase ^ 1, abort_flag);
+                        ok = mbar_wait(k_full(kb), fphase, abort_flag) && mbar_wait(acc_empty(acc), aphase ^ 1, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t adesc = sdesc_sw128(k_smem + stage * k_bytes, 16, 1024);
@@ -389,7 +402,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                         umma_commit(k_empty(stage));
                         umma_commit(acc_full(acc));
                     }
-                    if (++stage == a.stages) stage = 0, kphase ^= 1;
+                    if (++stage == a.stages) stage = 0;
+                    if (++kb == 2 * a.stages) kb = 0, fphase ^= 1;
                     if (++acc == accs) acc = 0, aphase ^= 1;
                 }
                 umma_commit(q_empty(qb));                     // this thread's products of the unit
