@@ -473,8 +473,9 @@ typedef struct sfm_index_tensors {
  * Products are exact, sums are in fp32.  A key whose block id is outside the
  * cache scores -inf and sets SFM_STATUS_BAD_BLOCK (as does one behind the
  * cache's last row, with up to three neighbours).  Rows of q at or beyond
- * seqused_q score -inf everywhere; rows behind the last sequence (TND) are
- * left as they were.
+ * seqused_q score -inf everywhere; rows behind the last sequence (TND), and
+ * those of a sequence beyond max_seqlen_q (SFM_STATUS_BAD_LENGTH), are left as
+ * they were.
  * scores: device fp32, score_stride (>= max_seqlen_kv) elements apart.
  * visible: device int32 (tokens) or NULL: visible(t). */
 int sfm_index_scores(const sfm_index_params *params, const sfm_index_tensors *tensors, float *scores,

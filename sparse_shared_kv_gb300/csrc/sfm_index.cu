@@ -620,8 +620,7 @@ cudaError_t launch(const IndexArgs &a, const CUtensorMap &q, const CUtensorMap &
             return cudaFuncSetAttribute(sfm_index_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
         },
         [&] {
-            sfm_index_kernel<HP><<<grid, kThreads, smem, st>>>(a, q, k);
-            return cudaGetLastError();
+            return launch_plain(sfm_index_kernel<HP>, dim3((unsigned)grid), dim3(kThreads), smem, st, a, q, k);
         });
 }
 

@@ -363,6 +363,19 @@ inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 blo
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// An ordinary launch that reports its own error alone (the runtime's last error
+// may be another call's).
+template <typename... Args>
+inline cudaError_t launch_plain(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ----------------------------------------------------------------------------
 // what a launch asks the runtime for, remembered per device (each question
 // costs a good part of a launch)

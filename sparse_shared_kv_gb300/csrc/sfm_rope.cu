@@ -42,7 +42,7 @@ struct RopeArgs {
 // enough for every SM, so that a long row works its cosines out a few times
 // only.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(RopeArgs a)
 {
     __shared__ __align__(16) float2 cs[kMaxPairs];
     const int tid = threadIdx.x, half = a.rot / 2;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(const RopeAr
 // first and second members of VEC pairs, or one access outside the rotated
 // part, which is copied.
 template <typename T, int VEC, bool HALF>
-__global__ void __launch_bounds__(kThreads) sfm_rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kThreads) sfm_rope_kernel(RopeArgs a)
 {
     using Access = typename std::conditional<VEC == 8, uint4, T>::type;
     __shared__ float2 cs[kMaxPairs];
@@ -206,15 +206,13 @@ bool rows_overlap(int64_t tokens, int64_t token_stride, int64_t heads, int64_t h
 template <typename T, int VEC, bool HALF>
 cudaError_t launch(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    sfm_rope_kernel<T, VEC, HALF><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_plain(sfm_rope_kernel<T, VEC, HALF>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <typename T, bool HALF>
 cudaError_t launch_rows(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    sfm_rope_rows_kernel<T, HALF><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_plain(sfm_rope_rows_kernel<T, HALF>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <typename T>

@@ -72,7 +72,7 @@ __device__ __forceinline__ float fast_inverse(float x)      // one unit in the l
 // LANES lanes per row, STEPS 16-byte accesses per lane; FORMAT: enum sfm_kv_format;
 // ROPE: 0 none, 1 interleaved, 2 half with the rotated part inside one step, 3 half
 template <typename T, int FORMAT, int LANES, int STEPS, int ROPE>
-__global__ void __launch_bounds__(kThreads) sfm_store_kernel(const StoreArgs a)
+__global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
 {
     constexpr int kGroups = kThreads / LANES;
     constexpr int kPairs = ROPE == 0 ? 1 : LANES * STEPS * 4 < kMaxDim / 2 ? LANES * STEPS * 4 : kMaxDim / 2;
@@ -295,13 +295,11 @@ cudaError_t launch(const StoreArgs &a, cudaStream_t st)
     const int width = LANES * 8;
     const int form = !a.rot ? 0 : !a.half ? 1 : a.off / width == (a.off + a.rot - 1) / width ? 2 : 3;
     const size_t smem = form == 3 ? (size_t)kGroups * a.rot * sizeof(float) : 0;
-    switch (form) {
-    case 0: sfm_store_kernel<T, FORMAT, LANES, STEPS, 0><<<grid, kThreads, smem, st>>>(a); break;
-    case 1: sfm_store_kernel<T, FORMAT, LANES, STEPS, 1><<<grid, kThreads, smem, st>>>(a); break;
-    case 2: sfm_store_kernel<T, FORMAT, LANES, STEPS, 2><<<grid, kThreads, smem, st>>>(a); break;
-    default: sfm_store_kernel<T, FORMAT, LANES, STEPS, 3><<<grid, kThreads, smem, st>>>(a); break;
-    }
-    return cudaGetLastError();
+    void (*kernel)(StoreArgs) = form == 0   ? sfm_store_kernel<T, FORMAT, LANES, STEPS, 0>
+                                : form == 1 ? sfm_store_kernel<T, FORMAT, LANES, STEPS, 1>
+                                : form == 2 ? sfm_store_kernel<T, FORMAT, LANES, STEPS, 2>
+                                            : sfm_store_kernel<T, FORMAT, LANES, STEPS, 3>;
+    return launch_plain(kernel, dim3(grid), dim3(kThreads), smem, st, a);
 }
 
 template <typename T>

@@ -566,6 +566,44 @@ def test_topk_rows_that_mislead_a_sample(rows, n, k):
 
 
 # ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+def test_far_offsets():
+    """Rows whose elements lie more than 2^32 bytes (and 2^31 elements) from the start of their tensors."""
+    g = gen(11)
+    far = torch.empty((1 << 31) + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    x = far.as_strided((2, 3, 128), ((1 << 31), 128, 1))
+    x.copy_(randn(g, 2, 3, 128, dtype=torch.bfloat16))
+    pos = torch.tensor([5, 70000], dtype=torch.int32)
+    f, _ = sfm.rope_frequencies(64, device="cuda")
+    for inter in (True, False):
+        y = sfm.apply_rope(x, pos.cuda(), f, interleaved=inter)
+        rope_check(y, x, pos, f, 0, inter, False, 1.0)
+    rows = (1 << 32) // 1024 + 100
+    cache = far[:rows * 512].view(rows, 512)
+    values = randn(g, 2, 512, dtype=torch.bfloat16).cuda()
+    slots = torch.tensor([rows - 1, 3], dtype=torch.int32).cuda()
+    sfm.store_kv(values, cache, slot_mapping=slots)
+    assert torch.equal(cache[rows - 1], values[0]) and torch.equal(cache[3], values[1])
+    # index keys at the end of a pool of more than 2^32 bytes, scores in rows 2^31 elements apart
+    blocks = (1 << 32) // (256 * 64) + 8
+    pool = far[:blocks * 64 * 128].view(blocks, 64, 128)
+    k, q, w = randn(g, 100, 128, dtype=torch.bfloat16), randn(g, 2, 16, 128, dtype=torch.bfloat16), randn(g, 2, 16)
+    pool[blocks - 1] = k[:64].cuda()
+    pool[blocks - 2, :36] = k[64:].cuda()
+    wide = torch.empty((1 << 31) + 256, device="cuda")
+    out = wide.as_strided((2, 100), (1 << 31, 1))
+    sfm.index_scores(q.cuda().view(1, 2, 16, 128), pool, w.cuda().view(1, 2, 16), max_seqlen_kv=100, layout_kv="PAGED", mask_mode=0,
+                     block_table=torch.tensor([[blocks - 1, blocks - 2]], dtype=torch.int32).cuda(),
+                     seqused_kv=torch.tensor([100], dtype=torch.int32).cuda(), out=out)
+    want, mag = P.scores(q, k, w)
+    assert_within(out, want, SCORE_TOL * mag)
+    host = out.cpu().tolist()
+    got = sfm.select_topk(out, 10).tolist()
+    assert got == [P.topk(host[r], 10, 100) for r in range(2)]
+
+
+# ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
 def _slots(table, block, b, n):
