@@ -10,8 +10,14 @@
 // must not count spoils nothing but its own lane, and scores of neighbouring
 // keys are stored side by side.
 //
-// One persistent CTA per SM walks work units; a unit is up to `chunk` tiles of
-// keys for one group of queries of one sequence.
+// One persistent CTA per SM walks work units; a unit is a run of key tiles for
+// one group of queries of one sequence, and the columns behind the group's last
+// visible key, which only have to be set to -inf (16 tiles of them count as
+// one).  With up to 1024 groups each CTA takes an equal share of all groups'
+// work, counted from the lengths on the device when it starts: a decode batch
+// whose sequences differ by a factor of two would keep the CTA with the most
+// work busy for 1.6 times the mean otherwise.  More groups are dealt out in
+// chunks.
 //   warp 16       loads: the unit's queries (two buffers) and its key tiles
 //                 (a ring of stages) by TMA into 128-byte-swizzled operands,
 //                 one box per run of keys that lies inside a page;
@@ -59,7 +65,8 @@ struct IndexArgs {
     const int32_t *table, *cu_q, *cu_k, *used_q, *used_k, *residual;
     int64_t stride, k_rows;
     int32_t heads, batch, max_q, total_q, max_k, ratio, causal, layout_q, layout_kv, block, table_stride;
-    int32_t groups_per_seq, groups, chunk, units;   // tiles per unit; units in all
+    int32_t groups_per_seq, groups, chunk, units;   // chunk: work of a unit (0: equal shares); units in all, then
+    int32_t all_tiles;                         // tiles of max_k keys
     int32_t run, boxes_log2;                   // keys per TMA box, boxes per tile
     int32_t parts_log2;                        // 64-column parts of a tile: 1, 2 or 4
     int32_t stages;
@@ -68,11 +75,19 @@ struct IndexArgs {
     int32_t fp8;
 };
 
+constexpr int kShareGroups = 1024;             // groups up to which CTAs take equal shares
+constexpr int kFillTiles = 16;                 // tiles of -inf that count as one tile of products
+
 struct Unit {
+    // the group
     int32_t b, t0, nq, rows;                   // sequence, first token, live queries, query rows to write
-    int32_t i0, q_len, len, tiles, first_tile; // position of the first query, lengths, tiles with visible keys
-    int64_t p0;                                // visible(i) = floor((p0 + i) / ratio) for query i of the unit
+    int32_t len, seen, work;                   // keys, tiles with visible keys, work in all
+    int64_t p0;                                // visible(i) = floor((p0 + i) / ratio) for query i of the group
     int64_t k_base;                            // first key row (contiguous layouts)
+    // the unit
+    int32_t first_tile, tiles;                 // its tiles
+    int32_t fill0, fill1;                      // and its columns without a product
+    bool begins;                               // it holds the group's first work
 };
 
 __device__ __forceinline__ int32_t clamp_to(int64_t v, int64_t lo, int64_t hi, bool *bad)
@@ -94,12 +109,12 @@ __device__ __forceinline__ int32_t visible_of(const IndexArgs &a, const Unit &u,
     return (int32_t)(v < u.len ? v : u.len);
 }
 
-__device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int queries, bool *bad)
+// Group g, without a unit of it.
+__device__ __forceinline__ Unit group_of(const IndexArgs &a, int g, int queries, bool *bad)
 {
-    Unit u;
-    const int c = (int)fdiv((uint32_t)unit, a.groups_div), g = unit - c * a.groups;
+    Unit u = {};
     u.b = (int)fdiv((uint32_t)g, a.seq_div);
-    u.i0 = (g - u.b * a.groups_per_seq) * queries;
+    const int i0 = (g - u.b * a.groups_per_seq) * queries;
     int q_cap, t_base;
     if (a.layout_q == SFM_LAYOUT_BSND) {
         t_base = u.b * a.max_q;
@@ -109,10 +124,10 @@ __device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int querie
         const int end = clamp_to(__ldg(a.cu_q + u.b + 1), t_base, a.total_q, bad);
         q_cap = clamp_to(end - t_base, 0, a.max_q, bad);
     }
-    u.q_len = a.used_q ? clamp_to(__ldg(a.used_q + u.b), 0, q_cap, bad) : q_cap;
-    u.t0 = t_base + u.i0;
-    u.rows = min(max(q_cap - u.i0, 0), queries);
-    u.nq = min(max(u.q_len - u.i0, 0), queries);
+    const int q_len = a.used_q ? clamp_to(__ldg(a.used_q + u.b), 0, q_cap, bad) : q_cap;
+    u.t0 = t_base + i0;
+    u.rows = min(max(q_cap - i0, 0), queries);
+    u.nq = min(max(q_len - i0, 0), queries);
 
     int cap = a.max_k;
     u.k_base = 0;
@@ -126,43 +141,121 @@ __device__ __forceinline__ Unit unit_of(const IndexArgs &a, int unit, int querie
     }
     u.len = a.used_k ? clamp_to(__ldg(a.used_k + u.b), 0, cap, bad) : cap;
     const int64_t rest = a.residual ? (int64_t)__ldg(a.residual + u.b) : 0;
-    u.p0 = (int64_t)u.len * a.ratio + rest - u.q_len + u.i0 + 1;
-    u.first_tile = c * a.chunk;
+    u.p0 = (int64_t)u.len * a.ratio + rest - q_len + i0 + 1;
     const int most = u.nq > 0 ? visible_of(a, u, u.nq - 1) : 0;
-    u.tiles = min(max((most + kTile - 1) / kTile - u.first_tile, 0), a.chunk);
+    u.seen = (most + kTile - 1) / kTile;
+    u.work = u.rows ? u.seen + (a.all_tiles - u.seen + kFillTiles - 1) / kFillTiles : 0;
     return u;
 }
 
-// The units of a CTA, for a warp: each lane works one of the next 32 out, and
-// the warp takes them from there one after the other (working a unit out is a
-// long chain of dependent steps).
+// Work [lo, hi) of the group: its tiles first, then the rest of its columns.
+__device__ __forceinline__ void cut(const IndexArgs &a, Unit &u, int lo, int hi)
+{
+    u.begins = lo == 0;
+    u.first_tile = lo;
+    u.tiles = max(min(hi, u.seen) - lo, 0);
+    u.fill0 = u.fill1 = 0;
+    if (hi > u.seen) {
+        const int64_t from = u.seen + (int64_t)(max(lo, u.seen) - u.seen) * kFillTiles;
+        const int64_t to = u.seen + (int64_t)(hi - u.seen) * kFillTiles;
+        u.fill0 = (int32_t)min(from * kTile, (int64_t)a.max_k);
+        u.fill1 = (int32_t)min(to * kTile, (int64_t)a.max_k);
+    }
+}
+
+// A CTA's share of all groups' work: [from, from + n) counted from the start of group g.
+struct Share {
+    int32_t g, from;
+    int64_t n;
+};
+
+// One warp: every lane sums the work of a run of groups (at most 32), the warp
+// finds the group that the CTA's share starts in.
+__device__ __forceinline__ Share share_of(const IndexArgs &a, int queries, int lane, bool *bad)
+{
+    const int run = (a.groups + 31) / 32, g0 = lane * run, g1 = min(g0 + run, a.groups);
+    int64_t mine = 0;
+    for (int g = g0; g < g1; ++g) mine += group_of(a, g, queries, bad).work;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, upto, 31), per = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t start = per * blockIdx.x;
+    Share s = {0, 0, min(per, all - start)};
+    if (s.n <= 0) return s;
+    const uint32_t holds = __ballot_sync(0xffffffffu, upto - mine <= start && start < upto);
+    const int src = __ffs(holds) - 1;
+    int64_t rest = start - (upto - mine);
+    int g = g0;
+    if (lane == src && run > 1) {
+        for (; g < g1; ++g) {
+            const int w = group_of(a, g, queries, bad).work;
+            if (rest < w) break;
+            rest -= w;
+        }
+    }
+    s.g = __shfl_sync(0xffffffffu, g, src);
+    s.from = __shfl_sync(0xffffffffu, (int32_t)rest, src);
+    return s;
+}
+
+// The units of a CTA.  For a whole warp (WARP) each lane works one of the next
+// 32 groups out, and the warp takes them from there one after the other
+// (working a group out is a long chain of dependent steps).
+template <bool WARP>
 struct Units {
     Unit ahead;
-    int32_t k = 0;                             // units taken so far
+    int32_t k = 0, g, from;                    // groups taken so far; equal shares: the next group, and where to start in it
+    int64_t left;                              // equal shares: work left
 
-    __device__ __forceinline__ bool next(const IndexArgs &a, int queries, int lane, bool *bad, Unit &u)
+    __device__ __forceinline__ explicit Units(const Share &s) : g(s.g), from(s.from), left(s.n) {}
+
+    __device__ __forceinline__ bool next(const IndexArgs &a, int queries, bool *bad, Unit &u)
     {
-        const int64_t unit = blockIdx.x + (int64_t)k * gridDim.x;
-        if (unit >= a.units) return false;
-        if ((k & 31) == 0) {
-            const int64_t mine = unit + (int64_t)lane * gridDim.x;
-            if (mine < a.units) ahead = unit_of(a, (int)mine, queries, bad);
+        const int lane = threadIdx.x & 31;
+        while (true) {
+            int lo, hi;
+            if (a.chunk) {
+                const int64_t unit = blockIdx.x + (int64_t)k * gridDim.x;
+                if (unit >= a.units) return false;
+                const int c = (int)fdiv((uint32_t)unit, a.groups_div);
+                lo = c * a.chunk;
+                hi = lo + a.chunk;
+                const int64_t mine = unit + (WARP ? (int64_t)lane * gridDim.x : 0);
+                if ((!WARP || (k & 31) == 0) && mine < a.units)
+                    ahead = group_of(a, (int)(mine - (int64_t)fdiv((uint32_t)mine, a.groups_div) * a.groups), queries, bad);
+            } else {
+                if (left <= 0 || g >= a.groups) return false;
+                lo = from;
+                const int mine = g + (WARP ? lane : 0);
+                if ((!WARP || (k & 31) == 0) && mine < a.groups) ahead = group_of(a, mine, queries, bad);
+            }
+            const int src = k & 31;
+            auto take = [&](auto v) { return WARP ? __shfl_sync(0xffffffffu, v, src) : v; };
+            u.b = take(ahead.b);
+            u.t0 = take(ahead.t0);
+            u.nq = take(ahead.nq);
+            u.rows = take(ahead.rows);
+            u.len = take(ahead.len);
+            u.seen = take(ahead.seen);
+            u.work = take(ahead.work);
+            u.p0 = take(ahead.p0);
+            u.k_base = take(ahead.k_base);
+            ++k;
+            if (!a.chunk) {
+                hi = (int)min((int64_t)u.work, lo + left);
+                left -= hi - lo;
+                from = 0;
+                ++g;
+            }
+            hi = min(hi, u.work);
+            if (lo >= hi) continue;               // nothing of the group falls to this unit
+            cut(a, u, lo, hi);
+            return true;
         }
-        const int src = k & 31;
-        auto take = [&](auto v) { return __shfl_sync(0xffffffffu, v, src); };
-        u.b = take(ahead.b);
-        u.t0 = take(ahead.t0);
-        u.nq = take(ahead.nq);
-        u.rows = take(ahead.rows);
-        u.i0 = take(ahead.i0);
-        u.q_len = take(ahead.q_len);
-        u.len = take(ahead.len);
-        u.tiles = take(ahead.tiles);
-        u.first_tile = take(ahead.first_tile);
-        u.p0 = take(ahead.p0);
-        u.k_base = take(ahead.k_base);
-        ++k;
-        return true;
     }
 };
 
@@ -274,6 +367,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + 416);
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 420);
     volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 424);     // [kMaxAcc] a bit per four keys
+    Share *share = reinterpret_cast<Share *>(gmisc + 456);
     float *weights = reinterpret_cast<float *>(gmisc + 512);                            // [2][256]: by column
     float *half_sum = weights + 512;                                                    // HP 128 only: [2 pairs][128]
     float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes - (HP == 128 ? 0 : 1024));   // [kMaxAcc][kTile]
@@ -295,24 +389,28 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             *reinterpret_cast<uint4 *>(gbase + i) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
+    bool bad = false;
     if (warp == 17) {
         tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
         tmem_relinquish();
+    } else if (warp == 18 && a.chunk == 0) {
+        const Share mine = share_of(a, queries, lane, &bad);
+        if (lane == 0) *share = mine;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
+    const Share my_share = a.chunk ? Share{} : *share;
 
-    bool bad = false;
     if (warp == 16) {
         // ---------------- loads ----------------
         int stage = 0, kphase = 0, n = 0;                     // the next stage and its phase; units with tiles
         int kb = 0, fphase = 0, fills = 0;                    // the next fill's barrier and its phase; fills so far
         bool ok = true;
-        Units units;
+        Units<true> units(my_share);
         Unit u = {};
-        while (ok && units.next(a, queries, lane, &bad, u)) {
+        while (ok && units.next(a, queries, &bad, u)) {
             if (u.tiles == 0) continue;
             const int qb = n & 1;
             ok = wait_warp(q_empty(qb), ((n >> 1) & 1) ^ 1, abort_flag);
@@ -376,8 +474,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             int64_t g = 0;
             int stage = 0, kb = 0, fphase = 0, acc = 0, aphase = 0, n = 0;
             bool ok = true;
-            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-                const Unit u = unit_of(a, unit, queries, &bad);
+            Units<false> units(my_share);
+            Unit u = {};
+            while (ok && units.next(a, queries, &bad, u)) {
                 if (u.tiles == 0) continue;
                 const int qb = n & 1;
                 ok = mbar_wait(q_full(qb), (n >> 1) & 1, abort_flag);
@@ -421,9 +520,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         // ---------------- masks and scales of the keys ----------------
         int acc = 0, aphase = 0;
         bool ok = true;
-        Units units;
+        Units<true> units(my_share);
         Unit u = {};
-        while (ok && units.next(a, queries, lane, &bad, u)) {
+        while (ok && units.next(a, queries, &bad, u)) {
             if (u.tiles == 0) continue;
             const int most = visible_of(a, u, u.nq - 1);
             int j = u.first_tile * kTile + 4 * lane;          // four neighbouring keys per lane: they share a box
@@ -468,10 +567,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         int halves = 0;                                       // HP 128: exchanges so far
         int n = 0;                                            // units with tiles
         bool ok = true;
-        Units units;
+        Units<true> units(my_share);
         Unit u = {};
-        while (ok && units.next(a, queries, lane, &bad, u)) {
-            if (a.visible && u.first_tile == 0 && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
+        while (ok && units.next(a, queries, &bad, u)) {
+            if (a.visible && u.begins && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
             int vis[kSums];
             float *w = weights + (n & 1) * 256;
             if (u.tiles) {
@@ -558,15 +657,18 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             }
             done += u.tiles;
             if (!ok) break;
-            // columns that no product reached, and rows without a query
-            const int c0 = u.first_tile * kTile, c1 = min(c0 + a.chunk * kTile, a.max_k);
+            // columns that no product reached, and under the products the rows without a query
             for (int i = warp; i < u.rows; i += kEpiWarps) {
                 float *dst = a.scores + (int64_t)(u.t0 + i) * a.stride;
-                for (int j = c0 + (i < u.nq ? u.tiles * kTile : 0) + lane; j < c1; j += 32) dst[j] = -INFINITY;
+                for (int j = u.fill0 + lane; j < u.fill1; j += 32) dst[j] = -INFINITY;
+                if (i >= u.nq) {
+                    const int c0 = u.first_tile * kTile, c1 = min(c0 + u.tiles * kTile, a.max_k);
+                    for (int j = c0 + lane; j < c1; j += 32) dst[j] = -INFINITY;
+                }
             }
         }
-        if (bad && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
     }
+    if (bad && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
 
     tc_fence_before();
     __syncthreads();
@@ -716,22 +818,26 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     const int fit = (int)((kSmemLimit - misc_bytes - 2 * q_bytes) / k_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 
-    // units: some six per CTA, so that sequences of different lengths even out,
-    // but not more than 32 tiles
     a.groups_per_seq = (p.max_seqlen_q + queries - 1) / queries;
     const int64_t groups = (int64_t)a.groups_per_seq * p.batch_size;
     const int64_t tiles = (p.max_seqlen_kv + kTile - 1) / kTile;
     if (groups > INT32_MAX) return SFM_ERR_UNSUPPORTED;
-    int64_t chunk = groups * tiles / (6 * (int64_t)sms);
-    chunk = chunk < 1 ? 1 : chunk > 32 ? 32 : chunk;
-    const int64_t chunks = (tiles + chunk - 1) / chunk;
-    a.chunk = (int32_t)((tiles + chunks - 1) / chunks);
-    const int64_t units = groups * ((tiles + a.chunk - 1) / a.chunk);
-    if (units > INT32_MAX - sms) return SFM_ERR_UNSUPPORTED;
     a.groups = (int32_t)groups;
-    a.units = (int32_t)units;
+    a.all_tiles = (int32_t)tiles;
     a.groups_div = make_fastdiv((uint32_t)groups);
     a.seq_div = make_fastdiv((uint32_t)a.groups_per_seq);
+    int64_t units = groups * tiles;                // at most one CTA per tile
+    if (groups > kShareGroups || units <= sms) {
+        // one tile per CTA where that many CTAs are there (counting shares out would cost them a microsecond), else
+        // units of 8 to 32 tiles, some six per CTA at least
+        int64_t chunk = groups * tiles / (6 * (int64_t)sms);
+        chunk = chunk < 8 ? 8 : chunk > 32 ? 32 : chunk;
+        const int64_t chunks = (tiles + chunk - 1) / chunk;
+        a.chunk = units <= sms ? 1 : (int32_t)((tiles + chunks - 1) / chunks);
+        units = groups * ((tiles + a.chunk - 1) / a.chunk);
+        if (units > INT32_MAX - sms) return SFM_ERR_UNSUPPORTED;
+        a.units = (int32_t)units;
+    }
 
     CUtensorMap q_map, k_map;
     int rc = make_map(&q_map, t->q, p.dtype, tokens * p.num_heads, (int64_t)kDim * elem, p.num_heads);

@@ -404,6 +404,9 @@ INDEX_CASES = [   # dtype, heads, q_lens, key counts, layouts, block, ratio
     ("fp8", 64, [96, 96, 96], [5000, 4100, 7000], "TND", "PAGED", 32, 1), ("bf16", 64, [200], [6001], "BSND", "PAGED", 128, 1),
     ("fp8", 16, [1] * 48, [6000 - 50 * b for b in range(48)], "BSND", "PAGED", 128, 4),
     ("bf16", 128, [1] * 30, [8000 - 99 * b for b in range(30)], "BSND", "PAGED", 16, 1),
+    # sequences without keys among long ones, and more groups of queries than are shared out equally
+    ("bf16", 16, [1] * 40, [0 if b % 3 else 3000 * (b % 2) + b for b in range(40)], "TND", "PAGED", 64, 1),
+    ("fp8", 8, [1] * 1100, [5000 if b in (7, 1050) else b % 60 for b in range(1100)], "BSND", "PAGED", 64, 1),
 ]
 
 
