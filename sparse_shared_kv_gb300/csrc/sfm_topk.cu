@@ -146,6 +146,25 @@ __device__ __forceinline__ void find_bin(const uint32_t *bins, uint32_t need, ui
     __syncthreads();
 }
 
+// One warp: the want-th largest of n <= 32 keys.
+template <int BINS>
+__device__ __forceinline__ void rank_few(Shared<BINS> &sh, const uint32_t *few, int n, uint32_t want)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t key = lane < n ? few[lane] : 0u;
+    uint32_t above = 0, equal = 0;
+#pragma unroll
+    for (int o = 0; o < 32; ++o) {
+        const uint32_t other = __shfl_sync(0xffffffffu, key, o);
+        above += other > key;
+        equal += other == key;
+    }
+    if (lane < n && above < want && want <= above + equal) {         // the lanes of one key alone
+        sh.threshold = above + equal == want ? key - 1 : key;
+        sh.take_equal = above + equal == want ? 0 : want - above;
+    }
+}
+
 // The want-th largest of the n listed keys, all of which share the bits above
 // `open`: selected are keys > sh.threshold and the first sh.take_equal equal to
 // it.  All threads of the CTA call it.  Eight bits at a time; the last 32
@@ -154,6 +173,11 @@ template <int NT, int BINS>
 __device__ __forceinline__ void search_list(Shared<BINS> &sh, const uint32_t *list, uint32_t n, int open, uint32_t prefix,
                                             uint32_t want)
 {
+    if (n <= 32) {
+        if (threadIdx.x < 32) rank_few(sh, list, (int)n, want);
+        __syncthreads();
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31;
     while (true) {
         const int b = open < 8 ? open : 8;
@@ -209,20 +233,7 @@ __device__ __forceinline__ void search_list(Shared<BINS> &sh, const uint32_t *li
                 if ((key >> open) == prefix) sh.few[atomicAdd(&sh.few_n, 1u)] = key;
             }
             __syncthreads();
-            if (tid < 32) {
-                const uint32_t key = lane < (int)in_bin ? sh.few[lane] : 0u;
-                uint32_t above = 0, equal = 0;
-#pragma unroll
-                for (int o = 0; o < 32; ++o) {
-                    const uint32_t other = __shfl_sync(0xffffffffu, key, o);
-                    above += other > key;
-                    equal += other == key;
-                }
-                if (lane < (int)in_bin && above < want && want <= above + equal) {     // the lanes of one key alone
-                    sh.threshold = above + equal == want ? key - 1 : key;
-                    sh.take_equal = above + equal == want ? 0 : want - above;
-                }
-            }
+            if (tid < 32) rank_few(sh, sh.few, (int)in_bin, want);
             break;
         }
         __syncthreads();                          // found has been read
@@ -267,13 +278,14 @@ __device__ __forceinline__ void pool_chunk(const float4 *src, int lane, Store st
     }
 }
 
-// CTAs of 256 threads work on many short rows: fewer bins and registers, so that five of them share an SM (2048 rows of
-// 8192: 50 -> 42 us, 2048 rows of 256 blocks: 39 -> 34 us).
-template <int NT, bool CACHED>
-__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const TopkArgs a)
+// POOLED: blocks of several scores.
+// CTAs of at most 256 threads work on many short rows: fewer bins, and registers for four of 256 threads (pooled, whose
+// loads are most of the work: five) to share an SM.
+template <int NT, bool CACHED, bool POOLED>
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : (POOLED ? 1280 : 1024) / NT) sfm_topk_kernel(const TopkArgs a)
 {
     constexpr int NW = NT / 32;
-    constexpr int kTop = NT == 256 ? 11 : 12, kMine = 1 << kTop;       // bits of the first digit, bins
+    constexpr int kTop = NT <= 256 ? 11 : 12, kMine = 1 << kTop;       // bits of the first digit, bins
     __shared__ Shared<kMine> sh;
     extern __shared__ __align__(16) uint32_t keys[];
     uint32_t *bits = keys + a.slice_cap;          // a word per 16 keys: above the digit, and (upper half) in it
@@ -320,12 +332,29 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
         if (CACHED) return keys[key_slot(i)];
         return forced(base + i) ? kForced : block_key(row, base + i, l, len);
     };
+    // Bins: the keys' top bits, or, once a row's CTA has seen the largest of its first keys, the four octaves below it
+    // in steps of 1 << kNear, with all that lies outside in the first and last bin.  Then a bin holds a few keys, and
+    // not some percent of the row, and the list is short.  Should the k-th key lie outside, the top bits are counted
+    // after all.
+    constexpr int kNear = 25 - kTop;
+    uint32_t near = 0;                            // the key that the second bin starts at
+    int bin_shift = 32 - kTop;
+    auto look = [&](uint32_t most) {              // all threads call it
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) sh.warp_above[warp] = most;
+        __syncthreads();
+        most = __reduce_max_sync(0xffffffffu, lane < NW ? sh.warp_above[lane] : 0u);
+        if (most > kLeast + (kMine << kNear)) {
+            near = ((most >> kNear) - (kMine - 3)) << kNear;
+            bin_shift = kNear;
+        }
+    };
     auto count = [&](uint32_t key) {
-        atomicAdd(&sh.hist[key >> (32 - kTop)], 1u);
+        atomicAdd(&sh.hist[min((max(key, near) - near) >> bin_shift, (uint32_t)kMine - 1)], 1u);
     };
 
-    // ---- keys, and the histogram of their top 12 bits ------------------------------
-    if (CACHED && l == 0 && a.aligned) {
+    // ---- keys, and their histogram ---------------------------------------------------
+    if (CACHED && !POOLED && a.aligned) {
         const float4 *src = reinterpret_cast<const float4 *>(row + base);
         const int quads = cnt >> 2;
         auto quad = [&](int q, const float4 &v) {
@@ -343,37 +372,44 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
             count(w.z);
             count(w.w);
         };
-        int q = tid;
         constexpr int kAhead = NT > 512 ? 4 : 8;
-        for (; q + (kAhead - 1) * NT < quads; q += kAhead * NT) {
+        for (int q0 = 0; q0 < quads; q0 += kAhead * NT) {
             float4 v[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) v[i] = __ldg(src + q + i * NT);
+            for (int i = 0; i < kAhead; ++i) {
+                const int q = q0 + i * NT + tid;
+                v[i] = q < quads ? __ldg(src + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (C == 1 && q0 == 0) look(tid < quads ? key_of(fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w))) : 0u);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) quad(q + i * NT, v[i]);
+            for (int i = 0; i < kAhead; ++i)
+                if (q0 + i * NT + tid < quads) quad(q0 + i * NT + tid, v[i]);
         }
-        for (; q < quads; q += NT) quad(q, __ldg(src + q));
         const int i = (quads << 2) + tid;
         if (i < cnt) {
             const uint32_t key = forced(base + i) ? kForced : key_of(__ldg(row + base + i));
             keys[key_slot(i)] = key;
             count(key);
         }
-    } else if (CACHED && l == 0) {
-        auto one = [&](int i, float v) {
-            const uint32_t key = forced(base + i) ? kForced : key_of(v);
-            keys[key_slot(i)] = key;
-            count(key);
-        };
-        int i = tid;
-        for (; i + 7 * NT < cnt; i += 8 * NT) {
+    } else if (CACHED && !POOLED) {
+        for (int i0 = 0; i0 < cnt; i0 += 8 * NT) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __ldg(row + base + i + e * NT);
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * NT + tid;
+                v[e] = i < cnt ? __ldg(row + base + i) : 0.f;
+            }
+            if (C == 1 && i0 == 0) look(tid < cnt ? key_of(v[0]) : 0u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) one(i + e * NT, v[e]);
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * NT + tid;
+                if (i < cnt) {
+                    const uint32_t key = forced(base + i) ? kForced : key_of(v[e]);
+                    keys[key_slot(i)] = key;
+                    count(key);
+                }
+            }
         }
-        for (; i < cnt; i += NT) one(i, __ldg(row + base + i));
     } else if (CACHED) {
         // a block's largest score is taken before it becomes a key: fmaxf passes over NaN
         auto store = [&](int j, float best) {
@@ -446,10 +482,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
         }
         return v;
     };
+    // pass -1: the bins near the largest key
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 32 - kTop : pass == 1 ? 10 : 0, bits_n = pass == 0 ? kTop : pass == 1 ? 22 - kTop : 10;
-        if (pass > 0) {                           // too many keys share the digits so far: count the next ones
+    for (int pass = near ? -1 : 0; pass < 3; ++pass) {
+        const int shift = pass < 0 ? kNear : pass == 0 ? 32 - kTop : pass == 1 ? 10 : 0;
+        const int bits_n = pass == 0 ? kTop : pass == 1 ? 22 - kTop : 10;
+        if (pass > 0 || (pass == 0 && near)) {    // too many keys share the digits so far: count the next ones
             clear(sh.hist, kMine);
             if (C > 1) {
                 clear(cs.total, kBins);
@@ -459,7 +497,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
             }
             for (int i = tid; i < cnt; i += NT) {
                 const uint32_t key = key_at(i);
-                if ((key >> (shift + bits_n)) == prefix) atomicAdd(&sh.hist[(key >> shift) & ((1u << bits_n) - 1)], 1u);
+                if (pass == 0 || (key >> (shift + bits_n)) == prefix)
+                    atomicAdd(&sh.hist[(key >> shift) & ((1u << bits_n) - 1)], 1u);
             }
             __syncthreads();
         }
@@ -474,10 +513,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
         if (C > 1) find_bin<NT, kBins>(cs.total, need, sh.warp_above, sh.found);
         else find_bin<NT, kMine>(sh.hist, need, sh.warp_above, sh.found);
         const uint32_t in_bin = sh.found[2];
-        // first pass: fewer scores than k (or the k-th would be none), all are taken
-        if (in_bin == 0 || (pass == 0 && sh.found[0] < kLeast >> shift)) break;
+        if (pass < 0) {
+            // outside of the fine bins, or too many equal keys for the list
+            if (in_bin == 0 || in_bin > (uint32_t)kMine || sh.found[0] == 0 || sh.found[0] == kMine - 1) continue;
+            prefix = (near >> kNear) + sh.found[0];
+        } else {
+            // first digit: fewer scores than k (or the k-th would be none), all are taken
+            if (in_bin == 0 || (pass == 0 && sh.found[0] < kLeast >> shift)) break;
+            prefix = prefix << bits_n | sh.found[0];
+        }
         need -= sh.found[1];
-        prefix = prefix << bits_n | sh.found[0];
         if (in_bin == need) {                     // the whole bin is taken
             threshold = (prefix << shift) - 1;
             break;
@@ -634,11 +679,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1) sfm_topk_kernel(const T
     for (int64_t i = filled + rank * NT + tid; i < a.k; i += (int64_t)C * NT) out[i] = -1;
 }
 
-template <int NT, bool CACHED>
+template <int NT, bool CACHED, bool POOLED>
 cudaError_t launch(const TopkArgs &a, int device, int64_t rows, size_t smem, cudaStream_t st)
 {
     static std::atomic<bool> ready[kMaxDevices];
-    auto kernel = sfm_topk_kernel<NT, CACHED>;
+    auto kernel = sfm_topk_kernel<NT, CACHED, POOLED>;
     return prepared_launch(
         ready, device,
         [&] {
@@ -709,9 +754,12 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     const size_t smem = (size_t)a.slice_cap * 4 + (size_t)a.slice_cap / 4 + (c > 1 ? sizeof(ClusterShared) : 0);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (!cached) e = launch<1024, false>(a, dev, p.rows, smem, st);
-    else if (slice(c) > 16384) e = launch<1024, true>(a, dev, p.rows, smem, st);
-    else if (c > 1) e = launch<512, true>(a, dev, p.rows, smem, st);
-    else e = launch<256, true>(a, dev, p.rows, smem, st);
+    const bool pooled = a.bs_log2 > 0;
+    if (!cached) e = launch<1024, false, false>(a, dev, p.rows, smem, st);
+    else if (slice(c) > 16384)
+        e = pooled ? launch<1024, true, true>(a, dev, p.rows, smem, st) : launch<1024, true, false>(a, dev, p.rows, smem, st);
+    else if (c > 1)
+        e = pooled ? launch<512, true, true>(a, dev, p.rows, smem, st) : launch<512, true, false>(a, dev, p.rows, smem, st);
+    else e = pooled ? launch<256, true, true>(a, dev, p.rows, smem, st) : launch<256, true, false>(a, dev, p.rows, smem, st);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
