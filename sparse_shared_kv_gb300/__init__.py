@@ -646,8 +646,9 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     float8_e4m3fn; index_k: (b, S, 128), (t, 128) or paged (blocks,
     block_size, 128) of the same dtype, rows may be padded apart; weights:
     fp32 (tokens, heads) in q's leading shape; k_scales: fp32, one per row of
-    index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, -inf where a key
-    is not visible; visible (tokens) int32).  ``out`` may be a
+    index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, its rows a
+    multiple of four values apart, -inf where a key is not visible; visible
+    (tokens) int32).  ``out`` may be a
     view with wider rows."""
     code, dev = _first("q", q, _INDEX_TYPES)
     if stream is not None or dev != _current_device():
@@ -696,8 +697,10 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
         0 if seqused_kv is None else _address("seqused_kv", seqused_kv, _I32, dev, each),
         0 if cmp_residual_kv is None else _address("cmp_residual_kv", cmp_residual_kv, _I32, dev, each))
     if out is None:
-        out = torch.empty((tokens, max(max_seqlen_kv, 0)), dtype=_F32, device=q.device)
-        stride = max_seqlen_kv
+        stride = (max_seqlen_kv + 3) // 4 * 4     # rows on 16-byte boundaries, which the selection reads fastest
+        out = torch.empty((tokens, max(stride, 0)), dtype=_F32, device=q.device)
+        if stride != max_seqlen_kv:
+            out = out[:, :max(max_seqlen_kv, 0)]
     else:
         if not (isinstance(out, torch.Tensor) and out.dtype is _F32 and out.get_device() == dev
                 and out.shape == (tokens, max_seqlen_kv) and (out.stride(1) == 1 or max_seqlen_kv == 1)):

@@ -29,7 +29,7 @@ struct RopeArgs {
     int64_t xt, xh, yt, yh;                    // strides in elements
     int32_t tokens, heads, dim, rot, off;
     int32_t units, token_units, block_tokens;  // units per head, per token; tokens per block
-    int32_t block_units;                       // units per block
+    int32_t block_units, span_tokens;          // rows: units of a token per block, tokens one after the other
     FastDiv units_div, token_div;
     float amplitude;
     int32_t inverse, in_place;
@@ -37,69 +37,81 @@ struct RopeArgs {
 
 // The common form: 16-byte accesses in the order of memory, out of place (or in
 // place with interleaved pairs).  A half-layout vector also reads its partners
-// (a neighbour loads them too, so they come from L1) and writes its own values
-// only.  A block takes a run of a token's vectors, as long as there are blocks
-// enough for every SM, so that a long row works its cosines out a few times
-// only.
+// (a neighbour loads them too, so they come from L1; by shuffle 8 % slower) and
+// writes its own values only.  A block takes a run of a token's vectors, or of
+// several tokens, as long as there are blocks enough for every SM: the
+// frequencies are turned into steps of a turn once per block (64-bit floating
+// point is slow here), the cosines worked out once per token.
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(RopeArgs a)
 {
-    __shared__ __align__(16) float2 cs[kMaxPairs];
+    constexpr int kPer = HALF ? 8 : 4;                    // pairs of a vector, and one unused between vectors: then the
+    __shared__ float2 cs[kMaxPairs + kMaxPairs / kPer];   // lanes' reads of their e-th pairs meet in no bank
+    extern __shared__ unsigned long long step[];          // [rot / 2]
     const int tid = threadIdx.x, half = a.rot / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * a.block_tokens;
-    const int ntok = (int)min((int64_t)a.block_tokens, a.tokens - t0);
-    const int first = blockIdx.y * a.block_units;
-    const int last = min(first + a.block_units, ntok * a.token_units);
-
-    for (int base = first; base < last; base += kBlockUnits) {
-        uint4 va[kUnits], vb[kUnits];
-        int32_t tok[kUnits], head[kUnits], at[kUnits];
+    const int64_t end = min((int64_t)a.tokens, ((int64_t)blockIdx.x + 1) * a.span_tokens);
+    bool fresh = true;                                    // the steps are still to come
+    for (int64_t t0 = (int64_t)blockIdx.x * a.span_tokens; t0 < end; t0 += a.block_tokens) {
+        const int ntok = (int)min((int64_t)a.block_tokens, end - t0);
+        const int first = blockIdx.y * a.block_units;
+        const int last = min(first + a.block_units, ntok * a.token_units);
+        for (int base = first; base < last; base += kBlockUnits) {
+            uint4 va[kUnits], vb[kUnits];
+            int32_t tok[kUnits], head[kUnits], at[kUnits];
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = base + k * kThreads + tid;
-            if (u >= last) continue;
-            tok[k] = (int)fdiv((uint32_t)u, a.token_div);
-            const int r = u - tok[k] * a.token_units;
-            head[k] = (int)fdiv((uint32_t)r, a.units_div);
-            at[k] = (r - head[k] * a.units) * 8 + (a.in_place ? a.off : 0);
-            const T *src = static_cast<const T *>(a.x) + (t0 + tok[k]) * a.xt + (int64_t)head[k] * a.xh + at[k];
-            va[k] = *reinterpret_cast<const uint4 *>(src);
-            const int in = at[k] - a.off;
-            if (HALF && in >= 0 && in < a.rot) vb[k] = *reinterpret_cast<const uint4 *>(src + (in < half ? half : -half));
-        }
-        if (base == first) {
-            for (int i = tid; i < ntok * half; i += kThreads) {
-                const int t = i / half;
-                cs[i] = rope::cos_sin(__ldg(a.positions + t0 + t), rope::turn_step(__ldg(a.inv_freq + i - t * half)),
-                                      a.amplitude, a.inverse != 0);
+            for (int k = 0; k < kUnits; ++k) {
+                const int u = base + k * kThreads + tid;
+                if (u >= last) continue;
+                tok[k] = (int)fdiv((uint32_t)u, a.token_div);
+                const int r = u - tok[k] * a.token_units;
+                head[k] = (int)fdiv((uint32_t)r, a.units_div);
+                at[k] = (r - head[k] * a.units) * 8 + (a.in_place ? a.off : 0);
+                const T *src = static_cast<const T *>(a.x) + (t0 + tok[k]) * a.xt + (int64_t)head[k] * a.xh + at[k];
+                va[k] = *reinterpret_cast<const uint4 *>(src);
+                const int in = at[k] - a.off;
+                if (HALF && in >= 0 && in < a.rot) vb[k] = *reinterpret_cast<const uint4 *>(src + (in < half ? half : -half));
             }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            if (base + k * kThreads + tid >= last) continue;
-            const int in = at[k] - a.off;
-            if (in >= 0 && in < a.rot) {
-                float p[8];
-                rope::unpack8<T>(va[k], p);
-                const float2 *c = cs + tok[k] * half + (HALF ? (in < half ? in : in - half) : in / 2);
-                if (HALF) {
-                    float q[8];
-                    rope::unpack8<T>(vb[k], q);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = fmaf(p[e], c[e].x, in < half ? -q[e] * c[e].y : q[e] * c[e].y);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 r = rope::rotate(p[2 * e], p[2 * e + 1], c[e]);
-                        p[2 * e] = r.x;
-                        p[2 * e + 1] = r.y;
-                    }
+            if (base == first) {                          // (the loads above are on their way)
+                if (fresh) {
+                    for (int i = tid; i < half; i += kThreads) step[i] = rope::turn_step(__ldg(a.inv_freq + i));
+                    fresh = false;
                 }
-                va[k] = rope::pack8<T>(p);
+                __syncthreads();                          // the steps are there, the last tokens' cosines have been read
+                for (int i = tid; i < ntok * half; i += kThreads) {
+                    const int t = i / half, p = i - t * half;
+                    cs[i + i / kPer] = rope::cos_sin(__ldg(a.positions + t0 + t), step[p], a.amplitude, a.inverse != 0);
+                }
+                __syncthreads();
             }
-            T *dst = static_cast<T *>(a.y) + (t0 + tok[k]) * a.yt + (int64_t)head[k] * a.yh + at[k];
-            *reinterpret_cast<uint4 *>(dst) = va[k];
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                if (base + k * kThreads + tid >= last) continue;
+                const int in = at[k] - a.off;
+                if (in >= 0 && in < a.rot) {
+                    float p[8];
+                    rope::unpack8<T>(va[k], p);
+                    const float2 *c = cs + (tok[k] * half / kPer + (HALF ? (in < half ? in : in - half) : in) / 8) * (kPer + 1);
+                    if (HALF) {
+                        float q[8];
+                        rope::unpack8<T>(vb[k], q);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 t = c[e];
+                            p[e] = fmaf(p[e], t.x, in < half ? -q[e] * t.y : q[e] * t.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 r = rope::rotate(p[2 * e], p[2 * e + 1], c[e]);
+                            p[2 * e] = r.x;
+                            p[2 * e + 1] = r.y;
+                        }
+                    }
+                    va[k] = rope::pack8<T>(p);
+                }
+                T *dst = static_cast<T *>(a.y) + (t0 + tok[k]) * a.yt + (int64_t)head[k] * a.yh + at[k];
+                *reinterpret_cast<uint4 *>(dst) = va[k];
+            }
         }
     }
 }
@@ -139,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(RopeArgs a)
         if (i < pair_units) {
             at = a.off + (HALF ? i * VEC : 2 * i);
             other[k] = HALF ? a.rot / 2 : 1;
-            pair[k] = tok * (a.rot / 2) + i * VEC;
+            pair[k] = tok * (a.rot / 2) + i;
         } else {
             at = (i - pair_units) * VEC;
             if (at >= a.off) at += a.rot;
@@ -153,9 +165,10 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(RopeArgs a)
 
     const int np = ntok * (a.rot / 2);
     for (int i = tid; i < np; i += kThreads) {
-        const int tok = i / (a.rot / 2);
-        cs[i] = rope::cos_sin(__ldg(a.positions + t0 + tok), rope::turn_step(__ldg(a.inv_freq + i - tok * (a.rot / 2))),
-                              a.amplitude, a.inverse != 0);
+        const int tok = i / (a.rot / 2), p = i - tok * (a.rot / 2);
+        // the e-th pairs of all units side by side: neighbouring lanes read neighbouring words
+        cs[i - p + (p % VEC) * (a.rot / 2 / VEC) + p / VEC] =
+            rope::cos_sin(__ldg(a.positions + t0 + tok), rope::turn_step(__ldg(a.inv_freq + p)), a.amplitude, a.inverse != 0);
     }
     __syncthreads();
 
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(RopeArgs a)
                 rope::unpack8<T>(vb[k], q);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float2 r = rope::rotate(p[e], q[e], cs[pair[k] + e]);
+                    const float2 r = rope::rotate(p[e], q[e], cs[pair[k] + e * (a.rot / 2 / VEC)]);
                     p[e] = r.x;
                     q[e] = r.y;
                 }
@@ -212,7 +225,7 @@ cudaError_t launch(const RopeArgs &a, dim3 grid, cudaStream_t st)
 template <typename T, bool HALF>
 cudaError_t launch_rows(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    return launch_plain(sfm_rope_rows_kernel<T, HALF>, grid, dim3(kThreads), 0, st, a);
+    return launch_plain(sfm_rope_rows_kernel<T, HALF>, grid, dim3(kThreads), (size_t)a.rot / 2 * 8, st, a);
 }
 
 template <typename T>
@@ -318,8 +331,8 @@ extern "C" int sfm_rope(const sfm_rope_params *pp, const void *x, const int32_t 
     const int64_t token_units = (int64_t)a.units * p.heads;
     int dev = 0, sms = 0;
     if (current_sms(&dev, &sms) != cudaSuccess) return SFM_ERR_CUDA;
-    // rows: a block takes up to eight steps of a token while the tokens alone
-    // give every SM its blocks
+    // rows: a block takes up to eight steps of 1024 units, of one token or of
+    // several, while there are 16 blocks for every SM
     int64_t steps = 1;
     while (rows && steps < 8 && p.tokens * token_units / (2 * steps * kBlockUnits) >= 16 * (int64_t)sms) steps *= 2;
     a.block_units = (int32_t)(steps * kBlockUnits);
@@ -331,7 +344,10 @@ extern "C" int sfm_rope(const sfm_rope_params *pp, const void *x, const int32_t 
     a.block_tokens = (int32_t)(bt < 1 ? 1 : bt > kMaxTokens ? kMaxTokens : bt);
     a.units_div = make_fastdiv((uint32_t)a.units);
     a.token_div = make_fastdiv((uint32_t)token_units);
-    const dim3 grid((unsigned)((p.tokens + (int64_t)a.block_tokens - 1) / a.block_tokens), (unsigned)chunks);
+    const int64_t groups = rows && chunks == 1 ? steps * kBlockUnits / (a.block_tokens * token_units) : 1;
+    a.span_tokens = (int32_t)(a.block_tokens * (groups > 1 ? groups : 1));
+    const int64_t span = rows ? a.span_tokens : a.block_tokens;
+    const dim3 grid((unsigned)((p.tokens + span - 1) / span), (unsigned)chunks);
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = p.dtype == SFM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, vec, half, rows, grid, st)
                                                     : launch_type<__half>(a, vec, half, rows, grid, st);

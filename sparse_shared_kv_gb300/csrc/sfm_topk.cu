@@ -21,6 +21,8 @@
 // and the cluster's first CTA searches the list.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "sfm_internal.cuh"
 
 namespace cg = cooperative_groups;
@@ -245,15 +247,19 @@ __device__ __forceinline__ void search_list(Shared<BINS> &sh, const uint32_t *li
 // whole blocks of a warp, which share GL lanes' bits.  Lanes swap half of what
 // they hold while they hold more than one value, so eight values cost eight
 // exchanges and not 8 GL.  store(block, value) gets each block once.
-template <int GL, typename Store>
-__device__ __forceinline__ void pool_chunk(const float4 *src, int lane, Store store)
+template <int GL, bool ALIGNED, typename Store>
+__device__ __forceinline__ void pool_chunk(const float *src, int lane, Store store)
 {
     constexpr int kSwaps = GL < 3 ? GL : 3;
     float v[8];
     {
         float4 w[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) w[s] = __ldg(src + 32 * s + lane);
+        for (int s = 0; s < 8; ++s) {
+            const float *at = src + 4 * (32 * s + lane);
+            w[s] = ALIGNED ? __ldg(reinterpret_cast<const float4 *>(at))
+                           : make_float4(__ldg(at), __ldg(at + 1), __ldg(at + 2), __ldg(at + 3));
+        }
 #pragma unroll
         for (int s = 0; s < 8; ++s) v[s] = fmaxf(fmaxf(w[s].x, w[s].y), fmaxf(w[s].z, w[s].w));
     }
@@ -419,20 +425,24 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : (POOLED ? 1280 : 1024) / NT
         };
         const int gl = l - 2;
         int done = 0;                             // blocks of the chunks that lie inside the row
-        if (a.aligned && l >= 2) {
+        if (l >= 2) {
             const int chunk = 256 >> gl;
             const int whole = (int)min((int64_t)cnt, (len >> l) - (int64_t)base) / chunk;
-            const float4 *src = reinterpret_cast<const float4 *>(row + ((int64_t)base << l));
+            const float *src = row + ((int64_t)base << l);
             for (int c = warp; c < whole; c += NW) {
-                const float4 *from = src + (int64_t)c * 256;
+                const float *from = src + (int64_t)c * 1024;
                 auto put = [&](int b, float best) { store(c * chunk + b, best); };
+                auto pool = [&](auto g) {
+                    if (a.aligned) pool_chunk<g.value, true>(from, lane, put);
+                    else pool_chunk<g.value, false>(from, lane, put);
+                };
                 switch (gl) {
-                case 0: pool_chunk<0>(from, lane, put); break;
-                case 1: pool_chunk<1>(from, lane, put); break;
-                case 2: pool_chunk<2>(from, lane, put); break;
-                case 3: pool_chunk<3>(from, lane, put); break;
-                case 4: pool_chunk<4>(from, lane, put); break;
-                default: pool_chunk<5>(from, lane, put); break;
+                case 0: pool(std::integral_constant<int, 0>{}); break;
+                case 1: pool(std::integral_constant<int, 1>{}); break;
+                case 2: pool(std::integral_constant<int, 2>{}); break;
+                case 3: pool(std::integral_constant<int, 3>{}); break;
+                case 4: pool(std::integral_constant<int, 4>{}); break;
+                default: pool(std::integral_constant<int, 5>{}); break;
                 }
             }
             done = max(whole, 0) * chunk;
@@ -741,12 +751,13 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     a.last = p.last_blocks;
     a.aligned = ((uintptr_t)scores & 15u) == 0 && p.score_stride % 4 == 0;
     const int64_t blocks = ((int64_t)p.n + p.block_size - 1) >> a.bs_log2;
-    // CTAs of a row: as many as it takes to hold its keys, and while half the
-    // SMs would stay idle and a CTA still has some thousand keys, twice as many
-    // (32 rows of 32768: 4 CTAs a row 9.3 us, 8 10.3 us, 2 10.4 us)
+    // CTAs of a row: as many as it takes to hold its keys, and while a CTA still
+    // has some thousand keys twice as many, up to six sevenths of the SMs (the
+    // CTAs of a cluster share a GPC, so clusters of eight do not fill them all):
+    // 32 rows of 32768 with 4 CTAs a row 9.3 us, with 8 10.3 us, with 2 10.4 us
     int c = 1;
     auto slice = [&](int q) { return ((blocks + q - 1) / q + 127) / 128 * 128; };
-    while (c < kMaxCluster && (slice(c) > kMaxSlice || ((int64_t)p.rows * c * 2 <= sms && slice(c) > 4096))) c *= 2;
+    while (c < kMaxCluster && (slice(c) > kMaxSlice || ((int64_t)p.rows * c * 14 <= (int64_t)sms * 6 && slice(c) > 4096))) c *= 2;
     if ((int64_t)p.rows * c > INT32_MAX) return SFM_ERR_UNSUPPORTED;
     a.cluster = c;
     const bool cached = slice(c) <= kMaxSlice;
