@@ -698,9 +698,7 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
         0 if cmp_residual_kv is None else _address("cmp_residual_kv", cmp_residual_kv, _I32, dev, each))
     if out is None:
         stride = (max_seqlen_kv + 3) // 4 * 4     # rows on 16-byte boundaries, which the selection reads fastest
-        out = torch.empty((tokens, max(stride, 0)), dtype=_F32, device=q.device)
-        if stride != max_seqlen_kv:
-            out = out[:, :max(max_seqlen_kv, 0)]
+        out = torch.empty_strided((tokens, max(max_seqlen_kv, 0)), (max(stride, 1), 1), dtype=_F32, device=q.device)
     else:
         if not (isinstance(out, torch.Tensor) and out.dtype is _F32 and out.get_device() == dev
                 and out.shape == (tokens, max_seqlen_kv) and (out.stride(1) == 1 or max_seqlen_kv == 1)):

@@ -766,11 +766,16 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     const bool pooled = a.bs_log2 > 0;
+    // Threads: a short slice has few keys per thread, and many small CTAs hide each other's barriers (2048 x
+    // 16384 scores in blocks of 64, 256 keys a row: 35 us with 256 threads, 33 with 128; 2690 x 1055 in blocks of
+    // 16: 20.4 and 13.6).  Long slices want every lane that the SM has.
     if (!cached) e = launch<1024, false, false>(a, dev, p.rows, smem, st);
     else if (slice(c) > 16384)
         e = pooled ? launch<1024, true, true>(a, dev, p.rows, smem, st) : launch<1024, true, false>(a, dev, p.rows, smem, st);
     else if (c > 1)
         e = pooled ? launch<512, true, true>(a, dev, p.rows, smem, st) : launch<512, true, false>(a, dev, p.rows, smem, st);
-    else e = pooled ? launch<256, true, true>(a, dev, p.rows, smem, st) : launch<256, true, false>(a, dev, p.rows, smem, st);
+    else if (slice(c) > 2048)
+        e = pooled ? launch<256, true, true>(a, dev, p.rows, smem, st) : launch<256, true, false>(a, dev, p.rows, smem, st);
+    else e = pooled ? launch<128, true, true>(a, dev, p.rows, smem, st) : launch<128, true, false>(a, dev, p.rows, smem, st);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
