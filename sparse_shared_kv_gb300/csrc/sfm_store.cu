@@ -11,6 +11,13 @@
 // token's other heads.  The next row's values are under way while a row is
 // worked on.  Everything is held in fp32 until the one rounding to the
 // cache's format.
+//
+// Measured on one GB300: 16381 rows of 512 values, normed, rotated and stored as
+// bf16: 9.3 us (3.6 TB/s), 131072 index rows of 128 values to E4M3: 16.7 us
+// (3.0 TB/s), 441488 such rows normed: 56 us (3.0 TB/s), where instructions
+// bound it more than memory; 64 packed rows: 2.8 us, latency.  Eight lanes per row with sixteen values
+// each need fewer shuffles but spill the half layout's cosines: 48 us for the
+// 441488 rows, but 24.6 for the 131072, so sixteen it is.
 #include <math.h>
 
 #include "sfm_internal.cuh"
@@ -62,6 +69,13 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+__device__ __forceinline__ float max_abs(float a, float b, float c)       // of magnitudes; NaN if one is
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ float fast_inverse(float x)      // one unit in the last place
 {
     float r;
@@ -92,21 +106,25 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
     const int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * per;
     const int64_t r1 = min(r0 + per, a.total);
 
+    // the next row: its values, and its token's position and slot
     uint4 w[STEPS];
-    int32_t token, head, position, slot;
-    auto load = [&](int64_t r) {                  // row r: its values, position and slot
-        token = a.heads == 1 ? (int)r : (int)fdiv((uint32_t)r, a.heads_div);
-        head = (int)(r - (int64_t)token * a.heads);
-        const T *src = static_cast<const T *>(a.x) + (int64_t)token * a.xt + (int64_t)head * a.xh;
+    int32_t position = 0, slot;
+    int token = a.heads == 1 ? (int)(r0 < r1 ? r0 : 0) : (int)fdiv((uint32_t)(r0 < r1 ? r0 : 0), a.heads_div);
+    int head = (int)((r0 < r1 ? r0 : 0) - (int64_t)token * a.heads);
+    const T *src = static_cast<const T *>(a.x) + (int64_t)token * a.xt + (int64_t)head * a.xh + lane * 8;
+    const int64_t to_next = a.xt - (int64_t)(a.heads - 1) * a.xh;
+    auto load_row = [&] {
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int at = (s * LANES + lane) * 8;
-            w[s] = at < a.dim ? __ldg(reinterpret_cast<const uint4 *>(src + at)) : make_uint4(0, 0, 0, 0);
-        }
+        for (int s = 0; s < STEPS; ++s)
+            w[s] = (s * LANES + lane) * 8 < a.dim ? __ldg(reinterpret_cast<const uint4 *>(src + s * LANES * 8))
+                                                  : make_uint4(0, 0, 0, 0);
+    };
+    auto load_token = [&] {
         slot = a.slots ? __ldg(a.slots + token) : token;
         if (ROPE) position = __ldg(a.positions + token);
     };
-    load(r0 < r1 ? r0 : 0);
+    load_row();
+    load_token();
     if (ROPE) {
         for (int i = tid; i < pairs; i += kThreads) step[i] = rope::turn_step(__ldg(a.inv_freq + i));
         __syncthreads();
@@ -122,22 +140,37 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
 #pragma unroll
         for (int e = 0; e < kOwn; e += 2) {
             const float4 two = *reinterpret_cast<const float4 *>(cs + first + e);
-            c[e] = make_float2(two.x, two.y);
-            c[e + 1] = make_float2(two.z, two.w);
+            // half layout: the sine's sign is that of the partner's part
+            const bool minus = ROPE > 1 && at < pairs;
+            c[e] = make_float2(two.x, minus ? -two.y : two.y);
+            c[e + 1] = make_float2(two.z, minus ? -two.w : two.w);
         }
     };
     int last_token = -1;
-    for (int64_t i = 0; i < per; ++i) {          // every group runs the same count: warp collectives inside
-        const int64_t r = r0 + i;
-        const bool live = r < r1;
+    const int32_t left = (int32_t)(r1 - r0);     // zero or less: nothing to do for this group
+    for (int32_t i = 0; i < (int32_t)per; ++i) { // every group runs the same count: warp collectives inside
+        const bool live = i < left;
         float v[STEPS][8];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) rope::unpack8<T>(w[s], v[s]);
+        const int32_t this_token = token, this_position = position;
+        const bool fresh = this_token != last_token;
         const int64_t row = (int64_t)slot * a.heads + head;
         const bool inside = slot >= 0 && row < a.rows;
         if (live && slot >= 0 && !inside && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
-        const int32_t this_token = token, this_position = position;
-        if (r + 1 < r1) load(r + 1);
+        last_token = this_token;
+        if (i + 1 < left) {
+            if (++head == a.heads) {
+                head = 0;
+                ++token;
+                src += to_next;
+                load_row();
+                load_token();
+            } else {
+                src += a.xh;
+                load_row();
+            }
+        }
 
         if (a.norm) {
             float sum = 0.f;
@@ -169,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
         }
 
         if (ROPE) {
-            if (__any_sync(0xffffffffu, this_token != last_token)) {
+            if (__any_sync(0xffffffffu, fresh)) {
                 __syncwarp();
                 for (int p = lane; p < pairs; p += LANES) cs[p] = rope::cos_sin(this_position, step[p], a.amplitude, false);
                 __syncwarp();
@@ -177,7 +210,6 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
                     const int at = lane * 8 - a.off;
                     if (at >= 0 && at < a.rot) own(at, kept);
                 }
-                last_token = this_token;
             }
             if (ROPE == 3) {
                 __syncwarp();
@@ -191,12 +223,9 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
                 }
                 __syncwarp();
             }
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int at = (s * LANES + lane) * 8 - a.off;
+            auto rotate_step = [&](float(&x)[8], int at) {
                 const bool in = at >= 0 && at < a.rot;
-                // (half layout inside one step: the other steps rotate nothing in any lane)
-                if (ROPE == 2 ? a.off / (LANES * 8) != s : !in) continue;
+                if (ROPE != 2 && !in) return;
                 float2 c[kOwn];
                 if constexpr (kKeep) {
 #pragma unroll
@@ -204,23 +233,32 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
                 } else if (in) {
                     own(at, c);
                 }
-                const bool second = at >= pairs;
                 if (ROPE == 1) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 q = rope::rotate(v[s][2 * e], v[s][2 * e + 1], c[e]);
-                        v[s][2 * e] = q.x;
-                        v[s][2 * e + 1] = q.y;
+                        const float2 q = rope::rotate(x[2 * e], x[2 * e + 1], c[e]);
+                        x[2 * e] = q.x;
+                        x[2 * e + 1] = q.y;
                     }
                 } else {
-                    const int from = (tid & 31) + (in ? (second ? -pairs : pairs) / 8 : 0);
+                    const int away = at >= pairs ? -pairs : pairs;       // to the partner
+                    const int from = (tid & 31) + (in ? away / 8 : 0);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float other = ROPE == 2 ? __shfl_sync(0xffffffffu, v[s][e], from)
-                                                      : turn[second ? at - pairs + e : at + pairs + e];
-                        if (in) v[s][e] = fmaf(v[s][e], c[e % kOwn].x, second ? other * c[e % kOwn].y : -other * c[e % kOwn].y);
+                        const float other = ROPE == 2 ? __shfl_sync(0xffffffffu, x[e], from) : turn[at + away + e];
+                        if (in) x[e] = fmaf(x[e], c[e % kOwn].x, other * c[e % kOwn].y);
                     }
                 }
+            };
+            const int at = lane * 8 - a.off;
+            // half layout inside one step: the other steps rotate nothing in any lane
+            const int only = ROPE == 2 ? a.off / (LANES * 8) : 0;
+            if (ROPE != 2 || only == 0) rotate_step(v[0], at);
+            if constexpr (STEPS > 1) {
+                if (ROPE != 2 || only == 1) rotate_step(v[1], at + LANES * 8);
+            }
+            if constexpr (STEPS > 2) {
+                if (ROPE != 2 || only == 2) rotate_step(v[2], at + 2 * LANES * 8);
             }
         }
 
@@ -240,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
             for (int s = 0; s < STEPS; ++s) {
                 most[s] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) most[s] = max_nan(most[s], fabsf(v[s][e]));
+                for (int e = 0; e < 8; e += 2) most[s] = max_abs(most[s], v[s][e], v[s][e + 1]);
             }
             if (kRow) {
 #pragma unroll
@@ -290,7 +328,9 @@ cudaError_t launch(const StoreArgs &a, cudaStream_t st)
     int dev = 0, sms = 0;
     const cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
-    const int64_t want = (a.total + kGroups - 1) / kGroups, most = (int64_t)sms * 8;
+    // four CTAs per SM, what its registers hold (131072 index rows: 16.7 us; with eight, two waves, 17.9; with five
+    // of 48 registers 20.0)
+    const int64_t want = (a.total + kGroups - 1) / kGroups, most = (int64_t)sms * 4;
     const unsigned grid = (unsigned)(want < most ? want : most);
     const int width = LANES * 8;
     const int form = !a.rot ? 0 : !a.half ? 1 : a.off / width == (a.off + a.rot - 1) / width ? 2 : 3;

@@ -74,13 +74,11 @@ struct ClusterShared {
 constexpr int kMaxDynamic = kMaxSlice * 4 + kMaxSlice / 4 + (int)sizeof(ClusterShared);
 static_assert(kMaxDynamic + sizeof(Shared<kBins>) <= 232448, "shared memory budget");
 
-// x's key.  NaN and -inf get one of eight keys below kLeast by lane, so that
-// rows of little else do not meet in one bin of the histogram.
+// x's key.  NaN becomes -inf, whose key lies below kLeast, and -0 becomes 0.
 __device__ __forceinline__ uint32_t key_of(float x)
 {
-    const uint32_t b = __float_as_uint(x + 0.f);          // -0 becomes 0
-    const uint32_t key = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    return x > -INFINITY ? key : (threadIdx.x & 7u) << 20;
+    const uint32_t b = __float_as_uint(fmaxf(x + 0.f, -INFINITY));
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // the key of block j of a row: scores [j << l, min((j + 1) << l, len))
