@@ -568,6 +568,20 @@ def test_topk_rows_that_mislead_a_sample(rows, n, k):
             assert torch.equal(got, torch.where(want < n, want, -1).to(torch.int32))
 
 
+@pytest.mark.parametrize("n", [700, 9001, 70001])
+@pytest.mark.parametrize("k,first,last", [(1, 0, 0), (8, 3, 5), (1, 0, 1), (700, 1, 2), (64, 40, 0), (600, 300, 300)])
+def test_topk_short_lengths_in_long_rows(n, k, first, last):
+    """Lengths that leave a part of a row's share-out with nothing, or with one to three scores."""
+    ends = [e for e in (0, 1, 2, 3, 5, 127, 129, 700, 1923, 6273, 6274, 6275, 28801, 28802, 28803, 70001) if e <= n]
+    g = gen(n + k)
+    x = torch.stack([randn(g, n) for _ in ends]).cuda()
+    x[1::2] = (x[1::2] * 2).round()
+    lengths = torch.tensor(ends, dtype=torch.int32).cuda()
+    topk_check(x, k, lengths, first_blocks=first, last_blocks=last)
+    for r in range(len(ends)):
+        topk_check(x[r:r + 1], k, lengths[r:r + 1], first_blocks=first, last_blocks=last)
+
+
 # ---------------------------------------------------------------------------
 # offsets past 32 bits
 # ---------------------------------------------------------------------------
