@@ -19,6 +19,16 @@
 // to 16 for the long rows of a few requests), each CTA holding a contiguous
 // slice; histograms and counts are added up through distributed shared memory,
 // and the cluster's first CTA searches the list.
+//
+// Measured on one GB300: 32 rows of 32768, k 512: 9.0 us; one row of 600001, k
+// 2048: 17.5 us; 2048 causal rows of up to 8192, k 1024: 33.5 us (1.75 TB/s);
+// 2048 causal rows of up to 16384 in blocks of 64, k 32: 33 us (3.8 TB/s).
+// Loading and counting take about two thirds of the last two, some fifteen block
+// barriers with little work between them the rest, and the many small passes'
+// instructions (50 per 32 keys) more than memory bound the rows of 8192.  Rows
+// kept as floats and counted in equal bins of a sample's range (34.5 us), a list
+// of the scores above a sampled value (52) and loading later rows into L2 (35.5)
+// were slower.
 #include <cooperative_groups.h>
 
 #include <type_traits>
