@@ -478,6 +478,22 @@ def test_index_scores_keep_nan_and_infinities_where_they_are():
     assert torch.equal(got[:, keep.cuda()], clean[:, keep.cuda()])
 
 
+@pytest.mark.parametrize("heads", [1, 5, 16, 24, 33, 64, 100, 128])
+def test_index_scores_of_infinite_keys(heads):
+    """A key's infinity meets the heads that are there and nothing else."""
+    p = index_problem(7, "bf16", heads, [2, 2], [300, 140], "BSND", "BSND")
+    w = p["wd"].abs() + 0.25
+    keys = p["cache"].clone()
+    for j, d, v in ((3, 5, math.inf), (130, 127, -math.inf), (139, 0, math.inf)):
+        keys[:, j, d] = v
+    got, _ = sfm.index_scores(p["qd"], keys, w, mask_mode=0, **p["kw"])
+    for b, n in enumerate([300, 140]):
+        t0 = p["first"][b]
+        want, _ = P.scores(p["q"][t0:t0 + 2], keys[b, :n].cpu(), w[b].cpu(), p["ks"][b])
+        have = got[t0:t0 + 2, :n].cpu()
+        assert torch.equal(have.isnan(), want.isnan()) and torch.equal(have.isinf(), want.isinf())
+
+
 # ---------------------------------------------------------------------------
 # selection
 # ---------------------------------------------------------------------------
