@@ -20,8 +20,8 @@
 // slice; histograms and counts are added up through distributed shared memory,
 // and the cluster's first CTA searches the list.
 //
-// Measured on one GB300: 32 rows of 32768, k 512: 9.0 us; one row of 600001, k
-// 2048: 17.5 us; 2048 causal rows of up to 8192, k 1024: 33.5 us (1.75 TB/s);
+// Measured on one GB300: 32 rows of 32768, k 512: 8.7 us; one row of 600001, k
+// 2048: 17.4 us; 2048 causal rows of up to 8192, k 1024: 32.5 us (1.8 TB/s);
 // 2048 causal rows of up to 16384 in blocks of 64, k 32: 33 us (3.8 TB/s).
 // Loading and counting take about two thirds of the last two, some fifteen block
 // barriers with little work between them the rest, and the many small passes'
@@ -293,10 +293,10 @@ __device__ __forceinline__ void pool_chunk(const float *src, int lane, Store sto
 }
 
 // POOLED: blocks of several scores.
-// CTAs of at most 256 threads work on many short rows: fewer bins, and registers for four of 256 threads (pooled, whose
-// loads are most of the work: five) to share an SM.
+// CTAs of at most 256 threads work on many short rows: fewer bins, and registers for five of 256 threads to share an
+// SM (2048 rows of up to 8192: 32.4 us with four loads ahead, with eight, which spill, 33.9; four CTAs and eight 33.4).
 template <int NT, bool CACHED, bool POOLED>
-__global__ void __launch_bounds__(NT, NT > 256 ? 1 : (POOLED ? 1280 : 1024) / NT) sfm_topk_kernel(const TopkArgs a)
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(const TopkArgs a)
 {
     constexpr int NW = NT / 32;
     constexpr int kTop = NT <= 256 ? 11 : 12, kMine = 1 << kTop;       // bits of the first digit, bins
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : (POOLED ? 1280 : 1024) / NT
     const int C = a.cluster;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = C > 1 ? (int)cluster.block_rank() : 0;
-    const int64_t r = blockIdx.x / (unsigned)C;
+    const int64_t r = (gridDim.x - 1 - blockIdx.x) / (unsigned)C;    // a prompt's longest rows first
     const float *row = a.scores + r * a.stride;
     int32_t *out = a.out + r * a.k;
 
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : (POOLED ? 1280 : 1024) / NT
             count(w.z);
             count(w.w);
         };
-        constexpr int kAhead = NT > 512 ? 4 : 8;
+        constexpr int kAhead = 4;
         for (int q0 = 0; q0 < quads; q0 += kAhead * NT) {
             float4 v[kAhead];
 #pragma unroll
