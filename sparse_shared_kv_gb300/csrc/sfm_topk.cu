@@ -78,7 +78,8 @@ struct ClusterShared {
     uint32_t total[kBins];                     // the cluster's histogram
     uint32_t list[kBins];
     uint32_t above[kMaxCluster], equal[kMaxCluster];   // selected keys per CTA
-    uint32_t list_n, list_base;
+    uint32_t list_base[kMaxCluster];           // where this CTA's keys go in each CTA's list
+    uint32_t list_n;
 };
 
 constexpr int kMaxDynamic = kMaxSlice * 4 + kMaxSlice / 4 + (int)sizeof(ClusterShared);
@@ -552,15 +553,13 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
         }
         if (in_bin > (uint32_t)kMine) continue;
 
-        // ---- the list of the keys in the bin, in the cluster's first CTA ----
-        uint32_t *to = sh.hist;                   // one CTA: the list takes the histogram's place
-        if (tid == 0) {
-            sh.list_n = 0;
-            if (C > 1)                            // where this CTA's keys go: one remote addition
-                cs.list_base = atomicAdd(cluster.map_shared_rank(&cs.list_n, 0), sh.hist[prefix & ((1u << bits_n) - 1)]);
-        }
+        // ---- the list of the keys in the bin, in the histogram's place.  Every CTA of a cluster gets all CTAs' lists and
+        // searches for itself: one that searches and tells the others costs one more barrier ----
+        if (tid == 0) sh.list_n = 0;
+        if (tid < C && C > 1)                     // where this CTA's keys go
+            cs.list_base[tid] = atomicAdd(cluster.map_shared_rank(&cs.list_n, tid), sh.hist[prefix & ((1u << bits_n) - 1)]);
         __syncthreads();
-        if (C > 1) to = cluster.map_shared_rank(cs.list, 0) + cs.list_base;
+        uint32_t *to = sh.hist;
         if (CACHED) {
             listed = true;
             const uint32_t from = prefix << shift, width = 1u << shift;
@@ -587,15 +586,16 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
                 if ((key >> shift) == prefix) to[atomicAdd(&sh.list_n, 1u)] = key;
             }
         }
-        if (C > 1) cluster.sync(); else __syncthreads();
-        if (rank == 0) {
-            search_list<NT, kMine>(sh, C > 1 ? cs.list : sh.hist, in_bin, shift, prefix, need);
-            if (tid > 0 && tid < C) {
-                *cluster.map_shared_rank(&sh.threshold, tid) = sh.threshold;
-                *cluster.map_shared_rank(&sh.take_equal, tid) = sh.take_equal;
+        __syncthreads();
+        if (C > 1) {
+            const int n = (int)sh.list_n;
+            for (int q = warp; q < C; q += NW) {
+                uint32_t *there = cluster.map_shared_rank(cs.list, q) + cs.list_base[q];
+                for (int i = lane; i < n; i += 32) there[i] = to[i];
             }
+            cluster.sync();
         }
-        if (C > 1) cluster.sync();
+        search_list<NT, kMine>(sh, C > 1 ? cs.list : sh.hist, in_bin, shift, prefix, need);
         threshold = sh.threshold;
         take_equal = sh.take_equal;
         break;
