@@ -13,11 +13,11 @@
 // cache's format.
 //
 // Measured on one GB300: 16381 rows of 512 values, normed, rotated and stored as
-// bf16: 9.3 us (3.6 TB/s), 131072 index rows of 128 values to E4M3: 16.7 us
-// (3.0 TB/s), 441488 such rows normed: 56 us (3.0 TB/s), where instructions
-// bound it more than memory; 64 packed rows: 2.8 us, latency.  Eight lanes per row with sixteen values
-// each need fewer shuffles but spill the half layout's cosines: 48 us for the
-// 441488 rows, but 24.6 for the 131072, so sixteen it is.
+// bf16: 9.3 us (3.6 TB/s); 131072 index rows of 128 values to E4M3: 16.5 us (3.0
+// TB/s) and 441488 such rows, normed, 50 us (3.4 TB/s), where instructions bound
+// it more than memory; 64 packed rows: 2.8 us, latency.  Eight lanes per row with
+// sixteen values each need fewer shuffles but spill the half layout's cosines:
+// better by a fifth on the 441488 rows, worse by a fifth on the 131072.
 #include <math.h>
 
 #include "sfm_internal.cuh"
@@ -146,6 +146,12 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
             c[e + 1] = make_float2(two.z, minus ? -two.w : two.w);
         }
     };
+    // one step per row: a lane's weights stay in registers too (441488 rows: 55.8 -> 50.1 us)
+    float weight[8];
+    if (STEPS == 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) weight[e] = a.weight && lane * 8 < a.norm_dim ? __ldg(a.weight + lane * 8 + e) : 1.f;
+    }
     int last_token = -1;
     const int32_t left = (int32_t)(r1 - r0);     // zero or less: nothing to do for this group
     for (int32_t i = 0; i < (int32_t)per; ++i) { // every group runs the same count: warp collectives inside
@@ -187,7 +193,10 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
             for (int s = 0; s < STEPS; ++s) {
                 const int at = (s * LANES + lane) * 8;
                 if (at < a.norm_dim) {
-                    if (a.weight) {
+                    if (STEPS == 1) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[s][e] = v[s][e] * rs * weight[e];
+                    } else if (a.weight) {
                         const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight + at));
                         const float4 w1 = __ldg(reinterpret_cast<const float4 *>(a.weight + at + 4));
                         const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -243,10 +252,12 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
                 } else {
                     const int away = at >= pairs ? -pairs : pairs;       // to the partner
                     const int from = (tid & 31) + (in ? away / 8 : 0);
+                    float other[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float other = ROPE == 2 ? __shfl_sync(0xffffffffu, x[e], from) : turn[at + away + e];
-                        if (in) x[e] = fmaf(x[e], c[e % kOwn].x, other * c[e % kOwn].y);
+                    for (int e = 0; e < 8; ++e) other[e] = ROPE == 2 ? __shfl_sync(0xffffffffu, x[e], from) : turn[at + away + e];
+                    if (in) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], c[e % kOwn].x, other[e] * c[e % kOwn].y);
                     }
                 }
             };
