@@ -18,10 +18,10 @@
 // cluster of CTAs that works on it (one CTA for the many rows of a prompt, up
 // to 16 for the long rows of a few requests), each CTA holding a contiguous
 // slice; histograms and counts are added up through distributed shared memory,
-// and the cluster's first CTA searches the list.
+// and every CTA searches the list of all.
 //
-// Measured on one GB300: 32 rows of 32768, k 512: 8.7 us; one row of 600001, k
-// 2048: 17.4 us; 2048 causal rows of up to 8192, k 1024: 32.5 us (1.8 TB/s);
+// Measured on one GB300: 32 rows of 32768, k 512: 8.5 us; one row of 600001, k
+// 2048: 17.4 us; 2048 causal rows of up to 8192, k 1024: 31.9 us (1.8 TB/s);
 // 2048 causal rows of up to 16384 in blocks of 64, k 32: 33 us (3.8 TB/s).
 // Loading and counting take about two thirds of the last two, some fifteen block
 // barriers with little work between them the rest, and the many small passes'
