@@ -263,6 +263,44 @@ def test_store(case, dt, tokens):
             assert bool((scales[left.cuda()] == 9.0).all())
 
 
+MANY_ROWS = [      # format, dim, rot, offset, interleaved, heads, tokens
+    ("rows", 128, 64, 0, False, 64, 701), ("rows", 128, 64, 64, True, 5, 9001), ("rows", 512, 64, 0, False, 3, 7001),
+    ("plain", 48, 16, 8, False, 7, 9001), ("plain", 512, 64, 448, True, 1, 20011), ("plain", 272, 32, 240, False, 2, 9001),
+    ("plain", 512, 512, 0, False, 2, 6001), ("int8", 576, 64, 512, False, 1, 12007), ("fp8", 512, 0, 0, True, 1, 12007),
+    ("fp8", 576, 64, 512, True, 1, 12007),
+]
+
+
+@pytest.mark.parametrize("case", MANY_ROWS, ids=str)
+def test_store_many_rows_as_in_pieces(case):
+    """Rows that one group of lanes works on one after the other hold what they hold when each has its own."""
+    fmt, D, rot, off, inter, H, tokens = case
+    g = torch.Generator(device="cuda").manual_seed(D + H)
+    dtype = torch.bfloat16
+    wide = torch.randn(tokens, H + 1, D + 16, generator=g, device="cuda").to(dtype)
+    x = wide[:, :H, 8:8 + D]
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda").to(torch.int32)
+    f = sfm.rope_frequencies(rot, device="cuda")[0] if rot else None
+    w = 1 + 0.2 * torch.randn(min(D, 512), generator=g, device="cuda")
+    slots = torch.randperm(tokens, generator=g, device="cuda").to(torch.int32)
+    slots[::13] = -1
+    rows = (tokens - 5) * H + H // 2                 # a few slots lie outside, one with some of its heads
+    got = []
+    for piece in (tokens, 97):
+        raw, cache = make_cache(fmt, rows, D, dtype, pad=16)
+        scales = torch.full((rows,), 9.0, device="cuda") if fmt == "rows" else None
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, tokens, piece):
+            e = min(i + piece, tokens)
+            sfm.store_kv(x[i:e], cache, slot_mapping=slots[i:e], kv_format=FORMATS[fmt], norm_weight=w, norm_eps=1e-5,
+                         positions=pos[i:e] if rot else None, inv_freq=f, rope_offset=off if rot else None,
+                         interleaved=inter, scales=scales, status=status)
+        got.append((raw, scales, int(status)))
+    (raw, scales, status), (raw1, scales1, status1) = got
+    assert status == status1 == sfm.STATUS_BAD_BLOCK
+    assert torch.equal(raw, raw1) and (scales is None or torch.equal(scales, scales1))
+
+
 @pytest.mark.parametrize("fmt,D", [("plain", 512), ("int8", 576), ("fp8", 512), ("rows", 128)])
 def test_store_slots_outside_the_cache(fmt, D):
     g = gen(3)
