@@ -99,6 +99,25 @@ def test_rope(shape, inter, dt):
         assert torch.equal(z, y)
 
 
+@pytest.mark.parametrize("shape", [(100003, 8, 64, 16, 48), (40009, 17, 64, 64, 0), (1301, 64, 512, 64, 448), (3001, 200, 80, 48, 16)],
+                         ids=str)
+@pytest.mark.parametrize("inter", [True, False], ids=["pairs", "halves"])
+def test_rope_many_rows_as_in_pieces(shape, inter):
+    """Tokens that one block works on one after the other turn as they do alone."""
+    T, H, D, rot, off = shape
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, H + 1, D, generator=g, device="cuda").to(torch.bfloat16)[:, :H]
+    pos = torch.randint(-(1 << 31), (1 << 31) - 1, (T,), generator=g, device="cuda").to(torch.int32)
+    f, _ = sfm.rope_frequencies(rot, device="cuda")
+    kw = dict(rope_offset=off, interleaved=inter, inverse=True, amplitude=1.25)
+    y = sfm.apply_rope(x, pos, f, **kw)
+    for i in range(0, T, max(T // 64, 1)):
+        e = min(i + max(T // 64, 1), T)
+        assert torch.equal(y[i:e], sfm.apply_rope(x[i:e], pos[i:e], f, **kw))
+    some = slice(T // 2, T // 2 + 40)
+    rope_check(y[some], x[some], pos[some], f, off, inter, True, 1.25)
+
+
 @pytest.mark.parametrize("inter", [True, False], ids=["pairs", "halves"])
 def test_rope_strided_views(inter):
     g = gen(5)
