@@ -38,7 +38,7 @@
 // 25 us, 4.3 TB/s, bound by reading the keys but for some 5 us of starting;
 // 2048 queries of 64 heads over 8192 bf16 keys: 163 us, 1.47 PFLOP/s (75 % of
 // what a library product reaches), bound by the clipped sums beside the matrix
-// products (133 us without them); four short sequences: 5.9 us, latency.  Taken
+// products (133 us without them); four short sequences: 5.6 us, latency.  Taken
 // out because slower on the 2048 queries: weights in registers with 192 columns
 // and twelve warps (174-180 us), a register split (488), the next 32 columns
 // loaded during the sums (190), 64 columns at once (176).
@@ -399,6 +399,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             *reinterpret_cast<uint4 *>(gbase + i) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
+    // (no early start of dependents: `visible` may be a length tensor of the next call)
+    grid_dependency_wait();
     bool bad = false;
     if (warp == 17) {
         tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
@@ -755,7 +757,7 @@ cudaError_t launch(const IndexArgs &a, const CUtensorMap &q, const CUtensorMap &
             return cudaFuncSetAttribute(sfm_index_kernel<HP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
         },
         [&] {
-            return launch_plain(sfm_index_kernel<HP, FULL>, dim3((unsigned)grid), dim3(kThreads), smem, st, a, q, k);
+            return launch_dependent(sfm_index_kernel<HP, FULL>, dim3((unsigned)grid), dim3(kThreads), smem, st, a, q, k);
         });
 }
 

@@ -346,6 +346,16 @@ __device__ __forceinline__ void grid_launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The kernels around the attention do the first thing after the second: what a
+// dependent of theirs (the planner's length loads) reads before it waits is
+// then older than their own predecessors.  Between calls of one operator this
+// saves 0.2 to 0.8 us (the selection of a decode batch: 8.5 -> 7.7 us).
+__device__ __forceinline__ void grid_follow()
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+}
+
 template <typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                     Args... args)
@@ -360,19 +370,6 @@ inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 blo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// An ordinary launch that reports its own error alone (the runtime's last error
-// may be another call's).
-template <typename... Args>
-inline cudaError_t launch_plain(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

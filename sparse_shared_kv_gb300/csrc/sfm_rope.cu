@@ -9,8 +9,8 @@
 // fp32 and stored, one rounding per value.
 //
 // Measured on one GB300: 4093 tokens of 128 heads of 512 values with 64 of them
-// rotated, half layout: 170 us, 6.3 TB/s; 18676 of 64 heads of 128 values: 112
-// us; a decode batch of 32 tokens: 2.8 us, latency.
+// rotated, half layout: 169 us, 6.3 TB/s; 18676 of 64 heads of 128 values: 112
+// us; a decode batch of 32 tokens: 2.6 us, latency.
 #include <math.h>
 
 #include "sfm_internal.cuh"
@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kThreads, 4) sfm_rope_rows_kernel(RopeArgs a)
     __shared__ float2 cs[kMaxPairs + kMaxPairs / kPer];   // lanes' reads of their e-th pairs meet in no bank
     extern __shared__ unsigned long long step[];          // [rot / 2]
     const int tid = threadIdx.x, half = a.rot / 2;
+    grid_follow();
     const int64_t end = min((int64_t)a.tokens, ((int64_t)blockIdx.x + 1) * a.span_tokens);
     bool fresh = true;                                    // the steps are still to come
     for (int64_t t0 = (int64_t)blockIdx.x * a.span_tokens; t0 < end; t0 += a.block_tokens) {
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(kThreads) sfm_rope_kernel(RopeArgs a)
     __shared__ float2 cs[kMaxPairs];
 
     const int tid = threadIdx.x;
+    grid_follow();
     const int64_t t0 = (int64_t)blockIdx.x * a.block_tokens;
     const int ntok = (int)min((int64_t)a.block_tokens, a.tokens - t0);
     const int first = blockIdx.y * kBlockUnits;
@@ -223,13 +225,13 @@ bool rows_overlap(int64_t tokens, int64_t token_stride, int64_t heads, int64_t h
 template <typename T, int VEC, bool HALF>
 cudaError_t launch(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    return launch_plain(sfm_rope_kernel<T, VEC, HALF>, grid, dim3(kThreads), 0, st, a);
+    return launch_dependent(sfm_rope_kernel<T, VEC, HALF>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <typename T, bool HALF>
 cudaError_t launch_rows(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
-    return launch_plain(sfm_rope_rows_kernel<T, HALF>, grid, dim3(kThreads), (size_t)a.rot / 2 * 8, st, a);
+    return launch_dependent(sfm_rope_rows_kernel<T, HALF>, grid, dim3(kThreads), (size_t)a.rot / 2 * 8, st, a);
 }
 
 template <typename T>

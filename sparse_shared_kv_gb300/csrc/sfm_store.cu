@@ -13,9 +13,9 @@
 // cache's format.
 //
 // Measured on one GB300: 16381 rows of 512 values, normed, rotated and stored as
-// bf16: 9.3 us (3.6 TB/s); 131072 index rows of 128 values to E4M3: 16.5 us (3.0
+// bf16: 8.7 us (3.9 TB/s); 131072 index rows of 128 values to E4M3: 15.9 us (3.2
 // TB/s) and 441488 such rows, normed, 50 us (3.4 TB/s), where instructions bound
-// it more than memory; 64 packed rows: 2.8 us, latency.  Eight lanes per row with
+// it more than memory; 64 packed rows: 2.6 us, latency.  Eight lanes per row with
 // sixteen values each need fewer shuffles but spill the half layout's cosines:
 // better by a fifth on the 441488 rows, worse by a fifth on the 131072.
 #include <math.h>
@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
     extern __shared__ float turn_all[];          // ROPE 3: [kGroups][rot]
 
     const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
+    grid_follow();
     float2 *cs = cs_all[group];
     float *turn = turn_all + group * a.rot;
     const int pairs = ROPE ? a.rot / 2 : 0;
@@ -350,7 +351,7 @@ cudaError_t launch(const StoreArgs &a, cudaStream_t st)
                                 : form == 1 ? sfm_store_kernel<T, FORMAT, LANES, STEPS, 1>
                                 : form == 2 ? sfm_store_kernel<T, FORMAT, LANES, STEPS, 2>
                                             : sfm_store_kernel<T, FORMAT, LANES, STEPS, 3>;
-    return launch_plain(kernel, dim3(grid), dim3(kThreads), smem, st, a);
+    return launch_dependent(kernel, dim3(grid), dim3(kThreads), smem, st, a);
 }
 
 template <typename T>

@@ -20,9 +20,9 @@
 // slice; histograms and counts are added up through distributed shared memory,
 // and every CTA searches the list of all.
 //
-// Measured on one GB300: 32 rows of 32768, k 512: 8.5 us; one row of 600001, k
-// 2048: 17.4 us; 2048 causal rows of up to 8192, k 1024: 31.9 us (1.8 TB/s);
-// 2048 causal rows of up to 16384 in blocks of 64, k 32: 33 us (3.8 TB/s).
+// Measured on one GB300: 32 rows of 32768, k 512: 7.7 us; one row of 600001, k
+// 2048: 16.7 us; 2048 causal rows of up to 8192, k 1024: 31.4 us (1.9 TB/s);
+// 2048 causal rows of up to 16384 in blocks of 64, k 32: 32.5 us (3.9 TB/s).
 // Loading and counting take about two thirds of the last two, some fifteen block
 // barriers with little work between them the rest, and the many small passes'
 // instructions (50 per 32 keys) more than memory bound the rows of 8192.  Rows
@@ -315,6 +315,17 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
     const float *row = a.scores + r * a.stride;
     int32_t *out = a.out + r * a.k;
 
+    auto clear = [&](uint32_t *words, int n) {
+        for (int i = tid; i < n / 4; i += NT) reinterpret_cast<uint4 *>(words)[i] = make_uint4(0, 0, 0, 0);
+    };
+    clear(sh.hist, kMine);
+    if (C > 1) {
+        clear(cs.total, kBins);
+        if (tid == 0) cs.list_n = 0;
+        cluster.barrier_arrive();             // zeros before anyone adds to them: waited for below
+    }
+    grid_follow();
+
     int len = a.n;
     if (a.lengths) {
         len = __ldg(a.lengths + r);
@@ -330,17 +341,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
     const int cnt = min(per, have - base);
     const int last_from = have - a.last;
     const bool any_forced = a.first | a.last;
-
-    auto clear = [&](uint32_t *words, int n) {
-        for (int i = tid; i < n / 4; i += NT) reinterpret_cast<uint4 *>(words)[i] = make_uint4(0, 0, 0, 0);
-    };
-    clear(sh.hist, kMine);
-    if (C > 1) {
-        clear(cs.total, kBins);
-        if (tid == 0) cs.list_n = 0;
-        cluster.barrier_arrive();             // zeros before anyone adds to them: waited for below
-    }
-    __syncthreads();
+    __syncthreads();                              // the zeros are there
 
     auto forced = [&](int j) { return any_forced && (j < a.first || j >= last_from); };
     auto key_at = [&](int i) -> uint32_t {
@@ -714,12 +715,14 @@ cudaError_t launch(const TopkArgs &a, int device, int64_t rows, size_t smem, cud
             cfg.blockDim = dim3(NT);
             cfg.dynamicSmemBytes = smem;
             cfg.stream = st;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = (unsigned)a.cluster;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = (unsigned)a.cluster;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
             cfg.attrs = attr;
-            cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+            cfg.numAttrs = a.cluster > 1 ? 2 : 1;
             return cudaLaunchKernelEx(&cfg, kernel, a);
         });
 }

@@ -656,6 +656,58 @@ def test_topk_short_lengths_in_long_rows(n, k, first, last):
 
 
 # ---------------------------------------------------------------------------
+# calls behind each other: a kernel may be set up while the one before it runs
+# ---------------------------------------------------------------------------
+def test_calls_read_what_the_calls_before_them_wrote():
+    """Every call's inputs are the outputs of the calls right before it; the same buffers hold other values each time."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    B, n, D, heads, block, k = 8, 700, 128, 64, 64, 96
+    f, _ = sfm.rope_frequencies(64, device="cuda")
+    x = torch.randn(B * n, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    q0 = torch.randn(B, heads, D, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand(B, heads, generator=g, device="cuda")
+    pos = torch.arange(B * n, dtype=torch.int32, device="cuda")
+    ones = torch.ones(B, dtype=torch.int32, device="cuda")
+    pages = -(-n // block)
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    slots = (torch.arange(B * n, device="cuda") // n * pages * block + torch.arange(B * n, device="cuda") % n).to(torch.int32)
+
+    def run(between):
+        rows, queries = x.clone(), q0.clone()
+        cache = torch.zeros(B * pages, block, D, dtype=torch.bfloat16, device="cuda")
+        out = torch.zeros(B, n, device="cuda")
+        seen = torch.zeros(B, dtype=torch.int32, device="cuda")
+        lens = torch.full((B,), n - 40, dtype=torch.int32, device="cuda")
+        picked = torch.zeros(B, k, dtype=torch.int32, device="cuda")
+        past = []
+        torch.cuda.synchronize()
+        for i in range(24):
+            sfm.apply_rope(rows, pos, f, out=rows, interleaved=i % 2 == 0)
+            between()
+            sfm.store_kv(rows[:, 0], cache, slot_mapping=slots)
+            between()
+            sfm.apply_rope(queries, lens, f, out=queries, inverse=i % 3 == 0)
+            between()
+            sfm.index_scores(queries.view(B, 1, heads, D), cache, w.view(B, 1, heads), max_seqlen_kv=n, block_table=table,
+                             seqused_kv=lens, layout_kv="PAGED", out=out, visible=seen)
+            between()
+            sfm.select_topk(out, k, lengths=seen, out=picked)
+            between()
+            sfm.index_scores(queries.view(B, 1, heads, D), cache, w.view(B, 1, heads), max_seqlen_kv=n, block_table=table,
+                             seqused_kv=seen, layout_kv="PAGED", out=out, visible=lens)
+            between()
+            lens.add_(ones)
+            between()
+            past.append(picked.clone())
+        torch.cuda.synchronize()
+        return [rows, queries, cache, out, seen, lens, torch.stack(past)]
+    apart = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(run(lambda: None), apart):
+            assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
 # offsets past 32 bits
 # ---------------------------------------------------------------------------
 def test_far_offsets():
