@@ -18,11 +18,13 @@
 // cluster of CTAs that works on it (one CTA for the many rows of a prompt, up
 // to 16 for the long rows of a few requests), each CTA holding a contiguous
 // slice; histograms and counts are added up through distributed shared memory,
-// and every CTA searches the list of all.
+// and every CTA searches the list of all.  Where rows that no CTA can hold are
+// many, each has one CTA that reads it twice and holds the marks alone.
 //
 // Measured on one GB300: 32 rows of 32768, k 512: 7.5 us; one row of 600001, k
 // 2048: 15.8 us; 2048 causal rows of up to 8192, k 1024: 29.9 us (2.0 TB/s);
-// 2048 causal rows of up to 16384 in blocks of 64, k 32: 32.2 us (3.9 TB/s).
+// 2048 causal rows of up to 16384 in blocks of 64, k 32: 32.2 us (3.9 TB/s);
+// 529 causal rows of up to 63406, k 512: 79 us (1.7 TB/s).
 // Loading and counting take about two thirds of the last two, some fifteen block
 // barriers with little work between them the rest, and the many small passes'
 // instructions (50 per 32 keys) more than memory bound the rows of 8192.  Rows
@@ -43,6 +45,8 @@ namespace {
 constexpr int kBins = 4096;                    // of a cluster's histogram
 constexpr int kMaxCluster = 16;
 constexpr int kMaxSlice = 40448;               // keys of a CTA: 158 KB and 10 KB of bits
+constexpr int kMaxStream = 1 << 19;            // scores of a row that is read twice: 128 KB of bits
+enum { kRecompute, kCached, kStreamed };       // where a CTA's keys are: nowhere, in shared memory, in the row itself
 constexpr uint32_t kForced = 0xffffffffu;
 constexpr uint32_t kLeast = 0x00800000u;       // the least key of a score: below it there is none
 
@@ -306,10 +310,11 @@ __device__ __forceinline__ void pool_chunk(const float *src, int lane, Store sto
 // POOLED: blocks of several scores.
 // CTAs of at most 256 threads work on many short rows: fewer bins, and registers for five of 256 threads to share an
 // SM (2048 rows of up to 8192: 32.4 us with four loads ahead, with eight, which spill, 33.9; four CTAs and eight 33.4).
-template <int NT, bool CACHED, bool POOLED>
-__global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(const TopkArgs a)
+template <int NT, int MODE, bool POOLED>
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 + (MODE == kStreamed) : 1280 / NT) sfm_topk_kernel(const TopkArgs a)
 {
     constexpr int NW = NT / 32;
+    constexpr bool CACHED = MODE == kCached, STREAMED = MODE == kStreamed, kBits = CACHED || STREAMED;
     constexpr int kTop = NT <= 256 ? 11 : 12, kMine = 1 << kTop;       // bits of the first digit, bins
     __shared__ Shared<kMine> sh;
     extern __shared__ __align__(16) uint32_t keys[];
@@ -379,19 +384,54 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
         atomicAdd(&sh.hist[min((max(key, near) - near) >> bin_shift, (uint32_t)kMine - 1)], 1u);
     };
 
+    // four scores of the row
+    auto load4 = [&](int q) {
+        const float *at = row + base + 4 * q;
+        return a.aligned ? __ldg(reinterpret_cast<const float4 *>(at))
+                         : make_float4(__ldg(at), __ldg(at + 1), __ldg(at + 2), __ldg(at + 3));
+    };
+    auto keys4 = [&](int q, const float4 &v) {
+        uint4 w = make_uint4(key_of(v.x), key_of(v.y), key_of(v.z), key_of(v.w));
+        if (any_forced) {
+            const int j = base + 4 * q;
+            if (forced(j)) w.x = kForced;
+            if (forced(j + 1)) w.y = kForced;
+            if (forced(j + 2)) w.z = kForced;
+            if (forced(j + 3)) w.w = kForced;
+        }
+        return w;
+    };
+
     // ---- keys, and their histogram ---------------------------------------------------
-    if (CACHED && !POOLED && a.aligned) {
+    if (STREAMED) {
+        const int quads = cnt >> 2;
+        constexpr int kAhead = 4;
+        for (int q0 = 0; q0 < quads; q0 += kAhead * NT) {
+            float4 v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int q = q0 + i * NT + tid;
+                v[i] = q < quads ? load4(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (q0 == 0) look(tid < quads ? key_of(fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w))) : 0u);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (q0 + i * NT + tid < quads) {
+                    const uint4 w = keys4(q0 + i * NT + tid, v[i]);
+                    count(w.x);
+                    count(w.y);
+                    count(w.z);
+                    count(w.w);
+                }
+            }
+        }
+        const int i = (quads << 2) + tid;
+        if (i < cnt) count(key_at(i));
+    } else if (CACHED && !POOLED && a.aligned) {
         const float4 *src = reinterpret_cast<const float4 *>(row + base);
         const int quads = cnt >> 2;
         auto quad = [&](int q, const float4 &v) {
-            uint4 w = make_uint4(key_of(v.x), key_of(v.y), key_of(v.z), key_of(v.w));
-            if (any_forced) {
-                const int j = base + 4 * q;
-                if (forced(j)) w.x = kForced;
-                if (forced(j + 1)) w.y = kForced;
-                if (forced(j + 2)) w.z = kForced;
-                if (forced(j + 3)) w.w = kForced;
-            }
+            const uint4 w = keys4(q, v);
             reinterpret_cast<uint4 *>(keys)[quad_at(q)] = w;
             count(w.x);
             count(w.y);
@@ -490,20 +530,50 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
     // each warp's part of the slice, in order: 16 neighbouring keys per lane and step
     const int seg = ((cnt + NW - 1) / NW + 511) & ~511;
     const int s0 = min(warp * seg, cnt), s1 = min(s0 + seg, cnt);
+    // (streamed: 16 keys that are four quads, 128 keys apart, so that a warp reads the row in order)
     auto read16 = [&](int i0, auto use) {
+        if constexpr (STREAMED) {
+            float4 v[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint4 w = reinterpret_cast<const uint4 *>(keys)[quad_at((i0 >> 2) + 4 * lane + g)];
-            use(4 * g, w.x);
-            use(4 * g + 1, w.y);
-            use(4 * g + 2, w.z);
-            use(4 * g + 3, w.w);
+            for (int g = 0; g < 4; ++g) {
+                const int q = (i0 >> 2) + 32 * g + lane;
+                v[g] = 4 * q + 3 < s1 ? load4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int q = (i0 >> 2) + 32 * g + lane;
+                uint4 w = keys4(q, v[g]);
+                if (4 * q < s1 && 4 * q + 3 >= s1) {       // the row's last quad
+                    w.x = key_at(4 * q);
+                    if (4 * q + 1 < s1) w.y = key_at(4 * q + 1);
+                    if (4 * q + 2 < s1) w.z = key_at(4 * q + 2);
+                }
+                use(4 * g, w.x);
+                use(4 * g + 1, w.y);
+                use(4 * g + 2, w.z);
+                use(4 * g + 3, w.w);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint4 w = reinterpret_cast<const uint4 *>(keys)[quad_at((i0 >> 2) + 4 * lane + g)];
+                use(4 * g, w.x);
+                use(4 * g + 1, w.y);
+                use(4 * g + 2, w.z);
+                use(4 * g + 3, w.w);
+            }
         }
     };
     auto valid16 = [&](int i0) -> uint32_t {      // keys of this lane that exist
-        const int n = s1 - (i0 + 16 * lane);
-        return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1;
+        if (i0 + 512 <= s1) return 0xffffu;
+        auto low = [](int n) -> uint32_t { return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1; };
+        if constexpr (!STREAMED) return low(s1 - (i0 + 16 * lane));
+        uint32_t m = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) m |= low(min(s1 - (i0 + 128 * g + 4 * lane), 4)) << (4 * g);
+        return m;
     };
+    auto place = [&](int i0, int e) { return STREAMED ? i0 + 128 * (e >> 2) + 4 * lane + (e & 3) : i0 + 16 * lane + e; };
     auto scan = [&](uint32_t v) {                 // sums over the lanes up to this one
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -571,7 +641,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
             cs.list_base[tid] = atomicAdd(cluster.map_shared_rank(&cs.list_n, tid), sh.hist[prefix & ((1u << bits_n) - 1)]);
         __syncthreads();
         uint32_t *to = sh.hist;
-        if (CACHED) {
+        if (kBits) {
             listed = true;
             const uint32_t from = prefix << shift, last = from + ((1u << shift) - 1);
             for (int i0 = s0; i0 < s1; i0 += 512) {
@@ -590,12 +660,16 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
                 uint32_t at = 0;
                 if (lane == 31 && upto) at = atomicAdd(&sh.list_n, upto);
                 at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
-                for (; in; in &= in - 1) to[at++] = key_at(i0 + 16 * lane + __ffs(in) - 1);
+                for (; in; in &= in - 1, ++at)
+                    if (CACHED || at < (uint32_t)kMine) to[at] = key_at(place(i0, __ffs(in) - 1));
             }
         } else {
             for (int i = tid; i < cnt; i += NT) {
                 const uint32_t key = key_at(i);
-                if ((key >> shift) == prefix) to[atomicAdd(&sh.list_n, 1u)] = key;
+                if ((key >> shift) == prefix) {
+                    const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                    if (at < (uint32_t)kMine) to[at] = key;
+                }
             }
         }
         __syncthreads();
@@ -616,7 +690,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
     // ---- the selected indices, ascending ------------------------------------------
     // bits: above the threshold, and (upper half) equal to it where ties matter
     uint32_t n_above = 0, n_equal = 0;
-    if (CACHED) {
+    if (kBits) {
         for (int i0 = s0; i0 < s1; i0 += 512) {
             uint32_t m = 0;
             if (listed) {                         // only the keys in the digit are still open
@@ -624,7 +698,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
                 m = was & 0xffffu;
                 for (uint32_t in = was >> 16; in; in &= in - 1) {
                     const int e = __ffs(in) - 1;
-                    const uint32_t key = key_at(i0 + 16 * lane + e);
+                    const uint32_t key = key_at(place(i0, e));
                     m |= (uint32_t)(key > threshold) << e | (uint32_t)(take_equal && key == threshold) << (16 + e);
                 }
             } else {
@@ -673,7 +747,34 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
             }
         }
     }
-    if (CACHED) {
+    if (STREAMED) {
+        auto four = [](uint32_t m) {              // the quads' numbers of marks, a byte each
+            return (uint32_t)(__popc(m & 0xfu) | __popc(m & 0xf0u) << 8 | __popc(m & 0xf00u) << 16 | __popc(m & 0xf000u) << 24);
+        };
+        for (int i0 = s0; i0 < s1; i0 += 512) {
+            const uint32_t m = bits[(i0 >> 4) + lane];
+            const uint32_t up = four(m), up_to = scan(up), ups = __shfl_sync(0xffffffffu, up_to, 31);
+            uint32_t eq = 0, eq_to = 0, eqs = 0;
+            if (take_equal) {
+                eq = four(m >> 16);
+                eq_to = scan(eq);
+                eqs = __shfl_sync(0xffffffffu, eq_to, 31);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t at = before_above + ((up_to - up) >> (8 * g) & 0xffu), mine = m >> (4 * g) & 0xfu;
+                before_above += ups >> (8 * g) & 0xffu;
+                if (take_equal) {
+                    uint32_t room = before_equal + ((eq_to - eq) >> (8 * g) & 0xffu);
+                    at += min(room, take_equal);
+                    before_equal += eqs >> (8 * g) & 0xffu;
+                    for (uint32_t e = m >> (16 + 4 * g) & 0xfu; e && room < take_equal; e &= e - 1, ++room) mine |= e & -e;
+                }
+                for (; mine; mine &= mine - 1, ++at)
+                    if (at < (uint32_t)a.k) out[at] = base + place(i0, 4 * g + __ffs(mine) - 1);
+            }
+        }
+    } else if (CACHED) {
         for (int i0 = s0; i0 < s1; i0 += 512) {
             uint32_t m = bits[(i0 >> 4) + lane];
             uint32_t e = m >> 16;
@@ -699,7 +800,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
             const uint32_t ea = before_equal + __popc(me & below);
             if (up || (eq && ea < take_equal)) {
                 const uint32_t at = before_above + __popc(mu & below) + min(ea, take_equal);
-                out[at] = base + i;
+                if (at < (uint32_t)a.k) out[at] = base + i;
             }
             before_above += __popc(mu);
             before_equal += __popc(me);
@@ -709,11 +810,11 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 1280 / NT) sfm_topk_kernel(
     for (int64_t i = filled + rank * NT + tid; i < a.k; i += (int64_t)C * NT) out[i] = -1;
 }
 
-template <int NT, bool CACHED, bool POOLED>
+template <int NT, int MODE, bool POOLED>
 cudaError_t launch(const TopkArgs &a, int device, int64_t rows, size_t smem, cudaStream_t st)
 {
     static std::atomic<bool> ready[kMaxDevices];
-    auto kernel = sfm_topk_kernel<NT, CACHED, POOLED>;
+    auto kernel = sfm_topk_kernel<NT, MODE, POOLED>;
     return prepared_launch(
         ready, device,
         [&] {
@@ -773,31 +874,38 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     a.last = p.last_blocks;
     a.aligned = ((uintptr_t)scores & 15u) == 0 && p.score_stride % 4 == 0;
     const int64_t blocks = ((int64_t)p.n + p.block_size - 1) >> a.bs_log2;
+    // Rows that no CTA can hold, and enough of them for two thirds of the SMs: one CTA each, which reads its row twice
+    // (the second time from L2) and keeps the marks alone, beats a cluster that holds it: 529 rows of up to 63406 79
+    // us for 101, 256 of 131072 71 for 104, 152 of 60000 26 for 27, but 70 of 60000 24 for 12.  Rows of 32768, which
+    // a CTA holds: 68 for 65.
+    const bool pooled = a.bs_log2 > 0;
+    const bool streamed = !pooled && (int64_t)p.rows * 3 > (int64_t)sms * 2 && p.n > kMaxSlice && p.n <= kMaxStream;
     // CTAs of a row: as many as it takes to hold its keys, and while a CTA still
     // has some thousand keys twice as many, up to six sevenths of the SMs (the
     // CTAs of a cluster share a GPC, so clusters of eight do not fill them all):
     // 32 rows of 32768 with 4 CTAs a row 9.3 us, with 8 10.3 us, with 2 10.4 us
     int c = 1;
     auto slice = [&](int q) { return ((blocks + q - 1) / q + 127) / 128 * 128; };
-    while (c < kMaxCluster && (slice(c) > kMaxSlice || ((int64_t)p.rows * c * 14 <= (int64_t)sms * 6 && slice(c) > 4096))) c *= 2;
+    while (!streamed && c < kMaxCluster && (slice(c) > kMaxSlice || ((int64_t)p.rows * c * 14 <= (int64_t)sms * 6 && slice(c) > 4096))) c *= 2;
     if ((int64_t)p.rows * c > INT32_MAX) return SFM_ERR_UNSUPPORTED;
     a.cluster = c;
     const bool cached = slice(c) <= kMaxSlice;
-    a.slice_cap = cached ? (int32_t)((slice(c) + 511) / 512 * 512) : 0;
-    const size_t smem = (size_t)a.slice_cap * 4 + (size_t)a.slice_cap / 4 + (c > 1 ? sizeof(ClusterShared) : 0);
+    a.slice_cap = cached && !streamed ? (int32_t)((slice(c) + 511) / 512 * 512) : 0;
+    const size_t smem = streamed ? ((size_t)p.n + 511) / 512 * 128
+                                 : (size_t)a.slice_cap * 4 + (size_t)a.slice_cap / 4 + (c > 1 ? sizeof(ClusterShared) : 0);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    const bool pooled = a.bs_log2 > 0;
     // Threads: a short slice has few keys per thread, and many small CTAs hide each other's barriers (2048 x
     // 16384 scores in blocks of 64, 256 keys a row: 35 us with 256 threads, 33 with 128; 2690 x 1055 in blocks of
     // 16: 20.4 and 13.6).  Long slices want every lane that the SM has.
-    if (!cached) e = launch<1024, false, false>(a, dev, p.rows, smem, st);
+    if (streamed) e = launch<512, kStreamed, false>(a, dev, p.rows, smem, st);
+    else if (!cached) e = launch<1024, kRecompute, false>(a, dev, p.rows, smem, st);
     else if (slice(c) > 16384)
-        e = pooled ? launch<1024, true, true>(a, dev, p.rows, smem, st) : launch<1024, true, false>(a, dev, p.rows, smem, st);
+        e = pooled ? launch<1024, kCached, true>(a, dev, p.rows, smem, st) : launch<1024, kCached, false>(a, dev, p.rows, smem, st);
     else if (c > 1)
-        e = pooled ? launch<512, true, true>(a, dev, p.rows, smem, st) : launch<512, true, false>(a, dev, p.rows, smem, st);
+        e = pooled ? launch<512, kCached, true>(a, dev, p.rows, smem, st) : launch<512, kCached, false>(a, dev, p.rows, smem, st);
     else if (slice(c) > 2048)
-        e = pooled ? launch<256, true, true>(a, dev, p.rows, smem, st) : launch<256, true, false>(a, dev, p.rows, smem, st);
-    else e = pooled ? launch<128, true, true>(a, dev, p.rows, smem, st) : launch<128, true, false>(a, dev, p.rows, smem, st);
+        e = pooled ? launch<256, kCached, true>(a, dev, p.rows, smem, st) : launch<256, kCached, false>(a, dev, p.rows, smem, st);
+    else e = pooled ? launch<128, kCached, true>(a, dev, p.rows, smem, st) : launch<128, kCached, false>(a, dev, p.rows, smem, st);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }

@@ -641,6 +641,33 @@ def test_topk_rows_that_mislead_a_sample(rows, n, k):
             assert torch.equal(got, torch.where(want < n, want, -1).to(torch.int32))
 
 
+@pytest.mark.parametrize("n", [16385, 20003, 65536, 131075])
+@pytest.mark.parametrize("k,first,last", [(1, 0, 0), (2048, 0, 0), (300, 2, 5), (60, 20, 40)])
+def test_topk_many_long_rows(n, k, first, last):
+    """Rows that are longer than a CTA's share and as many as there are SMs."""
+    g = torch.Generator(device="cuda").manual_seed(n + k)
+    rows = 160
+    x = torch.randn(rows, n + 3, generator=g, device="cuda")[:, :n]
+    x[1::4] = (x[1::4] * 2).round()
+    x[2::8] = 0.25
+    x[3::8, :n // 2] = -math.inf
+    x[5::16, 7::3] = math.nan
+    x[6::16] += 1e6
+    lengths = torch.randint(0, n + 1, (rows,), generator=g, device="cuda").to(torch.int32)
+    lengths[:8] = torch.tensor([0, 1, 2, 3, 511, 513, n - 1, n], dtype=torch.int32)
+    j = torch.arange(n, device="cuda")
+    for y in (x, x.contiguous()):
+        for ends in (lengths, None):
+            got = sfm.select_topk(y, k, lengths=ends, first_blocks=first, last_blocks=last)
+            e = lengths[:, None] if ends is not None else torch.full((rows, 1), n, device="cuda")
+            v = y.double().nan_to_num(nan=-math.inf, posinf=1e300, neginf=-math.inf)
+            v = torch.where(j < e, v, -math.inf)
+            v = torch.where((j < e) & ((j < first) | (j >= e - last)), math.inf, v)
+            best = torch.sort(v, dim=1, descending=True, stable=True)
+            want = torch.where(best.values[:, :k] > -math.inf, best.indices[:, :k], n).sort(1).values
+            assert torch.equal(got, torch.where(want < n, want, -1).to(torch.int32))
+
+
 @pytest.mark.parametrize("n", [700, 9001, 70001])
 @pytest.mark.parametrize("k,first,last", [(1, 0, 0), (8, 3, 5), (1, 0, 1), (700, 1, 2), (64, 40, 0), (600, 300, 300)])
 def test_topk_short_lengths_in_long_rows(n, k, first, last):
