@@ -25,7 +25,7 @@
 // 2048: 15.8 us; 2048 causal rows of up to 8192, k 1024: 29.9 us (2.0 TB/s);
 // 2048 causal rows of up to 16384 in blocks of 64, k 32: 32.2 us (3.9 TB/s);
 // 529 causal rows of up to 63406, k 512: 79 us (1.7 TB/s).
-// Loading and counting take about two thirds of the last two, some fifteen block
+// Loading and counting take half to two thirds of the prompt rows, some fifteen block
 // barriers with little work between them the rest, and the many small passes'
 // instructions (50 per 32 keys) more than memory bound the rows of 8192.  Rows
 // kept as floats and counted in equal bins of a sample's range (34.5 us), a list
@@ -311,7 +311,7 @@ __device__ __forceinline__ void pool_chunk(const float *src, int lane, Store sto
 // CTAs of at most 256 threads work on many short rows: fewer bins, and registers for five of 256 threads to share an
 // SM (2048 rows of up to 8192: 32.4 us with four loads ahead, with eight, which spill, 33.9; four CTAs and eight 33.4).
 template <int NT, int MODE, bool POOLED>
-__global__ void __launch_bounds__(NT, NT > 256 ? 1 + (MODE == kStreamed) : 1280 / NT) sfm_topk_kernel(const TopkArgs a)
+__global__ void __launch_bounds__(NT, NT > 512 ? 1 : NT > 256 ? 2 : 1280 / NT) sfm_topk_kernel(const TopkArgs a)
 {
     constexpr int NW = NT / 32;
     constexpr bool CACHED = MODE == kCached, STREAMED = MODE == kStreamed, kBits = CACHED || STREAMED;
@@ -897,12 +897,14 @@ extern "C" int sfm_topk_select(const sfm_topk_params *pp, const float *scores, c
     cudaError_t e;
     // Threads: a short slice has few keys per thread, and many small CTAs hide each other's barriers (2048 x
     // 16384 scores in blocks of 64, 256 keys a row: 35 us with 256 threads, 33 with 128; 2690 x 1055 in blocks of
-    // 16: 20.4 and 13.6).  Long slices want every lane that the SM has.
+    // 16: 20.4 and 13.6).  Slices of which an SM holds two at most take 512 (1024 x 16384: 39.1 us with 256, 31.6 with
+    // 512; 1024 x 12000, three per SM: 26.7 and 28.8), those of which it holds one 1024 (1024 x 20000, two per SM: 52.2
+    // with 1024, 40.3 with 512).
     if (streamed) e = launch<512, kStreamed, false>(a, dev, p.rows, smem, st);
     else if (!cached) e = launch<1024, kRecompute, false>(a, dev, p.rows, smem, st);
-    else if (slice(c) > 16384)
+    else if (slice(c) > 22528)
         e = pooled ? launch<1024, kCached, true>(a, dev, p.rows, smem, st) : launch<1024, kCached, false>(a, dev, p.rows, smem, st);
-    else if (c > 1)
+    else if (c > 1 || slice(c) > 14336)
         e = pooled ? launch<512, kCached, true>(a, dev, p.rows, smem, st) : launch<512, kCached, false>(a, dev, p.rows, smem, st);
     else if (slice(c) > 2048)
         e = pooled ? launch<256, kCached, true>(a, dev, p.rows, smem, st) : launch<256, kCached, false>(a, dev, p.rows, smem, st);
