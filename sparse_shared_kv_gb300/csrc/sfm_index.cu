@@ -24,8 +24,9 @@
 //   warps 17, 19  tcgen05.mma, M = 128, N = queries x HP, K = 128 -> TMEM, in
 //                 turns, so that one tile's waits and commits run beside the
 //                 other's products (issuing blocks while the pipe is busy);
-//   warp 18       tells the sums which keys exist and brings their scales
-//                 (cp.async), so that no sum waits for global memory;
+//   warp 18       brings the units' weights (two buffers), tells the sums which
+//                 keys exist and brings their scales (cp.async), so that no sum
+//                 waits for global memory;
 //   warps 0-15    four warpgroups that drain the accumulator: a warpgroup
 //                 takes 64 columns of a tile, a thread a key's 64 products,
 //                 32 at a time: a clip each and a multiply-add per two of
@@ -392,6 +393,8 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gmisc + 420);
     volatile uint32_t *key_mask = reinterpret_cast<volatile uint32_t *>(gmisc + 424);     // [kMaxAcc] a bit per four keys
     Share *share = reinterpret_cast<Share *>(gmisc + 456);
+    static_assert(sizeof(Share) <= 16, "room before the barriers behind it");
+    auto w_empty = [&](int i) { return bars + 472u + 8u * i; };    // the sums have read a unit's weights
     float *weights = reinterpret_cast<float *>(gmisc + 512);                            // [2][256]: by column
     float *half_sum = weights + 512;                                                    // HP 128 only: [2 pairs][128]
     float *key_scales = reinterpret_cast<float *>(gmisc + kMiscBytes - (HP == 128 ? 0 : 1024));   // [kMaxAcc][kTile]
@@ -404,7 +407,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         for (int i = 0; i < a.stages; ++i) mbar_init(k_empty(i), 1);
         for (int i = 0; i < accs; ++i) mbar_init(acc_full(i), 34), mbar_init(acc_empty(i), 4 * parts);
         for (int i = 0; i < 4; ++i) mbar_init(half_full(i), 4);
-        for (int i = 0; i < 2; ++i) mbar_init(w_full(i), kEpiWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(w_full(i), 1), mbar_init(w_empty(i), kEpiWarps);
         mbar_init(teardown, 1), mbar_init(teardown + 8, 1);
         fence_barrier_init();
     }
@@ -543,19 +546,35 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         }
         __syncwarp();
     } else if (warp == 18) {
-        // ---------------- masks and scales of the keys ----------------
-        int acc = 0, aphase = 0;
+        // ---------------- weights of the units, masks and scales of the keys ----------------
+        int acc = 0, aphase = 0, units_n = 0;
         bool ok = true;
         Units<true> units(my_share);
         Unit u = {};
         while (ok && units.next(a, queries, &bad, u)) {
             if (u.tiles == 0) continue;
             const int most = visible_of(a, u, u.nq - 1);
+            // zero for heads and queries that are not there
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int col = 32 * k + lane, i = col / HP, h = col % HP;
+                v[k] = i < u.nq && h < a.heads ? __ldg(a.weights + (int64_t)(u.t0 + i) * a.heads + h) : 0.f;
+                if (FP8 && doubled(lane)) v[k] *= 0.5f;
+            }
+            int32_t batch = rows_of(a, u, u.first_tile * kTile, lane);
+            const int wb = units_n & 1;
+            ok = wait_warp(w_empty(wb), ((units_n >> 1) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) weights[wb * 256 + 32 * k + lane] = v[k];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w_full(wb));
+            ++units_n;
             int j = u.first_tile * kTile + 4 * lane;          // four neighbouring keys per lane: they share a box
-            int32_t batch = -1;
             for (int t = 0; t < u.tiles; ++t, j += kTile) {
                 const int in = (t << a.boxes_log2) & 31;
-                if (in == 0) batch = rows_of(a, u, (u.first_tile + t) * kTile, lane);
+                if (in == 0 && t > 0) batch = rows_of(a, u, (u.first_tile + t) * kTile, lane);
                 int64_t row = __shfl_sync(0xffffffffu, batch, in + (4 * lane >> (7 - a.boxes_log2)));
                 row = row >= 0 && j < u.len ? row + (4 * lane & (a.run - 1)) : -1;
                 const int n = min(4, u.len - j);
@@ -602,15 +621,6 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             if (u.tiles) {
 #pragma unroll
                 for (int q = 0; q < kSums; ++q) vis[q] = visible_of(a, u, i_part + q);
-                // the unit's weights, zero for heads and queries that are not there.  The buffer was last read two
-                // units ago, and every warp has since arrived here for the unit between
-                if (lane < 16) {
-                    const int col = warp * 16 + lane, i = col / HP, h = col % HP;
-                    const float v = i < u.nq && h < a.heads ? __ldg(a.weights + (int64_t)(u.t0 + i) * a.heads + h) : 0.f;
-                    w[col] = FP8 && doubled(col) ? 0.5f * v : v;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(w_full(n & 1));
                 ok = wait_warp(w_full(n & 1), (n >> 1) & 1, abort_flag);
                 if (!ok) break;
                 ++n;
@@ -708,6 +718,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             }
             done += u.tiles;
             if (!ok) break;
+            if (u.tiles) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_empty((n - 1) & 1));
+            }
             // columns that no product reached, and under the products the rows without a query
             for (int i = warp; i < u.rows; i += kEpiWarps) {
                 float *dst = a.scores + (int64_t)(u.t0 + i) * a.stride;
