@@ -410,8 +410,10 @@ typedef struct sfm_store_params {
  * then rounded to the format: PLAIN to dtype; the others per tile (packed:
  * 128 values, FP8_ROWS: the row)
  *     scale = max(max |v| / M, 2^-126),   code = round(v / scale),   M = 127 (int8) or 448 (E4M3),
- * to nearest, ties to even; packed rope values (512..575) are rounded to
- * dtype.  A NaN anywhere in a tile makes its scale NaN.
+ * to nearest, ties to even, both quotients too, so that values which are
+ * neither normed nor rotated have the codes that these two lines give in fp32;
+ * packed rope values (512..575) are rounded to dtype.  A NaN anywhere in a tile
+ * makes its scale NaN.
  *   slots    (tokens) int32 or NULL (identity): head h of token t goes to cache
  *            row slots[t] * heads + h.  A negative slot writes nothing (padding).
  *            A slot whose rows lie outside the cache writes nothing and sets

@@ -354,6 +354,38 @@ def test_store_extreme_tiles(fmt):
     assert bool((raw[0, :D] == 0).all())
 
 
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "rows"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_store_codes_are_the_rounded_quotients(fmt, dt):
+    """Values that are neither normed nor rotated: scale = max |v| / M and code = v / scale, every operation one rounding
+    to nearest with ties to even.  Quotients of 16-bit values meet ties of the codes; no code may be off."""
+    D, n = (128, 6000) if fmt == "rows" else (512, 1500)
+    tile, most = 128, torch.tensor(127.0 if fmt == "int8" else 448.0)
+    dtype = DT[dt]
+    x = randn(gen(77), n, D, dtype=dtype)
+    lo = -24 if dt == "fp16" else -133
+    for r, e in enumerate((1, 0, -3, -9, lo, lo + 3, lo + 7, lo + 12, lo + 20)):      # tiles of other sizes, the smallest among them
+        x[r] = (randn(gen(r), D) * 2.0 ** e).to(dtype)
+    x[9] = (randn(gen(9), D) * 0.2 * torch.finfo(dtype).max).clamp(-torch.finfo(dtype).max, torch.finfo(dtype).max).to(dtype)
+    x[10, 5] = math.inf
+    raw, cache = make_cache(fmt, n, D, dtype)
+    scales = torch.zeros(n, device="cuda") if fmt == "rows" else None
+    sfm.store_kv(x.cuda(), cache, kv_format=FORMATS[fmt], scales=scales)
+    v = x.float().view(n, -1, tile)
+    scale = (v.abs().amax(-1) / most).clamp(min=P.TINY)
+    quotient = v / scale[..., None]
+    got = raw[:, :D].cpu()
+    finite = quotient.isfinite().view(n, D)
+    if fmt == "int8":
+        want, got = quotient.nan_to_num().round().to(torch.int8).view(n, D), got.view(torch.int8)
+    else:
+        want, got = quotient.to(torch.float8_e4m3fn).float().view(n, D), got.view(torch.float8_e4m3fn).float()
+    have = scales.cpu()[:, None] if fmt == "rows" else cache[:, -16:].contiguous().view(torch.float32).cpu()
+    assert torch.equal(have, scale)
+    wrong = (got != want) & finite
+    assert not wrong.any(), f"{int(wrong.sum())} of {wrong.numel()} codes"
+
+
 def test_store_without_tokens_and_noncontiguous_input():
     raw, cache = make_cache("plain", 3, 512, torch.bfloat16)
     sfm.store_kv(torch.empty(0, 512, dtype=torch.bfloat16, device="cuda"), cache)
