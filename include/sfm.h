@@ -416,10 +416,10 @@ typedef struct sfm_store_params {
  * makes its scale NaN.
  *   slots    (tokens) int32 or NULL (identity): head h of token t goes to cache
  *            row slots[t] * heads + h.  A negative slot writes nothing (padding).
- *            A slot whose rows lie outside the cache writes nothing and sets
- *            SFM_STATUS_BAD_BLOCK.  Two tokens of one call must not name the
- *            same slot: each 16-byte piece of that row is then one of the two.
- *            Rows no slot names are left as they were.
+ *            A slot of whose rows one lies outside the cache writes none of
+ *            them and sets SFM_STATUS_BAD_BLOCK.  Two tokens of one call must
+ *            not name the same slot: each 16-byte piece of that row is then one
+ *            of the two.  Rows no slot names are left as they were.
  *   norm_weight  (min(head_dim, 512)) fp32 or NULL (ones)
  *   positions, inv_freq  as in sfm_rope (NULL without rotation)
  *   scales   (rows) fp32, FP8_ROWS only

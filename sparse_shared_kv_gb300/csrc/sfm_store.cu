@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
         const int32_t this_token = token, this_position = position;
         const bool fresh = this_token != last_token;
         const int64_t row = (int64_t)slot * a.heads + head;
-        const bool inside = slot >= 0 && row < a.rows;
+        const bool inside = slot >= 0 && ((int64_t)slot + 1) * a.heads <= a.rows;    // all of the token's rows
         if (live && slot >= 0 && !inside && lane == 0 && a.status) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
         last_token = this_token;
         if (i + 1 < left) {

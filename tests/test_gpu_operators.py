@@ -334,6 +334,23 @@ def test_store_slots_outside_the_cache(fmt, D):
     assert bool((raw[[1, 3]] == 0x33).all())
 
 
+@pytest.mark.parametrize("fmt,D,H", [("plain", 128, 4), ("plain", 512, 3), ("int8", 512, 2), ("fp8", 576, 5), ("rows", 128, 64)])
+def test_store_writes_all_heads_of_a_token_or_none(fmt, D, H):
+    """A cache that ends inside a token's rows: that token is not written, with slots and without."""
+    g = gen(13)
+    x = randn(g, 3, H, D, dtype=torch.bfloat16)
+    rows = 2 * H + H // 2
+    for slots in (None, torch.tensor([2, 0, 1], dtype=torch.int32).cuda()):
+        raw, cache = make_cache(fmt, rows, D, torch.bfloat16)
+        scales = torch.full((rows,), 9.0, device="cuda") if fmt == "rows" else None
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sfm.store_kv(x.cuda(), cache, slot_mapping=slots, kv_format=FORMATS[fmt], scales=scales, status=status)
+        assert int(status) == sfm.STATUS_BAD_BLOCK
+        kept = x[:2] if slots is None else x[1:]
+        check_rows(fmt, cache, scales, torch.arange(2 * H), kept.reshape(-1, D).to(F64), torch.zeros(2 * H, D, dtype=F64), torch.bfloat16)
+        assert bool((raw[2 * H:] == 0x33).all()) and (scales is None or bool((scales[2 * H:] == 9.0).all()))
+
+
 @pytest.mark.parametrize("fmt", ["int8", "fp8", "rows"])
 def test_store_extreme_tiles(fmt):
     """Zero tiles, tiny ones, large ones, and a NaN that spoils its own tile alone."""
