@@ -2,10 +2,13 @@
 //
 // A pair's angle is position * f radians.  Only its fraction of a turn
 // matters, so f / (2 pi) is held as a 64-bit binary fraction of a turn and
-// multiplied by the position modulo 2^64: two integer multiplications, exact
-// to 2^-56 of a turn per position (f's own 53 bits) however far the position
-// is, negative ones included.  The top 32 bits then give the angle in half
-// turns, which sincospif takes without a further reduction.
+// multiplied by the position modulo 2^64.  The fraction is the product of f's 53
+// bits with those of 1 / (2 pi) that they meet (the reduction of Payne and Hanek;
+// 64-bit floating point is slow here, and a product with the rounded 1 / (2 pi)
+// would be off by 2^-56 f of a turn per position): it is at most 1.001 * 2^-64 of
+// a turn low for |f| < 2^53, and the angle of any 32-bit position, negative ones
+// included, off by less than 2^-32 of a turn.  The top 32 bits then give it in
+// half turns, rounded to fp32, which sincospif takes without a further reduction.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,9 +21,14 @@ namespace rope {
 
 __device__ __forceinline__ unsigned long long turn_step(double inv_freq)
 {
-    double f = inv_freq * 0.15915494309189535;    // 1 / (2 pi): turns per position
-    f -= floor(f);
-    return __double2ull_rz(f * 18446744073709551616.0);
+    // 2^128 / (2 pi)
+    constexpr unsigned __int128 kTurns = (unsigned __int128)0x28be60db9391054aull << 64 | 0x7f09d5f47d4d3770ull;
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(inv_freq);
+    const int shift = 1075 - (int)(bits >> 52 & 0x7ff);
+    const unsigned long long m = (bits & ((1ull << 52) - 1)) | 1ull << 52;
+    if (shift < 0 || shift > 127) return 0;       // 2^53 and above; below 2^-75: no turn within 32 bits of position
+    const unsigned long long step = (unsigned long long)((m * (kTurns >> shift)) >> 64);
+    return inv_freq < 0.0 ? 0ull - step : step;
 }
 
 // (cos, sin) of position * inv_freq, times the amplitude

@@ -138,6 +138,27 @@ def test_rope_strided_views(inter):
         sfm.apply_rope(one, pos.cuda(), f, out=one)
 
 
+@pytest.mark.parametrize("inter", [True, False], ids=["pairs", "halves"])
+def test_rope_angles_of_far_positions(inter):
+    """The angle is reduced as exactly at 2^31 as at 1, for fast pairs too.  Pairs whose first result nearly cancels show
+    it: its rounding to fp16 is 2^-11 of next to nothing, and what is left of the bound is that of the coefficients."""
+    freq = torch.tensor([1000.3, -1000.7, 100.9, 33.3, 6.5, 1.0, -0.7, 0.01], dtype=F64)
+    n = freq.numel()
+    pos = torch.tensor([1, 3, -5, 1000, 2 ** 20 + 1, 2 ** 30 - 7, -(2 ** 31), 2 ** 31 - 1], dtype=torch.int64)
+    T, g = pos.numel(), gen(21)
+    unit = torch.zeros(T, 1, 2 * n, dtype=F64)
+    first, second = (slice(0, None, 2), slice(1, None, 2)) if inter else (slice(0, n), slice(n, None))
+    unit[..., first] = 1.0
+    turned, _ = P.rope_parts(unit, pos.tolist(), freq, 0, inter)
+    c, s = turned[..., first], turned[..., second]
+    for _ in range(8):
+        r = 0.5 + 0.5 * torch.rand(T, 1, n, generator=g, dtype=F64)
+        x = torch.zeros(T, 1, 2 * n, dtype=torch.float16)
+        x[..., first], x[..., second] = (r * s).to(torch.float16), (r * c).to(torch.float16)      # a cos = b sin, nearly
+        y = sfm.apply_rope(x.cuda(), pos.to(torch.int32).cuda(), freq.cuda(), interleaved=inter)
+        rope_check(y, x, pos, freq, 0, inter, False, 1.0)
+
+
 def test_rope_gradient_is_the_inverse_call():
     g = gen(9)
     x, gy = randn(g, 3, 2, 64, dtype=torch.float16).cuda(), randn(g, 3, 2, 64, dtype=torch.float16).cuda()
