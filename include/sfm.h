@@ -433,9 +433,9 @@ typedef struct sfm_index_params {
     int32_t num_heads;          /* index heads, 1..128 */
     int32_t index_dim;          /* 128 */
     int32_t batch_size;         /* b (> 0) */
-    int32_t max_seqlen_q;       /* BSND: q_s; TND: max q length */
+    int32_t max_seqlen_q;       /* BSND: q_s; TND: max q length, or any bound above it */
     int32_t total_q;            /* TND: rows of q; ignored for BSND */
-    int32_t max_seqlen_kv;      /* columns of the scores; BSND: S dim of k; TND / paged: max key count */
+    int32_t max_seqlen_kv;      /* columns of the scores, at most 2^31 - 257; BSND: S dim of k; TND / paged: max key count */
     int32_t cmp_ratio;          /* tokens per key (1: one key per token) */
     int32_t mask_mode;          /* 0 no mask, 3 right-down causal */
     int32_t layout_q;           /* SFM_LAYOUT_BSND or SFM_LAYOUT_TND */

@@ -814,6 +814,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     if (p.batch_size <= 0 || p.max_seqlen_q <= 0 || p.max_seqlen_kv <= 0 || p.cmp_ratio <= 0) return SFM_ERR_INVALID_ARG;
     if (p.mask_mode != 0 && p.mask_mode != 3) return SFM_ERR_INVALID_ARG;
     if (p.layout_q == SFM_LAYOUT_TND && p.total_q < 0) return SFM_ERR_INVALID_ARG;
+    if (p.max_seqlen_kv > INT32_MAX - 2 * kTile) return SFM_ERR_UNSUPPORTED;    // columns are counted in whole tiles
     const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
     if (tokens * p.num_heads > INT32_MAX) return SFM_ERR_UNSUPPORTED;      // rows that a copy's coordinate names
     const bool paged = p.layout_kv == SFM_LAYOUT_PAGED;
@@ -836,6 +837,8 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     int dev = 0, sms = 0;
     if (current_sms(&dev, &sms) != cudaSuccess) return SFM_ERR_CUDA;
 
+    // a ragged batch may come with any upper bound: no sequence has more queries than all have
+    const int32_t max_q = p.layout_q == SFM_LAYOUT_TND && p.total_q < p.max_seqlen_q ? p.total_q : p.max_seqlen_q;
     const int hp = p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : p.num_heads <= 64 ? 64 : 128;
     IndexArgs a = {};
     a.weights = t->weights;
@@ -854,7 +857,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     a.k_rows = t->k_rows;
     a.heads = p.num_heads;
     a.batch = p.batch_size;
-    a.max_q = p.max_seqlen_q;
+    a.max_q = max_q;
     a.total_q = p.total_q;
     a.max_k = p.max_seqlen_kv;
     a.ratio = p.cmp_ratio;
@@ -867,7 +870,7 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     a.fp8 = p.dtype == SFM_DTYPE_E4M3;
 
     // 64-column parts of a tile: as many as one sequence's queries fill
-    const int64_t cols = (int64_t)p.max_seqlen_q * hp;
+    const int64_t cols = (int64_t)max_q * hp;
     a.parts_log2 = cols <= 64 ? 0 : cols <= 128 ? 1 : 2;
     const int queries = (64 << a.parts_log2) / hp;
     // accumulate in fp32; types of A and B; M = 128
@@ -886,9 +889,9 @@ extern "C" int sfm_index_scores(const sfm_index_params *pp, const sfm_index_tens
     const int fit = (int)((kSmemLimit - misc_bytes - 2 * q_bytes) / k_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 
-    a.groups_per_seq = (p.max_seqlen_q + queries - 1) / queries;
+    a.groups_per_seq = (int32_t)(((int64_t)max_q + queries - 1) / queries);
     const int64_t groups = (int64_t)a.groups_per_seq * p.batch_size;
-    const int64_t tiles = (p.max_seqlen_kv + kTile - 1) / kTile;
+    const int64_t tiles = ((int64_t)p.max_seqlen_kv + kTile - 1) / kTile;
     if (groups > INT32_MAX) return SFM_ERR_UNSUPPORTED;
     a.groups = (int32_t)groups;
     a.all_tiles = (int32_t)tiles;

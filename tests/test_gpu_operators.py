@@ -573,6 +573,20 @@ def test_index_scores_rows_behind_the_last_sequence_stay():
     assert bool((out[8:] == 5.0).all()) and vis[8:].tolist() == [-9] * 4
 
 
+@pytest.mark.parametrize("heads", [8, 64, 128])
+def test_index_scores_take_any_bound_on_ragged_queries(heads):
+    """max_seqlen_q of a ragged batch is an upper bound: loose ones, up to the largest there is, change nothing."""
+    q_lens, lens = [5, 3, 0, 21], [70, 300, 9, 140]
+    p = index_problem(4, "bf16", heads, q_lens, lens, "TND", "PAGED", 16)
+    want, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], **p["kw"])
+    check_scores(p, q_lens, lens, 1, True, want, seen)
+    for bound in (29, 100, 1 << 20, (1 << 31) - 8, (1 << 31) - 1):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got, seen = sfm.index_scores(p["qd"], p["cache"], p["wd"], status=status, **{**p["kw"], "max_seqlen_q": bound})
+        check_scores(p, q_lens, lens, 1, True, got, seen)
+        assert torch.equal(got, want) and int(status) == 0
+
+
 def test_index_scores_bad_blocks_and_lengths():
     p = index_problem(5, "bf16", 64, [1, 1], [300, 200], "BSND", "PAGED", 64)
     p["kw"]["block_table"][0, 2] = 1 << 20

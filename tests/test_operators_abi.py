@@ -125,6 +125,12 @@ def test_index_refusals(lib, kw, tkw, code):
     assert lib.sfm_index_scores(C.byref(_index(**kw)), C.byref(_index_tensors(**tkw)), ADDR, 1000, None, None, None) == code
 
 
+def test_index_columns_are_counted_in_whole_tiles(lib):
+    t = C.byref(_index_tensors())
+    for n in (2 ** 31 - 1, 2 ** 31 - 128, 2 ** 31 - 256):
+        assert lib.sfm_index_scores(C.byref(_index(max_seqlen_kv=n)), t, ADDR, n, None, None, None) == 2
+
+
 def test_index_refuses_outputs(lib):
     p, t = C.byref(_index()), C.byref(_index_tensors())
     assert lib.sfm_index_scores(p, t, ADDR, 999, None, None, None) == 3
