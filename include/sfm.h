@@ -237,8 +237,9 @@ int sfm_workspace_size(const sfm_params *params, size_t *bytes);
  * Ordering: the planner is launched as a programmatic dependent of the kernel
  * before it in the stream and reads the length tensors before waiting for
  * that kernel to finish (it waits before writing `metadata`).  The kernels
- * of this library never write length tensors, copies and ordinary kernels
- * finish before it starts; a kernel of the caller's that triggers its
+ * of this library never write length tensors, except for sfm_index_scores(),
+ * whose `visible` may be one: it is in place before that kernel's CTAs end.
+ * Copies and ordinary kernels finish before the planner starts; a kernel of the caller's that triggers its
  * dependents early (griddepcontrol.launch_dependents) must not write the
  * length tensors after that trigger. */
 int sfm_metadata(const sfm_params *params, const sfm_tensors *lengths, int32_t *metadata, size_t metadata_n,

@@ -419,7 +419,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
             *reinterpret_cast<uint4 *>(gbase + i) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
-    // (no early start of dependents: `visible` may be a length tensor of the next call)
+    // (no early start of dependents: `visible` may be a length tensor of the next call, see where it is written)
     grid_dependency_wait();
     bool bad = false;
     if (warp == 17) {
@@ -434,6 +434,7 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
     const Share my_share = a.chunk ? Share{} : *share;
+    int shown = 0;                                            // groups whose `visible` this thread has written
 
     if (warp == 16) {
         // ---------------- loads ----------------
@@ -618,7 +619,11 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         Units<true> units(my_share);
         Unit u = {};
         while (ok && units.next(a, queries, &bad, u)) {
-            if (a.visible && u.begins && tid < u.rows) a.visible[u.t0 + tid] = visible_of(a, u, tid);
+            if (a.visible && u.begins && tid < u.rows) {
+                a.visible[u.t0 + tid] = visible_of(a, u, tid);
+                if (shown == 0) __threadfence();
+                ++shown;
+            }
             int vis[kSums];
             float *w = weights + (n & 1) * 256;
             if (u.tiles) {
@@ -737,6 +742,10 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         }
     }
     if (bad && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
+    // `visible` may be a length tensor of the planner behind this kernel, which reads lengths as soon as all CTAs have
+    // ended.  (A fence after the first unit's, beside its loads and products, and one here for all others: only here
+    // costs few short sequences half a microsecond, after each unit's 17 sequences of 974 queries and keys 7 %.)
+    if (shown > 1) __threadfence();
 
     tc_fence_before();
     __syncthreads();

@@ -242,6 +242,15 @@ __device__ __forceinline__ int32_t clamp_len(const KParams &kp, int64_t v, int64
     return (int32_t)v;
 }
 
+// A sequence's length, from L2: the planner reads it before it waits for the
+// kernel before it, whose `visible` (sfm_index_scores) it may be.
+__device__ __forceinline__ int32_t ld_length(const int32_t *p)
+{
+    int32_t v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 __device__ inline Tok token_info(const KParams &kp, int t)
 {
     Tok k;
@@ -261,14 +270,14 @@ __device__ inline Tok token_info(const KParams &kp, int t)
         qcap = __ldg(kp.cu_q + lo + 1) - __ldg(kp.cu_q + lo);
     }
     const int b = k.b;
-    k.q_len = kp.used_q ? clamp_len(kp, __ldg(kp.used_q + b), qcap) : qcap;
+    k.q_len = kp.used_q ? clamp_len(kp, ld_length(kp.used_q + b), qcap) : qcap;
 
     int64_t cap;
     int64_t kv;
     if (kp.layout_kv == SFM_LAYOUT_BSND) cap = kp.ori_s;
     else if (kp.layout_kv == SFM_LAYOUT_TND) cap = __ldg(kp.cu_ori + b + 1) - __ldg(kp.cu_ori + b);
     else cap = kp.ori_max;      // paged: the declared max length (the planner sees no block table)
-    kv = kp.used_ori ? (int64_t)__ldg(kp.used_ori + b) : cap;
+    kv = kp.used_ori ? (int64_t)ld_length(kp.used_ori + b) : cap;
     k.kv_len = clamp_len(kp, kv, cap);
 
     k.cmp_len = 0;
@@ -276,10 +285,10 @@ __device__ inline Tok token_info(const KParams &kp, int t)
         if (kp.layout_kv == SFM_LAYOUT_BSND) cap = kp.cmp_s;
         else if (kp.layout_kv == SFM_LAYOUT_TND) cap = __ldg(kp.cu_cmp + b + 1) - __ldg(kp.cu_cmp + b);
         else cap = kp.cmp_max;
-        int64_t c = kp.used_cmp ? (int64_t)__ldg(kp.used_cmp + b) : cap;
+        int64_t c = kp.used_cmp ? (int64_t)ld_length(kp.used_cmp + b) : cap;
         k.cmp_len = clamp_len(kp, c, cap);
     }
-    const int64_t r = kp.residual ? (int64_t)__ldg(kp.residual + b) : 0;
+    const int64_t r = kp.residual ? (int64_t)ld_length(kp.residual + b) : 0;
     k.p = k.kv_len - k.q_len + k.i;
     const int64_t pc = (int64_t)k.cmp_len * kp.cmp_ratio + r - k.q_len + k.i;
     k.p_cmp = (int32_t)pc;

@@ -101,11 +101,12 @@ __global__ void __launch_bounds__(kPlanThreads) sfm_plan_kernel(KParams kp)
     // to finish before it reads the plan.  This grid itself is launched as a
     // dependent of whatever ran before it on the stream (its launch latency
     // overlaps that kernel's tail).  It reads only the length tensors, which
-    // no kernel of this library that lets its dependents start early writes,
-    // and waits for its predecessor before it writes the plan (a previous
-    // forward may still be reading an earlier plan in the same buffer): while
-    // the rows fit in shared memory, the row phase (the length loads) runs
-    // before that wait.
+    // no kernel of this library that lets its dependents start early writes
+    // (sfm_index_scores does not, and its lengths have reached L2, where they
+    // are read, before its CTAs end), and waits for its predecessor before it
+    // writes the plan (a previous forward may still be reading an earlier plan
+    // in the same buffer): while the rows fit in shared memory, the row phase
+    // (the length loads) runs before that wait.
     grid_launch_dependents();
 
     int32_t *meta = kp.meta_w;

@@ -818,6 +818,55 @@ def test_calls_read_what_the_calls_before_them_wrote():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("batch", [6, 200], ids=["small planner", "large planner"])
+def test_plans_read_the_lengths_the_call_before_them_wrote(batch):
+    """`visible` of the index scores is a length tensor of the plan right behind them, eager and captured: the plan reads
+    lengths before it waits for the kernel before it.  Each round's scores see one key less, or all again."""
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    n, heads = 900, 16
+    q = torch.randn(batch, 1, heads, 128, generator=g, device="cuda").to(torch.bfloat16)
+    keys = torch.randn(batch, n, 128, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand(batch, 1, heads, generator=g, device="cuda")
+    out, seen = torch.zeros(batch, n, device="cuda"), torch.zeros(batch, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    first = torch.randint(1, n + 1, (batch,), generator=g, device="cuda").to(torch.int32)
+
+    params = sfm.make_params(num_heads_q=64, batch_size=batch, max_seqlen_q=1, max_seqlen_ori_kv=n, ori_mask_mode=3)
+    tensors = sfm.make_tensors(None, None, seqused_ori_kv=seen, ori_row_stride=0)
+    words = sfm.sfm_metadata_size(params)
+
+    def score():
+        sfm.index_scores(q, keys, w, max_seqlen_kv=n, seqused_kv=lens, out=out, visible=seen)
+
+    def run(between):
+        lens.copy_(first)
+        plans = [torch.zeros(words, dtype=torch.int32, device="cuda") for _ in range(12)]
+        torch.cuda.synchronize()
+        for p in plans:
+            score()
+            between()
+            sfm.sfm_metadata(params, tensors, p)
+            between()
+            lens.sub_(1).clamp_(min=0)
+        torch.cuda.synchronize()
+        return torch.stack(plans)
+    apart = run(torch.cuda.synchronize)
+    assert not torch.equal(apart[0], apart[1])
+    for _ in range(3):
+        assert torch.equal(run(lambda: None), apart)
+    planned = torch.zeros(words, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        score()
+        sfm.sfm_metadata(params, tensors, planned)
+    lens.copy_(first)
+    for i in range(12):
+        planned.zero_()
+        graph.replay()
+        assert torch.equal(planned, apart[i])
+        lens.sub_(1).clamp_(min=0)
+
+
 # ---------------------------------------------------------------------------
 # offsets past 32 bits
 # ---------------------------------------------------------------------------
