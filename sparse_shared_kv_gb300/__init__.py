@@ -648,8 +648,12 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     fp32 (tokens, heads) in q's leading shape; k_scales: fp32, one per row of
     index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, its rows a
     multiple of four values apart, -inf where a key is not visible; visible
-    (tokens) int32).  ``out`` may be a
-    view with wider rows."""
+    (tokens) int32).  ``out`` may be a view with wider rows.
+
+    Rows of a TND batch behind its last sequence are not written: a new
+    ``visible`` is 0 there, so that ``select_topk(scores, k, lengths=visible)``
+    selects nothing, while the new scores hold no particular values; in ``out``
+    and ``visible`` of the caller's they stay as they were."""
     code, dev = _first("q", q, _INDEX_TYPES)
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
@@ -705,7 +709,8 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
             raise ValueError(f"out: needs fp32 ({tokens}, {max_seqlen_kv}) with contiguous rows on cuda:{dev}")
         stride = out.stride(0) if tokens > 1 else max_seqlen_kv
     if visible is None:
-        visible = torch.empty(each if tokens == batch else (tokens,), dtype=_I32, device=q.device)
+        # rows behind the last sequence (TND) are not written: they see nothing
+        visible = (torch.empty if lq == BSND else torch.zeros)((tokens,), dtype=_I32, device=q.device)
         seen = visible.data_ptr()
     else:
         seen = _address("visible", visible, _I32, dev, (tokens,))

@@ -573,6 +573,21 @@ def test_index_scores_rows_behind_the_last_sequence_stay():
     assert bool((out[8:] == 5.0).all()) and vis[8:].tolist() == [-9] * 4
 
 
+def test_index_scores_padding_behind_the_last_sequence_selects_nothing():
+    p = index_problem(4, "bf16", 16, [5, 3], [70, 30], "TND", "PAGED", 16)
+    q = torch.cat((p["qd"], p["qd"][:4]))
+    w = torch.cat((p["wd"], p["wd"][:4]))
+    for junk in (-9, 1 << 20, 7):                    # what the allocator's last owner left
+        rest = torch.full((12,), junk, dtype=torch.int32, device="cuda")
+        del rest
+        scores, seen = sfm.index_scores(q, p["cache"], w, **p["kw"])
+        check_scores(p, [5, 3], [70, 30], 1, True, scores[:8], seen[:8])
+        assert seen[8:].tolist() == [0] * 4
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        picked = sfm.select_topk(scores, 6, lengths=seen, status=status)
+        assert int(status) == 0 and bool((picked[8:] == -1).all()) and bool((picked[:8, 0] >= 0).all())
+
+
 @pytest.mark.parametrize("heads", [8, 64, 128])
 def test_index_scores_take_any_bound_on_ragged_queries(heads):
     """max_seqlen_q of a ragged batch is an upper bound: loose ones, up to the largest there is, change nothing."""
