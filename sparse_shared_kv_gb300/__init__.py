@@ -19,6 +19,8 @@ Two layers:
   ``sfm_rope_frequencies`` / ``sfm_rope`` / ``sfm_kv_store`` /
   ``sfm_index_scores`` / ``sfm_topk_select``: rotary positions, the rows of the
   caches, and the sparse indices the attention reads.
+
+None of the torch-level calls records a gradient.
 """
 from __future__ import annotations
 
@@ -419,6 +421,7 @@ def sparse_flash_mla(q: torch.Tensor, *, metadata: Metadata, ori_kv=None, cmp_kv
 # ---------------------------------------------------------------------------
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_increment_version = torch.autograd.graph.increment_version
 _I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 # The structs of include/sfm.h as native-layout packers (the calls below build them every time; packing
@@ -545,8 +548,14 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     positions: int32, one per token.  ``inverse=True`` applies the transposed
     map: the gradient with respect to x, and the way back for amplitude 1.
     ``out``: None for a new tensor, x itself to rotate in place, or a tensor
-    of x's shape that does not overlap it.  Views with strides are taken as they are."""
+    of x's shape that does not overlap it.  Views with strides are taken as they are.
+    The call records no gradient of its own: where one would be lost (x or out
+    requires it and grad mode is on) it raises, so a training step calls it inside
+    its own torch.autograd.Function, with ``inverse=True`` in the backward pass."""
     code, dev = _first("x", x, _SIXTEEN_BIT)
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("x: requires a gradient, which this call does not record (use no_grad, or an autograd.Function "
+                         "with inverse=True as its backward pass)")
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return apply_rope(x, positions, inv_freq, amplitude=amplitude, rope_offset=rope_offset, interleaved=interleaved,
@@ -555,7 +564,8 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     pos = _address("positions", positions, _I32, dev, (tokens,) if positions.dim() == 1 else x.shape[:-2])
     n = inv_freq.numel()
     freq = _address("inv_freq", inv_freq, _F64, dev, (n,))
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         yt, yh = heads * dim, dim
     elif out is x:
@@ -563,12 +573,16 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     else:
         if not (isinstance(out, torch.Tensor) and out.dtype is x.dtype and out.get_device() == dev and out.shape == x.shape):
             raise ValueError(f"out: needs {tuple(x.shape)} of {x.dtype} on cuda:{dev}")
+        if out.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out: requires a gradient, which this call does not record")
         _, _, _, yt, yh = _heads(out, "out")
     params = _ROPE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, 2 * n, rope_offset,
                                ROPE_INTERLEAVED if interleaved else ROPE_HALF, bool(inverse), code, amplitude, 0, xt, xh, yt, yh)
     rc = (_lib or lib()).sfm_rope(params, x.data_ptr(), pos, freq, out.data_ptr(), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_rope", rc)
+    if given and not out.is_inference():
+        _increment_version(out)      # a graph that saved it for its backward pass must notice
     return out
 
 

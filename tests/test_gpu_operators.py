@@ -183,6 +183,50 @@ def test_rope_gradient_is_the_inverse_call():
         assert_within(back, x.cpu().to(F64), torch.where(mag > 0, lim + 2 * floor_of(torch.float16), 0.0))
 
 
+def test_rope_and_autograd():
+    """No gradient is lost in silence: the call refuses to be recorded, works inside a Function of the caller's, and
+    what it writes is noticed by graphs that saved it."""
+    g = gen(15)
+    x, gy = randn(g, 5, 3, 64, dtype=torch.float16).cuda(), randn(g, 5, 3, 64, dtype=torch.float16).cuda()
+    pos, (f, _) = torch.arange(5, dtype=torch.int32).cuda(), sfm.rope_frequencies(32, device="cuda")
+    want = sfm.apply_rope(x, pos, f, amplitude=1.5)
+    leaf = x.clone().requires_grad_()
+    for t in (leaf, leaf * 1):
+        for kw in (dict(), dict(out=t), dict(out=torch.empty_like(x)), dict(stream=torch.cuda.Stream())):
+            with pytest.raises(ValueError, match="gradient"):
+                sfm.apply_rope(t, pos, f, **kw)
+    with pytest.raises(ValueError, match="gradient"):
+        sfm.apply_rope(x, pos, f, out=torch.empty_like(x).requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(sfm.apply_rope(leaf, pos, f, amplitude=1.5), want)
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return sfm.apply_rope(x, pos, f, amplitude=1.5)
+
+        @staticmethod
+        def backward(ctx, gy):
+            return sfm.apply_rope(gy, pos, f, amplitude=1.5, inverse=True)
+    y = Rope.apply(leaf)
+    y.backward(gy)
+    assert torch.equal(y, want) and torch.equal(leaf.grad, sfm.apply_rope(gy, pos, f, amplitude=1.5, inverse=True))
+
+    weight = torch.ones_like(x).requires_grad_()
+    for place in (True, False):
+        a = x.clone()
+        loss = (a * weight).sum()
+        sfm.apply_rope(a if place else x, pos, f, out=a)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    with torch.inference_mode():
+        a = x.clone()
+        assert torch.equal(sfm.apply_rope(a, pos, f, amplitude=1.5, out=a), want)
+    with torch.inference_mode():
+        a = x.clone()
+    assert torch.equal(sfm.apply_rope(a, pos, f, amplitude=1.5, out=a), want)
+
+
 def test_rope_without_tokens_and_on_another_stream():
     f, _ = sfm.rope_frequencies(64, device="cuda")
     assert sfm.apply_rope(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"),
