@@ -472,6 +472,12 @@ def _address(name, x, dtype, dev, shape):
     _refuse(name, x, dtype, dev, shape)
 
 
+def _tensor(name, x):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{name}: not a tensor")
+    return x
+
+
 def _status_address(status, dev):
     if not (isinstance(status, torch.Tensor) and status.dtype is _I32 and status.get_device() == dev and status.numel() >= 1):
         raise ValueError(f"status: needs an int32 tensor on cuda:{dev}")
@@ -561,8 +567,8 @@ def apply_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
             return apply_rope(x, positions, inv_freq, amplitude=amplitude, rope_offset=rope_offset, interleaved=interleaved,
                               inverse=inverse, out=out)
     tokens, heads, dim, xt, xh = _heads(x, "x")
-    pos = _address("positions", positions, _I32, dev, (tokens,) if positions.dim() == 1 else x.shape[:-2])
-    n = inv_freq.numel()
+    pos = _address("positions", positions, _I32, dev, (tokens,) if _tensor("positions", positions).dim() == 1 else x.shape[:-2])
+    n = _tensor("inv_freq", inv_freq).numel()
     freq = _address("inv_freq", inv_freq, _F64, dev, (n,))
     given = out is not None
     if not given:
@@ -631,7 +637,7 @@ def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_form
         raise ValueError("positions and inv_freq go together")
     if norm_eps is None and norm_weight is not None:
         raise ValueError("norm_weight: needs norm_eps")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    rot = 0 if inv_freq is None else 2 * _tensor("inv_freq", inv_freq).numel()
     offset = 0 if not rot else dim - rot if rope_offset is None else rope_offset
     params = _STORE_PARAMS.pack(tokens if heads else 0, heads or 1, dim, code, kv_format, norm_eps is not None,
                                 norm_eps or 0.0, rot, offset, ROPE_INTERLEAVED if interleaved else ROPE_HALF, amplitude, 0,
@@ -642,7 +648,7 @@ def store_kv(x: torch.Tensor, cache: torch.Tensor, *, slot_mapping=None, kv_form
         0 if positions is None else _address("positions", positions, _I32, dev, each),
         0 if inv_freq is None else _address("inv_freq", inv_freq, _F64, dev, (rot // 2,)),
         0 if slot_mapping is None else _address("slot_mapping", slot_mapping, _I32, dev, each), cache.data_ptr(),
-        0 if scales is None else _address("scales", scales, _F32, dev, (rows,) if scales.dim() == 1 else cache.shape[:-1]),
+        0 if scales is None else _address("scales", scales, _F32, dev, (rows,) if _tensor("scales", scales).dim() == 1 else cache.shape[:-1]),
         0 if status is None else _status_address(status, dev), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_kv_store", rc)
@@ -687,7 +693,7 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     elif cu_seqlens_q is None:
         raise ValueError("cu_seqlens_q: required for TND")
     else:
-        batch, tokens = cu_seqlens_q.numel() - 1, shape[0]
+        batch, tokens = _tensor("cu_seqlens_q", cu_seqlens_q).numel() - 1, shape[0]
     if not (isinstance(index_k, torch.Tensor) and index_k.dtype is q.dtype and index_k.get_device() == dev):
         raise ValueError(f"index_k: needs {q.dtype} on cuda:{dev}")
     kshape = index_k.shape
@@ -699,7 +705,7 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     cols = table = 0
     each = (batch,)
     if block_table is not None:
-        if block_table.dim() != 2:
+        if _tensor("block_table", block_table).dim() != 2:
             raise ValueError("block_table: needs (b, blocks)")
         cols = block_table.shape[1]
         table = _address("block_table", block_table, _I32, dev, (batch, cols))
@@ -707,7 +713,7 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
                                 kshape[1] if lkv == PAGED else 0)
     tensors = _INDEX_TENSORS.pack(
         _address("q", q, q.dtype, dev, shape), index_k.data_ptr(), row_stride, rows,
-        0 if k_scales is None else _address("k_scales", k_scales, _F32, dev, (rows,) if k_scales.dim() == 1 else kshape[:-1]),
+        0 if k_scales is None else _address("k_scales", k_scales, _F32, dev, (rows,) if _tensor("k_scales", k_scales).dim() == 1 else kshape[:-1]),
         _address("weights", weights, _F32, dev, shape[:-1]), table, cols,
         0 if cu_seqlens_q is None else _address("cu_seqlens_q", cu_seqlens_q, _I32, dev, (batch + 1,)),
         0 if cu_seqlens_kv is None else _address("cu_seqlens_kv", cu_seqlens_kv, _I32, dev, (batch + 1,)),

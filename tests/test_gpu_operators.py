@@ -825,6 +825,42 @@ def test_topk_short_lengths_in_long_rows(n, k, first, last):
         topk_check(x[r:r + 1], k, lengths[r:r + 1], first_blocks=first, last_blocks=last)
 
 
+def test_arguments_that_are_no_tensors_are_refused():
+    """... by name, whatever they are instead."""
+    x = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    pos, lens = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    f, cu = torch.zeros(8, dtype=F64, device="cuda"), torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    w, keys = torch.zeros(2, 4, device="cuda"), torch.zeros(2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros(8, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cache = torch.zeros(8, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+
+    def rope(**kw):
+        sfm.apply_rope(**{**dict(x=x, positions=pos, inv_freq=f), **kw})
+
+    def store(**kw):
+        sfm.store_kv(**{**dict(x=x, cache=cache, positions=pos, inv_freq=f), **kw})
+
+    def rows(**kw):
+        sfm.store_kv(**{**dict(x=x, cache=codes, kv_format=sfm.KV_FP8_ROWS), **kw})
+
+    def scores(**kw):
+        sfm.index_scores(**{**dict(q=x, index_k=keys, weights=w, max_seqlen_kv=16, max_seqlen_q=2, cu_seqlens_q=cu, seqused_kv=lens,
+                                   block_table=table, layout_q="TND", layout_kv="PAGED"), **kw})
+
+    def topk(**kw):
+        sfm.select_topk(**{**dict(scores=w, k=2), **kw})
+    rope(), store(), rows(scales=torch.zeros(8, device="cuda")), scores(), topk()
+    for call, names in ((rope, ("x", "positions", "inv_freq", "out")), (store, ("x", "cache", "positions", "inv_freq", "slot_mapping", "status")),
+                        (rows, ("scales",)), (topk, ("scores", "lengths", "out", "status")),
+                        (scores, ("q", "index_k", "weights", "k_scales", "block_table", "cu_seqlens_q", "seqused_kv", "seqused_q",
+                                  "cmp_residual_kv", "out", "visible", "status"))):
+        for name in names:
+            for other in ([0, 1], 3.5, "x"):
+                with pytest.raises(ValueError, match=name):
+                    call(**{name: other})
+
+
 # ---------------------------------------------------------------------------
 # calls behind each other: a kernel may be set up while the one before it runs
 # ---------------------------------------------------------------------------
