@@ -449,7 +449,10 @@ typedef struct sfm_index_params {
  *   k              BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned;
  *                  k_row_stride bytes apart (multiple of 16), k_rows rows in all
  *   k_scales       (k_rows) fp32 or NULL (ones), >= 0
- *   weights        (tokens, num_heads) fp32
+ *   weights        (tokens, num_heads) fp32.  Quantised queries come with a scale
+ *                  per token and head (sfm_kv_store writes them beside E4M3
+ *                  rows), which this call does not take: multiply it into the
+ *                  head's weight, w s max(0, q.k) = w max(0, (s q).k) for s >= 0
  *   the length tensors as in sfm_tensors (seqused_kv required for PAGED;
  *   cmp_residual_kv required for mask mode 3 with cmp_ratio > 1) */
 typedef struct sfm_index_tensors {

@@ -665,8 +665,9 @@ def index_scores(q: torch.Tensor, index_k: torch.Tensor, weights: torch.Tensor, 
     q: (b, q_s, heads, 128) or TND (tokens, heads, 128) in bf16, fp16 or
     float8_e4m3fn; index_k: (b, S, 128), (t, 128) or paged (blocks,
     block_size, 128) of the same dtype, rows may be padded apart; weights:
-    fp32 (tokens, heads) in q's leading shape; k_scales: fp32, one per row of
-    index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, its rows a
+    fp32 (tokens, heads) in q's leading shape, and the scales of quantised
+    queries (those of ``store_kv`` with KV_FP8_ROWS) belong multiplied into them;
+    k_scales: fp32, one per row of index_k.  Returns (scores (tokens, max_seqlen_kv) fp32, its rows a
     multiple of four values apart, -inf where a key is not visible; visible
     (tokens) int32).  ``out`` may be a view with wider rows.
 

@@ -595,6 +595,18 @@ def test_index_scores(case, mask):
     assert torch.equal(got, again)
 
 
+def test_index_scores_of_quantised_queries():
+    """Queries that store_kv wrote as E4M3 rows: their scales, multiplied into the weights, give the scores of the values."""
+    p = index_problem(8, "fp8", 16, [3, 3], [300, 40], "BSND", "PAGED", 64)
+    x = randn(gen(8), 6 * 16, 128, dtype=torch.bfloat16) * 3
+    codes = torch.zeros(6 * 16, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    qs = torch.zeros(6 * 16, device="cuda")
+    sfm.store_kv(x.cuda(), codes, kv_format=sfm.KV_FP8_ROWS, scales=qs)
+    got, seen = sfm.index_scores(codes.view(2, 3, 16, 128), p["cache"], p["wd"] * qs.view(2, 3, 16), **p["kw"])
+    p["q"] = (codes.float().cpu().to(F64) * qs.cpu().to(F64)[:, None]).view(6, 16, 128)
+    check_scores(p, [3, 3], [300, 40], 1, True, got, seen)
+
+
 def test_index_scores_padded_rows_strided_output_and_used_queries():
     for dt, scales in (("bf16", True), ("fp8", False)):
         p = index_problem(3, dt, 64, [6, 6], [300, 40], "BSND", "PAGED", 64, 1, pad=16, scales=scales)
