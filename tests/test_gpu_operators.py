@@ -823,6 +823,36 @@ def test_topk_many_long_rows(n, k, first, last):
             assert torch.equal(got, torch.where(want < n, want, -1).to(torch.int32))
 
 
+# rows, scores, block: one to sixteen CTAs per row with 128 to 1024 threads each, and rows that no cluster holds
+@pytest.mark.parametrize("rows,n,block", [
+    (1, 131072, 64), (1, 300001, 4), (2, 600000, 16), (1, 600003, 64), (3, 524288, 128), (2, 100003, 2), (70, 60001, 2), (70, 70000, 4),
+    (100, 100001, 2), (9, 200004, 16), (1, 1400001, 2), (2, 2700004, 4)])
+def test_topk_blocks_of_long_rows(rows, n, block):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    wide = torch.randn(rows, n + 3, generator=g, device="cuda")
+    wide[0] = (wide[0] * 2).round()
+    wide[-1, ::5] = math.nan
+    wide[rows // 2, n // 3:n // 2] = -math.inf
+    x = wide[:, :n]
+    blocks, j = -(-n // block), torch.arange(n, device="cuda")
+    each = torch.arange(blocks, device="cuda")
+    ends = [n, 0, 1, block, n // 2 + 1, n // 16 // block * block + 3, n - 1, n - n // 5]     # some CTAs get a part, some nothing
+    plans = [None] + [torch.tensor([ends[(r + i) % len(ends)] for r in range(rows)], dtype=torch.int32, device="cuda")
+                      for i in range(len(ends) if rows < len(ends) else 1)]
+    for y in (x.contiguous(), x):                    # rows on 16-byte boundaries (where n allows it) and off them
+        for lengths in plans:
+            e = lengths[:, None].long() if lengths is not None else torch.full((rows, 1), n, device="cuda")
+            v = torch.where(j < e, y.double().nan_to_num(nan=-math.inf, posinf=math.inf, neginf=-math.inf), -math.inf)
+            v = torch.nn.functional.pad(v, (0, blocks * block - n), value=-math.inf).view(rows, blocks, block).amax(-1)
+            have = -(-e // block)
+            for k, first, last in ((31, 0, 0), (500, 1, 2), (1000, 300, 40)):
+                got = sfm.select_topk(y, k, lengths=lengths, block_size=block, first_blocks=first, last_blocks=last)
+                w = torch.where((each < have) & ((each < first) | (each >= have - last)), math.inf, v)
+                best = torch.sort(w, dim=1, descending=True, stable=True)
+                want = torch.where(best.values[:, :k] > -math.inf, best.indices[:, :k], blocks).sort(1).values
+                assert torch.equal(got, torch.where(want < blocks, want, -1).to(torch.int32))
+
+
 @pytest.mark.parametrize("n", [700, 9001, 70001])
 @pytest.mark.parametrize("k,first,last", [(1, 0, 0), (8, 3, 5), (1, 0, 1), (700, 1, 2), (64, 40, 0), (600, 300, 300)])
 def test_topk_short_lengths_in_long_rows(n, k, first, last):
