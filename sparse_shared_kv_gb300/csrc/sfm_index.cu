@@ -434,7 +434,6 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
     const Share my_share = a.chunk ? Share{} : *share;
-    int shown = 0;                                            // groups whose `visible` this thread has written
 
     if (warp == 16) {
         // ---------------- loads ----------------
@@ -619,10 +618,12 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
         Units<true> units(my_share);
         Unit u = {};
         while (ok && units.next(a, queries, &bad, u)) {
+            // It may be a length tensor of the planner behind this kernel, which reads lengths as soon as all CTAs have
+            // ended: fenced beside the first unit's loads and products, and at the end for all others.  (Only there costs
+            // few short sequences half a microsecond, after each unit 17 sequences of 974 queries and keys 7 %.)
             if (a.visible && u.begins && tid < u.rows) {
                 a.visible[u.t0 + tid] = visible_of(a, u, tid);
-                if (shown == 0) __threadfence();
-                ++shown;
+                if (units.k == 1) __threadfence();
             }
             int vis[kSums];
             float *w = weights + (n & 1) * 256;
@@ -740,12 +741,9 @@ sfm_index_kernel(const IndexArgs a, const __grid_constant__ CUtensorMap q_map, c
                 }
             }
         }
+        if (a.visible && warp == 0 && units.k > 1) __threadfence();
     }
     if (bad && a.status) atomicOr(a.status, SFM_STATUS_BAD_LENGTH);
-    // `visible` may be a length tensor of the planner behind this kernel, which reads lengths as soon as all CTAs have
-    // ended.  (A fence after the first unit's, beside its loads and products, and one here for all others: only here
-    // costs few short sequences half a microsecond, after each unit's 17 sequences of 974 queries and keys 7 %.)
-    if (shown > 1) __threadfence();
 
     tc_fence_before();
     __syncthreads();
