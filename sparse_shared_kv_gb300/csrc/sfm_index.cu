@@ -37,14 +37,16 @@
 //
 // Measured on one GB300: 32 sequences of up to 32768 E4M3 keys, one query each:
 // 25 us, 4.3 TB/s, bound by reading the keys but for some 5 us of starting;
-// 2048 queries of 64 heads over 8192 bf16 keys: 162 us, 1.48 PFLOP/s (76 % of
+// 2048 queries of 64 heads over 8192 bf16 keys: 163 us, 1.47 PFLOP/s (75 % of
 // what a library product reaches), bound by the clipped sums beside the matrix
-// products (133 us without them), over as many E4M3 keys 149; 17 sequences of 974
-// queries and keys, in units of 4 queries and 4 tiles: 122 us (139 with the
-// weights fetched by the sums); four short sequences: 5.5 us, latency.  Taken
-// out because slower on the 2048 queries: weights in registers with 192 columns
-// and twelve warps (174-180 us), a register split (488), the next 32 columns
-// loaded during the sums (190), 64 columns at once (176).
+// products (133 us without them), for some tenths of a second; back to back for
+// longer the power cap lowers the clock from 2070 to 1920 MHz and it takes 174 us.
+// Over as many E4M3 keys 149; 17 sequences of 974 queries and keys, in units of 4
+// queries and 4 tiles: 131 us (a seventh more with the weights fetched by the
+// sums); four short sequences: 5.7 us, latency.  Taken out because slower on the
+// 2048 queries: weights in registers with 192 columns and twelve warps (174-180
+// us), a register split (488), the next 32 columns loaded during the sums (190),
+// 64 columns at once (176).
 //
 // Every wait is bounded as in the attention kernel (sfm_tc.cuh).
 #include <cuda.h>
@@ -359,7 +361,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 
 // HP: columns per query; FULL: as many heads.  Without, a tile is drained only
 // after its sums are known to need no second look (2048 queries of 48 heads over
-// 8192 keys: 177 us, leaving columns out in every sum 206; of 64 heads 163).
+// 8192 keys: 178 us, leaving columns out in every sum 206; of 64 heads 163).
 // FP8: E4M3 queries and keys.
 template <int HP, bool FULL, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)

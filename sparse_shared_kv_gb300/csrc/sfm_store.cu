@@ -13,10 +13,12 @@
 // cache's format.
 //
 // Measured on one GB300: 16381 rows of 512 values, normed, rotated and stored as
-// bf16: 8.7 us (3.9 TB/s); 131072 index rows of 128 values to E4M3: 15.9 us (3.2
-// TB/s) and 441488 such rows, normed, 50 us (3.4 TB/s), where instructions bound
-// it more than memory; 64 packed rows: 2.6 us, latency.  Eight lanes per row with
-// sixteen values each need fewer shuffles but spill the half layout's cosines:
+// bf16: 8.8 us (3.8 TB/s); 131072 index rows (2048 tokens of 64 heads) of 128
+// values to E4M3: 17.0 us (3.0 TB/s) and 441488 such rows of 16 heads, normed, 56 us
+// (3.0 TB/s), where instructions bound it more than memory; 16381 packed rows of
+// 576: 12.4 us as E4M3, 13.7 as int8; 64 packed rows: 2.7 us, latency.  The
+// quotients' remainders are 6 to 11 % of the quantised ones.  Eight lanes per row
+// with sixteen values each need fewer shuffles but spill the half layout's cosines:
 // better by a fifth on the 441488 rows, worse by a fifth on the 131072.
 #include <math.h>
 
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) sfm_store_kernel(StoreArgs a)
             c[e + 1] = make_float2(two.z, minus ? -two.w : two.w);
         }
     };
-    // one step per row: a lane's weights stay in registers too (441488 rows: 55.8 -> 50.1 us)
+    // one step per row: a lane's weights stay in registers too (441488 rows: by a tenth)
     float weight[8];
     if (STEPS == 1) {
 #pragma unroll
@@ -374,8 +376,8 @@ cudaError_t launch(const StoreArgs &a, cudaStream_t st)
     int dev = 0, sms = 0;
     const cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
-    // four CTAs per SM, what its registers hold (131072 index rows: 16.7 us; with eight, two waves, 17.9; with five
-    // of 48 registers 20.0)
+    // four CTAs per SM, what its registers hold (131072 index rows, before the remainders: 16.7 us; with eight, two
+    // waves, 17.9; with five of 48 registers 20.0)
     const int64_t want = (a.total + kGroups - 1) / kGroups, most = (int64_t)sms * 4;
     const unsigned grid = (unsigned)(want < most ? want : most);
     const int width = LANES * 8;
