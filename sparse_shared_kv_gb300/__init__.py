@@ -535,12 +535,15 @@ def _rows(x, name):
         raise ValueError(f"{name}: needs (..., row) with contiguous rows")
     rows, stride = shape[0], strides[0]
     if len(shape) != 2:
-        rows, stride = shape[:-1].numel(), strides[-2]
-        for i in range(len(shape) - 2):
-            if shape[i] != 1 and strides[i] != strides[i + 1] * shape[i + 1]:
+        rows, span = shape[:-1].numel(), None
+        for i in range(len(shape) - 2, -1, -1):
+            if shape[i] == 1 or not rows:
+                continue        # a dimension of one entry may report any stride
+            if span is None:
+                stride = span = strides[i]
+            elif strides[i] != span:
                 raise ValueError(f"{name}: the row dimensions do not flatten to one stride")
-        if shape[-2] == 1:      # the stride of the innermost dimension with more than one entry
-            stride = next((strides[i] for i in range(len(shape) - 2, -1, -1) if shape[i] > 1), shape[-1])
+            span *= shape[i]
     return rows, (stride if rows > 1 else shape[-1]) * x.element_size()
 
 

@@ -181,6 +181,23 @@ def test_packed_structs_match_the_ctypes_ones():
         assert packer.size == C.sizeof(struct) and packer.pack(*values) == bytes(made), struct
 
 
+def test_row_dimensions_of_one_entry_may_have_any_stride():
+    """Caches cut or unflattened to blocks of one row are rows like any other."""
+    wide = torch.zeros(60, 144)
+    for x, want in ((wide[:, :128].unflatten(0, (60, 1)), (60, 576)), (wide[:, :128].unflatten(0, (1, 60)), (60, 576)),
+                    (wide[:, :128].unflatten(0, (10, 6)), (60, 576)), (wide[:1, :128].unflatten(0, (1, 1)), (1, 512)),
+                    (torch.zeros(5, 4, 128)[:, :1], (5, 2048)), (torch.zeros(5, 4, 128)[:1], (4, 512)),
+                    (torch.zeros(6, 4, 2, 144)[:, :1, :, :128], None), (torch.zeros(6, 4, 2, 144)[:, 1:2, :1, :128], (6, 4608)),
+                    (torch.zeros(1, 7, 128).expand(5, 7, 128), None), (torch.zeros(5, 4, 128)[:, :2], None),
+                    (torch.zeros(3, 0, 128), (0, 512)), (torch.zeros(0, 4, 128), (0, 512)), (torch.zeros(4, 128), (4, 512)),
+                    (wide[:, :128], (60, 576)), (wide[:1, :128], (1, 512))):
+        if want is None:
+            with pytest.raises(ValueError, match="one stride"):
+                sfm._rows(x, "cache")
+        else:
+            assert sfm._rows(x, "cache") == want, (x.shape, x.stride())
+
+
 # ---------------------------------------------------------------------------
 # frequencies
 # ---------------------------------------------------------------------------
