@@ -381,7 +381,7 @@ typedef struct sfm_rope_params {
  * touches the rotated part only, otherwise every value of y is written and the
  * two must not overlap.  positions: (tokens) int32, any sign.  inv_freq:
  * DEVICE array of rope_dim / 2 doubles, |inv_freq| < 2^53.  The angle is reduced
- * to one turn in integers, to 2^-32 of a turn at every position, and then rounded
+ * to one turn in integers, to 2^-31 of a turn at every position, and then rounded
  * to fp32. */
 int sfm_rope(const sfm_rope_params *params, const void *x, const int32_t *positions, const double *inv_freq, void *y,
              sfm_stream_t stream);

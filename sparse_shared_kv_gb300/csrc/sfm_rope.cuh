@@ -7,8 +7,9 @@
 // 64-bit floating point is slow here, and a product with the rounded 1 / (2 pi)
 // would be off by 2^-56 f of a turn per position): it is at most 1.001 * 2^-64 of
 // a turn low for |f| < 2^53, and the angle of any 32-bit position, negative ones
-// included, off by less than 2^-32 of a turn.  The top 32 bits then give it in
-// half turns, rounded to fp32, which sincospif takes without a further reduction.
+// included, off by less than 2^-32 of a turn.  Its top 32 bits (cut off, another
+// 2^-32 at most) then give it in half turns, rounded to fp32, which sincospif takes
+// without a further reduction.
 #pragma once
 
 #include <cuda_bf16.h>
