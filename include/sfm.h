@@ -510,6 +510,144 @@ typedef struct sfm_topk_params {
 int sfm_topk_select(const sfm_topk_params *params, const float *scores, const int32_t *lengths, int32_t *indices,
                     int32_t *status, sfm_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention of many queries over the same rows: prompts, single tokens over a
+ * cache, and trees of drafted tokens, with more kinds of scores and masks than
+ * sfm_forward(); the joining of attention results over separate sets of keys;
+ * and the moving of an accepted path's rows.  The conventions of the calls
+ * above hold here too.
+ * ------------------------------------------------------------------------- */
+
+typedef struct sfm_dense_params {
+    int32_t num_heads;          /* query heads, 1..128 */
+    int32_t head_dim;           /* 512 */
+    int32_t batch_size;         /* b (> 0) */
+    int32_t max_seqlen_q;       /* BSND: q_s; TND: ignored */
+    int32_t total_q;            /* TND: rows of q (>= 0); BSND: ignored */
+    int32_t max_seqlen_kv;      /* BSND: S dim of kv; TND / paged: max key count (longer sequences are cut, SFM_STATUS_BAD_LENGTH) */
+    int32_t mask_mode;          /* 0 no mask, 3 right-down causal, 4 window */
+    int32_t win_left;           /* mode 4: -1 (unbounded) or >= 0 past keys */
+    int32_t win_right;          /* mode 4: -1 (unbounded) or >= 0 future keys */
+    int32_t layout_q;           /* SFM_LAYOUT_BSND or SFM_LAYOUT_TND */
+    int32_t layout_kv;          /* BSND, TND or PAGED; non-paged must equal layout_q */
+    int32_t dtype;              /* of q, kv and out: BF16 or FP16 */
+    int32_t block_size;         /* paged: rows per block, multiple of 16, <= 1024 */
+    int32_t tree_words;         /* 0: no tree; 1..16: 64-bit words per row of tree_mask */
+    int32_t split_keys;         /* 0: long key ranges are cut so that the SMs are filled, which depends on the batch;
+                                   > 0 (a multiple of 128): into pieces of this many keys, whatever else is in the
+                                   batch (a row's result is then bit for bit the same in every batch) */
+    int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 1: O = 0 and LSE = -inf; 0: left as they were */
+    float softmax_scale;        /* finite */
+    float softcap;              /* 0: none; > 0: scores are capped */
+} sfm_dense_params;
+
+/*   q              BSND (b, q_s, num_heads, 512) / TND (q_t, num_heads, 512), dense, 16-byte aligned
+ *   kv             BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned; rows of 512
+ *                  values, kv_row_stride bytes apart (>= 1024, multiple of 16), kv_rows rows in all
+ *   the length tensors and sinks as in sfm_tensors (seqused_kv required for PAGED)
+ *   bias_slopes    (num_heads) fp32 or NULL
+ *   prefix_lens    (b) int32 or NULL
+ *   key_begin, key_end   (tokens) int32 or NULL
+ *   tree_mask      (tokens, tree_words) int64, with tree_words > 0
+ *   positions      (tokens) int32 in [0, 2^30), with tree_words > 0 */
+typedef struct sfm_dense_tensors {
+    const void *q;
+    const void *kv;
+    int64_t kv_row_stride;
+    int64_t kv_rows;
+    const int32_t *block_table;
+    int32_t block_table_stride;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_kv;
+    const int32_t *seqused_q;
+    const int32_t *seqused_kv;
+    const float *sinks;
+    const float *bias_slopes;
+    const int32_t *prefix_lens;
+    const int32_t *key_begin;
+    const int32_t *key_end;
+    const int64_t *tree_mask;
+    const int32_t *positions;
+} sfm_dense_tensors;
+
+/* Device workspace bytes sfm_dense_forward() needs for these params on the
+ * current device (0 where no key range is cut).  Host only. */
+int sfm_dense_workspace_size(const sfm_dense_params *params, size_t *bytes);
+
+/* Attention over one source of rows, K~ = V~ = kv.  For query i of a sequence
+ * of q_len queries and len keys, head h and key j:
+ *     x = softmax_scale * (q[i][h] . kv[j])
+ *     x = softcap * tanh(x / softcap)                       (softcap > 0)
+ *     x = x - bias_slopes[h] * |pos(i) - pos(j)|            (bias_slopes)
+ *     O = sum_j e^x kv[j] / (sum_j e^x + e^sinks[h]),   LSE = log sum_j e^x     (over the visible j)
+ * Without a tree, pos(i) = p = len - q_len + i and pos(j) = j, and j is visible iff
+ *     (j is inside the mask mode's range of p, which is [0, len) (0), [0, p] (3)
+ *      or [p - win_left, p + win_right] (4), and key_begin[i] <= j < key_end[i])
+ *     or j < prefix_lens[sequence].
+ * key_begin / key_end are the document of a query in a packed sequence (or any
+ * other range of keys), prefix_lens the keys that every query sees.
+ * With a tree (tree_words > 0; neither prefix_lens nor key_begin / key_end) the
+ * last q_len keys are the queries' own rows, written before, in the same order.
+ * Key j < len - q_len is at pos(j) = j; key j = len - q_len + k at
+ * positions[k], and query i at pos(i) = positions[i] (those of the sequence).
+ * Every key of the first kind is visible, of the second those whose bit k of
+ * tree_mask[i] is set (word k / 64, bit k % 64: the ancestors of token i and
+ * itself); mode 4 takes away those outside [pos(i) - win_left, pos(i) + win_right].
+ * A row without visible keys has O = 0 and LSE = -inf, as have rows of q at or
+ * beyond seqused_q.  Keys that a row does not see have no part in it, whatever
+ * they hold (NaN and infinities too); a row that sees a key with a score that is
+ * NaN or +inf is NaN.  A block outside the cache is not visible and sets
+ * SFM_STATUS_BAD_BLOCK.
+ * out: q's layout; lse: device fp32 (tokens x num_heads) or NULL; workspace:
+ * device, >= sfm_dense_workspace_size() bytes, 256-byte aligned, used by one
+ * call at a time.  Products are exact, sums in fp32; weights e^x are rounded to
+ * dtype for the product with kv. */
+int sfm_dense_forward(const sfm_dense_params *params, const sfm_dense_tensors *tensors, void *out, float *lse,
+                      void *workspace, size_t workspace_bytes, int32_t *status, sfm_stream_t stream);
+
+#define SFM_MERGE_MAX_PARTS 8
+
+typedef struct sfm_merge_params {
+    int32_t tokens, heads;      /* rows: tokens x heads (>= 0, 1..) */
+    int32_t head_dim;           /* a multiple of 8 */
+    int32_t parts;              /* 1..SFM_MERGE_MAX_PARTS */
+    int32_t dtype;              /* of outs and out: BF16 or FP16 */
+    int32_t reserved;           /* 0 */
+} sfm_merge_params;
+
+/* Join attention results over separate sets of keys.  Per row, with part n's
+ * output O_n and LSE_n (natural, without sinks):
+ *     LSE = log sum_n e^LSE_n,   O = sum_n e^LSE_n O_n / (sum_n e^LSE_n + e^sinks[head])
+ * A part with LSE_n = -inf has no keys: its O_n is not read.  No keys at all
+ * give O = 0 and LSE = -inf.
+ * outs, lses: HOST arrays of `parts` device pointers to dense (tokens, heads,
+ * head_dim), 16-byte aligned, and fp32 (tokens, heads).  sinks: fp32 (heads) or
+ * NULL (the parts must then have been computed without them, or all but one).
+ * out may be one of outs; lse is NULL or none of lses. */
+int sfm_merge(const sfm_merge_params *params, const void *const *outs, const float *const *lses, const float *sinks,
+              void *out, float *lse, sfm_stream_t stream);
+
+typedef struct sfm_move_params {
+    int32_t batch_size;         /* b (>= 0) */
+    int32_t max_path;           /* entries per sequence of path (>= 0) */
+    int32_t row_bytes;          /* a multiple of 16 */
+    int32_t block_size;         /* paged: rows per block (> 0); 0: sequence b has rows [b max_seqlen_kv, (b + 1) max_seqlen_kv) */
+    int32_t max_seqlen_kv;      /* not paged: rows per sequence */
+    int32_t block_table_stride; /* paged: blocks per sequence of block_table */
+    int64_t row_stride;         /* bytes between cache rows: >= row_bytes, a multiple of 16 */
+    int64_t rows;               /* rows the cache holds */
+} sfm_move_params;
+
+/* Move the rows of an accepted path together: for every sequence b,
+ *     row(first[b] + i) = what row(first[b] + path[b][i]) was before the call,   i = 0, 1, ...
+ * up to the first negative entry of path[b].  Entries are the drafted tokens'
+ * numbers along the path and grow (path[i] < path[i + 1]); one that does not
+ * ends the path (SFM_STATUS_BAD_INDEX).  A row outside the sequence's blocks or
+ * the cache ends it too (SFM_STATUS_BAD_BLOCK).  Rows that are not written stay.
+ * Sequences must not share the rows that they move.  cache is 16-byte aligned. */
+int sfm_kv_move(const sfm_move_params *params, const int32_t *path, const int32_t *first, const int32_t *block_table,
+                void *cache, int32_t *status, sfm_stream_t stream);
+
 /* Static description of an sfm_error code. */
 const char *sfm_error_string(int code);
 

@@ -18,7 +18,11 @@ Two layers:
   ``select_topk`` -- the operators around the attention in the same form, over
   ``sfm_rope_frequencies`` / ``sfm_rope`` / ``sfm_kv_store`` /
   ``sfm_index_scores`` / ``sfm_topk_select``: rotary positions, the rows of the
-  caches, and the sparse indices the attention reads.
+  caches, and the sparse indices the attention reads;
+* ``masked_attention`` / ``tree_attention`` / ``merge_attention`` / ``move_kv``
+  -- attention of many queries over the same rows (``sfm_dense_forward``), the
+  joining of results over separate keys (``sfm_merge``) and the moving of an
+  accepted path's rows (``sfm_kv_move``).
 
 None of the torch-level calls records a gradient.
 """
@@ -128,9 +132,33 @@ class SfmTopkParams(_Params):
     _fields_ = _i32("rows", "n", "k", "block_size", "first_blocks", "last_blocks") + [("score_stride", C.c_int64)]
 
 
+class SfmDenseParams(_Params):
+    _fields_ = _i32("num_heads", "head_dim", "batch_size", "max_seqlen_q", "total_q", "max_seqlen_kv", "mask_mode",
+                    "win_left", "win_right", "layout_q", "layout_kv", "dtype", "block_size", "tree_words", "split_keys",
+                    "zero_rest") + [("softmax_scale", C.c_float), ("softcap", C.c_float)]
+
+
+class SfmDenseTensors(_Params):
+    _fields_ = [("q", C.c_void_p), ("kv", C.c_void_p), ("kv_row_stride", C.c_int64), ("kv_rows", C.c_int64),
+                ("block_table", C.c_void_p), ("block_table_stride", C.c_int32)] + \
+        [(n, C.c_void_p) for n in ("cu_seqlens_q", "cu_seqlens_kv", "seqused_q", "seqused_kv", "sinks", "bias_slopes",
+                                   "prefix_lens", "key_begin", "key_end", "tree_mask", "positions")]
+
+
+class SfmMergeParams(_Params):
+    _fields_ = _i32("tokens", "heads", "head_dim", "parts", "dtype", "reserved")
+
+
+class SfmMoveParams(_Params):
+    _fields_ = _i32("batch_size", "max_path", "row_bytes", "block_size", "max_seqlen_kv", "block_table_stride") + \
+        [("row_stride", C.c_int64), ("rows", C.c_int64)]
+
+
 EXPORTS = ("sfm_metadata_size", "sfm_workspace_size", "sfm_metadata", "sfm_forward", "sfm_forward_noalloc",
            "sfm_debug_attended", "sfm_set_profile_events", "sfm_error_string", "sfm_abi_version",
-           "sfm_rope_frequencies", "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select")
+           "sfm_rope_frequencies", "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select",
+           "sfm_dense_workspace_size", "sfm_dense_forward", "sfm_merge", "sfm_kv_move")
+MERGE_MAX_PARTS = 8
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 
 _lib = None
@@ -169,9 +197,14 @@ def lib():
         l.sfm_kv_store.argtypes = [V] * 10
         l.sfm_index_scores.argtypes = [V, V, V, C.c_int64, V, V, V]
         l.sfm_topk_select.argtypes = [V] * 6
+        l.sfm_dense_workspace_size.argtypes = [V, C.POINTER(C.c_size_t)]
+        l.sfm_dense_forward.argtypes = [V, V, V, V, V, C.c_size_t, V, V]
+        l.sfm_merge.argtypes = [V] * 7
+        l.sfm_kv_move.argtypes = [V] * 7
         for n in ("sfm_metadata_size", "sfm_workspace_size", "sfm_metadata", "sfm_forward", "sfm_forward_noalloc",
                   "sfm_debug_attended", "sfm_set_profile_events", "sfm_abi_version", "sfm_rope_frequencies",
-                  "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select"):
+                  "sfm_rope", "sfm_kv_store", "sfm_index_scores", "sfm_topk_select", "sfm_dense_workspace_size",
+                  "sfm_dense_forward", "sfm_merge", "sfm_kv_move"):
             getattr(l, n).restype = C.c_int
         _lib = l
     return _lib
@@ -431,6 +464,10 @@ _STORE_PARAMS = struct.Struct("@6if3ifi4q")
 _INDEX_PARAMS = struct.Struct("@12i")
 _INDEX_TENSORS = struct.Struct("@PPqqPPPiPPPPP")
 _TOPK_PARAMS = struct.Struct("@6iq")
+_DENSE_PARAMS = struct.Struct("@16i2f")
+_DENSE_TENSORS = struct.Struct("@PPqqPi11P")
+_MERGE_PARAMS = struct.Struct("@6i")
+_MOVE_PARAMS = struct.Struct("@6i2q")
 _SCORE_TYPES = {torch.float32: 0}
 _SIXTEEN_BIT = {torch.bfloat16: BF16, torch.float16: FP16}
 _INDEX_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
@@ -776,3 +813,253 @@ def select_topk(scores: torch.Tensor, k: int, *, lengths=None, block_size: int =
     if rc:
         raise SfmError("sfm_topk_select", rc)
     return out
+
+
+# ---------------------------------------------------------------------------
+# many queries over the same rows: more kinds of scores and masks, drafted trees
+# ---------------------------------------------------------------------------
+_I64 = torch.int64
+
+
+def _no_gradient(name, x):
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, which this call does not record (use no_grad)")
+
+
+def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right,
+           prefix_lens, key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv,
+           layout_q, layout_kv, split_keys, out, lse, workspace, status, stream):
+    code, dev = _first("q", q, _SIXTEEN_BIT)
+    _no_gradient("q", q)
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left,
+                          win_right, prefix_lens, key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q,
+                          seqused_kv, max_seqlen_kv, layout_q, layout_kv, split_keys, out, lse, workspace, status, None)
+    if layout_q not in ("BSND", "TND") or layout_kv not in _LAYOUTS:
+        raise ValueError(f"layouts: {layout_q!r}, {layout_kv!r}")
+    lq, lkv = _LAYOUTS[layout_q], _LAYOUTS[layout_kv]
+    shape = q.shape
+    if len(shape) != (4 if lq == BSND else 3):
+        raise ValueError("q: BSND has 4 dimensions, TND 3")
+    heads, dim, rows_shape = shape[-2], shape[-1], shape[:-1]
+    if lq == BSND:
+        batch, max_seqlen_q = shape[0], shape[1]
+        tokens = batch * max_seqlen_q
+    elif cu_seqlens_q is None:
+        raise ValueError("cu_seqlens_q: required for TND")
+    else:
+        batch, max_seqlen_q, tokens = _tensor("cu_seqlens_q", cu_seqlens_q).numel() - 1, 0, shape[0]
+    if not (isinstance(kv, torch.Tensor) and kv.dtype is q.dtype and kv.get_device() == dev):
+        raise ValueError(f"kv: needs {q.dtype} on cuda:{dev}")
+    _no_gradient("kv", kv)
+    kshape = kv.shape
+    if len(kshape) == (3 if lkv == TND else 4) and kshape[-2] == 1:
+        kv = kv.squeeze(-2)          # the one KV head
+        kshape = kv.shape
+    if len(kshape) != (2 if lkv == TND else 3) or kshape[-1] != dim:
+        raise ValueError("kv: needs (t, dim), (b, S, dim) or (blocks, block_size, dim), a KV head of 1 before dim or not")
+    if lkv == BSND:
+        if kshape[0] != batch:
+            raise ValueError("kv: needs (b, S, dim)")
+        max_seqlen_kv = kshape[1]
+    rows, row_stride = _rows(kv, "kv")
+    max_seqlen_kv = max_seqlen_kv or rows        # no sequence has more
+    cols = table = words = tree = place = 0
+    each, per_token = (batch,), (tokens,) if lq == TND else rows_shape[:-1]
+    if block_table is not None:
+        if _tensor("block_table", block_table).dim() != 2:
+            raise ValueError("block_table: needs (b, blocks)")
+        cols = block_table.shape[1]
+        table = _address("block_table", block_table, _I32, dev, (batch, cols))
+    if tree_mask is not None:
+        words = _tensor("tree_mask", tree_mask).shape[-1] if _tensor("tree_mask", tree_mask).dim() else 0
+        tree = _address("tree_mask", tree_mask, _I64, dev, per_token + (words,))
+        place = _address("positions", positions, _I32, dev, per_token)
+        if not words:
+            raise ValueError("tree_mask: needs a word per token")
+    ints = [0 if x is None else _address(name, x, _I32, dev, need)
+            for name, x, need in (("cu_seqlens_q", cu_seqlens_q, (batch + 1,)), ("cu_seqlens_kv", cu_seqlens_kv, (batch + 1,)),
+                                  ("seqused_q", seqused_q, each), ("seqused_kv", seqused_kv, each),
+                                  ("prefix_lens", prefix_lens, each), ("key_begin", key_begin, per_token),
+                                  ("key_end", key_end, per_token))]
+    params = _DENSE_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
+                                code, kshape[1] if lkv == PAGED else 0, words, split_keys, out is None, softmax_scale, softcap)
+    tensors = _DENSE_TENSORS.pack(
+        _address("q", q, q.dtype, dev, shape), kv.data_ptr(), row_stride, rows, table, cols, *ints[:4],
+        0 if sinks is None else _address("sinks", sinks, _F32, dev, (heads,)),
+        0 if bias_slopes is None else _address("bias_slopes", bias_slopes, _F32, dev, (heads,)), *ints[4:], tree, place)
+    given = [x for x in (out, lse) if x is not None]
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(rows_shape, dtype=_F32, device=q.device)
+    got = _address("out", out, q.dtype, dev, shape), _address("lse", lse, _F32, dev, rows_shape)
+    for x in given:
+        _no_gradient("out" if x is out else "lse", x)
+    need = C.c_size_t(0)
+    rc = (_lib or lib()).sfm_dense_workspace_size(params, need)
+    if not rc:
+        if workspace is None and need.value:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        room = 0
+        if workspace is not None:
+            if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
+                raise ValueError(f"workspace: needs a contiguous tensor on cuda:{dev}")
+            room = workspace.numel() * workspace.element_size()
+        rc = _lib.sfm_dense_forward(params, tensors, got[0], got[1], workspace.data_ptr() if room else 0, room,
+                                    0 if status is None else _status_address(status, dev), _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_dense_forward", rc)
+    for x in given:
+        if not x.is_inference():
+            _increment_version(x)
+    return out, lse
+
+
+def masked_attention(q: torch.Tensor, kv: torch.Tensor, *, softmax_scale: float = 1.0, softcap: float = 0.0, bias_slopes=None,
+                     sinks=None, mask_mode: int = 3, win_left: int = -1, win_right: int = -1, prefix_lens=None, key_begin=None,
+                     key_end=None, block_table=None, cu_seqlens_q=None, cu_seqlens_kv=None, seqused_q=None, seqused_kv=None,
+                     max_seqlen_q: int = 0, max_seqlen_kv: int = 0, layout_q="BSND", layout_kv="BSND", split_keys: int = 0,
+                     out=None, lse=None, workspace=None, status=None, stream=None):
+    """Attention of q over the shared rows kv (K = V), all queries of a
+    sequence over the same rows: prompts, and single tokens over a cache (see
+    sfm_dense_forward).  Returns (out, q's shape; LSE, fp32, q's shape without
+    its last dimension).
+
+    q: (b, q_s, heads, 512) or TND (tokens, heads, 512), bf16 or fp16, dense;
+    kv: (b, S, 512), (t, 512) or paged (blocks, block_size, 512) of the same
+    dtype, with a KV head of 1 before the values or not, rows may be padded
+    apart.  The scores are softmax_scale q.k, then ``softcap`` tanh(x / softcap)
+    (0: none), then minus ``bias_slopes`` (fp32, heads) times the distance of
+    query and key; ``sinks`` (fp32, heads) count in the denominator only.
+    Query i of q_len sits at p = len - q_len + i, and sees key j if the mask
+    mode allows it (0: all, 3: j <= p, 4: p - win_left <= j <= p + win_right,
+    -1 for no bound) and ``key_begin`` <= j < ``key_end`` (int32, one per
+    token: the bounds of the token's document), or if j < ``prefix_lens``
+    (int32, one per sequence: keys that every token sees).
+
+    ``split_keys``: 0 cuts long ranges of keys so that the GPU is filled; a
+    multiple of 128 cuts them into pieces of that many keys, so that a row's
+    result does not depend on what else is in the batch.  ``max_seqlen_kv`` (TND,
+    paged): a bound on the keys of a sequence, which keeps the workspace small;
+    longer sequences are cut.  ``workspace``: a
+    uint8 tensor to use instead of a new one, sfm_dense_workspace_size bytes,
+    for one call at a time.  Rows of a TND batch behind its last sequence are
+    0 with LSE -inf in new outputs, and stay as they were where ``out`` is given.
+    No gradient is recorded: inputs that require one are refused in grad mode."""
+    return _dense(q, kv, None, None, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right, prefix_lens,
+                  key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv, layout_q,
+                  layout_kv, split_keys, out, lse, workspace, status, stream)
+
+
+def tree_attention(q: torch.Tensor, kv: torch.Tensor, tree_mask: torch.Tensor, positions: torch.Tensor, *,
+                   softmax_scale: float = 1.0, softcap: float = 0.0, bias_slopes=None, sinks=None, mask_mode: int = 3,
+                   win_left: int = -1, win_right: int = -1, block_table=None, cu_seqlens_q=None, cu_seqlens_kv=None,
+                   seqused_q=None, seqused_kv=None, max_seqlen_q: int = 0, max_seqlen_kv: int = 0, layout_q="BSND",
+                   layout_kv="BSND", split_keys: int = 0, out=None, lse=None, workspace=None, status=None, stream=None):
+    """Attention of a tree of drafted tokens over a cache: as masked_attention,
+    but the last q_len keys of a sequence are the drafted tokens' own rows
+    (written before, in the queries' order), of which token i sees those whose
+    bit is set in its row of ``tree_mask`` (int64, (tokens, words): bit k % 64
+    of word k / 64 for drafted token k: the ancestors of i, and i itself).  It
+    sees all keys before them, or with mask_mode 4 those inside the window.
+    ``positions`` (int32, one per token) are the drafted tokens' places in the
+    text (len - q_len + depth), which window and bias go by."""
+    if tree_mask is None or positions is None:
+        raise ValueError("tree_mask and positions are needed")
+    return _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right, None,
+                  None, None, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv, layout_q,
+                  layout_kv, split_keys, out, lse, workspace, status, stream)
+
+
+def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
+    """Join attention results over separate sets of keys (see sfm_merge): outs
+    (up to 8 of (..., heads, dim), bf16 or fp16, dense) with their LSEs (fp32,
+    one per row, any shape) to (out, LSE) over all keys.  ``sinks`` (fp32,
+    heads) count once, so the parts are computed without them.  ``out`` may be
+    one of the parts."""
+    outs, lses = list(outs), list(lses)
+    if not outs or len(outs) != len(lses) or len(outs) > MERGE_MAX_PARTS:
+        raise ValueError(f"outs and lses: need 1 to {MERGE_MAX_PARTS} each, as many of one as of the other")
+    code, dev = _first("outs", outs[0], _SIXTEEN_BIT)
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return merge_attention(outs, lses, sinks=sinks, out=out, lse=lse)
+    x = outs[0]
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError("outs: need (..., heads, dim)")
+    heads, dim, rows = shape[-2], shape[-1], shape[:-1].numel()
+    parts, ends = [], []
+    for o, l in zip(outs, lses):
+        parts.append(_address("outs", o, x.dtype, dev, shape))
+        if _tensor("lses", l).numel() != rows:
+            raise ValueError(f"lses: {l.numel()} values, expected {rows}")
+        ends.append(_address("lses", l, _F32, dev, l.shape))
+        _no_gradient("outs", o)
+        _no_gradient("lses", l)
+    given = [y for y in (out, lse) if y is not None]
+    for y in given:
+        _no_gradient("out" if y is out else "lse", y)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+    elif any(lse.data_ptr() == e for e in ends):
+        raise ValueError("lse: must not be one of lses")
+    n = len(outs)
+    params = _MERGE_PARAMS.pack(rows // heads if heads else 0, heads or 1, dim, n, code, 0)
+    rc = (_lib or lib()).sfm_merge(params, struct.pack(f"@{n}P", *parts), struct.pack(f"@{n}P", *ends),
+                                   0 if sinks is None else _address("sinks", sinks, _F32, dev, (heads,)),
+                                   _address("out", out, x.dtype, dev, shape), _address("lse", lse, _F32, dev, shape[:-1]),
+                                   _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_merge", rc)
+    for y in given:
+        if not y.is_inference():
+            _increment_version(y)
+    return out, lse
+
+
+def move_kv(cache: torch.Tensor, path: torch.Tensor, first: torch.Tensor, *, block_table=None, status=None, stream=None):
+    """Move the rows of the accepted path of every sequence to the front of
+    its drafted rows (see sfm_kv_move): row first[b] + i becomes what row
+    first[b] + path[b, i] was, up to the first negative entry.  path: int32
+    (b, n), growing; first: int32 (b), the place of the first drafted row.
+    cache: (blocks, block_size, row) with ``block_table`` (b, blocks) int32, or
+    (b, S, row); any dtype, rows of a multiple of 16 bytes, a KV head of 1
+    before the values or not.  Returns ``cache``."""
+    if not isinstance(cache, torch.Tensor) or cache.get_device() < 0:
+        raise ValueError("cache: not on a CUDA device" if isinstance(cache, torch.Tensor) else "cache: not a tensor")
+    dev = cache.get_device()
+    _no_gradient("cache", cache)
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return move_kv(cache, path, first, block_table=block_table, status=status)
+    kv = cache.squeeze(-2) if cache.dim() == 4 and cache.shape[-2] == 1 else cache
+    if kv.dim() != 3:
+        raise ValueError("cache: needs (blocks, block_size, row) or (b, S, row)")
+    rows, row_stride = _rows(kv, "cache")
+    if _tensor("path", path).dim() != 2:
+        raise ValueError("path: needs (b, n)")
+    batch, most = path.shape
+    cols = table = 0
+    if block_table is None:
+        if kv.shape[0] != batch:
+            raise ValueError("cache: needs (b, S, row) without a block table")
+    else:
+        if _tensor("block_table", block_table).dim() != 2:
+            raise ValueError("block_table: needs (b, blocks)")
+        cols = block_table.shape[1]
+        table = _address("block_table", block_table, _I32, dev, (batch, cols))
+    params = _MOVE_PARAMS.pack(batch, most, kv.shape[-1] * kv.element_size(), kv.shape[1] if table or cols else 0, kv.shape[1],
+                               cols, row_stride, rows)
+    rc = (_lib or lib()).sfm_kv_move(params, _address("path", path, _I32, dev, (batch, most)),
+                                     _address("first", first, _I32, dev, (batch,)), table, kv.data_ptr(),
+                                     0 if status is None else _status_address(status, dev), _raw_stream(dev))
+    if rc:
+        raise SfmError("sfm_kv_move", rc)
+    if not cache.is_inference():
+        _increment_version(cache)
+    return cache

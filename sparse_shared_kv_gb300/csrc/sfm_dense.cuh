@@ -1,0 +1,104 @@
+// sfm_dense.cuh -- what the kernels of sfm_dense_forward() agree on: their
+// arguments, the lengths of a sequence and the keys that a query sees.
+#pragma once
+
+#include "sfm_internal.cuh"
+
+namespace sfm {
+
+struct DenseArgs {
+    const void *q, *kv;
+    void *out;
+    float *lse;
+    int32_t *status;
+    const int32_t *table, *cu_q, *cu_kv, *used_q, *used_kv, *prefix, *begin, *end, *positions;
+    const float *sinks, *slopes;
+    const uint64_t *tree;
+    int64_t kv_row_stride, kv_rows;
+    int32_t heads, batch, q_s, total_q, max_kv, mode, win_left, win_right, layout_kv, block, cols, words, zero_rest;
+    float scale, cap;
+    FastDiv block_div, heads_div;
+};
+
+__device__ __forceinline__ void dense_status(const DenseArgs &a, int bits)
+{
+    if (a.status) atomicOr(a.status, bits);
+}
+
+// A sequence: its rows of q (the first q_len of q_cap count) and its keys.
+struct DenseSeq {
+    int32_t b, q0, q_cap, q_len, len, prefix;
+    int64_t kv0;              // row of its first key (not paged)
+};
+
+__device__ __forceinline__ int32_t dense_cut(const DenseArgs &a, int64_t v, int64_t lo, int64_t hi)
+{
+    if (v >= lo && v <= hi) return (int32_t)v;
+    dense_status(a, SFM_STATUS_BAD_LENGTH);
+    return (int32_t)(v < lo ? lo : hi);
+}
+
+__device__ __forceinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
+{
+    DenseSeq s;
+    s.b = b;
+    if (a.cu_q) {
+        s.q0 = dense_cut(a, __ldg(a.cu_q + b), 0, a.total_q);
+        s.q_cap = dense_cut(a, __ldg(a.cu_q + b + 1), s.q0, a.total_q) - s.q0;
+    } else {
+        s.q0 = b * a.q_s;
+        s.q_cap = a.q_s;
+    }
+    s.q_len = a.used_q ? dense_cut(a, __ldg(a.used_q + b), 0, s.q_cap) : s.q_cap;
+    int64_t most;
+    s.kv0 = 0;
+    if (a.layout_kv == SFM_LAYOUT_PAGED) {
+        most = (int64_t)a.cols * a.block;
+        if (most > a.max_kv) most = a.max_kv;
+    } else if (a.cu_kv) {
+        s.kv0 = __ldg(a.cu_kv + b);
+        if (s.kv0 < 0 || s.kv0 > a.kv_rows) {
+            dense_status(a, SFM_STATUS_BAD_LENGTH);
+            s.kv0 = a.kv_rows;
+        }
+        int64_t end = __ldg(a.cu_kv + b + 1);
+        if (end > a.kv_rows) {
+            dense_status(a, SFM_STATUS_BAD_LENGTH);
+            end = a.kv_rows;
+        }
+        most = dense_cut(a, end - s.kv0, 0, a.max_kv);
+    } else {
+        s.kv0 = (int64_t)b * a.max_kv;
+        most = a.max_kv;
+    }
+    s.len = a.used_kv ? dense_cut(a, __ldg(a.used_kv + b), 0, most) : (int32_t)most;
+    s.prefix = a.prefix ? min(max(__ldg(a.prefix + b), 0), s.len) : 0;
+    return s;
+}
+
+// What query i of a sequence sees: keys [0, prefix) and [lo, hi); with a tree
+// [lo, hi) among the keys before `first`, and those of its bits from there on.
+struct DenseRow {
+    int32_t p, lo, hi;
+};
+
+__device__ __forceinline__ DenseRow dense_row(const DenseArgs &a, const DenseSeq &s, int i)
+{
+    DenseRow r;
+    const int32_t first = s.len - s.q_len;
+    r.p = a.words ? __ldg(a.positions + s.q0 + i) : first + i;
+    int64_t lo = 0, hi = a.words ? max(first, 0) : s.len;
+    if (a.mode == 3 && !a.words) hi = min(hi, (int64_t)r.p + 1);
+    if (a.mode == 4) {
+        lo = max(lo, (int64_t)r.p - a.win_left);
+        hi = min(hi, (int64_t)r.p + a.win_right + 1);
+    }
+    if (a.begin) lo = max(lo, (int64_t)__ldg(a.begin + s.q0 + i));
+    if (a.end) hi = min(hi, (int64_t)__ldg(a.end + s.q0 + i));
+    if (lo >= hi) lo = hi = 0;
+    r.lo = (int32_t)lo;
+    r.hi = (int32_t)hi;
+    return r;
+}
+
+}  // namespace sfm
