@@ -1,115 +1,847 @@
 // sfm_dense.cu -- attention of many queries over the same rows
 // (sfm_dense_forward): prompts, single tokens over a cache, drafted trees.
+//
+// A tile of the work is 128 rows of Q -- consecutive (token, head) rows of one
+// sequence, whatever the number of heads -- against 128 keys at a time.  A pair
+// of CTAs holds it, 64 rows each, and both products are pair products (M = 128):
+//
+//     S = Q K^T      N = 128 keys, K = 512    CTA c stages keys [64 c, 64 c + 64)
+//     O += P V       N = 2 x 256, K = 128     CTA c stages 256 of the 512 columns of all 128 keys
+//
+// The rows are K and V at once, but a CTA's part of K and its part of V share a
+// quarter of the tile only, so both are copied (TMA, 128 KB per tile and CTA; the second copy
+// hits L2).  O fills half of the tensor memory (64 x 512 fp32 in 128 lanes x 256
+// columns), two S tiles of 64 columns lie beside it.
+//
+// Per CTA, 12 warps:
+//   0      copies: Q of a unit, then K(0), K(1), V(0), K(2), V(1), ... in stages of 16 KB (two boxes of 64 values x 64 rows),
+//          eight of them in a ring
+//   1      products, in the pair's first CTA: S(0); S(i + 1), O += P(i) V(i); ...
+//   2      tensor memory; takes NaN and infinities out of V rows that some row must not see (below)
+//   3      units: which rows and keys come next, two units ahead
+//   4-11   softmax: four threads per row, 32 keys each; running maximum, moved (and O rescaled) only when it grows by more
+//          than 8 in the log2 domain; P in dtype into shared memory; the result at the unit's end
+//
+// A unit is a tile of Q and a piece of its range of keys.  Pieces of a range
+// leave fp32 partial results in the workspace, which a second kernel joins.
+//
+// A weight of 0 for a key that a row does not see leaves NaN where the key's
+// row holds NaN or an infinity.  Such a key has scores that are not finite for
+// every row, so the softmax finds it among the keys it masks; the products
+// then wait until the values that are not finite are zeros in the staged V.
+//
+// Every wait is bounded (2 s); a timeout raises the CTA's abort flag, every role
+// leaves its loop, copies and products in flight are waited for, tensor memory
+// is freed and SFM_STATUS_TIMEOUT is set.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
 #include "sfm_dense.cuh"
+#include "sfm_pair.cuh"
 
 namespace sfm {
 namespace {
 
-constexpr int kD = 512;
-constexpr int kWarps = 8;
-constexpr float kLog2e = 1.4426950408889634f;
+using namespace tc;
 
-template <typename T>
-__device__ __forceinline__ void widen(uint4 v, float *f)
+constexpr int kD = 512;
+constexpr int kThreads = 384;
+constexpr int kRows = 128;                    // rows of Q of a pair
+constexpr int kKeys = 128;                    // keys of a tile
+constexpr int kStages = 8;
+constexpr uint32_t kStageBytes = 16384;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;              // log2 units
+
+constexpr uint32_t Q_OFF = 0;                 // 8 blocks of 64 rows x 64 values
+constexpr uint32_t P_OFF = 65536;             // 2 buffers x 2 blocks of 64 rows x 64 keys
+constexpr uint32_t KV_OFF = P_OFF + 32768;
+constexpr uint32_t MISC_OFF = KV_OFF + kStages * kStageBytes;
+constexpr uint32_t kSmemBytes = MISC_OFF + 3072;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+constexpr uint32_t TM_O = 0, TM_S = 256, kTmemCols = 512;
+
+// barriers (8 bytes each) at MISC_OFF; "first": used in the pair's first CTA
+enum Bar {
+    B_KV_FULL = 0,       // [8] first: both CTAs' halves of a stage have landed
+    B_KV_EMPTY = 8,      // [8] the products that read the stage are done
+    B_Q_FULL = 16,       // first
+    B_Q_EMPTY = 17,      // the unit's last S is done
+    B_S_FULL = 18,       // [2] S of a tile
+    B_P_FULL = 20,       // [2] first: P written, O rescaled, S read, by the 16 softmax warps of both CTAs
+    B_O_DONE = 22,       // [2] O += P V of a tile
+    B_O_FREE = 24,       // first: the 16 softmax warps have read the unit's O
+    B_UNIT_FULL = 25,    // [2]
+    B_UNIT_EMPTY = 27,   // [2]
+    B_FIX = 29,          // rows to be made finite
+    B_FIXED = 30,        // first: both CTAs have
+    B_END = 31,
+    kBars = 32
+};
+constexpr uint32_t EXCH_REL = 256;            // [2][4][64] floats: the row's four maxima (or sums)
+constexpr uint32_t UNIT_REL = EXCH_REL + 2048;   // [2] Unit
+constexpr uint32_t CAND_REL = UNIT_REL + 256;    // first: [2][4] words of keys that may hold NaN or infinities
+constexpr uint32_t FIX_REL = CAND_REL + 32;      // words, first stage, quit
+constexpr uint32_t TMEM_REL = FIX_REL + 32;
+constexpr uint32_t ABORT_REL = TMEM_REL + 4;
+constexpr uint32_t BEAT_REL = ABORT_REL + 4;
+static_assert(kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= 3072, "misc area");
+
+struct Unit {
+    int64_t row0;            // first row of Q (and of the outputs)
+    int64_t kv0;
+    int32_t valid, b, rows, used;      // rows of the tile, and those of queries that count
+    int32_t i0, h0;          // query and head of the first row
+    int32_t q0, q_len, len, prefix;
+    int32_t prefix_tiles, b0, tile0, tiles;    // tiles: [0, prefix_tiles) from key 0, then from key b0; this unit's part
+    int32_t slot, split, splits, bad;  // bad: a block of the range is outside the cache
+};
+static_assert(sizeof(Unit) <= 128, "unit area");
+
+struct Plan {
+    int32_t slots, splits, chunk, box_rows, align, units;
+    uint32_t idesc_s, idesc_o;
+    float4 *part_o;          // [slot][split][128][128]
+    float2 *part_ml;         // [slot][split][128]
+    int4 *head;              // [slot]: splits, rows that count, first row
+    FastDiv slots_div, per_seq_div;
+    int32_t per_seq;         // BSND: tiles per sequence
+};
+
+// First slot of sequence b of a TND batch: at least one more per sequence than whole tiles lie before it, so that every
+// sequence has as many slots as tiles.
+__device__ __forceinline__ int slot_base(const DenseArgs &a, int b)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            f[2 * i] = p.x;
-            f[2 * i + 1] = p.y;
-        }
-    }
+    const int64_t c = min(max(__ldg(a.cu_q + b), 0), a.total_q);
+    return (int)(c * a.heads / kRows) + b;
 }
 
-// One warp per query row and head, one key at a time, with a running maximum
-// and sum; lane l holds values [8 l, 8 l + 8) and [256 + 8 l, 256 + 8 l + 8).
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) sfm_dense_rows_kernel(const DenseArgs a)
+// The largest b with slot_base(b) <= slot, found by the warp, 32 ways at a time.
+__device__ __forceinline__ int find_sequence(const DenseArgs &a, int slot, int lane)
 {
-    grid_follow();
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)a.total_q * a.heads, row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int t = (int)(row / a.heads), h = (int)(row % a.heads);
-    int b = 0;
+    int lo = 0, n = a.batch;
+    while (n > 1) {
+        const int step = (n + 31) / 32, b = lo + lane * step;
+        const bool below = lane * step < n && (lane == 0 || slot_base(a, b) <= slot);
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int warp_min(int v) { return __reduce_min_sync(0xffffffffu, v); }
+__device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Cache row of key j (a multiple of the box's rows, so that its page holds the whole box), or a row behind the cache, which
+// the copies fill with zeros.
+__device__ __forceinline__ int32_t box_row(const DenseArgs &a, int b, int64_t kv0, int len, int j, bool *bad)
+{
+    if (j >= len) return (int32_t)a.kv_rows;
+    if (a.layout_kv != SFM_LAYOUT_PAGED) return (int32_t)(kv0 + j);
+    const int blk = (int)fdiv((uint32_t)j, a.block_div);
+    const int32_t id = __ldg(a.table + (int64_t)b * a.cols + blk);
+    if (id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows) {
+        *bad = true;
+        return (int32_t)a.kv_rows;
+    }
+    return id * a.block + (j - blk * a.block);
+}
+
+// Unit u, worked out by the whole warp.  False: nothing to do.
+__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, int u, int lane, Unit &w)
+{
+    const int split = (int)fdiv((uint32_t)u, pl.slots_div), slot = pl.slots - 1 - (u - split * pl.slots);
+    int b, k;
     if (a.cu_q) {
-        while (b + 1 < a.batch && __ldg(a.cu_q + b + 1) <= t) ++b;
+        b = find_sequence(a, slot, lane);
+        k = slot - slot_base(a, b);
     } else {
-        b = t / a.q_s;
+        b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
+        k = slot - b * pl.per_seq;
     }
     const DenseSeq s = dense_seq(a, b);
-    const int i = t - s.q0;
-    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * kD);
-    if (i < 0 || i >= s.q_cap) {
-        if (a.zero_rest) {
-            out[lane] = out[lane + 32] = make_uint4(0, 0, 0, 0);
-            if (a.lse && lane == 0) a.lse[row] = -INFINITY;
-        }
-        return;
+    const int64_t first_row = (int64_t)k * kRows, all = (int64_t)s.q_cap * a.heads;
+    if (k < 0 || first_row >= all) {
+        if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(0, 0, 0, 0);
+        return false;
     }
-    float q[16], o[16] = {}, m = -INFINITY, l = 0.f;
-    widen<T>(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + row * kD)[lane], q);
-    widen<T>(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + row * kD)[lane + 32], q + 8);
-    if (i < s.q_len) {
-        const DenseRow r = dense_row(a, s, i);
-        const int first = s.len - s.q_len;
-        for (int j = 0; j < s.len; ++j) {
-            bool seen = (j >= r.lo && j < r.hi) || j < s.prefix;
-            int64_t pos = j;
-            if (a.words && j >= first) {
-                const int k = j - first;
-                pos = __ldg(a.positions + s.q0 + k);
-                seen = k < 64 * a.words && (__ldg(a.tree + (int64_t)t * a.words + (k >> 6)) >> (k & 63) & 1);
-                if (a.mode == 4 && (pos < (int64_t)r.p - a.win_left || pos > (int64_t)r.p + a.win_right)) seen = false;
+    w.row0 = (int64_t)s.q0 * a.heads + first_row;
+    w.rows = (int32_t)min((int64_t)kRows, all - first_row);
+    w.used = (int32_t)min(max((int64_t)s.q_len * a.heads - first_row, (int64_t)0), (int64_t)w.rows);
+    w.i0 = (int32_t)fdiv((uint32_t)first_row, a.heads_div);
+    w.h0 = (int32_t)(first_row - (int64_t)w.i0 * a.heads);
+    // the keys that any of the tile's queries sees
+    int lo = INT32_MAX, hi = 0;
+    if (w.used > 0) {
+        const int i1 = (int)fdiv((uint32_t)(first_row + w.used - 1), a.heads_div);
+        for (int i = w.i0 + lane; i <= i1; i += 32) {
+            const DenseRow r = dense_row(a, s, i);
+            if (r.hi > r.lo) {
+                lo = min(lo, r.lo);
+                hi = max(hi, r.hi);
             }
-            if (!seen) continue;
-            int64_t at = s.kv0 + j;
-            if (a.layout_kv == SFM_LAYOUT_PAGED) {
-                const int id = __ldg(a.table + (int64_t)b * a.cols + j / a.block);
-                at = (int64_t)id * a.block + j % a.block;
-                if (id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows) {
-                    if (lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
-                    continue;
+        }
+        if (a.words) {
+            lo = min(lo, max(s.len - s.q_len, 0));
+            hi = s.len;
+        }
+    }
+    lo = warp_min(lo);
+    hi = warp_max(hi);
+    w.prefix = w.used > 0 ? s.prefix : 0;
+    w.prefix_tiles = (w.prefix + kKeys - 1) / kKeys;
+    w.b0 = w.prefix_tiles * kKeys;
+    int tiles = w.prefix_tiles;
+    if (hi > lo) {
+        w.b0 = max(w.b0, lo & ~(pl.align - 1));
+        if (hi > w.b0) tiles += (hi - w.b0 + kKeys - 1) / kKeys;
+    }
+    w.splits = tiles > pl.chunk ? min((tiles + pl.chunk - 1) / pl.chunk, pl.splits) : 1;
+    const int per = (tiles + w.splits - 1) / w.splits;
+    if (per > 0) w.splits = (tiles + per - 1) / per;
+    if (split >= w.splits) return false;
+    w.tile0 = min(split * per, tiles);
+    w.tiles = min(per, tiles - w.tile0);
+    w.valid = 1;
+    w.b = b;
+    w.kv0 = s.kv0;
+    w.q0 = s.q0;
+    w.q_len = s.q_len;
+    w.len = s.len;
+    w.slot = slot;
+    w.split = split;
+    if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, 0);
+    w.bad = 0;
+    if (a.layout_kv == SFM_LAYOUT_PAGED) {
+        bool bad = false;
+        for (int i = lane; i < w.tiles * (kKeys / 16); i += 32) {
+            const int t = w.tile0 + i / (kKeys / 16);
+            const int j = (t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys) + i % (kKeys / 16) * 16;
+            box_row(a, b, 0, w.len, j, &bad);
+        }
+        w.bad = __any_sync(0xffffffffu, bad);
+        if (w.bad && lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
+    }
+    return true;
+}
+
+__device__ __forceinline__ int tile_key(const Unit &w, int i)
+{
+    const int t = w.tile0 + i;
+    return t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys;
+}
+
+// bits [lo, hi) of a word whose bit 0 stands for key j0
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi, int j0)
+{
+    const int l = min(max(lo - j0, 0), 32), h = min(max(hi - j0, 0), 32);
+    const uint32_t up = h >= 32 ? 0xffffffffu : (1u << h) - 1u, down = l >= 32 ? 0xffffffffu : (1u << l) - 1u;
+    return h > l ? up & ~down : 0u;
+}
+
+__device__ __forceinline__ uint32_t pack(float x, float y, bool bf16)
+{
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The 256 softmax threads meet; true if all of them say so.
+__device__ __forceinline__ bool rows_meet(bool ok)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(all)
+                 : "r"(ok ? 1u : 0u)
+                 : "memory");
+    return all != 0;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap kv_map)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    uint8_t *const misc = smem + MISC_OFF;
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + ABORT_REL);
+    volatile int *const beat = reinterpret_cast<volatile int *>(misc + BEAT_REL);
+    float *const exch = reinterpret_cast<float *>(misc + EXCH_REL);
+    volatile uint32_t *const cand_words = reinterpret_cast<volatile uint32_t *>(misc + CAND_REL);
+    volatile uint32_t *const fix_words = reinterpret_cast<volatile uint32_t *>(misc + FIX_REL);
+    const bool bf16 = (pl.idesc_s >> 7 & 7u) == 1u;
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+    if (warp == 0) {
+        prefetch_map(&q_map);
+        prefetch_map(&kv_map);
+    }
+    if (tid == 0) {
+        auto init = [&](int i, int n) { mbar_init(sb + MISC_OFF + 8u * i, n); };
+        for (int i = 0; i < kStages; ++i) {
+            init(B_KV_FULL + i, 1);
+            init(B_KV_EMPTY + i, 1);
+        }
+        init(B_Q_FULL, 1);
+        init(B_Q_EMPTY, 1);
+        for (int i = 0; i < 2; ++i) {
+            init(B_S_FULL + i, 1);
+            init(B_P_FULL + i, 16);
+            init(B_O_DONE + i, 1);
+            init(B_UNIT_FULL + i, 1);
+            init(B_UNIT_EMPTY + i, rank == 0 ? 10 : 9);
+        }
+        init(B_O_FREE, 16);
+        init(B_FIX, 1);
+        init(B_FIXED, 2);
+        init(B_END, 1);
+        for (int i = 0; i < 8; ++i) cand_words[i] = fix_words[i] = 0;
+        *abort_flag = 0;
+        *beat = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) pair_alloc(sb + MISC_OFF + TMEM_REL, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(misc + TMEM_REL), 0);
+    sb = __shfl_sync(0xffffffffu, sb, 0);
+    const uint32_t bar0 = sb + MISC_OFF;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const uint32_t first0 = in_cta(bar0, 0);
+    auto first_bar = [&](int i) { return first0 + 8u * static_cast<uint32_t>(i); };
+    Unit *const units = reinterpret_cast<Unit *>(misc + UNIT_REL);
+    grid_follow();
+
+    if (warp == 3) {
+        // ======================= units =======================
+        int n = 0;
+        bool ok = true;
+        for (int u = cluster; ok; u += clusters) {
+            Unit w;
+            const bool end = u >= pl.units;
+            if (end) w.valid = 0;
+            else if (!make_unit(a, pl, u, lane, w)) continue;
+            const int slot = n & 1;
+            if (n >= 2 && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), (n >> 1) - 1 & 1, abort_flag)) break;
+            if (lane == 0) {
+                units[slot] = w;
+                mbar_arrive(bar(B_UNIT_FULL + slot));
+            }
+            __syncwarp();
+            ++n;
+            if (end) break;
+        }
+    } else if (warp == 0) {
+        // ======================= copies =======================
+        int n = 0, nq = 0, c = 0;                  // units, units with keys, stages
+        const int boxes = 64 / pl.box_rows;        // per stage and 64 values
+        bool ok = true;
+        const bool one = elect_one();
+        while (ok) {
+            const int us = n & 1;
+            if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
+            const Unit w = units[us];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
+            ++n;
+            if (!w.valid) break;
+            if (w.tiles == 0) continue;
+            if (nq > 0 && !pair_wait_warp(bar(B_Q_EMPTY), nq - 1 & 1, abort_flag)) break;
+            ++nq;
+            if (one) {
+                if (rank == 0) expect_tx(bar(B_Q_FULL), 2 * 65536);
+                for (int d = 0; d < 8; ++d)
+                    pair_load(sb + Q_OFF + d * 8192u, &q_map, d * 64, (int)w.row0 + 64 * (int)rank, first_bar(B_Q_FULL));
+            }
+            __syncwarp();
+            // lane l holds the row of the box of keys [l box_rows, (l + 1) box_rows) of a tile
+            bool bad = false;
+            auto rows_of = [&](int i) {
+                return lane < 2 * boxes && i < w.tiles ? box_row(a, w.b, w.kv0, w.len, tile_key(w, i) + lane * pl.box_rows, &bad) : 0;
+            };
+            auto stage = [&](int x, int half, int32_t row) {
+                const int st = c & (kStages - 1), use = c / kStages;
+                ++c;
+                if (use > 0 && !pair_wait_warp(bar(B_KV_EMPTY + st), use - 1 & 1, abort_flag)) return false;
+                int32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
+                if (one) {
+                    if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
+                    const uint32_t dst = sb + KV_OFF + st * kStageBytes;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k < boxes) {
+                            pair_load(dst + k * pl.box_rows * 128u, &kv_map, x, y[k], first_bar(B_KV_FULL + st));
+                            pair_load(dst + 8192u + k * pl.box_rows * 128u, &kv_map, x + 64, y[k], first_bar(B_KV_FULL + st));
+                        }
+                    }
+                }
+                __syncwarp();
+                return true;
+            };
+            int32_t before = 0, now = rows_of(0), next = rows_of(1);
+            for (int i = 0; i <= w.tiles && ok; ++i) {
+                if (i < w.tiles)
+                    for (int k = 0; k < 4 && ok; ++k) ok = stage(128 * k, (int)rank, now);
+                if (i > 0)
+                    for (int k = 0; k < 4 && ok; ++k) ok = stage(256 * (k >> 1) + 128 * (int)rank, k & 1, before);
+                before = now;
+                now = next;
+                next = rows_of(i + 2);
+            }
+        }
+    } else if (warp == 1) {
+        // ======================= products =======================
+        if (rank == 0) {
+            int n = 0, nq = 0, c = 0, g = 0, fixes = 0;      // units, units with keys, stages, tiles
+            bool ok = true;
+            const uint32_t id_s = pl.idesc_s, id_o = pl.idesc_o;
+            auto scores = [&](int gi) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int st = c & (kStages - 1);
+                    if (!pair_wait_warp(bar(B_KV_FULL + st), c / kStages & 1, abort_flag)) return false;
+                    ++c;
+                    tc_fence_after();
+                    const uint32_t stg = sb + KV_OFF + st * kStageBytes;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t sub = (j >> 2) * 8192u + (j & 3) * 32u;
+                            pair_mma(tmem + TM_S + (gi & 1) * 64, sdesc_sw128(sb + Q_OFF + k * 16384u + sub, 16, 1024),
+                                     sdesc_sw128(stg + sub, 16, 1024), id_s, (k | j) > 0);
+                        }
+                        pair_commit(bar(B_KV_EMPTY + st));
+                        if (k == 3) pair_commit(bar(B_S_FULL + (gi & 1)));
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            while (ok) {
+                const int us = n & 1;
+                if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
+                const int valid = __shfl_sync(0xffffffffu, units[us].valid, 0), tiles = __shfl_sync(0xffffffffu, units[us].tiles, 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
+                ++n;
+                if (!valid) break;
+                if (tiles == 0) continue;
+                if (!pair_wait_warp(bar(B_Q_FULL), nq & 1, abort_flag)) break;
+                tc_fence_after();
+                ok = scores(g);
+                for (int i = 0; i < tiles && ok; ++i) {
+                    const int gi = g + i, buf = gi & 1;
+                    if (i + 1 < tiles) ok = scores(gi + 1);
+                    if ((i + 2 == tiles || tiles == 1) && elect_one()) pair_commit(bar(B_Q_EMPTY));
+                    __syncwarp();
+                    ok = ok && pair_wait_warp(bar(B_P_FULL + buf), gi >> 1 & 1, abort_flag);
+                    if (i == 0 && nq > 0) ok = ok && pair_wait_warp(bar(B_O_FREE), nq - 1 & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t found = lane < 4 ? cand_words[4 * buf + lane] : 0u;
+                    if (__any_sync(0xffffffffu, found != 0)) {
+                        // the staged V, made finite in both CTAs before it is used
+                        for (int k = 0; k < 4 && ok; ++k)
+                            ok = pair_wait_warp(bar(B_KV_FULL + (c + k & (kStages - 1))), (c + k) / kStages & 1, abort_flag);
+                        if (!ok) break;
+                        for (uint32_t r = 0; r < 2; ++r) {
+                            const uint32_t to = in_cta(bar0 + FIX_REL, r);
+                            if (lane < 4) store_remote(to + 4 * lane, found);
+                            if (lane == 4) store_remote(to + 16, (uint32_t)c & (kStages - 1));
+                        }
+                        if (lane < 4) cand_words[4 * buf + lane] = 0;
+                        __syncwarp();
+                        if (lane < 2) arrive_remote(in_cta(bar(B_FIX), lane));
+                        __syncwarp();
+                        ok = pair_wait_warp(bar(B_FIXED), fixes & 1, abort_flag);
+                        ++fixes;
+                        if (!ok) break;
+                        fence_proxy_async_smem();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int st = c & (kStages - 1);
+                        ok = ok && pair_wait_warp(bar(B_KV_FULL + st), c / kStages & 1, abort_flag);
+                        ++c;
+                        tc_fence_after();
+                        const uint32_t stg = sb + KV_OFF + st * kStageBytes;
+                        if (elect_one() && ok) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                pair_mma(tmem + TM_O + (k >> 1) * 128, sdesc_sw128(sb + P_OFF + buf * 16384u + (k & 1) * 8192u + j * 32u, 16, 1024),
+                                         sdesc_sw128(stg + j * 2048u, 8192, 1024), id_o, i > 0 || (k & 1) || j > 0);
+                            pair_commit(bar(B_KV_EMPTY + st));
+                            if (k == 3) pair_commit(bar(B_O_DONE + buf));
+                        }
+                        __syncwarp();
+                    }
+                }
+                ++nq;
+                g += tiles;
+            }
+            // nothing of this warp's is under way when tensor memory is freed
+            if (elect_one()) pair_commit(bar(B_END));
+            __syncwarp();
+            const uint64_t t0 = globaltimer_ns();
+            while (!pair_try_wait(bar(B_END), 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+            }
+            __syncwarp();
+            if (lane < 2) {
+                store_remote(in_cta(bar0 + FIX_REL, lane) + 20, 1u);
+                arrive_remote(in_cta(bar(B_FIX), lane));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ======================= V rows made finite =======================
+        for (int n = 0;; ++n) {
+            // as long as tiles go by there may be nothing to do
+            bool ok = true;
+            if (lane == 0) {
+                uint64_t t0 = globaltimer_ns();
+                int seen = *beat;
+                while (!pair_try_wait(bar(B_FIX), n & 1)) {
+                    if (*abort_flag) { ok = false; break; }
+                    if (*beat != seen) {
+                        seen = *beat;
+                        t0 = globaltimer_ns();
+                    } else if (globaltimer_ns() - t0 > 2 * kTimeoutNs) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
                 }
             }
-            const uint4 *key = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.kv) + at * a.kv_row_stride);
-            float k[16], x = 0.f;
-            widen<T>(__ldg(key + lane), k);
-            widen<T>(__ldg(key + lane + 32), k + 8);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+            if (ok) ok = pair_try_wait(bar(B_FIX), n & 1);        // every lane has seen the phase
+            if (!__all_sync(0xffffffffu, ok) || fix_words[5]) break;
+            const uint16_t inf = bf16 ? 0x7f80 : 0x7c00;
+            for (int w = 0; w < 4; ++w) {
+                uint32_t m = fix_words[w];
+                while (m) {
+                    const int key = 32 * w + __ffs(m) - 1;
+                    m &= m - 1;
+                    // the key's 256 values in this CTA: two stages (column halves) of two blocks, 128 bytes each
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t st = fix_words[4] + 2 * (q >> 1) + (key >> 6) & (kStages - 1);
+                        uint16_t *row = reinterpret_cast<uint16_t *>(smem + KV_OFF + st * kStageBytes + (q & 1) * 8192 + (key & 63) * 128);
+                        for (int k = lane; k < 64; k += 32)
+                            if ((row[k] & inf) == inf) row[k] = 0;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_remote(first_bar(B_FIXED));
+        }
+    } else {
+        // ======================= softmax =======================
+        const int part = (warp - 4) & 3, wg = (warp - 4) >> 2;
+        const int r = (part & 1) * 32 + lane, half = part >> 1;     // row; keys and columns of O in halves
+        const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+        const int quarter = half * 2 + wg, c0 = half * 64 + wg * 32;      // this thread's keys of a tile: [c0, c0 + 32)
+        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, to_cap = a.cap > 0.f ? 2.f * sl2 / a.cap : 0.f;
+        uint8_t *const p_row = smem + P_OFF + half * 8192;
+        if (a.zero_rest && a.cu_q) {
+            // rows of no sequence
+            const int64_t lo = (int64_t)min(max(__ldg(a.cu_q), 0), a.total_q) * a.heads,
+                          hi = (int64_t)min(max(__ldg(a.cu_q + a.batch), 0), a.total_q) * a.heads, all = (int64_t)a.total_q * a.heads;
+            const int64_t rest = lo + max(all - max(hi, lo), (int64_t)0);
+            for (int64_t i = (int64_t)blockIdx.x * 256 + (tid - 128); i < rest * 64; i += (int64_t)gridDim.x * 256) {
+                const int64_t k = i >> 6, row = k < lo ? k : max(hi, lo) + (k - lo);
+                reinterpret_cast<uint4 *>(a.out)[row * 64 + (i & 63)] = make_uint4(0, 0, 0, 0);
+                if (a.lse && (i & 63) == 0) a.lse[row] = -INFINITY;
+            }
+        }
+        int n = 0, g = 0, ex = 0;
+        bool ok = true;
+        // all 256 threads' values of a row, four of them, through shared memory
+        // (a role that gave up ends the loops of all of them at the same place)
+        auto row_values = [&](float v, float (&got)[4]) {
+            float *e = exch + (ex & 1) * 256;
+            ++ex;
+            e[quarter * 64 + r] = v;
+            ok = rows_meet(ok);
 #pragma unroll
-            for (int d = 0; d < 16; ++d) x = fmaf(q[d], k[d], x);
+            for (int k = 0; k < 4; ++k) got[k] = e[k * 64 + r];
+        };
+        while (ok) {
+            const int us = n & 1;
+            if (!rows_meet(pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag))) break;
+            const Unit w = units[us];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
+            ++n;
+            if (!w.valid) break;
+            const int R = 64 * (int)rank + r;
+            const bool live = R < w.used;
+            const int hr = w.h0 + R, di = (int)fdiv((uint32_t)hr, a.heads_div), i_q = w.i0 + di, head = hr - di * a.heads;
+            DenseRow row = {0, 0, INT32_MAX};        // rows that do not count see all: nothing to mask
+            const uint64_t *tree = nullptr;
+            const int first = w.len - w.q_len;
+            float slope = 0.f;
+            if (live) {
+                DenseSeq s;
+                s.q0 = w.q0;
+                s.q_len = w.q_len;
+                s.len = w.len;
+                row = dense_row(a, s, i_q);
+                if (a.words) tree = a.tree + (int64_t)(w.q0 + i_q) * a.words;
+                if (a.slopes) slope = __ldg(a.slopes + head) * kLog2e;
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < w.tiles; ++i) {
+                const int gi = g + i, buf = gi & 1, j0 = tile_key(w, i) + c0;
+                // what this row sees of its 32 keys
+                uint32_t vis = bits_between(row.lo, row.hi, j0);
+                if (live) {
+                    vis |= bits_between(0, w.prefix, j0);
+                    if (tree && j0 + 32 > first && j0 < w.len) {
+                        // drafted keys: bits [j0 - first, j0 - first + 32) of the mask
+                        const int o = j0 - first;
+                        uint32_t bits;
+                        if (o >= 0) {
+                            const int word = o >> 6, sh = o & 63;
+                            const uint64_t x0 = word < a.words ? __ldg(tree + word) : 0, x1 = word + 1 < a.words ? __ldg(tree + word + 1) : 0;
+                            bits = (uint32_t)(sh ? x0 >> sh | x1 << (64 - sh) : x0);
+                        } else {
+                            bits = (uint32_t)(__ldg(tree) << -o);
+                        }
+                        bits &= bits_between(max(first, 0), w.len, j0);
+                        if (a.mode == 4) {
+                            for (uint32_t left = bits; left; left &= left - 1) {
+                                const int c = __ffs(left) - 1;
+                                const int64_t pos = __ldg(a.positions + w.q0 + o + c);
+                                if (pos < (int64_t)row.p - a.win_left || pos > (int64_t)row.p + a.win_right) bits &= ~(1u << c);
+                            }
+                        }
+                        vis |= bits;
+                    }
+                    if (w.bad) {
+                        bool bad = false, worse = false;
+                        box_row(a, w.b, 0, w.len, j0, &bad);
+                        box_row(a, w.b, 0, w.len, j0 + 16, &worse);
+                        if (bad) vis &= 0xffff0000u;
+                        if (worse) vis &= 0x0000ffffu;
+                    }
+                }
+                ok = ok && pair_wait_warp(bar(B_S_FULL + buf), gi >> 1 & 1, abort_flag);
+                tc_fence_after();
+                uint32_t raw[32];
+                tmem_ld32(tmem + lanes + TM_S + buf * 64 + wg * 32, raw);
+                tmem_wait_ld();
+                if (part == 0 && wg == 0 && lane == 0) *beat = gi;
+                float y[32];
+                if (a.cap > 0.f) {
+                    // tanh z = 1 - 2 / (e^2z + 1): off by some 2^-23 of the cap, which is what a score of its size has
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            x *= a.scale;
-            if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
-            if (a.slopes) x -= a.slopes[h] * fabsf((float)(r.p - pos));
-            const float top = x > m || x != x ? x : m, old = top == -INFINITY ? 1.f : expf(m - top);
-            const float e = top == -INFINITY ? 0.f : expf(x - top);
-            l = l * old + e;
+                    for (int c = 0; c < 32; ++c)
+                        y[c] = fmaf(__fdividef(-2.f, fast_exp2(__uint_as_float(raw[c]) * to_cap) + 1.f), cap2, cap2);
+                } else {
 #pragma unroll
-            for (int d = 0; d < 16; ++d) o[d] = fmaf(e, k[d], o[d] * old);
-            m = top;
+                    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(raw[c]) * sl2;
+                }
+                if (a.slopes) {
+                    if (!a.words || j0 + 31 < first) {
+                        const float d0 = (float)(row.p - j0);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) y[c] = fmaf(-slope, fabsf(d0 - (float)c), y[c]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (!(vis >> c & 1)) continue;
+                            const int k = j0 + c - first;
+                            y[c] = fmaf(-slope, fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k)))), y[c]);
+                        }
+                    }
+                }
+                if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (!(fabsf(__uint_as_float(raw[c])) < INFINITY)) odd |= 1u << c;
+                        if (!(vis >> c & 1)) y[c] = -INFINITY;
+                    }
+                    odd = __reduce_or_sync(0xffffffffu, odd & ~vis);
+                    if (odd && lane == 0) or_remote(first0 + CAND_REL + 16u * buf + 4u * quarter, odd);
+                }
+                float top = -INFINITY, got[4];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) top = fmaxf(top, y[c]);
+                row_values(top, got);
+                if (!ok) break;
+                top = fmaxf(fmaxf(got[0], got[1]), fmaxf(got[2], got[3]));
+                float alpha = 1.f;
+                if (top > m + kRescale || m == -INFINITY) {      // the first tile that the row sees, or a maximum that left the range
+                    if (m != -INFINITY) alpha = fast_exp2(m - top);
+                    m = top;
+                    l *= alpha;
+                }
+                const float m_use = m == -INFINITY ? 0.f : m;
+                uint32_t pk[16];
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float p0 = fast_exp2(y[2 * c] - m_use), p1 = fast_exp2(y[2 * c + 1] - m_use);
+                    sum0 += p0;
+                    sum1 += p1;
+                    pk[c] = pack(p0, p1, bf16);
+                }
+                l += sum0 + sum1;
+                // P's buffer is free once O += P V of the tile before the last is done
+                if (gi >= 2 && ok) ok = pair_wait_warp(bar(B_O_DONE + buf), (gi >> 1) - 1 & 1, abort_flag);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(p_row + buf * 16384 + sw128(r, wg * 4 + c)) =
+                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if (ok) ok = pair_wait_warp(bar(B_O_DONE + (buf ^ 1)), (gi - 1) >> 1 & 1, abort_flag);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        tmem_ld32(tmem + lanes + TM_O + wg * 128 + c, raw);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * alpha);
+                        tmem_st32(tmem + lanes + TM_O + wg * 128 + c, raw);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_remote(first_bar(B_P_FULL + buf));
+            }
+            if (!rows_meet(ok)) break;
+            // the row's result: columns [256 wg + 128 half, + 128) of O
+            if (w.tiles > 0) {
+                const int last = g + w.tiles - 1;
+                if (ok) ok = pair_wait_warp(bar(B_O_DONE + (last & 1)), last >> 1 & 1, abort_flag);
+                tc_fence_after();
+            }
+            float got[4];
+            row_values(l, got);
+            if (!ok) break;
+            l = (got[0] + got[1]) + (got[2] + got[3]);
+            const bool whole = w.splits == 1;
+            const int64_t out_row = w.row0 + R;
+            float inv = 0.f;
+            const bool empty = m == -INFINITY && l == 0.f;      // (a row of NaN has no maximum)
+            if (live && !empty) inv = 1.f / (a.sinks && whole ? l + fast_exp2(__ldg(a.sinks + head) * kLog2e - m) : l);
+            const int64_t part_row = ((int64_t)w.slot * pl.splits + w.split) * kRows + R;
+            if (quarter == 0) {
+                if (whole || !live) {
+                    if (a.lse && R < w.rows && (live || w.split == 0))
+                        a.lse[out_row] = live && !empty ? (m + log2f(l)) * kLn2 : -INFINITY;
+                } else {
+                    pl.part_ml[part_row] = make_float2(m, l);
+                }
+            }
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t o[32];
+                if (w.tiles > 0) {
+                    tmem_ld32(tmem + lanes + TM_O + wg * 128 + c, o);
+                    tmem_wait_ld();
+                }
+                const int col = 256 * wg + 128 * half + c;
+                if (!live || whole) {
+                    if (R < w.rows && (live || w.split == 0)) {
+                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_row * kD + col);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = inv != 0.f ? pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv, bf16) : 0u;
+                            to[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                } else {
+                    float4 *to = pl.part_o + part_row * (kD / 4) + col / 4;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        to[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                            __uint_as_float(o[4 * k + 3]));
+                }
+            }
+            if (w.tiles > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(first_bar(B_O_FREE));
+            }
+            g += w.tiles;
         }
     }
-    const float inv = m == -INFINITY ? 0.f : 1.f / (a.sinks ? l + expf(a.sinks[h] - m) : l);
-    uint16_t v[16];
-#pragma unroll
-    for (int d = 0; d < 16; ++d) {
-        const T x = static_cast<T>(o[d] * inv);
-        v[d] = *reinterpret_cast<const uint16_t *>(&x);
+
+    __syncwarp();
+    if (*abort_flag) {
+        // copies of a role that gave up may still be landing
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+        if (tid == 0) dense_status(a, SFM_STATUS_TIMEOUT);
     }
-    out[lane] = *reinterpret_cast<const uint4 *>(v);
-    out[lane + 32] = *reinterpret_cast<const uint4 *>(v + 8);
-    if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(l);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 2) pair_dealloc(tmem, kTmemCols);
+}
+
+// Partial results of the pieces of a tile's keys, joined: a warp per row, four
+// times four values per lane.
+__global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, const Plan pl)
+{
+    grid_follow();
+    const int slot = blockIdx.x >> 4, r = (blockIdx.x & 15) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 head = pl.head[slot];
+    if (head.x <= 1 || r >= head.y) return;
+    const int64_t base = (int64_t)slot * pl.splits * kRows + r;
+    float m = -INFINITY, l = 0.f;
+    bool empty = true;
+    for (int s = 0; s < head.x; ++s) {
+        const float2 ml = pl.part_ml[base + s * kRows];
+        m = fmaxf(m, ml.x);
+        empty &= ml.x == -INFINITY && ml.y == 0.f;
+    }
+    float4 o[4] = {};
+    for (int s = 0; s < head.x; ++s) {
+        const float2 ml = pl.part_ml[base + s * kRows];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float e = fast_exp2(ml.x - m);
+        l = fmaf(e, ml.y, l);
+        const float4 *from = pl.part_o + (base + s * kRows) * (kD / 4) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = from[32 * k];
+            o[k].x = fmaf(e, v.x, o[k].x);
+            o[k].y = fmaf(e, v.y, o[k].y);
+            o[k].z = fmaf(e, v.z, o[k].z);
+            o[k].w = fmaf(e, v.w, o[k].w);
+        }
+    }
+    const int64_t row = (int64_t)head.z + r;
+    const bool bf16 = (pl.idesc_s >> 7 & 7u) == 1u;
+    float inv = 0.f;
+    if (!empty) inv = 1.f / (a.sinks ? l + fast_exp2(__ldg(a.sinks + row % a.heads) * kLog2e - m) : l);
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        out[32 * k] = inv != 0.f ? make_uint2(pack(o[k].x * inv, o[k].y * inv, bf16), pack(o[k].z * inv, o[k].w * inv, bf16)) : make_uint2(0u, 0u);
+    if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 int dense_check(const sfm_dense_params *pp)
@@ -136,6 +868,94 @@ int dense_check(const sfm_dense_params *pp)
     return SFM_OK;
 }
 
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+// the driver's encoder of TMA descriptors (a pure host function), looked up once
+EncodeFn encoder()
+{
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows)
+{
+    const EncodeFn encode = encoder();
+    if (!encode) return SFM_ERR_CUDA;
+    const cuuint64_t dims[2] = {kD, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    const CUresult r = encode(map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                              const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SFM_OK : SFM_ERR_CUDA;
+}
+
+int64_t dense_tokens(const sfm_dense_params &p)
+{
+    return p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
+}
+
+// How the work is cut, from what the host knows, for a GPU that holds `clusters` pairs.
+int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
+{
+    const int64_t tokens = dense_tokens(p), rows = tokens * p.num_heads;
+    pl->per_seq = (int32_t)(((int64_t)p.max_seqlen_q * p.num_heads + kRows - 1) / kRows);
+    const int64_t slots = p.layout_q == SFM_LAYOUT_TND ? rows / kRows + p.batch_size : (int64_t)p.batch_size * pl->per_seq;
+    const int64_t tiles = ((int64_t)p.max_seqlen_kv + kKeys - 1) / kKeys + 2;
+    int64_t chunk = tiles;
+    if (p.split_keys) {
+        chunk = p.split_keys / kKeys;
+    } else if (slots < 2 * (int64_t)clusters) {
+        const int64_t pieces = 2 * (int64_t)clusters / (slots > 0 ? slots : 1);
+        chunk = (tiles + pieces - 1) / pieces;
+        if (chunk < 4) chunk = 4;
+    }
+    const int64_t splits = (tiles + chunk - 1) / chunk;
+    if (slots * splits > INT32_MAX - 2 * (int64_t)clusters) return SFM_ERR_UNSUPPORTED;
+    pl->slots = (int32_t)slots;
+    pl->splits = (int32_t)splits;
+    pl->chunk = (int32_t)chunk;
+    pl->units = (int32_t)(slots * splits);
+    return SFM_OK;
+}
+
+// workspace: partial rows, then their maxima and sums, then a word of four integers per slot
+size_t dense_bytes(const Plan &pl)
+{
+    if (pl.splits <= 1) return 0;
+    return (size_t)pl.units * kRows * (kD * 4 + 8) + (size_t)pl.slots * 16;
+}
+
+// Pairs of CTAs that the current device holds at once.
+int dense_clusters(int *device, int *clusters)
+{
+    static std::atomic<int> known[kMaxDevices];
+    if (cudaGetDevice(device) != cudaSuccess) return SFM_ERR_CUDA;
+    const bool keep = *device < kMaxDevices;
+    *clusters = keep ? known[*device].load(std::memory_order_relaxed) : 0;
+    if (*clusters > 0) return SFM_OK;
+    if (cudaFuncSetAttribute(sfm_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess) return SFM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(clusters, sfm_dense_kernel, &cfg) != cudaSuccess || *clusters < 1) return SFM_ERR_CUDA;
+    if (keep) known[*device].store(*clusters, std::memory_order_relaxed);
+    return SFM_OK;
+}
+
 }  // namespace
 }  // namespace sfm
 
@@ -143,17 +963,25 @@ using namespace sfm;
 
 extern "C" int sfm_dense_workspace_size(const sfm_dense_params *params, size_t *bytes)
 {
-    const int rc = dense_check(params);
+    int rc = dense_check(params);
     if (rc) return rc;
     if (!bytes) return SFM_ERR_INVALID_ARG;
     *bytes = 0;
+    if (dense_tokens(*params) == 0) return SFM_OK;
+    int device = 0, clusters = 0;
+    rc = dense_clusters(&device, &clusters);
+    if (rc) return rc;
+    Plan pl = {};
+    rc = dense_plan(*params, clusters, &pl);
+    if (rc) return rc;
+    *bytes = dense_bytes(pl);
     return SFM_OK;
 }
 
 extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_tensors *t, void *out, float *lse,
                                  void *workspace, size_t workspace_bytes, int32_t *status, sfm_stream_t stream)
 {
-    const int rc = dense_check(pp);
+    int rc = dense_check(pp);
     if (rc) return rc;
     if (!t) return SFM_ERR_INVALID_ARG;
     const sfm_dense_params &p = *pp;
@@ -211,10 +1039,46 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     a.cap = p.softcap;
     a.block_div = make_fastdiv(paged ? (uint32_t)p.block_size : 1u);
     a.heads_div = make_fastdiv((uint32_t)p.num_heads);
-    const int64_t rows = (int64_t)tokens * p.num_heads;
-    const dim3 grid((unsigned)((rows + kWarps - 1) / kWarps));
-    const cudaError_t e = p.dtype == SFM_DTYPE_BF16
-                              ? launch_dependent(sfm_dense_rows_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, (cudaStream_t)stream, a)
-                              : launch_dependent(sfm_dense_rows_kernel<__half>, grid, dim3(32 * kWarps), 0, (cudaStream_t)stream, a);
+
+    int device = 0, clusters = 0;
+    rc = dense_clusters(&device, &clusters);
+    if (rc) return rc;
+    Plan pl = {};
+    rc = dense_plan(p, clusters, &pl);
+    if (rc) return rc;
+    if (workspace_bytes < dense_bytes(pl) || (dense_bytes(pl) && !workspace)) return SFM_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 255u) return SFM_ERR_LAYOUT;
+    // rows per box of keys: as many as a page holds whole boxes of, 64 at most
+    pl.box_rows = 64;
+    if (paged) {
+        pl.box_rows = p.block_size & -p.block_size;
+        if (pl.box_rows > 64) pl.box_rows = 64;
+    }
+    pl.align = paged ? pl.box_rows : 1;
+    pl.slots_div = make_fastdiv((uint32_t)pl.slots);
+    pl.per_seq_div = make_fastdiv((uint32_t)(pl.per_seq > 0 ? pl.per_seq : 1));
+    const bool bf16 = p.dtype == SFM_DTYPE_BF16;
+    pl.idesc_s = idesc_f16(kRows, kKeys, bf16, false, false);
+    pl.idesc_o = idesc_f16(kRows, 256, bf16, false, true);
+    if (pl.splits > 1) {
+        pl.part_o = static_cast<float4 *>(workspace);
+        pl.part_ml = reinterpret_cast<float2 *>(pl.part_o + (size_t)pl.units * kRows * (kD / 4));
+        pl.head = reinterpret_cast<int4 *>(pl.part_ml + (size_t)pl.units * kRows);
+    }
+    CUtensorMap q_map, kv_map;
+    rc = make_map(&q_map, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64);
+    if (!rc) rc = make_map(&kv_map, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows);
+    if (rc) return rc;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const int pairs = pl.units < clusters ? pl.units : clusters;
+    static std::atomic<bool> ready[kMaxDevices];
+    cudaError_t e = prepared_launch(
+        ready, device,
+        [&] { return cudaFuncSetAttribute(sfm_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes); },
+        [&] {
+            return launch_dependent(sfm_dense_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kSmemBytes, st, a, pl, q_map, kv_map);
+        });
+    if (e == cudaSuccess && pl.splits > 1)
+        e = launch_dependent(sfm_dense_join_kernel, dim3((unsigned)pl.slots * 16), dim3(256), 0, st, a, pl);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
