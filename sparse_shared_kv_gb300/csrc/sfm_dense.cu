@@ -49,8 +49,10 @@ constexpr int kD = 512;
 constexpr int kThreads = 384;
 constexpr int kRows = 128;                    // rows of Q of a pair
 constexpr int kKeys = 128;                    // keys of a tile
-constexpr int kStages = 8;
-constexpr uint32_t kStageBytes = 16384;
+constexpr int kStages = 4;
+constexpr int kBlocks = 4;                    // blocks of 64 values x 64 rows (8 KB) of a stage
+constexpr int kSteps = 8 / kBlocks;           // stages of K, and of V, of a tile
+constexpr uint32_t kStageBytes = kBlocks * 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;              // log2 units
@@ -229,9 +231,12 @@ __device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, in
     return true;
 }
 
+// First key of the unit's i-th tile, from the last keys to the first: where scores fall with the distance a row's maximum
+// is then found in its first tiles (from the first keys on, every tile of a steep head moved it and rescaled O: 900 to 1200
+// clocks per tile).
 __device__ __forceinline__ int tile_key(const Unit &w, int i)
 {
-    const int t = w.tile0 + i;
+    const int t = w.tile0 + w.tiles - 1 - i;
     return t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys;
 }
 
@@ -253,16 +258,17 @@ __device__ __forceinline__ uint32_t pack(float x, float y, bool bf16)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The 256 softmax threads meet; true if all of them say so.
-__device__ __forceinline__ bool rows_meet(bool ok)
+// The 256 softmax threads meet; true if any of them says so.
+__device__ __forceinline__ bool rows_meet_any(bool yes)
 {
-    uint32_t all;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-                 : "=r"(all)
-                 : "r"(ok ? 1u : 0u)
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(any)
+                 : "r"(yes ? 1u : 0u)
                  : "memory");
-    return all != 0;
+    return any != 0;
 }
+__device__ __forceinline__ bool rows_meet(bool ok) { return !rows_meet_any(!ok); }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUtensorMap q_map,
@@ -345,9 +351,9 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
     } else if (warp == 0) {
         // ======================= copies =======================
         int n = 0, nq = 0, c = 0;                  // units, units with keys, stages
-        const int boxes = 64 / pl.box_rows;        // per stage and 64 values
+        const int boxes = 64 / pl.box_rows;        // per block
+        const bool paged = a.layout_kv == SFM_LAYOUT_PAGED;
         bool ok = true;
-        const bool one = elect_one();
         while (ok) {
             const int us = n & 1;
             if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
@@ -359,47 +365,62 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             if (w.tiles == 0) continue;
             if (nq > 0 && !pair_wait_warp(bar(B_Q_EMPTY), nq - 1 & 1, abort_flag)) break;
             ++nq;
-            if (one) {
+            if (elect_one()) {
                 if (rank == 0) expect_tx(bar(B_Q_FULL), 2 * 65536);
-                for (int d = 0; d < 8; ++d)
-                    pair_load(sb + Q_OFF + d * 8192u, &q_map, d * 64, (int)w.row0 + 64 * (int)rank, first_bar(B_Q_FULL));
+                pair_load(sb + Q_OFF, &q_map, 0, (int)w.row0 + 64 * (int)rank, 0, first_bar(B_Q_FULL));
             }
             __syncwarp();
-            // lane l holds the row of the box of keys [l box_rows, (l + 1) box_rows) of a tile
-            bool bad = false;
-            auto rows_of = [&](int i) {
-                return lane < 2 * boxes && i < w.tiles ? box_row(a, w.b, w.kv0, w.len, tile_key(w, i) + lane * pl.box_rows, &bad) : 0;
+            // lane l looks after the box of keys [l box_rows, (l + 1) box_rows) of a tile: its page's id is under way a tile
+            // before it is needed
+            auto page_of = [&](int i) {
+                const int j = i < w.tiles ? tile_key(w, i) + lane * pl.box_rows : w.len;
+                const bool real = paged && lane < 2 * boxes && j < w.len;
+                return real ? __ldg(a.table + (int64_t)w.b * a.cols + fdiv((uint32_t)j, a.block_div)) : 0;
             };
-            auto stage = [&](int x, int half, int32_t row) {
+            auto row_of = [&](int i, int32_t id) {
+                const int j = tile_key(w, i) + lane * pl.box_rows;
+                if (j >= w.len) return (int32_t)a.kv_rows;
+                if (!paged) return (int32_t)(w.kv0 + j);
+                if (id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows) return (int32_t)a.kv_rows;
+                return id * a.block + (j - (int)fdiv((uint32_t)j, a.block_div) * a.block);
+            };
+            auto stage = [&](int block, int half, int32_t row) {
                 const int st = c & (kStages - 1), use = c / kStages;
                 ++c;
                 if (use > 0 && !pair_wait_warp(bar(B_KV_EMPTY + st), use - 1 & 1, abort_flag)) return false;
-                int32_t y[4];
+                const uint32_t dst = sb + KV_OFF + st * kStageBytes;
+                if (boxes == 1) {
+                    const int y = __shfl_sync(0xffffffffu, row, half);
+                    if (elect_one()) {
+                        if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
+                        pair_load(dst, &kv_map, 0, y, block, first_bar(B_KV_FULL + st));
+                    }
+                } else {
+                    int y[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
-                if (one) {
-                    if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
-                    const uint32_t dst = sb + KV_OFF + st * kStageBytes;
+                    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
+                    if (elect_one()) {
+                        if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < boxes) {
-                            pair_load(dst + k * pl.box_rows * 128u, &kv_map, x, y[k], first_bar(B_KV_FULL + st));
-                            pair_load(dst + 8192u + k * pl.box_rows * 128u, &kv_map, x + 64, y[k], first_bar(B_KV_FULL + st));
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            if (k < boxes)
+#pragma unroll
+                                for (int d = 0; d < kBlocks; ++d)
+                                    pair_load(dst + d * 8192u + k * pl.box_rows * 128u, &kv_map, 0, y[k], block + d, first_bar(B_KV_FULL + st));
                     }
                 }
                 __syncwarp();
                 return true;
             };
-            int32_t before = 0, now = rows_of(0), next = rows_of(1);
+            int32_t before = 0, now = row_of(0, page_of(0)), page = page_of(1);
             for (int i = 0; i <= w.tiles && ok; ++i) {
                 if (i < w.tiles)
-                    for (int k = 0; k < 4 && ok; ++k) ok = stage(128 * k, (int)rank, now);
+                    for (int k = 0; k < kSteps && ok; ++k) ok = stage(kBlocks * k, (int)rank, now);
                 if (i > 0)
-                    for (int k = 0; k < 4 && ok; ++k) ok = stage(256 * (k >> 1) + 128 * (int)rank, k & 1, before);
+                    for (int k = 0; k < kSteps && ok; ++k) ok = stage(4 * (int)rank + (k >> 1) * kBlocks, k & 1, before);
                 before = now;
-                now = next;
-                next = rows_of(i + 2);
+                if (i + 1 < w.tiles) now = row_of(i + 1, page);
+                page = page_of(i + 2);
             }
         }
     } else if (warp == 1) {
@@ -408,29 +429,10 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             int n = 0, nq = 0, c = 0, g = 0, fixes = 0;      // units, units with keys, stages, tiles
             bool ok = true;
             const uint32_t id_s = pl.idesc_s, id_o = pl.idesc_o;
-            auto scores = [&](int gi) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int st = c & (kStages - 1);
-                    if (!pair_wait_warp(bar(B_KV_FULL + st), c / kStages & 1, abort_flag)) return false;
-                    ++c;
-                    tc_fence_after();
-                    const uint32_t stg = sb + KV_OFF + st * kStageBytes;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t sub = (j >> 2) * 8192u + (j & 3) * 32u;
-                            pair_mma(tmem + TM_S + (gi & 1) * 64, sdesc_sw128(sb + Q_OFF + k * 16384u + sub, 16, 1024),
-                                     sdesc_sw128(stg + sub, 16, 1024), id_s, (k | j) > 0);
-                        }
-                        pair_commit(bar(B_KV_EMPTY + st));
-                        if (k == 3) pair_commit(bar(B_S_FULL + (gi & 1)));
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
+            const Desc q_desc = desc_sw128(sb + Q_OFF, 16, 1024), k_desc = desc_sw128(sb + KV_OFF, 16, 1024);
+            const Desc p_desc = desc_sw128(sb + P_OFF, 16, 1024), v_desc = desc_sw128(sb + KV_OFF, 8192, 1024);
             while (ok) {
+                // the whole warp keeps count of units and tiles; one lane issues all products of a unit
                 const int us = n & 1;
                 if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
                 const int valid = __shfl_sync(0xffffffffu, units[us].valid, 0), tiles = __shfl_sync(0xffffffffu, units[us].tiles, 0);
@@ -439,56 +441,77 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 ++n;
                 if (!valid) break;
                 if (tiles == 0) continue;
-                if (!pair_wait_warp(bar(B_Q_FULL), nq & 1, abort_flag)) break;
-                tc_fence_after();
-                ok = scores(g);
-                for (int i = 0; i < tiles && ok; ++i) {
-                    const int gi = g + i, buf = gi & 1;
-                    if (i + 1 < tiles) ok = scores(gi + 1);
-                    if ((i + 2 == tiles || tiles == 1) && elect_one()) pair_commit(bar(B_Q_EMPTY));
-                    __syncwarp();
-                    ok = ok && pair_wait_warp(bar(B_P_FULL + buf), gi >> 1 & 1, abort_flag);
-                    if (i == 0 && nq > 0) ok = ok && pair_wait_warp(bar(B_O_FREE), nq - 1 & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t found = lane < 4 ? cand_words[4 * buf + lane] : 0u;
-                    if (__any_sync(0xffffffffu, found != 0)) {
+                int fixed = 0;
+                if (elect_one()) {
+                    int at = c;
+                    auto landed = [&](int k) { return pair_wait(bar(B_KV_FULL + (k & (kStages - 1))), k / kStages & 1, abort_flag); };
+                    auto scores = [&](int gi) {
+                        const uint32_t d = tmem + TM_S + (gi & 1) * 64;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const uint32_t st = at & (kStages - 1);
+                            if (!landed(at)) return false;
+                            ++at;
+                            tc_fence_after();
+                            const Desc kd = {k_desc.lo + st * (kStageBytes >> 4), k_desc.hi};
+#pragma unroll
+                            for (int j = 0; j < 4 * kBlocks; ++j) {
+                                const uint32_t sub = (j >> 2) * 8192u + (j & 3) * 32u;
+                                pair_mma(d, desc_at(q_desc, k * kStageBytes + sub), desc_at(kd, sub), id_s, (k | j) > 0);
+                            }
+                            pair_commit(bar(B_KV_EMPTY + st));
+                        }
+                        pair_commit(bar(B_S_FULL + (gi & 1)));
+                        return true;
+                    };
+                    auto finite = [&](int buf) {
                         // the staged V, made finite in both CTAs before it is used
-                        for (int k = 0; k < 4 && ok; ++k)
-                            ok = pair_wait_warp(bar(B_KV_FULL + (c + k & (kStages - 1))), (c + k) / kStages & 1, abort_flag);
-                        if (!ok) break;
+                        for (int k = 0; k < kSteps; ++k)
+                            if (!landed(at + k)) return false;
                         for (uint32_t r = 0; r < 2; ++r) {
                             const uint32_t to = in_cta(bar0 + FIX_REL, r);
-                            if (lane < 4) store_remote(to + 4 * lane, found);
-                            if (lane == 4) store_remote(to + 16, (uint32_t)c & (kStages - 1));
+                            for (int k = 0; k < 4; ++k) store_remote(to + 4 * k, cand_words[4 * buf + k]);
+                            store_remote(to + 16, (uint32_t)at & (kStages - 1));
+                            arrive_remote_release(in_cta(bar(B_FIX), r));
                         }
-                        if (lane < 4) cand_words[4 * buf + lane] = 0;
-                        __syncwarp();
-                        if (lane < 2) arrive_remote(in_cta(bar(B_FIX), lane));
-                        __syncwarp();
-                        ok = pair_wait_warp(bar(B_FIXED), fixes & 1, abort_flag);
-                        ++fixes;
-                        if (!ok) break;
+                        for (int k = 0; k < 4; ++k) cand_words[4 * buf + k] = 0;
+                        if (!pair_wait(bar(B_FIXED), (fixes + fixed) & 1, abort_flag)) return false;
+                        ++fixed;
                         fence_proxy_async_smem();
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int st = c & (kStages - 1);
-                        ok = ok && pair_wait_warp(bar(B_KV_FULL + st), c / kStages & 1, abort_flag);
-                        ++c;
+                        return true;
+                    };
+                    ok = pair_wait(bar(B_Q_FULL), nq & 1, abort_flag);
+                    tc_fence_after();
+                    ok = ok && scores(g);
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const int gi = g + i, buf = gi & 1;
+                        if (i + 1 < tiles) ok = scores(gi + 1);
+                        if (i + 2 == tiles || tiles == 1) pair_commit(bar(B_Q_EMPTY));
+                        ok = ok && pair_wait(bar(B_P_FULL + buf), gi >> 1 & 1, abort_flag);
+                        if (i == 0 && nq > 0) ok = ok && pair_wait(bar(B_O_FREE), nq - 1 & 1, abort_flag);
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t stg = sb + KV_OFF + st * kStageBytes;
-                        if (elect_one() && ok) {
+                        if (cand_words[4 * buf] | cand_words[4 * buf + 1] | cand_words[4 * buf + 2] | cand_words[4 * buf + 3]) ok = finite(buf);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                pair_mma(tmem + TM_O + (k >> 1) * 128, sdesc_sw128(sb + P_OFF + buf * 16384u + (k & 1) * 8192u + j * 32u, 16, 1024),
-                                         sdesc_sw128(stg + j * 2048u, 8192, 1024), id_o, i > 0 || (k & 1) || j > 0);
+                        for (int k = 0; k < kSteps; ++k) {
+                            const uint32_t st = at & (kStages - 1);
+                            if (!ok || !landed(at)) { ok = false; break; }
+                            ++at;
+                            tc_fence_after();
+                            const Desc pd = {p_desc.lo + buf * (16384u >> 4), p_desc.hi}, vd = {v_desc.lo + st * (kStageBytes >> 4), v_desc.hi};
+#pragma unroll
+                            for (int j = 0; j < 2 * kBlocks; ++j)        // columns of the stage, 16 keys of its 64
+                                pair_mma(tmem + TM_O + ((k >> 1) * kBlocks / 2 + (j >> 2)) * 128, desc_at(pd, (k & 1) * 8192u + (j & 3) * 32u),
+                                         desc_at(vd, (j >> 2) * 16384u + (j & 3) * 2048u), id_o, i > 0 || (k & 1) || (j & 3) > 0);
                             pair_commit(bar(B_KV_EMPTY + st));
-                            if (k == 3) pair_commit(bar(B_O_DONE + buf));
                         }
-                        __syncwarp();
+                        pair_commit(bar(B_O_DONE + buf));
                     }
                 }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+                fixes += __reduce_max_sync(0xffffffffu, fixed);
+                c += 2 * kSteps * tiles;
                 ++nq;
                 g += tiles;
             }
@@ -501,7 +524,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             __syncwarp();
             if (lane < 2) {
                 store_remote(in_cta(bar0 + FIX_REL, lane) + 20, 1u);
-                arrive_remote(in_cta(bar(B_FIX), lane));
+                arrive_remote_release(in_cta(bar(B_FIX), lane));
             }
         }
         __syncwarp();
@@ -534,10 +557,10 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 while (m) {
                     const int key = 32 * w + __ffs(m) - 1;
                     m &= m - 1;
-                    // the key's 256 values in this CTA: two stages (column halves) of two blocks, 128 bytes each
+                    // the key's 256 values in this CTA: four blocks, 128 bytes each, in the stages of its half of the keys
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t st = fix_words[4] + 2 * (q >> 1) + (key >> 6) & (kStages - 1);
-                        uint16_t *row = reinterpret_cast<uint16_t *>(smem + KV_OFF + st * kStageBytes + (q & 1) * 8192 + (key & 63) * 128);
+                        const uint32_t st = fix_words[4] + q / kBlocks * 2 + (key >> 6) & (kStages - 1);
+                        uint16_t *row = reinterpret_cast<uint16_t *>(smem + KV_OFF + st * kStageBytes + q % kBlocks * 8192 + (key & 63) * 128);
                         for (int k = lane; k < 64; k += 32)
                             if ((row[k] & inf) == inf) row[k] = 0;
                     }
@@ -545,7 +568,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_remote(first_bar(B_FIXED));
+            if (lane == 0) arrive_remote_release(first_bar(B_FIXED));
         }
     } else {
         // ======================= softmax =======================
@@ -676,19 +699,30 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         if (!(vis >> c & 1)) y[c] = -INFINITY;
                     }
                     odd = __reduce_or_sync(0xffffffffu, odd & ~vis);
-                    if (odd && lane == 0) or_remote(first0 + CAND_REL + 16u * buf + 4u * quarter, odd);
+                    if (odd && lane == 0) {
+                        or_remote(first0 + CAND_REL + 16u * buf + 4u * quarter, odd);
+                        fence_cluster();         // before this warp's arrival
+                    }
                 }
-                float top = -INFINITY, got[4];
+                float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) top = fmaxf(top, y[c]);
-                row_values(top, got);
-                if (!ok) break;
-                top = fmaxf(fmaxf(got[0], got[1]), fmaxf(got[2], got[3]));
-                float alpha = 1.f;
-                if (top > m + kRescale || m == -INFINITY) {      // the first tile that the row sees, or a maximum that left the range
-                    if (m != -INFINITY) alpha = fast_exp2(m - top);
-                    m = top;
-                    l *= alpha;
+                for (int c = 0; c < 32; c += 2) {
+                    top0 = fmaxf(top0, y[c]);
+                    top1 = fmaxf(top1, y[c + 1]);
+                }
+                float top = fmaxf(top0, top1), alpha = 1.f;
+                // A row's four threads share their maxima only where one of all rows' has left the range (or a role gave up)
+                const bool beyond = top > m + kRescale || (m == -INFINITY && top != -INFINITY);
+                if (rows_meet_any(beyond || !ok)) {
+                    float got[4];
+                    row_values(top, got);
+                    if (!ok) break;
+                    top = fmaxf(fmaxf(got[0], got[1]), fmaxf(got[2], got[3]));
+                    if (top > m + kRescale || m == -INFINITY) {
+                        if (m != -INFINITY) alpha = fast_exp2(m - top);
+                        m = top;
+                        l *= alpha;
+                    }
                 }
                 const float m_use = m == -INFINITY ? 0.f : m;
                 uint32_t pk[16];
@@ -701,8 +735,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     pk[c] = pack(p0, p1, bf16);
                 }
                 l += sum0 + sum1;
-                // P's buffer is free once O += P V of the tile before the last is done
-                if (gi >= 2 && ok) ok = pair_wait_warp(bar(B_O_DONE + buf), (gi >> 1) - 1 & 1, abort_flag);
+                // P's buffer is free: O += P V of the tile before the last was issued before this tile's S
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4 *>(p_row + buf * 16384 + sw128(r, wg * 4 + c)) =
@@ -726,7 +759,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 if (lane == 0) arrive_remote(first_bar(B_P_FULL + buf));
             }
             if (!rows_meet(ok)) break;
-            // the row's result: columns [256 wg + 128 half, + 128) of O
+            // the row's result: columns [256 half + 128 wg, + 128) of O
             if (w.tiles > 0) {
                 const int last = g + w.tiles - 1;
                 if (ok) ok = pair_wait_warp(bar(B_O_DONE + (last & 1)), last >> 1 & 1, abort_flag);
@@ -750,6 +783,14 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     pl.part_ml[part_row] = make_float2(m, l);
                 }
             }
+            // 128 bytes of each of the warp's 32 rows at a time, through shared memory (P's, which nothing reads now: the
+            // warps meet before the next unit's first P), so that they are written whole
+            const bool parts = !whole;
+            const bool write = live ? true : !parts || w.split == 0;
+            uint8_t *const pad = smem + P_OFF + (warp - 4) * 4096;
+            const int col0 = 256 * half + 128 * wg, row_first = 64 * (int)rank + (part & 1) * 32;
+            const uint32_t rows_now = __ballot_sync(0xffffffffu, R < w.rows && write);
+            const uint32_t rows_part = __ballot_sync(0xffffffffu, live && parts), rows_out = rows_now & ~rows_part;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
                 uint32_t o[32];
@@ -757,25 +798,49 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     tmem_ld32(tmem + lanes + TM_O + wg * 128 + c, o);
                     tmem_wait_ld();
                 }
-                const int col = 256 * wg + 128 * half + c;
-                if (!live || whole) {
-                    if (R < w.rows && (live || w.split == 0)) {
-                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_row * kD + col);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[e] = inv != 0.f ? pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv, bf16) : 0u;
-                            to[k] = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
-                } else {
-                    float4 *to = pl.part_o + part_row * (kD / 4) + col / 4;
+                if (rows_part) {
+                    // fp32 partial results: 32 values of a row
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        to[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                            __uint_as_float(o[4 * k + 3]));
+                        *reinterpret_cast<uint4 *>(pad + sw128(lane, k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rr = 4 * k + (lane >> 3);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(pad + sw128(rr, lane & 7));
+                        if (rows_part >> rr & 1)
+                            reinterpret_cast<uint4 *>(pl.part_o)[((part_row - r) + (part & 1) * 32 + rr) * (kD / 4) + (col0 + c) / 4 + (lane & 7)] = v;
+                    }
+                    __syncwarp();
+                    // rows that do not count, beside them
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rr = 4 * k + (lane >> 3);
+                        if (rows_out >> rr & 1 && (lane & 4) == 0)
+                            reinterpret_cast<uint4 *>(a.out)[(w.row0 + row_first + rr) * 64 + (col0 + c) / 8 + (lane & 3)] = make_uint4(0, 0, 0, 0);
+                    }
+                } else if (rows_out) {
+                    // 64 values of dtype of a row: two rounds of 32 make its 128 bytes
+                    const int side = c >> 5 & 1;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = inv != 0.f ? pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv, bf16) : 0u;
+                        *reinterpret_cast<uint4 *>(pad + sw128(lane, 4 * side + k)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    if (side) {
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = 4 * k + (lane >> 3);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(pad + sw128(rr, lane & 7));
+                            if (rows_out >> rr & 1)
+                                reinterpret_cast<uint4 *>(a.out)[(w.row0 + row_first + rr) * 64 + (col0 + c - 32) / 8 + (lane & 7)] = v;
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             if (w.tiles > 0) {
@@ -884,13 +949,15 @@ EncodeFn encoder()
     return fn;
 }
 
-int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows)
+// Rows of 512 values as eight blocks of 64: boxes of `blocks` blocks x `box_rows` rows land block after block, as the
+// products read them.
+int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows, int blocks)
 {
     const EncodeFn encode = encoder();
     if (!encode) return SFM_ERR_CUDA;
-    const cuuint64_t dims[2] = {kD, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
-    const CUresult r = encode(map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 8}, strides[2] = {(cuuint64_t)row_bytes, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks}, steps[3] = {1, 1, 1};
+    const CUresult r = encode(map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                               const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SFM_OK : SFM_ERR_CUDA;
@@ -1066,8 +1133,8 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
         pl.head = reinterpret_cast<int4 *>(pl.part_ml + (size_t)pl.units * kRows);
     }
     CUtensorMap q_map, kv_map;
-    rc = make_map(&q_map, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64);
-    if (!rc) rc = make_map(&kv_map, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows);
+    rc = make_map(&q_map, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
+    if (!rc) rc = make_map(&kv_map, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, pl.box_rows == 64 ? kBlocks : 1);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
     const int pairs = pl.units < clusters ? pl.units : clusters;

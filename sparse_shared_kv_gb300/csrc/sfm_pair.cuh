@@ -52,7 +52,15 @@ __device__ __forceinline__ void cluster_sync()
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// Arrive at a barrier of either CTA.  This thread's writes to its own CTA's memory (made visible to the tensor cores by a
+// proxy fence) and its tensor memory accesses come before it; what it wrote into the other CTA's does after
+// arrive_remote_release() alone, which waits for those writes and took 1500 clocks per softmax warp and tile.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -66,6 +74,8 @@ __device__ __forceinline__ void or_remote(uint32_t cluster_addr, uint32_t v)
 {
     asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
+
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
 {
@@ -118,6 +128,23 @@ __device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// A shared-memory matrix descriptor (sdesc_sw128) as two words: operands a few bytes on differ in the first one only, by the
+// bytes / 16, so that a product needs one addition per operand.
+struct Desc {
+    uint32_t lo, hi;
+};
+
+__device__ __forceinline__ Desc desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    const uint64_t d = sdesc_sw128(addr, lbo, sbo);
+    return {static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+
+__device__ __forceinline__ uint64_t desc_at(const Desc &d, uint32_t bytes)
+{
+    return static_cast<uint64_t>(d.hi) << 32 | (d.lo + (bytes >> 4));
+}
+
 __device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
@@ -137,11 +164,11 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
 }
 
 // Copy a box into this CTA's memory, counted at a barrier of the pair (a shared::cluster address).
-__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t cluster_bar)
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t cluster_bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
         : "memory");
 }
 
