@@ -538,7 +538,7 @@ typedef struct sfm_dense_params {
                                    batch (a row's result is then bit for bit the same in every batch) */
     int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 1: O = 0 and LSE = -inf; 0: left as they were */
     float softmax_scale;        /* finite */
-    float softcap;              /* 0: none; > 0: scores are capped */
+    float softcap;              /* 0: none; >= 2^-100: scores are capped */
 } sfm_dense_params;
 
 /*   q              BSND (b, q_s, num_heads, 512) / TND (q_t, num_heads, 512), dense, 16-byte aligned

@@ -68,31 +68,33 @@ constexpr uint32_t TM_O = 0, TM_S = 256, kTmemCols = 512;
 
 // barriers (8 bytes each) at MISC_OFF; "first": used in the pair's first CTA
 enum Bar {
-    B_KV_FULL = 0,       // [8] first: both CTAs' halves of a stage have landed
-    B_KV_EMPTY = 8,      // [8] the products that read the stage are done
-    B_Q_FULL = 16,       // first
-    B_Q_EMPTY = 17,      // the unit's last S is done
-    B_S_FULL = 18,       // [2] S of a tile
-    B_P_FULL = 20,       // [2] first: P written, O rescaled, S read, by the 16 softmax warps of both CTAs
-    B_O_DONE = 22,       // [2] O += P V of a tile
-    B_O_FREE = 24,       // first: the 16 softmax warps have read the unit's O
-    B_UNIT_FULL = 25,    // [2]
-    B_UNIT_EMPTY = 27,   // [2]
-    B_FIX = 29,          // rows to be made finite
-    B_FIXED = 30,        // first: both CTAs have
-    B_END = 31,
-    kBars = 32
+    B_KV_FULL = 0,       // [4] first: both CTAs' halves of a stage have landed
+    B_KV_EMPTY = 4,      // [4] the products that read the stage are done
+    B_Q_FULL = 8,        // first
+    B_Q_EMPTY = 9,       // the unit's last S is done
+    B_S_FULL = 10,       // [4] S of a tile
+    B_P_FULL = 14,       // [2] first: P written, O rescaled, S read, by the 16 softmax warps of both CTAs
+    B_O_DONE = 16,       // [2] O += P V of a tile
+    B_O_FREE = 18,       // first: the 16 softmax warps have read the unit's O
+    B_UNIT_FULL = 19,    // [4]
+    B_UNIT_EMPTY = 23,   // [4]
+    B_FIX = 27,          // rows to be made finite
+    B_FIXED = 28,        // first: both CTAs have
+    B_END = 29,
+    kBars = 30
 };
+constexpr int kUnits = 4;                     // units that are worked out ahead
+constexpr int kAhead = 3;                     // tiles whose S is issued before the first of them gets its O += P V
 constexpr uint32_t EXCH_REL = 256;            // [2][4][64] floats: the row's four maxima (or sums)
-constexpr uint32_t UNIT_REL = EXCH_REL + 2048;   // [2] Unit
-constexpr uint32_t CAND_REL = UNIT_REL + 256;    // first: [2][4] words of keys that may hold NaN or infinities
+constexpr uint32_t UNIT_REL = EXCH_REL + 2048;   // [4] Unit
+constexpr uint32_t CAND_REL = UNIT_REL + 4 * 128;    // first: [2][4] words of keys that may hold NaN or infinities
 constexpr uint32_t FIX_REL = CAND_REL + 32;      // words, first stage, quit
 constexpr uint32_t TMEM_REL = FIX_REL + 32;
 constexpr uint32_t ABORT_REL = TMEM_REL + 4;
 constexpr uint32_t BEAT_REL = ABORT_REL + 4;
 static_assert(kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= 3072, "misc area");
 
-struct Unit {
+struct alignas(128) Unit {
     int64_t row0;            // first row of Q (and of the outputs)
     int64_t kv0;
     int32_t valid, b, rows, used;      // rows of the tile, and those of queries that count
@@ -240,6 +242,41 @@ __device__ __forceinline__ int tile_key(const Unit &w, int i)
     return t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys;
 }
 
+// The order of the products, and of the copies for them, over all units: S of a tile comes kAhead - 1 tiles before its
+// O += P V, so that the softmax has two tiles in hand while the tensor cores work (with one the two waited for each other:
+// half a softmax more per tile), across the ends of units too.  The first S of a unit comes behind the last but one O += P V
+// of the unit before, when its Q has had the time to land.
+struct Order {
+    int k = 0, k_tiles = 0, v = 0, v_tiles = 0, later = 0;   // next tile and tiles of the units of S and of O; tiles of the unit after O's
+    int units = 0, done = 0, ahead = 0;                      // units that S has entered and that O has left; tiles between the two
+    bool over = false;
+    __device__ bool at_new_unit() const { return k == k_tiles; }
+    __device__ bool wants_scores() const
+    {
+        if (k < k_tiles) return ahead < kAhead;
+        return !over && ahead < 2 && units - done <= 1;
+    }
+    __device__ void end() { over = true; }
+    __device__ void enter(int tiles)
+    {
+        k = 0;
+        k_tiles = tiles;
+        if (units == done) v_tiles = tiles;
+        else later = tiles;
+        ++units;
+    }
+    __device__ void scores_done() { ++k, ++ahead; }
+    __device__ void output_done()
+    {
+        --ahead;
+        if (++v == v_tiles) {
+            v = 0;
+            v_tiles = later;
+            ++done;
+        }
+    }
+};
+
 // bits [lo, hi) of a word whose bit 0 stands for key j0
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi, int j0)
 {
@@ -258,17 +295,89 @@ __device__ __forceinline__ uint32_t pack(float x, float y, bool bf16)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The 256 softmax threads meet; true if any of them says so.
-__device__ __forceinline__ bool rows_meet_any(bool yes)
+// The 128 softmax threads that share rows [0, 32) (0) or [32, 64) (1) meet; true if any of them says so.
+__device__ __forceinline__ bool rows_meet_any(int who, bool yes)
 {
     uint32_t any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\tbar.red.or.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
                  : "=r"(any)
-                 : "r"(yes ? 1u : 0u)
+                 : "r"(1 + who), "r"(yes ? 1u : 0u)
                  : "memory");
     return any != 0;
 }
-__device__ __forceinline__ bool rows_meet(bool ok) { return !rows_meet_any(!ok); }
+
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t pair_bits(float2 v) { return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 pair_of(uint64_t b)
+{
+    return make_float2(__uint_as_float(static_cast<uint32_t>(b)), __uint_as_float(static_cast<uint32_t>(b >> 32)));
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(x)), "l"(pair_bits(y)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 x, float y) { return mul2(x, make_float2(y, y)); }
+__device__ __forceinline__ float2 add2(float2 x, float2 y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(x)), "l"(pair_bits(y)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float y) { return add2(x, make_float2(y, y)); }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(x)), "l"(pair_bits(y)), "l"(pair_bits(make_float2(z, z))));
+    return pair_of(r);
+}
+
+// y -> cap tanh(y / cap).  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 7 that interpolates tanh(sqrt u) /
+// sqrt u at the Chebyshev nodes of [0, 1] (off by 4e-9, and 2^-23 of roundings): multiplications and additions, where the
+// exponentials and quotients of tanh z = 1 - 2 / (e^2z + 1) would take as long as all else of a tile (scores of a tile
+// 1300 clocks against 570).  That form is for larger ones.
+__device__ __forceinline__ void cap_scores(float2 (&y)[16], float inv, float cap)
+{
+    float far = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
+    if (__all_sync(0xffffffffu, far <= cap)) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const float2 z = mul2(y[c], inv), u = mul2(z, z);
+            float2 p = fma2(u, make_float2(-3.548834123e-04f, -3.548834123e-04f), 2.287645486e-03f);
+            p = fma2(p, u, -7.924946301e-03f);
+            p = fma2(p, u, 2.146998064e-02f);
+            p = fma2(p, u, -5.387273878e-02f);
+            p = fma2(p, u, 1.333219053e-01f);
+            p = fma2(p, u, -3.333328064e-01f);
+            p = fma2(p, u, 1.f);
+            y[c] = mul2(y[c], p);
+        }
+    } else {
+        const float twice = 2.f * kLog2e * inv;
+        auto f = [&](float x) { return fmaf(__fdividef(-2.f, fast_exp2(x * twice) + 1.f), cap, cap); };
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            y[c].x = f(y[c].x);
+            y[c].y = f(y[c].y);
+        }
+    }
+}
+
+// 32 bytes, one sector of memory, at once where they are aligned to that
+__device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide)
+{
+    if (!wide) {
+        static_cast<uint4 *>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUtensorMap q_map,
@@ -299,10 +408,12 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
         }
         init(B_Q_FULL, 1);
         init(B_Q_EMPTY, 1);
+        for (int i = 0; i < 4; ++i) init(B_S_FULL + i, 1);
         for (int i = 0; i < 2; ++i) {
-            init(B_S_FULL + i, 1);
             init(B_P_FULL + i, 16);
             init(B_O_DONE + i, 1);
+        }
+        for (int i = 0; i < kUnits; ++i) {
             init(B_UNIT_FULL + i, 1);
             init(B_UNIT_EMPTY + i, rank == 0 ? 10 : 9);
         }
@@ -338,8 +449,8 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             const bool end = u >= pl.units;
             if (end) w.valid = 0;
             else if (!make_unit(a, pl, u, lane, w)) continue;
-            const int slot = n & 1;
-            if (n >= 2 && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), (n >> 1) - 1 & 1, abort_flag)) break;
+            const int slot = n % kUnits;
+            if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
             if (lane == 0) {
                 units[slot] = w;
                 mbar_arrive(bar(B_UNIT_FULL + slot));
@@ -350,109 +461,145 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
         }
     } else if (warp == 0) {
         // ======================= copies =======================
-        int n = 0, nq = 0, c = 0;                  // units, units with keys, stages
         const int boxes = 64 / pl.box_rows;        // per block
         const bool paged = a.layout_kv == SFM_LAYOUT_PAGED;
+        int n = 0, c = 0;                          // units, stages
+        Order o;
+        Unit wk = {};                                   // the unit of the next K
         bool ok = true;
-        while (ok) {
-            const int us = n & 1;
-            if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
-            const Unit w = units[us];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
-            ++n;
-            if (!w.valid) break;
-            if (w.tiles == 0) continue;
-            if (nq > 0 && !pair_wait_warp(bar(B_Q_EMPTY), nq - 1 & 1, abort_flag)) break;
-            ++nq;
-            if (elect_one()) {
-                if (rank == 0) expect_tx(bar(B_Q_FULL), 2 * 65536);
-                pair_load(sb + Q_OFF, &q_map, 0, (int)w.row0 + 64 * (int)rank, 0, first_bar(B_Q_FULL));
-            }
-            __syncwarp();
-            // lane l looks after the box of keys [l box_rows, (l + 1) box_rows) of a tile: its page's id is under way a tile
-            // before it is needed
-            auto page_of = [&](int i) {
-                const int j = i < w.tiles ? tile_key(w, i) + lane * pl.box_rows : w.len;
-                const bool real = paged && lane < 2 * boxes && j < w.len;
-                return real ? __ldg(a.table + (int64_t)w.b * a.cols + fdiv((uint32_t)j, a.block_div)) : 0;
-            };
-            auto row_of = [&](int i, int32_t id) {
-                const int j = tile_key(w, i) + lane * pl.box_rows;
-                if (j >= w.len) return (int32_t)a.kv_rows;
-                if (!paged) return (int32_t)(w.kv0 + j);
-                if (id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows) return (int32_t)a.kv_rows;
-                return id * a.block + (j - (int)fdiv((uint32_t)j, a.block_div) * a.block);
-            };
-            auto stage = [&](int block, int half, int32_t row) {
-                const int st = c & (kStages - 1), use = c / kStages;
-                ++c;
-                if (use > 0 && !pair_wait_warp(bar(B_KV_EMPTY + st), use - 1 & 1, abort_flag)) return false;
-                const uint32_t dst = sb + KV_OFF + st * kStageBytes;
-                if (boxes == 1) {
-                    const int y = __shfl_sync(0xffffffffu, row, half);
-                    if (elect_one()) {
-                        if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
-                        pair_load(dst, &kv_map, 0, y, block, first_bar(B_KV_FULL + st));
-                    }
-                } else {
-                    int y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
-                    if (elect_one()) {
-                        if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < boxes)
-#pragma unroll
-                                for (int d = 0; d < kBlocks; ++d)
-                                    pair_load(dst + d * 8192u + k * pl.box_rows * 128u, &kv_map, 0, y[k], block + d, first_bar(B_KV_FULL + st));
-                    }
+        // lane l looks after the box of keys [l box_rows, (l + 1) box_rows) of a tile: its page's id is under way a tile
+        // before it is needed
+        auto page_of = [&](int i) {
+            const int j = i < wk.tiles ? tile_key(wk, i) + lane * pl.box_rows : wk.len;
+            const bool real = paged && lane < 2 * boxes && j < wk.len;
+            return real ? __ldg(a.table + (int64_t)wk.b * a.cols + fdiv((uint32_t)j, a.block_div)) : 0;
+        };
+        auto row_of = [&](int i, int32_t id) {
+            const int j = tile_key(wk, i) + lane * pl.box_rows;
+            if (j >= wk.len) return (int32_t)a.kv_rows;
+            if (!paged) return (int32_t)(wk.kv0 + j);
+            if (id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows) return (int32_t)a.kv_rows;
+            return id * a.block + (j - (int)fdiv((uint32_t)j, a.block_div) * a.block);
+        };
+        auto stage = [&](int block, int half, int32_t row) {
+            const int st = c & (kStages - 1), use = c / kStages;
+            ++c;
+            if (use > 0 && !pair_wait_warp(bar(B_KV_EMPTY + st), use - 1 & 1, abort_flag)) return false;
+            const uint32_t dst = sb + KV_OFF + st * kStageBytes;
+            if (boxes == 1) {
+                const int y = __shfl_sync(0xffffffffu, row, half);
+                if (elect_one()) {
+                    if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
+                    pair_load(dst, &kv_map, 0, y, block, first_bar(B_KV_FULL + st));
                 }
-                __syncwarp();
-                return true;
-            };
-            int32_t before = 0, now = row_of(0, page_of(0)), page = page_of(1);
-            for (int i = 0; i <= w.tiles && ok; ++i) {
-                if (i < w.tiles)
-                    for (int k = 0; k < kSteps && ok; ++k) ok = stage(kBlocks * k, (int)rank, now);
-                if (i > 0)
-                    for (int k = 0; k < kSteps && ok; ++k) ok = stage(4 * (int)rank + (k >> 1) * kBlocks, k & 1, before);
-                before = now;
-                if (i + 1 < w.tiles) now = row_of(i + 1, page);
-                page = page_of(i + 2);
+            } else {
+                int y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
+                if (elect_one()) {
+                    if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < boxes)
+#pragma unroll
+                            for (int d = 0; d < kBlocks; ++d)
+                                pair_load(dst + d * 8192u + k * pl.box_rows * 128u, &kv_map, 0, y[k], block + d, first_bar(B_KV_FULL + st));
+                }
             }
+            __syncwarp();
+            return true;
+        };
+        // rows of the tiles whose K is copied and V is not yet: their V's copies find them in L2
+        int32_t row0 = 0, row1 = 0, row2 = 0, page = 0;
+        auto next_unit = [&]() -> int {            // tiles of the next unit with keys, 0 at the end, -1 on a timeout
+            for (;;) {
+                const int us = n % kUnits;
+                if (!pair_wait_warp(bar(B_UNIT_FULL + us), n / kUnits & 1, abort_flag)) return -1;
+                wk = units[us];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
+                ++n;
+                if (!wk.valid) return 0;
+                if (wk.tiles) return wk.tiles;
+            }
+        };
+        while (ok) {
+            while (ok && o.wants_scores()) {
+                if (o.at_new_unit()) {
+                    const int tiles = next_unit();
+                    if (tiles <= 0) {
+                        o.end();
+                        ok = tiles == 0;
+                        break;
+                    }
+                    o.enter(tiles);
+                    if (o.units > 1 && !pair_wait_warp(bar(B_Q_EMPTY), o.units - 2 & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        if (rank == 0) expect_tx(bar(B_Q_FULL), 2 * 65536);
+                        pair_load(sb + Q_OFF, &q_map, 0, (int)wk.row0 + 64 * (int)rank, 0, first_bar(B_Q_FULL));
+                    }
+                    __syncwarp();
+                    page = page_of(0);
+                }
+                const int32_t row = row_of(o.k, page);
+                page = page_of(o.k + 1);
+                if (o.ahead == 0) row0 = row;
+                else if (o.ahead == 1) row1 = row;
+                else row2 = row;
+                for (int k = 0; k < kSteps && ok; ++k) ok = stage(kBlocks * k, (int)rank, row);
+                o.scores_done();
+            }
+            if (!ok || o.ahead == 0) break;
+            for (int k = 0; k < kSteps && ok; ++k) ok = stage(4 * (int)rank + (k >> 1) * kBlocks, k & 1, row0);
+            row0 = row1;
+            row1 = row2;
+            o.output_done();
         }
     } else if (warp == 1) {
         // ======================= products =======================
         if (rank == 0) {
-            int n = 0, nq = 0, c = 0, g = 0, fixes = 0;      // units, units with keys, stages, tiles
+            int n = 0, c = 0, gk = 0, gv = 0, fixes = 0;      // units, stages, tiles of S and of O
             bool ok = true;
+            Order o;
             const uint32_t id_s = pl.idesc_s, id_o = pl.idesc_o;
             const Desc q_desc = desc_sw128(sb + Q_OFF, 16, 1024), k_desc = desc_sw128(sb + KV_OFF, 16, 1024);
             const Desc p_desc = desc_sw128(sb + P_OFF, 16, 1024), v_desc = desc_sw128(sb + KV_OFF, 8192, 1024);
+            auto landed = [&](int k) { return pair_wait_warp(bar(B_KV_FULL + (k & (kStages - 1))), k / kStages & 1, abort_flag); };
+            auto next_unit = [&]() -> int {
+                for (;;) {
+                    const int us = n % kUnits;
+                    if (!pair_wait_warp(bar(B_UNIT_FULL + us), n / kUnits & 1, abort_flag)) return -1;
+                    const int valid = __shfl_sync(0xffffffffu, units[us].valid, 0), tiles = __shfl_sync(0xffffffffu, units[us].tiles, 0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
+                    ++n;
+                    if (!valid) return 0;
+                    if (tiles) return tiles;
+                }
+            };
             while (ok) {
-                // the whole warp keeps count of units and tiles; one lane issues all products of a unit
-                const int us = n & 1;
-                if (!pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag)) break;
-                const int valid = __shfl_sync(0xffffffffu, units[us].valid, 0), tiles = __shfl_sync(0xffffffffu, units[us].tiles, 0);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
-                ++n;
-                if (!valid) break;
-                if (tiles == 0) continue;
-                int fixed = 0;
-                if (elect_one()) {
-                    int at = c;
-                    auto landed = [&](int k) { return pair_wait(bar(B_KV_FULL + (k & (kStages - 1))), k / kStages & 1, abort_flag); };
-                    auto scores = [&](int gi) {
-                        const uint32_t d = tmem + TM_S + (gi & 1) * 64;
+                while (ok && o.wants_scores()) {
+                    if (o.at_new_unit()) {
+                        const int tiles = next_unit();
+                        if (tiles <= 0) {
+                            o.end();
+                            ok = tiles == 0;
+                            break;
+                        }
+                        o.enter(tiles);
+                        ok = pair_wait_warp(bar(B_Q_FULL), o.units - 1 & 1, abort_flag);
+                    }
+                    const uint32_t d = tmem + TM_S + (gk & 3) * 64;
 #pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            const uint32_t st = at & (kStages - 1);
-                            if (!landed(at)) return false;
-                            ++at;
-                            tc_fence_after();
+                    for (int k = 0; k < kSteps; ++k) {
+                        const uint32_t st = c & (kStages - 1);
+                        ok = ok && landed(c);
+                        ++c;
+                        tc_fence_after();
+                        if (ok && elect_one()) {
                             const Desc kd = {k_desc.lo + st * (kStageBytes >> 4), k_desc.hi};
 #pragma unroll
                             for (int j = 0; j < 4 * kBlocks; ++j) {
@@ -460,60 +607,60 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                                 pair_mma(d, desc_at(q_desc, k * kStageBytes + sub), desc_at(kd, sub), id_s, (k | j) > 0);
                             }
                             pair_commit(bar(B_KV_EMPTY + st));
+                            if (k == kSteps - 1) {
+                                pair_commit(bar(B_S_FULL + (gk & 3)));
+                                if (o.k + 1 == o.k_tiles) pair_commit(bar(B_Q_EMPTY));
+                            }
                         }
-                        pair_commit(bar(B_S_FULL + (gi & 1)));
-                        return true;
-                    };
-                    auto finite = [&](int buf) {
-                        // the staged V, made finite in both CTAs before it is used
-                        for (int k = 0; k < kSteps; ++k)
-                            if (!landed(at + k)) return false;
-                        for (uint32_t r = 0; r < 2; ++r) {
-                            const uint32_t to = in_cta(bar0 + FIX_REL, r);
-                            for (int k = 0; k < 4; ++k) store_remote(to + 4 * k, cand_words[4 * buf + k]);
-                            store_remote(to + 16, (uint32_t)at & (kStages - 1));
-                            arrive_remote_release(in_cta(bar(B_FIX), r));
-                        }
-                        for (int k = 0; k < 4; ++k) cand_words[4 * buf + k] = 0;
-                        if (!pair_wait(bar(B_FIXED), (fixes + fixed) & 1, abort_flag)) return false;
-                        ++fixed;
-                        fence_proxy_async_smem();
-                        return true;
-                    };
-                    ok = pair_wait(bar(B_Q_FULL), nq & 1, abort_flag);
-                    tc_fence_after();
-                    ok = ok && scores(g);
-                    for (int i = 0; i < tiles && ok; ++i) {
-                        const int gi = g + i, buf = gi & 1;
-                        if (i + 1 < tiles) ok = scores(gi + 1);
-                        if (i + 2 == tiles || tiles == 1) pair_commit(bar(B_Q_EMPTY));
-                        ok = ok && pair_wait(bar(B_P_FULL + buf), gi >> 1 & 1, abort_flag);
-                        if (i == 0 && nq > 0) ok = ok && pair_wait(bar(B_O_FREE), nq - 1 & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (cand_words[4 * buf] | cand_words[4 * buf + 1] | cand_words[4 * buf + 2] | cand_words[4 * buf + 3]) ok = finite(buf);
-#pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            const uint32_t st = at & (kStages - 1);
-                            if (!ok || !landed(at)) { ok = false; break; }
-                            ++at;
-                            tc_fence_after();
-                            const Desc pd = {p_desc.lo + buf * (16384u >> 4), p_desc.hi}, vd = {v_desc.lo + st * (kStageBytes >> 4), v_desc.hi};
-#pragma unroll
-                            for (int j = 0; j < 2 * kBlocks; ++j)        // columns of the stage, 16 keys of its 64
-                                pair_mma(tmem + TM_O + ((k >> 1) * kBlocks / 2 + (j >> 2)) * 128, desc_at(pd, (k & 1) * 8192u + (j & 3) * 32u),
-                                         desc_at(vd, (j >> 2) * 16384u + (j & 3) * 2048u), id_o, i > 0 || (k & 1) || (j & 3) > 0);
-                            pair_commit(bar(B_KV_EMPTY + st));
-                        }
-                        pair_commit(bar(B_O_DONE + buf));
+                        __syncwarp();
                     }
+                    ++gk;
+                    o.scores_done();
                 }
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, ok);
-                fixes += __reduce_max_sync(0xffffffffu, fixed);
-                c += 2 * kSteps * tiles;
-                ++nq;
-                g += tiles;
+                if (!ok || o.ahead == 0) break;
+                const int buf = gv & 1;
+                ok = pair_wait_warp(bar(B_P_FULL + buf), gv >> 1 & 1, abort_flag);
+                if (o.v == 0 && o.done > 0) ok = ok && pair_wait_warp(bar(B_O_FREE), o.done - 1 & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t found = lane < 4 ? cand_words[4 * buf + lane] : 0u;
+                if (__any_sync(0xffffffffu, found != 0)) {
+                    // the staged V, made finite in both CTAs before it is used
+                    for (int k = 0; k < kSteps && ok; ++k) ok = landed(c + k);
+                    if (!ok) break;
+                    for (uint32_t r = 0; r < 2; ++r) {
+                        const uint32_t to = in_cta(bar0 + FIX_REL, r);
+                        if (lane < 4) store_remote(to + 4 * lane, found);
+                        if (lane == 4) store_remote(to + 16, (uint32_t)c & (kStages - 1));
+                    }
+                    if (lane < 4) cand_words[4 * buf + lane] = 0;
+                    __syncwarp();
+                    if (lane < 2) arrive_remote_release(in_cta(bar(B_FIX), lane));
+                    __syncwarp();
+                    ok = pair_wait_warp(bar(B_FIXED), fixes & 1, abort_flag);
+                    ++fixes;
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint32_t st = c & (kStages - 1);
+                    ok = ok && landed(c);
+                    ++c;
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        const Desc pd = {p_desc.lo + buf * (16384u >> 4), p_desc.hi}, vd = {v_desc.lo + st * (kStageBytes >> 4), v_desc.hi};
+#pragma unroll
+                        for (int j = 0; j < 2 * kBlocks; ++j)        // columns of the stage, 16 keys of its 64
+                            pair_mma(tmem + TM_O + ((k >> 1) * kBlocks / 2 + (j >> 2)) * 128, desc_at(pd, (k & 1) * 8192u + (j & 3) * 32u),
+                                     desc_at(vd, (j >> 2) * 16384u + (j & 3) * 2048u), id_o, o.v > 0 || (k & 1) || (j & 3) > 0);
+                        pair_commit(bar(B_KV_EMPTY + st));
+                        if (k == kSteps - 1) pair_commit(bar(B_O_DONE + buf));
+                    }
+                    __syncwarp();
+                }
+                ++gv;
+                o.output_done();
             }
             // nothing of this warp's is under way when tensor memory is freed
             if (elect_one()) pair_commit(bar(B_END));
@@ -576,7 +723,8 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
         const int r = (part & 1) * 32 + lane, half = part >> 1;     // row; keys and columns of O in halves
         const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
         const int quarter = half * 2 + wg, c0 = half * 64 + wg * 32;      // this thread's keys of a tile: [c0, c0 + 32)
-        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, to_cap = a.cap > 0.f ? 2.f * sl2 / a.cap : 0.f;
+        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint8_t *const p_row = smem + P_OFF + half * 8192;
         if (a.zero_rest && a.cu_q) {
             // rows of no sequence
@@ -591,19 +739,69 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
         }
         int n = 0, g = 0, ex = 0;
         bool ok = true;
-        // all 256 threads' values of a row, four of them, through shared memory
-        // (a role that gave up ends the loops of all of them at the same place)
+        // a row's four values, through shared memory (a role that gave up ends the loops of all of them at the same place)
         auto row_values = [&](float v, float (&got)[4]) {
             float *e = exch + (ex & 1) * 256;
             ++ex;
             e[quarter * 64 + r] = v;
-            ok = rows_meet(ok);
+            ok = !rows_meet_any(part & 1, !ok);
 #pragma unroll
             for (int k = 0; k < 4; ++k) got[k] = e[k * 64 + r];
         };
+        // A unit's O is written after the first tile of the unit behind it, which the tensor cores wait for: what is needed then
+        struct {
+            bool any, out, parts;      // a unit is left; this row is written to the outputs, or to the workspace
+            int last;                  // its last tile
+            float inv;
+            void *to;                  // this thread's 128 columns
+        } left = {false, false, false, 0, 0.f, nullptr};
+        auto write_left = [&]() {
+            if (!left.any) return;
+            left.any = false;
+            if (ok) ok = pair_wait_warp(bar(B_O_DONE + (left.last & 1)), left.last >> 1 & 1, abort_flag);
+            tc_fence_after();
+            const uint32_t from = tmem + lanes + TM_O + wg * 128;
+            if (__any_sync(0xffffffffu, left.parts)) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(from + c, o);
+                    tmem_wait_ld();
+                    if (left.parts)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) store32(static_cast<float *>(left.to) + c + k, o + k, true);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(first_bar(B_O_FREE));
+            } else {
+                uint32_t v[64];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(from + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        v[c / 2 + k] = pack(__uint_as_float(o[2 * k]) * left.inv, __uint_as_float(o[2 * k + 1]) * left.inv, bf16);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(first_bar(B_O_FREE));
+                if (left.inv == 0.f)
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) v[k] = 0u;
+                if (left.out)
+#pragma unroll
+                    for (int k = 0; k < 64; k += 8) store32(static_cast<uint16_t *>(left.to) + 2 * k, v + k, wide);
+            }
+        };
         while (ok) {
-            const int us = n & 1;
-            if (!rows_meet(pair_wait_warp(bar(B_UNIT_FULL + us), n >> 1 & 1, abort_flag))) break;
+            const int us = n % kUnits;
+            if (rows_meet_any(part & 1, !pair_wait_warp(bar(B_UNIT_FULL + us), n / kUnits & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
             const Unit w = units[us];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_UNIT_EMPTY + us));
@@ -625,7 +823,8 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 if (a.words) tree = a.tree + (int64_t)(w.q0 + i_q) * a.words;
                 if (a.slopes) slope = __ldg(a.slopes + head) * kLog2e;
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY;
+            float2 sum = make_float2(0.f, 0.f);
             for (int i = 0; i < w.tiles; ++i) {
                 const int gi = g + i, buf = gi & 1, j0 = tile_key(w, i) + c0;
                 // what this row sees of its 32 keys
@@ -645,8 +844,8 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         }
                         bits &= bits_between(max(first, 0), w.len, j0);
                         if (a.mode == 4) {
-                            for (uint32_t left = bits; left; left &= left - 1) {
-                                const int c = __ffs(left) - 1;
+                            for (uint32_t rest = bits; rest; rest &= rest - 1) {
+                                const int c = __ffs(rest) - 1;
                                 const int64_t pos = __ldg(a.positions + w.q0 + o + c);
                                 if (pos < (int64_t)row.p - a.win_left || pos > (int64_t)row.p + a.win_right) bits &= ~(1u << c);
                             }
@@ -661,42 +860,48 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         if (worse) vis &= 0x0000ffffu;
                     }
                 }
-                ok = ok && pair_wait_warp(bar(B_S_FULL + buf), gi >> 1 & 1, abort_flag);
+                // P's buffer is free once the O += P V that read it is done
+                if (ok && gi >= 2) ok = pair_wait_warp(bar(B_O_DONE + buf), (gi >> 1) - 1 & 1, abort_flag);
+                ok = ok && pair_wait_warp(bar(B_S_FULL + (gi & 3)), gi >> 2 & 1, abort_flag);
                 tc_fence_after();
                 uint32_t raw[32];
-                tmem_ld32(tmem + lanes + TM_S + buf * 64 + wg * 32, raw);
+                tmem_ld32(tmem + lanes + TM_S + (gi & 3) * 64 + wg * 32, raw);
                 tmem_wait_ld();
                 if (part == 0 && wg == 0 && lane == 0) *beat = gi;
-                float y[32];
-                if (a.cap > 0.f) {
-                    // tanh z = 1 - 2 / (e^2z + 1): off by some 2^-23 of the cap, which is what a score of its size has
+                float2 y[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        y[c] = fmaf(__fdividef(-2.f, fast_exp2(__uint_as_float(raw[c]) * to_cap) + 1.f), cap2, cap2);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(raw[c]) * sl2;
-                }
+                for (int c = 0; c < 16; ++c) y[c] = mul2(make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), sl2);
+                if (a.cap > 0.f) cap_scores(y, 1.f / cap2, cap2);
                 if (a.slopes) {
                     if (!a.words || j0 + 31 < first) {
                         const float d0 = (float)(row.p - j0);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) y[c] = fmaf(-slope, fabsf(d0 - (float)c), y[c]);
+                        for (int c = 0; c < 16; ++c) {
+                            y[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), y[c].x);
+                            y[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), y[c].y);
+                        }
                     } else {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (!(vis >> c & 1)) continue;
+                        auto fall = [&](int c) {
+                            if (!(vis >> c & 1)) return 0.f;
                             const int k = j0 + c - first;
-                            y[c] = fmaf(-slope, fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k)))), y[c]);
+                            return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k))));
+                        };
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            y[c].x -= fall(2 * c);
+                            y[c].y -= fall(2 * c + 1);
                         }
                     }
                 }
                 if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
                     uint32_t odd = 0;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
+                    for (int c = 0; c < 32; ++c)
                         if (!(fabsf(__uint_as_float(raw[c])) < INFINITY)) odd |= 1u << c;
-                        if (!(vis >> c & 1)) y[c] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        if (!(vis >> (2 * c) & 1)) y[c].x = -INFINITY;
+                        if (!(vis >> (2 * c + 1) & 1)) y[c].y = -INFINITY;
                     }
                     odd = __reduce_or_sync(0xffffffffu, odd & ~vis);
                     if (odd && lane == 0) {
@@ -704,16 +909,13 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         fence_cluster();         // before this warp's arrival
                     }
                 }
-                float top0 = -INFINITY, top1 = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    top0 = fmaxf(top0, y[c]);
-                    top1 = fmaxf(top1, y[c + 1]);
-                }
-                float top = fmaxf(top0, top1), alpha = 1.f;
-                // A row's four threads share their maxima only where one of all rows' has left the range (or a role gave up)
+                for (int c = 0; c < 16; ++c) tops[c & 3] = fmaxf(tops[c & 3], fmaxf(y[c].x, y[c].y));
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), alpha = 1.f;
+                // A row's four threads share their maxima only where one of them has left the range (or a role gave up)
                 const bool beyond = top > m + kRescale || (m == -INFINITY && top != -INFINITY);
-                if (rows_meet_any(beyond || !ok)) {
+                if (rows_meet_any(part & 1, beyond || !ok)) {
                     float got[4];
                     row_values(top, got);
                     if (!ok) break;
@@ -721,21 +923,24 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     if (top > m + kRescale || m == -INFINITY) {
                         if (m != -INFINITY) alpha = fast_exp2(m - top);
                         m = top;
-                        l *= alpha;
+                        sum.x *= alpha;
+                        sum.y *= alpha;
                     }
                 }
-                const float m_use = m == -INFINITY ? 0.f : m;
+                const float back = m == -INFINITY ? 0.f : -m;
                 uint32_t pk[16];
-                float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    const float p0 = fast_exp2(y[2 * c] - m_use), p1 = fast_exp2(y[2 * c + 1] - m_use);
-                    sum0 += p0;
-                    sum1 += p1;
-                    pk[c] = pack(p0, p1, bf16);
+                    y[c] = add2(y[c], back);
+                    y[c].x = fast_exp2(y[c].x);
+                    y[c].y = fast_exp2(y[c].y);
+                    pk[c] = pack(y[c].x, y[c].y, bf16);
                 }
-                l += sum0 + sum1;
-                // P's buffer is free: O += P V of the tile before the last was issued before this tile's S
+#pragma unroll
+                for (int c = 0; c < 8; ++c) y[c] = add2(y[c], y[c + 8]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = add2(y[c], y[c + 4]);
+                sum = add2(sum, add2(add2(y[0], y[1]), add2(y[2], y[3])));
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4 *>(p_row + buf * 16384 + sw128(r, wg * 4 + c)) =
@@ -757,99 +962,44 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_remote(first_bar(B_P_FULL + buf));
+                if (i == 0) write_left();
             }
-            if (!rows_meet(ok)) break;
-            // the row's result: columns [256 half + 128 wg, + 128) of O
-            if (w.tiles > 0) {
-                const int last = g + w.tiles - 1;
-                if (ok) ok = pair_wait_warp(bar(B_O_DONE + (last & 1)), last >> 1 & 1, abort_flag);
-                tc_fence_after();
-            }
+            // the row's sum and LSE; its values come later (columns [256 half + 128 wg, + 128) of O)
             float got[4];
-            row_values(l, got);
+            row_values(sum.x + sum.y, got);
             if (!ok) break;
-            l = (got[0] + got[1]) + (got[2] + got[3]);
+            const float l = (got[0] + got[1]) + (got[2] + got[3]);
             const bool whole = w.splits == 1;
             const int64_t out_row = w.row0 + R;
-            float inv = 0.f;
             const bool empty = m == -INFINITY && l == 0.f;      // (a row of NaN has no maximum)
+            float inv = 0.f;
             if (live && !empty) inv = 1.f / (a.sinks && whole ? l + fast_exp2(__ldg(a.sinks + head) * kLog2e - m) : l);
             const int64_t part_row = ((int64_t)w.slot * pl.splits + w.split) * kRows + R;
+            const bool parts = live && !whole, out = !parts && R < w.rows && (live || w.split == 0);
             if (quarter == 0) {
-                if (whole || !live) {
-                    if (a.lse && R < w.rows && (live || w.split == 0))
-                        a.lse[out_row] = live && !empty ? (m + log2f(l)) * kLn2 : -INFINITY;
-                } else {
-                    pl.part_ml[part_row] = make_float2(m, l);
-                }
+                if (parts) pl.part_ml[part_row] = make_float2(m, l);
+                else if (out && a.lse) a.lse[out_row] = live && !empty ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
-            // 128 bytes of each of the warp's 32 rows at a time, through shared memory (P's, which nothing reads now: the
-            // warps meet before the next unit's first P), so that they are written whole
-            const bool parts = !whole;
-            const bool write = live ? true : !parts || w.split == 0;
-            uint8_t *const pad = smem + P_OFF + (warp - 4) * 4096;
-            const int col0 = 256 * half + 128 * wg, row_first = 64 * (int)rank + (part & 1) * 32;
-            const uint32_t rows_now = __ballot_sync(0xffffffffu, R < w.rows && write);
-            const uint32_t rows_part = __ballot_sync(0xffffffffu, live && parts), rows_out = rows_now & ~rows_part;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t o[32];
-                if (w.tiles > 0) {
-                    tmem_ld32(tmem + lanes + TM_O + wg * 128 + c, o);
-                    tmem_wait_ld();
-                }
-                if (rows_part) {
-                    // fp32 partial results: 32 values of a row
+            const int col = 256 * half + 128 * wg;
+            void *const to = parts ? static_cast<void *>(reinterpret_cast<float *>(pl.part_o) + part_row * kD + col)
+                                   : static_cast<void *>(static_cast<uint16_t *>(a.out) + out_row * kD + col);
+            // rows that do not count have no O: zeros now where others of the warp leave partial results, or no tile was
+            if (out && (w.tiles == 0 || !whole)) {
+                const uint32_t none[8] = {};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(pad + sw128(lane, k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int rr = 4 * k + (lane >> 3);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(pad + sw128(rr, lane & 7));
-                        if (rows_part >> rr & 1)
-                            reinterpret_cast<uint4 *>(pl.part_o)[((part_row - r) + (part & 1) * 32 + rr) * (kD / 4) + (col0 + c) / 4 + (lane & 7)] = v;
-                    }
-                    __syncwarp();
-                    // rows that do not count, beside them
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int rr = 4 * k + (lane >> 3);
-                        if (rows_out >> rr & 1 && (lane & 4) == 0)
-                            reinterpret_cast<uint4 *>(a.out)[(w.row0 + row_first + rr) * 64 + (col0 + c) / 8 + (lane & 3)] = make_uint4(0, 0, 0, 0);
-                    }
-                } else if (rows_out) {
-                    // 64 values of dtype of a row: two rounds of 32 make its 128 bytes
-                    const int side = c >> 5 & 1;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = inv != 0.f ? pack(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv, bf16) : 0u;
-                        *reinterpret_cast<uint4 *>(pad + sw128(lane, 4 * side + k)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    if (side) {
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int rr = 4 * k + (lane >> 3);
-                            const uint4 v = *reinterpret_cast<const uint4 *>(pad + sw128(rr, lane & 7));
-                            if (rows_out >> rr & 1)
-                                reinterpret_cast<uint4 *>(a.out)[(w.row0 + row_first + rr) * 64 + (col0 + c - 32) / 8 + (lane & 7)] = v;
-                        }
-                        __syncwarp();
-                    }
-                }
+                for (int k = 0; k < 128; k += 16) store32(static_cast<uint16_t *>(to) + k, none, wide);
             }
             if (w.tiles > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_remote(first_bar(B_O_FREE));
+                left.any = true;
+                left.out = out && whole;
+                left.parts = parts;
+                left.last = g + w.tiles - 1;
+                left.inv = inv;
+                left.to = to;
+                g += w.tiles;
             }
-            g += w.tiles;
         }
+        if (ok) write_left();
     }
 
     __syncwarp();
@@ -926,7 +1076,7 @@ int dense_check(const sfm_dense_params *pp)
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
     if (p.layout_kv == SFM_LAYOUT_PAGED && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
     if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128) return SFM_ERR_INVALID_ARG;
-    if (!std::isfinite(p.softmax_scale) || !(p.softcap >= 0.f) || !std::isfinite(p.softcap)) return SFM_ERR_INVALID_ARG;
+    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || p.softcap >= 0x1p-100f) || !std::isfinite(p.softcap)) return SFM_ERR_INVALID_ARG;
     if (p.max_seqlen_kv > 1 << 30) return SFM_ERR_UNSUPPORTED;
     const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
     if (tokens * p.num_heads > INT32_MAX - 256) return SFM_ERR_UNSUPPORTED;      // rows that a copy's coordinate names

@@ -36,7 +36,7 @@ PARAMS_BAD = [
     (dict(mask_mode=1), 1), (dict(mask_mode=4, win_left=-2), 1), (dict(mask_mode=4, win_right=-2), 1), (dict(block_size=8), 3),
     (dict(block_size=40), 3), (dict(block_size=2048), 3), (dict(tree_words=-1), 1), (dict(tree_words=17), 1), (dict(split_keys=-128), 1),
     (dict(split_keys=64), 1), (dict(softmax_scale=math.inf), 1), (dict(softmax_scale=math.nan), 1), (dict(softcap=-1.0), 1),
-    (dict(softcap=math.inf), 1), (dict(softcap=math.nan), 1), (dict(batch_size=1 << 16, max_seqlen_q=1 << 10), 2),
+    (dict(softcap=math.inf), 1), (dict(softcap=math.nan), 1), (dict(softcap=1e-35), 1), (dict(batch_size=1 << 16, max_seqlen_q=1 << 10), 2),
 ]
 TENSORS_BAD = [
     ({}, dict(kv_row_stride=1008), 3), ({}, dict(kv_row_stride=1032), 3), ({}, dict(kv_rows=0), 3), ({}, dict(kv_rows=1 << 31), 2),
