@@ -285,9 +285,10 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi, int j0)
     return h > l ? up & ~down : 0u;
 }
 
-__device__ __forceinline__ uint32_t pack(float x, float y, bool bf16)
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float x, float y)
 {
-    if (bf16) {
+    if constexpr (kBf16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
@@ -333,6 +334,10 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
     return pair_of(r);
 }
 
+// Hidden keys, blocks outside the cache and drafted keys are rare among a call's tiles: their code is kept away from the
+// softmax's loop, which is long enough (with it in between, the jumps over it took 300 clocks per tile)
+#define SFM_RARELY(x) __builtin_expect(!!(x), 0)
+
 // y -> cap tanh(y / cap).  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 7 that interpolates tanh(sqrt u) /
 // sqrt u at the Chebyshev nodes of [0, 1] (off by 4e-9, and 2^-23 of roundings): multiplications and additions, where the
 // exponentials and quotients of tanh z = 1 - 2 / (e^2z + 1) would take as long as all else of a tile (scores of a tile
@@ -342,7 +347,7 @@ __device__ __forceinline__ void cap_scores(float2 (&y)[16], float inv, float cap
     float far = 0.f;
 #pragma unroll
     for (int c = 0; c < 16; ++c) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
-    if (__all_sync(0xffffffffu, far <= cap)) {
+    if (!SFM_RARELY(!__all_sync(0xffffffffu, far <= cap))) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
             const float2 z = mul2(y[c], inv), u = mul2(z, z);
@@ -379,6 +384,7 @@ __device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide)
                  : "memory");
 }
 
+template <bool kBf16, bool kCap, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap kv_map)
@@ -393,7 +399,6 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
     float *const exch = reinterpret_cast<float *>(misc + EXCH_REL);
     volatile uint32_t *const cand_words = reinterpret_cast<volatile uint32_t *>(misc + CAND_REL);
     volatile uint32_t *const fix_words = reinterpret_cast<volatile uint32_t *>(misc + FIX_REL);
-    const bool bf16 = (pl.idesc_s >> 7 & 7u) == 1u;
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -698,7 +703,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
             if (ok) ok = pair_try_wait(bar(B_FIX), n & 1);        // every lane has seen the phase
             if (!__all_sync(0xffffffffu, ok) || fix_words[5]) break;
-            const uint16_t inf = bf16 ? 0x7f80 : 0x7c00;
+            const uint16_t inf = kBf16 ? 0x7f80 : 0x7c00;
             for (int w = 0; w < 4; ++w) {
                 uint32_t m = fix_words[w];
                 while (m) {
@@ -783,7 +788,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        v[c / 2 + k] = pack(__uint_as_float(o[2 * k]) * left.inv, __uint_as_float(o[2 * k + 1]) * left.inv, bf16);
+                        v[c / 2 + k] = pack<kBf16>(__uint_as_float(o[2 * k]) * left.inv, __uint_as_float(o[2 * k + 1]) * left.inv);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -821,7 +826,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 s.len = w.len;
                 row = dense_row(a, s, i_q);
                 if (a.words) tree = a.tree + (int64_t)(w.q0 + i_q) * a.words;
-                if (a.slopes) slope = __ldg(a.slopes + head) * kLog2e;
+                if constexpr (kBias) slope = __ldg(a.slopes + head) * kLog2e;
             }
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
@@ -831,7 +836,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 uint32_t vis = bits_between(row.lo, row.hi, j0);
                 if (live) {
                     vis |= bits_between(0, w.prefix, j0);
-                    if (tree && j0 + 32 > first && j0 < w.len) {
+                    if (SFM_RARELY(tree && j0 + 32 > first && j0 < w.len)) {
                         // drafted keys: bits [j0 - first, j0 - first + 32) of the mask
                         const int o = j0 - first;
                         uint32_t bits;
@@ -852,7 +857,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         }
                         vis |= bits;
                     }
-                    if (w.bad) {
+                    if (SFM_RARELY(w.bad)) {
                         bool bad = false, worse = false;
                         box_row(a, w.b, 0, w.len, j0, &bad);
                         box_row(a, w.b, 0, w.len, j0 + 16, &worse);
@@ -871,9 +876,9 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 float2 y[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) y[c] = mul2(make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), sl2);
-                if (a.cap > 0.f) cap_scores(y, 1.f / cap2, cap2);
-                if (a.slopes) {
-                    if (!a.words || j0 + 31 < first) {
+                if constexpr (kCap) cap_scores(y, 1.f / cap2, cap2);
+                if constexpr (kBias) {
+                    if (!SFM_RARELY(a.words && j0 + 31 >= first)) {
                         const float d0 = (float)(row.p - j0);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
@@ -893,7 +898,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                         }
                     }
                 }
-                if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+                if (SFM_RARELY(!__all_sync(0xffffffffu, vis == 0xffffffffu))) {
                     uint32_t odd = 0;
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -915,7 +920,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), alpha = 1.f;
                 // A row's four threads share their maxima only where one of them has left the range (or a role gave up)
                 const bool beyond = top > m + kRescale || (m == -INFINITY && top != -INFINITY);
-                if (rows_meet_any(part & 1, beyond || !ok)) {
+                if (SFM_RARELY(rows_meet_any(part & 1, beyond || !ok))) {
                     float got[4];
                     row_values(top, got);
                     if (!ok) break;
@@ -934,7 +939,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                     y[c] = add2(y[c], back);
                     y[c].x = fast_exp2(y[c].x);
                     y[c].y = fast_exp2(y[c].y);
-                    pk[c] = pack(y[c].x, y[c].y, bf16);
+                    pk[c] = pack<kBf16>(y[c].x, y[c].y);
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) y[c] = add2(y[c], y[c + 8]);
@@ -945,7 +950,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4 *>(p_row + buf * 16384 + sw128(r, wg * 4 + c)) =
                         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (SFM_RARELY(i > 0 && __any_sync(0xffffffffu, alpha != 1.f))) {
                     if (ok) ok = pair_wait_warp(bar(B_O_DONE + (buf ^ 1)), (gi - 1) >> 1 & 1, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
@@ -962,7 +967,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_remote(first_bar(B_P_FULL + buf));
-                if (i == 0) write_left();
+                if (SFM_RARELY(i == 0)) write_left();
             }
             // the row's sum and LSE; its values come later (columns [256 half + 128 wg, + 128) of O)
             float got[4];
@@ -1018,6 +1023,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
 
 // Partial results of the pieces of a tile's keys, joined: a warp per row, four
 // times four values per lane.
+template <bool kBf16>
 __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, const Plan pl)
 {
     grid_follow();
@@ -1049,13 +1055,12 @@ __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, 
         }
     }
     const int64_t row = (int64_t)head.z + r;
-    const bool bf16 = (pl.idesc_s >> 7 & 7u) == 1u;
     float inv = 0.f;
     if (!empty) inv = 1.f / (a.sinks ? l + fast_exp2(__ldg(a.sinks + row % a.heads) * kLog2e - m) : l);
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        out[32 * k] = inv != 0.f ? make_uint2(pack(o[k].x * inv, o[k].y * inv, bf16), pack(o[k].z * inv, o[k].w * inv, bf16)) : make_uint2(0u, 0u);
+        out[32 * k] = inv != 0.f ? make_uint2(pack<kBf16>(o[k].x * inv, o[k].y * inv), pack<kBf16>(o[k].z * inv, o[k].w * inv)) : make_uint2(0u, 0u);
     if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -1149,7 +1154,10 @@ size_t dense_bytes(const Plan &pl)
     return (size_t)pl.units * kRows * (kD * 4 + 8) + (size_t)pl.slots * 16;
 }
 
-// Pairs of CTAs that the current device holds at once.
+using Kernel = void (*)(DenseArgs, Plan, CUtensorMap, CUtensorMap);
+
+// Pairs of CTAs that the current device holds at once (the same for all of the kernel's forms, which have its whole
+// shared memory).
 int dense_clusters(int *device, int *clusters)
 {
     static std::atomic<int> known[kMaxDevices];
@@ -1157,7 +1165,8 @@ int dense_clusters(int *device, int *clusters)
     const bool keep = *device < kMaxDevices;
     *clusters = keep ? known[*device].load(std::memory_order_relaxed) : 0;
     if (*clusters > 0) return SFM_OK;
-    if (cudaFuncSetAttribute(sfm_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess) return SFM_ERR_CUDA;
+    const auto kernel = sfm_dense_kernel<true, false, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess) return SFM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
@@ -1168,9 +1177,19 @@ int dense_clusters(int *device, int *clusters)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(clusters, sfm_dense_kernel, &cfg) != cudaSuccess || *clusters < 1) return SFM_ERR_CUDA;
+    if (cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg) != cudaSuccess || *clusters < 1) return SFM_ERR_CUDA;
     if (keep) known[*device].store(*clusters, std::memory_order_relaxed);
     return SFM_OK;
+}
+
+template <bool kBf16, bool kCap, bool kBias>
+cudaError_t launch(const DenseArgs &a, const Plan &pl, const CUtensorMap &q, const CUtensorMap &kv, int device, int pairs, cudaStream_t st)
+{
+    static std::atomic<bool> ready[kMaxDevices];
+    const Kernel kernel = sfm_dense_kernel<kBf16, kCap, kBias>;
+    return prepared_launch(
+        ready, device, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes); },
+        [&] { return launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kSmemBytes, st, a, pl, q, kv); });
 }
 
 }  // namespace
@@ -1288,14 +1307,12 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
     const int pairs = pl.units < clusters ? pl.units : clusters;
-    static std::atomic<bool> ready[kMaxDevices];
-    cudaError_t e = prepared_launch(
-        ready, device,
-        [&] { return cudaFuncSetAttribute(sfm_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes); },
-        [&] {
-            return launch_dependent(sfm_dense_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kSmemBytes, st, a, pl, q_map, kv_map);
-        });
+    const int form = (bf16 ? 4 : 0) | (a.cap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0);
+    static constexpr decltype(&launch<true, true, true>) forms[8] = {
+        launch<false, false, false>, launch<false, false, true>, launch<false, true, false>, launch<false, true, true>,
+        launch<true, false, false>,  launch<true, false, true>,  launch<true, true, false>,  launch<true, true, true>};
+    cudaError_t e = forms[form](a, pl, q_map, kv_map, device, pairs, st);
     if (e == cudaSuccess && pl.splits > 1)
-        e = launch_dependent(sfm_dense_join_kernel, dim3((unsigned)pl.slots * 16), dim3(256), 0, st, a, pl);
+        e = launch_dependent(bf16 ? sfm_dense_join_kernel<true> : sfm_dense_join_kernel<false>, dim3((unsigned)pl.slots * 16), dim3(256), 0, st, a, pl);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
