@@ -101,19 +101,26 @@ struct alignas(128) Unit {
     int32_t i0, h0;          // query and head of the first row
     int32_t q0, q_len, len, prefix;
     int32_t prefix_tiles, b0, tile0, tiles;    // tiles: [0, prefix_tiles) from key 0, then from key b0; this unit's part
-    int32_t slot, split, splits, bad;  // bad: a block of the range is outside the cache
+    int32_t piece, splits, part, bad;  // of how many pieces of the tile's keys (first or not), where its partial result goes;
+                                       // bad: a block of the range is outside the cache
 };
 static_assert(sizeof(Unit) <= 128, "unit area");
 
+// A slot is a tile of Q of some sequence.  Either every slot's keys are cut into pieces of at most `chunk` tiles, at most
+// `splits` of them, and units (slot, piece) go to the pairs in turns, or (balanced) the pairs share all tiles of all slots
+// evenly: pair c works through tiles [c per, (c + 1) per) of their concatenation, so that it starts in the middle of one
+// slot and ends in the middle of another.
 struct Plan {
-    int32_t slots, splits, chunk, box_rows, align, units;
+    int32_t slots, splits, chunk, box_rows, align, units, balanced, pairs;
     uint32_t idesc_s, idesc_o;
-    float4 *part_o;          // [slot][split][128][128]
-    float2 *part_ml;         // [slot][split][128]
-    int4 *head;              // [slot]: splits, rows that count, first row
+    float4 *part_o;          // partial results: [part][128][128]; balanced: part 2 c of pair c continues a slot, 2 c + 1 begins one
+    float2 *part_ml;         // [part][128]
+    int4 *head;              // [slot]: pieces, rows that count, first row, first part (balanced: pair)
     FastDiv slots_div, per_seq_div;
     int32_t per_seq;         // BSND: tiles per sequence
 };
+constexpr int kMostBalanced = 1536;           // slots; their tiles are counted by every CTA, four per thread at most
+constexpr int kLeastTiles = 4;                // of a pair's share
 
 // First slot of sequence b of a TND batch: at least one more per sequence than whole tiles lie before it, so that every
 // sequence has as many slots as tiles.
@@ -155,10 +162,71 @@ __device__ __forceinline__ int32_t box_row(const DenseArgs &a, int b, int64_t kv
     return id * a.block + (j - blk * a.block);
 }
 
-// Unit u, worked out by the whole warp.  False: nothing to do.
-__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, int u, int lane, Unit &w)
+// Keys [lo, hi) that queries [i0, i1] of a sequence see besides its prefix, by `lanes` threads of which this is the lane-th;
+// each gets its share's.  Without ranges of their own the first query sees the first key and the last one the last.
+__device__ __forceinline__ void span(const DenseArgs &a, const DenseSeq &s, int i0, int i1, int lane, int lanes, int &lo, int &hi)
 {
-    const int split = (int)fdiv((uint32_t)u, pl.slots_div), slot = pl.slots - 1 - (u - split * pl.slots);
+    lo = INT32_MAX;
+    hi = 0;
+    if (a.begin || a.end || (a.words && a.mode == 4)) {
+        for (int i = i0 + lane; i <= i1; i += lanes) {
+            const DenseRow r = dense_row(a, s, i);
+            if (r.hi > r.lo) {
+                lo = min(lo, r.lo);
+                hi = max(hi, r.hi);
+            }
+        }
+    } else {
+        lo = dense_row(a, s, i0).lo;       // 0 where that query sees nothing
+        hi = dense_row(a, s, i1).hi;
+    }
+    if (a.words) {
+        lo = min(lo, max(s.len - s.q_len, 0));
+        hi = s.len;
+    }
+}
+
+// Tiles of keys of a tile of Q whose queries see [0, prefix) and [lo, hi), and where those behind the prefix begin.
+__device__ __forceinline__ int tiles_of(const Plan &pl, int prefix, int lo, int hi, int &b0)
+{
+    int tiles = (prefix + kKeys - 1) / kKeys;
+    b0 = tiles * kKeys;
+    if (hi > lo) {
+        b0 = max(b0, lo & ~(pl.align - 1));
+        if (hi > b0) tiles += (hi - b0 + kKeys - 1) / kKeys;
+    }
+    return tiles;
+}
+
+// What a slot counts among all (balanced), found by one thread: its tiles, one if it has rows without keys, none without rows.
+__device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, int slot)
+{
+    int b, k;
+    if (a.cu_q) {
+        int lo = 0, hi = a.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot_base(a, mid) <= slot) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        k = slot - slot_base(a, b);
+    } else {
+        b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
+        k = slot - b * pl.per_seq;
+    }
+    const DenseSeq s = dense_seq(a, b);
+    const int64_t row = (int64_t)k * kRows;
+    if (k < 0 || row >= (int64_t)s.q_cap * a.heads) return 0;
+    const int64_t used = min((int64_t)s.q_len * a.heads - row, (int64_t)kRows);
+    if (used <= 0) return 1;
+    int lo, hi, b0;
+    span(a, s, (int)fdiv((uint32_t)row, a.heads_div), (int)fdiv((uint32_t)(row + used - 1), a.heads_div), 0, 1, lo, hi);
+    return max(tiles_of(pl, s.prefix, lo, hi, b0), 1);
+}
+
+// A slot, worked out by the whole warp: everything but which of its tiles a unit takes.  -1: no rows; otherwise its tiles.
+__device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int slot, int lane, Unit &w)
+{
     int b, k;
     if (a.cu_q) {
         b = find_sequence(a, slot, lane);
@@ -169,40 +237,50 @@ __device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, in
     }
     const DenseSeq s = dense_seq(a, b);
     const int64_t first_row = (int64_t)k * kRows, all = (int64_t)s.q_cap * a.heads;
-    if (k < 0 || first_row >= all) {
-        if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(0, 0, 0, 0);
-        return false;
-    }
+    if (k < 0 || first_row >= all) return -1;
     w.row0 = (int64_t)s.q0 * a.heads + first_row;
     w.rows = (int32_t)min((int64_t)kRows, all - first_row);
     w.used = (int32_t)min(max((int64_t)s.q_len * a.heads - first_row, (int64_t)0), (int64_t)w.rows);
     w.i0 = (int32_t)fdiv((uint32_t)first_row, a.heads_div);
     w.h0 = (int32_t)(first_row - (int64_t)w.i0 * a.heads);
-    // the keys that any of the tile's queries sees
     int lo = INT32_MAX, hi = 0;
-    if (w.used > 0) {
-        const int i1 = (int)fdiv((uint32_t)(first_row + w.used - 1), a.heads_div);
-        for (int i = w.i0 + lane; i <= i1; i += 32) {
-            const DenseRow r = dense_row(a, s, i);
-            if (r.hi > r.lo) {
-                lo = min(lo, r.lo);
-                hi = max(hi, r.hi);
-            }
-        }
-        if (a.words) {
-            lo = min(lo, max(s.len - s.q_len, 0));
-            hi = s.len;
-        }
-    }
+    if (w.used > 0) span(a, s, w.i0, (int)fdiv((uint32_t)(first_row + w.used - 1), a.heads_div), lane, 32, lo, hi);
     lo = warp_min(lo);
     hi = warp_max(hi);
     w.prefix = w.used > 0 ? s.prefix : 0;
     w.prefix_tiles = (w.prefix + kKeys - 1) / kKeys;
-    w.b0 = w.prefix_tiles * kKeys;
-    int tiles = w.prefix_tiles;
-    if (hi > lo) {
-        w.b0 = max(w.b0, lo & ~(pl.align - 1));
-        if (hi > w.b0) tiles += (hi - w.b0 + kKeys - 1) / kKeys;
+    w.valid = 1;
+    w.b = b;
+    w.kv0 = s.kv0;
+    w.q0 = s.q0;
+    w.q_len = s.q_len;
+    w.len = s.len;
+    return tiles_of(pl, w.prefix, lo, hi, w.b0);
+}
+
+// Blocks outside the cache among the unit's tiles, found by the whole warp.
+__device__ __forceinline__ void check_blocks(const DenseArgs &a, Unit &w, int lane)
+{
+    w.bad = 0;
+    if (a.layout_kv != SFM_LAYOUT_PAGED) return;
+    bool bad = false;
+    for (int i = lane; i < w.tiles * (kKeys / 16); i += 32) {
+        const int t = w.tile0 + i / (kKeys / 16);
+        const int j = (t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys) + i % (kKeys / 16) * 16;
+        box_row(a, w.b, 0, w.len, j, &bad);
+    }
+    w.bad = __any_sync(0xffffffffu, bad);
+    if (w.bad && lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
+}
+
+// Unit u of the plan that cuts every slot into pieces.  False: nothing to do.
+__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, int u, int lane, Unit &w)
+{
+    const int split = (int)fdiv((uint32_t)u, pl.slots_div), slot = pl.slots - 1 - (u - split * pl.slots);
+    const int tiles = make_slot(a, pl, slot, lane, w);
+    if (tiles < 0) {
+        if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(0, 0, 0, 0);
+        return false;
     }
     w.splits = tiles > pl.chunk ? min((tiles + pl.chunk - 1) / pl.chunk, pl.splits) : 1;
     const int per = (tiles + w.splits - 1) / w.splits;
@@ -210,26 +288,64 @@ __device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, in
     if (split >= w.splits) return false;
     w.tile0 = min(split * per, tiles);
     w.tiles = min(per, tiles - w.tile0);
-    w.valid = 1;
-    w.b = b;
-    w.kv0 = s.kv0;
-    w.q0 = s.q0;
-    w.q_len = s.q_len;
-    w.len = s.len;
-    w.slot = slot;
-    w.split = split;
-    if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, 0);
-    w.bad = 0;
-    if (a.layout_kv == SFM_LAYOUT_PAGED) {
-        bool bad = false;
-        for (int i = lane; i < w.tiles * (kKeys / 16); i += 32) {
-            const int t = w.tile0 + i / (kKeys / 16);
-            const int j = (t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys) + i % (kKeys / 16) * 16;
-            box_row(a, b, 0, w.len, j, &bad);
-        }
-        w.bad = __any_sync(0xffffffffu, bad);
-        if (w.bad && lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
+    w.piece = split;
+    w.part = slot * pl.splits + split;
+    if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, slot * pl.splits);
+    return true;
+}
+
+// The balanced plan's walk through a pair's share of the tiles.
+struct Share {
+    int slot = 0, off = 0, at = 0, end = 0, per = 1;      // next slot and tile of it; that tile among all, the share's end; tiles per pair
+};
+
+// Where pair c's share begins, from the slots' weights, by the whole warp.
+__device__ __forceinline__ Share make_share(const Plan &pl, const int32_t *weights, int c, int lane)
+{
+    const int each = (pl.slots + 31) / 32, at = lane * each, end = min(at + each, pl.slots);
+    int mine = 0;
+    for (int i = at; i < end; ++i) mine += weights[i];
+    int before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += v;
     }
+    const int total = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    Share s;
+    s.per = max((total + pl.pairs - 1) / pl.pairs, kLeastTiles);
+    const int64_t first = (int64_t)c * s.per;
+    if (first >= total) return s;
+    s.at = (int)first;
+    s.end = min(s.at + s.per, total);
+    // the lane whose slots hold the first tile looks for it among them
+    const int who = 31 - __clz(__ballot_sync(0xffffffffu, before <= first && (mine > 0 || lane == 0)));
+    int slot = at, off = (int)first - before;
+    if (lane == who)
+        while (slot < end - 1 && off >= weights[slot]) off -= weights[slot++];
+    s.slot = __shfl_sync(0xffffffffu, slot, who);
+    s.off = __shfl_sync(0xffffffffu, off, who);
+    return s;
+}
+
+// The share's next unit.  False: this slot has none.
+__device__ __forceinline__ bool next_of_share(const DenseArgs &a, const Plan &pl, Share &s, int c, int lane, Unit &w)
+{
+    const int slot = s.slot, off = s.off, tiles = make_slot(a, pl, slot, lane, w);
+    ++s.slot;
+    s.off = 0;
+    if (tiles < 0) return false;
+    const int weight = max(tiles, 1), take = min(weight - off, s.end - s.at), start = s.at - off;
+    s.at += take;
+    w.tile0 = off;
+    w.tiles = tiles ? take : 0;
+    w.piece = off > 0;
+    // pieces: the pairs from the one of the slot's first tile to the one of its last
+    const int c0 = start / s.per, c1 = (start + weight - 1) / s.per;
+    w.splits = c1 - c0 + 1;
+    w.part = 2 * c + (off == 0);
+    if (off == 0 && lane == 0) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, c0);
     return true;
 }
 
@@ -338,35 +454,91 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
 // softmax's loop, which is long enough (with it in between, the jumps over it took 300 clocks per tile)
 #define SFM_RARELY(x) __builtin_expect(!!(x), 0)
 
+// Hidden keys, blocks outside the cache and drafted keys are rare among a call's tiles: their code is kept away from the
+// softmax's loop, which is long enough (with it in between, the jumps over it took 300 clocks per tile)
+#define SFM_RARELY(x) __builtin_expect(!!(x), 0)
+
 // y -> cap tanh(y / cap).  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 7 that interpolates tanh(sqrt u) /
 // sqrt u at the Chebyshev nodes of [0, 1] (off by 4e-9, and 2^-23 of roundings): multiplications and additions, where the
 // exponentials and quotients of tanh z = 1 - 2 / (e^2z + 1) would take as long as all else of a tile (scores of a tile
 // 1300 clocks against 570).  That form is for larger ones.
-__device__ __forceinline__ void cap_scores(float2 (&y)[16], float inv, float cap)
+// cap tanh z of a row's 32 products with z = to_z * product.  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 5
+// that interpolates tanh(sqrt u) / sqrt u at the Chebyshev nodes of [0, 1] (off by 4.8e-7); tanh z = 1 - 2 / (e^2z + 1) for
+// larger ones, and for five pairs of the sixteen anyway: the exponentials and quotients of these run beside the
+// multiplications of the others (all by the second form, the scores of a tile took 1300 clocks; all by the first, 900).
+__device__ __forceinline__ float2 cap_wide(float2 z, float cap)
+{
+    const float2 t = mul2(z, 2.f * kLog2e);
+    return make_float2(fmaf(__fdividef(-2.f, fast_exp2(t.x) + 1.f), cap, cap), fmaf(__fdividef(-2.f, fast_exp2(t.y) + 1.f), cap, cap));
+}
+
+__device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float cap)
 {
     float far = 0.f;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
-    if (!SFM_RARELY(!__all_sync(0xffffffffu, far <= cap))) {
+    for (int c = 0; c < 16; ++c) {
+        y[c] = mul2(y[c], to_z);
+        if (c < 11) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
+    }
+    if (!SFM_RARELY(!__all_sync(0xffffffffu, far <= 1.f))) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-            const float2 z = mul2(y[c], inv), u = mul2(z, z);
-            float2 p = fma2(u, make_float2(-3.548834123e-04f, -3.548834123e-04f), 2.287645486e-03f);
-            p = fma2(p, u, -7.924946301e-03f);
-            p = fma2(p, u, 2.146998064e-02f);
-            p = fma2(p, u, -5.387273878e-02f);
-            p = fma2(p, u, 1.333219053e-01f);
-            p = fma2(p, u, -3.333328064e-01f);
-            p = fma2(p, u, 1.f);
-            y[c] = mul2(y[c], p);
+            // (in the order in which the two kinds go out side by side)
+            const int k = c % 3 == 2 ? 11 + c / 3 : c - c / 3;
+            if (k >= 11) {
+                y[k] = cap_wide(y[k], cap);
+            } else {
+                const float2 u = mul2(y[k], y[k]);
+                float2 p = fma2(u, make_float2(-3.080409251e-03f, -3.080409251e-03f), 1.677677624e-02f);
+                p = fma2(p, u, -5.163545866e-02f);
+                p = fma2(p, u, 1.328251381e-01f);
+                p = fma2(p, u, -3.332918032e-01f);
+                p = fma2(p, u, 9.999994421e-01f);
+                y[k] = mul2(mul2(y[k], cap), p);
+            }
         }
     } else {
-        const float twice = 2.f * kLog2e * inv;
-        auto f = [&](float x) { return fmaf(__fdividef(-2.f, fast_exp2(x * twice) + 1.f), cap, cap); };
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            y[c].x = f(y[c].x);
-            y[c].y = f(y[c].y);
+        for (int c = 0; c < 16; ++c) y[c] = cap_wide(y[c], cap);
+    }
+}
+
+// 16 lanes x 64 columns of tensor memory: thread t gets of every eight columns 8 i the columns 8 i + 2 (t % 4) and the one
+// behind it, of lane t / 4 in r[4 i], r[4 i + 1] and of lane t / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Thread q of four holds words 4 i + q (i = 0..7) of 32; afterwards words 8 q + i.
+__device__ __forceinline__ void gather_quad(uint32_t (&w)[8], int lane)
+{
+    uint32_t a[8];
+    // threads q and q ^ 2: the lower two take words of i < 4, the upper two the others; a[2 i], a[2 i + 1]: from the lower, the upper
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 2;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + 4], 2), own = up ? w[i + 4] : w[i];
+        a[2 * i] = up ? got : own;
+        a[2 * i + 1] = up ? own : got;
+    }
+    // threads q and q ^ 1: i of 0, 1 or of 2, 3
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a[2 * i + k] : a[2 * i + 4 + k], 1), own = up ? a[2 * i + 4 + k] : a[2 * i + k];
+            w[4 * i + 2 * k] = up ? got : own;
+            w[4 * i + 2 * k + 1] = up ? own : got;
         }
     }
 }
@@ -444,16 +616,27 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
     auto first_bar = [&](int i) { return first0 + 8u * static_cast<uint32_t>(i); };
     Unit *const units = reinterpret_cast<Unit *>(misc + UNIT_REL);
     grid_follow();
+    if (pl.balanced) {
+        // every slot's weight, for the units' warp (the softmax writes P here once it has a unit)
+        int32_t *const weights = reinterpret_cast<int32_t *>(smem + P_OFF);
+        for (int i = tid; i < pl.slots; i += kThreads) {
+            weights[i] = slot_weight(a, pl, i);
+            if (weights[i] == 0 && cluster == 0) pl.head[i] = make_int4(0, 0, 0, 0);
+        }
+        __syncthreads();
+    }
 
     if (warp == 3) {
         // ======================= units =======================
         int n = 0;
-        bool ok = true;
-        for (int u = cluster; ok; u += clusters) {
+        Share share;
+        if (pl.balanced) share = make_share(pl, reinterpret_cast<const int32_t *>(smem + P_OFF), cluster, lane);
+        for (int u = cluster;; u += clusters) {
             Unit w;
-            const bool end = u >= pl.units;
+            const bool end = pl.balanced ? share.at >= share.end || share.slot >= pl.slots : u >= pl.units;
             if (end) w.valid = 0;
-            else if (!make_unit(a, pl, u, lane, w)) continue;
+            else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w) : !make_unit(a, pl, u, lane, w)) continue;
+            else check_blocks(a, w, lane);
             const int slot = n % kUnits;
             if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
             if (lane == 0) {
@@ -728,7 +911,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
         const int r = (part & 1) * 32 + lane, half = part >> 1;     // row; keys and columns of O in halves
         const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
         const int quarter = half * 2 + wg, c0 = half * 64 + wg * 32;      // this thread's keys of a tile: [c0, c0 + 32)
-        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e;
+        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, to_z = kCap ? a.scale / a.cap : 0.f;
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint8_t *const p_row = smem + P_OFF + half * 8192;
         if (a.zero_rest && a.cu_q) {
@@ -780,25 +963,38 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 __syncwarp();
                 if (lane == 0) arrive_remote(first_bar(B_O_FREE));
             } else {
-                uint32_t v[64];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                // Four threads per row, so that a store writes 128 bytes of each of eight rows.  A loop with a small body:
+                // this code runs once per unit, and unrolled it took 3000 clocks to be fetched.
+                const uint32_t rows_out = __ballot_sync(0xffffffffu, left.out), rows_none = __ballot_sync(0xffffffffu, left.inv == 0.f);
+                // the warp's first row; rows lie 512 values apart
+                uint16_t *const top = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(left.to), 0));
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    // 16 rows, 64 columns
+                    const int h = q & 1, c = q >> 1;
                     uint32_t o[32];
-                    tmem_ld32(from + c, o);
+                    tmem_ld_quads(from + c * 64 + (static_cast<uint32_t>(16 * h) << 16), o);
                     tmem_wait_ld();
+                    if (q == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_remote(first_bar(B_O_FREE));
+                    }
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        v[c / 2 + k] = pack<kBf16>(__uint_as_float(o[2 * k]) * left.inv, __uint_as_float(o[2 * k + 1]) * left.inv);
+                    for (int e = 0; e < 2; ++e) {
+                        const int rr = 16 * h + 8 * e + (lane >> 2);
+                        const float inv = __shfl_sync(0xffffffffu, left.inv, rr);
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = pack<kBf16>(__uint_as_float(o[4 * i + 2 * e]) * inv, __uint_as_float(o[4 * i + 2 * e + 1]) * inv);
+                        gather_quad(v, lane);
+                        if (rows_none >> rr & 1)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = 0u;
+                        if (rows_out >> rr & 1) store32(top + rr * kD + 64 * c + 16 * (lane & 3), v, wide);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_remote(first_bar(B_O_FREE));
-                if (left.inv == 0.f)
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) v[k] = 0u;
-                if (left.out)
-#pragma unroll
-                    for (int k = 0; k < 64; k += 8) store32(static_cast<uint16_t *>(left.to) + 2 * k, v + k, wide);
             }
         };
         while (ok) {
@@ -875,8 +1071,13 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 if (part == 0 && wg == 0 && lane == 0) *beat = gi;
                 float2 y[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) y[c] = mul2(make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), sl2);
-                if constexpr (kCap) cap_scores(y, 1.f / cap2, cap2);
+                for (int c = 0; c < 16; ++c) y[c] = make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
+                if constexpr (kCap) {
+                    cap_scores(y, to_z, cap2);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) y[c] = mul2(y[c], sl2);
+                }
                 if constexpr (kBias) {
                     if (!SFM_RARELY(a.words && j0 + 31 >= first)) {
                         const float d0 = (float)(row.p - j0);
@@ -978,12 +1179,12 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             const int64_t out_row = w.row0 + R;
             const bool empty = m == -INFINITY && l == 0.f;      // (a row of NaN has no maximum)
             float inv = 0.f;
-            if (live && !empty) inv = 1.f / (a.sinks && whole ? l + fast_exp2(__ldg(a.sinks + head) * kLog2e - m) : l);
-            const int64_t part_row = ((int64_t)w.slot * pl.splits + w.split) * kRows + R;
-            const bool parts = live && !whole, out = !parts && R < w.rows && (live || w.split == 0);
+            if (live && !empty) inv = __fdividef(1.f, a.sinks && whole ? l + fast_exp2(__ldg(a.sinks + head) * kLog2e - m) : l);
+            const int64_t part_row = (int64_t)w.part * kRows + R;
+            const bool parts = live && !whole, out = !parts && R < w.rows && (live || w.piece == 0);
             if (quarter == 0) {
                 if (parts) pl.part_ml[part_row] = make_float2(m, l);
-                else if (out && a.lse) a.lse[out_row] = live && !empty ? (m + log2f(l)) * kLn2 : -INFINITY;
+                else if (out && a.lse) a.lse[out_row] = live && !empty ? (m + __log2f(l)) * kLn2 : -INFINITY;
             }
             const int col = 256 * half + 128 * wg;
             void *const to = parts ? static_cast<void *>(reinterpret_cast<float *>(pl.part_o) + part_row * kD + col)
@@ -1030,21 +1231,22 @@ __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, 
     const int slot = blockIdx.x >> 4, r = (blockIdx.x & 15) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int4 head = pl.head[slot];
     if (head.x <= 1 || r >= head.y) return;
-    const int64_t base = (int64_t)slot * pl.splits * kRows + r;
+    // rows of the pieces' partial results
+    auto row_of = [&](int s) { return (int64_t)(!pl.balanced ? head.w + s : s == 0 ? 2 * head.w + 1 : 2 * (head.w + s)) * kRows + r; };
     float m = -INFINITY, l = 0.f;
     bool empty = true;
     for (int s = 0; s < head.x; ++s) {
-        const float2 ml = pl.part_ml[base + s * kRows];
+        const float2 ml = pl.part_ml[row_of(s)];
         m = fmaxf(m, ml.x);
         empty &= ml.x == -INFINITY && ml.y == 0.f;
     }
     float4 o[4] = {};
     for (int s = 0; s < head.x; ++s) {
-        const float2 ml = pl.part_ml[base + s * kRows];
+        const float2 ml = pl.part_ml[row_of(s)];
         if (ml.x == -INFINITY && ml.y == 0.f) continue;
         const float e = fast_exp2(ml.x - m);
         l = fmaf(e, ml.y, l);
-        const float4 *from = pl.part_o + (base + s * kRows) * (kD / 4) + lane;
+        const float4 *from = pl.part_o + row_of(s) * (kD / 4) + lane;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float4 v = from[32 * k];
@@ -1081,7 +1283,8 @@ int dense_check(const sfm_dense_params *pp)
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
     if (p.layout_kv == SFM_LAYOUT_PAGED && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
     if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128) return SFM_ERR_INVALID_ARG;
-    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || p.softcap >= 0x1p-100f) || !std::isfinite(p.softcap)) return SFM_ERR_INVALID_ARG;
+    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || p.softcap >= 0x1p-100f) || !std::isfinite(p.softcap) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
+        return SFM_ERR_INVALID_ARG;
     if (p.max_seqlen_kv > 1 << 30) return SFM_ERR_UNSUPPORTED;
     const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
     if (tokens * p.num_heads > INT32_MAX - 256) return SFM_ERR_UNSUPPORTED;      // rows that a copy's coordinate names
@@ -1131,15 +1334,16 @@ int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
     const int64_t slots = p.layout_q == SFM_LAYOUT_TND ? rows / kRows + p.batch_size : (int64_t)p.batch_size * pl->per_seq;
     const int64_t tiles = ((int64_t)p.max_seqlen_kv + kKeys - 1) / kKeys + 2;
     int64_t chunk = tiles;
+    pl->balanced = 0;
     if (p.split_keys) {
         chunk = p.split_keys / kKeys;
-    } else if (slots < 2 * (int64_t)clusters) {
-        const int64_t pieces = 2 * (int64_t)clusters / (slots > 0 ? slots : 1);
-        chunk = (tiles + pieces - 1) / pieces;
-        if (chunk < 4) chunk = 4;
+    } else if (slots <= kMostBalanced && p.max_seqlen_kv > 8 * kKeys && slots * tiles < 1ll << 30) {
+        pl->balanced = 1;
     }
-    const int64_t splits = (tiles + chunk - 1) / chunk;
+    const int64_t splits = pl->balanced ? 2 : (tiles + chunk - 1) / chunk;
     if (slots * splits > INT32_MAX - 2 * (int64_t)clusters) return SFM_ERR_UNSUPPORTED;
+    const int64_t most = pl->balanced ? (slots * tiles + kLeastTiles - 1) / kLeastTiles : slots * splits;
+    pl->pairs = (int32_t)(most < clusters ? most : clusters);
     pl->slots = (int32_t)slots;
     pl->splits = (int32_t)splits;
     pl->chunk = (int32_t)chunk;
@@ -1147,11 +1351,11 @@ int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
     return SFM_OK;
 }
 
-// workspace: partial rows, then their maxima and sums, then a word of four integers per slot
+// workspace: partial rows, then their maxima and sums, then four integers per slot
+size_t dense_parts(const Plan &pl) { return pl.splits <= 1 ? 0 : pl.balanced ? 2 * (size_t)pl.pairs : (size_t)pl.units; }
 size_t dense_bytes(const Plan &pl)
 {
-    if (pl.splits <= 1) return 0;
-    return (size_t)pl.units * kRows * (kD * 4 + 8) + (size_t)pl.slots * 16;
+    return pl.splits <= 1 ? 0 : dense_parts(pl) * kRows * (kD * 4 + 8) + (size_t)pl.slots * 16;
 }
 
 using Kernel = void (*)(DenseArgs, Plan, CUtensorMap, CUtensorMap);
@@ -1183,13 +1387,13 @@ int dense_clusters(int *device, int *clusters)
 }
 
 template <bool kBf16, bool kCap, bool kBias>
-cudaError_t launch(const DenseArgs &a, const Plan &pl, const CUtensorMap &q, const CUtensorMap &kv, int device, int pairs, cudaStream_t st)
+cudaError_t launch(const DenseArgs &a, const Plan &pl, const CUtensorMap &q, const CUtensorMap &kv, int device, cudaStream_t st)
 {
     static std::atomic<bool> ready[kMaxDevices];
     const Kernel kernel = sfm_dense_kernel<kBf16, kCap, kBias>;
     return prepared_launch(
         ready, device, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes); },
-        [&] { return launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kSmemBytes, st, a, pl, q, kv); });
+        [&] { return launch_dependent(kernel, dim3((unsigned)(2 * pl.pairs)), dim3(kThreads), (size_t)kSmemBytes, st, a, pl, q, kv); });
 }
 
 }  // namespace
@@ -1298,20 +1502,19 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     pl.idesc_o = idesc_f16(kRows, 256, bf16, false, true);
     if (pl.splits > 1) {
         pl.part_o = static_cast<float4 *>(workspace);
-        pl.part_ml = reinterpret_cast<float2 *>(pl.part_o + (size_t)pl.units * kRows * (kD / 4));
-        pl.head = reinterpret_cast<int4 *>(pl.part_ml + (size_t)pl.units * kRows);
+        pl.part_ml = reinterpret_cast<float2 *>(pl.part_o + dense_parts(pl) * kRows * (kD / 4));
+        pl.head = reinterpret_cast<int4 *>(pl.part_ml + dense_parts(pl) * kRows);
     }
     CUtensorMap q_map, kv_map;
     rc = make_map(&q_map, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
     if (!rc) rc = make_map(&kv_map, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, pl.box_rows == 64 ? kBlocks : 1);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
-    const int pairs = pl.units < clusters ? pl.units : clusters;
     const int form = (bf16 ? 4 : 0) | (a.cap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0);
     static constexpr decltype(&launch<true, true, true>) forms[8] = {
         launch<false, false, false>, launch<false, false, true>, launch<false, true, false>, launch<false, true, true>,
         launch<true, false, false>,  launch<true, false, true>,  launch<true, true, false>,  launch<true, true, true>};
-    cudaError_t e = forms[form](a, pl, q_map, kv_map, device, pairs, st);
+    cudaError_t e = forms[form](a, pl, q_map, kv_map, device, st);
     if (e == cudaSuccess && pl.splits > 1)
         e = launch_dependent(bf16 ? sfm_dense_join_kernel<true> : sfm_dense_join_kernel<false>, dim3((unsigned)pl.slots * 16), dim3(256), 0, st, a, pl);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
