@@ -468,6 +468,7 @@ _DENSE_PARAMS = struct.Struct("@16i2f")
 _DENSE_TENSORS = struct.Struct("@PPqqPi11P")
 _MERGE_PARAMS = struct.Struct("@6i")
 _MOVE_PARAMS = struct.Struct("@6i2q")
+_POINTERS = [struct.Struct(f"@{n}P") for n in range(MERGE_MAX_PARTS + 1)]
 _SCORE_TYPES = {torch.float32: 0}
 _SIXTEEN_BIT = {torch.bfloat16: BF16, torch.float16: FP16}
 _INDEX_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
@@ -819,6 +820,7 @@ def select_topk(scores: torch.Tensor, k: int, *, lengths=None, block_size: int =
 # many queries over the same rows: more kinds of scores and masks, drafted trees
 # ---------------------------------------------------------------------------
 _I64 = torch.int64
+_dense_need = {}
 
 
 def _no_gradient(name, x):
@@ -873,42 +875,58 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         cols = block_table.shape[1]
         table = _address("block_table", block_table, _I32, dev, (batch, cols))
     if tree_mask is not None:
-        words = _tensor("tree_mask", tree_mask).shape[-1] if _tensor("tree_mask", tree_mask).dim() else 0
+        words = tree_mask.shape[-1] if _tensor("tree_mask", tree_mask).dim() else 0
         tree = _address("tree_mask", tree_mask, _I64, dev, per_token + (words,))
         place = _address("positions", positions, _I32, dev, per_token)
         if not words:
             raise ValueError("tree_mask: needs a word per token")
-    ints = [0 if x is None else _address(name, x, _I32, dev, need)
-            for name, x, need in (("cu_seqlens_q", cu_seqlens_q, (batch + 1,)), ("cu_seqlens_kv", cu_seqlens_kv, (batch + 1,)),
-                                  ("seqused_q", seqused_q, each), ("seqused_kv", seqused_kv, each),
-                                  ("prefix_lens", prefix_lens, each), ("key_begin", key_begin, per_token),
-                                  ("key_end", key_end, per_token))]
     params = _DENSE_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
                                 code, kshape[1] if lkv == PAGED else 0, words, split_keys, out is None, softmax_scale, softcap)
     tensors = _DENSE_TENSORS.pack(
-        _address("q", q, q.dtype, dev, shape), kv.data_ptr(), row_stride, rows, table, cols, *ints[:4],
+        _address("q", q, q.dtype, dev, shape), kv.data_ptr(), row_stride, rows, table, cols,
+        0 if cu_seqlens_q is None else _address("cu_seqlens_q", cu_seqlens_q, _I32, dev, (batch + 1,)),
+        0 if cu_seqlens_kv is None else _address("cu_seqlens_kv", cu_seqlens_kv, _I32, dev, (batch + 1,)),
+        0 if seqused_q is None else _address("seqused_q", seqused_q, _I32, dev, each),
+        0 if seqused_kv is None else _address("seqused_kv", seqused_kv, _I32, dev, each),
         0 if sinks is None else _address("sinks", sinks, _F32, dev, (heads,)),
-        0 if bias_slopes is None else _address("bias_slopes", bias_slopes, _F32, dev, (heads,)), *ints[4:], tree, place)
-    given = [x for x in (out, lse) if x is not None]
+        0 if bias_slopes is None else _address("bias_slopes", bias_slopes, _F32, dev, (heads,)),
+        0 if prefix_lens is None else _address("prefix_lens", prefix_lens, _I32, dev, each),
+        0 if key_begin is None else _address("key_begin", key_begin, _I32, dev, per_token),
+        0 if key_end is None else _address("key_end", key_end, _I32, dev, per_token), tree, place)
+    given = ()
+    if out is not None:
+        given = (out,)
+        to = _address("out", out, q.dtype, dev, shape)
+        _no_gradient("out", out)
+    if lse is not None:
+        given += (lse,)
+        end = _address("lse", lse, _F32, dev, rows_shape)
+        _no_gradient("lse", lse)
+    # the workspace's size depends on the parameters and the device alone
+    need = _dense_need.get((params, dev))
+    if need is None:
+        size = C.c_size_t(0)
+        rc = lib().sfm_dense_workspace_size(params, size)
+        if rc:
+            raise SfmError("sfm_dense_workspace_size", rc)
+        if len(_dense_need) >= 4096:
+            _dense_need.clear()
+        need = _dense_need[params, dev] = size.value
+    room = 0
+    if workspace is not None:
+        if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
+            raise ValueError(f"workspace: needs a contiguous tensor on cuda:{dev}")
+        room = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, room = torch.empty(need, dtype=torch.uint8, device=q.device), need
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        to = out.data_ptr()
     if lse is None:
         lse = torch.empty(rows_shape, dtype=_F32, device=q.device)
-    got = _address("out", out, q.dtype, dev, shape), _address("lse", lse, _F32, dev, rows_shape)
-    for x in given:
-        _no_gradient("out" if x is out else "lse", x)
-    need = C.c_size_t(0)
-    rc = (_lib or lib()).sfm_dense_workspace_size(params, need)
-    if not rc:
-        if workspace is None and need.value:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-        room = 0
-        if workspace is not None:
-            if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
-                raise ValueError(f"workspace: needs a contiguous tensor on cuda:{dev}")
-            room = workspace.numel() * workspace.element_size()
-        rc = _lib.sfm_dense_forward(params, tensors, got[0], got[1], workspace.data_ptr() if room else 0, room,
-                                    0 if status is None else _status_address(status, dev), _raw_stream(dev))
+        end = lse.data_ptr()
+    rc = _lib.sfm_dense_forward(params, tensors, to, end, workspace.data_ptr() if room else 0, room,
+                                0 if status is None else _status_address(status, dev), _raw_stream(dev))
     if rc:
         raise SfmError("sfm_dense_forward", rc)
     for x in given:
@@ -990,30 +1008,40 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
     shape = x.shape
     if len(shape) < 2:
         raise ValueError("outs: need (..., heads, dim)")
-    heads, dim, rows = shape[-2], shape[-1], shape[:-1].numel()
+    kind, lead, grad = x.dtype, shape[:-1], torch.is_grad_enabled()
+    heads, dim, rows = lead[-1], shape[-1], lead.numel()
     parts, ends = [], []
-    for o, l in zip(outs, lses):
-        parts.append(_address("outs", o, x.dtype, dev, shape))
+    for o in outs:
+        parts.append(_address("outs", o, kind, dev, shape))
+        if grad and o.requires_grad:
+            _no_gradient("outs", o)
+    for l in lses:
         if _tensor("lses", l).numel() != rows:
             raise ValueError(f"lses: {l.numel()} values, expected {rows}")
         ends.append(_address("lses", l, _F32, dev, l.shape))
-        _no_gradient("outs", o)
-        _no_gradient("lses", l)
-    given = [y for y in (out, lse) if y is not None]
-    for y in given:
-        _no_gradient("out" if y is out else "lse", y)
+        if grad and l.requires_grad:
+            _no_gradient("lses", l)
+    given = ()
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=kind, device=x.device)
+        to = out.data_ptr()
+    else:
+        given = (out,)
+        to = _address("out", out, kind, dev, shape)
+        _no_gradient("out", out)
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=_F32, device=x.device)
-    elif any(lse.data_ptr() == e for e in ends):
-        raise ValueError("lse: must not be one of lses")
-    n = len(outs)
-    params = _MERGE_PARAMS.pack(rows // heads if heads else 0, heads or 1, dim, n, code, 0)
-    rc = (_lib or lib()).sfm_merge(params, struct.pack(f"@{n}P", *parts), struct.pack(f"@{n}P", *ends),
-                                   0 if sinks is None else _address("sinks", sinks, _F32, dev, (heads,)),
-                                   _address("out", out, x.dtype, dev, shape), _address("lse", lse, _F32, dev, shape[:-1]),
-                                   _raw_stream(dev))
+        lse = torch.empty(lead, dtype=_F32, device=x.device)
+        end = lse.data_ptr()
+    else:
+        given += (lse,)
+        end = _address("lse", lse, _F32, dev, lead)
+        _no_gradient("lse", lse)
+        if end in ends:
+            raise ValueError("lse: must not be one of lses")
+    n = len(parts)
+    rc = (_lib or lib()).sfm_merge(_MERGE_PARAMS.pack(rows // heads if heads else 0, heads or 1, dim, n, code, 0),
+                                   _POINTERS[n].pack(*parts), _POINTERS[n].pack(*ends),
+                                   0 if sinks is None else _address("sinks", sinks, _F32, dev, (heads,)), to, end, _raw_stream(dev))
     if rc:
         raise SfmError("sfm_merge", rc)
     for y in given:

@@ -3,7 +3,9 @@
 //
 //     M = max_n LSE_n,  w_n = e^(LSE_n - M),  O = sum_n w_n O_n / (sum_n w_n + e^(sink - M)),  LSE = M + log sum_n w_n
 //
-// Every value is read and written once, a few operations each: memory bounds it.
+// Every value is read and written once, a few operations each: memory bounds
+// it.  A warp takes a row at a time; its lanes work out the same weights and
+// take 16 bytes of the row each, all parts' loads before the first use.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -13,7 +15,9 @@
 namespace sfm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct MergeArgs {
     const uint4 *outs[SFM_MERGE_MAX_PARTS];
@@ -21,9 +25,8 @@ struct MergeArgs {
     const float *sinks;
     uint4 *out;
     float *lse;
-    int64_t rows;
-    int32_t heads, chunks, parts;     // chunks: 16-byte pieces of a row
-    FastDiv chunk_div;
+    int32_t rows, chunks, parts;      // chunks: 16-byte pieces of a row
+    FastDiv heads_div;
 };
 
 template <typename T>
@@ -60,36 +63,88 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One thread per 16-byte piece of a row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sfm_merge_kernel(const MergeArgs a)
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// N: the number of parts, as far as the loads of a piece go out together
+template <typename T, int N>
+__global__ void __launch_bounds__(32 * kWarps) sfm_merge_kernel(const MergeArgs a)
 {
     grid_follow();
-    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t row = at / a.chunks;
-    if (row >= a.rows) return;
-    float w[SFM_MERGE_MAX_PARTS], m = -INFINITY;
-    for (int n = 0; n < a.parts; ++n) {
-        w[n] = a.lses[n][row];
-        m = w[n] > m || w[n] != w[n] ? w[n] : m;       // a NaN stays
-    }
-    float f[8] = {}, total = 0.f;
-    if (m != -INFINITY) {
-        for (int n = 0; n < a.parts; ++n) {
-            if (w[n] == -INFINITY) continue;
-            const float e = expf(w[n] - m);
-            float x[8];
-            widen<T>(a.outs[n][at], x);
-            total += e;
+    const int lane = threadIdx.x & 31;
+    for (int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); row < a.rows; row += (int64_t)gridDim.x * kWarps) {
+        const int64_t base = row * a.chunks;
+        // the lane's first pieces are under way while the weights are worked out; a part without keys is not used
+        uint4 v[N][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = fmaf(e, x[i], f[i]);
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (n < a.parts && lane + 32 * k < a.chunks) v[n][k] = a.outs[n][base + lane + 32 * k];
+        float w[N], m = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            w[n] = n < a.parts ? a.lses[n][row] : -INFINITY;
+            m = w[n] > m || w[n] != w[n] ? w[n] : m;       // a NaN stays
         }
-        const float inv = 1.f / (a.sinks ? total + expf(a.sinks[row % a.heads] - m) : total);
+        float total = 0.f, inv = 0.f;
+        if (m != -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= inv;
+            for (int n = 0; n < N; ++n) {
+                w[n] = w[n] == -INFINITY ? 0.f : exp2_fast((w[n] - m) * kLog2e);
+                total += w[n];
+            }
+            float under = total;
+            if (a.sinks) {
+                const int head = (int)((uint32_t)row - fdiv((uint32_t)row, a.heads_div) * a.heads_div.d);
+                under += exp2_fast((__ldg(a.sinks + head) - m) * kLog2e);
+            }
+            inv = 1.f / under;
+        }
+        uint32_t used = 0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if (m != -INFINITY && w[n] != 0.f) used |= 1u << n;
+            w[n] *= inv;
+        }
+        for (int c0 = 0; c0 < a.chunks; c0 += 64) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = c0 + 32 * k + lane;
+                if (c >= a.chunks) continue;
+                float f[8] = {};
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if (!(used >> n & 1)) continue;
+                    float x[8];
+                    widen<T>(c0 == 0 ? v[n][k] : a.outs[n][base + c], x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = fmaf(w[n], x[i], f[i]);
+                }
+                a.out[base + c] = narrow<T>(f);
+            }
+        }
+        if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? m : m + __log2f(total) * kLn2;
     }
-    a.out[at] = narrow<T>(f);
-    if (a.lse && at == row * a.chunks) a.lse[row] = m == -INFINITY ? m : m + logf(total);
+}
+
+template <typename T>
+cudaError_t launch(const MergeArgs &a, int sms, cudaStream_t st)
+{
+    // as many rows per warp as keep some 8 CTAs on every SM busy
+    const int64_t blocks = ((int64_t)a.rows + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
+    const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(32 * kWarps);
+    switch (a.parts) {
+    case 1: return launch_dependent(sfm_merge_kernel<T, 1>, grid, block, 0, st, a);
+    case 2: return launch_dependent(sfm_merge_kernel<T, 2>, grid, block, 0, st, a);
+    case 3: return launch_dependent(sfm_merge_kernel<T, 3>, grid, block, 0, st, a);
+    case 4: return launch_dependent(sfm_merge_kernel<T, 4>, grid, block, 0, st, a);
+    default: return launch_dependent(sfm_merge_kernel<T, SFM_MERGE_MAX_PARTS>, grid, block, 0, st, a);
+    }
 }
 
 }  // namespace
@@ -107,9 +162,10 @@ extern "C" int sfm_merge(const sfm_merge_params *pp, const void *const *outs, co
     if (p.dtype != SFM_DTYPE_BF16 && p.dtype != SFM_DTYPE_FP16) return SFM_ERR_INVALID_ARG;
     if (p.head_dim % 8) return SFM_ERR_LAYOUT;
     if (p.tokens == 0) return SFM_OK;
-    if (!out || ((uintptr_t)sinks | (uintptr_t)lse) & 3u) return !out ? SFM_ERR_INVALID_ARG : SFM_ERR_LAYOUT;
+    if (!out) return SFM_ERR_INVALID_ARG;
+    if ((int64_t)p.tokens * p.heads > INT32_MAX) return SFM_ERR_UNSUPPORTED;
     MergeArgs a = {};
-    uintptr_t bits = (uintptr_t)out;
+    uintptr_t bits = (uintptr_t)out | (((uintptr_t)sinks | (uintptr_t)lse) & 3u);
     for (int n = 0; n < p.parts; ++n) {
         if (!outs[n] || !lses[n]) return SFM_ERR_INVALID_ARG;
         bits |= (uintptr_t)outs[n] | ((uintptr_t)lses[n] & 3u);
@@ -120,17 +176,12 @@ extern "C" int sfm_merge(const sfm_merge_params *pp, const void *const *outs, co
     a.sinks = sinks;
     a.out = static_cast<uint4 *>(out);
     a.lse = lse;
-    a.rows = (int64_t)p.tokens * p.heads;
-    if (a.rows > INT32_MAX) return SFM_ERR_UNSUPPORTED;
-    a.heads = p.heads;
+    a.rows = p.tokens * p.heads;
     a.chunks = p.head_dim / 8;
     a.parts = p.parts;
-    const int64_t blocks = (a.rows * a.chunks + kThreads - 1) / kThreads;
-    if (blocks > INT32_MAX) return SFM_ERR_UNSUPPORTED;
-    const cudaError_t e = p.dtype == SFM_DTYPE_BF16
-                              ? launch_dependent(sfm_merge_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                                                 (cudaStream_t)stream, a)
-                              : launch_dependent(sfm_merge_kernel<__half>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                                                 (cudaStream_t)stream, a);
+    a.heads_div = make_fastdiv((uint32_t)p.heads);
+    int device = 0, sms = 0;
+    if (current_sms(&device, &sms) != cudaSuccess) return SFM_ERR_CUDA;
+    const cudaError_t e = p.dtype == SFM_DTYPE_BF16 ? launch<__nv_bfloat16>(a, sms, (cudaStream_t)stream) : launch<__half>(a, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }

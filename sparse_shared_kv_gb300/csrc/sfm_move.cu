@@ -52,32 +52,39 @@ __global__ void __launch_bounds__(kThreads) sfm_move_kernel(const MoveArgs a)
     int32_t before = -1;
     bool more = true;
     for (int i0 = 0; i0 < a.max_path && more; i0 += kAhead) {
-        uint4 v[kAhead];
-        uint8_t *to[kAhead];
+        // eight entries, then their pages, then their rows: three round trips for all of them
+        int32_t from[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) from[k] = i0 + k < a.max_path ? __ldg(path + i0 + k) : -1;
+        int64_t src[kAhead], dst[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            to[k] = nullptr;
-            if (!more || i0 + k >= a.max_path) continue;
-            const int32_t from = __ldg(path + i0 + k);
-            more = from > before;
-            if (!more) {
-                if (from >= 0 && tell) atomicOr(a.status, SFM_STATUS_BAD_INDEX);
+            src[k] = row_of(a, b, from[k] >= 0 ? first + from[k] : -1);
+            dst[k] = row_of(a, b, from[k] >= 0 ? first + i0 + k : -1);
+        }
+        uint4 v[kAhead];
+        uint32_t moved = 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (!more) continue;
+            if (from[k] <= before) {
+                more = false;
+                if (from[k] >= 0 && tell) atomicOr(a.status, SFM_STATUS_BAD_INDEX);
                 continue;
             }
-            before = from;
-            const int64_t src = row_of(a, b, first + from), dst = row_of(a, b, first + i0 + k);
-            more = src >= 0 && dst >= 0;
-            if (!more) {
+            before = from[k];
+            if (src[k] < 0 || dst[k] < 0) {
+                more = false;
                 if (tell) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
                 continue;
             }
-            if (src == dst) continue;
-            v[k] = *reinterpret_cast<const uint4 *>(a.cache + src * a.row_stride + (int64_t)piece * 16);
-            to[k] = a.cache + dst * a.row_stride + (int64_t)piece * 16;
+            if (src[k] == dst[k]) continue;
+            v[k] = *reinterpret_cast<const uint4 *>(a.cache + src[k] * a.row_stride + (int64_t)piece * 16);
+            moved |= 1u << k;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = v[k];
+            if (moved >> k & 1) *reinterpret_cast<uint4 *>(a.cache + dst[k] * a.row_stride + (int64_t)piece * 16) = v[k];
     }
 }
 
