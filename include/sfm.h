@@ -595,10 +595,11 @@ int sfm_dense_workspace_size(const sfm_dense_params *params, size_t *bytes);
  * itself); mode 4 takes away those outside [pos(i) - win_left, pos(i) + win_right].
  * A row without visible keys has O = 0 and LSE = -inf, as have rows of q at or
  * beyond seqused_q.  Keys that a row does not see have no part in it, whatever
- * they hold (NaN and infinities too); a row that sees a key with a score that is
- * NaN or +inf is NaN.  A block outside the cache is not visible and sets
+ * they hold (NaN and infinities too); a row that sees a NaN is NaN, and what a row
+ * holds that sees an infinity is not specified.  A block outside the cache is not visible and sets
  * SFM_STATUS_BAD_BLOCK.
- * out: q's layout; lse: device fp32 (tokens x num_heads) or NULL; workspace:
+ * out: q's layout, 16-byte aligned (fastest with 32), apart from the inputs;
+ * lse: device fp32 (tokens x num_heads) or NULL; workspace:
  * device, >= sfm_dense_workspace_size() bytes, 256-byte aligned, used by one
  * call at a time.  Products are exact, sums in fp32; weights e^x are rounded to
  * dtype for the product with kv. */

@@ -119,29 +119,49 @@ struct Plan {
     FastDiv slots_div, per_seq_div;
     int32_t per_seq;         // BSND: tiles per sequence
 };
-constexpr int kMostBalanced = 1536;           // slots; their tiles are counted by every CTA, four per thread at most
+constexpr int kMostBalanced = 1536;           // slots, and sequences; their tiles are counted by every CTA, four slots per thread at most
 constexpr int kLeastTiles = 4;                // of a pair's share
+static_assert(kMostBalanced * 4 <= 32768 && kMostBalanced * sizeof(DenseSeq) <= kStages * kStageBytes, "counted in P's and the stages' memory");
 
-// First slot of sequence b of a TND batch: at least one more per sequence than whole tiles lie before it, so that every
-// sequence has as many slots as tiles.
-__device__ __forceinline__ int slot_base(const DenseArgs &a, int b)
-{
-    const int64_t c = min(max(__ldg(a.cu_q + b), 0), a.total_q);
-    return (int)(c * a.heads / kRows) + b;
-}
+// First slot of a sequence of a TND batch whose first row is q0: at least one more per sequence than whole tiles lie before
+// it, so that every sequence has as many slots as tiles.
+__device__ __forceinline__ int slot_base(const DenseArgs &a, int b, int q0) { return (int)((int64_t)q0 * a.heads / kRows) + b; }
 
-// The largest b with slot_base(b) <= slot, found by the warp, 32 ways at a time.
-__device__ __forceinline__ int find_sequence(const DenseArgs &a, int slot, int lane)
+__device__ __forceinline__ int first_query(const DenseArgs &a, int b) { return min(max(__ldg(a.cu_q + b), 0), a.total_q); }
+
+// The sequence of a slot, found by the whole warp, and the slot's number k in it (< 0: none).  Up to 32 sequences are all
+// read at once; of more the one is found 32 ways at a time.
+__device__ __forceinline__ DenseSeq slot_sequence(const DenseArgs &a, const Plan &pl, int slot, int lane, int &k)
 {
+    if (!a.cu_q) {
+        const int b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
+        k = slot - b * pl.per_seq;
+        return dense_seq(a, b);
+    }
+    if (a.batch <= 32) {
+        DenseSeq s = dense_seq(a, min(lane, a.batch - 1));
+        const int who = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || (lane < a.batch && slot_base(a, lane, s.q0) <= slot)));
+        s.b = who;
+        s.q0 = __shfl_sync(0xffffffffu, s.q0, who);
+        s.q_cap = __shfl_sync(0xffffffffu, s.q_cap, who);
+        s.q_len = __shfl_sync(0xffffffffu, s.q_len, who);
+        s.len = __shfl_sync(0xffffffffu, s.len, who);
+        s.prefix = __shfl_sync(0xffffffffu, s.prefix, who);
+        s.kv0 = __shfl_sync(0xffffffffu, s.kv0, who);
+        k = slot - slot_base(a, who, s.q0);
+        return s;
+    }
     int lo = 0, n = a.batch;
     while (n > 1) {
         const int step = (n + 31) / 32, b = lo + lane * step;
-        const bool below = lane * step < n && (lane == 0 || slot_base(a, b) <= slot);
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));
-        lo += k * step;
-        n = min(step, n - k * step);
+        const bool below = lane * step < n && (lane == 0 || slot_base(a, b, first_query(a, b)) <= slot);
+        const int w = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        lo += w * step;
+        n = min(step, n - w * step);
     }
-    return lo;
+    const DenseSeq s = dense_seq(a, lo);
+    k = slot - slot_base(a, lo, s.q0);
+    return s;
 }
 
 __device__ __forceinline__ int warp_min(int v) { return __reduce_min_sync(0xffffffffu, v); }
@@ -198,23 +218,30 @@ __device__ __forceinline__ int tiles_of(const Plan &pl, int prefix, int lo, int 
     return tiles;
 }
 
-// What a slot counts among all (balanced), found by one thread: its tiles, one if it has rows without keys, none without rows.
-__device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, int slot)
+// The same from the batch's sequences in shared memory, by one thread.
+__device__ __forceinline__ DenseSeq known_sequence(const DenseArgs &a, const Plan &pl, int slot, const DenseSeq *seqs, int &k)
 {
-    int b, k;
+    int b;
     if (a.cu_q) {
         int lo = 0, hi = a.batch - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (slot_base(a, mid) <= slot) lo = mid; else hi = mid - 1;
+            if (slot_base(a, mid, seqs[mid].q0) <= slot) lo = mid; else hi = mid - 1;
         }
         b = lo;
-        k = slot - slot_base(a, b);
+        k = slot - slot_base(a, b, seqs[b].q0);
     } else {
         b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
         k = slot - b * pl.per_seq;
     }
-    const DenseSeq s = dense_seq(a, b);
+    return seqs[b];
+}
+
+// What a slot counts among all (balanced), found by one thread: its tiles, one if it has rows without keys, none without rows.
+__device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, int slot, const DenseSeq *seqs)
+{
+    int k;
+    const DenseSeq s = known_sequence(a, pl, slot, seqs, k);
     const int64_t row = (int64_t)k * kRows;
     if (k < 0 || row >= (int64_t)s.q_cap * a.heads) return 0;
     const int64_t used = min((int64_t)s.q_len * a.heads - row, (int64_t)kRows);
@@ -225,17 +252,10 @@ __device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, i
 }
 
 // A slot, worked out by the whole warp: everything but which of its tiles a unit takes.  -1: no rows; otherwise its tiles.
-__device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int slot, int lane, Unit &w)
+__device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int slot, int lane, Unit &w, const DenseSeq *seqs = nullptr)
 {
-    int b, k;
-    if (a.cu_q) {
-        b = find_sequence(a, slot, lane);
-        k = slot - slot_base(a, b);
-    } else {
-        b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
-        k = slot - b * pl.per_seq;
-    }
-    const DenseSeq s = dense_seq(a, b);
+    int k;
+    const DenseSeq s = seqs ? known_sequence(a, pl, slot, seqs, k) : slot_sequence(a, pl, slot, lane, k);
     const int64_t first_row = (int64_t)k * kRows, all = (int64_t)s.q_cap * a.heads;
     if (k < 0 || first_row >= all) return -1;
     w.row0 = (int64_t)s.q0 * a.heads + first_row;
@@ -250,7 +270,7 @@ __device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int
     w.prefix = w.used > 0 ? s.prefix : 0;
     w.prefix_tiles = (w.prefix + kKeys - 1) / kKeys;
     w.valid = 1;
-    w.b = b;
+    w.b = s.b;
     w.kv0 = s.kv0;
     w.q0 = s.q0;
     w.q_len = s.q_len;
@@ -263,12 +283,20 @@ __device__ __forceinline__ void check_blocks(const DenseArgs &a, Unit &w, int la
 {
     w.bad = 0;
     if (a.layout_kv != SFM_LAYOUT_PAGED) return;
+    // pages of the tiles in the prefix, then of those behind it
     bool bad = false;
-    for (int i = lane; i < w.tiles * (kKeys / 16); i += 32) {
-        const int t = w.tile0 + i / (kKeys / 16);
-        const int j = (t < w.prefix_tiles ? t * kKeys : w.b0 + (t - w.prefix_tiles) * kKeys) + i % (kKeys / 16) * 16;
-        box_row(a, w.b, 0, w.len, j, &bad);
-    }
+    auto check = [&](int tile, int end, int key) {
+        if (tile >= end) return;
+        const int last = (min(key + (end - tile) * kKeys, w.len) - 1) / a.block;
+#pragma unroll 4
+        for (int i = key / a.block + lane; i <= last; i += 32) {
+            const int32_t id = __ldg(a.table + (int64_t)w.b * a.cols + i);
+            bad |= id < 0 || ((int64_t)id + 1) * a.block > a.kv_rows;
+        }
+    };
+    const int end = w.tile0 + w.tiles, second = max(w.tile0, w.prefix_tiles);
+    check(w.tile0, min(end, w.prefix_tiles), w.tile0 * kKeys);
+    check(second, end, w.b0 + (second - w.prefix_tiles) * kKeys);
     w.bad = __any_sync(0xffffffffu, bad);
     if (w.bad && lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
 }
@@ -330,9 +358,9 @@ __device__ __forceinline__ Share make_share(const Plan &pl, const int32_t *weigh
 }
 
 // The share's next unit.  False: this slot has none.
-__device__ __forceinline__ bool next_of_share(const DenseArgs &a, const Plan &pl, Share &s, int c, int lane, Unit &w)
+__device__ __forceinline__ bool next_of_share(const DenseArgs &a, const Plan &pl, Share &s, int c, int lane, Unit &w, const DenseSeq *seqs)
 {
-    const int slot = s.slot, off = s.off, tiles = make_slot(a, pl, slot, lane, w);
+    const int slot = s.slot, off = s.off, tiles = make_slot(a, pl, slot, lane, w, seqs);
     ++s.slot;
     s.off = 0;
     if (tiles < 0) return false;
@@ -558,7 +586,7 @@ __device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide)
 
 template <bool kBf16, bool kCap, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUtensorMap q_map,
+sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Plan pl, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap kv_map)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -616,13 +644,17 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
     auto first_bar = [&](int i) { return first0 + 8u * static_cast<uint32_t>(i); };
     Unit *const units = reinterpret_cast<Unit *>(misc + UNIT_REL);
     grid_follow();
+    DenseSeq *const seqs = reinterpret_cast<DenseSeq *>(smem + KV_OFF);
     if (pl.balanced) {
-        // every slot's weight, for the units' warp (the softmax writes P here once it has a unit)
+        // the batch's sequences, then every slot's weight, for the units' warp (copies come and P goes here once it has a unit)
         int32_t *const weights = reinterpret_cast<int32_t *>(smem + P_OFF);
+        for (int i = tid; i < a.batch; i += kThreads) seqs[i] = dense_seq(a, i);
+        __syncthreads();
         for (int i = tid; i < pl.slots; i += kThreads) {
-            weights[i] = slot_weight(a, pl, i);
+            weights[i] = slot_weight(a, pl, i, seqs);
             if (weights[i] == 0 && cluster == 0) pl.head[i] = make_int4(0, 0, 0, 0);
         }
+        fence_proxy_async_smem();
         __syncthreads();
     }
 
@@ -635,7 +667,7 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
             Unit w;
             const bool end = pl.balanced ? share.at >= share.end || share.slot >= pl.slots : u >= pl.units;
             if (end) w.valid = 0;
-            else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w) : !make_unit(a, pl, u, lane, w)) continue;
+            else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w, n == 0 ? seqs : nullptr) : !make_unit(a, pl, u, lane, w)) continue;
             else check_blocks(a, w, lane);
             const int slot = n % kUnits;
             if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
@@ -850,47 +882,49 @@ sfm_dense_kernel(const DenseArgs a, const Plan pl, const __grid_constant__ CUten
                 ++gv;
                 o.output_done();
             }
-            // nothing of this warp's is under way when tensor memory is freed
-            if (elect_one()) pair_commit(bar(B_END));
-            __syncwarp();
-            const uint64_t t0 = globaltimer_ns();
-            while (!pair_try_wait(bar(B_END), 0) && globaltimer_ns() - t0 < kTimeoutNs) {
-            }
-            __syncwarp();
+            // no more rows to be made finite
             if (lane < 2) {
                 store_remote(in_cta(bar0 + FIX_REL, lane) + 20, 1u);
                 arrive_remote_release(in_cta(bar(B_FIX), lane));
+            }
+            __syncwarp();
+            if (!ok) {
+                // (the softmax has waited for all products otherwise) nothing is under way when tensor memory is freed
+                if (elect_one()) pair_commit(bar(B_END));
+                __syncwarp();
+                const uint64_t t0 = globaltimer_ns();
+                while (!pair_try_wait(bar(B_END), 0) && globaltimer_ns() - t0 < kTimeoutNs) {
+                }
             }
         }
         __syncwarp();
     } else if (warp == 2) {
         // ======================= V rows made finite =======================
-        for (int n = 0;; ++n) {
-            // as long as tiles go by there may be nothing to do
-            bool ok = true;
-            if (lane == 0) {
-                uint64_t t0 = globaltimer_ns();
-                int seen = *beat;
-                while (!pair_try_wait(bar(B_FIX), n & 1)) {
-                    if (*abort_flag) { ok = false; break; }
+        uint64_t t0 = globaltimer_ns();
+        int seen = 0;
+        for (int n = 0;;) {
+            if (!__all_sync(0xffffffffu, pair_try_wait(bar(B_FIX), n & 1))) {
+                // as long as tiles go by there may be nothing to do
+                bool ok = true;
+                if (lane == 0) {
                     if (*beat != seen) {
                         seen = *beat;
                         t0 = globaltimer_ns();
                     } else if (globaltimer_ns() - t0 > 2 * kTimeoutNs) {
                         *abort_flag = 1;
-                        ok = false;
-                        break;
                     }
+                    ok = !*abort_flag;
                 }
+                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+                continue;
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-            if (ok) ok = pair_try_wait(bar(B_FIX), n & 1);        // every lane has seen the phase
-            if (!__all_sync(0xffffffffu, ok) || fix_words[5]) break;
+            ++n;
+            if (fix_words[5]) break;
             const uint16_t inf = kBf16 ? 0x7f80 : 0x7c00;
-            for (int w = 0; w < 4; ++w) {
-                uint32_t m = fix_words[w];
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t m = fix_words[q4];
                 while (m) {
-                    const int key = 32 * w + __ffs(m) - 1;
+                    const int key = 32 * q4 + __ffs(m) - 1;
                     m &= m - 1;
                     // the key's 256 values in this CTA: four blocks, 128 bytes each, in the stages of its half of the keys
                     for (int q = 0; q < 4; ++q) {
@@ -1233,32 +1267,40 @@ __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, 
     if (head.x <= 1 || r >= head.y) return;
     // rows of the pieces' partial results
     auto row_of = [&](int s) { return (int64_t)(!pl.balanced ? head.w + s : s == 0 ? 2 * head.w + 1 : 2 * (head.w + s)) * kRows + r; };
+    // the pieces' maxima and sums, 32 at a time
     float m = -INFINITY, l = 0.f;
-    bool empty = true;
-    for (int s = 0; s < head.x; ++s) {
-        const float2 ml = pl.part_ml[row_of(s)];
-        m = fmaxf(m, ml.x);
-        empty &= ml.x == -INFINITY && ml.y == 0.f;
+    bool some = false;
+    for (int s0 = 0; s0 < head.x; s0 += 32) {
+        const float2 ml = s0 + lane < head.x ? pl.part_ml[row_of(s0 + lane)] : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        m = fmaxf(m, top);
+        some |= __any_sync(0xffffffffu, ml.x != -INFINITY || ml.y != 0.f);
     }
+    const bool empty = !some;
     float4 o[4] = {};
+#pragma unroll 2
     for (int s = 0; s < head.x; ++s) {
         const float2 ml = pl.part_ml[row_of(s)];
+        const float4 *from = pl.part_o + row_of(s) * (kD / 4) + lane;
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = from[32 * k];
         if (ml.x == -INFINITY && ml.y == 0.f) continue;
         const float e = fast_exp2(ml.x - m);
         l = fmaf(e, ml.y, l);
-        const float4 *from = pl.part_o + row_of(s) * (kD / 4) + lane;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 v = from[32 * k];
-            o[k].x = fmaf(e, v.x, o[k].x);
-            o[k].y = fmaf(e, v.y, o[k].y);
-            o[k].z = fmaf(e, v.z, o[k].z);
-            o[k].w = fmaf(e, v.w, o[k].w);
+            o[k].x = fmaf(e, v[k].x, o[k].x);
+            o[k].y = fmaf(e, v[k].y, o[k].y);
+            o[k].z = fmaf(e, v[k].z, o[k].z);
+            o[k].w = fmaf(e, v[k].w, o[k].w);
         }
     }
     const int64_t row = (int64_t)head.z + r;
     float inv = 0.f;
-    if (!empty) inv = 1.f / (a.sinks ? l + fast_exp2(__ldg(a.sinks + row % a.heads) * kLog2e - m) : l);
+    if (!empty) inv = __fdividef(1.f, a.sinks ? l + fast_exp2(__ldg(a.sinks + row % a.heads) * kLog2e - m) : l);
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -1292,33 +1334,55 @@ int dense_check(const sfm_dense_params *pp)
 }
 
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+using ReplaceFn = decltype(&cuTensorMapReplaceAddress);
 
-// the driver's encoder of TMA descriptors (a pure host function), looked up once
-EncodeFn encoder()
+// the driver's makers of TMA descriptors (pure host functions), looked up once
+template <typename Fn>
+Fn driver_function(const char *name)
 {
-    static const EncodeFn fn = [] {
+    static const Fn fn = [name] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
+        if (cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &r) != cudaSuccess || r != cudaDriverEntryPointSuccess)
             p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
+        return reinterpret_cast<Fn>(p);
     }();
     return fn;
 }
 
 // Rows of 512 values as eight blocks of 64: boxes of `blocks` blocks x `box_rows` rows land block after block, as the
-// products read them.
-int make_map(CUtensorMap *map, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows, int blocks)
+// products read them.  The last map of a thread's (for queries, for keys) is kept with its sizes and gets another address
+// where they are the same: encoding costs as much as the rest of a launch.
+struct KeptMap {
+    CUtensorMap map;
+    int64_t rows = 0, row_bytes = 0;
+    int dtype = 0, box_rows = 0, blocks = 0;
+};
+
+int make_map(CUtensorMap *map, KeptMap &kept, const void *ptr, int dtype, int64_t rows, int64_t row_bytes, int box_rows, int blocks)
 {
-    const EncodeFn encode = encoder();
-    if (!encode) return SFM_ERR_CUDA;
-    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 8}, strides[2] = {(cuuint64_t)row_bytes, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks}, steps[3] = {1, 1, 1};
-    const CUresult r = encode(map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                              const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SFM_OK : SFM_ERR_CUDA;
+    if (kept.rows != rows || kept.row_bytes != row_bytes || kept.dtype != dtype || kept.box_rows != box_rows || kept.blocks != blocks) {
+        const EncodeFn encode = driver_function<EncodeFn>("cuTensorMapEncodeTiled");
+        if (!encode) return SFM_ERR_CUDA;
+        const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 8}, strides[2] = {(cuuint64_t)row_bytes, 128};
+        const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks}, steps[3] = {1, 1, 1};
+        kept.rows = 0;
+        if (encode(&kept.map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return SFM_ERR_CUDA;
+        kept.rows = rows;
+        kept.row_bytes = row_bytes;
+        kept.dtype = dtype;
+        kept.box_rows = box_rows;
+        kept.blocks = blocks;
+        *map = kept.map;
+        return SFM_OK;
+    }
+    const ReplaceFn replace = driver_function<ReplaceFn>("cuTensorMapReplaceAddress");
+    if (!replace) return SFM_ERR_CUDA;
+    *map = kept.map;
+    return replace(map, const_cast<void *>(ptr)) == CUDA_SUCCESS ? SFM_OK : SFM_ERR_CUDA;
 }
 
 int64_t dense_tokens(const sfm_dense_params &p)
@@ -1337,7 +1401,7 @@ int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
     pl->balanced = 0;
     if (p.split_keys) {
         chunk = p.split_keys / kKeys;
-    } else if (slots <= kMostBalanced && p.max_seqlen_kv > 8 * kKeys && slots * tiles < 1ll << 30) {
+    } else if (slots <= kMostBalanced && p.batch_size <= kMostBalanced && p.max_seqlen_kv > 8 * kKeys && slots * tiles < 1ll << 30) {
         pl->balanced = 1;
     }
     const int64_t splits = pl->balanced ? 2 : (tiles + chunk - 1) / chunk;
@@ -1506,8 +1570,9 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
         pl.head = reinterpret_cast<int4 *>(pl.part_ml + dense_parts(pl) * kRows);
     }
     CUtensorMap q_map, kv_map;
-    rc = make_map(&q_map, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
-    if (!rc) rc = make_map(&kv_map, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, pl.box_rows == 64 ? kBlocks : 1);
+    static thread_local KeptMap kept_q, kept_kv;
+    rc = make_map(&q_map, kept_q, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
+    if (!rc) rc = make_map(&kv_map, kept_kv, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, pl.box_rows == 64 ? kBlocks : 1);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
     const int form = (bf16 ? 4 : 0) | (a.cap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0);

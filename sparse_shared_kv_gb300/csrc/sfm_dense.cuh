@@ -40,28 +40,33 @@ __device__ __forceinline__ int32_t dense_cut(const DenseArgs &a, int64_t v, int6
 
 __device__ __forceinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
 {
+    // all loads go out before the first of them is looked at
+    const int32_t q0 = a.cu_q ? __ldg(a.cu_q + b) : b * a.q_s, q1 = a.cu_q ? __ldg(a.cu_q + b + 1) : 0;
+    const int32_t used_q = a.used_q ? __ldg(a.used_q + b) : 0, used_kv = a.used_kv ? __ldg(a.used_kv + b) : 0;
+    const int32_t k0 = a.cu_kv ? __ldg(a.cu_kv + b) : 0, k1 = a.cu_kv ? __ldg(a.cu_kv + b + 1) : 0;
+    const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
     DenseSeq s;
     s.b = b;
     if (a.cu_q) {
-        s.q0 = dense_cut(a, __ldg(a.cu_q + b), 0, a.total_q);
-        s.q_cap = dense_cut(a, __ldg(a.cu_q + b + 1), s.q0, a.total_q) - s.q0;
+        s.q0 = dense_cut(a, q0, 0, a.total_q);
+        s.q_cap = dense_cut(a, q1, s.q0, a.total_q) - s.q0;
     } else {
-        s.q0 = b * a.q_s;
+        s.q0 = q0;
         s.q_cap = a.q_s;
     }
-    s.q_len = a.used_q ? dense_cut(a, __ldg(a.used_q + b), 0, s.q_cap) : s.q_cap;
+    s.q_len = a.used_q ? dense_cut(a, used_q, 0, s.q_cap) : s.q_cap;
     int64_t most;
     s.kv0 = 0;
     if (a.layout_kv == SFM_LAYOUT_PAGED) {
         most = (int64_t)a.cols * a.block;
         if (most > a.max_kv) most = a.max_kv;
     } else if (a.cu_kv) {
-        s.kv0 = __ldg(a.cu_kv + b);
-        if (s.kv0 < 0 || s.kv0 > a.kv_rows) {
+        s.kv0 = k0;
+        if (k0 < 0 || k0 > a.kv_rows) {
             dense_status(a, SFM_STATUS_BAD_LENGTH);
             s.kv0 = a.kv_rows;
         }
-        int64_t end = __ldg(a.cu_kv + b + 1);
+        int64_t end = k1;
         if (end > a.kv_rows) {
             dense_status(a, SFM_STATUS_BAD_LENGTH);
             end = a.kv_rows;
@@ -71,8 +76,8 @@ __device__ __forceinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
         s.kv0 = (int64_t)b * a.max_kv;
         most = a.max_kv;
     }
-    s.len = a.used_kv ? dense_cut(a, __ldg(a.used_kv + b), 0, most) : (int32_t)most;
-    s.prefix = a.prefix ? min(max(__ldg(a.prefix + b), 0), s.len) : 0;
+    s.len = a.used_kv ? dense_cut(a, used_kv, 0, most) : (int32_t)most;
+    s.prefix = min(max(prefix, 0), s.len);
     return s;
 }
 

@@ -298,6 +298,39 @@ def test_long_ranges_are_cut_and_joined():
         check(p, out, lse)
 
 
+@pytest.mark.parametrize("batch,heads,most_q,most_kv", [(33, 16, 3, 600), (40, 128, 1, 1500), (100, 128, 40, 300), (700, 8, 2, 90),
+                                                        (1600, 3, 2, 40), (2000, 128, 1, 33), (70, 64, 60, 2000)])
+@pytest.mark.parametrize("layout_q", ["TND", "BSND"])
+def test_many_sequences(batch, heads, most_q, most_kv, layout_q):
+    """More sequences than a warp reads at once, more tiles of queries than are shared evenly, and both."""
+    r = random.Random(batch)
+    q_lens = [r.randint(0 if layout_q == "TND" else 1, most_q) for _ in range(batch)]
+    lens = [r.randint(0, most_kv) for _ in range(batch)]
+    go(seed=batch, heads=heads, q_lens=q_lens, lens=lens, layout_q=layout_q, layout_kv="PAGED", sinks=batch < 50)
+
+
+def test_one_long_sequence_among_short_ones():
+    """Shares that begin and end inside of one tile's keys, and shares of many whole tiles."""
+    lens = [60000] + [140] * 50 + [20000]
+    for heads in (4, 64):
+        go(seed=36, heads=heads, q_lens=[1] * 52, lens=lens, layout_kv="PAGED", block=128, bias=True)
+    go(seed=37, heads=128, q_lens=[9, 0, 3, 1], lens=[40000, 0, 3, 0], tree=True)
+
+
+def test_outputs_at_any_sixteen_bytes():
+    p = problem(seed=38, heads=3, q_lens=(50, 7), lens=(300, 1500), rest=9)
+    want = run(p)
+    room = torch.zeros(want[0].numel() + 64, dtype=p["dtype"], device="cuda")
+    for shift in (8, 16, 24):
+        mine = room[shift:shift + want[0].numel()].view(want[0].shape)
+        out, lse = sfm.masked_attention(p["q"], p["kv"], out=mine, **p["args"])
+        assert torch.equal(mine[:57], want[0][:57])
+    room = torch.zeros(p["q"].numel() + 64, dtype=p["dtype"], device="cuda")
+    q = room[8:8 + p["q"].numel()].view(p["q"].shape)
+    q.copy_(p["q"])
+    assert torch.equal(sfm.masked_attention(q, p["kv"], **p["args"])[0], want[0])
+
+
 def test_prefix_far_before_the_window_in_pieces():
     for split in (0, 128, 256):
         p = problem(seed=11, heads=8, q_lens=(20, 40), lens=(5000, 3000), mode=4, left=300, right=0, prefix=(1000, 2950))
