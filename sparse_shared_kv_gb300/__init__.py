@@ -832,7 +832,8 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
            prefix_lens, key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv,
            layout_q, layout_kv, split_keys, out, lse, workspace, status, stream):
     code, dev = _first("q", q, _SIXTEEN_BIT)
-    _no_gradient("q", q)
+    if q.requires_grad:
+        _no_gradient("q", q)
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left,
@@ -854,7 +855,8 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         batch, max_seqlen_q, tokens = _tensor("cu_seqlens_q", cu_seqlens_q).numel() - 1, 0, shape[0]
     if not (isinstance(kv, torch.Tensor) and kv.dtype is q.dtype and kv.get_device() == dev):
         raise ValueError(f"kv: needs {q.dtype} on cuda:{dev}")
-    _no_gradient("kv", kv)
+    if kv.requires_grad:
+        _no_gradient("kv", kv)
     kshape = kv.shape
     if len(kshape) == (3 if lkv == TND else 4) and kshape[-2] == 1:
         kv = kv.squeeze(-2)          # the one KV head
@@ -865,10 +867,10 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         if kshape[0] != batch:
             raise ValueError("kv: needs (b, S, dim)")
         max_seqlen_kv = kshape[1]
-    rows, row_stride = _rows(kv, "kv")
+    rows, row_stride = (kv.numel() // dim, 2 * dim) if dim and kv.is_contiguous() else _rows(kv, "kv")
     max_seqlen_kv = max_seqlen_kv or rows        # no sequence has more
     cols = table = words = tree = place = 0
-    each, per_token = (batch,), (tokens,) if lq == TND else rows_shape[:-1]
+    each, per_token = (batch,), shape[:-2]
     if block_table is not None:
         if _tensor("block_table", block_table).dim() != 2:
             raise ValueError("block_table: needs (b, blocks)")
@@ -880,10 +882,11 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         place = _address("positions", positions, _I32, dev, per_token)
         if not words:
             raise ValueError("tree_mask: needs a word per token")
+    kind = q.dtype
     params = _DENSE_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
                                 code, kshape[1] if lkv == PAGED else 0, words, split_keys, out is None, softmax_scale, softcap)
     tensors = _DENSE_TENSORS.pack(
-        _address("q", q, q.dtype, dev, shape), kv.data_ptr(), row_stride, rows, table, cols,
+        _address("q", q, kind, dev, shape), kv.data_ptr(), row_stride, rows, table, cols,
         0 if cu_seqlens_q is None else _address("cu_seqlens_q", cu_seqlens_q, _I32, dev, (batch + 1,)),
         0 if cu_seqlens_kv is None else _address("cu_seqlens_kv", cu_seqlens_kv, _I32, dev, (batch + 1,)),
         0 if seqused_q is None else _address("seqused_q", seqused_q, _I32, dev, each),
@@ -896,7 +899,7 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
     given = ()
     if out is not None:
         given = (out,)
-        to = _address("out", out, q.dtype, dev, shape)
+        to = _address("out", out, kind, dev, shape)
         _no_gradient("out", out)
     if lse is not None:
         given += (lse,)
@@ -920,7 +923,7 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
     elif need:
         workspace, room = torch.empty(need, dtype=torch.uint8, device=q.device), need
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
         to = out.data_ptr()
     if lse is None:
         lse = torch.empty(rows_shape, dtype=_F32, device=q.device)
@@ -1023,7 +1026,7 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
             _no_gradient("lses", l)
     given = ()
     if out is None:
-        out = torch.empty(shape, dtype=kind, device=x.device)
+        out = torch.empty_like(x)
         to = out.data_ptr()
     else:
         given = (out,)

@@ -76,23 +76,24 @@ enum Bar {
     B_P_FULL = 14,       // [2] first: P written, O rescaled, S read, by the 16 softmax warps of both CTAs
     B_O_DONE = 16,       // [2] O += P V of a tile
     B_O_FREE = 18,       // first: the 16 softmax warps have read the unit's O
-    B_UNIT_FULL = 19,    // [4]
-    B_UNIT_EMPTY = 23,   // [4]
+    B_UNIT_FULL = 19,    // [kUnits]
+    B_UNIT_EMPTY = 23,   // [kUnits]
     B_FIX = 27,          // rows to be made finite
     B_FIXED = 28,        // first: both CTAs have
     B_END = 29,
-    kBars = 30
+    B_CHECKED = 30,      // [kUnits] the unit's blocks have been looked at
+    kBars = 33
 };
-constexpr int kUnits = 4;                     // units that are worked out ahead
+constexpr int kUnits = 3;                     // units that are worked out ahead
 constexpr int kAhead = 3;                     // tiles whose S is issued before the first of them gets its O += P V
-constexpr uint32_t EXCH_REL = 256;            // [2][4][64] floats: the row's four maxima (or sums)
-constexpr uint32_t UNIT_REL = EXCH_REL + 2048;   // [4] Unit
-constexpr uint32_t CAND_REL = UNIT_REL + 4 * 128;    // first: [2][4] words of keys that may hold NaN or infinities
+constexpr uint32_t EXCH_REL = 272;            // [2][4][64] floats: the row's four maxima (or sums)
+constexpr uint32_t UNIT_REL = EXCH_REL + 2048 + 112;   // [kUnits] Unit
+constexpr uint32_t CAND_REL = UNIT_REL + kUnits * 128;    // first: [2][4] words of keys that may hold NaN or infinities
 constexpr uint32_t FIX_REL = CAND_REL + 32;      // words, first stage, quit
 constexpr uint32_t TMEM_REL = FIX_REL + 32;
 constexpr uint32_t ABORT_REL = TMEM_REL + 4;
 constexpr uint32_t BEAT_REL = ABORT_REL + 4;
-static_assert(kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= 3072, "misc area");
+static_assert(UNIT_REL % 128 == 0 && kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= 3072, "misc area");
 
 struct alignas(128) Unit {
     int64_t row0;            // first row of Q (and of the outputs)
@@ -620,6 +621,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         }
         for (int i = 0; i < kUnits; ++i) {
             init(B_UNIT_FULL + i, 1);
+            init(B_CHECKED + i, 1);
             init(B_UNIT_EMPTY + i, rank == 0 ? 10 : 9);
         }
         init(B_O_FREE, 16);
@@ -665,15 +667,21 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         if (pl.balanced) share = make_share(pl, reinterpret_cast<const int32_t *>(smem + P_OFF), cluster, lane);
         for (int u = cluster;; u += clusters) {
             Unit w;
+            w.bad = 0;
             const bool end = pl.balanced ? share.at >= share.end || share.slot >= pl.slots : u >= pl.units;
             if (end) w.valid = 0;
             else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w, n == 0 ? seqs : nullptr) : !make_unit(a, pl, u, lane, w)) continue;
-            else check_blocks(a, w, lane);
             const int slot = n % kUnits;
             if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
             if (lane == 0) {
                 units[slot] = w;
                 mbar_arrive(bar(B_UNIT_FULL + slot));
+            }
+            // the copies and products may begin, the softmax waits for this too
+            if (!end) check_blocks(a, w, lane);
+            if (lane == 0) {
+                units[slot].bad = w.bad;
+                mbar_arrive(bar(B_CHECKED + slot));
             }
             __syncwarp();
             ++n;
@@ -1033,7 +1041,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         };
         while (ok) {
             const int us = n % kUnits;
-            if (rows_meet_any(part & 1, !pair_wait_warp(bar(B_UNIT_FULL + us), n / kUnits & 1, abort_flag))) {
+            if (rows_meet_any(part & 1, !pair_wait_warp(bar(B_CHECKED + us), n / kUnits & 1, abort_flag))) {
                 ok = false;
                 break;
             }
@@ -1530,6 +1538,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     a.q_s = p.max_seqlen_q;
     a.total_q = tokens;
     a.max_kv = p.max_seqlen_kv;
+    if (paged && (int64_t)t->block_table_stride * p.block_size < a.max_kv) a.max_kv = (int32_t)((int64_t)t->block_table_stride * p.block_size);
     a.mode = p.mask_mode;
     const int32_t far = 1 << 30;
     a.win_left = p.win_left < 0 || p.win_left > far ? far : p.win_left;

@@ -31,53 +31,36 @@ struct DenseSeq {
     int64_t kv0;              // row of its first key (not paged)
 };
 
-__device__ __forceinline__ int32_t dense_cut(const DenseArgs &a, int64_t v, int64_t lo, int64_t hi)
-{
-    if (v >= lo && v <= hi) return (int32_t)v;
-    dense_status(a, SFM_STATUS_BAD_LENGTH);
-    return (int32_t)(v < lo ? lo : hi);
-}
-
+// All loads go out before the first of them is looked at; lengths outside of what the buffers hold are cut.
 __device__ __forceinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
 {
-    // all loads go out before the first of them is looked at
-    const int32_t q0 = a.cu_q ? __ldg(a.cu_q + b) : b * a.q_s, q1 = a.cu_q ? __ldg(a.cu_q + b + 1) : 0;
+    const int32_t q0 = a.cu_q ? __ldg(a.cu_q + b) : b * a.q_s, q1 = a.cu_q ? __ldg(a.cu_q + b + 1) : q0 + a.q_s;
+    const int32_t k0 = a.cu_kv ? __ldg(a.cu_kv + b) : 0, k1 = a.cu_kv ? __ldg(a.cu_kv + b + 1) : a.max_kv;
     const int32_t used_q = a.used_q ? __ldg(a.used_q + b) : 0, used_kv = a.used_kv ? __ldg(a.used_kv + b) : 0;
-    const int32_t k0 = a.cu_kv ? __ldg(a.cu_kv + b) : 0, k1 = a.cu_kv ? __ldg(a.cu_kv + b + 1) : 0;
     const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
+    int bad = 0;
+    auto cut = [&](int v, int lo, int hi) {
+        const int c = min(max(v, lo), hi);
+        bad |= c ^ v;
+        return c;
+    };
     DenseSeq s;
     s.b = b;
-    if (a.cu_q) {
-        s.q0 = dense_cut(a, q0, 0, a.total_q);
-        s.q_cap = dense_cut(a, q1, s.q0, a.total_q) - s.q0;
-    } else {
-        s.q0 = q0;
-        s.q_cap = a.q_s;
-    }
-    s.q_len = a.used_q ? dense_cut(a, used_q, 0, s.q_cap) : s.q_cap;
-    int64_t most;
-    s.kv0 = 0;
-    if (a.layout_kv == SFM_LAYOUT_PAGED) {
-        most = (int64_t)a.cols * a.block;
-        if (most > a.max_kv) most = a.max_kv;
-    } else if (a.cu_kv) {
-        s.kv0 = k0;
-        if (k0 < 0 || k0 > a.kv_rows) {
-            dense_status(a, SFM_STATUS_BAD_LENGTH);
-            s.kv0 = a.kv_rows;
-        }
-        int64_t end = k1;
-        if (end > a.kv_rows) {
-            dense_status(a, SFM_STATUS_BAD_LENGTH);
-            end = a.kv_rows;
-        }
-        most = dense_cut(a, end - s.kv0, 0, a.max_kv);
-    } else {
-        s.kv0 = (int64_t)b * a.max_kv;
+    s.q0 = cut(q0, 0, a.total_q);
+    s.q_cap = cut(q1, s.q0, a.total_q) - s.q0;
+    s.q_len = a.used_q ? cut(used_q, 0, s.q_cap) : s.q_cap;
+    // paged and (b, S) caches: k0 = 0 and k1 = max_kv, which the host has cut to what a sequence's blocks hold
+    const int rows = (int)min(a.kv_rows, (int64_t)INT32_MAX);
+    const int first = cut(k0, 0, a.cu_kv ? rows : 0);
+    int most = cut(k1, first, a.cu_kv ? rows : a.max_kv) - first;
+    if (most > a.max_kv) {
         most = a.max_kv;
+        bad = 1;
     }
-    s.len = a.used_kv ? dense_cut(a, used_kv, 0, most) : (int32_t)most;
+    s.kv0 = a.layout_kv == SFM_LAYOUT_BSND ? (int64_t)b * a.max_kv : first;
+    s.len = a.used_kv ? cut(used_kv, 0, most) : most;
     s.prefix = min(max(prefix, 0), s.len);
+    if (__builtin_expect(bad, 0)) dense_status(a, SFM_STATUS_BAD_LENGTH);
     return s;
 }
 
