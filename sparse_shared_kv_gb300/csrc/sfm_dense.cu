@@ -108,21 +108,22 @@ struct alignas(128) Unit {
 static_assert(sizeof(Unit) <= 128, "unit area");
 
 // A slot is a tile of Q of some sequence.  Either every slot's keys are cut into pieces of at most `chunk` tiles, at most
-// `splits` of them, and units (slot, piece) go to the pairs in turns, or (balanced) the pairs share all tiles of all slots
-// evenly: pair c works through tiles [c per, (c + 1) per) of their concatenation, so that it starts in the middle of one
-// slot and ends in the middle of another.
+// `splits` of them, and units (slot, piece) go to the pairs in turns, or (balanced) the pairs get the same number of tiles:
+// whole slots in turns first, as long as none gets more than its share, so that the pairs go through a sequence's keys side
+// by side and find them in L2; then parts of the concatenation of the other slots' tiles, which begin and end in the middle
+// of slots.  (With such parts alone every sequence is under way at once: 16 trees of 16 tokens over 200 MB of keys 509 us.)
 struct Plan {
     int32_t slots, splits, chunk, box_rows, align, units, balanced, pairs;
     uint32_t idesc_s, idesc_o;
-    float4 *part_o;          // partial results: [part][128][128]; balanced: part 2 c of pair c continues a slot, 2 c + 1 begins one
+    float4 *part_o;          // partial results: [part][128][128]; balanced: part 2 n of the n-th part of the tiles continues a slot, 2 n + 1 begins one
     float2 *part_ml;         // [part][128]
-    int4 *head;              // [slot]: pieces, rows that count, first row, first part (balanced: pair)
+    int4 *head;              // [slot]: pieces, rows that count, first row, first part (balanced: part of the tiles)
     FastDiv slots_div, per_seq_div;
     int32_t per_seq;         // BSND: tiles per sequence
 };
-constexpr int kMostBalanced = 1536;           // slots, and sequences; their tiles are counted by every CTA, four slots per thread at most
+constexpr int kMostBalanced = 1536;           // slots, and sequences: every CTA counts their tiles
 constexpr int kLeastTiles = 4;                // of a pair's share
-static_assert(kMostBalanced * 4 <= 32768 && kMostBalanced * sizeof(DenseSeq) <= kStages * kStageBytes, "counted in P's and the stages' memory");
+constexpr int kMostPairs = 512;
 
 // First slot of a sequence of a TND batch whose first row is q0: at least one more per sequence than whole tiles lie before
 // it, so that every sequence has as many slots as tiles.
@@ -238,15 +239,18 @@ __device__ __forceinline__ DenseSeq known_sequence(const DenseArgs &a, const Pla
     return seqs[b];
 }
 
-// What a slot counts among all (balanced), found by one thread: its tiles, one if it has rows without keys, none without rows.
-__device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, int slot, const DenseSeq *seqs)
+// What a slot counts among all (balanced), found by one thread: its tiles, one if it has rows without keys, none without
+// rows; its first row and how many count.
+__device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, int slot, const DenseSeq *seqs, int &row0, int &used)
 {
     int k;
     const DenseSeq s = known_sequence(a, pl, slot, seqs, k);
     const int64_t row = (int64_t)k * kRows;
+    row0 = used = 0;
     if (k < 0 || row >= (int64_t)s.q_cap * a.heads) return 0;
-    const int64_t used = min((int64_t)s.q_len * a.heads - row, (int64_t)kRows);
-    if (used <= 0) return 1;
+    row0 = (int)((int64_t)s.q0 * a.heads + row);
+    used = (int)min(max((int64_t)s.q_len * a.heads - row, (int64_t)0), (int64_t)kRows);
+    if (used == 0) return 1;
     int lo, hi, b0;
     span(a, s, (int)fdiv((uint32_t)row, a.heads_div), (int)fdiv((uint32_t)(row + used - 1), a.heads_div), 0, 1, lo, hi);
     return max(tiles_of(pl, s.prefix, lo, hi, b0), 1);
@@ -323,58 +327,123 @@ __device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, in
     return true;
 }
 
-// The balanced plan's walk through a pair's share of the tiles.
-struct Share {
-    int slot = 0, off = 0, at = 0, end = 0, per = 1;      // next slot and tile of it; that tile among all, the share's end; tiles per pair
+// What every CTA works out for the balanced plan, in P's memory.
+struct Balance {
+    int32_t before[kMostBalanced + 1];    // a slot's weight, then the weights of all slots before it
+    int32_t row0[kMostBalanced], used[kMostBalanced];     // its first row, and how many count
+    int32_t begin[kMostPairs + 1];        // of the tiles behind the whole slots: where each pair's part begins
+    int32_t rank[kMostPairs + 1];         // pairs before it whose part is not empty
+    int32_t waves;                        // whole slots per pair
 };
 
-// Where pair c's share begins, from the slots' weights, by the whole warp.
-__device__ __forceinline__ Share make_share(const Plan &pl, const int32_t *weights, int c, int lane)
+static_assert(sizeof(Balance) <= 32768 && kMostBalanced * sizeof(DenseSeq) <= kStages * kStageBytes, "counted in P's and the stages' memory");
+
+// before, begin, rank and waves from the slots' weights, by one warp.
+__device__ __forceinline__ void make_balance(const Plan &pl, Balance &b, int lane)
 {
-    const int each = (pl.slots + 31) / 32, at = lane * each, end = min(at + each, pl.slots);
+    const int n = pl.slots, G = pl.pairs, each = (n + 31) / 32, at = min(lane * each, n), end = min(at + each, n);
     int mine = 0;
-    for (int i = at; i < end; ++i) mine += weights[i];
-    int before = mine;
+    for (int i = at; i < end; ++i) mine += b.before[i];
+    int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += v;
+        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
     }
-    const int total = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
+    const int total = __shfl_sync(0xffffffffu, sum, 31);
+    sum -= mine;
+    for (int i = at; i < end; ++i) {
+        const int w = b.before[i];
+        b.before[i] = sum;
+        sum += w;
+    }
+    if (lane == 31) b.before[n] = total;
+    __syncwarp();
+    const int per = max((total + G - 1) / G, kLeastTiles);
+    auto load = [&](int c, int waves) {
+        int l = 0;
+        for (int w = 0; w < waves; ++w) l += b.before[c + w * G + 1] - b.before[c + w * G];
+        return l;
+    };
+    int waves = n / G;
+    while (waves > 0) {
+        bool over = false;
+        for (int c = lane; c < G; c += 32) over |= load(c, waves) > per;
+        if (!__any_sync(0xffffffffu, over)) break;
+        --waves;
+    }
+    const int rest = total - b.before[min(waves * G, n)];
+    int begin = 0, rank = 0;
+    for (int c0 = 0; c0 < G; c0 += 32) {
+        const int c = c0 + lane;
+        int part = c < G ? per - load(c, waves) : 0, incl = part;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        const int first = min(begin + incl - part, rest), last = min(begin + incl, rest);
+        const uint32_t some = __ballot_sync(0xffffffffu, last > first);
+        if (c < G) {
+            b.begin[c] = first;
+            b.rank[c] = rank + __popc(some & ((1u << lane) - 1u));
+        }
+        begin += __shfl_sync(0xffffffffu, incl, 31);
+        rank += __popc(some);
+    }
+    if (lane == 0) {
+        b.begin[G] = rest;
+        b.rank[G] = rank;
+        b.waves = waves;
+    }
+    __syncwarp();
+}
+
+// The last entry of n sorted ones that is at most x.
+__device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A pair's way through its whole slots and its part of the tiles behind them.
+struct Share {
+    int wave, waves, slot, off, at, end, rank;      // next slot and tile of it; that tile among all of the part's kind, the part's end
+};
+
+__device__ __forceinline__ Share make_share(const Plan &pl, const Balance &b, int c)
+{
     Share s;
-    s.per = max((total + pl.pairs - 1) / pl.pairs, kLeastTiles);
-    const int64_t first = (int64_t)c * s.per;
-    if (first >= total) return s;
-    s.at = (int)first;
-    s.end = min(s.at + s.per, total);
-    // the lane whose slots hold the first tile looks for it among them
-    const int who = 31 - __clz(__ballot_sync(0xffffffffu, before <= first && (mine > 0 || lane == 0)));
-    int slot = at, off = (int)first - before;
-    if (lane == who)
-        while (slot < end - 1 && off >= weights[slot]) off -= weights[slot++];
-    s.slot = __shfl_sync(0xffffffffu, slot, who);
-    s.off = __shfl_sync(0xffffffffu, off, who);
+    const int first = min(b.waves * pl.pairs, pl.slots), base = b.before[first];
+    s.wave = 0;
+    s.waves = b.waves;
+    s.at = b.begin[c];
+    s.end = b.begin[c + 1];
+    s.rank = b.rank[c];
+    s.slot = last_at_most(b.before, pl.slots, base + s.at);      // (of slots without rows, which begin where the next does, the last)
+    s.off = base + s.at - b.before[s.slot];
     return s;
 }
 
 // The share's next unit.  False: this slot has none.
 __device__ __forceinline__ bool next_of_share(const DenseArgs &a, const Plan &pl, Share &s, int c, int lane, Unit &w, const DenseSeq *seqs)
 {
-    const int slot = s.slot, off = s.off, tiles = make_slot(a, pl, slot, lane, w, seqs);
-    ++s.slot;
-    s.off = 0;
+    const bool wave = s.wave < s.waves;
+    const int slot = wave ? c + s.wave++ * pl.pairs : s.slot++, off = wave ? 0 : s.off;
+    if (!wave) s.off = 0;
+    const int tiles = make_slot(a, pl, slot, lane, w, seqs);
     if (tiles < 0) return false;
-    const int weight = max(tiles, 1), take = min(weight - off, s.end - s.at), start = s.at - off;
-    s.at += take;
+    const int weight = max(tiles, 1), take = wave ? weight : min(weight - off, s.end - s.at);
+    if (!wave) s.at += take;
     w.tile0 = off;
     w.tiles = tiles ? take : 0;
     w.piece = off > 0;
-    // pieces: the pairs from the one of the slot's first tile to the one of its last
-    const int c0 = start / s.per, c1 = (start + weight - 1) / s.per;
-    w.splits = c1 - c0 + 1;
-    w.part = 2 * c + (off == 0);
-    if (off == 0 && lane == 0) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, c0);
+    w.splits = take == weight ? 1 : 2;
+    w.part = 2 * s.rank + (off == 0);
     return true;
 }
 
@@ -647,28 +716,39 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
     Unit *const units = reinterpret_cast<Unit *>(misc + UNIT_REL);
     grid_follow();
     DenseSeq *const seqs = reinterpret_cast<DenseSeq *>(smem + KV_OFF);
+    Balance &balance = *reinterpret_cast<Balance *>(smem + P_OFF);
     if (pl.balanced) {
-        // the batch's sequences, then every slot's weight, for the units' warp (copies come and P goes here once it has a unit)
-        int32_t *const weights = reinterpret_cast<int32_t *>(smem + P_OFF);
+        // the batch's sequences, then every slot's weight, then the pairs' parts (copies come and P goes here once there is a unit)
         for (int i = tid; i < a.batch; i += kThreads) seqs[i] = dense_seq(a, i);
         __syncthreads();
-        for (int i = tid; i < pl.slots; i += kThreads) {
-            weights[i] = slot_weight(a, pl, i, seqs);
-            if (weights[i] == 0 && cluster == 0) pl.head[i] = make_int4(0, 0, 0, 0);
-        }
+        for (int i = tid; i < pl.slots; i += kThreads) balance.before[i] = slot_weight(a, pl, i, seqs, balance.row0[i], balance.used[i]);
+        __syncthreads();
+        if (warp == 3) make_balance(pl, balance, lane);
         fence_proxy_async_smem();
+        __syncthreads();
+        // what the joining of pieces has to know of every slot, from some thread of some pair
+        const int first = min(balance.waves * pl.pairs, pl.slots), base = balance.before[first];
+        for (int i = cluster + tid * clusters; i < pl.slots && rank == 0; i += kThreads * clusters) {
+            int pieces = 1, of = 0;
+            const int begin = balance.before[i] - base, end = balance.before[i + 1] - base;
+            if (i >= first && end > begin) {
+                of = balance.rank[last_at_most(balance.begin, pl.pairs, begin)];
+                pieces = balance.rank[last_at_most(balance.begin, pl.pairs, end - 1)] - of + 1;
+            }
+            pl.head[i] = make_int4(pieces, balance.used[i], balance.row0[i], of);
+        }
         __syncthreads();
     }
 
     if (warp == 3) {
         // ======================= units =======================
         int n = 0;
-        Share share;
-        if (pl.balanced) share = make_share(pl, reinterpret_cast<const int32_t *>(smem + P_OFF), cluster, lane);
+        Share share = {};
+        if (pl.balanced) share = make_share(pl, balance, cluster);
         for (int u = cluster;; u += clusters) {
             Unit w;
             w.bad = 0;
-            const bool end = pl.balanced ? share.at >= share.end || share.slot >= pl.slots : u >= pl.units;
+            const bool end = pl.balanced ? share.wave >= share.waves && (share.at >= share.end || share.slot >= pl.slots) : u >= pl.units;
             if (end) w.valid = 0;
             else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w, n == 0 ? seqs : nullptr) : !make_unit(a, pl, u, lane, w)) continue;
             const int slot = n % kUnits;
@@ -1409,7 +1489,7 @@ int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
     pl->balanced = 0;
     if (p.split_keys) {
         chunk = p.split_keys / kKeys;
-    } else if (slots <= kMostBalanced && p.batch_size <= kMostBalanced && p.max_seqlen_kv > 8 * kKeys && slots * tiles < 1ll << 30) {
+    } else if (slots <= kMostBalanced && p.batch_size <= kMostBalanced && clusters <= kMostPairs && p.max_seqlen_kv > 8 * kKeys && slots * tiles < 1ll << 30) {
         pl->balanced = 1;
     }
     const int64_t splits = pl->balanced ? 2 : (tiles + chunk - 1) / chunk;
