@@ -131,38 +131,23 @@ __device__ __forceinline__ int slot_base(const DenseArgs &a, int b, int q0) { re
 
 __device__ __forceinline__ int first_query(const DenseArgs &a, int b) { return min(max(__ldg(a.cu_q + b), 0), a.total_q); }
 
-// The sequence of a slot, found by the whole warp, and the slot's number k in it (< 0: none).  Up to 32 sequences are all
-// read at once; of more the one is found 32 ways at a time.
+// The sequence of a slot, found by the whole warp 32 ways at a time, and the slot's number k in it (< 0: none).
 __device__ __forceinline__ DenseSeq slot_sequence(const DenseArgs &a, const Plan &pl, int slot, int lane, int &k)
 {
-    if (!a.cu_q) {
-        const int b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
-        k = slot - b * pl.per_seq;
-        return dense_seq(a, b);
+    int b = 0;
+    if (a.cu_q) {
+        for (int n = a.batch; n > 1;) {
+            const int step = (n + 31) / 32, i = b + lane * step;
+            const bool below = lane * step < n && (lane == 0 || slot_base(a, i, first_query(a, i)) <= slot);
+            const int w = 31 - __clz(__ballot_sync(0xffffffffu, below));
+            b += w * step;
+            n = min(step, n - w * step);
+        }
+    } else {
+        b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
     }
-    if (a.batch <= 32) {
-        DenseSeq s = dense_seq(a, min(lane, a.batch - 1));
-        const int who = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || (lane < a.batch && slot_base(a, lane, s.q0) <= slot)));
-        s.b = who;
-        s.q0 = __shfl_sync(0xffffffffu, s.q0, who);
-        s.q_cap = __shfl_sync(0xffffffffu, s.q_cap, who);
-        s.q_len = __shfl_sync(0xffffffffu, s.q_len, who);
-        s.len = __shfl_sync(0xffffffffu, s.len, who);
-        s.prefix = __shfl_sync(0xffffffffu, s.prefix, who);
-        s.kv0 = __shfl_sync(0xffffffffu, s.kv0, who);
-        k = slot - slot_base(a, who, s.q0);
-        return s;
-    }
-    int lo = 0, n = a.batch;
-    while (n > 1) {
-        const int step = (n + 31) / 32, b = lo + lane * step;
-        const bool below = lane * step < n && (lane == 0 || slot_base(a, b, first_query(a, b)) <= slot);
-        const int w = 31 - __clz(__ballot_sync(0xffffffffu, below));
-        lo += w * step;
-        n = min(step, n - w * step);
-    }
-    const DenseSeq s = dense_seq(a, lo);
-    k = slot - slot_base(a, lo, s.q0);
+    const DenseSeq s = dense_seq(a, b);
+    k = a.cu_q ? slot - slot_base(a, b, s.q0) : slot - b * pl.per_seq;
     return s;
 }
 
@@ -306,27 +291,6 @@ __device__ __forceinline__ void check_blocks(const DenseArgs &a, Unit &w, int la
     if (w.bad && lane == 0) dense_status(a, SFM_STATUS_BAD_BLOCK);
 }
 
-// Unit u of the plan that cuts every slot into pieces.  False: nothing to do.
-__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, int u, int lane, Unit &w)
-{
-    const int split = (int)fdiv((uint32_t)u, pl.slots_div), slot = pl.slots - 1 - (u - split * pl.slots);
-    const int tiles = make_slot(a, pl, slot, lane, w);
-    if (tiles < 0) {
-        if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(0, 0, 0, 0);
-        return false;
-    }
-    w.splits = tiles > pl.chunk ? min((tiles + pl.chunk - 1) / pl.chunk, pl.splits) : 1;
-    const int per = (tiles + w.splits - 1) / w.splits;
-    if (per > 0) w.splits = (tiles + per - 1) / per;
-    if (split >= w.splits) return false;
-    w.tile0 = min(split * per, tiles);
-    w.tiles = min(per, tiles - w.tile0);
-    w.piece = split;
-    w.part = slot * pl.splits + split;
-    if (split == 0 && lane == 0 && pl.head) pl.head[slot] = make_int4(w.splits, w.used, (int32_t)w.row0, slot * pl.splits);
-    return true;
-}
-
 // What every CTA works out for the balanced plan, in P's memory.
 struct Balance {
     int32_t before[kMostBalanced + 1];    // a slot's weight, then the weights of all slots before it
@@ -429,21 +393,42 @@ __device__ __forceinline__ Share make_share(const Plan &pl, const Balance &b, in
     return s;
 }
 
-// The share's next unit.  False: this slot has none.
-__device__ __forceinline__ bool next_of_share(const DenseArgs &a, const Plan &pl, Share &s, int c, int lane, Unit &w, const DenseSeq *seqs)
+// The next unit: of the pair's share, or (not balanced) piece and slot u.  False: there is nothing to do.
+__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, Share &s, int u, int c, int lane, Unit &w, const DenseSeq *seqs)
 {
     const bool wave = s.wave < s.waves;
-    const int slot = wave ? c + s.wave++ * pl.pairs : s.slot++, off = wave ? 0 : s.off;
-    if (!wave) s.off = 0;
+    int slot, off = 0, split = 0;
+    if (!pl.balanced) {
+        split = (int)fdiv((uint32_t)u, pl.slots_div);
+        slot = pl.slots - 1 - (u - split * pl.slots);
+    } else if (wave) {
+        slot = c + s.wave++ * pl.pairs;
+    } else {
+        slot = s.slot++;
+        off = s.off;
+        s.off = 0;
+    }
     const int tiles = make_slot(a, pl, slot, lane, w, seqs);
-    if (tiles < 0) return false;
-    const int weight = max(tiles, 1), take = wave ? weight : min(weight - off, s.end - s.at);
-    if (!wave) s.at += take;
-    w.tile0 = off;
-    w.tiles = tiles ? take : 0;
-    w.piece = off > 0;
-    w.splits = take == weight ? 1 : 2;
-    w.part = 2 * s.rank + (off == 0);
+    if (pl.balanced) {
+        if (tiles < 0) return false;
+        const int weight = max(tiles, 1), take = wave ? weight : min(weight - off, s.end - s.at);
+        if (!wave) s.at += take;
+        w.tile0 = off;
+        w.tiles = tiles ? take : 0;
+        w.piece = off > 0;
+        w.splits = take == weight ? 1 : 2;
+        w.part = 2 * s.rank + (off == 0);
+        return true;
+    }
+    w.splits = tiles > pl.chunk ? min((tiles + pl.chunk - 1) / pl.chunk, pl.splits) : 1;
+    const int per = (max(tiles, 0) + w.splits - 1) / w.splits;
+    if (per > 0) w.splits = (tiles + per - 1) / per;
+    if (split == 0 && lane == 0 && pl.head) pl.head[slot] = tiles < 0 ? make_int4(0, 0, 0, 0) : make_int4(w.splits, w.used, (int32_t)w.row0, slot * pl.splits);
+    if (tiles < 0 || split >= w.splits) return false;
+    w.tile0 = min(split * per, tiles);
+    w.tiles = min(per, tiles - w.tile0);
+    w.piece = split;
+    w.part = slot * pl.splits + split;
     return true;
 }
 
@@ -750,7 +735,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             w.bad = 0;
             const bool end = pl.balanced ? share.wave >= share.waves && (share.at >= share.end || share.slot >= pl.slots) : u >= pl.units;
             if (end) w.valid = 0;
-            else if (pl.balanced ? !next_of_share(a, pl, share, cluster, lane, w, n == 0 ? seqs : nullptr) : !make_unit(a, pl, u, lane, w)) continue;
+            else if (!make_unit(a, pl, share, u, cluster, lane, w, pl.balanced && n == 0 ? seqs : nullptr)) continue;
             const int slot = n % kUnits;
             if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
             if (lane == 0) {

@@ -31,8 +31,9 @@ struct DenseSeq {
     int64_t kv0;              // row of its first key (not paged)
 };
 
-// All loads go out before the first of them is looked at; lengths outside of what the buffers hold are cut.
-__device__ __forceinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
+// All loads go out before the first of them is looked at; lengths outside of what the buffers hold are cut.  (One copy in a
+// kernel: the code that plans runs a few times, and to fetch it is most of what it costs.)
+__device__ __noinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
 {
     const int32_t q0 = a.cu_q ? __ldg(a.cu_q + b) : b * a.q_s, q1 = a.cu_q ? __ldg(a.cu_q + b + 1) : q0 + a.q_s;
     const int32_t k0 = a.cu_kv ? __ldg(a.cu_kv + b) : 0, k1 = a.cu_kv ? __ldg(a.cu_kv + b + 1) : a.max_kv;
