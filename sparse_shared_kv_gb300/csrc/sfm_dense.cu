@@ -9,18 +9,27 @@
 //     O += P V       N = 2 x 256, K = 128     CTA c stages 256 of the 512 columns of all 128 keys
 //
 // The rows are K and V at once, but a CTA's part of K and its part of V share a
-// quarter of the tile only, so both are copied (TMA, 128 KB per tile and CTA; the second copy
+// quarter of the tile only, and a pair product wants both CTAs' operands at the
+// same offsets, so both are copied (TMA, 128 KB per tile and CTA; the second copy
 // hits L2).  O fills half of the tensor memory (64 x 512 fp32 in 128 lanes x 256
-// columns), two S tiles of 64 columns lie beside it.
+// columns), four S tiles of 64 columns the other.
 //
 // Per CTA, 12 warps:
-//   0      copies: Q of a unit, then K(0), K(1), V(0), K(2), V(1), ... in stages of 16 KB (two boxes of 64 values x 64 rows),
-//          eight of them in a ring
-//   1      products, in the pair's first CTA: S(0); S(i + 1), O += P(i) V(i); ...
+//   0      copies: Q of a unit, then K(0), K(1), K(2), V(0), K(3), V(1), ... in stages of 32 KB, one copy each (64 keys x 256
+//          values as four blocks of 64 values; pages of fewer rows take more), four stages in a ring
+//   1      products, in the pair's first CTA: S(0), S(1), S(2), O += P(0) V(0), S(3), O += P(1) V(1), ...
 //   2      tensor memory; takes NaN and infinities out of V rows that some row must not see (below)
-//   3      units: which rows and keys come next, two units ahead
+//   3      units: which rows and keys come next, three units ahead
 //   4-11   softmax: four threads per row, 32 keys each; running maximum, moved (and O rescaled) only when it grows by more
-//          than 8 in the log2 domain; P in dtype into shared memory; the result at the unit's end
+//          than 8 in the log2 domain; P in dtype into shared memory; the results
+//
+// What bounds it: a tile is 2048 clocks of the tensor cores (16384 FLOP per clock and pair).  Of long ranges of keys it takes
+// 2700 to 2800 (tensor cores 71 to 76 % busy, 1.60 to 1.68 PFLOP/s where the GPU is cool: 84 to 88 % of a 1914 TFLOP/s burst
+// of matrix products); called again and again it runs into the GPU's power limit, as such products do (1721), and the
+// clock falls to 1.6 to 1.75 GHz (1.46 to 1.49 PFLOP/s).  Every unit costs some 5000 clocks of the softmax's besides (its
+// results are written, the next unit's rows looked up), which units of few tiles do not hide: 4096 causal tokens of 64
+// heads 1.31, documents of some 1600 1.29 PFLOP/s.  Single tokens are bound by memory: 32 x 24 k keys 4.5 TB/s with 10 us to
+// plan and 9 us to join.
 //
 // A unit is a tile of Q and a piece of its range of keys.  Pieces of a range
 // leave fp32 partial results in the workspace, which a second kernel joins.
@@ -77,17 +86,17 @@ enum Bar {
     B_O_DONE = 16,       // [2] O += P V of a tile
     B_O_FREE = 18,       // first: the 16 softmax warps have read the unit's O
     B_UNIT_FULL = 19,    // [kUnits]
-    B_UNIT_EMPTY = 23,   // [kUnits]
-    B_FIX = 27,          // rows to be made finite
-    B_FIXED = 28,        // first: both CTAs have
-    B_END = 29,
-    B_CHECKED = 30,      // [kUnits] the unit's blocks have been looked at
-    kBars = 33
+    B_UNIT_EMPTY = 22,   // [kUnits]
+    B_FIX = 25,          // rows to be made finite
+    B_FIXED = 26,        // first: both CTAs have
+    B_END = 27,          // after a timeout: all products are done
+    B_CHECKED = 28,      // [kUnits] the unit's blocks have been looked at
+    kBars = 31
 };
 constexpr int kUnits = 3;                     // units that are worked out ahead
 constexpr int kAhead = 3;                     // tiles whose S is issued before the first of them gets its O += P V
-constexpr uint32_t EXCH_REL = 272;            // [2][4][64] floats: the row's four maxima (or sums)
-constexpr uint32_t UNIT_REL = EXCH_REL + 2048 + 112;   // [kUnits] Unit
+constexpr uint32_t EXCH_REL = 256;            // [2][4][64] floats: the row's four maxima (or sums)
+constexpr uint32_t UNIT_REL = EXCH_REL + 2048;   // [kUnits] Unit
 constexpr uint32_t CAND_REL = UNIT_REL + kUnits * 128;    // first: [2][4] words of keys that may hold NaN or infinities
 constexpr uint32_t FIX_REL = CAND_REL + 32;      // words, first stage, quit
 constexpr uint32_t TMEM_REL = FIX_REL + 32;
@@ -117,7 +126,8 @@ struct Plan {
     uint32_t idesc_s, idesc_o;
     float4 *part_o;          // partial results: [part][128][128]; balanced: part 2 n of the n-th part of the tiles continues a slot, 2 n + 1 begins one
     float2 *part_ml;         // [part][128]
-    int4 *head;              // [slot]: pieces, rows that count, first row, first part (balanced: part of the tiles)
+    int4 *head;              // per slot, or (balanced) per part of the tiles for the slot that begins in it and goes on behind it: pieces, rows that
+                             // count, first row, first part (balanced: of the tiles)
     FastDiv slots_div, per_seq_div;
     int32_t per_seq;         // BSND: tiles per sequence
 };
@@ -711,16 +721,17 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         if (warp == 3) make_balance(pl, balance, lane);
         fence_proxy_async_smem();
         __syncthreads();
-        // what the joining of pieces has to know of every slot, from some thread of some pair
-        const int first = min(balance.waves * pl.pairs, pl.slots), base = balance.before[first];
-        for (int i = cluster + tid * clusters; i < pl.slots && rank == 0; i += kThreads * clusters) {
-            int pieces = 1, of = 0;
-            const int begin = balance.before[i] - base, end = balance.before[i + 1] - base;
-            if (i >= first && end > begin) {
-                of = balance.rank[last_at_most(balance.begin, pl.pairs, begin)];
-                pieces = balance.rank[last_at_most(balance.begin, pl.pairs, end - 1)] - of + 1;
+        // what the joining of pieces has to know: at most one slot begins in a part and goes on behind it
+        if (tid == 0 && rank == 0) {
+            const int begin = balance.begin[cluster], end = balance.begin[cluster + 1], n = balance.rank[cluster];
+            int4 head = make_int4(0, 0, 0, 0);
+            if (end > begin) {
+                const int base = balance.before[min(balance.waves * pl.pairs, pl.slots)];
+                const int i = last_at_most(balance.before, pl.slots, base + end - 1), last = balance.before[i + 1] - base;
+                if (balance.before[i] - base >= begin && last > end)
+                    head = make_int4(balance.rank[last_at_most(balance.begin, pl.pairs, last - 1)] - n + 1, balance.used[i], balance.row0[i], n);
             }
-            pl.head[i] = make_int4(pieces, balance.used[i], balance.row0[i], of);
+            pl.head[end > begin ? n : balance.rank[pl.pairs] + cluster - n] = head;
         }
         __syncthreads();
     }
@@ -1335,8 +1346,8 @@ template <bool kBf16>
 __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, const Plan pl)
 {
     grid_follow();
-    const int slot = blockIdx.x >> 4, r = (blockIdx.x & 15) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int4 head = pl.head[slot];
+    const int r = (blockIdx.x & 15) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 head = pl.head[blockIdx.x >> 4];
     if (head.x <= 1 || r >= head.y) return;
     // rows of the pieces' partial results
     auto row_of = [&](int s) { return (int64_t)(!pl.balanced ? head.w + s : s == 0 ? 2 * head.w + 1 : 2 * (head.w + s)) * kRows + r; };
@@ -1488,11 +1499,11 @@ int dense_plan(const sfm_dense_params &p, int clusters, Plan *pl)
     return SFM_OK;
 }
 
-// workspace: partial rows, then their maxima and sums, then four integers per slot
+// workspace: partial rows, then their maxima and sums, then four integers per slot or part
 size_t dense_parts(const Plan &pl) { return pl.splits <= 1 ? 0 : pl.balanced ? 2 * (size_t)pl.pairs : (size_t)pl.units; }
 size_t dense_bytes(const Plan &pl)
 {
-    return pl.splits <= 1 ? 0 : dense_parts(pl) * kRows * (kD * 4 + 8) + (size_t)pl.slots * 16;
+    return pl.splits <= 1 ? 0 : dense_parts(pl) * kRows * (kD * 4 + 8) + (size_t)(pl.balanced ? pl.pairs : pl.slots) * 16;
 }
 
 using Kernel = void (*)(DenseArgs, Plan, CUtensorMap, CUtensorMap);
@@ -1655,6 +1666,6 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
         launch<true, false, false>,  launch<true, false, true>,  launch<true, true, false>,  launch<true, true, true>};
     cudaError_t e = forms[form](a, pl, q_map, kv_map, device, st);
     if (e == cudaSuccess && pl.splits > 1)
-        e = launch_dependent(bf16 ? sfm_dense_join_kernel<true> : sfm_dense_join_kernel<false>, dim3((unsigned)pl.slots * 16), dim3(256), 0, st, a, pl);
+        e = launch_dependent(bf16 ? sfm_dense_join_kernel<true> : sfm_dense_join_kernel<false>, dim3(16 * (unsigned)(pl.balanced ? pl.pairs : pl.slots)), dim3(256), 0, st, a, pl);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
