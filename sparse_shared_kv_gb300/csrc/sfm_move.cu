@@ -2,23 +2,26 @@
 // drafted ones (sfm_kv_move).
 //
 // path[i] >= i and it grows, so the row that step i writes lies before every
-// row that a later step reads (path[k] >= k > i for k > i): a thread that owns
-// one 16-byte column of a sequence's rows may take the steps in order, several
-// reads ahead of their writes, and needs no other thread.
+// row that a later step reads (path[k] >= k > i for k > i), but it may be one
+// that an earlier step reads.  A CTA takes a sequence's steps in batches: all of a
+// batch's rows are read before the first of them is written.  A few round trips
+// bound it: the path, the pages of its rows, the rows (32 sequences of up to 5
+// rows of 1 KB 2.2 us, 512 of up to 24 rows of 256 bytes 2.9; one thread per
+// 16-byte column that took eight steps at a time needed 7 for the latter).
 #include "sfm_internal.cuh"
 
 namespace sfm {
 namespace {
 
-constexpr int kThreads = 64;
-constexpr int kAhead = 8;             // rows read before the first of them is written
+constexpr int kThreads = 256;
+constexpr int kEach = 4;              // rows per thread and batch
 
 struct MoveArgs {
     const int32_t *path, *first, *table;
     uint8_t *cache;
     int32_t *status;
     int64_t row_stride, rows;
-    int32_t max_path, pieces, block, seq_rows, cols;
+    int32_t max_path, pieces, block, seq_rows, cols, lanes_log2;
     FastDiv block_div;
 };
 
@@ -40,51 +43,53 @@ __device__ __forceinline__ int64_t row_of(const MoveArgs &a, int b, int64_t j)
     return row < a.rows ? row : -1;
 }
 
-// grid (column groups, sequences)
+// grid (groups of 256 pieces, sequences).  A row is taken by 2^lanes_log2 threads, a 16-byte piece each.
 __global__ void __launch_bounds__(kThreads) sfm_move_kernel(const MoveArgs a)
 {
+    __shared__ int64_t src[kThreads], dst[kThreads];
+    __shared__ int good;
     grid_follow();
-    const int b = blockIdx.y, piece = blockIdx.x * kThreads + threadIdx.x;
-    const bool tell = a.status && piece == 0;
-    if (piece >= a.pieces) return;
+    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & ((1 << a.lanes_log2) - 1), row = tid >> a.lanes_log2;
+    const int rows = kThreads >> a.lanes_log2, piece = blockIdx.x * kThreads + lane;
     const int32_t *path = a.path + (int64_t)b * a.max_path;
     const int64_t first = a.first[b];
-    int32_t before = -1;
-    bool more = true;
-    for (int i0 = 0; i0 < a.max_path && more; i0 += kAhead) {
-        // eight entries, then their pages, then their rows: three round trips for all of them
-        int32_t from[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) from[k] = i0 + k < a.max_path ? __ldg(path + i0 + k) : -1;
-        int64_t src[kAhead], dst[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            src[k] = row_of(a, b, from[k] >= 0 ? first + from[k] : -1);
-            dst[k] = row_of(a, b, from[k] >= 0 ? first + i0 + k : -1);
+    for (int base = 0; base < a.max_path; base += kThreads) {
+        // where the next 256 entries lead, and how many of them count
+        const int i = base + tid, n = min(a.max_path - base, kThreads);
+        if (tid == 0) good = n;
+        __syncthreads();
+        if (tid < n) {
+            const int32_t from = __ldg(path + i), before = i > 0 ? __ldg(path + i - 1) : -1;
+            const bool grows = from > before && from >= 0;
+            src[tid] = grows ? row_of(a, b, first + from) : -1;
+            dst[tid] = grows ? row_of(a, b, first + i) : -1;
+            if (src[tid] < 0 || dst[tid] < 0) atomicMin(&good, tid);
         }
-        uint4 v[kAhead];
-        uint32_t moved = 0;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (!more) continue;
-            if (from[k] <= before) {
-                more = false;
-                if (from[k] >= 0 && tell) atomicOr(a.status, SFM_STATUS_BAD_INDEX);
-                continue;
-            }
-            before = from[k];
-            if (src[k] < 0 || dst[k] < 0) {
-                more = false;
-                if (tell) atomicOr(a.status, SFM_STATUS_BAD_BLOCK);
-                continue;
-            }
-            if (src[k] == dst[k]) continue;
-            v[k] = *reinterpret_cast<const uint4 *>(a.cache + src[k] * a.row_stride + (int64_t)piece * 16);
-            moved |= 1u << k;
+        __syncthreads();
+        const int count = good;
+        if (a.status && blockIdx.x == 0 && tid == count && count < n) {
+            // the entry that ends the path, unless it is the negative one behind it
+            const int32_t from = __ldg(path + i), before = i > 0 ? __ldg(path + i - 1) : -1;
+            if (from >= 0) atomicOr(a.status, from > before ? SFM_STATUS_BAD_BLOCK : SFM_STATUS_BAD_INDEX);
         }
+        for (int k0 = 0; k0 < count; k0 += rows * kEach) {
+            uint4 v[kEach];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (moved >> k & 1) *reinterpret_cast<uint4 *>(a.cache + dst[k] * a.row_stride + (int64_t)piece * 16) = v[k];
+            for (int e = 0; e < kEach; ++e) {
+                const int k = k0 + e * rows + row;
+                if (k < count && piece < a.pieces) v[e] = *reinterpret_cast<const uint4 *>(a.cache + src[k] * a.row_stride + (int64_t)piece * 16);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int k = k0 + e * rows + row;
+                if (k < count && piece < a.pieces && src[k] != dst[k])
+                    *reinterpret_cast<uint4 *>(a.cache + dst[k] * a.row_stride + (int64_t)piece * 16) = v[e];
+            }
+            __syncthreads();
+        }
+        if (count < n) return;
+        __syncthreads();
     }
 }
 
@@ -122,6 +127,7 @@ extern "C" int sfm_kv_move(const sfm_move_params *pp, const int32_t *path, const
     a.seq_rows = p.max_seqlen_kv;
     a.cols = p.block_table_stride;
     a.block_div = make_fastdiv(p.block_size ? (uint32_t)p.block_size : 1u);
+    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < a.pieces) ++a.lanes_log2;
     const dim3 grid((unsigned)((a.pieces + kThreads - 1) / kThreads), (unsigned)p.batch_size);
     return launch_dependent(sfm_move_kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a) == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;
 }
