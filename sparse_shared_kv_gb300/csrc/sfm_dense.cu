@@ -1206,7 +1206,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         }
                     } else {
                         auto fall = [&](int c) {
-                            if (!(vis >> c & 1)) return 0.f;
+                            if (!live || !(vis >> c & 1)) return 0.f;     // (a row that does not count masks nothing)
                             const int k = j0 + c - first;
                             return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k))));
                         };

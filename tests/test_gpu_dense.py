@@ -380,6 +380,28 @@ def test_trees_of_any_mask():
     go(seed=15, heads=3, q_lens=(90, 130), lens=(50, 131), tree=True, general_tree=True, bias=True)
 
 
+@pytest.mark.parametrize("mode", [3, 4])
+def test_trees_whose_arrays_end_with_their_memory(mode):
+    """Rows of a tile that do not count read no positions, masks or bounds: those of the last token are the last of 32 MB."""
+    p = problem(seed=39, heads=3, q_lens=(5,), lens=(200,), tree=True, bias=True, mode=mode, left=60, right=0)
+    want = run(p)
+    mask, place = (x.cell_contents for x in p["call"].__closure__)
+    ends = [torch.empty(4 << 20, dtype=x.dtype, device="cuda") for x in (mask, place)]
+    for end, x in zip(ends, (mask, place)):
+        end[-x.numel():] = x.flatten()
+    got = sfm.tree_attention(p["q"], p["kv"], ends[0][-mask.numel():].view(mask.shape), ends[1][-place.numel():].view(place.shape), **p["args"])
+    assert torch.equal(got[0].view(-1), want[0].view(-1)) and torch.equal(got[1].view(-1), want[1].view(-1))
+    p = problem(seed=40, heads=3, q_lens=(5,), lens=(200,), docs=True, bias=True, mode=mode, left=60, right=0)
+    want = run(p)
+    args = dict(p["args"])
+    for name in ("key_begin", "key_end"):
+        end = torch.empty(8 << 20, dtype=torch.int32, device="cuda")
+        end[-5:] = args[name]
+        args[name] = end[-5:]
+    got = sfm.masked_attention(p["q"], p["kv"], **args)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_a_chain_is_causal_attention():
     p = problem(seed=16, heads=16, q_lens=(70,), lens=(400,))
     out, lse, _ = run(p)
