@@ -862,6 +862,12 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             row1 = row2;
             o.output_done();
         }
+        // The products' last arrivals at this CTA's barriers: none may be on its way when the CTA ends.  (S's are waited for by
+        // the softmax, all of them.)
+        const int tiles = c / (2 * kSteps);
+        for (int i = max(c - kStages, 0); i < c && ok; ++i) ok = pair_wait_warp(bar(B_KV_EMPTY + (i & (kStages - 1))), i / kStages & 1, abort_flag);
+        for (int i = max(tiles - 2, 0); i < tiles && ok; ++i) ok = pair_wait_warp(bar(B_O_DONE + (i & 1)), i >> 1 & 1, abort_flag);
+        if (ok && o.units > 0) pair_wait_warp(bar(B_Q_EMPTY), o.units - 1 & 1, abort_flag);
     } else if (warp == 1) {
         // ======================= products =======================
         if (rank == 0) {
