@@ -596,6 +596,14 @@ __device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float ca
     }
 }
 
+// 1 / (l + 2^(sink - m)), also where the sink lies so far above m that the power, or the quotient, leaves fp32's normal range
+// (what is left of such a row is small, but values of the type).
+__device__ __forceinline__ float beside_sink(float l, float m, float sink)
+{
+    const float top = fmaxf(m, sink), e = fast_exp2(0.5f * (m - top));
+    return __fdividef(e, fmaf(l, e * e, sink >= m ? 1.f : fast_exp2(sink - m))) * e;
+}
+
 // 16 lanes x 64 columns of tensor memory: thread t gets of every eight columns 8 i the columns 8 i + 2 (t % 4) and the one
 // behind it, of lane t / 4 in r[4 i], r[4 i + 1] and of lane t / 4 + 8 in r[4 i + 2], r[4 i + 3].
 __device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[32])
@@ -1303,7 +1311,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             const int64_t out_row = w.row0 + R;
             const bool empty = m == -INFINITY && l == 0.f;      // (a row of NaN has no maximum)
             float inv = 0.f;
-            if (live && !empty) inv = __fdividef(1.f, a.sinks && whole ? l + fast_exp2(__ldg(a.sinks + head) * kLog2e - m) : l);
+            if (live && !empty) inv = a.sinks && whole ? beside_sink(l, m, __ldg(a.sinks + head) * kLog2e) : __fdividef(1.f, l);
             const int64_t part_row = (int64_t)w.part * kRows + R;
             const bool parts = live && !whole, out = !parts && R < w.rows && (live || w.piece == 0);
             if (quarter == 0) {
@@ -1390,7 +1398,7 @@ __global__ void __launch_bounds__(256) sfm_dense_join_kernel(const DenseArgs a, 
     }
     const int64_t row = (int64_t)head.z + r;
     float inv = 0.f;
-    if (!empty) inv = __fdividef(1.f, a.sinks ? l + fast_exp2(__ldg(a.sinks + row % a.heads) * kLog2e - m) : l);
+    if (!empty) inv = a.sinks ? beside_sink(l, m, __ldg(a.sinks + row % a.heads) * kLog2e) : __fdividef(1.f, l);
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD) + lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k)

@@ -100,12 +100,15 @@ __global__ void __launch_bounds__(32 * kWarps) sfm_merge_kernel(const MergeArgs 
                 w[n] = w[n] == -INFINITY ? 0.f : exp2_fast((w[n] - m) * kLog2e);
                 total += w[n];
             }
-            float under = total;
+            // 1 / (total + e^(sink - m)), also where the sink lies so far above that the power leaves fp32's range
+            float e = 1.f, under = total;
             if (a.sinks) {
                 const int head = (int)((uint32_t)row - fdiv((uint32_t)row, a.heads_div) * a.heads_div.d);
-                under += exp2_fast((__ldg(a.sinks + head) - m) * kLog2e);
+                const float sink = __ldg(a.sinks + head);
+                e = exp2_fast(0.5f * kLog2e * (m - fmaxf(m, sink)));
+                under = fmaf(total, e * e, sink >= m ? 1.f : exp2_fast((sink - m) * kLog2e));
             }
-            inv = 1.f / under;
+            inv = e / under * e;
         }
         uint32_t used = 0;
 #pragma unroll

@@ -469,6 +469,23 @@ def test_large_scores():
         check(p, out, lse)
 
 
+def test_sinks_far_above_all_scores_leave_what_the_type_holds():
+    """Every visible key far away under a steep bias: the rows are e^-80 and less of the keys, which bf16 holds."""
+    p = problem(seed=41, heads=8, q_lens=(3,), lens=(300,), bias=True, sinks=True, prefix=(100,), mode=4, left=-1, right=-1)
+    p["args"].update(mask_mode=4, win_left=0, win_right=0, key_begin=ints([5] * 3), key_end=ints([5] * 3))
+    at, ql, cap, keys, dist, seen = p["seqs"][0]
+    p["seqs"][0] = (at, ql, cap, keys, dist, (torch.arange(300, device="cuda") < 100).expand(3, 300))
+    for sink in (-20.0, 0.0, 40.0):
+        p["args"]["sinks"] = torch.full((8,), sink, device="cuda")
+        out, lse, _ = run(p)
+        check(p, out, lse)
+        part, end = sfm.masked_attention(p["q"], p["kv"], **{**p["args"], "sinks": None})
+        joined, _ = sfm.merge_attention([part], [end], sinks=p["args"]["sinks"])
+        # three roundings of 2^-8, of the LSE (below 2^8) a few of 2^-16, and at the end of the range a step of 2^-133 each
+        off = (joined.double() - out.double()).abs()
+        assert (off <= 2.0 ** -6 * out.double().abs() + 2.0 ** -132).all()
+
+
 def test_sinks_above_all_scores():
     p = problem(seed=21, heads=16, q_lens=(4,), lens=(50,))
     p["args"]["sinks"] = torch.full((16,), 500.0, device="cuda")
