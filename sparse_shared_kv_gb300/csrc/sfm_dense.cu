@@ -70,7 +70,7 @@ constexpr uint32_t Q_OFF = 0;                 // 8 blocks of 64 rows x 64 values
 constexpr uint32_t P_OFF = 65536;             // 2 buffers x 2 blocks of 64 rows x 64 keys
 constexpr uint32_t KV_OFF = P_OFF + 32768;
 constexpr uint32_t MISC_OFF = KV_OFF + kStages * kStageBytes;
-constexpr uint32_t kSmemBytes = MISC_OFF + 3072;
+constexpr uint32_t kMiscBytes = 3 << 10, kSmemBytes = MISC_OFF + kMiscBytes;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_O = 0, TM_S = 256, kTmemCols = 512;
@@ -102,7 +102,7 @@ constexpr uint32_t FIX_REL = CAND_REL + 32;      // words, first stage, quit
 constexpr uint32_t TMEM_REL = FIX_REL + 32;
 constexpr uint32_t ABORT_REL = TMEM_REL + 4;
 constexpr uint32_t BEAT_REL = ABORT_REL + 4;
-static_assert(UNIT_REL % 128 == 0 && kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= 3072, "misc area");
+static_assert(UNIT_REL % 128 == 0 && kBars * 8 <= EXCH_REL && BEAT_REL + 4 <= kMiscBytes, "misc area");
 
 struct alignas(128) Unit {
     int64_t row0;            // first row of Q (and of the outputs)
@@ -547,14 +547,6 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
 // softmax's loop, which is long enough (with it in between, the jumps over it took 300 clocks per tile)
 #define SFM_RARELY(x) __builtin_expect(!!(x), 0)
 
-// Hidden keys, blocks outside the cache and drafted keys are rare among a call's tiles: their code is kept away from the
-// softmax's loop, which is long enough (with it in between, the jumps over it took 300 clocks per tile)
-#define SFM_RARELY(x) __builtin_expect(!!(x), 0)
-
-// y -> cap tanh(y / cap).  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 7 that interpolates tanh(sqrt u) /
-// sqrt u at the Chebyshev nodes of [0, 1] (off by 4e-9, and 2^-23 of roundings): multiplications and additions, where the
-// exponentials and quotients of tanh z = 1 - 2 / (e^2z + 1) would take as long as all else of a tile (scores of a tile
-// 1300 clocks against 570).  That form is for larger ones.
 // cap tanh z of a row's 32 products with z = to_z * product.  For |z| <= 1, tanh z = z P(z^2) with the polynomial of degree 5
 // that interpolates tanh(sqrt u) / sqrt u at the Chebyshev nodes of [0, 1] (off by 4.8e-7); tanh z = 1 - 2 / (e^2z + 1) for
 // larger ones, and for five pairs of the sixteen anyway: the exponentials and quotients of these run beside the

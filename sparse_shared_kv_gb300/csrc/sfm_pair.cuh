@@ -49,8 +49,6 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Arrive at a barrier of either CTA.  This thread's writes to its own CTA's memory (made visible to the tensor cores by a
 // proxy fence) and its tensor memory accesses come before it; what it wrote into the other CTA's does after
