@@ -475,8 +475,9 @@ def test_sinks_far_above_all_scores_leave_what_the_type_holds():
     p["args"].update(mask_mode=4, win_left=0, win_right=0, key_begin=ints([5] * 3), key_end=ints([5] * 3))
     at, ql, cap, keys, dist, seen = p["seqs"][0]
     p["seqs"][0] = (at, ql, cap, keys, dist, (torch.arange(300, device="cuda") < 100).expand(3, 300))
-    for sink in (-20.0, 0.0, 40.0):
-        p["args"]["sinks"] = torch.full((8,), sink, device="cuda")
+    _, alone, _ = run(p, sinks=None)
+    for above in (60.0, 85.0, 88.5, 90.0, 95.0, 300.0):
+        p["args"]["sinks"] = alone.amax(0) + above
         out, lse, _ = run(p)
         check(p, out, lse)
         part, end = sfm.masked_attention(p["q"], p["kv"], **{**p["args"], "sinks": None})
