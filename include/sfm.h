@@ -536,7 +536,7 @@ typedef struct sfm_dense_params {
     int32_t split_keys;         /* 0: long key ranges are cut so that the SMs are filled, which depends on the batch;
                                    > 0 (a multiple of 128): into pieces of this many keys, whatever else is in the
                                    batch (a row's result is then bit for bit the same in every batch) */
-    int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 1: O = 0 and LSE = -inf; 0: left as they were */
+    int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 0: left as they were; 1: O = 0; 2: LSE = -inf; 3: both */
     float softmax_scale;        /* finite */
     float softcap;              /* 0: none; >= 2^-100: scores are capped */
 } sfm_dense_params;

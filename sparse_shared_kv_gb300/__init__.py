@@ -884,7 +884,8 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
             raise ValueError("tree_mask: needs a word per token")
     kind = q.dtype
     params = _DENSE_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
-                                code, kshape[1] if lkv == PAGED else 0, words, split_keys, out is None, softmax_scale, softcap)
+                                code, kshape[1] if lkv == PAGED else 0, words, split_keys,
+                                (out is None) + 2 * (lse is None), softmax_scale, softcap)
     tensors = _DENSE_TENSORS.pack(
         _address("q", q, kind, dev, shape), kv.data_ptr(), row_stride, rows, table, cols,
         0 if cu_seqlens_q is None else _address("cu_seqlens_q", cu_seqlens_q, _I32, dev, (batch + 1,)),
@@ -967,7 +968,7 @@ def masked_attention(q: torch.Tensor, kv: torch.Tensor, *, softmax_scale: float 
     longer sequences are cut.  ``workspace``: a
     uint8 tensor to use instead of a new one, sfm_dense_workspace_size bytes,
     for one call at a time.  Rows of a TND batch behind its last sequence are
-    0 with LSE -inf in new outputs, and stay as they were where ``out`` is given.
+    0 in a new output and -inf in a new LSE, and stay as they were in given ones.
     No gradient is recorded: inputs that require one are refused in grad mode."""
     return _dense(q, kv, None, None, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right, prefix_lens,
                   key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv, layout_q,

@@ -1045,8 +1045,8 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             const int64_t rest = lo + max(all - max(hi, lo), (int64_t)0);
             for (int64_t i = (int64_t)blockIdx.x * 256 + (tid - 128); i < rest * 64; i += (int64_t)gridDim.x * 256) {
                 const int64_t k = i >> 6, row = k < lo ? k : max(hi, lo) + (k - lo);
-                reinterpret_cast<uint4 *>(a.out)[row * 64 + (i & 63)] = make_uint4(0, 0, 0, 0);
-                if (a.lse && (i & 63) == 0) a.lse[row] = -INFINITY;
+                if (a.zero_rest & 1) reinterpret_cast<uint4 *>(a.out)[row * 64 + (i & 63)] = make_uint4(0, 0, 0, 0);
+                if (a.zero_rest & 2 && a.lse && (i & 63) == 0) a.lse[row] = -INFINITY;
             }
         }
         int n = 0, g = 0, ex = 0;
@@ -1414,7 +1414,7 @@ int dense_check(const sfm_dense_params *pp)
     if (p.mask_mode != 0 && p.mask_mode != 3 && p.mask_mode != 4) return SFM_ERR_INVALID_ARG;
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
     if (p.layout_kv == SFM_LAYOUT_PAGED && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
-    if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128) return SFM_ERR_INVALID_ARG;
+    if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128 || p.zero_rest & ~3) return SFM_ERR_INVALID_ARG;
     if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || p.softcap >= 0x1p-100f) || !std::isfinite(p.softcap) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
         return SFM_ERR_INVALID_ARG;
     if (p.max_seqlen_kv > 1 << 30) return SFM_ERR_UNSUPPORTED;
@@ -1629,7 +1629,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     a.block = p.block_size;
     a.cols = t->block_table_stride;
     a.words = p.tree_words;
-    a.zero_rest = p.zero_rest != 0;
+    a.zero_rest = p.zero_rest;
     a.scale = p.softmax_scale;
     a.cap = p.softcap;
     a.block_div = make_fastdiv(paged ? (uint32_t)p.block_size : 1u);

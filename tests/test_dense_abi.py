@@ -77,6 +77,12 @@ def test_pointers_are_refused(lib):
     assert lib.sfm_dense_forward(none, t, None, None, None, 0, None, None) == 0
 
 
+@pytest.mark.parametrize("rest", [-1, 4, 1 << 20])
+def test_rest_is_refused(lib, rest):
+    size = C.c_size_t(0)
+    assert lib.sfm_dense_workspace_size(C.byref(_dense(zero_rest=rest)), C.byref(size)) == 1
+
+
 def _merge(**kw):
     return sfm.SfmMergeParams(**{**dict(tokens=3, heads=4, head_dim=512, parts=2, dtype=sfm.FP16), **kw})
 

@@ -508,6 +508,18 @@ def test_rows_behind_the_last_sequence():
     assert (mine[13:] == 7).all() and (ends[13:] == 7).all()
 
 
+def test_rows_behind_the_last_sequence_with_one_given_output():
+    p = problem(seed=42, heads=20, q_lens=(5, 8), lens=(30, 9), rest=40)
+    out, lse, _ = run(p)
+    torch.full_like(lse, 7.0)          # (memory that a new tensor may get)
+    mine = torch.full_like(out, 7.0)
+    got, end, _ = run(p, out=mine)
+    assert (mine[13:] == 7).all() and (end[13:] == -INF).all() and torch.equal(mine[:13], out[:13]) and torch.equal(end, lse)
+    ends = torch.full_like(lse, 7.0)
+    got, end, _ = run(p, lse=ends)
+    assert (got[13:] == 0).all() and (ends[13:] == 7).all() and torch.equal(got, out) and torch.equal(ends[:13], lse[:13])
+
+
 @pytest.mark.parametrize("layout", ["TND", "BSND"])
 def test_used_queries(layout):
     go(seed=23, heads=16, q_lens=(40, 40, 40), lens=(100, 30, 50), used_q=(0, 17, 40), layout_q=layout, layout_kv=layout)
