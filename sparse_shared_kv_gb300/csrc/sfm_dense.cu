@@ -1593,7 +1593,11 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     if (tokens == 0) return SFM_OK;
     if (!t->q || !t->kv || !out) return SFM_ERR_INVALID_ARG;
     if (((uintptr_t)t->q | (uintptr_t)t->kv | (uintptr_t)out) & 15u) return SFM_ERR_LAYOUT;
-    if (((uintptr_t)lse | (uintptr_t)t->sinks | (uintptr_t)t->bias_slopes) & 3u || (uintptr_t)t->tree_mask & 7u) return SFM_ERR_LAYOUT;
+    const void *const words[] = {lse, status, t->sinks, t->bias_slopes, t->block_table, t->cu_seqlens_q, t->cu_seqlens_kv, t->seqused_q, t->seqused_kv,
+                                 t->prefix_lens, t->key_begin, t->key_end, t->positions};
+    uintptr_t bits = 0;
+    for (const void *x : words) bits |= (uintptr_t)x;
+    if (bits & 3u || (uintptr_t)t->tree_mask & 7u) return SFM_ERR_LAYOUT;
 
     DenseArgs a = {};
     a.q = t->q;

@@ -77,6 +77,21 @@ def test_pointers_are_refused(lib):
     assert lib.sfm_dense_forward(none, t, None, None, None, 0, None, None) == 0
 
 
+@pytest.mark.parametrize("name", ["block_table", "cu_seqlens_q", "cu_seqlens_kv", "seqused_q", "seqused_kv", "prefix_lens", "key_begin",
+                                  "key_end", "positions", "status"])
+def test_unaligned_integers_are_refused(lib, name):
+    kw, tkw, status = {}, {}, None
+    if name == "status":
+        status = ADDR + 2
+    else:
+        tkw[name] = ADDR + 2
+    if name == "positions":
+        kw, tkw = dict(tree_words=1), dict(tkw, tree_mask=ADDR)
+    if name.startswith("cu"):
+        kw, tkw = dict(layout_q=sfm.TND, layout_kv=sfm.TND, total_q=4), {**dict(cu_seqlens_q=ADDR, cu_seqlens_kv=ADDR, block_table=None), **tkw}
+    assert lib.sfm_dense_forward(C.byref(_dense(**kw)), C.byref(_tensors(**tkw)), ADDR, ADDR, None, 0, status, None) == 3
+
+
 @pytest.mark.parametrize("rest", [-1, 4, 1 << 20])
 def test_rest_is_refused(lib, rest):
     size = C.c_size_t(0)
