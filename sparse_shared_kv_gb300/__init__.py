@@ -1085,7 +1085,7 @@ def move_kv(cache: torch.Tensor, path: torch.Tensor, first: torch.Tensor, *, blo
             raise ValueError("block_table: needs (b, blocks)")
         cols = block_table.shape[1]
         table = _address("block_table", block_table, _I32, dev, (batch, cols))
-    params = _MOVE_PARAMS.pack(batch, most, kv.shape[-1] * kv.element_size(), kv.shape[1] if table or cols else 0, kv.shape[1],
+    params = _MOVE_PARAMS.pack(batch, most, kv.shape[-1] * kv.element_size(), 0 if block_table is None else kv.shape[1], kv.shape[1],
                                cols, row_stride, rows)
     rc = (_lib or lib()).sfm_kv_move(params, _address("path", path, _I32, dev, (batch, most)),
                                      _address("first", first, _I32, dev, (batch,)), table, kv.data_ptr(),

@@ -894,3 +894,11 @@ def test_refusals():
                            ((c, path, ints([0, 1])), dict(block_table=ints([[0]])), "first"), ((c, path, first), dict(block_table=ints([0])), "block_table"),
                            ((c[0], path, first), {}, "cache")):
         bad(word, sfm.move_kv, *args, **kw)
+
+
+def test_moved_rows_through_tables_without_blocks_are_refused():
+    c = torch.arange(4 * 16 * 64, device="cuda").view(4, 16, 64).half()
+    was = c.clone()
+    with pytest.raises(sfm.SfmError, match="invalid"):
+        sfm.move_kv(c, ints([[1, 2]] * 4), ints([0] * 4), block_table=torch.empty(4, 0, dtype=torch.int32, device="cuda"))
+    assert torch.equal(c, was)
