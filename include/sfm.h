@@ -592,7 +592,7 @@ int sfm_dense_workspace_size(const sfm_dense_params *params, size_t *bytes);
  * positions[k], and query i at pos(i) = positions[i] (those of the sequence).
  * Every key of the first kind is visible, of the second those whose bit k of
  * tree_mask[i] is set (word k / 64, bit k % 64: the ancestors of token i and
- * itself); mode 4 takes away those outside [pos(i) - win_left, pos(i) + win_right].
+ * itself; bits behind the last word count as 0); mode 4 takes away those outside [pos(i) - win_left, pos(i) + win_right].
  * A row without visible keys has O = 0 and LSE = -inf, as have rows of q at or
  * beyond seqused_q.  Keys that a row does not see have no part in it, whatever
  * they hold (NaN and infinities too); a row that sees a NaN is NaN, and what a row
@@ -619,7 +619,7 @@ typedef struct sfm_merge_params {
 /* Join attention results over separate sets of keys.  Per row, with part n's
  * output O_n and LSE_n (natural, without sinks):
  *     LSE = log sum_n e^LSE_n,   O = sum_n e^LSE_n O_n / (sum_n e^LSE_n + e^sinks[head])
- * A part with LSE_n = -inf has no keys: its O_n is not read.  No keys at all
+ * A part with LSE_n = -inf has no keys: its O_n does not count, whatever it holds.  No keys at all
  * give O = 0 and LSE = -inf.
  * outs, lses: HOST arrays of `parts` device pointers to dense (tokens, heads,
  * head_dim), 16-byte aligned, and fp32 (tokens, heads).  sinks: fp32 (heads) or

@@ -736,6 +736,26 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         __syncthreads();
     }
 
+    // a wait that may take a whole unit, which has no longest time: it ends when no tile has gone by for some time
+    auto wait_as_long_as_tiles_go_by = [&](uint32_t bar, uint32_t parity) {
+        uint64_t t0 = globaltimer_ns();
+        int seen = *beat;
+        while (!__all_sync(0xffffffffu, pair_try_wait(bar, parity))) {
+            bool ok = true;
+            if (lane == 0) {
+                if (*beat != seen) {
+                    seen = *beat;
+                    t0 = globaltimer_ns();
+                } else if (globaltimer_ns() - t0 > 2 * kTimeoutNs) {
+                    *abort_flag = 1;
+                }
+                ok = !*abort_flag;
+            }
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return false;
+        }
+        return true;
+    };
+
     if (warp == 3) {
         // ======================= units =======================
         int n = 0;
@@ -748,7 +768,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             if (end) w.valid = 0;
             else if (!make_unit(a, pl, share, u, cluster, lane, w, pl.balanced && n == 0 ? seqs : nullptr)) continue;
             const int slot = n % kUnits;
-            if (n >= kUnits && !pair_wait_warp(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1, abort_flag)) break;
+            if (n >= kUnits && !wait_as_long_as_tiles_go_by(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1)) break;
             if (lane == 0) {
                 units[slot] = w;
                 mbar_arrive(bar(B_UNIT_FULL + slot));
@@ -990,24 +1010,8 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         __syncwarp();
     } else if (warp == 2) {
         // ======================= V rows made finite =======================
-        uint64_t t0 = globaltimer_ns();
-        int seen = 0;
         for (int n = 0;;) {
-            if (!__all_sync(0xffffffffu, pair_try_wait(bar(B_FIX), n & 1))) {
-                // as long as tiles go by there may be nothing to do
-                bool ok = true;
-                if (lane == 0) {
-                    if (*beat != seen) {
-                        seen = *beat;
-                        t0 = globaltimer_ns();
-                    } else if (globaltimer_ns() - t0 > 2 * kTimeoutNs) {
-                        *abort_flag = 1;
-                    }
-                    ok = !*abort_flag;
-                }
-                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-                continue;
-            }
+            if (!wait_as_long_as_tiles_go_by(bar(B_FIX), n & 1)) break;
             ++n;
             if (fix_words[5]) break;
             const uint16_t inf = kBf16 ? 0x7f80 : 0x7c00;
