@@ -65,10 +65,11 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// (small results are kept: they count where the other parts' values are 0)
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

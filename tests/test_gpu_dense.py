@@ -469,6 +469,16 @@ def test_large_scores():
         check(p, out, lse)
 
 
+@pytest.mark.parametrize("far", [60.0, 87.0, 88.5, 91.0, 200.0])
+def test_a_part_far_below_another_one_of_zeros(far):
+    """What is left of it are values of the type, off by the roundings of the LSEs' difference, of the type and by a step at the end of the range."""
+    outs = [torch.zeros(3, 2, 512, dtype=torch.bfloat16, device="cuda"), randn(gen(43), 3, 2, 512, dtype=torch.bfloat16)]
+    ends = [torch.zeros(3, 2, device="cuda"), torch.full((3, 2), -far, device="cuda")]
+    got, lse = sfm.merge_attention(outs, ends)
+    want = outs[1].double() * math.exp(-far)
+    assert ((got.double() - want).abs() <= (2.0 ** -8 + far * 2.0 ** -22) * want.abs() + 2.0 ** -133).all() and (lse == 0).all()
+
+
 def test_sinks_far_above_all_scores_leave_what_the_type_holds():
     """Every visible key far away under a steep bias: the rows are e^-80 and less of the keys, which bf16 holds."""
     p = problem(seed=41, heads=8, q_lens=(3,), lens=(300,), bias=True, sinks=True, prefix=(100,), mode=4, left=-1, right=-1)
