@@ -544,6 +544,7 @@ typedef struct sfm_dense_params {
 /*   q              BSND (b, q_s, num_heads, 512) / TND (q_t, num_heads, 512), dense, 16-byte aligned
  *   kv             BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned; rows of 512
  *                  values, kv_row_stride bytes apart (>= 1024, multiple of 16), kv_rows rows in all
+ *                  (paged: a block at least)
  *   the length tensors and sinks as in sfm_tensors (seqused_kv required for PAGED)
  *   bias_slopes    (num_heads) fp32 or NULL
  *   prefix_lens    (b) int32 or NULL

@@ -123,6 +123,7 @@ static_assert(sizeof(Unit) <= 128, "unit area");
 // of slots.  (With such parts alone every sequence is under way at once: 16 trees of 16 tokens over 200 MB of keys 509 us.)
 struct Plan {
     int32_t slots, splits, chunk, box_rows, align, units, balanced, pairs;
+    int32_t block_bytes, octet_bytes;     // of a stage's 64 keys: from one block of 64 values to the next, from eight keys to the next
     uint32_t idesc_s, idesc_o;
     float4 *part_o;          // partial results: [part][128][128]; balanced: part 2 n of the n-th part of the tiles continues a slot, 2 n + 1 begins one
     float2 *part_ml;         // [part][128]
@@ -516,6 +517,9 @@ __device__ __forceinline__ bool rows_meet_any(int who, bool yes)
     return any != 0;
 }
 
+template <uint32_t kBytes>
+using Bytes = std::integral_constant<uint32_t, kBytes>;
+
 // two fp32 operations at once
 __device__ __forceinline__ uint64_t pair_bits(float2 v) { return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x); }
 __device__ __forceinline__ float2 pair_of(uint64_t b)
@@ -810,24 +814,22 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             ++c;
             if (use > 0 && !pair_wait_warp(bar(B_KV_EMPTY + st), use - 1 & 1, abort_flag)) return false;
             const uint32_t dst = sb + KV_OFF + st * kStageBytes;
-            if (boxes == 1) {
+            if (!SFM_RARELY(boxes != 1)) {
                 const int y = __shfl_sync(0xffffffffu, row, half);
                 if (elect_one()) {
                     if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
                     pair_load(dst, &kv_map, 0, y, block, first_bar(B_KV_FULL + st));
                 }
             } else {
+                // pages of 16 or 32 rows (or a multiple that has no 64): a copy each, eight rows of the four blocks after eight rows
                 int y[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31);
+                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, row, half * boxes + k & 31) >> 3;
                 if (elect_one()) {
                     if (rank == 0) expect_tx(bar(B_KV_FULL + st), 2 * kStageBytes);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (k < boxes)
-#pragma unroll
-                            for (int d = 0; d < kBlocks; ++d)
-                                pair_load(dst + d * 8192u + k * pl.box_rows * 128u, &kv_map, 0, y[k], block + d, first_bar(B_KV_FULL + st));
+                        if (k < boxes) pair_load_octets(dst + k * pl.box_rows * 512u, &kv_map, block, y[k], first_bar(B_KV_FULL + st));
                 }
             }
             __syncwarp();
@@ -895,8 +897,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             bool ok = true;
             Order o;
             const uint32_t id_s = pl.idesc_s, id_o = pl.idesc_o;
-            const Desc q_desc = desc_sw128(sb + Q_OFF, 16, 1024), k_desc = desc_sw128(sb + KV_OFF, 16, 1024);
-            const Desc p_desc = desc_sw128(sb + P_OFF, 16, 1024), v_desc = desc_sw128(sb + KV_OFF, 8192, 1024);
+            const Desc q_desc = desc_sw128(sb + Q_OFF, 16, 1024), p_desc = desc_sw128(sb + P_OFF, 16, 1024);
             auto landed = [&](int k) { return pair_wait_warp(bar(B_KV_FULL + (k & (kStages - 1))), k / kStages & 1, abort_flag); };
             auto next_unit = [&]() -> int {
                 for (;;) {
@@ -910,88 +911,95 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                     if (tiles) return tiles;
                 }
             };
-            while (ok) {
-                while (ok && o.wants_scores()) {
-                    if (o.at_new_unit()) {
-                        const int tiles = next_unit();
-                        if (tiles <= 0) {
-                            o.end();
-                            ok = tiles == 0;
-                            break;
+            // (twice, for the two ways in which keys lie in a stage: distances that the kernel has to add up made prompts a tenth slower)
+            auto multiply = [&](auto block_bytes, auto octet_bytes) {
+                constexpr uint32_t block = decltype(block_bytes)::value, octet = decltype(octet_bytes)::value;
+                const Desc k_desc = desc_sw128(sb + KV_OFF, 16, octet), v_desc = desc_sw128(sb + KV_OFF, block, octet);
+                while (ok) {
+                    while (ok && o.wants_scores()) {
+                        if (o.at_new_unit()) {
+                            const int tiles = next_unit();
+                            if (tiles <= 0) {
+                                o.end();
+                                ok = tiles == 0;
+                                break;
+                            }
+                            o.enter(tiles);
+                            ok = pair_wait_warp(bar(B_Q_FULL), o.units - 1 & 1, abort_flag);
                         }
-                        o.enter(tiles);
-                        ok = pair_wait_warp(bar(B_Q_FULL), o.units - 1 & 1, abort_flag);
+                        const uint32_t d = tmem + TM_S + (gk & 3) * 64;
+    #pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const uint32_t st = c & (kStages - 1);
+                            ok = ok && landed(c);
+                            ++c;
+                            tc_fence_after();
+                            if (ok && elect_one()) {
+                                const Desc kd = {k_desc.lo + st * (kStageBytes >> 4), k_desc.hi};
+    #pragma unroll
+                                for (int j = 0; j < 4 * kBlocks; ++j) {
+                                    const uint32_t sub = (j & 3) * 32u;
+                                    pair_mma(d, desc_at(q_desc, k * kStageBytes + (j >> 2) * 8192u + sub), desc_at(kd, (j >> 2) * block + sub), id_s, (k | j) > 0);
+                                }
+                                pair_commit(bar(B_KV_EMPTY + st));
+                                if (k == kSteps - 1) {
+                                    pair_commit(bar(B_S_FULL + (gk & 3)));
+                                    if (o.k + 1 == o.k_tiles) pair_commit(bar(B_Q_EMPTY));
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        ++gk;
+                        o.scores_done();
                     }
-                    const uint32_t d = tmem + TM_S + (gk & 3) * 64;
-#pragma unroll
+                    if (!ok || o.ahead == 0) break;
+                    const int buf = gv & 1;
+                    ok = pair_wait_warp(bar(B_P_FULL + buf), gv >> 1 & 1, abort_flag);
+                    if (o.v == 0 && o.done > 0) ok = ok && pair_wait_warp(bar(B_O_FREE), o.done - 1 & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t found = lane < 4 ? cand_words[4 * buf + lane] : 0u;
+                    if (__any_sync(0xffffffffu, found != 0)) {
+                        // the staged V, made finite in both CTAs before it is used
+                        for (int k = 0; k < kSteps && ok; ++k) ok = landed(c + k);
+                        if (!ok) break;
+                        for (uint32_t r = 0; r < 2; ++r) {
+                            const uint32_t to = in_cta(bar0 + FIX_REL, r);
+                            if (lane < 4) store_remote(to + 4 * lane, found);
+                            if (lane == 4) store_remote(to + 16, (uint32_t)c & (kStages - 1));
+                        }
+                        if (lane < 4) cand_words[4 * buf + lane] = 0;
+                        __syncwarp();
+                        if (lane < 2) arrive_remote_release(in_cta(bar(B_FIX), lane));
+                        __syncwarp();
+                        ok = pair_wait_warp(bar(B_FIXED), fixes & 1, abort_flag);
+                        ++fixes;
+                        if (!ok) break;
+                        fence_proxy_async_smem();
+                    }
+    #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
                         const uint32_t st = c & (kStages - 1);
                         ok = ok && landed(c);
                         ++c;
                         tc_fence_after();
                         if (ok && elect_one()) {
-                            const Desc kd = {k_desc.lo + st * (kStageBytes >> 4), k_desc.hi};
-#pragma unroll
-                            for (int j = 0; j < 4 * kBlocks; ++j) {
-                                const uint32_t sub = (j >> 2) * 8192u + (j & 3) * 32u;
-                                pair_mma(d, desc_at(q_desc, k * kStageBytes + sub), desc_at(kd, sub), id_s, (k | j) > 0);
-                            }
+                            const Desc pd = {p_desc.lo + buf * (16384u >> 4), p_desc.hi}, vd = {v_desc.lo + st * (kStageBytes >> 4), v_desc.hi};
+    #pragma unroll
+                            for (int j = 0; j < 2 * kBlocks; ++j)        // columns of the stage, 16 keys of its 64
+                                pair_mma(tmem + TM_O + ((k >> 1) * kBlocks / 2 + (j >> 2)) * 128, desc_at(pd, (k & 1) * 8192u + (j & 3) * 32u),
+                                         desc_at(vd, (j >> 2) * 2 * block + (j & 3) * 2 * octet), id_o, o.v > 0 || (k & 1) || (j & 3) > 0);
                             pair_commit(bar(B_KV_EMPTY + st));
-                            if (k == kSteps - 1) {
-                                pair_commit(bar(B_S_FULL + (gk & 3)));
-                                if (o.k + 1 == o.k_tiles) pair_commit(bar(B_Q_EMPTY));
-                            }
+                            if (k == kSteps - 1) pair_commit(bar(B_O_DONE + buf));
                         }
                         __syncwarp();
                     }
-                    ++gk;
-                    o.scores_done();
+                    ++gv;
+                    o.output_done();
                 }
-                if (!ok || o.ahead == 0) break;
-                const int buf = gv & 1;
-                ok = pair_wait_warp(bar(B_P_FULL + buf), gv >> 1 & 1, abort_flag);
-                if (o.v == 0 && o.done > 0) ok = ok && pair_wait_warp(bar(B_O_FREE), o.done - 1 & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t found = lane < 4 ? cand_words[4 * buf + lane] : 0u;
-                if (__any_sync(0xffffffffu, found != 0)) {
-                    // the staged V, made finite in both CTAs before it is used
-                    for (int k = 0; k < kSteps && ok; ++k) ok = landed(c + k);
-                    if (!ok) break;
-                    for (uint32_t r = 0; r < 2; ++r) {
-                        const uint32_t to = in_cta(bar0 + FIX_REL, r);
-                        if (lane < 4) store_remote(to + 4 * lane, found);
-                        if (lane == 4) store_remote(to + 16, (uint32_t)c & (kStages - 1));
-                    }
-                    if (lane < 4) cand_words[4 * buf + lane] = 0;
-                    __syncwarp();
-                    if (lane < 2) arrive_remote_release(in_cta(bar(B_FIX), lane));
-                    __syncwarp();
-                    ok = pair_wait_warp(bar(B_FIXED), fixes & 1, abort_flag);
-                    ++fixes;
-                    if (!ok) break;
-                    fence_proxy_async_smem();
-                }
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    const uint32_t st = c & (kStages - 1);
-                    ok = ok && landed(c);
-                    ++c;
-                    tc_fence_after();
-                    if (ok && elect_one()) {
-                        const Desc pd = {p_desc.lo + buf * (16384u >> 4), p_desc.hi}, vd = {v_desc.lo + st * (kStageBytes >> 4), v_desc.hi};
-#pragma unroll
-                        for (int j = 0; j < 2 * kBlocks; ++j)        // columns of the stage, 16 keys of its 64
-                            pair_mma(tmem + TM_O + ((k >> 1) * kBlocks / 2 + (j >> 2)) * 128, desc_at(pd, (k & 1) * 8192u + (j & 3) * 32u),
-                                     desc_at(vd, (j >> 2) * 16384u + (j & 3) * 2048u), id_o, o.v > 0 || (k & 1) || (j & 3) > 0);
-                        pair_commit(bar(B_KV_EMPTY + st));
-                        if (k == kSteps - 1) pair_commit(bar(B_O_DONE + buf));
-                    }
-                    __syncwarp();
-                }
-                ++gv;
-                o.output_done();
-            }
+            };
+            if (SFM_RARELY(pl.octet_bytes != 1024)) multiply(Bytes<1024>(), Bytes<4096>());
+            else multiply(Bytes<8192>(), Bytes<1024>());
             // no more rows to be made finite
             if (lane < 2) {
                 store_remote(in_cta(bar0 + FIX_REL, lane) + 20, 1u);
@@ -1023,7 +1031,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                     // the key's 256 values in this CTA: four blocks, 128 bytes each, in the stages of its half of the keys
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t st = fix_words[4] + q / kBlocks * 2 + (key >> 6) & (kStages - 1);
-                        uint16_t *row = reinterpret_cast<uint16_t *>(smem + KV_OFF + st * kStageBytes + q % kBlocks * 8192 + (key & 63) * 128);
+                        uint16_t *row = reinterpret_cast<uint16_t *>(smem + KV_OFF + st * kStageBytes + q % kBlocks * pl.block_bytes + (key >> 3 & 7) * pl.octet_bytes + (key & 7) * 128);
                         for (int k = lane; k < 64; k += 32)
                             if ((row[k] & inf) == inf) row[k] = 0;
                     }
@@ -1445,7 +1453,9 @@ Fn driver_function(const char *name)
 }
 
 // Rows of 512 values as eight blocks of 64: boxes of `blocks` blocks x `box_rows` rows land block after block, as the
-// products read them.  The last map of a thread's (for queries, for keys) is kept with its sizes and gets another address
+// products read them.  Boxes of fewer than 64 rows, of which a stage takes several, land by eight rows instead: eight rows of
+// each block, then the next eight, so that the distances stay the same across boxes (a copy per block and page took 64 of
+// them for a tile of pages of 16: 16 trees of 16 tokens 607 us against 538, with pages of 48 657 against 577).  The last map of a thread's (for queries, for keys) is kept with its sizes and gets another address
 // where they are the same: encoding costs as much as the rest of a launch.
 struct KeptMap {
     CUtensorMap map;
@@ -1458,10 +1468,11 @@ int make_map(CUtensorMap *map, KeptMap &kept, const void *ptr, int dtype, int64_
     if (kept.rows != rows || kept.row_bytes != row_bytes || kept.dtype != dtype || kept.box_rows != box_rows || kept.blocks != blocks) {
         const EncodeFn encode = driver_function<EncodeFn>("cuTensorMapEncodeTiled");
         if (!encode) return SFM_ERR_CUDA;
-        const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 8}, strides[2] = {(cuuint64_t)row_bytes, 128};
-        const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)blocks}, steps[3] = {1, 1, 1};
+        const bool octets = box_rows < 64;
+        const cuuint64_t dims[4] = {64, (cuuint64_t)(octets ? 8 : rows), 8, (cuuint64_t)rows / 8}, strides[3] = {(cuuint64_t)row_bytes, 128, 8 * (cuuint64_t)row_bytes};
+        const cuuint32_t box[4] = {64, (cuuint32_t)(octets ? 8 : box_rows), (cuuint32_t)blocks, (cuuint32_t)box_rows / 8}, steps[4] = {1, 1, 1, 1};
         kept.rows = 0;
-        if (encode(&kept.map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+        if (encode(&kept.map, dtype == SFM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, octets ? 4 : 3,
                    const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SFM_ERR_CUDA;
@@ -1586,6 +1597,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     const bool paged = p.layout_kv == SFM_LAYOUT_PAGED, tnd = p.layout_q == SFM_LAYOUT_TND;
     if (t->kv_row_stride < 2 * kD || t->kv_row_stride % 16 || t->kv_rows <= 0) return SFM_ERR_LAYOUT;
     if (t->kv_rows > ((int64_t)1 << 31) - 1024) return SFM_ERR_UNSUPPORTED;
+    if (paged && t->kv_rows < p.block_size) return SFM_ERR_LAYOUT;
     if (p.layout_kv == SFM_LAYOUT_BSND && t->kv_rows < (int64_t)p.batch_size * p.max_seqlen_kv) return SFM_ERR_LAYOUT;
     if ((tnd && !t->cu_seqlens_q) || (p.layout_kv == SFM_LAYOUT_TND && !t->cu_seqlens_kv)) return SFM_ERR_INVALID_ARG;
     if (paged ? !t->seqused_kv || !t->block_table || t->block_table_stride <= 0 : t->block_table != nullptr)
@@ -1658,6 +1670,8 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
         if (pl.box_rows > 64) pl.box_rows = 64;
     }
     pl.align = paged ? pl.box_rows : 1;
+    pl.block_bytes = pl.box_rows == 64 ? 8192 : 1024;
+    pl.octet_bytes = pl.box_rows == 64 ? 1024 : 4096;
     pl.slots_div = make_fastdiv((uint32_t)pl.slots);
     pl.per_seq_div = make_fastdiv((uint32_t)(pl.per_seq > 0 ? pl.per_seq : 1));
     const bool bf16 = p.dtype == SFM_DTYPE_BF16;
@@ -1671,7 +1685,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     CUtensorMap q_map, kv_map;
     static thread_local KeptMap kept_q, kept_kv;
     rc = make_map(&q_map, kept_q, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
-    if (!rc) rc = make_map(&kv_map, kept_kv, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, pl.box_rows == 64 ? kBlocks : 1);
+    if (!rc) rc = make_map(&kv_map, kept_kv, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, kBlocks);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
     const int form = (bf16 ? 4 : 0) | (a.cap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0);

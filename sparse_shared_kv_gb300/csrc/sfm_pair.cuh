@@ -170,6 +170,15 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// The same from rows in groups of eight (four dimensions: values, rows of a group, blocks, groups).
+__device__ __forceinline__ void pair_load_octets(uint32_t dst, const CUtensorMap *map, int block, int octet, uint32_t cluster_bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(block), "r"(octet), "r"(cluster_bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

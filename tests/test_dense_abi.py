@@ -92,6 +92,11 @@ def test_unaligned_integers_are_refused(lib, name):
     assert lib.sfm_dense_forward(C.byref(_dense(**kw)), C.byref(_tensors(**tkw)), ADDR, ADDR, None, 0, status, None) == 3
 
 
+@pytest.mark.parametrize("rows", [1, 7, 63])
+def test_a_cache_of_less_than_a_block_is_refused(lib, rows):
+    assert lib.sfm_dense_forward(C.byref(_dense()), C.byref(_tensors(kv_rows=rows)), ADDR, ADDR, None, 0, None, None) == 3
+
+
 @pytest.mark.parametrize("rest", [-1, 4, 1 << 20])
 def test_rest_is_refused(lib, rest):
     size = C.c_size_t(0)
