@@ -65,6 +65,10 @@ constexpr uint32_t kStageBytes = kBlocks * 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;              // log2 units
+// fp16 weights are 2^6 times what they stand for: 2^14 at most, and those far below the largest keep their bits down to 2^-20
+// of it (from 1 on, to 2^-14)
+template <bool kBf16>
+constexpr float kLift = kBf16 ? 0.f : 6.f;
 
 constexpr uint32_t Q_OFF = 0;                 // 8 blocks of 64 rows x 64 values
 constexpr uint32_t P_OFF = 65536;             // 2 buffers x 2 blocks of 64 rows x 64 keys
@@ -1269,7 +1273,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         sum.y *= alpha;
                     }
                 }
-                const float back = m == -INFINITY ? 0.f : -m;
+                const float back = m == -INFINITY ? 0.f : kLift<kBf16> - m;
                 uint32_t pk[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -1311,6 +1315,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             row_values(sum.x + sum.y, got);
             if (!ok) break;
             const float l = (got[0] + got[1]) + (got[2] + got[3]);
+            m -= kLift<kBf16>;
             const bool whole = w.splits == 1;
             const int64_t out_row = w.row0 + R;
             const bool empty = m == -INFINITY && l == 0.f;      // (a row of NaN has no maximum)

@@ -469,6 +469,22 @@ def test_large_scores():
         check(p, out, lse)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_weights_far_below_the_largest_keep_their_bits(dt):
+    """Key j has one value, in column j: every weight e^-distance shows, off by its rounding and the result's (2 u), and 2^-17 of the sums."""
+    n, kind = 40, DT[dt]
+    kv = torch.zeros(n, 512, dtype=kind, device="cuda")
+    kv[range(n), range(n)] = 2.0 ** 14
+    q = torch.zeros(1, 2, 512, dtype=kind, device="cuda")
+    out, lse = sfm.masked_attention(q, kv, bias_slopes=torch.tensor([1.0, 0.5], device="cuda"), mask_mode=4, win_left=13, win_right=0,
+                                    cu_seqlens_q=ints([0, 1]), cu_seqlens_kv=ints([0, n]), layout_q="TND", layout_kv="TND")
+    far = (n - 1 - torch.arange(n, device="cuda", dtype=F64))
+    for h, slope in enumerate((1.0, 0.5)):
+        w = torch.where(far <= 13, torch.exp(-slope * far), 0.0)
+        assert ((out[0, h, :n].double() * 2.0 ** -14 - w / w.sum()).abs() <= (2 * half_step(kind) + 2.0 ** -17) * w / w.sum()).all()
+        assert abs(float(lse[0, h]) - float(torch.log(w.sum()))) < 2.0 ** -18
+
+
 @pytest.mark.parametrize("far", [60.0, 87.0, 88.5, 91.0, 200.0])
 def test_a_part_far_below_another_one_of_zeros(far):
     """What is left of it are values of the type, off by the roundings of the LSEs' difference, of the type and by a step at the end of the range."""
