@@ -16,7 +16,7 @@
 //
 // Per CTA, 12 warps:
 //   0      copies: Q of a unit, then K(0), K(1), K(2), V(0), K(3), V(1), ... in stages of 32 KB, one copy each (64 keys x 256
-//          values as four blocks of 64 values; pages of fewer rows take more), four stages in a ring
+//          values as four blocks of 64 values; pages of fewer rows one each), four stages in a ring
 //   1      products, in the pair's first CTA: S(0), S(1), S(2), O += P(0) V(0), S(3), O += P(1) V(1), ...
 //   2      tensor memory; takes NaN and infinities out of V rows that some row must not see (below)
 //   3      units: which rows and keys come next, three units ahead
@@ -28,7 +28,7 @@
 // of matrix products); called again and again it runs into the GPU's power limit, as such products do (1721), and the
 // clock falls to 1.6 to 1.75 GHz (1.46 to 1.49 PFLOP/s).  Every unit costs some 5000 clocks of the softmax's besides (its
 // results are written, the next unit's rows looked up), which units of few tiles do not hide: 4096 causal tokens of 64
-// heads 1.31, documents of some 1600 1.29 PFLOP/s.  Single tokens are bound by memory: 32 x 24 k keys 4.5 TB/s with 10 us to
+// heads 1.30, documents of some 1600 1.27 PFLOP/s.  Single tokens are bound by memory: 32 x 24 k keys 4.5 TB/s with 10 us to
 // plan and 9 us to join.
 //
 // A unit is a tile of Q and a piece of its range of keys.  Pieces of a range
@@ -39,7 +39,8 @@
 // every row, so the softmax finds it among the keys it masks; the products
 // then wait until the values that are not finite are zeros in the staged V.
 //
-// Every wait is bounded (2 s); a timeout raises the CTA's abort flag, every role
+// Every wait is bounded (2 s, of those that may take a unit 4 s without a tile); a
+// timeout raises the CTA's abort flag, every role
 // leaves its loop, copies and products in flight are waited for, tensor memory
 // is freed and SFM_STATUS_TIMEOUT is set.
 #include <cuda_bf16.h>
@@ -1460,7 +1461,8 @@ Fn driver_function(const char *name)
 // Rows of 512 values as eight blocks of 64: boxes of `blocks` blocks x `box_rows` rows land block after block, as the
 // products read them.  Boxes of fewer than 64 rows, of which a stage takes several, land by eight rows instead: eight rows of
 // each block, then the next eight, so that the distances stay the same across boxes (a copy per block and page took 64 of
-// them for a tile of pages of 16: 16 trees of 16 tokens 607 us against 538, with pages of 48 657 against 577).  The last map of a thread's (for queries, for keys) is kept with its sizes and gets another address
+// them for a tile of pages of 16: 16 trees of 16 tokens 607 us against 538, with pages of 48 657 against 577).
+// The last map of a thread's (for queries, for keys) is kept with its sizes and gets another address
 // where they are the same: encoding costs as much as the rest of a launch.
 struct KeptMap {
     CUtensorMap map;
