@@ -566,7 +566,9 @@ __device__ __forceinline__ float2 cap_wide(float2 z, float cap)
     return make_float2(fmaf(__fdividef(-2.f, fast_exp2(t.x) + 1.f), cap, cap), fmaf(__fdividef(-2.f, fast_exp2(t.y) + 1.f), cap, cap));
 }
 
-__device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float cap)
+// The latter form too where some row does not see all its keys: what it does not see does not choose the form, and so has no
+// part in the last bits of others.  (To leave such keys out of the search for large ones made trees of 61 tokens 5 to 9 % slower.)
+__device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float cap, bool all)
 {
     float far = 0.f;
 #pragma unroll
@@ -574,7 +576,7 @@ __device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float ca
         y[c] = mul2(y[c], to_z);
         if (c < 11) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
     }
-    if (!SFM_RARELY(!__all_sync(0xffffffffu, far <= 1.f))) {
+    if (!SFM_RARELY(!__all_sync(0xffffffffu, all && far <= 1.f))) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
             // (in the order in which the two kinds go out side by side)
@@ -1052,7 +1054,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
         const int r = (part & 1) * 32 + lane, half = part >> 1;     // row; keys and columns of O in halves
         const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
         const int quarter = half * 2 + wg, c0 = half * 64 + wg * 32;      // this thread's keys of a tile: [c0, c0 + 32)
-        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e, to_z = kCap ? a.scale / a.cap : 0.f;
+        const float sl2 = a.scale * kLog2e, cap2 = a.cap * kLog2e;
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint8_t *const p_row = smem + P_OFF + half * 8192;
         if (a.zero_rest && a.cu_q) {
@@ -1165,6 +1167,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                 if (a.words) tree = a.tree + (int64_t)(w.q0 + i_q) * a.words;
                 if constexpr (kBias) slope = __ldg(a.slopes + head) * kLog2e;
             }
+            const float to_z = kCap && live ? a.scale / a.cap : 0.f;       // (rows that do not count do not choose the cap's form)
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int i = 0; i < w.tiles; ++i) {
@@ -1214,7 +1217,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
 #pragma unroll
                 for (int c = 0; c < 16; ++c) y[c] = make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
                 if constexpr (kCap) {
-                    cap_scores(y, to_z, cap2);
+                    cap_scores(y, to_z, cap2, vis == 0xffffffffu);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) y[c] = mul2(y[c], sl2);

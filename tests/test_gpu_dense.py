@@ -470,6 +470,23 @@ def test_large_scores():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_capped_scores_do_not_depend_on_what_rows_do_not_see(dt):
+    """Large scores of the next sequence's rows, of rows behind a sequence's end and of hidden keys leave every bit as it was."""
+    p = problem(seed=44, dt=dt, heads=5, q_lens=(3, 40), lens=(150, 90), layout_kv="PAGED", block=64, cap=20.0, q_scale=0.1, mode=4, left=100, right=0)
+    kv, table = p["kv"].nan_to_num(0.0), p["args"]["block_table"]
+    first = sfm.masked_attention(p["q"], kv, split_keys=128, **p["args"])
+    check(p, first[0].view(-1, 5, 512), first[1].view(-1, 5))
+    q = p["q"].clone()
+    q[3:] *= 300.0
+    # behind the first sequence's end, and a key that its window hides
+    kv = kv.clone()
+    kv[table[0, 2].long(), 150 - 128:] = 30.0
+    kv[table[0, 0].long(), 40] = -30.0
+    then = sfm.masked_attention(q, kv, split_keys=128, **p["args"])
+    assert torch.equal(then[0][:3], first[0][:3]) and torch.equal(then[1][:3], first[1][:3])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_weights_far_below_the_largest_keep_their_bits(dt):
     """Key j has one value, in column j: every weight e^-distance shows, off by its rounding and the result's (2 u), and 2^-17 of the sums."""
     n, kind = 40, DT[dt]
