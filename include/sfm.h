@@ -545,7 +545,8 @@ typedef struct sfm_dense_params {
  *   kv             BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned; rows of 512
  *                  values, kv_row_stride bytes apart (>= 1024, multiple of 16), kv_rows rows in all
  *                  (paged: a block at least)
- *   the length tensors and sinks as in sfm_tensors (seqused_kv required for PAGED)
+ *   the length tensors and sinks as in sfm_tensors (seqused_kv required for PAGED; where cu_seqlens_q falls, the
+ *                  length is cut to 0, SFM_STATUS_BAD_LENGTH is set and rows of q may be skipped)
  *   bias_slopes    (num_heads) fp32 or NULL
  *   prefix_lens    (b) int32 or NULL
  *   key_begin, key_end   (tokens) int32 or NULL

@@ -147,11 +147,27 @@ __device__ __forceinline__ int slot_base(const DenseArgs &a, int b, int q0) { re
 
 __device__ __forceinline__ int first_query(const DenseArgs &a, int b) { return min(max(__ldg(a.cu_q + b), 0), a.total_q); }
 
-// The sequence of a slot, found by the whole warp 32 ways at a time, and the slot's number k in it (< 0: none).
-__device__ __forceinline__ DenseSeq slot_sequence(const DenseArgs &a, const Plan &pl, int slot, int lane, int &k)
+// The last sequence whose first slot is at most `slot`, by halves; query_of: a sequence's first row.
+template <typename Fn>
+__device__ __forceinline__ int sequence_by_halves(const DenseArgs &a, int slot, Fn query_of)
+{
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_base(a, mid, query_of(mid)) <= slot) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The sequence of a slot, found by the whole warp 32 ways at a time, and the slot's number k in it (< 0: none).  Where offsets
+// fall this search and the one by halves find different sequences, and the balanced plan was made with the latter: the units
+// then go by it too, so that they are what the plan has counted.
+__device__ __forceinline__ DenseSeq slot_sequence(const DenseArgs &a, const Plan &pl, int slot, int lane, int &k, bool falls)
 {
     int b = 0;
-    if (a.cu_q) {
+    if (a.cu_q && falls) {
+        b = sequence_by_halves(a, slot, [&](int i) { return first_query(a, i); });
+    } else if (a.cu_q) {
         for (int n = a.batch; n > 1;) {
             const int step = (n + 31) / 32, i = b + lane * step;
             const bool below = lane * step < n && (lane == 0 || slot_base(a, i, first_query(a, i)) <= slot);
@@ -226,12 +242,7 @@ __device__ __forceinline__ DenseSeq known_sequence(const DenseArgs &a, const Pla
 {
     int b;
     if (a.cu_q) {
-        int lo = 0, hi = a.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (slot_base(a, mid, seqs[mid].q0) <= slot) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
+        b = sequence_by_halves(a, slot, [&](int i) { return seqs[i].q0; });
         k = slot - slot_base(a, b, seqs[b].q0);
     } else {
         b = (int)fdiv((uint32_t)slot, pl.per_seq_div);
@@ -258,10 +269,10 @@ __device__ __forceinline__ int slot_weight(const DenseArgs &a, const Plan &pl, i
 }
 
 // A slot, worked out by the whole warp: everything but which of its tiles a unit takes.  -1: no rows; otherwise its tiles.
-__device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int slot, int lane, Unit &w, const DenseSeq *seqs = nullptr)
+__device__ __forceinline__ int make_slot(const DenseArgs &a, const Plan &pl, int slot, int lane, Unit &w, const DenseSeq *seqs, bool falls)
 {
     int k;
-    const DenseSeq s = seqs ? known_sequence(a, pl, slot, seqs, k) : slot_sequence(a, pl, slot, lane, k);
+    const DenseSeq s = seqs ? known_sequence(a, pl, slot, seqs, k) : slot_sequence(a, pl, slot, lane, k, falls);
     const int64_t first_row = (int64_t)k * kRows, all = (int64_t)s.q_cap * a.heads;
     if (k < 0 || first_row >= all) return -1;
     w.row0 = (int64_t)s.q0 * a.heads + first_row;
@@ -410,7 +421,7 @@ __device__ __forceinline__ Share make_share(const Plan &pl, const Balance &b, in
 }
 
 // The next unit: of the pair's share, or (not balanced) piece and slot u.  False: there is nothing to do.
-__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, Share &s, int u, int c, int lane, Unit &w, const DenseSeq *seqs)
+__device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, Share &s, int u, int c, int lane, Unit &w, const DenseSeq *seqs, bool falls)
 {
     const bool wave = s.wave < s.waves;
     int slot, off = 0, split = 0;
@@ -424,10 +435,11 @@ __device__ __forceinline__ bool make_unit(const DenseArgs &a, const Plan &pl, Sh
         off = s.off;
         s.off = 0;
     }
-    const int tiles = make_slot(a, pl, slot, lane, w, seqs);
+    const int tiles = make_slot(a, pl, slot, lane, w, seqs, falls);
     if (pl.balanced) {
         if (tiles < 0) return false;
         const int weight = max(tiles, 1), take = wave ? weight : min(weight - off, s.end - s.at);
+        if (take <= 0) return false;           // (no plan has such a part: the copies and products would take it for the end)
         if (!wave) s.at += take;
         w.tile0 = off;
         w.tiles = tiles ? take : 0;
@@ -723,12 +735,14 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
     grid_follow();
     DenseSeq *const seqs = reinterpret_cast<DenseSeq *>(smem + KV_OFF);
     Balance &balance = *reinterpret_cast<Balance *>(smem + P_OFF);
+    bool falls = false;                       // balanced: offsets of q fall somewhere
     if (pl.balanced) {
         // the batch's sequences, then every slot's weight, then the pairs' parts (copies come and P goes here once there is a unit)
         for (int i = tid; i < a.batch; i += kThreads) seqs[i] = dense_seq(a, i);
         __syncthreads();
         for (int i = tid; i < pl.slots; i += kThreads) balance.before[i] = slot_weight(a, pl, i, seqs, balance.row0[i], balance.used[i]);
-        __syncthreads();
+        for (int i = tid + 1; i < a.batch; i += kThreads) falls |= seqs[i].q0 < seqs[i - 1].q0;
+        falls = __syncthreads_or(falls);
         if (warp == 3) make_balance(pl, balance, lane);
         fence_proxy_async_smem();
         __syncthreads();
@@ -777,7 +791,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             w.bad = 0;
             const bool end = pl.balanced ? share.wave >= share.waves && (share.at >= share.end || share.slot >= pl.slots) : u >= pl.units;
             if (end) w.valid = 0;
-            else if (!make_unit(a, pl, share, u, cluster, lane, w, pl.balanced && n == 0 ? seqs : nullptr)) continue;
+            else if (!make_unit(a, pl, share, u, cluster, lane, w, pl.balanced && n == 0 ? seqs : nullptr, falls)) continue;
             const int slot = n % kUnits;
             if (n >= kUnits && !wait_as_long_as_tiles_go_by(bar(B_UNIT_EMPTY + slot), n / kUnits - 1 & 1)) break;
             if (lane == 0) {
@@ -793,6 +807,12 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
             __syncwarp();
             ++n;
             if (end) break;
+        }
+        if (!pl.balanced && a.cu_q && blockIdx.x == 0) {
+            // offsets that fall, also where no slot leads to the sequence (the balanced plan has looked at all)
+            bool bad = false;
+            for (int i = lane; i < a.batch; i += 32) bad |= __ldg(a.cu_q + i + 1) < __ldg(a.cu_q + i);
+            if (__any_sync(0xffffffffu, bad) && lane == 0) dense_status(a, SFM_STATUS_BAD_LENGTH);
         }
     } else if (warp == 0) {
         // ======================= copies =======================

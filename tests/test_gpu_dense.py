@@ -599,6 +599,40 @@ def test_bad_blocks_and_lengths():
         assert status & sfm.STATUS_BAD_LENGTH
 
 
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("most,split", [(9000, 0), (1000, 0), (9000, 512)])
+def test_offsets_that_fall_cut_lengths_and_nothing_else(seed, most, split):
+    """Long keys (ranges cut evenly or into pieces) and short ones: such a batch ends, says so, and leaves its surroundings alone."""
+    r = random.Random(seed)
+    B, T, heads = r.randint(3, 120), r.randint(200, 900), r.choice((16, 64))
+    pool = randn(gen(seed), 200, 64, 512, dtype=torch.bfloat16)
+    cols = -(-most // 64)
+    args = dict(softmax_scale=512 ** -0.5, layout_q="TND", layout_kv="PAGED", max_seqlen_kv=most, split_keys=split,
+                seqused_kv=ints([r.choice((0, 100, 700, most)) for _ in range(B)]),
+                block_table=ints([[r.randrange(200) for _ in range(cols)] for _ in range(B)]))
+    q = randn(gen(100 + seed), T, heads, 512, dtype=torch.bfloat16)
+    fine = [0] + sorted(r.randint(0, T) for _ in range(B - 1)) + [T]
+    want = sfm.masked_attention(q, pool, cu_seqlens_q=ints(fine), **args)
+    for n in range(4):
+        cu = list(fine)
+        if n < 3:
+            for _ in range(n + 1):
+                i = r.randint(1, B - 1)
+                cu[i], cu[i - 1] = cu[i - 1], cu[i]
+        else:
+            r.shuffle(cu)
+        if all(x <= y for x, y in zip(cu, cu[1:])):
+            cu[0] = T
+        room, ends = torch.full((T + 16, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T + 16, heads), 7.0, device="cuda")
+        status = ints([0])
+        sfm.masked_attention(q, pool, cu_seqlens_q=ints(cu), out=room[8:-8], lse=ends[8:-8], status=status, **args)
+        assert int(status) == sfm.STATUS_BAD_LENGTH
+        for x in (room, ends):
+            assert (x[:8] == 7).all() and (x[-8:] == 7).all()
+    again = sfm.masked_attention(q, pool, cu_seqlens_q=ints(fine), **args)
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+
+
 def test_far_offsets():
     """A page more than 2^32 bytes behind the start of its cache."""
     blocks = (1 << 32) // (1024 * 64) + 3
