@@ -1211,7 +1211,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         if (a.mode == 4) {
                             for (uint32_t rest = bits; rest; rest &= rest - 1) {
                                 const int c = __ffs(rest) - 1;
-                                const int64_t pos = __ldg(a.positions + w.q0 + o + c);
+                                const int64_t pos = __ldg(a.positions + w.q0 + drafted_entry(o + c, w.q_len));
                                 if (pos < (int64_t)row.p - a.win_left || pos > (int64_t)row.p + a.win_right) bits &= ~(1u << c);
                             }
                         }
@@ -1254,7 +1254,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         auto fall = [&](int c) {
                             if (!live || !(vis >> c & 1)) return 0.f;     // (a row that does not count masks nothing)
                             const int k = j0 + c - first;
-                            return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k))));
+                            return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + drafted_entry(k, w.q_len)))));
                         };
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {

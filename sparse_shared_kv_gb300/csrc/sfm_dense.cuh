@@ -65,6 +65,10 @@ __device__ __noinline__ DenseSeq dense_seq(const DenseArgs &a, int b)
     return s;
 }
 
+// Which of a sequence's q_len (> 0) entries of positions the k-th drafted key has: one of them whatever k is, so that no
+// lookup leaves the sequence's.
+__host__ __device__ constexpr int drafted_entry(int k, int q_len) { return k < 0 ? 0 : k < q_len ? k : q_len - 1; }
+
 // What query i of a sequence sees: keys [0, prefix) and [lo, hi); with a tree
 // [lo, hi) among the keys before `first`, and those of its bits from there on.
 struct DenseRow {

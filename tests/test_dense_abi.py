@@ -1,11 +1,13 @@
 """CPU checks of the calls over many queries: struct layouts and refusals before anything is launched."""
 import ctypes as C
 import math
+import subprocess
 
 import pytest
 import torch
 
 import sparse_shared_kv_gb300 as sfm
+from sparse_shared_kv_gb300 import buildlib
 
 ADDR = 1 << 20      # an aligned address that is never read
 
@@ -101,6 +103,30 @@ def test_a_cache_of_less_than_a_block_is_refused(lib, rows):
 def test_rest_is_refused(lib, rest):
     size = C.c_size_t(0)
     assert lib.sfm_dense_workspace_size(C.byref(_dense(zero_rest=rest)), C.byref(size)) == 1
+
+
+def test_lookups_of_drafted_keys_stay_with_their_sequence(tmp_path):
+    """The index that the kernel looks positions up with, on the host: the key's own where there is one, one of the sequence's anyway."""
+    source, program = tmp_path / "entry.cu", tmp_path / "entry"
+    source.write_text("""#include <climits>
+#include "sfm_dense.cuh"
+int main()
+{
+    const int far[] = {INT_MIN, INT_MIN + 1, -(1 << 30), 1 << 30, INT_MAX - 1, INT_MAX};
+    for (int n = 1; n < 400; ++n) {
+        for (int k = -700; k < 1100; ++k) {
+            const int i = sfm::drafted_entry(k, n);
+            if (i < 0 || i >= n || (k >= 0 && k < n && i != k)) return 1;
+        }
+        for (int k : far)
+            if (sfm::drafted_entry(k, n) < 0 || sfm::drafted_entry(k, n) >= n) return 2;
+    }
+    return 0;
+}
+""")
+    subprocess.run([buildlib._nvcc(), *buildlib.ARCH, "-std=c++17", "-I", buildlib.INCLUDE, "-I", buildlib.CSRC, str(source), "-o", str(program)],
+                   check=True)
+    assert subprocess.run([str(program)]).returncode == 0
 
 
 def _merge(**kw):
