@@ -538,7 +538,7 @@ typedef struct sfm_dense_params {
                                    batch (a row's result is then bit for bit the same in every batch) */
     int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 0: left as they were; 1: O = 0; 2: LSE = -inf; 3: both */
     float softmax_scale;        /* finite */
-    float softcap;              /* 0: none; >= 2^-100: scores are capped */
+    float softcap;              /* 0: none; 2^-100 to 2^127: scores are capped */
 } sfm_dense_params;
 
 /*   q              BSND (b, q_s, num_heads, 512) / TND (q_t, num_heads, 512), dense, 16-byte aligned
@@ -604,7 +604,8 @@ int sfm_dense_workspace_size(const sfm_dense_params *params, size_t *bytes);
  * lse: device fp32 (tokens x num_heads) or NULL; workspace:
  * device, >= sfm_dense_workspace_size() bytes, 256-byte aligned, used by one
  * call at a time.  Products are exact, sums in fp32; weights e^x are rounded to
- * dtype for the product with kv. */
+ * dtype for the product with kv.  A capped score is off by 2^-20 of itself, and
+ * with a softcap of 128 or less by 2^-21 of the softcap too. */
 int sfm_dense_forward(const sfm_dense_params *params, const sfm_dense_tensors *tensors, void *out, float *lse,
                       void *workspace, size_t workspace_bytes, int32_t *status, sfm_stream_t stream);
 

@@ -572,6 +572,20 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
 // that interpolates tanh(sqrt u) / sqrt u at the Chebyshev nodes of [0, 1] (off by 4.8e-7); tanh z = 1 - 2 / (e^2z + 1) for
 // larger ones, and for five pairs of the sixteen anyway: the exponentials and quotients of these run beside the
 // multiplications of the others (all by the second form, the scores of a tile took 1300 clocks; all by the first, 900).
+// The second form is off by up to 2^-21 of the cap, however small the score is: 6e-5 at kWideCap, an eighth of an fp16 weight's
+// half step.  Larger caps have a kernel of their own, which takes it for |z| > 1 alone.
+constexpr float kWideCap = 128.f;
+enum CapKind { kNoCap, kSmallCap, kLargeCap };
+
+__device__ __forceinline__ float2 tanh_ratio(float2 u)
+{
+    float2 p = fma2(u, make_float2(-3.080409251e-03f, -3.080409251e-03f), 1.677677624e-02f);
+    p = fma2(p, u, -5.163545866e-02f);
+    p = fma2(p, u, 1.328251381e-01f);
+    p = fma2(p, u, -3.332918032e-01f);
+    return fma2(p, u, 9.999994421e-01f);
+}
+
 __device__ __forceinline__ float2 cap_wide(float2 z, float cap)
 {
     const float2 t = mul2(z, 2.f * kLog2e);
@@ -596,18 +610,34 @@ __device__ __forceinline__ void cap_scores(float2 (&y)[16], float to_z, float ca
             if (k >= 11) {
                 y[k] = cap_wide(y[k], cap);
             } else {
-                const float2 u = mul2(y[k], y[k]);
-                float2 p = fma2(u, make_float2(-3.080409251e-03f, -3.080409251e-03f), 1.677677624e-02f);
-                p = fma2(p, u, -5.163545866e-02f);
-                p = fma2(p, u, 1.328251381e-01f);
-                p = fma2(p, u, -3.332918032e-01f);
-                p = fma2(p, u, 9.999994421e-01f);
+                const float2 p = tanh_ratio(mul2(y[k], y[k]));
                 y[k] = mul2(mul2(y[k], cap), p);
             }
         }
     } else {
 #pragma unroll
         for (int c = 0; c < 16; ++c) y[c] = cap_wide(y[c], cap);
+    }
+}
+
+// The same for caps above kWideCap: a score x = to_x * product is x P(z^2) for |z| <= 1, off in proportion to itself (and not
+// to the cap, also where z is too small for fp32), whatever its neighbours are.
+__device__ __forceinline__ void cap_scores_each(float2 (&y)[16], float to_z, float to_x, float cap)
+{
+    float far = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) far = fmaxf(far, fmaxf(fabsf(y[c].x), fabsf(y[c].y)));
+    const bool some = __any_sync(0xffffffffu, far * fabsf(to_z) > 1.f);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const float2 z = mul2(y[c], to_z);
+        float2 x = mul2(mul2(y[c], to_x), tanh_ratio(mul2(z, z)));
+        if (SFM_RARELY(some)) {
+            const float2 t = cap_wide(z, cap);
+            if (!(fabsf(z.x) <= 1.f)) x.x = t.x;
+            if (!(fabsf(z.y) <= 1.f)) x.y = t.y;
+        }
+        y[c] = x;
     }
 }
 
@@ -672,7 +702,7 @@ __device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide)
                  : "memory");
 }
 
-template <bool kBf16, bool kCap, bool kBias>
+template <bool kBf16, int kCap, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Plan pl, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap kv_map)
@@ -1188,6 +1218,7 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                 if constexpr (kBias) slope = __ldg(a.slopes + head) * kLog2e;
             }
             const float to_z = kCap && live ? a.scale / a.cap : 0.f;       // (rows that do not count do not choose the cap's form)
+            const float to_x = live ? sl2 : 0.f;
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int i = 0; i < w.tiles; ++i) {
@@ -1236,8 +1267,10 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                 float2 y[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) y[c] = make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
-                if constexpr (kCap) {
+                if constexpr (kCap == kSmallCap) {
                     cap_scores(y, to_z, cap2, vis == 0xffffffffu);
+                } else if constexpr (kCap == kLargeCap) {
+                    cap_scores_each(y, to_z, to_x, cap2);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) y[c] = mul2(y[c], sl2);
@@ -1456,7 +1489,7 @@ int dense_check(const sfm_dense_params *pp)
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
     if (p.layout_kv == SFM_LAYOUT_PAGED && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
     if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128 || p.zero_rest & ~3) return SFM_ERR_INVALID_ARG;
-    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || p.softcap >= 0x1p-100f) || !std::isfinite(p.softcap) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
+    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || (p.softcap >= 0x1p-100f && p.softcap <= 0x1p127f)) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
         return SFM_ERR_INVALID_ARG;
     if (p.max_seqlen_kv > 1 << 30) return SFM_ERR_UNSUPPORTED;
     const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;
@@ -1568,7 +1601,7 @@ int dense_clusters(int *device, int *clusters)
     const bool keep = *device < kMaxDevices;
     *clusters = keep ? known[*device].load(std::memory_order_relaxed) : 0;
     if (*clusters > 0) return SFM_OK;
-    const auto kernel = sfm_dense_kernel<true, false, false>;
+    const auto kernel = sfm_dense_kernel<true, kNoCap, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess) return SFM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
@@ -1585,7 +1618,7 @@ int dense_clusters(int *device, int *clusters)
     return SFM_OK;
 }
 
-template <bool kBf16, bool kCap, bool kBias>
+template <bool kBf16, int kCap, bool kBias>
 cudaError_t launch(const DenseArgs &a, const Plan &pl, const CUtensorMap &q, const CUtensorMap &kv, int device, cudaStream_t st)
 {
     static std::atomic<bool> ready[kMaxDevices];
@@ -1718,11 +1751,13 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     if (!rc) rc = make_map(&kv_map, kept_kv, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, kBlocks);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
-    const int form = (bf16 ? 4 : 0) | (a.cap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0);
-    static constexpr decltype(&launch<true, true, true>) forms[8] = {
-        launch<false, false, false>, launch<false, false, true>, launch<false, true, false>, launch<false, true, true>,
-        launch<true, false, false>,  launch<true, false, true>,  launch<true, true, false>,  launch<true, true, true>};
-    cudaError_t e = forms[form](a, pl, q_map, kv_map, device, st);
+    const CapKind cap = a.cap > kWideCap ? kLargeCap : a.cap > 0.f ? kSmallCap : kNoCap;
+    static constexpr decltype(&launch<true, kNoCap, true>) forms[2][3][2] = {
+        {{launch<false, kNoCap, false>, launch<false, kNoCap, true>}, {launch<false, kSmallCap, false>, launch<false, kSmallCap, true>},
+         {launch<false, kLargeCap, false>, launch<false, kLargeCap, true>}},
+        {{launch<true, kNoCap, false>, launch<true, kNoCap, true>}, {launch<true, kSmallCap, false>, launch<true, kSmallCap, true>},
+         {launch<true, kLargeCap, false>, launch<true, kLargeCap, true>}}};
+    cudaError_t e = forms[bf16][cap][a.slopes != nullptr](a, pl, q_map, kv_map, device, st);
     if (e == cudaSuccess && pl.splits > 1)
         e = launch_dependent(bf16 ? sfm_dense_join_kernel<true> : sfm_dense_join_kernel<false>, dim3(16 * (unsigned)(pl.balanced ? pl.pairs : pl.slots)), dim3(256), 0, st, a, pl);
     return e == cudaSuccess ? SFM_OK : SFM_ERR_CUDA;

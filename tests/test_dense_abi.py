@@ -99,6 +99,13 @@ def test_a_cache_of_less_than_a_block_is_refused(lib, rows):
     assert lib.sfm_dense_forward(C.byref(_dense()), C.byref(_tensors(kv_rows=rows)), ADDR, ADDR, None, 0, None, None) == 3
 
 
+@pytest.mark.parametrize("cap", [1.8e38, 3.4e38])
+def test_caps_that_leave_fp32_in_steps_of_a_power_of_two_are_refused(lib, cap):
+    size = C.c_size_t(0)
+    assert lib.sfm_dense_workspace_size(C.byref(_dense(softcap=cap)), C.byref(size)) == 1
+    assert lib.sfm_dense_forward(C.byref(_dense(softcap=cap)), C.byref(_tensors()), ADDR, ADDR, None, 0, None, None) == 1
+
+
 @pytest.mark.parametrize("rest", [-1, 4, 1 << 20])
 def test_rest_is_refused(lib, rest):
     size = C.c_size_t(0)

@@ -486,6 +486,58 @@ def test_capped_scores_do_not_depend_on_what_rows_do_not_see(dt):
     assert torch.equal(then[0][:3], first[0][:3]) and torch.equal(then[1][:3], first[1][:3])
 
 
+def check_capped(p, out, lse):
+    """As check(), but with capped scores x off by 2^-20 (1 + |x|) whatever the cap is (tanh z / z off by 2^-21 of itself and a few
+    roundings up to |z| = 1; above, 1 - 2 / (e^2z + 1) by 2^-23 of the cap, which is at most 1.32 |x|), and up to a cap of 128,
+    where the quotient comes for smaller z too, by 2^-21 of the cap."""
+    a, H, dtype = p["args"], p["heads"], p["dtype"]
+    q, cap, scale = p["q"].reshape(-1, H, 512).double(), a["softcap"], a["softmax_scale"]
+    u, tiny = half_step(dtype), torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    for at, ql, _, keys, dist, seen in p["seqs"]:
+        qq, kk, n = q[at:at + ql], keys.double(), keys.shape[0]
+        x = cap * torch.tanh(torch.einsum("thd,nd->thn", qq, kk) * scale / cap)
+        d = 64 * 2.0 ** -23 * torch.einsum("thd,nd->thn", qq.abs(), kk.abs()) * abs(scale) + 2.0 ** -20 * (1 + x.abs())
+        if cap <= 128:
+            d = d + 2.0 ** -21 * cap
+        if a.get("bias_slopes") is not None:
+            fall = a["bias_slopes"].double()[:, None] * dist.abs().double()[:, None]
+            x, d = x - fall, d + 2.0 ** -20 * fall
+        x = torch.where(seen[:, None], x, -INF)
+        d = torch.where(seen[:, None], d, 0.0).amax(-1)
+        L = x.logsumexp(-1)
+        w = (x - L[..., None]).exp()
+        O, mag = torch.einsum("thn,nd->thd", w, kk), torch.einsum("thn,nd->thd", w, kk.abs())
+        off, bound = (lse[at:at + ql].double() - L).abs(), d + n * 2.0 ** -24 + 2.0 ** -20 * (1 + L.abs())
+        assert (off <= bound).all(), f"LSE off by {float((off / bound).max()):.3g} bounds"
+        off, bound = (out[at:at + ql].double() - O).abs(), (u + 2 * d[..., None] + n * 2.0 ** -23 + 2.0 ** -20) * mag + u * O.abs() + tiny
+        assert (off <= bound).all(), f"O off by {float((off / bound).max()):.3g} bounds"
+
+
+@pytest.mark.parametrize("cap", [20.0, 128.0, 129.0, 1e3, 1e4, 1e6, 1e9, 2.0 ** 60, 2.0 ** 127])
+@pytest.mark.parametrize("q_scale", [0.05, 3.0])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_large_caps_leave_small_scores_as_they_are(cap, q_scale, dt):
+    p = problem(seed=45, dt=dt, heads=20, q_lens=(7, 60), lens=(300, 1500), layout_kv="PAGED", cap=cap, q_scale=q_scale, mode=4, left=700, right=0,
+                bias=dt == "fp16")
+    out, lse, status = run(p)
+    assert status == 0
+    check_capped(p, out, lse)
+
+
+@pytest.mark.parametrize("cap", [129.0, 1e3, 1e4])
+def test_scores_about_as_large_as_a_large_cap(cap):
+    """|z| on both sides of 1; what is above it elsewhere in a warp changes no bit of a row."""
+    p = problem(seed=46, heads=20, q_lens=(40,), lens=(500,), cap=cap, q_scale=cap)
+    out, lse, _ = run(p)
+    check_capped(p, out, lse)
+    small = problem(seed=46, heads=20, q_lens=(40,), lens=(500,), cap=cap, q_scale=0.1)
+    mixed = small["q"].clone()
+    mixed[::2] = p["q"][::2]
+    one, both = sfm.masked_attention(small["q"], p["kv"], **p["args"]), sfm.masked_attention(mixed, p["kv"], **p["args"])
+    for x, y, z in zip(one, (out, lse), both):
+        assert torch.equal(z[1::2], x[1::2]) and torch.equal(z[::2], y.view(z.shape)[::2])
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_weights_far_below_the_largest_keep_their_bits(dt):
     """Key j has one value, in column j: every weight e^-distance shows, off by its rounding and the result's (2 u), and 2^-17 of the sums."""
