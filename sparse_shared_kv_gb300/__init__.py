@@ -455,6 +455,7 @@ def sparse_flash_mla(q: torch.Tensor, *, metadata: Metadata, ori_kv=None, cmp_kv
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _increment_version = torch.autograd.graph.increment_version
+_forward_ad = torch.autograd.forward_ad
 _I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 # The structs of include/sfm.h as native-layout packers (the calls below build them every time; packing
@@ -828,12 +829,26 @@ def _no_gradient(name, x):
         raise ValueError(f"{name}: requires a gradient, which this call does not record (use no_grad)")
 
 
+def _no_tangents(**inputs):
+    """Inside forward_ad.dual_level: none of the inputs is a dual tensor."""
+    for name, x in inputs.items():
+        for y in x if isinstance(x, list) else [x]:
+            if isinstance(y, torch.Tensor) and _forward_ad.unpack_dual(y).tangent is not None:
+                raise ValueError(f"{name}: has a tangent, which this call does not carry on")
+
+
 def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right,
            prefix_lens, key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv,
            layout_q, layout_kv, split_keys, out, lse, workspace, status, stream):
     code, dev = _first("q", q, _SIXTEEN_BIT)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(q=q, kv=kv, sinks=sinks, bias_slopes=bias_slopes, out=out, lse=lse)
     if q.requires_grad:
         _no_gradient("q", q)
+    if sinks is not None and _tensor("sinks", sinks).requires_grad:
+        _no_gradient("sinks", sinks)
+    if bias_slopes is not None and _tensor("bias_slopes", bias_slopes).requires_grad:
+        _no_gradient("bias_slopes", bias_slopes)
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left,
@@ -969,7 +984,8 @@ def masked_attention(q: torch.Tensor, kv: torch.Tensor, *, softmax_scale: float 
     uint8 tensor to use instead of a new one, sfm_dense_workspace_size bytes,
     for one call at a time.  Rows of a TND batch behind its last sequence are
     0 in a new output and -inf in a new LSE, and stay as they were in given ones.
-    No gradient is recorded: inputs that require one are refused in grad mode."""
+    No gradient is recorded: inputs that require one (sinks and bias_slopes too)
+    are refused in grad mode, and those that carry a tangent."""
     return _dense(q, kv, None, None, softmax_scale, softcap, bias_slopes, sinks, mask_mode, win_left, win_right, prefix_lens,
                   key_begin, key_end, block_table, cu_seqlens_q, cu_seqlens_kv, seqused_q, seqused_kv, max_seqlen_kv, layout_q,
                   layout_kv, split_keys, out, lse, workspace, status, stream)
@@ -1000,7 +1016,7 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
     (up to 8 of (..., heads, dim), bf16 or fp16, dense) with their LSEs (fp32,
     one per row, any shape) to (out, LSE) over all keys.  ``sinks`` (fp32,
     heads) count once, so the parts are computed without them.  ``out`` may be
-    one of the parts."""
+    one of the parts.  Inputs that require a gradient are refused in grad mode."""
     outs, lses = list(outs), list(lses)
     if not outs or len(outs) != len(lses) or len(outs) > MERGE_MAX_PARTS:
         raise ValueError(f"outs and lses: need 1 to {MERGE_MAX_PARTS} each, as many of one as of the other")
@@ -1008,6 +1024,8 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return merge_attention(outs, lses, sinks=sinks, out=out, lse=lse)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(outs=outs, lses=lses, sinks=sinks, out=out, lse=lse)
     x = outs[0]
     shape = x.shape
     if len(shape) < 2:
@@ -1025,6 +1043,8 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
         ends.append(_address("lses", l, _F32, dev, l.shape))
         if grad and l.requires_grad:
             _no_gradient("lses", l)
+    if sinks is not None and _tensor("sinks", sinks).requires_grad:
+        _no_gradient("sinks", sinks)
     given = ()
     if out is None:
         out = torch.empty_like(x)
@@ -1066,6 +1086,8 @@ def move_kv(cache: torch.Tensor, path: torch.Tensor, first: torch.Tensor, *, blo
         raise ValueError("cache: not on a CUDA device" if isinstance(cache, torch.Tensor) else "cache: not a tensor")
     dev = cache.get_device()
     _no_gradient("cache", cache)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(cache=cache)
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return move_kv(cache, path, first, block_table=block_table, status=status)

@@ -1025,6 +1025,40 @@ def test_refusals():
         bad(word, sfm.move_kv, *args, **kw)
 
 
+def test_gradients_of_parameters_and_tangents_are_not_lost():
+    p = problem(seed=47, heads=16, q_lens=(3, 1), lens=(50, 20), sinks=True, bias=True)
+    tree = problem(seed=47, heads=16, q_lens=(3, 1), lens=(50, 20), sinks=True, bias=True, tree=True)
+    o, l = torch.zeros(4, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 16, device="cuda")
+    s = torch.nn.Parameter(torch.ones(16, device="cuda"))
+    for name in ("sinks", "bias_slopes"):
+        for x in (p, tree):
+            want = run(x, **{name: s.detach()})
+            with pytest.raises(ValueError, match=name + ".*gradient"):
+                run(x, **{name: s})
+            with torch.no_grad():
+                got = run(x, **{name: s})
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError, match="sinks.*gradient"):
+        sfm.merge_attention([o], [l], sinks=s)
+    with torch.no_grad():
+        sfm.merge_attention([o], [l], sinks=s)
+    c, path, first = torch.zeros(1, 16, 64, dtype=torch.float16, device="cuda"), ints([[0, 1]]), ints([0])
+    with torch.autograd.forward_ad.dual_level():
+        def dual(x):
+            return torch.autograd.forward_ad.make_dual(x, torch.ones_like(x))
+        for name, args, kw in (("q", (dual(p["q"]), p["kv"]), p["args"]), ("kv", (p["q"], dual(p["kv"])), p["args"]),
+                               ("sinks", (p["q"], p["kv"]), {**p["args"], "sinks": dual(s.detach())}),
+                               ("bias_slopes", (p["q"], p["kv"]), {**p["args"], "bias_slopes": dual(s.detach())})):
+            with pytest.raises(ValueError, match=name + ".*tangent"):
+                sfm.masked_attention(*args, **kw)
+        for name, args, kw in (("outs", ([o, dual(o)], [l, l]), {}), ("lses", ([o, o], [l, dual(l)]), {}), ("sinks", ([o], [l]), dict(sinks=dual(s.detach())))):
+            with pytest.raises(ValueError, match=name + ".*tangent"):
+                sfm.merge_attention(*args, **kw)
+        with pytest.raises(ValueError, match="cache.*tangent"):
+            sfm.move_kv(dual(c), path, first)
+        run(p), sfm.merge_attention([o], [l]), sfm.move_kv(c, path, first)       # others go on as they are
+
+
 def test_moved_rows_through_tables_without_blocks_are_refused():
     c = torch.arange(4 * 16 * 64, device="cuda").view(4, 16, 64).half()
     was = c.clone()
