@@ -524,7 +524,7 @@ typedef struct sfm_dense_params {
     int32_t batch_size;         /* b (> 0) */
     int32_t max_seqlen_q;       /* BSND: q_s; TND: ignored */
     int32_t total_q;            /* TND: rows of q (>= 0); BSND: ignored */
-    int32_t max_seqlen_kv;      /* BSND: S dim of kv; TND / paged: max key count (longer sequences are cut, SFM_STATUS_BAD_LENGTH) */
+    int32_t max_seqlen_kv;      /* BSND: S dim of kv (>= 0); TND (>= 0) / paged (> 0): max key count (longer sequences are cut, SFM_STATUS_BAD_LENGTH) */
     int32_t mask_mode;          /* 0 no mask, 3 right-down causal, 4 window */
     int32_t win_left;           /* mode 4: -1 (unbounded) or >= 0 past keys */
     int32_t win_right;          /* mode 4: -1 (unbounded) or >= 0 future keys */
@@ -544,7 +544,7 @@ typedef struct sfm_dense_params {
 /*   q              BSND (b, q_s, num_heads, 512) / TND (q_t, num_heads, 512), dense, 16-byte aligned
  *   kv             BSND (b, S, row) / TND (t, row) / PAGED (blocks, block_size, row), 16-byte aligned; rows of 512
  *                  values, kv_row_stride bytes apart (>= 1024, multiple of 16), kv_rows rows in all
- *                  (paged: a block at least)
+ *                  (paged: a block at least; otherwise 0, with kv NULL or not, is a source without keys)
  *   the length tensors and sinks as in sfm_tensors (seqused_kv required for PAGED; where cu_seqlens_q falls, the
  *                  length is cut to 0, SFM_STATUS_BAD_LENGTH is set and rows of q may be skipped)
  *   bias_slopes    (num_heads) fp32 or NULL

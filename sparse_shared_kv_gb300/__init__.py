@@ -967,7 +967,8 @@ def masked_attention(q: torch.Tensor, kv: torch.Tensor, *, softmax_scale: float 
     q: (b, q_s, heads, 512) or TND (tokens, heads, 512), bf16 or fp16, dense;
     kv: (b, S, 512), (t, 512) or paged (blocks, block_size, 512) of the same
     dtype, with a KV head of 1 before the values or not, rows may be padded
-    apart.  The scores are softmax_scale q.k, then ``softcap`` tanh(x / softcap)
+    apart.  Contiguous kv may have no row (S or t of 0): every output is then 0 and every
+    LSE -inf.  The scores are softmax_scale q.k, then ``softcap`` tanh(x / softcap)
     (0: none), then minus ``bias_slopes`` (fp32, heads) times the distance of
     query and key; ``sinks`` (fp32, heads) count in the denominator only.
     Query i of q_len sits at p = len - q_len + i, and sees key j if the mask

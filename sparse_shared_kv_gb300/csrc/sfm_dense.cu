@@ -1483,7 +1483,7 @@ int dense_check(const sfm_dense_params *pp)
     if (p.layout_kv != SFM_LAYOUT_BSND && p.layout_kv != SFM_LAYOUT_TND && p.layout_kv != SFM_LAYOUT_PAGED)
         return SFM_ERR_LAYOUT;
     if (p.layout_kv != SFM_LAYOUT_PAGED && p.layout_kv != p.layout_q) return SFM_ERR_LAYOUT;
-    if (p.batch_size <= 0 || p.max_seqlen_kv <= 0) return SFM_ERR_INVALID_ARG;
+    if (p.batch_size <= 0 || p.max_seqlen_kv < (p.layout_kv == SFM_LAYOUT_PAGED)) return SFM_ERR_INVALID_ARG;
     if (p.layout_q == SFM_LAYOUT_BSND ? p.max_seqlen_q < 0 : p.total_q < 0) return SFM_ERR_INVALID_ARG;
     if (p.mask_mode != 0 && p.mask_mode != 3 && p.mask_mode != 4) return SFM_ERR_INVALID_ARG;
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
@@ -1658,7 +1658,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     if (!t) return SFM_ERR_INVALID_ARG;
     const sfm_dense_params &p = *pp;
     const bool paged = p.layout_kv == SFM_LAYOUT_PAGED, tnd = p.layout_q == SFM_LAYOUT_TND;
-    if (t->kv_row_stride < 2 * kD || t->kv_row_stride % 16 || t->kv_rows <= 0) return SFM_ERR_LAYOUT;
+    if (t->kv_row_stride < 2 * kD || t->kv_row_stride % 16 || t->kv_rows < 0) return SFM_ERR_LAYOUT;
     if (t->kv_rows > ((int64_t)1 << 31) - 1024) return SFM_ERR_UNSUPPORTED;
     if (paged && t->kv_rows < p.block_size) return SFM_ERR_LAYOUT;
     if (p.layout_kv == SFM_LAYOUT_BSND && t->kv_rows < (int64_t)p.batch_size * p.max_seqlen_kv) return SFM_ERR_LAYOUT;
@@ -1670,7 +1670,7 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
         return SFM_ERR_INVALID_ARG;
     const int32_t tokens = tnd ? p.total_q : p.batch_size * p.max_seqlen_q;
     if (tokens == 0) return SFM_OK;
-    if (!t->q || !t->kv || !out) return SFM_ERR_INVALID_ARG;
+    if (!t->q || (!t->kv && t->kv_rows) || !out) return SFM_ERR_INVALID_ARG;
     if (((uintptr_t)t->q | (uintptr_t)t->kv | (uintptr_t)out) & 15u) return SFM_ERR_LAYOUT;
     const void *const words[] = {lse, status, t->sinks, t->bias_slopes, t->block_table, t->cu_seqlens_q, t->cu_seqlens_kv, t->seqused_q, t->seqused_kv,
                                  t->prefix_lens, t->key_begin, t->key_end, t->positions};
@@ -1748,7 +1748,8 @@ extern "C" int sfm_dense_forward(const sfm_dense_params *pp, const sfm_dense_ten
     CUtensorMap q_map, kv_map;
     static thread_local KeptMap kept_q, kept_kv;
     rc = make_map(&q_map, kept_q, t->q, p.dtype, (int64_t)tokens * p.num_heads, 2 * kD, 64, 8);
-    if (!rc) rc = make_map(&kv_map, kept_kv, t->kv, p.dtype, t->kv_rows, t->kv_row_stride, pl.box_rows, kBlocks);
+    // (a map has a row at least; where kv has none no sequence has a key, and nothing is copied)
+    if (!rc) rc = make_map(&kv_map, kept_kv, t->kv_rows ? t->kv : t->q, p.dtype, t->kv_rows ? t->kv_rows : 1, t->kv_row_stride, pl.box_rows, kBlocks);
     if (rc) return rc;
     const cudaStream_t st = (cudaStream_t)stream;
     const CapKind cap = a.cap > kWideCap ? kLargeCap : a.cap > 0.f ? kSmallCap : kNoCap;

@@ -106,6 +106,18 @@ def test_caps_that_leave_fp32_in_steps_of_a_power_of_two_are_refused(lib, cap):
     assert lib.sfm_dense_forward(C.byref(_dense(softcap=cap)), C.byref(_tensors()), ADDR, ADDR, None, 0, None, None) == 1
 
 
+@pytest.mark.parametrize("layout", [sfm.BSND, sfm.TND])
+def test_contiguous_sources_may_have_no_row(lib, layout):
+    size, kw = C.c_size_t(0), dict(layout_q=layout, layout_kv=layout, total_q=8, max_seqlen_kv=0)
+    assert lib.sfm_dense_workspace_size(C.byref(_dense(**kw)), C.byref(size)) in (0, 5)          # 5: no GPU here
+    assert lib.sfm_dense_workspace_size(C.byref(_dense(**{**kw, "max_seqlen_kv": -1})), C.byref(size)) == 1
+    none = dict(block_table=None, kv_rows=0, cu_seqlens_q=ADDR, cu_seqlens_kv=ADDR)
+    # refused for what else is missing, not for the rows
+    assert lib.sfm_dense_forward(C.byref(_dense(**kw)), C.byref(_tensors(q=None, kv=None, **none)), ADDR, ADDR, None, 0, None, None) == 1
+    assert lib.sfm_dense_forward(C.byref(_dense(**kw)), C.byref(_tensors(q=ADDR + 8, kv=None, **none)), ADDR, ADDR, None, 0, None, None) == 3
+    assert lib.sfm_dense_forward(C.byref(_dense(**kw)), C.byref(_tensors(**{**none, "kv_rows": -1})), ADDR, ADDR, None, 0, None, None) == 3
+
+
 @pytest.mark.parametrize("rest", [-1, 4, 1 << 20])
 def test_rest_is_refused(lib, rest):
     size = C.c_size_t(0)

@@ -983,6 +983,41 @@ def test_given_buffers_and_no_queries():
     sfm.move_kv(cache, torch.empty(2, 0, dtype=torch.int32, device="cuda"), ints([0, 0]))
 
 
+@pytest.mark.parametrize("layout", ["BSND", "TND"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_sources_without_a_row(layout, dt):
+    """A compressed cache before its first row: no row sees a key, and the joined result is the other part."""
+    g, kind = gen(48), DT[dt]
+    q = randn(g, 2, 3, 16, 512, dtype=kind)
+    near = randn(g, 2, 40, 512, dtype=kind)
+    args = dict(softmax_scale=512 ** -0.5, layout_q=layout, layout_kv=layout)
+    if layout == "BSND":
+        none, some, kw, lens = near[:, :0], near, {}, {}
+    else:
+        q, none, some = q.view(6, 16, 512), near.new_empty(0, 512), near.view(80, 512)
+        args["cu_seqlens_q"] = ints([0, 3, 6])
+        kw, lens = dict(cu_seqlens_kv=ints([0, 0, 0])), dict(cu_seqlens_kv=ints([0, 40, 80]))
+    sinks = randn(g, 16)
+    mask, place = torch.full((*q.shape[:-2], 1), -1, dtype=torch.int64, device="cuda"), torch.zeros(q.shape[:-2], dtype=torch.int32, device="cuda")
+    ends = torch.full(q.shape[:-2], 7, dtype=torch.int32, device="cuda")
+    for more in ({}, dict(mask_mode=0, key_end=ends), dict(prefix_lens=ints([5, 0])), dict(split_keys=128), dict(softcap=20.0, max_seqlen_kv=5000)):
+        status = ints([0])
+        out, lse = sfm.masked_attention(q, none, sinks=sinks, status=status, **{**args, **kw, **more})
+        assert (out == 0).all() and (lse == -INF).all() and out.shape == q.shape and int(status) == 0
+    mine, end = torch.ones_like(q), torch.ones(q.shape[:-1], device="cuda")
+    sfm.tree_attention(q, none, mask, place, out=mine, lse=end, **args, **kw)
+    assert (mine == 0).all() and (end == -INF).all()
+    part = sfm.masked_attention(q, some, **args, **lens)
+    joined = sfm.merge_attention([part[0], out], [part[1], lse])
+    assert torch.equal(joined[0], part[0])
+    again = sfm.masked_attention(q, some, **args, **lens)
+    assert torch.equal(again[0], part[0]) and torch.equal(again[1], part[1])
+    if layout == "TND":
+        status = ints([0])
+        out, lse = sfm.masked_attention(q, none, status=status, **{**args, "cu_seqlens_kv": ints([0, 4, 9])})
+        assert int(status) == sfm.STATUS_BAD_LENGTH and (out == 0).all() and (lse == -INF).all()
+
+
 def test_refusals():
     p = problem(seed=35, heads=16, q_lens=(3, 1), lens=(50, 20))
     q, kv, a = p["q"], p["kv"], p["args"]
