@@ -868,6 +868,8 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         raise ValueError("cu_seqlens_q: required for TND")
     else:
         batch, max_seqlen_q, tokens = _tensor("cu_seqlens_q", cu_seqlens_q).numel() - 1, 0, shape[0]
+        if batch < 0:
+            raise ValueError("cu_seqlens_q: needs b + 1 offsets")
     if not (isinstance(kv, torch.Tensor) and kv.dtype is q.dtype and kv.get_device() == dev):
         raise ValueError(f"kv: needs {q.dtype} on cuda:{dev}")
     if kv.requires_grad:
@@ -898,7 +900,7 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         if not words:
             raise ValueError("tree_mask: needs a word per token")
     kind = q.dtype
-    params = _DENSE_PARAMS.pack(heads, dim, batch, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
+    params = _DENSE_PARAMS.pack(heads, dim, batch or 1, max_seqlen_q, tokens, max_seqlen_kv, mask_mode, win_left, win_right, lq, lkv,
                                 code, kshape[1] if lkv == PAGED else 0, words, split_keys,
                                 (out is None) + 2 * (lse is None), softmax_scale, softcap)
     tensors = _DENSE_TENSORS.pack(
@@ -931,6 +933,8 @@ def _dense(q, kv, tree_mask, positions, softmax_scale, softcap, bias_slopes, sin
         if len(_dense_need) >= 4096:
             _dense_need.clear()
         need = _dense_need[params, dev] = size.value
+    if not batch:                # no sequence: all rows of q (there are some in TND only) lie behind the last one
+        return torch.zeros_like(q) if out is None else out, q.new_full(rows_shape, -math.inf, dtype=_F32) if lse is None else lse
     room = 0
     if workspace is not None:
         if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):

@@ -1018,6 +1018,33 @@ def test_sources_without_a_row(layout, dt):
         assert int(status) == sfm.STATUS_BAD_LENGTH and (out == 0).all() and (lse == -INF).all()
 
 
+def test_batches_without_a_sequence():
+    kv, none = torch.zeros(30, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    for layout, kw in (("BSND", dict(kv=kv[None, :0].expand(0, 0, 512))), ("BSND", dict(kv=kv.new_empty(0, 30, 512))),
+                       ("PAGED", dict(kv=kv[:16][None], block_table=none.view(0, 1), seqused_kv=none))):
+        q = torch.empty(0, 3, 16, 512, dtype=torch.bfloat16, device="cuda")
+        out, lse = sfm.masked_attention(q, layout_kv=layout, sinks=torch.zeros(16, device="cuda"), **kw)
+        assert out.shape == q.shape and lse.shape == (0, 3, 16) and out.dtype is q.dtype and lse.dtype is torch.float32
+        out, lse = sfm.tree_attention(q, tree_mask=torch.empty(0, 3, 1, dtype=torch.int64, device="cuda"), positions=none.view(0, 3), layout_kv=layout, **kw)
+        assert out.shape == q.shape and lse.shape == (0, 3, 16)
+        joined = sfm.merge_attention([out, out], [lse, lse])
+        assert joined[0].shape == q.shape and joined[1].shape == (0, 3, 16)
+    # of a packed batch every row lies behind the last sequence
+    q = torch.ones(5, 16, 512, dtype=torch.bfloat16, device="cuda")
+    args = dict(cu_seqlens_q=ints([0]), cu_seqlens_kv=ints([0]), layout_q="TND", layout_kv="TND")
+    out, lse = sfm.masked_attention(q, kv, **args)
+    assert (out == 0).all() and (lse == -INF).all() and lse.shape == (5, 16)
+    mine, end = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    got = sfm.masked_attention(q, kv, out=mine, lse=end, **args)
+    assert got[0] is mine and got[1] is end and (mine == 7).all() and (end == 7).all()
+    got = sfm.masked_attention(q, kv, out=mine, **args)
+    assert (mine == 7).all() and (got[1] == -INF).all()
+    with pytest.raises(ValueError, match="cu_seqlens_q"):
+        sfm.masked_attention(q, kv, **{**args, "cu_seqlens_q": none})
+    with pytest.raises(sfm.SfmError, match="invalid"):
+        sfm.masked_attention(q, kv, softcap=-1.0, **args)
+
+
 def test_refusals():
     p = problem(seed=35, heads=16, q_lens=(3, 1), lens=(50, 20))
     q, kv, a = p["q"], p["kv"], p["args"]
