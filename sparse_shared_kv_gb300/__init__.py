@@ -1016,10 +1016,19 @@ def tree_attention(q: torch.Tensor, kv: torch.Tensor, tree_mask: torch.Tensor, p
                   layout_kv, split_keys, out, lse, workspace, status, stream)
 
 
+def _rows_in_order(shape, lead):
+    """Whether a shape lists the rows of `lead` (..., heads) in their order; dimensions of one entry do not count."""
+    def plain(s):
+        return [n for n in s if n != 1]
+    rows, heads = lead.numel(), lead[-1]
+    return plain(shape) in (plain(lead), plain((rows // heads if heads else 0, heads)), plain((rows,)))
+
+
 def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
     """Join attention results over separate sets of keys (see sfm_merge): outs
     (up to 8 of (..., heads, dim), bf16 or fp16, dense) with their LSEs (fp32,
-    one per row, any shape) to (out, LSE) over all keys.  ``sinks`` (fp32,
+    (..., heads), (tokens, heads) or flat, as sparse_flash_mla returns them) to
+    (out, LSE) over all keys.  ``sinks`` (fp32,
     heads) count once, so the parts are computed without them.  ``out`` may be
     one of the parts.  Inputs that require a gradient are refused in grad mode."""
     outs, lses = list(outs), list(lses)
@@ -1045,6 +1054,8 @@ def merge_attention(outs, lses, *, sinks=None, out=None, lse=None, stream=None):
     for l in lses:
         if _tensor("lses", l).numel() != rows:
             raise ValueError(f"lses: {l.numel()} values, expected {rows}")
+        if l.shape != lead and not _rows_in_order(l.shape, lead):
+            raise ValueError(f"lses: shape {tuple(l.shape)}, expected {tuple(lead)}, (tokens, heads) or flat")
         ends.append(_address("lses", l, _F32, dev, l.shape))
         if grad and l.requires_grad:
             _no_gradient("lses", l)

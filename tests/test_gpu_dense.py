@@ -778,6 +778,52 @@ def test_merge_of_pieces_is_attention_of_the_whole():
     assert ((out.double() - O).abs() <= (3 * half_step(torch.bfloat16) + 5e-3) * mag).all()
 
 
+def test_lses_come_in_the_order_of_the_rows():
+    g = gen(49)
+    outs = [randn(g, 2, 5, 8, 64, dtype=torch.bfloat16) for _ in range(2)]
+    lses = [randn(g, 2, 5, 8) for _ in range(2)]
+    want = sfm.merge_attention(outs, lses)
+    for shape in ((80,), (10, 8), (2, 5, 8, 1), (1, 10, 8), (80, 1), (1, 1, 80)):
+        got = sfm.merge_attention(outs, [lses[0], lses[1].view(shape)])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for shape in ((2, 8, 5), (8, 10), (8, 2, 5), (5, 2, 8), (2, 40), (10, 8, 1, 2), (16, 5), (40, 2)):
+        with pytest.raises(ValueError, match="lses"):
+            sfm.merge_attention(outs, [lses[0], lses[1].new_zeros(shape)])
+    one = [o[:, :, :1].contiguous() for o in outs]          # one head: rows are tokens
+    for shape in ((2, 5, 1), (1, 10), (10, 1), (10,), (2, 1, 5)):
+        got = sfm.merge_attention(one, [x[..., 0].contiguous().view(shape) for x in lses])
+        assert torch.equal(got[0], want[0][:, :, :1]) and torch.equal(got[1], want[1][..., :1])
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+def test_merge_with_sparse_flash_mla(sinks):
+    """A window by sparse_flash_mla, whose LSE is flat, joined with compressed rows by masked_attention."""
+    g, H, n = gen(50), 16, 4
+    q = 3 * randn(g, 2, n, H, 512)
+    q, kv, cmp = q.bfloat16(), randn(g, 2, 300, 1, 512, dtype=torch.bfloat16), randn(g, 2, 75, 512, dtype=torch.bfloat16)
+    s, scale = (randn(g, H) if sinks else None), 512 ** -0.5
+    md = sfm.sparse_flash_mla_metadata(H, 1, 512, batch_size=2, max_seqlen_q=n, max_seqlen_ori_kv=300, ori_mask_mode=4, ori_win_left=63,
+                                       ori_win_right=0, has_cmp_kv=False, return_softmax_lse=True)
+    near = sfm.sparse_flash_mla(q, metadata=md, ori_kv=kv, softmax_scale=scale)
+    visible = ints([[(297 + i) // 4 for i in range(n)]] * 2)
+    far = sfm.masked_attention(q, cmp, softmax_scale=scale, mask_mode=0, key_end=visible)
+    out, lse = sfm.merge_attention([near[0], far[0]], [near[1], far[1]], sinks=s)
+    assert near[1].dim() == 1 and out.shape == q.shape and lse.shape == q.shape[:-1]
+    for b in range(2):
+        keys = torch.cat((kv[b, :, 0], cmp[b])).double()
+        for i in range(n):
+            p = 296 + i
+            j = torch.arange(300, device="cuda")
+            seen = torch.cat(((j > p - 64) & (j <= p), torch.arange(75, device="cuda") < (p + 1) // 4))
+            x = torch.where(seen, torch.einsum("hd,nd->hn", q[b, i].double(), keys) * scale, -INF)
+            L = x.logsumexp(-1)
+            w = (x - (torch.logaddexp(L, s.double()) if sinks else L)[:, None]).exp()
+            O, mag = w @ keys, w @ keys.abs()
+            # the weights' rounding, the parts' and the result's
+            assert ((out[b, i].double() - O).abs() <= (3 * 2.0 ** -8 + 5e-3) * mag).all()
+            assert ((lse[b, i].double() - L).abs() <= 2e-3).all()
+
+
 # ---------------------------------------------------------------------------
 # moved rows
 # ---------------------------------------------------------------------------
