@@ -534,8 +534,11 @@ typedef struct sfm_dense_params {
     int32_t block_size;         /* paged: rows per block, multiple of 16, <= 1024 */
     int32_t tree_words;         /* 0: no tree; 1..16: 64-bit words per row of tree_mask */
     int32_t split_keys;         /* 0: long key ranges are cut so that the SMs are filled, which depends on the batch;
-                                   > 0 (a multiple of 128): into pieces of this many keys, whatever else is in the
-                                   batch (a row's result is then bit for bit the same in every batch) */
+                                   > 0 (a multiple of 128): into as few pieces of at most this many keys as there can
+                                   be, as even as tiles of 128 keys allow, whatever else is in the batch.  A row's result
+                                   is then bit for bit the same whatever other sequences there are.  The queries of its
+                                   own sequence still have a part in its last bits: 128 consecutive (token, head) rows
+                                   share a range of keys, and with a softcap of 128 or less 32 of them a form of the cap */
     int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 0: left as they were; 1: O = 0; 2: LSE = -inf; 3: both */
     float softmax_scale;        /* finite */
     float softcap;              /* 0: none; 2^-100 to 2^127: scores are capped */

@@ -982,8 +982,10 @@ def masked_attention(q: torch.Tensor, kv: torch.Tensor, *, softmax_scale: float 
     (int32, one per sequence: keys that every token sees).
 
     ``split_keys``: 0 cuts long ranges of keys so that the GPU is filled; a
-    multiple of 128 cuts them into pieces of that many keys, so that a row's
-    result does not depend on what else is in the batch.  ``max_seqlen_kv`` (TND,
+    multiple of 128 cuts them into as few even pieces of at most that many keys
+    as there can be, so that a row's result does not depend on the other sequences
+    of the batch.  ``max_seqlen_q`` may be given as to the other calls; nothing here
+    needs it.  ``max_seqlen_kv`` (TND,
     paged): a bound on the keys of a sequence, which keeps the workspace small;
     longer sequences are cut.  ``workspace``: a
     uint8 tensor to use instead of a new one, sfm_dense_workspace_size bytes,

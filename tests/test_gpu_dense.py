@@ -717,6 +717,20 @@ def test_pieces_of_one_size_make_rows_independent_of_the_batch():
         assert torch.equal(got, out[at:at + ql]) and torch.equal(end, lse[at:at + ql])
 
 
+@pytest.mark.parametrize("keys,same,apart", [(640, (384, 512), (128, 640)), (1024, (512, 640, 896), (384, 1024)), (1500, (512, 640), (384, 768))])
+def test_pieces_are_as_even_as_tiles_allow(keys, same, apart):
+    """5, 8 and 12 tiles: at most split_keys keys in a piece, and no more pieces than that takes."""
+    p = problem(seed=51, heads=64, q_lens=(2,), lens=(keys,), mode=0)
+    runs = [run(p, split_keys=n)[:2] for n in same]
+    check(p, *runs[0])
+    for o, l in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(l, runs[0][1])
+    for n in apart:
+        o, l, _ = run(p, split_keys=n)
+        check(p, o, l)
+        assert not torch.equal(l, runs[0][1])      # (sums of 128 rows in other groups)
+
+
 def test_same_inputs_same_bits():
     p = problem(seed=29, heads=64, q_lens=(40, 1, 9), lens=(3000, 20000, 77), layout_kv="PAGED")
     first = run(p)
