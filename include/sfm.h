@@ -540,7 +540,7 @@ typedef struct sfm_dense_params {
                                    own sequence still have a part in its last bits: 128 consecutive (token, head) rows
                                    share a range of keys, and with a softcap of 128 or less 32 of them a form of the cap */
     int32_t zero_rest;          /* TND, rows of q that belong to no sequence: 0: left as they were; 1: O = 0; 2: LSE = -inf; 3: both */
-    float softmax_scale;        /* finite */
+    float softmax_scale;        /* finite, times log2 e too */
     float softcap;              /* 0: none; 2^-100 to 2^127: scores are capped */
 } sfm_dense_params;
 

@@ -1489,7 +1489,7 @@ int dense_check(const sfm_dense_params *pp)
     if (p.mask_mode == 4 && (p.win_left < -1 || p.win_right < -1)) return SFM_ERR_INVALID_ARG;
     if (p.layout_kv == SFM_LAYOUT_PAGED && (p.block_size < 16 || p.block_size > 1024 || p.block_size % 16)) return SFM_ERR_LAYOUT;
     if (p.tree_words < 0 || p.tree_words > 16 || p.split_keys < 0 || p.split_keys % 128 || p.zero_rest & ~3) return SFM_ERR_INVALID_ARG;
-    if (!std::isfinite(p.softmax_scale) || !(p.softcap == 0.f || (p.softcap >= 0x1p-100f && p.softcap <= 0x1p127f)) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
+    if (!std::isfinite(p.softmax_scale * kLog2e) || !(p.softcap == 0.f || (p.softcap >= 0x1p-100f && p.softcap <= 0x1p127f)) || (p.softcap > 0.f && !std::isfinite(p.softmax_scale / p.softcap)))
         return SFM_ERR_INVALID_ARG;
     if (p.max_seqlen_kv > 1 << 30) return SFM_ERR_UNSUPPORTED;
     const int64_t tokens = p.layout_q == SFM_LAYOUT_TND ? p.total_q : (int64_t)p.batch_size * p.max_seqlen_q;

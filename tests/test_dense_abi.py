@@ -106,6 +106,13 @@ def test_caps_that_leave_fp32_in_steps_of_a_power_of_two_are_refused(lib, cap):
     assert lib.sfm_dense_forward(C.byref(_dense(softcap=cap)), C.byref(_tensors()), ADDR, ADDR, None, 0, None, None) == 1
 
 
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_that_leave_fp32_in_steps_of_a_power_of_two_are_refused(lib, scale):
+    size = C.c_size_t(0)
+    assert lib.sfm_dense_workspace_size(C.byref(_dense(softmax_scale=scale)), C.byref(size)) == 1
+    assert lib.sfm_dense_forward(C.byref(_dense(softmax_scale=scale)), C.byref(_tensors()), ADDR, ADDR, None, 0, None, None) == 1
+
+
 @pytest.mark.parametrize("layout", [sfm.BSND, sfm.TND])
 def test_contiguous_sources_may_have_no_row(lib, layout):
     size, kw = C.c_size_t(0), dict(layout_q=layout, layout_kv=layout, total_q=8, max_seqlen_kv=0)
