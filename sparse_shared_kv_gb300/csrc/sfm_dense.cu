@@ -504,14 +504,6 @@ struct Order {
     }
 };
 
-// bits [lo, hi) of a word whose bit 0 stands for key j0
-__device__ __forceinline__ uint32_t bits_between(int lo, int hi, int j0)
-{
-    const int l = min(max(lo - j0, 0), 32), h = min(max(hi - j0, 0), 32);
-    const uint32_t up = h >= 32 ? 0xffffffffu : (1u << h) - 1u, down = l >= 32 ? 0xffffffffu : (1u << l) - 1u;
-    return h > l ? up & ~down : 0u;
-}
-
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack(float x, float y)
 {
@@ -1238,11 +1230,11 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         } else {
                             bits = (uint32_t)(__ldg(tree) << -o);
                         }
-                        bits &= bits_between(max(first, 0), w.len, j0);
+                        bits &= drafted_keys(first, w.len, j0);
                         if (a.mode == 4) {
                             for (uint32_t rest = bits; rest; rest &= rest - 1) {
                                 const int c = __ffs(rest) - 1;
-                                const int64_t pos = __ldg(a.positions + w.q0 + drafted_entry(o + c, w.q_len));
+                                const int64_t pos = __ldg(a.positions + w.q0 + o + c);
                                 if (pos < (int64_t)row.p - a.win_left || pos > (int64_t)row.p + a.win_right) bits &= ~(1u << c);
                             }
                         }
@@ -1285,9 +1277,10 @@ sfm_dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ Pl
                         }
                     } else {
                         auto fall = [&](int c) {
-                            if (!live || !(vis >> c & 1)) return 0.f;     // (a row that does not count masks nothing)
+                            // (a row that does not count masks nothing; of one that does, visible keys from `first` on are drafted_keys)
+                            if (!live || !(vis >> c & 1)) return 0.f;
                             const int k = j0 + c - first;
-                            return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + drafted_entry(k, w.q_len)))));
+                            return slope * fabsf((float)(row.p - (k < 0 ? j0 + c : __ldg(a.positions + w.q0 + k))));
                         };
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {

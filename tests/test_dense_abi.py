@@ -132,21 +132,25 @@ def test_rest_is_refused(lib, rest):
 
 
 def test_lookups_of_drafted_keys_stay_with_their_sequence(tmp_path):
-    """The index that the kernel looks positions up with, on the host: the key's own where there is one, one of the sequence's anyway."""
+    """The keys of a word whose positions and bits the kernel looks up, on the host: the drafted ones, all of them, and no other."""
     source, program = tmp_path / "entry.cu", tmp_path / "entry"
-    source.write_text("""#include <climits>
-#include "sfm_dense.cuh"
+    source.write_text("""#include "sfm_dense.cuh"
 int main()
 {
-    const int far[] = {INT_MIN, INT_MIN + 1, -(1 << 30), 1 << 30, INT_MAX - 1, INT_MAX};
-    for (int n = 1; n < 400; ++n) {
-        for (int k = -700; k < 1100; ++k) {
-            const int i = sfm::drafted_entry(k, n);
-            if (i < 0 || i >= n || (k >= 0 && k < n && i != k)) return 1;
+    const int sizes[] = {0, 1, 2, 5, 31, 32, 33, 63, 64, 65, 100, 128, 200, 1000, (1 << 30) - 7, 1 << 30};
+    for (int len : sizes)
+        for (int n : sizes) {
+            const int first = len - n;
+            for (int at : {0, first > 0 ? first : 0, len})
+                for (int j0 = (at > 300 ? at - 300 : 0) & ~15; j0 < at + 300; j0 += 16) {
+                    const uint32_t bits = sfm::drafted_keys(first, len, j0);
+                    for (int c = 0; c < 32; ++c) {
+                        const long long j = (long long)j0 + c, k = j - first;
+                        const bool drafted = j >= 0 && j < len && k >= 0;
+                        if (drafted != (bits >> c & 1) || (drafted && k >= n)) return 1;
+                    }
+                }
         }
-        for (int k : far)
-            if (sfm::drafted_entry(k, n) < 0 || sfm::drafted_entry(k, n) >= n) return 2;
-    }
     return 0;
 }
 """)
