@@ -28,8 +28,10 @@
 // of matrix products); called again and again it runs into the GPU's power limit, as such products do (1721), and the
 // clock falls to 1.6 to 1.75 GHz (1.46 to 1.49 PFLOP/s).  Every unit costs some 5000 clocks of the softmax's besides (its
 // results are written, the next unit's rows looked up), which units of few tiles do not hide: 4096 causal tokens of 64
-// heads 1.30, documents of some 1600 1.27 PFLOP/s.  Single tokens are bound by memory: 32 x 24 k keys 4.5 TB/s with 10 us to
-// plan and 9 us to join.
+// heads 1.30, documents of some 1600 1.27 PFLOP/s, and prompts with a window of 128 (two or three tiles per unit) 1.5 to 2
+// times what their rows of q and out take to move.  Single tokens over long keys (32 x 24 k keys of 64 heads 4.4 TB/s, with 10 us to
+// plan and 9 us to join) wait for copies without filling the memory or the tensor cores (61 and 53 % busy): half of the ring
+// holds V, which comes from L2, so that 64 KB per SM are on their way from memory, and a token's 64 rows are half of a pair's.
 //
 // A unit is a tile of Q and a piece of its range of keys.  Pieces of a range
 // leave fp32 partial results in the workspace, which a second kernel joins.
@@ -565,7 +567,8 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float z)
 // larger ones, and for five pairs of the sixteen anyway: the exponentials and quotients of these run beside the
 // multiplications of the others (all by the second form, the scores of a tile took 1300 clocks; all by the first, 900).
 // The second form is off by up to 2^-21 of the cap, however small the score is: 6e-5 at kWideCap, an eighth of an fp16 weight's
-// half step.  Larger caps have a kernel of their own, which takes it for |z| > 1 alone.
+// half step.  Larger caps have a kernel of their own, which takes it for |z| > 1 alone (4096 causal tokens of 64 heads, bf16:
+// 751 us with a cap of 30, 880 with one of 129, 1136 where many scores are larger than that).
 constexpr float kWideCap = 128.f;
 enum CapKind { kNoCap, kSmallCap, kLargeCap };
 

@@ -5,9 +5,12 @@
 //
 // Every value is read and written once, a few operations each: memory bounds
 // it.  A warp takes a row at a time; its lanes work out the same weights and
-// take 16 bytes of the row each, all parts' loads before the first use (4093 x 64
-// rows of 512, three parts: 149 us, 7.2 TB/s; a thread per 16 bytes that each
-// found its row and weights 242).
+// take 16 bytes of the row each, all parts' loads before the first use.  4093 x 64
+// rows of 512: fp16 119 us of two parts (6.8 TB/s), 150 of three (7.1), 193 of four,
+// 342 of eight (7.1); bf16, whose kernels take more registers (three parts 110
+// instead of 64, eight 189 instead of 118), 117 (6.9 TB/s), 189 (5.7), 201, 424
+// (5.7).  A thread per 16 bytes that each found its row and weights took 242 of
+// three fp16 parts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -141,7 +144,8 @@ __global__ void __launch_bounds__(32 * kWarps) sfm_merge_kernel(const MergeArgs 
 template <typename T>
 cudaError_t launch(const MergeArgs &a, int sms, cudaStream_t st)
 {
-    // as many rows per warp as keep some 8 CTAs on every SM busy
+    // Sixteen CTAs per SM at most, so that a warp takes several rows of a long call.  How many an SM holds at once goes by the
+    // registers: of three parts four in fp16 and two in bf16, of eight two and one.
     const int64_t blocks = ((int64_t)a.rows + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
     const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(32 * kWarps);
     switch (a.parts) {
